@@ -429,6 +429,129 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
                                         int32_t num_tokens, int32_t num_heads, int32_t out_dtype,
                                         float q_scale, void* out, cudaStream_t stream);
 
+/*
+ * An e4m3 cache with group scales: scale_group (g) is a divisor of the block
+ * size, and cache slot s (a physical block times block_size plus the offset)
+ * holds 576 e4m3 codes that stand for code * kv_scales[s / g], kv_scales being
+ * [num_blocks * block_size / g] fp32: one scale for each g tokens of a block,
+ * from one per token (g = 1) to one per block. (The latent row is the cache's
+ * only head: the scale covers its latent and its rope columns.) The pages keep
+ * one scale for the whole tensor; a scale per group follows the tokens.
+ * mla_block_tables, mla_cache_append and mla_decode_fwd_scaled, in this order
+ * on one stream, are a step: blocks and slots from the lengths, the new rows
+ * quantised into them, and the attention over the cache.
+ */
+
+/*
+ * mla_decode_fwd_scaled -- mla_decode_fwd over a cache with group scales.
+ * score = softmax_scale * q_scale * s_j * (q . c_j) with c_j the codes of key
+ * j and s_j its group's scale; its value is s_j times the first 512 codes.
+ * Everything else is mla_decode_fwd's: dense requests of one or more tokens,
+ * sparse slot lists, sinks, the balanced schedule or a fixed num_segments,
+ * the workspace and its status word. The plan is one for kv_dtype =
+ * MLA_DTYPE_FP8_E4M3 (mla_decode_plan chooses among the same kernels).
+ *   kv_scales    [num_blocks * block_size / scale_group] fp32. The scales of
+ *                groups that hold visible keys must lie in [2^-60, 2^60]
+ *                (mla_cache_append writes such); others are not used.
+ *   scale_group  divisor of block_size
+ * Errors: as mla_decode_fwd, MLA_ERR_INVALID_ARG for a scale_group that does
+ * not divide block_size or NULL or misaligned kv_scales, MLA_ERR_UNSUPPORTED
+ * for a plan whose cache is not e4m3.
+ */
+MLA_API mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q, const void* kv_cache,
+                                           const float* kv_scales, int32_t scale_group,
+                                           const int32_t* block_table, int64_t block_table_stride,
+                                           const int32_t* seq_lens, const int32_t* qo_indptr,
+                                           const int32_t* sparse_slots, const int32_t* sparse_indptr,
+                                           float softmax_scale, float q_scale, const float* sinks,
+                                           void* workspace, size_t workspace_bytes, void* out,
+                                           float* lse, cudaStream_t stream);
+
+/*
+ * mla_decode_items_scaled -- mla_decode_items over a cache with group scales,
+ * between mla_decode_schedule and mla_merge_items, for callers that compute
+ * the work list once per step. Arguments as mla_decode_fwd_scaled.
+ */
+MLA_API mla_status_t mla_decode_items_scaled(const mla_plan_t* plan, const void* q,
+                                             const void* kv_cache, const float* kv_scales,
+                                             int32_t scale_group, const int32_t* block_table,
+                                             int64_t block_table_stride, const int32_t* seq_lens,
+                                             const int32_t* qo_indptr, const int32_t* sparse_slots,
+                                             const int32_t* sparse_indptr, float softmax_scale,
+                                             float q_scale, const float* sinks, void* workspace,
+                                             size_t workspace_bytes, void* out, float* lse,
+                                             cudaStream_t stream);
+
+/*
+ * mla_block_tables -- the block tables' new columns, and every token's slot,
+ * request and position, from the request lengths of a step. Request r has
+ * q_r = query_start_loc[r + 1] - query_start_loc[r] new tokens, the last ones
+ * of its seq_lens[r]; the other c_r are in the cache already, in the first
+ * old_r = ceil(c_r / block_size) columns of its table row. It takes the next
+ *   new_r = max(min(ceil(seq_lens[r] / block_size), max_blocks_per_req) - old_r, 0)
+ * entries of free_blocks, requests in order from entry 0, for its columns
+ * old_r, old_r + 1, ... No other cell of the table is written. Token t of
+ * request r sits at p = c_r + t - query_start_loc[r]:
+ *   slot_mapping[t] = block_table[r, p / block_size] * block_size + p % block_size,
+ * req_id[t] = r, positions[t] = p. Where the list is too short the missing
+ * columns become -1 and their tokens' slots too; a token past the table's
+ * columns, and one whose block is negative, has slot -1. Tokens before
+ * query_start_loc[0] or at or past query_start_loc[num_reqs] (the padding of
+ * a captured batch) get -1 in all three.
+ * *taken receives the sum of new_r; it exceeds num_free when the list was
+ * short. The caller drops that many entries from its list.
+ *   query_start_loc [num_reqs + 1] int32, nondecreasing, at most num_tokens
+ *   seq_lens        [num_reqs] int32, >= q_r
+ *   free_blocks     [num_free] int32 ids of unused blocks, or NULL when 0
+ *   block_table     [num_reqs, max_blocks_per_req] int32, row stride
+ *                   block_table_stride elements; read and written
+ *   slot_mapping    [num_tokens] int32; req_id, positions [num_tokens] int32
+ *                   or NULL; taken [1] int32
+ * The outputs must not overlap the inputs. One launch on `stream`, no
+ * workspace. Errors: MLA_ERR_INVALID_ARG for negative sizes, block_size or
+ * max_blocks_per_req <= 0, a short stride, NULL or misaligned pointers.
+ */
+MLA_API mla_status_t mla_block_tables(const int32_t* query_start_loc, const int32_t* seq_lens,
+                                      int32_t num_reqs, int32_t num_tokens, int32_t block_size,
+                                      const int32_t* free_blocks, int32_t num_free,
+                                      int32_t* block_table, int64_t block_table_stride,
+                                      int32_t max_blocks_per_req, int32_t* slot_mapping,
+                                      int32_t* req_id, int32_t* positions, int32_t* taken,
+                                      cudaStream_t stream);
+
+/*
+ * mla_cache_append -- a step's latent rows into an e4m3 cache with group
+ * scales. Token t goes to slot_mapping[t]; a slot outside
+ * [0, num_blocks * block_size) (the padding's -1) is skipped. A run is a
+ * maximal stretch of consecutive tokens at consecutive slots of one group;
+ * the rows of its group before its first slot are taken to be in use, those
+ * behind its last are left as they are. With a the largest finite |x| of the
+ * run's rows x = c_kv || k_pe, its group's scale becomes
+ *   s = max(2^k, 2^-60) with the least k for which a <= 448 * 2^k,
+ * or the old scale where that is larger and the run does not start its group;
+ * the rows are stored as e4m3 codes of x / s (times the fp32 reciprocal),
+ * rounded to nearest even, infinities as +-448, NaN as NaN. Where s exceeds
+ * the old scale, the group's rows before the run are requantised by
+ * old / s: exact but for codes that become subnormal, as long as every scale
+ * is a power of two.
+ * The runs of one call must lie in different groups, and no slot may occur
+ * twice (mla_block_tables gives such maps, as long as no two requests write
+ * to the same block): else the contents of those groups are undefined.
+ *   c_kv [num_tokens, 512] bf16, row stride c_kv_stride elements
+ *   k_pe [num_tokens, 64] bf16, row stride k_pe_stride elements
+ *   kv_cache [num_blocks, block_size, 576] e4m3 codes, kv_scales
+ *   [num_blocks * block_size / scale_group] fp32: both read and written
+ * c_kv, k_pe and kv_cache 16-byte aligned, the strides multiples of 8.
+ * One launch on `stream`. Errors: MLA_ERR_INVALID_ARG for bad sizes, a
+ * scale_group that does not divide block_size, NULL or misaligned pointers;
+ * MLA_ERR_UNSUPPORTED for more than INT32_MAX slots.
+ */
+MLA_API mla_status_t mla_cache_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe,
+                                      int64_t k_pe_stride, const int32_t* slot_mapping,
+                                      int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                                      int32_t scale_group, void* kv_cache, float* kv_scales,
+                                      cudaStream_t stream);
+
 /* Largest plan->workspace_bytes that mla_decode_fwd_static accepts. */
 #define MLA_STATIC_SCRATCH_BYTES ((size_t)64 << 20) /* 64 MiB */
 

@@ -12,3 +12,4 @@ from .mla_oracle import (  # noqa: F401
     segment_partials, tile_size_for_block, token_layout, visible_len, sparse_seqlen,
     fit_kpool_indices,
 )
+from . import scaled_oracle  # noqa: F401

@@ -122,6 +122,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _vp,
                                            _vp]
         lib.mla_concat_quant_q.restype = st
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        scaled = [ctypes.POINTER(Plan), _vp, _vp, _vp, i32, _vp, i64, _vp, _vp, _vp, _vp, f32, f32,
+                  _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
+        lib.mla_decode_fwd_scaled.argtypes = scaled
+        lib.mla_decode_fwd_scaled.restype = st
+        lib.mla_decode_items_scaled.argtypes = scaled
+        lib.mla_decode_items_scaled.restype = st
+        lib.mla_block_tables.argtypes = [_vp, _vp, i32, i32, i32, _vp, i32, _vp, i64, i32, _vp, _vp,
+                                         _vp, _vp, _vp]
+        lib.mla_block_tables.restype = st
+        lib.mla_cache_append.argtypes = [_vp, i64, _vp, i64, _vp, i32, i32, i32, i32, _vp, _vp, _vp]
+        lib.mla_cache_append.restype = st
         lib.mla_workspace_status.argtypes = [ctypes.POINTER(Plan), _vp, ctypes.POINTER(ctypes.c_int32),
                                              ctypes.c_int32, _vp]
         lib.mla_workspace_status.restype = st
@@ -327,6 +339,177 @@ def mla_sparse_seqlen(query_start_loc, seq_lens, *, topk: int, indptr, lens=None
     _check("mla_sparse_seqlen", lib.mla_sparse_seqlen(
         _ptr(query_start_loc), _ptr(seq_lens), num_reqs, num_tokens, int(topk), _ptr(lens),
         _ptr(indptr), _stream(stream)))
+
+
+# The calls over a cache with group scales check what their pointers cannot
+# tell the library: element type, device and density of each tensor.
+
+def _need(cond: bool, fn: str, what: str):
+    if not cond:
+        raise MLAError(fn, MLA_ERR_INVALID_ARG, what)
+
+
+def _need_dense(fn: str, device, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t.is_contiguous(), fn, f"{name} must be contiguous")
+            _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
+
+
+def _need_int32(fn: str, device, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None:
+            _need(t.dtype == torch.int32, fn, f"{name} must be int32")
+    _need_dense(fn, device, **tensors)
+
+
+def _need_current(fn: str, device):
+    import torch
+    _need(device.type == "cuda", fn, "the tensors must be on a CUDA device")
+    _need(device.index == torch.cuda.current_device(), fn, f"{device} is not the current device")
+
+
+def _need_scaled_cache(fn: str, device, kv_cache, kv_scales, scale_group: int):
+    import torch
+    _need(kv_cache.dtype in (torch.float8_e4m3fn, torch.uint8), fn, "kv_cache must hold e4m3 codes")
+    _need(kv_cache.dim() == 3 and kv_cache.shape[2] == HEAD_DIM, fn,
+          f"kv_cache must be [num_blocks, block_size, {HEAD_DIM}]")
+    _need(kv_scales.dtype == torch.float32, fn, "kv_scales must be float32")
+    nb, bs = kv_cache.shape[0], kv_cache.shape[1]
+    _need(scale_group > 0 and bs % scale_group == 0, fn, "scale_group must divide the block size")
+    _need(kv_scales.numel() == nb * bs // scale_group, fn,
+          "kv_scales must hold num_blocks * block_size / scale_group scales")
+    _need_dense(fn, device, kv_cache=kv_cache, kv_scales=kv_scales)
+
+
+def _scaled_args(fn: str, plan: Plan, q, kv_cache, kv_scales, scale_group, block_table,
+                 block_table_stride, seq_lens, qo_indptr, sparse_slots, sparse_indptr,
+                 softmax_scale, q_scale, sinks, workspace, out, lse, stream):
+    import torch
+    dev = q.device
+    pr = plan.prob
+    _need_current(fn, dev)
+    if pr.kv_dtype != MLA_DTYPE_FP8_E4M3:
+        raise MLAError(fn, MLA_ERR_UNSUPPORTED, "the plan's cache is not e4m3")
+    _need_scaled_cache(fn, dev, kv_cache, kv_scales, scale_group)
+    _need(kv_cache.shape[0] == pr.num_blocks and kv_cache.shape[1] == pr.block_size, fn,
+          "kv_cache is not the plan's")
+    _need(q.dtype in (torch.float8_e4m3fn, torch.uint8), fn, "q must hold e4m3 codes")
+    _need(tuple(q.shape) == (pr.num_tokens, pr.num_heads, HEAD_DIM), fn, "q is not the plan's")
+    _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (pr.num_tokens, pr.num_heads, KV_LORA_RANK),
+          fn, f"out must be bfloat16 [num_tokens, num_heads, {KV_LORA_RANK}]")
+    _need(lse.dtype == torch.float32 and tuple(lse.shape) == (pr.num_tokens, pr.num_heads), fn,
+          "lse must be float32 [num_tokens, num_heads]")
+    _need_dense(fn, dev, q=q, out=out, lse=lse, workspace=workspace)
+    if sinks is not None:
+        _need(sinks.dtype == torch.float32 and sinks.numel() == pr.num_heads, fn,
+              "sinks must be float32 [num_heads]")
+        _need_dense(fn, dev, sinks=sinks)
+    _need_int32(fn, dev, seq_lens=seq_lens, qo_indptr=qo_indptr, sparse_slots=sparse_slots,
+                sparse_indptr=sparse_indptr)
+    if pr.topk > 0:
+        if sparse_indptr is not None:
+            _need(sparse_indptr.numel() == pr.num_tokens + 1, fn, "sparse_indptr must be [num_tokens + 1]")
+        elif sparse_slots is not None:
+            _need(sparse_slots.numel() == pr.num_tokens * pr.topk, fn, "sparse_slots must be [num_tokens, topk]")
+    elif seq_lens is not None and block_table is not None:
+        _need(seq_lens.numel() == pr.num_reqs, fn, "seq_lens must be [num_reqs]")
+        _need(qo_indptr is None or qo_indptr.numel() == pr.num_reqs + 1, fn, "qo_indptr must be [num_reqs + 1]")
+        _need(block_table.dtype == torch.int32 and block_table.device == dev, fn,
+              "block_table must be int32 on the same device")
+        _need(block_table.dim() == 2 and block_table.shape[0] == pr.num_reqs
+              and block_table.shape[1] >= pr.max_blocks_per_req
+              and (block_table.stride(1) == 1 or block_table.shape[1] == 1), fn,
+              "block_table must be [num_reqs, >= max_blocks_per_req] with dense rows")
+    if block_table_stride is None:
+        block_table_stride = max(block_table.stride(0), block_table.shape[1]) if block_table is not None else 0
+    return (ctypes.byref(plan), _ptr(q), _ptr(kv_cache), _ptr(kv_scales), int(scale_group),
+            _ptr(block_table), int(block_table_stride), _ptr(seq_lens), _ptr(qo_indptr),
+            _ptr(sparse_slots), _ptr(sparse_indptr), float(softmax_scale), float(q_scale),
+            _ptr(sinks), _ptr(workspace), _ws_bytes(workspace), _ptr(out), _ptr(lse), _stream(stream))
+
+
+def mla_decode_fwd_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: int, block_table=None,
+                          block_table_stride=None, seq_lens=None, qo_indptr=None,
+                          sparse_slots=None, sparse_indptr=None, softmax_scale: float,
+                          q_scale: float = 1.0, sinks=None, workspace=None, out, lse,
+                          stream=None) -> None:
+    """mla_decode_fwd over an e4m3 cache with one fp32 scale per ``scale_group``
+    slots of a block (``kv_scales``)."""
+    lib = load_library()
+    fn = "mla_decode_fwd_scaled"
+    _check(fn, lib.mla_decode_fwd_scaled(*_scaled_args(
+        fn, plan, q, kv_cache, kv_scales, scale_group, block_table, block_table_stride, seq_lens,
+        qo_indptr, sparse_slots, sparse_indptr, softmax_scale, q_scale, sinks, workspace, out, lse,
+        stream)))
+
+
+def mla_decode_items_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: int,
+                            block_table=None, block_table_stride=None, seq_lens=None,
+                            qo_indptr=None, sparse_slots=None, sparse_indptr=None,
+                            softmax_scale: float, q_scale: float = 1.0, sinks=None, workspace,
+                            out, lse, stream=None) -> None:
+    """Balanced plans: the decode kernel of mla_decode_fwd_scaled over the work
+    list in ``workspace``."""
+    lib = load_library()
+    fn = "mla_decode_items_scaled"
+    _check(fn, lib.mla_decode_items_scaled(*_scaled_args(
+        fn, plan, q, kv_cache, kv_scales, scale_group, block_table, block_table_stride, seq_lens,
+        qo_indptr, sparse_slots, sparse_indptr, softmax_scale, q_scale, sinks, workspace, out, lse,
+        stream)))
+
+
+def mla_block_tables(query_start_loc, seq_lens, free_blocks, block_table, *, block_size: int,
+                     slot_mapping, req_id=None, positions=None, taken, stream=None) -> None:
+    """The step's new columns of ``block_table [R, C]`` from ``free_blocks``,
+    and ``slot_mapping``, ``req_id`` and ``positions`` (``[T]``) of its tokens;
+    ``taken`` (``[1]``) receives the number of blocks the step takes."""
+    lib = load_library()
+    fn = "mla_block_tables"
+    dev = query_start_loc.device
+    _need_current(fn, dev)
+    _need_int32(fn, dev, query_start_loc=query_start_loc, seq_lens=seq_lens, free_blocks=free_blocks,
+                slot_mapping=slot_mapping, req_id=req_id, positions=positions, taken=taken)
+    R, T = seq_lens.numel(), slot_mapping.numel()
+    _need(query_start_loc.numel() == R + 1, fn, "query_start_loc must be [num_reqs + 1]")
+    _need(taken.numel() == 1, fn, "taken must be [1]")
+    _need((req_id is None or req_id.numel() == T) and (positions is None or positions.numel() == T), fn,
+          "req_id and positions must be [num_tokens]")
+    _need(str(block_table.dtype) == "torch.int32" and block_table.device == dev, fn,
+          "block_table must be int32 on the same device")
+    _need(block_table.dim() == 2 and block_table.shape[0] == R
+          and (block_table.stride(1) == 1 or block_table.shape[1] == 1 or R == 0), fn,
+          "block_table must be [num_reqs, columns] with dense rows")
+    cols = block_table.shape[1]
+    _need(R <= 1 or block_table.stride(0) >= cols, fn, "block_table rows must not overlap")
+    _check(fn, lib.mla_block_tables(
+        _ptr(query_start_loc), _ptr(seq_lens), R, T, int(block_size), _ptr(free_blocks),
+        0 if free_blocks is None else free_blocks.numel(), _ptr(block_table),
+        max(block_table.stride(0), cols), cols, _ptr(slot_mapping), _ptr(req_id), _ptr(positions),
+        _ptr(taken), _stream(stream)))
+
+
+def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_group: int,
+                     stream=None) -> None:
+    """The rows ``c_kv [T, 512] || k_pe [T, 64]`` (bf16) into the slots of
+    ``slot_mapping``, as e4m3 codes under their groups' scales."""
+    import torch
+    lib = load_library()
+    fn = "mla_cache_append"
+    dev = kv_cache.device
+    _need_current(fn, dev)
+    _need_scaled_cache(fn, dev, kv_cache, kv_scales, scale_group)
+    _need_int32(fn, dev, slot_mapping=slot_mapping)
+    T = slot_mapping.numel()
+    for name, t, width in (("c_kv", c_kv, KV_LORA_RANK), ("k_pe", k_pe, HEAD_DIM - KV_LORA_RANK)):
+        _need(t.dtype == torch.bfloat16 and t.device == dev and tuple(t.shape) == (T, width)
+              and (t.stride(1) == 1 or T == 0), fn, f"{name} must be bfloat16 [num_tokens, {width}] with dense rows")
+    _check(fn, lib.mla_cache_append(
+        _ptr(c_kv), max(c_kv.stride(0), KV_LORA_RANK) if T <= 1 else c_kv.stride(0), _ptr(k_pe),
+        max(k_pe.stride(0), HEAD_DIM - KV_LORA_RANK) if T <= 1 else k_pe.stride(0),
+        _ptr(slot_mapping), T, kv_cache.shape[0], kv_cache.shape[1], int(scale_group),
+        _ptr(kv_cache), _ptr(kv_scales), _stream(stream)))
 
 
 def mla_fit_kpool_indices(token_indices, *, topk: int, out, stream=None) -> None:

@@ -78,6 +78,8 @@ struct Inputs {
   const int32_t* slots;
   const int32_t* slot_indptr;
   float softmax_scale, q_scale, kv_scale;
+  const float* kv_scales = nullptr;  // group scales of the cache, or null
+  int32_t scale_group = 0;
 };
 
 mla_status_t check_inputs(const mla_plan_t* plan, const Inputs& in) {
@@ -106,6 +108,17 @@ mla_status_t check_inputs(const mla_plan_t* plan, const Inputs& in) {
   return MLA_OK;
 }
 
+// The arguments that a call with group scales adds.
+mla_status_t check_group_scales(const mla_plan_t* plan, const float* kv_scales, int32_t scale_group) {
+  if (plan == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla_problem_t& p = plan->prob;
+  if (p.kv_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (p.block_size <= 0 || scale_group <= 0 || p.block_size % scale_group != 0) return MLA_ERR_INVALID_ARG;
+  if (p.num_tokens == 0) return MLA_OK;
+  if (kv_scales == nullptr || !aligned(kv_scales, 4)) return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
 mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   const mla_problem_t& p = plan->prob;
   mla::DecodeParams d{};
@@ -127,6 +140,8 @@ mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   d.row_tiles = plan->row_tiles;
   d.score_scale_log2 = in.softmax_scale * in.q_scale * in.kv_scale * 1.4426950408889634f;
   d.kv_scale = in.kv_scale;
+  d.kv_scales = in.kv_scales;
+  d.scale_group = in.scale_group;
   d.wait_ns = plan->wait_limit_us > 0 ? static_cast<uint64_t>(plan->wait_limit_us) * 1000ull : 0ull;
   return d;
 }
@@ -288,6 +303,73 @@ mla_status_t run_merge_items(const mla_plan_t* plan, const Inputs& in, const flo
   m.tile_rows = plan->tile_rows;
   m.sparse = sp.sparse;
   return cuda_status(mla::launch_merge(m, stream));
+}
+
+// ---- whole calls, with or without group scales
+
+mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* sinks, void* workspace,
+                        size_t workspace_bytes, void* out, float* lse, cudaStream_t stream) {
+  mla_status_t s = check_inputs(plan, in);
+  if (s != MLA_OK) return s;
+  const mla_problem_t& p = plan->prob;
+  if ((sinks != nullptr) != (p.has_sinks == 1)) return MLA_ERR_INVALID_ARG;
+  if (p.num_tokens == 0) return MLA_OK;
+  if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (sinks != nullptr && !aligned(sinks, 4)) return MLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < plan->workspace_bytes) return MLA_ERR_WORKSPACE;
+  if (!aligned(workspace, kWsAlign)) return MLA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int* status = reinterpret_cast<int*>(ws + plan->status_offset);
+  mla::DecodeParams d = make_params(plan, in);
+  if (plan->schedule == 1) {
+    s = run_schedule(plan, in, ws, stream);
+    if (s == MLA_OK) s = run_items(plan, in, sinks, ws, out, lse, stream);
+    if (s == MLA_OK) s = run_merge_items(plan, in, sinks, ws, out, lse, stream);
+    return s;
+  }
+  if (plan->num_segments == 1) {
+    d.final_mode = 1;
+    d.sinks = sinks;
+    d.out = out;
+    d.lse = lse;
+    return launch_decode(plan, d, status, stream);
+  }
+  d.final_mode = 0;
+  d.segm_out = reinterpret_cast<float*>(ws + plan->segm_output_offset);
+  d.segm_max = reinterpret_cast<float*>(ws + plan->segm_max_offset);
+  d.segm_expsum = reinterpret_cast<float*>(ws + plan->segm_expsum_offset);
+  s = launch_decode(plan, d, status, stream);
+  if (s != MLA_OK) return s;
+  mla::MergeParams m{};
+  m.segm_out = d.segm_out;
+  m.segm_max = d.segm_max;
+  m.segm_expsum = d.segm_expsum;
+  m.part = part_lens_for(plan, in);
+  m.num_tokens = p.num_tokens;
+  m.num_heads = p.num_heads;
+  m.num_segments = plan->num_segments;
+  m.rank = kRank;
+  m.tile_size = plan->tile_size;
+  m.sinks = sinks;
+  m.out = out;
+  m.lse = lse;
+  return cuda_status(mla::launch_merge(m, stream));
+}
+
+mla_status_t decode_items(const mla_plan_t* plan, const Inputs& in, const float* sinks, void* workspace,
+                          size_t workspace_bytes, void* out, float* lse, cudaStream_t stream) {
+  mla_status_t s = check_scheduled(plan, workspace, workspace_bytes);
+  if (s != MLA_OK) return s;
+  s = check_inputs(plan, in);
+  if (s != MLA_OK) return s;
+  const mla_problem_t& p = plan->prob;
+  if ((sinks != nullptr) != (p.has_sinks == 1)) return MLA_ERR_INVALID_ARG;
+  if (p.num_tokens == 0) return MLA_OK;
+  if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (sinks != nullptr && !aligned(sinks, 4)) return MLA_ERR_INVALID_ARG;
+  return run_items(plan, in, sinks, static_cast<uint8_t*>(workspace), out, lse, stream);
 }
 
 }  // namespace
@@ -468,52 +550,22 @@ mla_status_t mla_decode_fwd(const mla_plan_t* plan, const void* q, const void* k
                             void* out, float* lse, cudaStream_t stream) {
   const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr,
                   sparse_slots, sparse_indptr, softmax_scale, q_scale, kv_scale};
-  mla_status_t s = check_inputs(plan, in);
+  return decode_fwd(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q, const void* kv_cache,
+                                   const float* kv_scales, int32_t scale_group,
+                                   const int32_t* block_table, int64_t block_table_stride,
+                                   const int32_t* seq_lens, const int32_t* qo_indptr,
+                                   const int32_t* sparse_slots, const int32_t* sparse_indptr,
+                                   float softmax_scale, float q_scale, const float* sinks,
+                                   void* workspace, size_t workspace_bytes, void* out, float* lse,
+                                   cudaStream_t stream) {
+  const mla_status_t s = check_group_scales(plan, kv_scales, scale_group);
   if (s != MLA_OK) return s;
-  const mla_problem_t& p = plan->prob;
-  if ((sinks != nullptr) != (p.has_sinks == 1)) return MLA_ERR_INVALID_ARG;
-  if (p.num_tokens == 0) return MLA_OK;
-  if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
-    return MLA_ERR_INVALID_ARG;
-  if (sinks != nullptr && !aligned(sinks, 4)) return MLA_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < plan->workspace_bytes) return MLA_ERR_WORKSPACE;
-  if (!aligned(workspace, kWsAlign)) return MLA_ERR_INVALID_ARG;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int* status = reinterpret_cast<int*>(ws + plan->status_offset);
-  mla::DecodeParams d = make_params(plan, in);
-  if (plan->schedule == 1) {
-    s = run_schedule(plan, in, ws, stream);
-    if (s == MLA_OK) s = run_items(plan, in, sinks, ws, out, lse, stream);
-    if (s == MLA_OK) s = run_merge_items(plan, in, sinks, ws, out, lse, stream);
-    return s;
-  }
-  if (plan->num_segments == 1) {
-    d.final_mode = 1;
-    d.sinks = sinks;
-    d.out = out;
-    d.lse = lse;
-    return launch_decode(plan, d, status, stream);
-  }
-  d.final_mode = 0;
-  d.segm_out = reinterpret_cast<float*>(ws + plan->segm_output_offset);
-  d.segm_max = reinterpret_cast<float*>(ws + plan->segm_max_offset);
-  d.segm_expsum = reinterpret_cast<float*>(ws + plan->segm_expsum_offset);
-  s = launch_decode(plan, d, status, stream);
-  if (s != MLA_OK) return s;
-  mla::MergeParams m{};
-  m.segm_out = d.segm_out;
-  m.segm_max = d.segm_max;
-  m.segm_expsum = d.segm_expsum;
-  m.part = part_lens_for(plan, in);
-  m.num_tokens = p.num_tokens;
-  m.num_heads = p.num_heads;
-  m.num_segments = plan->num_segments;
-  m.rank = kRank;
-  m.tile_size = plan->tile_size;
-  m.sinks = sinks;
-  m.out = out;
-  m.lse = lse;
-  return cuda_status(mla::launch_merge(m, stream));
+  const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr, sparse_slots,
+                  sparse_indptr, softmax_scale, q_scale, 1.f, kv_scales, scale_group};
+  return decode_fwd(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
 }
 
 mla_status_t mla_workspace_status(const mla_plan_t* plan, const void* workspace, int32_t* code,
@@ -559,17 +611,22 @@ mla_status_t mla_decode_items(const mla_plan_t* plan, const void* q, const void*
                               void* out, float* lse, cudaStream_t stream) {
   const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr,
                   sparse_slots, sparse_indptr, softmax_scale, q_scale, kv_scale};
-  mla_status_t s = check_scheduled(plan, workspace, workspace_bytes);
+  return decode_items(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_items_scaled(const mla_plan_t* plan, const void* q, const void* kv_cache,
+                                     const float* kv_scales, int32_t scale_group,
+                                     const int32_t* block_table, int64_t block_table_stride,
+                                     const int32_t* seq_lens, const int32_t* qo_indptr,
+                                     const int32_t* sparse_slots, const int32_t* sparse_indptr,
+                                     float softmax_scale, float q_scale, const float* sinks,
+                                     void* workspace, size_t workspace_bytes, void* out, float* lse,
+                                     cudaStream_t stream) {
+  const mla_status_t s = check_group_scales(plan, kv_scales, scale_group);
   if (s != MLA_OK) return s;
-  s = check_inputs(plan, in);
-  if (s != MLA_OK) return s;
-  const mla_problem_t& p = plan->prob;
-  if ((sinks != nullptr) != (p.has_sinks == 1)) return MLA_ERR_INVALID_ARG;
-  if (p.num_tokens == 0) return MLA_OK;
-  if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4))
-    return MLA_ERR_INVALID_ARG;
-  if (sinks != nullptr && !aligned(sinks, 4)) return MLA_ERR_INVALID_ARG;
-  return run_items(plan, in, sinks, static_cast<uint8_t*>(workspace), out, lse, stream);
+  const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr, sparse_slots,
+                  sparse_indptr, softmax_scale, q_scale, 1.f, kv_scales, scale_group};
+  return decode_items(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
 }
 
 mla_status_t mla_merge_items(const mla_plan_t* plan, const int32_t* qo_indptr, const float* sinks,
@@ -711,6 +768,74 @@ mla_status_t mla_fit_kpool_indices(const int32_t* token_indices, int64_t ti_row_
   if (o0 < in1 && in0 < o1) return MLA_ERR_INVALID_ARG;
   return cuda_status(mla::launch_fit_kpool(token_indices, ti_row_stride, num_tokens, width, topk, out,
                                            out_row_stride, stream));
+}
+
+mla_status_t mla_block_tables(const int32_t* query_start_loc, const int32_t* seq_lens,
+                              int32_t num_reqs, int32_t num_tokens, int32_t block_size,
+                              const int32_t* free_blocks, int32_t num_free, int32_t* block_table,
+                              int64_t block_table_stride, int32_t max_blocks_per_req,
+                              int32_t* slot_mapping, int32_t* req_id, int32_t* positions,
+                              int32_t* taken, cudaStream_t stream) {
+  if (num_reqs < 0 || num_tokens < 0 || block_size <= 0 || num_free < 0 || max_blocks_per_req <= 0)
+    return MLA_ERR_INVALID_ARG;
+  if (block_table_stride < max_blocks_per_req) return MLA_ERR_INVALID_ARG;
+  if (query_start_loc == nullptr || taken == nullptr || !aligned(query_start_loc, 4) || !aligned(taken, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (num_reqs > 0 && (seq_lens == nullptr || block_table == nullptr || !aligned(seq_lens, 4) ||
+                       !aligned(block_table, 4)))
+    return MLA_ERR_INVALID_ARG;
+  if (num_free > 0 && (free_blocks == nullptr || !aligned(free_blocks, 4))) return MLA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (slot_mapping == nullptr || !aligned(slot_mapping, 4))) return MLA_ERR_INVALID_ARG;
+  if ((req_id != nullptr && !aligned(req_id, 4)) || (positions != nullptr && !aligned(positions, 4)))
+    return MLA_ERR_INVALID_ARG;
+  mla::BlockTableParams p{};
+  p.qsl = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.num_reqs = num_reqs;
+  p.num_tokens = num_tokens;
+  p.block_size = block_size;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.block_table = block_table;
+  p.bt_stride = block_table_stride;
+  p.cols = max_blocks_per_req;
+  p.slots = slot_mapping;
+  p.req_id = req_id;
+  p.positions = positions;
+  p.taken = taken;
+  return cuda_status(mla::launch_block_tables(p, stream));
+}
+
+mla_status_t mla_cache_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe,
+                              int64_t k_pe_stride, const int32_t* slot_mapping, int32_t num_tokens,
+                              int32_t num_blocks, int32_t block_size, int32_t scale_group,
+                              void* kv_cache, float* kv_scales, cudaStream_t stream) {
+  if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || scale_group <= 0 ||
+      block_size % scale_group != 0)
+    return MLA_ERR_INVALID_ARG;
+  const int64_t num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  if (num_slots > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MLA_OK;
+  if (c_kv == nullptr || k_pe == nullptr || slot_mapping == nullptr || kv_cache == nullptr ||
+      kv_scales == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (c_kv_stride < kRank || k_pe_stride < kHeadDim - kRank) return MLA_ERR_INVALID_ARG;
+  // 16-byte vector accesses of every 8-column group
+  if (!aligned(c_kv, 16) || !aligned(k_pe, 16) || !aligned(kv_cache, 16) || c_kv_stride % 8 ||
+      k_pe_stride % 8 || !aligned(slot_mapping, 4) || !aligned(kv_scales, 4))
+    return MLA_ERR_INVALID_ARG;
+  mla::AppendParams p{};
+  p.c_kv = c_kv;
+  p.c_stride = c_kv_stride;
+  p.k_pe = k_pe;
+  p.pe_stride = k_pe_stride;
+  p.slots = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.num_slots = static_cast<int32_t>(num_slots);
+  p.group = scale_group;
+  p.cache = kv_cache;
+  p.scales = kv_scales;
+  return cuda_status(mla::launch_cache_append(p, stream));
 }
 
 mla_status_t mla_sparse_index_convert(const int32_t* req_id, const int32_t* block_table,

@@ -24,6 +24,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
                "r"(src_bytes)
                : "memory");
 }
+// 4-byte global -> shared copy; src_bytes == 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::: "memory");
 }
@@ -91,6 +96,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
   return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// A key of a cache with group scales, as the softmax takes it. With s the
+// group's scale, s2 the key's base-2 score factor times the raw score q . c
+// (c the codes), and t = s2 s + log2 s, the weights 2^(t - m) multiply the
+// codes themselves in P.V and, divided by s, sum to the denominator:
+//   out = sum 2^(t - m) c / sum 2^(t - m) / s,  lse = ln 2 (m + log2 sum).
+// So the values' scale costs one addition in the exponent, P.V keeps 8-bit
+// operands, and the largest 2^(t - m) |c| of a row decides the range of P.
+struct KeyScale {
+  float mul;  // score factor times s
+  float add;  // log2 s
+  float inv;  // 1 / s
+};
+__device__ __forceinline__ KeyScale key_scale(float s, float score_scale_log2) {
+  KeyScale k;
+  k.mul = s * score_scale_log2;
+  k.add = log2f(s);
+  k.inv = 1.f / s;
+  return k;
 }
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }

@@ -27,7 +27,9 @@
 // shared memory; p = 2^(s - m_ref + 4) with a reference max m_ref that moves
 // only when a chunk max exceeds it by more than 4 (O^T is then rescaled in
 // TMEM), so p <= 2^8 fits e4m3 and the bulk of the weights stays in its
-// normal range; the true max is kept for the partials.
+// normal range; the true max is kept for the partials. With group scales (GS)
+// the thread's key has one scale, which enters its scores and the row sums
+// (KeyScale); everything else is the same.
 //
 // Requests of 65..128 rows run on a thread-block cluster of CL = 2 CTAs, CTA
 // r owning rows [r NR, (r + 1) NR) of the row tile: every key box is read
@@ -548,7 +550,7 @@ __device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32
 // [h NH, (h + 1) NH) of the CTA's rows, h = (w - 4) / 4, NH = NR / 2.
 // Thread t8 < 64 (warps 4, 5) also owns row t8's reference and true maxima
 // and causal end, which it resets for the next item in each epilogue.
-template <int NR, int CL>
+template <int NR, int CL, bool GS>
 __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParams& p) {
   using C = HnCfg<NR>;
   constexpr int NH = NR / 2;
@@ -579,7 +581,29 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
     float l[NH];
 #pragma unroll
     for (int n = 0; n < NH; ++n) l[n] = 0.f;
+    // GS: the cache row of this thread's key two chunks ahead and the scale
+    // of its group one chunk ahead, so that neither read is waited for
+    const int32_t* bt_row = p.block_table + static_cast<int64_t>(it.unit) * p.bt_stride;
+    auto key_row = [&](int ch) {
+      const int kp = it.seg_start + ch * kKeys + k;
+      return ch < it.n_chunks && kp < it.seg_end ? cache_row(p, bt_row, kp) : -1;
+    };
+    auto row_scale = [&](int row) {  // 1 for a key that does not exist
+      return row >= 0 ? p.kv_scales[static_cast<uint32_t>(row) / static_cast<uint32_t>(p.scale_group)] : 1.f;
+    };
+    float sc_next = 1.f;
+    int row_next = -1;
+    if constexpr (GS) {
+      sc_next = row_scale(key_row(0));
+      row_next = key_row(1);
+    }
     for (int c = 0; c < it.n_chunks && ok; ++c, ++g) {
+      KeyScale kq{};
+      if constexpr (GS) {
+        kq = key_scale(sc_next, scale2);
+        sc_next = row_scale(row_next);
+        row_next = key_row(c + 2);
+      }
       const int b = g & 1;
       const uint32_t par = (g >> 1) & 1;
       ok = warp_wait(x, x.bar(kSFull + b), par, 31);
@@ -591,6 +615,10 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(x.bar(kSFree + b));  // QK^T two chunks on may overwrite it
+      if constexpr (GS) {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) s[n] = fmaf(s[n], kq.mul, kq.add);
+      }
       // keys that exist (inside the segment) and that each row may see; a
       // chunk inside the segment and before every row's causal end needs no mask
       const int pos = it.seg_start + c * kKeys + k;
@@ -602,8 +630,8 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
         for (int n = 0; n < NH; ++n)
           if (!(key_ok && (!causal || pos < vis[r0 + n]))) s[n] = -INFINITY;
       }
-      // chunk max of every row over the raw scores (scale2 > 0): this warp's
-      // 32 keys, then the four lane quarters
+      // chunk max of every row over the raw scores (scale2 > 0; GS: the
+      // scaled ones): this warp's 32 keys, then the four lane quarters
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
         const float r = warp_max_f32(s[n]);
@@ -621,7 +649,8 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
       if (lane < NH) {
         const int r = r0 + lane;
         const float* w = wmax + b * 256 + r;
-        const float mc = fmaxf(fmaxf(w[0], w[64]), fmaxf(w[128], w[192])) * scale2;
+        const float mraw = fmaxf(fmaxf(w[0], w[64]), fmaxf(w[128], w[192]));
+        const float mc = GS ? mraw : mraw * scale2;
         const float mo = mref[(b ^ 1) * 64 + r];
         mt[r] = fmaxf(mtrue[(b ^ 1) * 64 + r], mc);
         float a = 1.f, m = mo;
@@ -689,10 +718,10 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
             const float2 m2 = *reinterpret_cast<const float2*>(mr + r0 + n);
             const float b0 = m2.x == -INFINITY ? 0.f : m2.x - kPBias;
             const float b1 = m2.y == -INFINITY ? 0.f : m2.y - kPBias;
-            const float p0 = fast_exp2(fmaf(s[n], scale2, -b0));
-            const float p1 = fast_exp2(fmaf(s[n + 1], scale2, -b1));
-            l[n] += p0;
-            l[n + 1] += p1;
+            const float p0 = fast_exp2(GS ? s[n] - b0 : fmaf(s[n], scale2, -b0));
+            const float p1 = fast_exp2(GS ? s[n + 1] - b1 : fmaf(s[n + 1], scale2, -b1));
+            l[n] = GS ? fmaf(p0, kq.inv, l[n]) : l[n] + p0;
+            l[n + 1] = GS ? fmaf(p1, kq.inv, l[n + 1]) : l[n + 1] + p1;
             p_terms(p0, p1, hc[e], lc[e]);
           }
           hw[q] = hc[0] | (hc[1] << 16);
@@ -879,7 +908,7 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
   __syncwarp();
 }
 
-template <int NR, int CL>
+template <int NR, int CL, bool GS>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_hn_kernel(const __grid_constant__ HnMaps maps, const DecodeParams p, int* status) {
   using C = HnCfg<NR>;
@@ -966,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (x.warp == 3) {
     pv_issue<NR, CL>(x, p);
   } else {
-    softmax_rows<NR, CL>(x, maps, p);
+    softmax_rows<NR, CL, GS>(x, maps, p);
   }
 
   __syncwarp();
@@ -999,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CL > 1) cluster_sync();
 }
 
-template <int NR, int CL>
+template <int NR, int CL, bool GS>
 cudaError_t prepare(int* smem_bytes) {
   using C = HnCfg<NR>;
   static std::atomic<uint64_t> done{0};
@@ -1008,7 +1037,7 @@ cudaError_t prepare(int* smem_bytes) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(decode_hn_kernel<NR, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_hn_kernel<NR, CL, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -1016,11 +1045,11 @@ cudaError_t prepare(int* smem_bytes) {
   return cudaSuccess;
 }
 
-template <int NR, int CL>
+template <int NR, int CL, bool GS>
 cudaError_t launch_rows(const HnMaps& maps, const DecodeParams& p, dim3 grid, int* status,
                         cudaStream_t stream) {
   int smem = 0;
-  cudaError_t e = prepare<NR, CL>(&smem);
+  cudaError_t e = prepare<NR, CL, GS>(&smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -1041,13 +1070,22 @@ cudaError_t launch_rows(const HnMaps& maps, const DecodeParams& p, dim3 grid, in
   // kernel's griddepcontrol.wait is then a no-op)
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, decode_hn_kernel<NR, CL>, maps, p, status);
+  return cudaLaunchKernelEx(&cfg, decode_hn_kernel<NR, CL, GS>, maps, p, status);
 }
 
+template <int NR, int CL>
+cudaError_t launch_scaled(const HnMaps& maps, const DecodeParams& p, dim3 grid, int* status,
+                          cudaStream_t stream) {
+  return p.kv_scales != nullptr ? launch_rows<NR, CL, true>(maps, p, grid, status, stream)
+                                : launch_rows<NR, CL, false>(maps, p, grid, status, stream);
+}
+
+// (the group-scaled variant has the same threads, shared memory and cluster,
+// and registers for one CTA per SM either way)
 template <int NR>
 cudaError_t max_pairs(int* n) {
   int smem = 0;
-  cudaError_t e = prepare<NR, 2>(&smem);
+  cudaError_t e = prepare<NR, 2, false>(&smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2, 1, 1);
@@ -1060,7 +1098,7 @@ cudaError_t max_pairs(int* n) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, decode_hn_kernel<NR, 2>, &cfg);
+  return cudaOccupancyMaxActiveClusters(n, decode_hn_kernel<NR, 2, false>, &cfg);
 }
 
 }  // namespace
@@ -1088,17 +1126,17 @@ cudaError_t launch_decode_hn(const DecodeParams& p, int rows, int cluster, int64
   }
   if (cluster == 1) {
     switch (rows) {
-      case 16: return launch_rows<16, 1>(maps, p, grid, status, stream);
-      case 32: return launch_rows<32, 1>(maps, p, grid, status, stream);
-      case 48: return launch_rows<48, 1>(maps, p, grid, status, stream);
-      case 64: return launch_rows<64, 1>(maps, p, grid, status, stream);
+      case 16: return launch_scaled<16, 1>(maps, p, grid, status, stream);
+      case 32: return launch_scaled<32, 1>(maps, p, grid, status, stream);
+      case 48: return launch_scaled<48, 1>(maps, p, grid, status, stream);
+      case 64: return launch_scaled<64, 1>(maps, p, grid, status, stream);
       default: return cudaErrorInvalidValue;
     }
   }
   if (cluster == 2) {
     switch (rows) {
-      case 48: return launch_rows<48, 2>(maps, p, grid, status, stream);
-      case 64: return launch_rows<64, 2>(maps, p, grid, status, stream);
+      case 48: return launch_scaled<48, 2>(maps, p, grid, status, stream);
+      case 64: return launch_scaled<64, 2>(maps, p, grid, status, stream);
       default: return cudaErrorInvalidValue;
     }
   }

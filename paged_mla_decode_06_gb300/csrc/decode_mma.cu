@@ -16,7 +16,8 @@
 //            512 columns of the same shared-memory rows.
 // bf16 inputs use bf16 MMAs; e4m3 inputs are widened exactly to f16 in
 // shared memory and use f16 MMAs (scores are rescaled by q_scale * kv_scale,
-// values by kv_scale).
+// values by kv_scale). With group scales (GS) the scale of each key's slot
+// travels through the ring beside its row and enters the softmax (KeyScale).
 //
 // Epilogue: either the segment's base-2 partials (m2, l, O / l), the format
 // of the rocm_aiter_mla_merge page, or -- when the whole row is one segment
@@ -41,8 +42,9 @@ constexpr int kWarps = 8;
 constexpr int kQStride = kHeadDim + 8;   // 16-bit elements per smem row (1168 B, conflict-free)
 constexpr int kRawStride = kHeadDim + 16;  // bytes per raw fp8 smem row
 
-template <int RG, bool FP8>
+template <int RG, bool FP8, bool GS = false>
 struct Cfg {
+  static_assert(FP8 || !GS, "group scales belong to the e4m3 cache");
   static constexpr int kRows = 16 * RG;
   static constexpr int kCS = kWarps / RG;            // warps sharing a row group
   static constexpr int kKC = (RG == 1) ? 64 : 32;    // keys per chunk
@@ -64,15 +66,16 @@ struct Cfg {
   static constexpr int kOffP = kOffCompute + kComputeBytes;
   static constexpr int kOffRed = kOffP + kPBytes;
   static constexpr int kOffOk = kOffRed + kRedBytes;
-  static constexpr int kSmem = kOffOk + kOkBytes;
+  static constexpr int kOffScale = kOffOk + kOkBytes;  // GS: the scale of each ring key
+  static constexpr int kSmem = kOffScale + (GS ? kOkBytes : 0);
   static_assert(kNTS >= 1 && kKW % 8 == 0, "key slice per warp must be whole n-tiles");
   static_assert(kNTV % 2 == 0, "value slice must be an even number of n-tiles");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-template <int RG, bool FP8>
+template <int RG, bool FP8, bool GS>
 __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodeParams p) {
-  using C = Cfg<RG, FP8>;
+  using C = Cfg<RG, FP8, GS>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x;
   const int lane = tid & 31;
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
   uint8_t* sP = smem + C::kOffP;
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   int* key_ok = reinterpret_cast<int*>(smem + C::kOffOk);
+  float* key_sc = reinterpret_cast<float*>(smem + C::kOffScale);
 
   // Rows of this thread: r_a = rg*16 + lane/4 and r_a + 8 (within the tile).
   const int ra = rg * 16 + (lane >> 2);
@@ -189,6 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       cp_async_16(smem_u32(dst + k * kRowStrideB + part * 16),
                   live ? kvbytes + slot * row_bytes + part * 16 : kvbytes, live ? 16u : 0u);
       if (part == 0) ok[k] = live ? 1 : 0;
+      if constexpr (GS)
+        if (part == 1)
+          cp_async_4(smem_u32(key_sc + stage * C::kKC + k),
+                     live ? p.kv_scales + static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.scale_group)
+                          : p.kv_scales,
+                     live ? 4u : 0u);
     }
   };
 
@@ -264,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
     // ---- mask, chunk max
     const int c0 = seg_start + c * C::kKC;
     float mx[2] = {-INFINITY, -INFINITY};
+    float inv[C::kNTS][2];  // GS: 1 / scale of this thread's keys, 0 where there is none
 #pragma unroll
     for (int n = 0; n < C::kNTS; ++n) {
 #pragma unroll
@@ -271,8 +282,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
         const int kl = cs * C::kKW + n * 8 + 2 * (lane & 3) + e;
         const int pos = c0 + kl;
         const bool live = ok[kl] != 0;
-        const float s0 = (live && pos < vis[0]) ? sacc[n][e] * scale2 : -INFINITY;
-        const float s1 = (live && pos < vis[1]) ? sacc[n][2 + e] * scale2 : -INFINITY;
+        float f0 = sacc[n][e] * scale2, f1 = sacc[n][2 + e] * scale2;
+        if constexpr (GS) {
+          const KeyScale ks = key_scale(live ? key_sc[stage * C::kKC + kl] : 1.f, scale2);
+          f0 = fmaf(sacc[n][e], ks.mul, ks.add);
+          f1 = fmaf(sacc[n][2 + e], ks.mul, ks.add);
+          inv[n][e] = ks.inv;
+        }
+        const float s0 = (live && pos < vis[0]) ? f0 : -INFINITY;
+        const float s1 = (live && pos < vis[1]) ? f1 : -INFINITY;
         sacc[n][e] = s0;
         sacc[n][2 + e] = s1;
         mx[0] = fmaxf(mx[0], s0);
@@ -309,8 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       const float p01 = fast_exp2(sacc[n][1] - base[0]);
       const float p10 = fast_exp2(sacc[n][2] - base[1]);
       const float p11 = fast_exp2(sacc[n][3] - base[1]);
-      psum[0] += p00 + p01;
-      psum[1] += p10 + p11;
+      if constexpr (GS) {
+        psum[0] = fmaf(p00, inv[n][0], fmaf(p01, inv[n][1], psum[0]));
+        psum[1] = fmaf(p10, inv[n][0], fmaf(p11, inv[n][1], psum[1]));
+      } else {
+        psum[0] += p00 + p01;
+        psum[1] += p10 + p11;
+      }
       const int col = cs * C::kKW + n * 8 + 2 * (lane & 3);
       *reinterpret_cast<uint32_t*>(sP + (ra * C::kPStride + col) * 2) = pack2<FP8>(p00, p01);
       *reinterpret_cast<uint32_t*>(sP + ((ra + 8) * C::kPStride + col) * 2) = pack2<FP8>(p10, p11);
@@ -427,13 +450,13 @@ cudaError_t ensure_smem_limit(K kernel, int bytes, std::atomic<uint64_t>& done) 
   return e;
 }
 
-template <int RG, bool FP8>
+template <int RG, bool FP8, bool GS = false>
 cudaError_t launch_variant(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
-  using C = Cfg<RG, FP8>;
+  using C = Cfg<RG, FP8, GS>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = ensure_smem_limit(decode_mma_kernel<RG, FP8>, C::kSmem, done);
+  cudaError_t e = ensure_smem_limit(decode_mma_kernel<RG, FP8, GS>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  decode_mma_kernel<RG, FP8><<<grid, kThreads, C::kSmem, stream>>>(p);
+  decode_mma_kernel<RG, FP8, GS><<<grid, kThreads, C::kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -450,6 +473,15 @@ int decode_mma_smem_bytes(int32_t kernel, bool fp8) {
 
 cudaError_t launch_decode_mma(int32_t kernel, bool fp8, const DecodeParams& p, dim3 grid,
                               cudaStream_t stream) {
+  if (p.kv_scales != nullptr) {
+    if (!fp8) return cudaErrorNotSupported;
+    switch (kernel) {
+      case kMmaRows16: return launch_variant<1, true, true>(p, grid, stream);
+      case kMmaRows32: return launch_variant<2, true, true>(p, grid, stream);
+      case kMmaRows64: return launch_variant<4, true, true>(p, grid, stream);
+      default: return cudaErrorInvalidValue;
+    }
+  }
   switch (kernel) {
     case kMmaRows16: return fp8 ? launch_variant<1, true>(p, grid, stream) : launch_variant<1, false>(p, grid, stream);
     case kMmaRows32: return fp8 ? launch_variant<2, true>(p, grid, stream) : launch_variant<2, false>(p, grid, stream);

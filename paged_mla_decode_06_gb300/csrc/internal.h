@@ -48,6 +48,10 @@ struct DecodeParams {
   // bounded waits of the tensor-core kernels give up after this many
   // nanoseconds (0: the default, 2 s)
   uint64_t wait_ns;
+  // e4m3 cache with a scale for each group of `scale_group` slots of a block:
+  // slot s is scaled by kv_scales[s / scale_group]; null: kv_scale alone
+  const float* kv_scales;
+  int32_t scale_group;
 };
 
 // Balanced work list (sched.cu).
@@ -136,6 +140,38 @@ cudaError_t launch_sparse_seqlen(const int32_t* qsl, const int32_t* seq_lens, in
                                  cudaStream_t stream);
 cudaError_t launch_fit_kpool(const int32_t* ti, int64_t ti_stride, int32_t num_tokens, int32_t width,
                              int32_t topk, int32_t* out, int64_t out_stride, cudaStream_t stream);
+
+// Block tables and slot maps (block_tables.cu).
+struct BlockTableParams {
+  const int32_t* qsl;          // [R+1]
+  const int32_t* seq_lens;     // [R]
+  int32_t num_reqs, num_tokens, block_size;
+  const int32_t* free_blocks;  // [num_free]
+  int32_t num_free;
+  int32_t* block_table;        // [R, cols]
+  int64_t bt_stride;
+  int32_t cols;
+  int32_t* slots;              // [T]
+  int32_t* req_id;             // [T] or null
+  int32_t* positions;          // [T] or null
+  int32_t* taken;              // [1]
+};
+
+cudaError_t launch_block_tables(const BlockTableParams& p, cudaStream_t stream);
+
+// Append to a cache with group scales (cache_append.cu).
+struct AppendParams {
+  const void* c_kv;            // [T, 512] bf16, row stride in elements
+  int64_t c_stride;
+  const void* k_pe;            // [T, 64] bf16
+  int64_t pe_stride;
+  const int32_t* slots;        // [T]
+  int32_t num_tokens, num_slots, group;
+  void* cache;                 // [num_slots, 576] e4m3
+  float* scales;               // [num_slots / group]
+};
+
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
 
 // tcgen05 CTA-pair kernel: q_rows / kv_rows are the row counts of the q
 // and cache tensors viewed as [rows, 576]; status (may be null) receives a

@@ -342,92 +342,109 @@ def mla_sparse_seqlen(query_start_loc, seq_lens, *, topk: int, indptr, lens=None
 
 
 # The calls over a cache with group scales check what their pointers cannot
-# tell the library: element type, device and density of each tensor.
+# tell the library: element type, shape, device and density of each tensor.
+# Each check is one chain of cheap reads (a call costs the host about as much
+# as its launch); only a call that fails it works out which tensor is at fault.
 
-def _need(cond: bool, fn: str, what: str):
-    if not cond:
-        raise MLAError(fn, MLA_ERR_INVALID_ARG, what)
+_torch = None
 
 
-def _need_dense(fn: str, device, **tensors):
-    for name, t in tensors.items():
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _refuse(fn: str, device: int, tensors, rules):
+    """Raise for the first tensor or rule that does not hold: ``tensors`` is
+    [(name, tensor, dtypes)], ``rules`` [(holds, what)]."""
+    def need(cond, what):
+        if not cond:
+            raise MLAError(fn, MLA_ERR_INVALID_ARG, what)
+
+    need(device >= 0, "the tensors must be on a CUDA device")
+    need(device == _torch.cuda.current_device(), f"cuda:{device} is not the current device")
+    for name, t, dtypes in tensors:
         if t is not None:
-            _need(t.is_contiguous(), fn, f"{name} must be contiguous")
-            _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
+            need(t.get_device() == device, f"{name} is on {t.device}, not cuda:{device}")
+            need(t.dtype in dtypes, f"{name} must be {' or '.join(str(d) for d in dtypes)}")
+    for holds, what in rules:
+        need(holds, what)
+    need(False, "bad arguments")
 
 
-def _need_int32(fn: str, device, **tensors):
-    import torch
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t.dtype == torch.int32, fn, f"{name} must be int32")
-    _need_dense(fn, device, **tensors)
-
-
-def _need_current(fn: str, device):
-    import torch
-    _need(device.type == "cuda", fn, "the tensors must be on a CUDA device")
-    _need(device.index == torch.cuda.current_device(), fn, f"{device} is not the current device")
-
-
-def _need_scaled_cache(fn: str, device, kv_cache, kv_scales, scale_group: int):
-    import torch
-    _need(kv_cache.dtype in (torch.float8_e4m3fn, torch.uint8), fn, "kv_cache must hold e4m3 codes")
-    _need(kv_cache.dim() == 3 and kv_cache.shape[2] == HEAD_DIM, fn,
-          f"kv_cache must be [num_blocks, block_size, {HEAD_DIM}]")
-    _need(kv_scales.dtype == torch.float32, fn, "kv_scales must be float32")
-    nb, bs = kv_cache.shape[0], kv_cache.shape[1]
-    _need(scale_group > 0 and bs % scale_group == 0, fn, "scale_group must divide the block size")
-    _need(kv_scales.numel() == nb * bs // scale_group, fn,
-          "kv_scales must hold num_blocks * block_size / scale_group scales")
-    _need_dense(fn, device, kv_cache=kv_cache, kv_scales=kv_scales)
+def _dense_rows(t, min_cols: int) -> bool:
+    """``t`` is a matrix of rows that are dense and do not overlap."""
+    rows, cols = t.shape
+    row_stride, col_stride = t.stride()
+    return cols >= min_cols and (rows == 0 or ((col_stride == 1 or cols == 1)
+                                               and (rows == 1 or row_stride >= cols)))
 
 
 def _scaled_args(fn: str, plan: Plan, q, kv_cache, kv_scales, scale_group, block_table,
                  block_table_stride, seq_lens, qo_indptr, sparse_slots, sparse_indptr,
                  softmax_scale, q_scale, sinks, workspace, out, lse, stream):
-    import torch
-    dev = q.device
+    torch = _torch or _load_torch()
+    dev = q.get_device()
     pr = plan.prob
-    _need_current(fn, dev)
-    if pr.kv_dtype != MLA_DTYPE_FP8_E4M3:
-        raise MLAError(fn, MLA_ERR_UNSUPPORTED, "the plan's cache is not e4m3")
-    _need_scaled_cache(fn, dev, kv_cache, kv_scales, scale_group)
-    _need(kv_cache.shape[0] == pr.num_blocks and kv_cache.shape[1] == pr.block_size, fn,
-          "kv_cache is not the plan's")
-    _need(q.dtype in (torch.float8_e4m3fn, torch.uint8), fn, "q must hold e4m3 codes")
-    _need(tuple(q.shape) == (pr.num_tokens, pr.num_heads, HEAD_DIM), fn, "q is not the plan's")
-    _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (pr.num_tokens, pr.num_heads, KV_LORA_RANK),
-          fn, f"out must be bfloat16 [num_tokens, num_heads, {KV_LORA_RANK}]")
-    _need(lse.dtype == torch.float32 and tuple(lse.shape) == (pr.num_tokens, pr.num_heads), fn,
-          "lse must be float32 [num_tokens, num_heads]")
-    _need_dense(fn, dev, q=q, out=out, lse=lse, workspace=workspace)
-    if sinks is not None:
-        _need(sinks.dtype == torch.float32 and sinks.numel() == pr.num_heads, fn,
-              "sinks must be float32 [num_heads]")
-        _need_dense(fn, dev, sinks=sinks)
-    _need_int32(fn, dev, seq_lens=seq_lens, qo_indptr=qo_indptr, sparse_slots=sparse_slots,
-                sparse_indptr=sparse_indptr)
-    if pr.topk > 0:
-        if sparse_indptr is not None:
-            _need(sparse_indptr.numel() == pr.num_tokens + 1, fn, "sparse_indptr must be [num_tokens + 1]")
-        elif sparse_slots is not None:
-            _need(sparse_slots.numel() == pr.num_tokens * pr.topk, fn, "sparse_slots must be [num_tokens, topk]")
-    elif seq_lens is not None and block_table is not None:
-        _need(seq_lens.numel() == pr.num_reqs, fn, "seq_lens must be [num_reqs]")
-        _need(qo_indptr is None or qo_indptr.numel() == pr.num_reqs + 1, fn, "qo_indptr must be [num_reqs + 1]")
-        _need(block_table.dtype == torch.int32 and block_table.device == dev, fn,
-              "block_table must be int32 on the same device")
-        _need(block_table.dim() == 2 and block_table.shape[0] == pr.num_reqs
-              and block_table.shape[1] >= pr.max_blocks_per_req
-              and (block_table.stride(1) == 1 or block_table.shape[1] == 1), fn,
-              "block_table must be [num_reqs, >= max_blocks_per_req] with dense rows")
+    T, H, R, nb, bs, topk = pr.num_tokens, pr.num_heads, pr.num_reqs, pr.num_blocks, pr.block_size, pr.topk
+    i32, f32, codes = torch.int32, torch.float32, (torch.float8_e4m3fn, torch.uint8)
+    ok = (pr.kv_dtype == MLA_DTYPE_FP8_E4M3 and dev >= 0 and dev == torch._C._cuda_getDevice()
+          and q.dtype in codes and q.shape == (T, H, HEAD_DIM) and q.is_contiguous()
+          and kv_cache.dtype in codes and kv_cache.get_device() == dev
+          and kv_cache.shape == (nb, bs, HEAD_DIM) and kv_cache.is_contiguous()
+          and scale_group > 0 and bs % scale_group == 0
+          and kv_scales.dtype is f32 and kv_scales.get_device() == dev
+          and kv_scales.numel() == nb * bs // scale_group and kv_scales.is_contiguous()
+          and out.dtype is torch.bfloat16 and out.get_device() == dev
+          and out.shape == (T, H, KV_LORA_RANK) and out.is_contiguous()
+          and lse.dtype is f32 and lse.get_device() == dev and lse.shape == (T, H) and lse.is_contiguous()
+          and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))
+          and (sinks is None or (sinks.dtype is f32 and sinks.get_device() == dev
+                                 and sinks.numel() == H and sinks.is_contiguous())))
+    if ok and topk > 0:
+        ok = (sparse_slots is None
+              or (sparse_slots.dtype is i32 and sparse_slots.get_device() == dev and sparse_slots.is_contiguous()
+                  and (sparse_indptr is not None or sparse_slots.numel() == T * topk)))
+        ok = ok and (sparse_indptr is None
+                     or (sparse_indptr.dtype is i32 and sparse_indptr.get_device() == dev
+                         and sparse_indptr.numel() == T + 1 and sparse_indptr.is_contiguous()))
+    elif ok:
+        ok = (seq_lens is None or (seq_lens.dtype is i32 and seq_lens.get_device() == dev
+                                   and seq_lens.numel() == R and seq_lens.is_contiguous()))
+        ok = ok and (qo_indptr is None or (qo_indptr.dtype is i32 and qo_indptr.get_device() == dev
+                                           and qo_indptr.numel() == R + 1 and qo_indptr.is_contiguous()))
+        ok = ok and (block_table is None
+                     or (block_table.dtype is i32 and block_table.get_device() == dev and block_table.dim() == 2
+                         and block_table.size(0) == R and _dense_rows(block_table, pr.max_blocks_per_req)))
+    if not ok:
+        if pr.kv_dtype != MLA_DTYPE_FP8_E4M3:
+            raise MLAError(fn, MLA_ERR_UNSUPPORTED, "the plan's cache is not e4m3")
+        dense = [("q", q), ("kv_cache", kv_cache), ("kv_scales", kv_scales), ("out", out), ("lse", lse),
+                 ("workspace", workspace), ("sinks", sinks), ("seq_lens", seq_lens), ("qo_indptr", qo_indptr),
+                 ("sparse_slots", sparse_slots), ("sparse_indptr", sparse_indptr)]
+        _refuse(fn, dev, [("q", q, codes), ("kv_cache", kv_cache, codes), ("kv_scales", kv_scales, (f32,)),
+                          ("out", out, (torch.bfloat16,)), ("lse", lse, (f32,)), ("sinks", sinks, (f32,)),
+                          ("seq_lens", seq_lens, (i32,)), ("qo_indptr", qo_indptr, (i32,)),
+                          ("sparse_slots", sparse_slots, (i32,)), ("sparse_indptr", sparse_indptr, (i32,)),
+                          ("block_table", block_table, (i32,))],
+                [(t is None or t.is_contiguous(), f"{name} must be contiguous") for name, t in dense] +
+                [(q.shape == (T, H, HEAD_DIM), f"q must be [{T}, {H}, {HEAD_DIM}] for this plan"),
+                 (kv_cache.shape == (nb, bs, HEAD_DIM), f"kv_cache must be [{nb}, {bs}, {HEAD_DIM}] for this plan"),
+                 (scale_group > 0 and bs % scale_group == 0, "scale_group must divide the block size"),
+                 (scale_group > 0 and kv_scales.numel() == nb * bs // scale_group,
+                  "kv_scales must hold num_blocks * block_size / scale_group scales"),
+                 (out.shape == (T, H, KV_LORA_RANK), f"out must be [{T}, {H}, {KV_LORA_RANK}]"),
+                 (lse.shape == (T, H), f"lse must be [{T}, {H}]"),
+                 (False, "sinks, seq_lens, qo_indptr, block_table or the slot lists do not have the plan's sizes")])
     if block_table_stride is None:
-        block_table_stride = max(block_table.stride(0), block_table.shape[1]) if block_table is not None else 0
-    return (ctypes.byref(plan), _ptr(q), _ptr(kv_cache), _ptr(kv_scales), int(scale_group),
-            _ptr(block_table), int(block_table_stride), _ptr(seq_lens), _ptr(qo_indptr),
-            _ptr(sparse_slots), _ptr(sparse_indptr), float(softmax_scale), float(q_scale),
-            _ptr(sinks), _ptr(workspace), _ws_bytes(workspace), _ptr(out), _ptr(lse), _stream(stream))
+        block_table_stride = 0 if block_table is None else max(block_table.stride(0), block_table.size(1))
+    return (ctypes.byref(plan), q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), scale_group,
+            _ptr(block_table), block_table_stride, _ptr(seq_lens), _ptr(qo_indptr),
+            _ptr(sparse_slots), _ptr(sparse_indptr), softmax_scale, q_scale,
+            _ptr(sinks), _ptr(workspace), _ws_bytes(workspace), out.data_ptr(), lse.data_ptr(),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
 
 
 def mla_decode_fwd_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: int, block_table=None,
@@ -437,7 +454,7 @@ def mla_decode_fwd_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: in
                           stream=None) -> None:
     """mla_decode_fwd over an e4m3 cache with one fp32 scale per ``scale_group``
     slots of a block (``kv_scales``)."""
-    lib = load_library()
+    lib = _lib or load_library()
     fn = "mla_decode_fwd_scaled"
     _check(fn, lib.mla_decode_fwd_scaled(*_scaled_args(
         fn, plan, q, kv_cache, kv_scales, scale_group, block_table, block_table_stride, seq_lens,
@@ -452,7 +469,7 @@ def mla_decode_items_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: 
                             out, lse, stream=None) -> None:
     """Balanced plans: the decode kernel of mla_decode_fwd_scaled over the work
     list in ``workspace``."""
-    lib = load_library()
+    lib = _lib or load_library()
     fn = "mla_decode_items_scaled"
     _check(fn, lib.mla_decode_items_scaled(*_scaled_args(
         fn, plan, q, kv_cache, kv_scales, scale_group, block_table, block_table_stride, seq_lens,
@@ -462,54 +479,84 @@ def mla_decode_items_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: 
 
 def mla_block_tables(query_start_loc, seq_lens, free_blocks, block_table, *, block_size: int,
                      slot_mapping, req_id=None, positions=None, taken, stream=None) -> None:
-    """The step's new columns of ``block_table [R, C]`` from ``free_blocks``,
-    and ``slot_mapping``, ``req_id`` and ``positions`` (``[T]``) of its tokens;
-    ``taken`` (``[1]``) receives the number of blocks the step takes."""
-    lib = load_library()
+    """The step's new columns of ``block_table [R, C]`` from ``free_blocks``
+    (None: no free block), and ``slot_mapping``, ``req_id`` and ``positions``
+    (``[T]``) of its tokens; ``taken`` (``[1]``) receives the number of blocks
+    the step takes."""
+    lib = _lib or load_library()
+    torch = _torch or _load_torch()
     fn = "mla_block_tables"
-    dev = query_start_loc.device
-    _need_current(fn, dev)
-    _need_int32(fn, dev, query_start_loc=query_start_loc, seq_lens=seq_lens, free_blocks=free_blocks,
-                slot_mapping=slot_mapping, req_id=req_id, positions=positions, taken=taken)
+    i32 = torch.int32
+    dev = query_start_loc.get_device()
     R, T = seq_lens.numel(), slot_mapping.numel()
-    _need(query_start_loc.numel() == R + 1, fn, "query_start_loc must be [num_reqs + 1]")
-    _need(taken.numel() == 1, fn, "taken must be [1]")
-    _need((req_id is None or req_id.numel() == T) and (positions is None or positions.numel() == T), fn,
-          "req_id and positions must be [num_tokens]")
-    _need(str(block_table.dtype) == "torch.int32" and block_table.device == dev, fn,
-          "block_table must be int32 on the same device")
-    _need(block_table.dim() == 2 and block_table.shape[0] == R
-          and (block_table.stride(1) == 1 or block_table.shape[1] == 1 or R == 0), fn,
-          "block_table must be [num_reqs, columns] with dense rows")
-    cols = block_table.shape[1]
-    _need(R <= 1 or block_table.stride(0) >= cols, fn, "block_table rows must not overlap")
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice()
+            and query_start_loc.dtype is i32 and query_start_loc.numel() == R + 1 and query_start_loc.is_contiguous()
+            and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous()
+            and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
+            and taken.dtype is i32 and taken.get_device() == dev and taken.numel() == 1
+            and (free_blocks is None or (free_blocks.dtype is i32 and free_blocks.get_device() == dev
+                                         and free_blocks.is_contiguous()))
+            and (req_id is None or (req_id.dtype is i32 and req_id.get_device() == dev
+                                    and req_id.numel() == T and req_id.is_contiguous()))
+            and (positions is None or (positions.dtype is i32 and positions.get_device() == dev
+                                       and positions.numel() == T and positions.is_contiguous()))
+            and block_table.dtype is i32 and block_table.get_device() == dev and block_table.dim() == 2
+            and block_table.size(0) == R and _dense_rows(block_table, 1)):
+        named = [("query_start_loc", query_start_loc), ("seq_lens", seq_lens), ("slot_mapping", slot_mapping),
+                 ("free_blocks", free_blocks), ("req_id", req_id), ("positions", positions)]
+        _refuse(fn, dev, [(n, t, (i32,)) for n, t in named + [("taken", taken), ("block_table", block_table)]],
+                [(t is None or t.is_contiguous(), f"{n} must be contiguous") for n, t in named] +
+                [(query_start_loc.numel() == R + 1, "query_start_loc must be [num_reqs + 1]"),
+                 (taken.numel() == 1, "taken must be [1]"),
+                 (req_id is None or req_id.numel() == T, "req_id must be [num_tokens]"),
+                 (positions is None or positions.numel() == T, "positions must be [num_tokens]"),
+                 (False, "block_table must be [num_reqs, columns] with dense rows that do not overlap")])
+    cols = block_table.size(1)
     _check(fn, lib.mla_block_tables(
-        _ptr(query_start_loc), _ptr(seq_lens), R, T, int(block_size), _ptr(free_blocks),
-        0 if free_blocks is None else free_blocks.numel(), _ptr(block_table),
-        max(block_table.stride(0), cols), cols, _ptr(slot_mapping), _ptr(req_id), _ptr(positions),
-        _ptr(taken), _stream(stream)))
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, block_size, _ptr(free_blocks),
+        0 if free_blocks is None else free_blocks.numel(), block_table.data_ptr(),
+        block_table.stride(0) if R > 1 else cols, cols, slot_mapping.data_ptr(), _ptr(req_id), _ptr(positions),
+        taken.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
 
 
 def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_group: int,
                      stream=None) -> None:
     """The rows ``c_kv [T, 512] || k_pe [T, 64]`` (bf16) into the slots of
     ``slot_mapping``, as e4m3 codes under their groups' scales."""
-    import torch
-    lib = load_library()
+    lib = _lib or load_library()
+    torch = _torch or _load_torch()
     fn = "mla_cache_append"
-    dev = kv_cache.device
-    _need_current(fn, dev)
-    _need_scaled_cache(fn, dev, kv_cache, kv_scales, scale_group)
-    _need_int32(fn, dev, slot_mapping=slot_mapping)
+    i32, f32, b16, codes = torch.int32, torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
+    dev = kv_cache.get_device()
     T = slot_mapping.numel()
-    for name, t, width in (("c_kv", c_kv, KV_LORA_RANK), ("k_pe", k_pe, HEAD_DIM - KV_LORA_RANK)):
-        _need(t.dtype == torch.bfloat16 and t.device == dev and tuple(t.shape) == (T, width)
-              and (t.stride(1) == 1 or T == 0), fn, f"{name} must be bfloat16 [num_tokens, {width}] with dense rows")
+    rope = HEAD_DIM - KV_LORA_RANK
+    ok = (dev >= 0 and dev == torch._C._cuda_getDevice() and kv_cache.dtype in codes and kv_cache.dim() == 3
+          and kv_cache.is_contiguous()
+          and kv_scales.dtype is f32 and kv_scales.get_device() == dev and kv_scales.is_contiguous()
+          and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
+          and c_kv.dtype is b16 and c_kv.get_device() == dev and c_kv.shape == (T, KV_LORA_RANK)
+          and k_pe.dtype is b16 and k_pe.get_device() == dev and k_pe.shape == (T, rope)
+          and _dense_rows(c_kv, 1) and _dense_rows(k_pe, 1))
+    nb, bs, width = kv_cache.shape if kv_cache.dim() == 3 else (0, 0, 0)
+    if not (ok and width == HEAD_DIM and scale_group > 0 and bs % scale_group == 0
+            and kv_scales.numel() == nb * bs // scale_group):
+        _refuse(fn, dev, [("kv_cache", kv_cache, codes), ("kv_scales", kv_scales, (f32,)),
+                          ("slot_mapping", slot_mapping, (i32,)), ("c_kv", c_kv, (b16,)), ("k_pe", k_pe, (b16,))],
+                [(t.is_contiguous(), f"{n} must be contiguous") for n, t in
+                 (("kv_cache", kv_cache), ("kv_scales", kv_scales), ("slot_mapping", slot_mapping))] +
+                [(width == HEAD_DIM, f"kv_cache must be [num_blocks, block_size, {HEAD_DIM}]"),
+                 (c_kv.shape == (T, KV_LORA_RANK), f"c_kv must be [num_tokens, {KV_LORA_RANK}]"),
+                 (k_pe.shape == (T, rope), f"k_pe must be [num_tokens, {rope}]"),
+                 (scale_group > 0 and bs % scale_group == 0, "scale_group must divide the block size"),
+                 (scale_group > 0 and kv_scales.numel() == nb * bs // scale_group,
+                  "kv_scales must hold num_blocks * block_size / scale_group scales"),
+                 (False, "the rows of c_kv and k_pe must be dense and must not overlap")])
+    many = T > 1
     _check(fn, lib.mla_cache_append(
-        _ptr(c_kv), max(c_kv.stride(0), KV_LORA_RANK) if T <= 1 else c_kv.stride(0), _ptr(k_pe),
-        max(k_pe.stride(0), HEAD_DIM - KV_LORA_RANK) if T <= 1 else k_pe.stride(0),
-        _ptr(slot_mapping), T, kv_cache.shape[0], kv_cache.shape[1], int(scale_group),
-        _ptr(kv_cache), _ptr(kv_scales), _stream(stream)))
+        c_kv.data_ptr(), c_kv.stride(0) if many else KV_LORA_RANK, k_pe.data_ptr(),
+        k_pe.stride(0) if many else rope, slot_mapping.data_ptr(), T, nb, bs, scale_group,
+        kv_cache.data_ptr(), kv_scales.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
 
 
 def mla_fit_kpool_indices(token_indices, *, topk: int, out, stream=None) -> None:

@@ -198,6 +198,15 @@ SchedLayout sched_layout(const mla_plan_t* plan) {
   return l;
 }
 
+// Whether a call with group scales runs on the value-split cluster, whatever
+// kernel the plan names for the same problem with one scale: every row tile
+// of more than 64 rows the plan gives to a tensor-core kernel, and sparse lists.
+bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
+  if (kv_scales == nullptr) return false;
+  if (plan->prob.topk > 0) return true;
+  return plan->kernel == mla::kTcPair128 || (plan->kernel == mla::kTcRowsN && plan->tile_rows > 64);
+}
+
 // d.items selects the balanced grid: one CTA pair per item slot (CTA-pair
 // kernel), one CTA or cluster per worker (rows-as-N kernel).
 mla_status_t launch_decode(const mla_plan_t* plan, const mla::DecodeParams& d, int* status,
@@ -207,6 +216,14 @@ mla_status_t launch_decode(const mla_plan_t* plan, const mla::DecodeParams& d, i
   const int64_t q_rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   const int64_t kv_rows = static_cast<int64_t>(p.num_blocks) * p.block_size;
   const unsigned items = static_cast<unsigned>(plan->max_items);
+  if (runs_value_split(plan, d.kv_scales)) {
+    const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
+    const unsigned tiles = static_cast<unsigned>((rows + 127) / 128);
+    const dim3 grid = d.items != nullptr ? dim3(2u * items, 1u, 1u)
+                                         : dim3(2u * tiles, static_cast<unsigned>(plan->num_segments),
+                                                static_cast<unsigned>(plan->grid_z));
+    return cuda_status(mla::launch_decode_vs(d, q_rows, kv_rows, grid, status, stream));
+  }
   if (plan->kernel == mla::kTcPair128) {
     const dim3 grid = d.items != nullptr ? dim3(2u * items, 1u, 1u) : grid_of(plan);
     return cuda_status(mla::launch_decode_tc(d, p.kv_dtype == MLA_DTYPE_FP8_E4M3, q_rows, kv_rows,
@@ -243,7 +260,9 @@ mla::SchedParams sched_params(const mla_plan_t* plan, const Inputs& in, uint8_t*
   sp.n_items = reinterpret_cast<int32_t*>(ws + l.n_items);
   sp.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
   sp.workers = plan_workers(plan);
-  if (plan->kernel == mla::kTcRowsN)  // workers run contiguous runs of items
+  // workers run contiguous runs of items (the value-split kernel takes one
+  // item a cluster, longest first, also under a rows-as-N plan)
+  if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales))
     sp.worker_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
   return sp;
 }
@@ -276,6 +295,7 @@ mla_status_t run_items(const mla_plan_t* plan, const Inputs& in, const float* si
   d.lse = lse;
   d.segm_out = reinterpret_cast<float*>(ws + plan->segm_output_offset);
   d.segm_rows = static_cast<int64_t>(plan->split_items) * plan->tile_rows;
+  d.slot_rows = plan->tile_rows;
   d.segm_max = reinterpret_cast<float*>(ws + plan->segm_max_offset);
   d.segm_expsum = reinterpret_cast<float*>(ws + plan->segm_expsum_offset);
   return launch_decode(plan, d, reinterpret_cast<int*>(ws + plan->status_offset), stream);

@@ -98,6 +98,21 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 
+// Two weights as two e4m3 code pairs: hi = e4m3(p), lo = e4m3(p - hi),
+// formed in f16 (p rounded to 11 bits first; the difference is then exact).
+__device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const __half2 ph = __floats2half2_rn(p0, p1);
+  const uint32_t phb = *reinterpret_cast<const uint32_t*>(&ph);
+  uint16_t h16, l16;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(h16) : "r"(phb));
+  uint32_t back;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(back) : "h"(h16));
+  const __half2 d = __hsub2(ph, *reinterpret_cast<const __half2*>(&back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(l16) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
+  hi = h16;
+  lo = l16;
+}
+
 // A key of a cache with group scales, as the softmax takes it. With s the
 // group's scale, s2 the key's base-2 score factor times the raw score q . c
 // (c the codes), and t = s2 s + log2 s, the weights 2^(t - m) multiply the

@@ -531,21 +531,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[NW]) {
   }
 }
 
-// p of two rows as two e4m3 code pairs: hi = e4m3(p), lo = e4m3(p - hi),
-// formed in f16 (p rounded to 11 bits first; the difference is then exact).
-__device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  const __half2 ph = __floats2half2_rn(p0, p1);
-  const uint32_t phb = *reinterpret_cast<const uint32_t*>(&ph);
-  uint16_t h16, l16;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(h16) : "r"(phb));
-  uint32_t back;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(back) : "h"(h16));
-  const __half2 d = __hsub2(ph, *reinterpret_cast<const __half2*>(&back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(l16) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
-  hi = h16;
-  lo = l16;
-}
-
 // Eight warps: warp w owns the keys of TMEM lane quarter w % 4 and the rows
 // [h NH, (h + 1) NH) of the CTA's rows, h = (w - 4) / 4, NH = NR / 2.
 // Thread t8 < 64 (warps 4, 5) also owns row t8's reference and true maxima

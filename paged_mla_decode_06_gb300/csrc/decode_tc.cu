@@ -28,8 +28,7 @@
 // warp issuing TMA loads moves only ~27 bytes per SM clock, several keep the
 // SM's load path busy. The value CTA re-reads
 // the first 512 columns of each row, which the score CTA has just pulled
-// through L2. With group scales (GS, e4m3) the keys' scales enter the scores
-// and the row sums in the score CTA (KeyScale); the value CTA is the same.
+// through L2.
 // Every wait is bounded; on a timeout the kernel records an error code in
 // the status word, stops issuing work, drains what it issued and exits.
 #include <atomic>
@@ -85,9 +84,8 @@ constexpr int kOffAlpha = 1024;  // 2 slots x 128 fp32 rescale factors (received
 constexpr int kHeader = 2048;
 static_assert(kScoreBars * 8 <= kOffTslot && kValueBars * 8 <= kOffTslot, "barrier space");
 
-template <bool FP8, bool SPARSE, bool GS = false>
+template <bool FP8, bool SPARSE>
 struct Cfg {
-  static_assert(FP8 || !GS, "group scales belong to the e4m3 cache");
   // warps 0 and 6-8 issue TMA loads where 6-9 have no other work
   static constexpr int kThreads = 320;
   static constexpr int kProdK = 4;             // score CTA key-ring producer warps
@@ -101,11 +99,9 @@ struct Cfg {
   static constexpr int kOffQ = kHeader;
   static constexpr int kOffRing = kOffQ + (FP8 ? 0 : 1) * kBoxQ;
   static constexpr int kBoxesQTmem = FP8 ? 5 : 8;  // q boxes staged through ring slots into TMEM
-  static constexpr int kScaleBytes = GS ? 4 * 3 * kKeys * 4 : 0;  // softmax warps' key scales
-  static constexpr int kSlots = (kUsable - kOffRing - 2 * kPBytes - kScaleBytes) / kSlot;
+  static constexpr int kSlots = (kUsable - kOffRing - 2 * kPBytes) / kSlot;
   static constexpr int kOffPStage = kOffRing + kSlots * kSlot;
-  static constexpr int kOffScale = kOffPStage + 2 * kPBytes;  // [4 warps][mul, add, inv][64]
-  static constexpr int kScoreEnd = kOffScale + kScaleBytes;
+  static constexpr int kScoreEnd = kOffPStage + 2 * kPBytes;
   // value CTA
   static constexpr int kOffPRecv = kHeader;
   static constexpr int kOffV = kOffPRecv + 2 * kPBytes;
@@ -209,9 +205,9 @@ __device__ __forceinline__ int cache_row(const DecodeParams& p, const int32_t* b
 // all 5, the last half zero-filled past column 576) and are copied into TMEM
 // by the softmax warps, which then free the ring; the bf16 rope box stays in
 // shared memory.
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void load_q(const Ctx& x, const TcMaps& maps) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   tma_prefetch_desc(&maps.q);
   const int qrow = x.tok0 * x.H + x.row0;
   mbar_arrive_expect_tx(x.bar(kQFull), (FP8 ? 5 : 9) * kBoxQ);
@@ -230,9 +226,9 @@ __device__ void load_q(const Ctx& x, const TcMaps& maps) {
 // goes to ring slot i % kSlots, i = g * kBoxesK + j. The boxes are dealt
 // round-robin to kProdK producer warps (one issuing warp moves ~27 bytes
 // per clock; several keep the SM's load path busy).
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void score_ring_tma(const Ctx& x, const TcMaps& maps, const DecodeParams& p, int pidx) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   const int n_groups = cdiv(x.n_chunks, 2);
   tma_prefetch_desc(&maps.kv);
@@ -323,9 +319,9 @@ __device__ void score_ring_gather(const Ctx& x, const TcMaps& maps, const Decode
 // ------------------------------------------------------------------ value CTA: stages (dense)
 // Producer warp pidx loads the boxes j = pidx, pidx + kProdV, ... of every
 // stage; the stage's barrier completes with all kProdV arrivals and bytes.
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void value_stage_tma(const Ctx& x, const TcMaps& maps, const DecodeParams& p, int pidx) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   const int nbox = (C::kBoxesV - pidx + C::kProdV - 1) / C::kProdV;
   tma_prefetch_desc(&maps.kv);
@@ -409,9 +405,9 @@ __device__ void value_stage_gather(const Ctx& x, const TcMaps& maps, const Decod
 // K = 16 (bf16, A = q in TMEM; the rope box with A in shared memory) or 4 of
 // K = 32 (e4m3, A in shared memory); each box's slot is released by its own
 // commit. Descriptors are a base plus compile-time offsets.
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void score_mma(const Ctx& x) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   if (x.lane != 0) return;
   const uint32_t idesc = FP8 ? instr_desc(kRows, kGroup, 0, 0, false, false)
                              : instr_desc(kRows, kGroup, 1, 1, false, false);
@@ -454,9 +450,9 @@ __device__ void score_mma(const Ctx& x) {
 }
 
 // ------------------------------------------------------------------ score CTA: softmax
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   const int lane = x.lane;
   const int q4 = x.warp & 3;               // TMEM lane quarter of this warp
   const int r = q4 * 32 + lane;            // row within the tile
@@ -498,46 +494,9 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
   const uint32_t alpha_u = smem_u32(alpha_st);
   float m_ref = -INFINITY, m_true = -INFINITY, l = 0.f;
   int sent = 0;
-  // GS: every warp keeps its own copy of the chunk's key scales; lane l reads
-  // those of keys l and l + 32 one chunk ahead (64 keys from a 64-aligned
-  // position lie in one block)
-  float* ksc = reinterpret_cast<float*>(x.smem + C::kOffScale) + q4 * 3 * kKeys;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
-  auto scale_at = [&](int pos, int row0, int j) {
-    return pos + j < x.seg_end
-               ? p.kv_scales[static_cast<uint32_t>(row0 + j) / static_cast<uint32_t>(p.scale_group)]
-               : 1.f;
-  };
-  float sc0 = 1.f, sc1 = 1.f;
-  int row_next = 0;  // cache row of the first key of the chunk after the next
-  if constexpr (GS) {
-    if (x.n_chunks > 0) {
-      const int row0 = cache_row(p, bt_row, x.seg_start);
-      sc0 = scale_at(x.seg_start, row0, lane);
-      sc1 = scale_at(x.seg_start, row0, lane + 32);
-    }
-    if (x.n_chunks > 1) row_next = cache_row(p, bt_row, x.seg_start + kKeys);
-  }
   for (int c = 0; c < x.n_chunks && ok; ++c) {
     const int b = c & 1;           // P staging / receive slot
     const int g = c >> 1;          // key group of the chunk and its S buffer g & 1
-    if constexpr (GS) {
-      const KeyScale k0 = key_scale(sc0, scale2), k1 = key_scale(sc1, scale2);
-      __syncwarp();  // every lane is done with the previous chunk's scales
-      ksc[lane] = k0.mul;
-      ksc[lane + 32] = k1.mul;
-      ksc[kKeys + lane] = k0.add;
-      ksc[kKeys + lane + 32] = k1.add;
-      ksc[2 * kKeys + lane] = k0.inv;
-      ksc[2 * kKeys + lane + 32] = k1.inv;
-      __syncwarp();
-      const int pos1 = x.seg_start + (c + 1) * kKeys;
-      if (c + 1 < x.n_chunks) {
-        sc0 = scale_at(pos1, row_next, lane);
-        sc1 = scale_at(pos1, row_next, lane + 32);
-      }
-      if (c + 2 < x.n_chunks) row_next = cache_row(p, bt_row, pos1 + kKeys);
-    }
     ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kSFull + (g & 1)), (g >> 1) & 1, false, 31));
     if (!ok) break;
     fence_after_sync();
@@ -548,17 +507,6 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 64; ++j) s[j] = __uint_as_float(sr[j]);
-    }
-    if constexpr (GS) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        const float4 mu = *reinterpret_cast<const float4*>(ksc + j);
-        const float4 ad = *reinterpret_cast<const float4*>(ksc + kKeys + j);
-        s[j] = fmaf(s[j], mu.x, ad.x);
-        s[j + 1] = fmaf(s[j + 1], mu.y, ad.y);
-        s[j + 2] = fmaf(s[j + 2], mu.z, ad.z);
-        s[j + 3] = fmaf(s[j + 3], mu.w, ad.w);
-      }
     }
     if ((c & 1) || c + 1 == x.n_chunks) {  // QK^T of group g + 2 may overwrite the buffer
       fence_before_sync();
@@ -591,7 +539,7 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
     for (int j = 8; j < 64; ++j) m8[j & 7] = fmaxf(m8[j & 7], s[j]);
     const float mraw = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                              fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-    const float mx = GS ? mraw : mraw * scale2;  // -inf stays -inf
+    const float mx = mraw * scale2;  // -inf stays -inf
     m_true = fmaxf(m_true, mx);
     float alpha = 1.f;
     if (mx > m_ref + 8.f) {
@@ -609,14 +557,9 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
     for (int i = 0; i < 8; ++i) ps8[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float p0 = fast_exp2(GS ? s[2 * j] - base : fmaf(s[2 * j], scale2, -base));
-      const float p1 = fast_exp2(GS ? s[2 * j + 1] - base : fmaf(s[2 * j + 1], scale2, -base));
-      if constexpr (GS) {
-        const float2 iv = *reinterpret_cast<const float2*>(ksc + 2 * kKeys + 2 * j);
-        ps8[j & 7] = fmaf(p0, iv.x, fmaf(p1, iv.y, ps8[j & 7]));
-      } else {
-        ps8[j & 7] += p0 + p1;
-      }
+      const float p0 = fast_exp2(fmaf(s[2 * j], scale2, -base));
+      const float p1 = fast_exp2(fmaf(s[2 * j + 1], scale2, -base));
+      ps8[j & 7] += p0 + p1;
       pk[j] = pack_p<FP8>(p0, p1);
     }
     l += ((ps8[0] + ps8[1]) + (ps8[2] + ps8[3])) + ((ps8[4] + ps8[5]) + (ps8[6] + ps8[7]));
@@ -698,9 +641,9 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
 }
 
 // ------------------------------------------------------------------ value CTA: MMA
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void value_mma(const Ctx& x) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   if (x.lane != 0) return;
   const uint32_t idesc = FP8 ? instr_desc(kRows, 256, 0, 0, false, true)
                              : instr_desc(kRows, 256, 1, 1, false, true);
@@ -740,9 +683,9 @@ __device__ void value_mma(const Ctx& x) {
 }
 
 // ------------------------------------------------------------------ value CTA: rescale + epilogue
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams& p) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   const int lane = x.lane;
   const int q4 = x.warp & 3;
   const int r = q4 * 32 + lane;
@@ -944,9 +887,9 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
 // ------------------------------------------------------------------ value CTA: e4m3 widening
 // 128 threads widen the chunk's 512 e4m3 value columns (4 boxes) to f16 (8
 // boxes, exact) in buffer c & 1, zeroing rows past the segment.
-template <bool SPARSE, bool GS>
+template <bool SPARSE>
 __device__ void widen_values(const Ctx& x) {
-  using C = Cfg<true, SPARSE, GS>;
+  using C = Cfg<true, SPARSE>;
   const int ct = x.tid - 192;
   bool ok = true;
   for (int c = 0; c < x.n_chunks && ok; ++c) {
@@ -987,10 +930,10 @@ __device__ void widen_values(const Ctx& x) {
   }
 }
 
-template <bool FP8, bool SPARSE, bool GS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8, SPARSE, GS>::kThreads, 1)
+template <bool FP8, bool SPARSE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8, SPARSE>::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ TcMaps maps, const DecodeParams p, int* status) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   static_assert(!(FP8 && SPARSE), "the sparse variant is bf16");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1123,32 +1066,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8, SPARSE, GS>
   if (score) {
     if (x.warp == 0) {
       if (x.lane == 0 && x.n_chunks > 0) {
-        load_q<FP8, SPARSE, GS>(x, maps);
-        if (!SPARSE) score_ring_tma<FP8, SPARSE, GS>(x, maps, p, 0);
+        load_q<FP8, SPARSE>(x, maps);
+        if (!SPARSE) score_ring_tma<FP8, SPARSE>(x, maps, p, 0);
         drain_wait(status, x.bar(kQFull), 0, 13);
       }
     } else if (x.warp == 1) {
-      score_mma<FP8, SPARSE, GS>(x);
+      score_mma<FP8, SPARSE>(x);
     } else if (x.warp < 6) {
-      score_softmax<FP8, SPARSE, GS>(x, p);
+      score_softmax<FP8, SPARSE>(x, p);
     } else if constexpr (SPARSE) {
       if (x.warp >= 6 && x.n_chunks > 0) score_ring_gather<SPARSE>(x, maps, p, x.warp - 6);
     } else {
       if (pidx >= 1 && pidx < C::kProdK && x.lane == 0 && x.n_chunks > 0)
-        score_ring_tma<FP8, SPARSE, GS>(x, maps, p, pidx);
+        score_ring_tma<FP8, SPARSE>(x, maps, p, pidx);
     }
   } else {
     if (x.warp == 1) {
-      value_mma<FP8, SPARSE, GS>(x);
+      value_mma<FP8, SPARSE>(x);
     } else if (x.warp >= 2 && x.warp < 6) {
-      value_rows<FP8, SPARSE, GS>(x, maps, p);
+      value_rows<FP8, SPARSE>(x, maps, p);
     } else if constexpr (SPARSE) {
       if (x.warp >= 6) value_stage_gather<SPARSE>(x, maps, p, x.warp - 6);
     } else if constexpr (FP8) {
-      if (x.warp == 0 && x.lane == 0) value_stage_tma<FP8, SPARSE, GS>(x, maps, p, 0);
-      if (x.warp >= 6) widen_values<SPARSE, GS>(x);
+      if (x.warp == 0 && x.lane == 0) value_stage_tma<FP8, SPARSE>(x, maps, p, 0);
+      if (x.warp >= 6) widen_values<SPARSE>(x);
     } else {
-      if (pidx >= 0 && pidx < C::kProdV && x.lane == 0) value_stage_tma<FP8, SPARSE, GS>(x, maps, p, pidx);
+      if (pidx >= 0 && pidx < C::kProdV && x.lane == 0) value_stage_tma<FP8, SPARSE>(x, maps, p, pidx);
     }
   }
 
@@ -1161,17 +1104,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8, SPARSE, GS>
   if (x.warp == 1) tmem_dealloc(x.tbase, kTmemCols);
 }
 
-template <bool FP8, bool SPARSE, bool GS>
+template <bool FP8, bool SPARSE>
 cudaError_t launch_variant(const TcMaps& maps, const DecodeParams& p, dim3 grid, int* status,
                            cudaStream_t stream) {
-  using C = Cfg<FP8, SPARSE, GS>;
+  using C = Cfg<FP8, SPARSE>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(decode_tc_kernel<FP8, SPARSE, GS>,
+    e = cudaFuncSetAttribute(decode_tc_kernel<FP8, SPARSE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_acq_rel);
@@ -1179,7 +1122,7 @@ cudaError_t launch_variant(const TcMaps& maps, const DecodeParams& p, dim3 grid,
   // an ordinary launch also after the schedule kernel: as a programmatic
   // dependent of it (set up while it runs) the DeepSeek-V3 call measured
   // 137.8 us against 131.0 us (its griddepcontrol.wait is then a no-op)
-  decode_tc_kernel<FP8, SPARSE, GS><<<grid, C::kThreads, C::kSmem, stream>>>(maps, p, status);
+  decode_tc_kernel<FP8, SPARSE><<<grid, C::kThreads, C::kSmem, stream>>>(maps, p, status);
   return cudaGetLastError();
 }
 
@@ -1211,14 +1154,10 @@ cudaError_t launch_decode_tc(const DecodeParams& p, bool fp8, int64_t q_rows, in
     if (fp8) return cudaErrorNotSupported;
     e = make_row_map(&maps.kv1, p.kv, static_cast<uint64_t>(kv_rows), 1, false);
     if (e != cudaSuccess) return e;
-    return launch_variant<false, true, false>(maps, p, grid, status, stream);
+    return launch_variant<false, true>(maps, p, grid, status, stream);
   }
-  if (p.kv_scales != nullptr) {
-    if (!fp8) return cudaErrorNotSupported;
-    return launch_variant<true, false, true>(maps, p, grid, status, stream);
-  }
-  return fp8 ? launch_variant<true, false, false>(maps, p, grid, status, stream)
-             : launch_variant<false, false, false>(maps, p, grid, status, stream);
+  return fp8 ? launch_variant<true, false>(maps, p, grid, status, stream)
+             : launch_variant<false, false>(maps, p, grid, status, stream);
 }
 
 }  // namespace mla

@@ -52,6 +52,7 @@ struct DecodeParams {
   // slot s is scaled by kv_scales[s / scale_group]; null: kv_scale alone
   const float* kv_scales;
   int32_t scale_group;
+  int32_t slot_rows;             // rows of a partial slot (balanced schedule)
 };
 
 // Balanced work list (sched.cu).
@@ -189,6 +190,12 @@ cudaError_t launch_decode_hn(const DecodeParams& p, int rows, int cluster, int64
 // Clusters of two CTAs of `rows` rows that can be resident at once on the
 // current device.
 cudaError_t decode_hn_max_pairs(int rows, int* n);
+
+// tcgen05 kernel of the group-scaled cache for row tiles of up to 128 rows, a
+// cluster of two CTAs that split the value columns: dense (block size a
+// multiple of 64) or sparse. grid.x counts CTAs: two per item or row tile.
+cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, dim3 grid, int* status,
+                             cudaStream_t stream);
 
 // Shared memory bytes a decode variant needs (host query for validation).
 int decode_mma_smem_bytes(int32_t kernel, bool fp8);

@@ -142,6 +142,17 @@ mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   d.kv_scale = in.kv_scale;
   d.kv_scales = in.kv_scales;
   d.scale_group = in.scale_group;
+  if (in.scale_group > 0) {
+    // division of a slot by the group size: with 2^k <= g < 2^(k+1), not a
+    // power of two, and M = ceil(2^(32+k) / g) < 2^32, mulhi(s, M) >> k is
+    // exact for s < 2^31: M g = 2^(32+k) + e with e < g < 2^(k+1), so the
+    // quotient is off by s e / (g 2^(32+k)) < 2^(31+k+1) / (g 2^(32+k)) = 1 / g
+    const uint32_t g = static_cast<uint32_t>(in.scale_group);
+    uint32_t k = 0;
+    while ((2ull << k) <= g) ++k;
+    d.scale_shift = k;
+    d.scale_magic = (g & (g - 1)) == 0 ? 0u : static_cast<uint32_t>(((1ull << (32 + k)) + g - 1) / g);
+  }
   d.wait_ns = plan->wait_limit_us > 0 ? static_cast<uint64_t>(plan->wait_limit_us) * 1000ull : 0ull;
   return d;
 }

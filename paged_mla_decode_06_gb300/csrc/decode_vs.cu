@@ -1,33 +1,36 @@
 // decode_vs.cu -- split-K paged MLA decode over an e4m3 cache with group
-// scales, for row tiles of up to 128 query rows: a cluster of two CTAs that
-// split the value columns (sm_103a).
+// scales, for row tiles of up to 128 query rows: two CTAs that split the value
+// columns of a tile (sm_103a).
 //
 // The fp32 accumulator of 128 rows x 512 value columns fills a whole tensor
 // memory, so a row tile takes two SMs. Here each CTA owns all 128 rows and 256
 // of the value columns; both compute all scores and the same softmax. That
-// doubles Q K^T, but no probabilities cross between the SMs (distributed
-// shared memory moves about 20 bytes a clock), the softmax has its row in one
-// thread with no exchange but one of maxima, and the second-largest cost, the
-// epilogue, is halved. Per 128 keys a CTA issues
+// doubles Q K^T, but nothing crosses between the SMs (probabilities would:
+// distributed shared memory moves about 20 bytes a clock), a row's softmax is
+// in four threads that exchange one maximum, and the epilogue is halved. Per
+// chunk of 128 keys a CTA issues
 //   S[rows, keys]  = Q K^T   M = 128 rows, N = 128 keys, K = 576: A = q from
 //                            TMEM (512 latent dims) and shared memory (64 rope
-//                            dims), B = the key rows of the ring, K-major:
+//                            dims), B = the key rows of the rings, K-major:
 //                            18 kind::f8f6f4 instructions of 64 cycles;
 //   O[rows, 256]  += P V     M = 128 rows, N = 256 columns, K = 128 keys, P as
 //                            two e4m3 terms (hi, lo), V = the same key rows
 //                            read MN-major: 8 instructions of 128 cycles.
-// That is 2176 tensor cycles per 128 keys, close to what the shared memory's
-// 128 bytes a clock allow for the operands, the copies in and P (284 KB, 2220
-// cycles). The softmax of 128 x 128 scores takes the eight warps about 1300
-// issue cycles and runs beside them: S is read into registers at once, so
+// That is 2176 tensor cycles a chunk, close to what the shared memory's 128
+// bytes a clock allow for the operands, the copies in and P (284 KB, 2220
+// cycles). The softmax runs beside them: S is read into registers at once, so
 // that the next chunk's Q K^T can overwrite it while its weights are formed,
 // and one buffer of S and one of P are enough.
 //
-// Every key box is read from memory once, by one CTA of the cluster, and
-// multicast to the ring slot of both (dense); a slot is refilled once both
-// CTAs have released it, a box of the other half's value columns after Q K^T,
-// one of the own half after P V. Sparse lists gather their rows with TMA
-// gather4, each CTA for itself.
+// Rings: the two latent boxes of the own value columns stay until P V, the
+// other two and the rope box only until Q K^T. They have rings of their own, of
+// three, two and two chunks: what limits the loop is a box's lifetime (load,
+// Q K^T, softmax, P V: about 8000 cycles for a value box), and in one ring of
+// ten slots the short-lived boxes would wait behind the long-lived ones
+// (4470 cycles a chunk, measured). The two CTAs of a tile read each key row
+// once from memory between them: the later one finds it in L2. Multicasting
+// each box to both, from one read of L2, ties each slot to the slower CTA and
+// measured 5930 cycles a chunk against 4730 (one ring).
 //
 // Weights: with group scales the thread's scores become t = score + log2 s and
 // the weights 2^(t - m) multiply the codes (KeyScale). They are formed as
@@ -35,10 +38,12 @@
 // exceeds it by more than 4 (O is then rescaled in TMEM), so p <= 2^8 fits
 // e4m3 and hi + lo carry 8 bits of it.
 //
-// Warps: 0, 2, 12, 13 load, 1 issues Q K^T, 3 P V, 4-11 softmax and epilogue
-// (a TMEM lane quarter of the rows and a half of the keys each). Every wait is
-// bounded: a timeout records a code in the status word, stops the CTA's work,
-// drains what was issued and exits.
+// Warps: 0 and 20-22 load (sparse: gather), 1 issues Q K^T, 2 prepares the
+// keys' scales, 3 issues P V, 4-19 softmax and epilogue (a TMEM lane quarter
+// of the rows and a quarter of the chunk's keys each: four warps to a
+// scheduler hide each other's latencies). Every wait is bounded: a timeout
+// records a code in the status word, stops the CTA's work, drains what was
+// issued and exits.
 #include <atomic>
 #include <climits>
 
@@ -57,13 +62,19 @@ constexpr int kKeys = 128;               // keys per chunk: N of Q K^T, K of P V
 constexpr int kHalf = 64;                // keys per TMA box, and per softmax warp
 constexpr int kSlot = kKeys * 128;       // ring slot: a 128-byte column box of a chunk (or of q)
 constexpr int kRSlot = kKeys * 64;       // rope ring slot
-constexpr int kBoxes = 5;                // per chunk: 4 latent boxes and the rope box
-constexpr int kSlots = 10;               // even: the two value boxes of a CTA are neighbours
+constexpr int kKSlots = 4;               // latent boxes of the other CTA's value columns
+constexpr int kVSlots = 6;               // latent boxes of the own value columns
 constexpr int kRSlots = 2;
-constexpr int kQStage = kSlots - 4;      // q's latent boxes land in the last four slots
-constexpr int kThreads = 448;
-constexpr int kProducers = 4;            // warps 0, 2, 12, 13
-constexpr int kSoftWarps = 8;            // warps 4-11
+constexpr int kAllSlots = kKSlots + kVSlots + kRSlots;
+constexpr int kQStage = 2;               // q's latent boxes land in value slots 2..5
+constexpr int kSoftWarps = 16;           // warps 4-19: two groups (even and odd chunks) of four
+                                         // TMEM lane quarters x two key halves
+constexpr int kGroupWarps = 8;
+constexpr int kPart = 32;                // keys that share a scale where groups are multiples of it
+constexpr int kThreads = 32 * (4 + kSoftWarps);
+constexpr int kLaunchRegs = 96;          // 65536 / 640, by allocation unit
+constexpr int kControlRegs = 56;
+constexpr int kSoftRegs = 104;
 constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P for 64 keys
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;           // 256 columns
@@ -75,38 +86,73 @@ constexpr float kPBias = 4.f;            // p = 2^(t - m_ref + kPBias) <= 2^(2 k
 constexpr float kMove = 4.f;             // m_ref moves when a chunk max exceeds it by more
 
 enum : int {
-  kFull = 0,                 // [kSlots] ring slot loaded
-  kEmpty = kSlots,           // [kSlots] ring slot released (by every CTA that loads into it)
-  kRFull = 2 * kSlots,       // [kRSlots]
-  kREmpty = kRFull + kRSlots,
-  kQFull = kREmpty + kRSlots,  // q staged
+  kFull = 0,                 // [kAllSlots] slot loaded (key ring, value ring, rope ring)
+  kEmpty = kAllSlots,        // [kAllSlots] slot released
+  kQFull = 2 * kAllSlots,    // q staged
   kQTmem,                    // q copied to TMEM: the staging slots are free
-  kSFull,                    // S written
-  kSFree,                    // S read
-  kPFull,                    // P written
-  kPFree,                    // P V complete: P may be replaced, O holds the chunk
-  kX,                        // [4] the two warps of a row quarter have posted
-  kDrain = kX + 4,           // the Q K^T issuer's MMAs complete
+  // by the parity of the chunk (each phase is then waited for by all that
+  // wait on the barrier at all):
+  kSFull,                    // [2] S written, key scales ready
+  kSFree = kSFull + 2,       // [2] S read
+  kPFull = kSFree + 2,       // [2] P written
+  kPFree = kPFull + 2,       // [2] P V complete: P may be replaced, O holds the chunk
+  kX = kPFree + 2,           // [2][4] the two warps of a row quarter have posted their maxima
+  kXL = kX + 8,              // [4] the four warps of a row quarter have posted their sums
+  kDrain = kXL + 4,          // the Q K^T issuer's MMAs complete
   kDrainPV,
   kNumBars
 };
 
-// Shared memory: header, q's rope columns, P, the rope ring, the ring.
+// Shared memory: header, q's rope columns, P, the three rings.
 constexpr int kOffBar = 0;
 constexpr int kOffTslot = 384;
 constexpr int kOffAbort = 388;
-constexpr int kOffIssued = 448;           // [kSlots + kRSlots] int: last use issued per slot
-constexpr int kOffXMax = 1024;            // [2][2][128] chunk maxima by parity and key half
-constexpr int kOffLsum = 3072;            // [2][128] row sums by key half
-constexpr int kOffScale = 4096;           // [8 warps][mul, add, inv][64]
+constexpr int kOffIssued = 448;           // [kAllSlots] int: last use issued per slot
+constexpr int kOffXMax = 1024;            // [4][2][128] maxima of chunk g (at g % 4) by key half;
+                                          // at the end the row sums, in the two oldest
+constexpr int kOffScale = 5120;           // [2][mul, add, inv][128] of chunk g (at g % 2)
+constexpr int kOffMask = kOffScale + 2 * 3 * kKeys * 4;  // [2][4] bits of existing keys
 constexpr int kOffQR = 10240;             // 128 rows x 64 bytes, 64-byte swizzle
 constexpr int kOffP = kOffQR + kRSlot;    // [key half][hi, lo] tiles, 64-byte swizzle
 constexpr int kOffRope = kOffP + 4 * kPTile;
-constexpr int kOffRing = kOffRope + kRSlots * kRSlot;
-constexpr int kSmem = kOffRing + kSlots * kSlot + 1024;  // + alignment slack
-static_assert(kNumBars * 8 <= kOffTslot && kOffIssued + 4 * (kSlots + kRSlots) <= kOffXMax, "header space");
-static_assert(kOffScale + kSoftWarps * 3 * kHalf * 4 <= kOffQR, "scale space");
-static_assert(kSlots % 2 == 0 && kSlots >= 8 && kSmem <= 232448, "shared memory budget");
+constexpr int kOffKey = kOffRope + kRSlots * kRSlot;
+constexpr int kOffVal = kOffKey + kKSlots * kSlot;
+constexpr int kSmem = kOffVal + kVSlots * kSlot + 1024;  // + alignment slack
+static_assert(kNumBars * 8 <= kOffTslot && kOffIssued + 4 * kAllSlots <= kOffXMax, "header space");
+static_assert(kOffMask + 32 <= kOffQR, "scale space");
+static_assert(kVSlots % 2 == 0 && kKSlots % 2 == 0 && kSmem <= 232448, "shared memory budget");
+
+// Box b of chunk g (in the order Q K^T takes them: two of the other CTA's
+// value columns, two of the own, the rope columns): its barrier index, shared
+// memory, use of the slot and first column.
+struct Box {
+  int index, use, col, off;
+  bool rope;
+};
+__device__ __forceinline__ Box box_of(int g, int b, int rank) {
+  Box x;
+  x.rope = b == 4;
+  if (b < 2) {
+    const int i = 2 * g + b, s = i % kKSlots;
+    x.index = s;
+    x.use = i / kKSlots;
+    x.col = 128 * (2 * (rank ^ 1) + b);
+    x.off = kOffKey + s * kSlot;
+  } else if (b < 4) {
+    const int i = 2 * g + b - 2, s = i % kVSlots;
+    x.index = kKSlots + s;
+    x.use = i / kVSlots;
+    x.col = 128 * (2 * rank + b - 2);
+    x.off = kOffVal + s * kSlot;
+  } else {
+    const int s = g % kRSlots;
+    x.index = kKSlots + kVSlots + s;
+    x.use = g / kRSlots;
+    x.col = kRank;
+    x.off = kOffRope + s * kRSlot;
+  }
+  return x;
+}
 
 struct VsMaps {
   CUtensorMap q;     // q as [T*H rows, 576] e4m3, box 128 bytes x 128 rows
@@ -133,18 +179,43 @@ struct Ctx {
   __device__ uint32_t bar(int i) const { return bar0 + 8u * i; }
 };
 
+// Largest of three (one instruction; NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ void report(int* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
 }
 
-// Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or
-// abort. kCluster: acquire at cluster scope (barriers the peer arrives on).
-template <bool kCluster = false>
+// Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or abort.
 __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
+  if (mbar_try_wait(bar, parity)) return true;
   const uint32_t nap = x.limit_ns < kSleepNs ? static_cast<uint32_t>(x.limit_ns) : kSleepNs;
-  while (!(kCluster ? mbar_try_wait_cluster_sleep(bar, parity, nap) : mbar_try_wait_sleep(bar, parity, nap))) {
+  // one sleep before the clock is read for the first time: nearly every wait
+  // ends in it, and reading the global timer takes longer than most waits
+  if (mbar_try_wait_sleep(bar, parity, nap)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, nap)) {
     if (*x.abort) return false;
     if (global_timer_ns() - t0 > x.limit_ns) {
       report(x.status, code);
@@ -154,28 +225,18 @@ __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code
   }
   return true;
 }
-template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  return __all_sync(0xffffffffu, wait_phase<kCluster>(x, bar, parity, code)) != 0;
+  return __all_sync(0xffffffffu, wait_phase(x, bar, parity, code)) != 0;
 }
 // Wait that ignores the abort flag (teardown), still bounded.
 __device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_cluster_sleep(bar, parity, kSleepNs)) {
+  while (!mbar_try_wait_sleep(bar, parity, kSleepNs)) {
     if (global_timer_ns() - t0 > kDefaultWaitNs) {
       report(x.status, code);
       return;
     }
   }
-}
-
-// Release of a ring slot by this CTA's MMAs: to both CTAs where both fill it.
-template <bool SPARSE>
-__device__ __forceinline__ void release(uint32_t bar) {
-  if constexpr (SPARSE)
-    mma_commit(bar);
-  else
-    mma_commit_mc(bar, static_cast<uint16_t>(3));
 }
 
 // Cache slot of key position pos (-1 past the segment or for an unused list entry).
@@ -188,421 +249,587 @@ __device__ __forceinline__ int key_slot(const Ctx& x, const DecodeParams& p, con
 }
 
 // ------------------------------------------------------------------ producers
-// Box j of chunk g: latent box j < 4 goes to ring slot i % kSlots, i = 4 g + j,
-// the rope box to rope slot g % kRSlots. The first use of the slots that
-// stage q waits until both CTAs have copied q out.
-__device__ __forceinline__ bool slot_ready(const Ctx& x, bool rope, int slot, int use, bool cluster) {
-  if (use >= 1) {
-    const uint32_t b = x.bar(rope ? kREmpty + slot : kEmpty + slot);
-    return cluster ? wait_phase<true>(x, b, (use - 1) & 1, 11) : wait_phase<false>(x, b, (use - 1) & 1, 11);
-  }
-  return rope || slot < kQStage || wait_phase<true>(x, x.bar(kQTmem), 0, 10);
+// The slot of box x may be filled: its last use is released, or (first use) q
+// has left the value slots that stage it.
+__device__ __forceinline__ bool slot_ready(const Ctx& x, const Box& b) {
+  if (b.use >= 1) return wait_phase(x, x.bar(kEmpty + b.index), (b.use - 1) & 1, 11);
+  const bool staged = b.index >= kKSlots + kQStage && b.index < kKSlots + kQStage + 4;
+  return !staged || wait_phase(x, x.bar(kQTmem), 0, 10);
 }
 
-// Dense: box b = 5 g + j is loaded by CTA b % 2, there by producer warp
-// (b / 2) % 4, and multicast to both. The whole warp looks up the cache rows
-// of 16 chunks at a time, a window ahead; lane 0 issues.
-__device__ void produce_dense(const Ctx& x, const VsMaps& maps, const DecodeParams& p, int pidx) {
+// Dense: warp 0 loads a chunk's boxes, first those that wait for Q K^T alone,
+// then the value boxes. Each is two 64-row TMA boxes from their blocks, one by
+// each of two lanes; the boxes of one kind go out together (a lane issuing
+// them in turn takes about 350 cycles each, which alone held the loop at 4240
+// cycles a chunk).
+template <bool VALUES>
+__device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int g, int row0, int row1) {
+  constexpr int kCount = VALUES ? 2 : 3;
   const int lane = x.lane;
-  volatile int* issued = reinterpret_cast<volatile int*>(x.smem + kOffIssued);
-  if (lane == 0) {
+  const int j = VALUES ? 2 + (lane >> 1) : (lane >> 1) < 2 ? (lane >> 1) : 4;
+  const bool two = x.seg_start + g * kKeys + kHalf < x.seg_end;
+  bool ok = true;
+  if (lane < 2 * kCount) {
+    const Box b = box_of(g, j, x.rank);
+    ok = slot_ready(x, b);
+    if (ok && ((lane & 1) == 0 || two)) {
+      const int half = (b.rope ? kRSlot : kSlot) / 2;
+      const uint32_t full = x.bar(kFull + b.index);
+      if ((lane & 1) == 0) {
+        mbar_arrive_expect_tx(full, two ? 2 * half : half);
+        reinterpret_cast<volatile int*>(x.smem + kOffIssued)[b.index] = b.use;
+      }
+      tma_load_2d(smem_u32(x.smem + b.off + (lane & 1) * half), b.rope ? &maps.kvr : &maps.kv, b.col,
+                  (lane & 1) != 0 ? row1 : row0, full);
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Sparse: lane l issues one gather4 of the rows of keys 4 l .. 4 l + 3 of each
+// box. A key without a slot reads row 0: its score is masked and its value
+// row zeroed by the softmax warps, whatever the row holds.
+template <bool VALUES>
+__device__ __forceinline__ bool gather_boxes(const Ctx& x, const VsMaps& maps, int g, const int (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < (VALUES ? 2 : 3); ++i) {
+    const Box b = box_of(g, VALUES ? 2 + i : (i < 2 ? i : 4), x.rank);
+    if (!__all_sync(0xffffffffu, slot_ready(x, b))) return false;
+    const uint32_t full = x.bar(kFull + b.index);
+    if (x.lane == 0) {
+      mbar_arrive_expect_tx(full, b.rope ? kRSlot : kSlot);
+      reinterpret_cast<volatile int*>(x.smem + kOffIssued)[b.index] = b.use;
+    }
+    __syncwarp();
+    tma_gather4(smem_u32(x.smem + b.off + (b.rope ? 256 : 512) * x.lane), b.rope ? &maps.kvr : &maps.kv, b.col, r[0],
+                r[1], r[2], r[3], full);
+  }
+  return true;
+}
+
+// Cache rows of the 64-key halves of a dense request's chunks: looked up by
+// the whole warp, 16 chunks at a time and a window ahead.
+struct RowWindow {
+  int cur, nxt;
+  __device__ __forceinline__ void load(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int w0, int& v) {
+    const int s =
+        key_slot<false>(x, p, bt_row, x.seg_start + (w0 + (x.lane >> 1)) * kKeys + (x.lane & 1) * kHalf);
+    v = s < 0 ? 0 : s;
+  }
+  __device__ __forceinline__ void start(const Ctx& x, const DecodeParams& p, const int32_t* bt_row) {
+    load(x, p, bt_row, 0, cur);
+    load(x, p, bt_row, 16, nxt);
+  }
+  // moves on to the window of chunk g (called for every chunk in turn)
+  __device__ __forceinline__ void at(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int g) {
+    if (g > 0 && (g & 15) == 0) {
+      cur = nxt;
+      load(x, p, bt_row, g + 16, nxt);
+    }
+  }
+  __device__ __forceinline__ int row(int g, int half) const {
+    return __shfl_sync(0xffffffffu, cur, 2 * (g & 15) + half);
+  }
+};
+
+__device__ void produce_dense(const Ctx& x, const VsMaps& maps, const DecodeParams& p) {
+  if (x.lane == 0) {
     tma_prefetch_desc(&maps.kv);
     tma_prefetch_desc(&maps.kvr);
   }
-  const uint64_t pol = l2_evict_first();  // each key row is read once
   const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
-  auto lookup = [&](int w0) {  // cache row of this lane's (chunk, half) in the window at w0
-    const int s = key_slot<false>(x, p, bt_row, x.seg_start + (w0 + (lane >> 1)) * kKeys + (lane & 1) * kHalf);
-    return s < 0 ? 0 : s;
-  };
-  int cur = lookup(0), nxt = lookup(16);
-  bool ok = true;
-  for (int g = 0; g < x.n_chunks && ok; ++g) {
-    if (g > 0 && (g & 15) == 0) {
-      cur = nxt;
-      nxt = lookup(g + 16);
-    }
-    const int row0 = __shfl_sync(0xffffffffu, cur, 2 * (g & 15));
-    const int row1 = __shfl_sync(0xffffffffu, cur, 2 * (g & 15) + 1);
-    const bool two = x.seg_start + g * kKeys + kHalf < x.seg_end;
-    if (lane == 0) {
-      for (int j = 0; j < kBoxes; ++j) {
-        const int b = g * kBoxes + j;
-        if ((b & 1) != x.rank || ((b >> 1) % kProducers) != pidx) continue;
-        const bool rope = j == kBoxes - 1;
-        const int i = rope ? g : 4 * g + j;
-        const int slot = i % (rope ? kRSlots : kSlots);
-        const int use = i / (rope ? kRSlots : kSlots);
-        if (!slot_ready(x, rope, slot, use, true)) {
-          ok = false;
-          break;
-        }
-        const int box = rope ? kRSlot : kSlot;
-        const uint32_t bytes = two ? box : box / 2;
-        const uint32_t full = x.bar(rope ? kRFull + slot : kFull + slot);
-        mbar_arrive_expect_tx(full, bytes);
-        // the peer's phase of this slot also waits for the box
-        mbar_arrive_expect_tx_cluster(map_to_rank(full, x.rank ^ 1), bytes);
-        const uint32_t dst = smem_u32(x.smem + (rope ? kOffRope + slot * kRSlot : kOffRing + slot * kSlot));
-        const CUtensorMap* map = rope ? &maps.kvr : &maps.kv;
-        tma_load_2d_mc_hint(dst, map, 128 * j, row0, full, 3, pol);
-        if (two) tma_load_2d_mc_hint(dst + box / 2, map, 128 * j, row1, full, 3, pol);
-        atomicMax(const_cast<int*>(issued + (rope ? kSlots + slot : slot)), use);
-      }
-    }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  RowWindow w;
+  w.start(x, p, bt_row);
+  for (int g = 0; g < x.n_chunks; ++g) {
+    w.at(x, p, bt_row, g);
+    const int row0 = w.row(g, 0), row1 = w.row(g, 1);
+    if (!load_boxes<false>(x, maps, g, row0, row1) || !load_boxes<true>(x, maps, g, row0, row1)) break;
   }
   __syncwarp();
 }
 
-// Sparse: box 5 g + j is gathered by warp (5 g + j) % 4 of each CTA: lane l
-// issues one gather4 of the rows of keys 4 l .. 4 l + 3. A key without a slot
-// reads row 0: its score is masked and its value row zeroed by the softmax
-// warps, whatever the row holds.
-__device__ void produce_sparse(const Ctx& x, const VsMaps& maps, const DecodeParams& p, int pidx) {
+// The scale of slot s (s >= 0): its group by a multiplication (scale_magic).
+__device__ __forceinline__ float scale_of_slot(const DecodeParams& p, int s) {
+  const uint32_t g = p.scale_magic != 0 ? __umulhi(static_cast<uint32_t>(s), p.scale_magic) >> p.scale_shift
+                                        : static_cast<uint32_t>(s) >> p.scale_shift;
+  return __ldg(p.kv_scales + g);
+}
+
+// Posts the key scales of chunk g (part i of 32 keys: lane's key 32 i + lane;
+// UNI: lane i < 4 has the scale of part i) and the bits of the keys that exist,
+// once the softmax is done with those two chunks back (it has posted P).
+template <bool UNI>
+__device__ __forceinline__ bool post_scales(const Ctx& x, const DecodeParams& p, int g, const float (&sc)[4],
+                                            uint32_t bits) {
   const int lane = x.lane;
-  volatile int* issued = reinterpret_cast<volatile int*>(x.smem + kOffIssued);
+  if (g >= 2 && !warp_wait(x, x.bar(kPFull + (g & 1)), ((g >> 1) - 1) & 1, 27)) return false;
+  float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + (g & 1) * 3 * kKeys;
+  if (lane < 4) reinterpret_cast<uint32_t*>(x.smem + kOffMask)[(g & 1) * 4 + lane] = bits;
+#pragma unroll
+  for (int i = 0; i < (UNI ? 1 : 4); ++i) {
+    const KeyScale k = key_scale(sc[i], p.score_scale_log2);
+    const int at = UNI ? 32 * lane : 32 * i + lane;
+    if (!UNI || lane < 4) {
+      ks[at] = k.mul;
+      ks[kKeys + at] = k.add;
+      ks[2 * kKeys + at] = k.inv;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(x.bar(kSFull + (g & 1)));
+  return true;
+}
+
+// Warp 2, dense: the scales, read one chunk ahead of the one posted.
+template <bool UNI>
+__device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
+  const int lane = x.lane;
+  const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
+  RowWindow w;
+  w.start(x, p, bt_row);
+  float sc[4];
+  auto read = [&](int g) {  // 1 for keys that do not exist
+    w.at(x, p, bt_row, g);
+    const int row0 = w.row(g, 0), row1 = w.row(g, 1);
+    const int n = x.seg_end - (x.seg_start + g * kKeys);
+#pragma unroll
+    for (int i = 0; i < (UNI ? 1 : 4); ++i) {
+      const int j = UNI ? 32 * lane : 32 * i + lane;
+      sc[i] = j < n && j < kKeys ? scale_of_slot(p, (j < kHalf ? row0 : row1) + (j & (kHalf - 1))) : 1.f;
+    }
+  };
+  if (x.n_chunks > 0) read(0);
+  for (int g = 0; g < x.n_chunks; ++g) {
+    const int n = x.seg_end - (x.seg_start + g * kKeys) - 32 * lane;
+    const uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    if (!post_scales<UNI>(x, p, g, sc, bits)) break;
+    if (g + 1 < x.n_chunks) read(g + 1);
+  }
+  __syncwarp();
+}
+
+// Sparse: warp 0 (VALUES) gathers the value boxes, warp 2 the others, and
+// prepares the scales: the slots of a lane's keys are read two chunks ahead
+// and their scales one.
+template <bool VALUES>
+__device__ void produce_sparse(const Ctx& x, const VsMaps& maps, const DecodeParams& p) {
+  const int lane = x.lane;
   if (lane == 0) {
     tma_prefetch_desc(&maps.kv);
     tma_prefetch_desc(&maps.kvr);
   }
-  const uint64_t pol = l2_evict_first();
-  int nx[4];
-  auto lookup = [&](int g) {
+  int rows[4];
+  auto gather_rows = [&](int g) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      nx[k] = g < x.n_chunks ? key_slot<true>(x, p, nullptr, x.seg_start + g * kKeys + 4 * lane + k) : 0;
+      rows[k] = g < x.n_chunks ? key_slot<true>(x, p, nullptr, x.seg_start + g * kKeys + 4 * lane + k) : 0;
   };
-  lookup(0);
-  bool ok = true;
-  for (int g = 0; g < x.n_chunks && ok; ++g) {
+  gather_rows(0);
+  int slot[4], next[4];
+  float sc[4];
+  auto slots_of = [&](int g, int (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = g < x.n_chunks ? key_slot<true>(x, p, nullptr, x.seg_start + g * kKeys + 32 * i + lane) : -1;
+  };
+  auto scales_of = [&](const int (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i] = v[i] >= 0 ? scale_of_slot(p, v[i]) : 1.f;
+  };
+  if constexpr (!VALUES) {
+    slots_of(0, slot);
+    scales_of(slot);
+    slots_of(1, next);
+  }
+  for (int g = 0; g < x.n_chunks; ++g) {
     int r[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = nx[k] >= 0 ? nx[k] : 0;
-    lookup(g + 1);
-    for (int j = 0; j < kBoxes && ok; ++j) {
-      if ((g * kBoxes + j) % kProducers != pidx) continue;
-      const bool rope = j == kBoxes - 1;
-      const int i = rope ? g : 4 * g + j;
-      const int slot = i % (rope ? kRSlots : kSlots);
-      const int use = i / (rope ? kRSlots : kSlots);
-      ok = __all_sync(0xffffffffu, slot_ready(x, rope, slot, use, false)) != 0;
-      if (!ok) break;
-      const uint32_t full = x.bar(rope ? kRFull + slot : kFull + slot);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(full, rope ? kRSlot : kSlot);
-        atomicMax(const_cast<int*>(issued + (rope ? kSlots + slot : slot)), use);
+    for (int k = 0; k < 4; ++k) r[k] = rows[k] >= 0 ? rows[k] : 0;
+    gather_rows(g + 1);
+    if (!gather_boxes<VALUES>(x, maps, g, r)) break;
+    if constexpr (!VALUES) {
+      uint32_t bits = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __ballot_sync(0xffffffffu, slot[i] >= 0);
+        if (lane == i) bits = b;
       }
-      __syncwarp();
-      if (rope)
-        tma_gather4_hint(smem_u32(x.smem + kOffRope + slot * kRSlot + 256 * lane), &maps.kvr, 128 * j, r[0], r[1], r[2],
-                         r[3], full, pol);
-      else
-        tma_gather4_hint(smem_u32(x.smem + kOffRing + slot * kSlot + 512 * lane), &maps.kv, 128 * j, r[0], r[1], r[2],
-                         r[3], full, pol);
+      if (!post_scales<false>(x, p, g, sc, bits)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) slot[i] = next[i];
+      scales_of(slot);
+      slots_of(g + 2, next);
     }
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ MMA issue
-template <bool SPARSE>
-__device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
-  if (x.lane != 0 || x.n_chunks == 0) return;
-  constexpr uint32_t kId = instr_desc(kRows, kKeys, 0, 0, false, false);
-  const uint64_t k_desc = smem_desc_sw128(smem_u32(x.smem + kOffRing), 16, 1024);
-  const uint64_t r_desc = smem_desc_sw64(smem_u32(x.smem + kOffRope), 512);
-  const uint64_t q_desc = smem_desc_sw64(smem_u32(x.smem + kOffQR), 512);
-  tma_prefetch_desc(&maps.q);
-  mbar_arrive_expect_tx(x.bar(kQFull), 4 * kSlot + kRSlot);
-  const int qrow = x.tok0 * x.H + x.row0;
-  for (int j = 0; j < 4; ++j)
-    tma_load_2d(smem_u32(x.smem + kOffRing + (kQStage + j) * kSlot), &maps.q, 128 * j, qrow, x.bar(kQFull));
-  tma_load_2d(smem_u32(x.smem + kOffQR), &maps.qr, 512, qrow, x.bar(kQFull));
-  bool ok = wait_phase(x, x.bar(kQFull), 0, 20) && wait_phase<true>(x, x.bar(kQTmem), 0, 21);
-  const uint32_t d = x.tbase + kTmemS;
-  for (int g = 0; g < x.n_chunks && ok; ++g) {
-    if (g >= 1 && !wait_phase(x, x.bar(kSFree), (g - 1) & 1, 22)) break;
-#pragma unroll
-    for (int j = 0; j < kBoxes; ++j) {
-      const bool rope = j == kBoxes - 1;
-      const int i = rope ? g : 4 * g + j;
-      const int slot = i % (rope ? kRSlots : kSlots);
-      const int use = i / (rope ? kRSlots : kSlots);
-      if (!wait_phase<!SPARSE>(x, x.bar(rope ? kRFull + slot : kFull + slot), use & 1, 23)) {
-        ok = false;
-        break;
-      }
-      fence_after_sync();
-      if (rope) {
-        const uint64_t b = r_desc + static_cast<uint64_t>(slot * (kRSlot >> 4));
-#pragma unroll
-        for (int s = 0; s < 2; ++s) mma_ss_f8(d, q_desc + 2 * s, b + 2 * s, kId, 1u);
-        release<SPARSE>(x.bar(kREmpty + slot));
-      } else {
-        const uint64_t b = k_desc + static_cast<uint64_t>(slot * (kSlot >> 4));
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mma_ts_f8(d, x.tbase + kTmemQ + 32 * j + 8 * s, b + 2 * s, kId, (j | s) != 0 ? 1u : 0u);
-        if ((j >> 1) != x.rank) release<SPARSE>(x.bar(kEmpty + slot));  // its values are the peer's
-      }
-    }
-    if (!ok) break;
-    mma_commit(x.bar(kSFull));
-  }
-  mma_commit(x.bar(kDrain));
-  drain_wait(x, x.bar(kDrain), 0, 25);
+// The issuing warps stay together: addresses and descriptors are computed
+// uniformly and one elected lane issues. (A lane on its own, with the values
+// in its vector registers, took about 165 cycles an instruction between the
+// softmax warps of its scheduler, more than twice its 64 tensor cycles.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
-template <bool SPARSE>
+// Four steps of 32 columns of a 128-byte column box: D (+)= A[tmem] B[smem].
+__device__ __forceinline__ void mma_box(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b32 l, t;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 b, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n"
+      " add.u32 l, %2, 2;\n add.u32 t, %1, 8;\n mov.b64 b, {l, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [t], b, %4, 1;\n"
+      " add.u32 l, %2, 4;\n add.u32 t, %1, 16;\n mov.b64 b, {l, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [t], b, %4, 1;\n"
+      " add.u32 l, %2, 6;\n add.u32 t, %1, 24;\n mov.b64 b, {l, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [t], b, %4, 1;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Position in a ring of N chunks, and the phase parity of its slots.
+template <int N>
+struct RingPos {
+  int at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
+  if (x.n_chunks == 0) return;
+  constexpr uint32_t kId = instr_desc(kRows, kKeys, 0, 0, false, false);
+  const uint32_t base = smem_u32(x.smem);
+  const uint64_t k_desc = smem_desc_sw128(base, 16, 1024);
+  const uint64_t r_desc = smem_desc_sw64(base + kOffRope, 512);
+  const uint64_t q_desc = smem_desc_sw64(base + kOffQR, 512);
+  const uint32_t k_lo = static_cast<uint32_t>(k_desc), k_hi = static_cast<uint32_t>(k_desc >> 32);
+  const bool one = elect_one();
+  if (one) {
+    tma_prefetch_desc(&maps.q);
+    mbar_arrive_expect_tx(x.bar(kQFull), 4 * kSlot + kRSlot);
+    const int qrow = x.tok0 * x.H + x.row0;
+    for (int j = 0; j < 4; ++j)
+      tma_load_2d(base + kOffVal + (kQStage + j) * kSlot, &maps.q, 128 * j, qrow, x.bar(kQFull));
+    tma_load_2d(base + kOffQR, &maps.qr, kRank, qrow, x.bar(kQFull));
+  }
+  __syncwarp();
+  bool ok = warp_wait(x, x.bar(kQFull), 0, 20) && warp_wait(x, x.bar(kQTmem), 0, 21);
+  const uint32_t d = x.tbase + kTmemS;
+  const uint32_t a_key = x.tbase + kTmemQ + 64u * (x.rank ^ 1), a_val = x.tbase + kTmemQ + 64u * x.rank;
+  RingPos<kKSlots / 2> kr;
+  RingPos<kVSlots / 2> vr;
+  RingPos<kRSlots> rr;
+  for (int g = 0; g < x.n_chunks && ok; ++g) {
+    ok = g == 0 || warp_wait(x, x.bar(kSFree + ((g - 1) & 1)), ((g - 1) >> 1) & 1, 22);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = j < 2 ? 2 * kr.at + j : kKSlots + 2 * vr.at + j - 2;
+      ok = ok && warp_wait(x, x.bar(kFull + slot), j < 2 ? kr.phase : vr.phase, 23);
+      if (!ok) break;
+      const uint32_t lo = k_lo + ((kOffKey + slot * kSlot) >> 4);  // (the value ring follows the key ring)
+      fence_after_sync();
+      if (one) {
+        mma_box(d, (j < 2 ? a_key : a_val) + 32u * (j & 1), lo, k_hi, kId, j != 0 ? 1u : 0u);
+        if (j < 2) mma_commit(x.bar(kEmpty + slot));  // its only read
+      }
+      __syncwarp();
+    }
+    ok = ok && warp_wait(x, x.bar(kFull + kKSlots + kVSlots + rr.at), rr.phase, 23);
+    if (!ok) break;
+    fence_after_sync();
+    const uint64_t rd = r_desc + static_cast<uint64_t>(rr.at * (kRSlot >> 4));
+    if (one) {
+      mma_ss_f8(d, q_desc, rd, kId, 1u);
+      mma_ss_f8(d, q_desc + 2, rd + 2, kId, 1u);
+      mma_commit(x.bar(kEmpty + kKSlots + kVSlots + rr.at));
+      mma_commit(x.bar(kSFull + (g & 1)));
+    }
+    __syncwarp();
+    kr.next();
+    vr.next();
+    rr.next();
+  }
+  if (one) {
+    mma_commit(x.bar(kDrain));
+    drain_wait(x, x.bar(kDrain), 0, 25);
+  }
+  __syncwarp();
+}
+static_assert(kOffVal == kOffKey + kKSlots * kSlot, "one descriptor base for both rings");
+
 __device__ void pv_issue(const Ctx& x) {
-  if (x.lane != 0 || x.n_chunks == 0) return;
+  if (x.n_chunks == 0) return;
   constexpr uint32_t kId = instr_desc(kRows, 256, 0, 0, false, true);
-  const uint64_t v_desc = smem_desc_sw128(smem_u32(x.smem + kOffRing), kSlot, 1024);  // MN-major
+  const uint64_t v_desc = smem_desc_sw128(smem_u32(x.smem + kOffVal), kSlot, 1024);  // MN-major, two boxes
   const uint64_t p_desc = smem_desc_sw64(smem_u32(x.smem + kOffP), 512);
   const uint32_t d = x.tbase + kTmemO;
+  const bool one = elect_one();
+  RingPos<kVSlots / 2> vr;
   for (int g = 0; g < x.n_chunks; ++g) {
     // P written; the softmax waited for S, whose Q K^T waited for these boxes
-    if (!wait_phase(x, x.bar(kPFull), g & 1, 24)) break;
+    if (!warp_wait(x, x.bar(kPFull + (g & 1)), (g >> 1) & 1, 24)) break;
     fence_after_sync();
-    const int slot = (4 * g + 2 * x.rank) % kSlots;
-    const uint64_t vb = v_desc + static_cast<uint64_t>(slot * (kSlot >> 4));
+    const uint64_t vb = v_desc + static_cast<uint64_t>(vr.at * (2 * kSlot >> 4));
     const bool two = x.seg_start + g * kKeys + kHalf < x.seg_end;  // else the second half holds no key
+    if (one) {
 #pragma unroll
-    for (int ks = 0; ks < kKeys / 32; ++ks) {
-      if (ks >= 2 && !two) break;
-      const uint64_t av = p_desc + static_cast<uint64_t>(((ks >> 1) * 2 * kPTile + (ks & 1) * 32) >> 4);
-      const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
-      mma_ss_f8(d, av, bv, kId, (g | ks) != 0 ? 1u : 0u);
-      mma_ss_f8(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kId, 1u);
+      for (int ks = 0; ks < kKeys / 32; ++ks) {
+        if (ks >= 2 && !two) break;
+        const uint64_t av = p_desc + static_cast<uint64_t>(((ks >> 1) * 2 * kPTile + (ks & 1) * 32) >> 4);
+        const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
+        mma_ss_f8(d, av, bv, kId, (g | ks) != 0 ? 1u : 0u);
+        mma_ss_f8(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kId, 1u);
+      }
+      mma_commit(x.bar(kEmpty + kKSlots + 2 * vr.at));
+      mma_commit(x.bar(kEmpty + kKSlots + 2 * vr.at + 1));
+      mma_commit(x.bar(kPFree + (g & 1)));
     }
-    release<SPARSE>(x.bar(kEmpty + slot));
-    release<SPARSE>(x.bar(kEmpty + slot + 1));
-    mma_commit(x.bar(kPFree));
+    __syncwarp();
+    vr.next();
   }
-  mma_commit(x.bar(kDrainPV));
-  drain_wait(x, x.bar(kDrainPV), 0, 26);
+  if (one) {
+    mma_commit(x.bar(kDrainPV));
+    drain_wait(x, x.bar(kDrainPV), 0, 26);
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax + epilogue
-template <bool SPARSE>
+template <bool SPARSE, bool UNI>
 __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParams& p) {
   const int lane = x.lane;
   const int sw = x.warp - 4;
   const int q4 = x.warp & 3;               // TMEM lane quarter of this warp
-  const int h = sw >> 2;                   // its half of a chunk's keys, and of the CTA's value columns
+  const int grp = sw >> 3;                 // chunks g with g % 2 == grp
+  const int h = (sw >> 2) & 1;             // its half of a chunk's keys
+  const int kq = sw >> 2;                  // its box of q, and quarter of the CTA's value columns at the end
   const int r = q4 * 32 + lane;            // row within the tile
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const int H = x.H;
   const int rho = x.row0 + r;
   const bool row_ok = rho < x.rows_total;
   const int vis = !row_ok ? 0 : (SPARSE ? INT_MAX : x.part_len - x.qlen + rho / H + 1);
-  const float scale2 = p.score_scale_log2;
+  const int n = x.n_chunks;
   bool ok = true;
 
-  // this row of q, staged in the ring's last slots, into TMEM (two of the
-  // four latent boxes each)
-  if (x.n_chunks > 0) {
+  // this row of q, staged in the value ring, into TMEM (one of the four
+  // latent boxes each)
+  if (n > 0) {
     ok = warp_wait(x, x.bar(kQFull), 0, 30);
     if (ok) {
-#pragma unroll 1
-      for (int j = 2 * h; j < 2 * h + 2; ++j) {
-        const uint8_t* src = x.smem + kOffRing + (kQStage + j) * kSlot + r * 128;
-        uint32_t v[32];
+      const uint8_t* src = x.smem + kOffVal + (kQStage + kq) * kSlot + r * 128;
+      uint32_t v[32];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 t = *reinterpret_cast<const uint4*>(src + ((q ^ (r & 7)) << 4));
-          v[4 * q] = t.x;
-          v[4 * q + 1] = t.y;
-          v[4 * q + 2] = t.z;
-          v[4 * q + 3] = t.w;
-        }
-        tmem_st_32x32b_x32(x.tbase + lane_off + kTmemQ + 32 * j, v);
+      for (int q = 0; q < 8; ++q) {
+        const uint4 t = *reinterpret_cast<const uint4*>(src + ((q ^ (r & 7)) << 4));
+        v[4 * q] = t.x;
+        v[4 * q + 1] = t.y;
+        v[4 * q + 2] = t.z;
+        v[4 * q + 3] = t.w;
       }
+      tmem_st_32x32b_x32(x.tbase + lane_off + kTmemQ + 32 * kq, v);
       tmem_st_wait();
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(x.bar(kQTmem));
-        mbar_arrive_cluster(map_to_rank(x.bar(kQTmem), x.rank ^ 1));
-      }
+      if (lane == 0) mbar_arrive(x.bar(kQTmem));
     }
   }
 
-  float* xmax = reinterpret_cast<float*>(x.smem + kOffXMax);
-  float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum);
-  float* ksc = reinterpret_cast<float*>(x.smem + kOffScale) + sw * 3 * kHalf;
+  float* xmax = reinterpret_cast<float*>(x.smem + kOffXMax) + r;
+  // the warp's keys in P: the row's 64 bytes of either tile, 64-byte swizzle
   uint8_t* prow = x.smem + kOffP + h * 2 * kPTile + r * 64;
-  const int pswz = (r >> 1) & 3;           // 64-byte swizzle of the row's 16-byte chunks
-  // slots of the warp's keys (lane l: keys l and l + 32 of its half) two
-  // chunks ahead and their scales one ahead, so that no read is waited for
-  const int32_t* bt_row = SPARSE ? nullptr : p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
-  auto slot_of = [&](int g, int i) {
-    return g < x.n_chunks ? key_slot<SPARSE>(x, p, bt_row, x.seg_start + g * kKeys + h * kHalf + lane + 32 * i) : -1;
-  };
-  auto scale_of = [&](int slot) {
-    return slot >= 0 ? p.kv_scales[static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.scale_group)] : 1.f;
-  };
-  int sl0 = slot_of(0, 0), sl1 = slot_of(0, 1);
-  float sc0 = scale_of(sl0), sc1 = scale_of(sl1);
-  int nsl0 = slot_of(1, 0), nsl1 = slot_of(1, 1);
+  const int pswz = (r >> 1) & 3;
+  const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + grp * 3 * kKeys + kHalf * h;
 
   float m_ref = -INFINITY, m_true = -INFINITY, l = 0.f;
-  for (int g = 0; g < x.n_chunks && ok; ++g) {
-    const uint64_t kmask = static_cast<uint64_t>(__ballot_sync(0xffffffffu, sl0 >= 0)) |
-                           (static_cast<uint64_t>(__ballot_sync(0xffffffffu, sl1 >= 0)) << 32);
-    {
-      const KeyScale k0 = key_scale(sc0, scale2), k1 = key_scale(sc1, scale2);
-      __syncwarp();  // every lane is done with the previous chunk's scales
-      ksc[lane] = k0.mul;
-      ksc[lane + 32] = k1.mul;
-      ksc[kHalf + lane] = k0.add;
-      ksc[kHalf + lane + 32] = k1.add;
-      ksc[2 * kHalf + lane] = k0.inv;
-      ksc[2 * kHalf + lane + 32] = k1.inv;
-      sl0 = nsl0;
-      sl1 = nsl1;
-      sc0 = scale_of(sl0);
-      sc1 = scale_of(sl1);
-      nsl0 = slot_of(g + 2, 0);
-      nsl1 = slot_of(g + 2, 1);
-      __syncwarp();
-    }
-    ok = warp_wait(x, x.bar(kSFull), g & 1, 31);
+  // Every thread follows its row's reference through the maxima of all chunks:
+  // the reference moves to a chunk's maximum that exceeds it by more than
+  // kMove. Returns the factor of what was formed before.
+  auto follow = [&](float mx) {
+    m_true = fmaxf(m_true, mx);
+    if (!(mx > m_ref + kMove)) return 1.f;  // (true also for a row's first visible key)
+    const float a = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - mx);
+    m_ref = mx;
+    l *= a;
+    return a;
+  };
+  // the maximum of chunk g, which the two warps of the other group posted
+  auto follow_other = [&](int g) {
+    if (!warp_wait(x, x.bar(kX + 4 * (g & 1) + q4), (g >> 1) & 1, 33)) return false;
+    const float* xm = xmax + (g & 3) * 2 * kRows;
+    follow(fmaxf(xm[0], xm[kRows]));
+    return true;
+  };
+  for (int g = grp; g < n && ok; g += 2) {
+    const int ph = (g >> 1) & 1;
+    ok = warp_wait(x, x.bar(kSFull + grp), ph, 31);
     if (!ok) break;
     fence_after_sync();
-    float s[64];
+    float s[kHalf];
     {
-      uint32_t sr[64];
+      uint32_t sr[kHalf];
       tmem_ld_32x32b_x64(x.tbase + lane_off + kTmemS + kHalf * h, sr);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 64; ++j) s[j] = __uint_as_float(sr[j]);
+      for (int j = 0; j < kHalf; ++j) s[j] = __uint_as_float(sr[j]);
     }
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kSFree));  // the next chunk's Q K^T may overwrite S
+    if (lane == 0) mbar_arrive(x.bar(kSFree + grp));  // the next chunk's Q K^T may overwrite S
+    const uint2 kmask = reinterpret_cast<const uint2*>(x.smem + kOffMask)[2 * grp + h];
+    KeyScale part[2] = {};  // UNI: the scales of the warp's first and second 32 keys
+    if constexpr (UNI) {
+      part[0] = KeyScale{ks[0], ks[kKeys], ks[2 * kKeys]};
+      part[1] = KeyScale{ks[kPart], ks[kKeys + kPart], ks[2 * kKeys + kPart]};
+    } else {
 #pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      const float4 mu = *reinterpret_cast<const float4*>(ksc + j);
-      const float4 ad = *reinterpret_cast<const float4*>(ksc + kHalf + j);
-      s[j] = fmaf(s[j], mu.x, ad.x);
-      s[j + 1] = fmaf(s[j + 1], mu.y, ad.y);
-      s[j + 2] = fmaf(s[j + 2], mu.z, ad.z);
-      s[j + 3] = fmaf(s[j + 3], mu.w, ad.w);
+      for (int j = 0; j < kHalf; j += 4) {
+        const float4 mu = *reinterpret_cast<const float4*>(ks + j);
+        const float4 ad = *reinterpret_cast<const float4*>(ks + kKeys + j);
+        const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(mu.x, mu.y), make_float2(ad.x, ad.y));
+        const float2 b = fma2(make_float2(s[j + 2], s[j + 3]), make_float2(mu.z, mu.w), make_float2(ad.z, ad.w));
+        s[j] = a.x;
+        s[j + 1] = a.y;
+        s[j + 2] = b.x;
+        s[j + 3] = b.y;
+      }
     }
     // keys that exist and that the row may see
-    const int lim = min(vis, x.seg_end) - (x.seg_start + g * kKeys + h * kHalf);
-    if (lim < kHalf || kmask != ~0ull) {
+    const int lim = min(vis, x.seg_end) - (x.seg_start + g * kKeys + kHalf * h);
+    if (lim < kHalf || (kmask.x & kmask.y) != 0xffffffffu) {
 #pragma unroll
-      for (int j = 0; j < 64; ++j)
-        if (!(j < lim && ((kmask >> j) & 1ull))) s[j] = -INFINITY;
+      for (int j = 0; j < kHalf; ++j)
+        if (!(j < lim && (((j < 32 ? kmask.x : kmask.y) >> (j & 31)) & 1u))) s[j] = -INFINITY;
     }
-    float m8[8];
+    float mine = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m8[i] = s[i];
+    for (int i = 0; i < 2; ++i) {
+      const float* v = s + kPart * i;
+      float m4[4];
 #pragma unroll
-    for (int j = 8; j < 64; ++j) m8[j & 7] = fmaxf(m8[j & 7], s[j]);
-    const float mine = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-    // the row's maximum over both key halves
-    float* xm = xmax + (g & 1) * 2 * kRows;
-    xm[h * kRows + r] = mine;
+      for (int j = 0; j < 4; ++j) m4[j] = max3(v[j], v[j + 4], v[j + 8]);
+#pragma unroll
+      for (int j = 12; j < kPart - 4; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], v[j + k], v[j + 4 + k]);
+      const float m = max3(fmaxf(m4[0], v[kPart - 4]), max3(m4[1], v[kPart - 3], m4[2]),
+                           max3(v[kPart - 2], m4[3], v[kPart - 1]));
+      mine = fmaxf(mine, UNI ? fmaf(m, part[i].mul, part[i].add) : m);  // (mul > 0; -inf stays)
+    }
+    static_assert((kPart - 12) % 8 == 4, "the last four scores");
+    // the row's maximum over both key halves; the previous chunk's before it
+    float* xm = xmax + (g & 3) * 2 * kRows;
+    xm[h * kRows] = mine;
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kX + q4));
-    ok = warp_wait(x, x.bar(kX + q4), g & 1, 32);
+    if (lane == 0) mbar_arrive(x.bar(kX + 4 * grp + q4));
+    ok = (g == 0 || follow_other(g - 1)) && warp_wait(x, x.bar(kX + 4 * grp + q4), ph, 32);
     if (!ok) break;
-    const float mx = fmaxf(mine, xm[(h ^ 1) * kRows + r]);
-    m_true = fmaxf(m_true, mx);
-    float alpha = 1.f;
-    if (mx > m_ref + kMove) {  // also when the row's first visible key arrives
-      if (m_ref != -INFINITY) {
-        alpha = fast_exp2(m_ref - mx);
-        l *= alpha;
-      }
-      m_ref = mx;
-    }
+    const float alpha = follow(fmaxf(mine, xm[(h ^ 1) * kRows]));
     // p as hi + lo e4m3 terms, 16 keys to a 16-byte chunk of each tile
     const float base = m_ref == -INFINITY ? 0.f : m_ref - kPBias;
-    uint32_t hi[16], lo[16];
-    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t hi[kHalf / 4], lo[kHalf / 4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float4 iv = *reinterpret_cast<const float4*>(ksc + 2 * kHalf + 4 * j);
-      const float p0 = fast_exp2(s[4 * j] - base), p1 = fast_exp2(s[4 * j + 1] - base);
-      const float p2 = fast_exp2(s[4 * j + 2] - base), p3 = fast_exp2(s[4 * j + 3] - base);
-      ps[0] = fmaf(p0, iv.x, ps[0]);
-      ps[1] = fmaf(p1, iv.y, ps[1]);
-      ps[2] = fmaf(p2, iv.z, ps[2]);
-      ps[3] = fmaf(p3, iv.w, ps[3]);
-      uint32_t h0, h1, l0, l1;
-      p_terms(p0, p1, h0, l0);
-      p_terms(p2, p3, h1, l1);
-      hi[j] = h0 | (h1 << 16);
-      lo[j] = l0 | (l1 << 16);
+    for (int i = 0; i < 2; ++i) {
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 mul2 = make_float2(part[i].mul, part[i].mul);
+      const float sh = UNI ? part[i].add - base : -base;
+      const float2 shift2 = make_float2(sh, sh);
+#pragma unroll
+      for (int j = kPart / 4 * i; j < kPart / 4 * (i + 1); ++j) {
+        float2 a = make_float2(s[4 * j], s[4 * j + 1]), b = make_float2(s[4 * j + 2], s[4 * j + 3]);
+        a = UNI ? fma2(a, mul2, shift2) : add2(a, shift2);
+        b = UNI ? fma2(b, mul2, shift2) : add2(b, shift2);
+        a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+        b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
+        if constexpr (UNI) {
+          ps[0] = add2(ps[0], a);
+          ps[1] = add2(ps[1], b);
+        } else {
+          const float4 iv = *reinterpret_cast<const float4*>(ks + 2 * kKeys + 4 * j);
+          ps[0] = fma2(a, make_float2(iv.x, iv.y), ps[0]);
+          ps[1] = fma2(b, make_float2(iv.z, iv.w), ps[1]);
+        }
+        uint32_t h0, h1, l0, l1;
+        p_terms(a.x, a.y, h0, l0);
+        p_terms(b.x, b.y, h1, l1);
+        hi[j] = h0 | (h1 << 16);
+        lo[j] = l0 | (l1 << 16);
+      }
+      const float psum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+      l = UNI ? fmaf(psum, part[i].inv, l) : l + psum;
     }
-    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
     // the previous chunk's P V has read P and O is complete up to it
     if (g >= 1) {
-      ok = warp_wait(x, x.bar(kPFree), (g - 1) & 1, 33);
+      ok = warp_wait(x, x.bar(kPFree + (grp ^ 1)), ((g - 1) >> 1) & 1, 37);
       if (!ok) break;
       if (__any_sync(0xffffffffu, alpha != 1.f)) {
         // some rows moved their reference: this warp rescales its rows of its
         // half of the value columns
         fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * h + 32 * c;
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(ta, o);
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * h + 16 * c;
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(ta, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st_32x32b_x32(ta, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st_32x32b_x16(ta, o);
         }
         tmem_st_wait();
       }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      *reinterpret_cast<uint4*>(prow + ((c ^ pswz) << 4)) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-      *reinterpret_cast<uint4*>(prow + kPTile + ((c ^ pswz) << 4)) =
-          make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+      uint8_t* dst = prow + ((c ^ pswz) << 4);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+      *reinterpret_cast<uint4*>(dst + kPTile) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
     }
     // value rows of keys that do not exist (stale or unloaded ring contents,
     // cache rows past the sequence, unused list entries) must not reach O
-    // through p = 0: they are zeroed, a quarter by each warp of the half
-    if (kmask != ~0ull && (h == 0 || x.seg_start + g * kKeys + kHalf < x.seg_end)) {
-      const int slot = (4 * g + 2 * x.rank) % kSlots;
-      uint8_t* box = x.smem + kOffRing + (slot + ((lane >> 3) & 1)) * kSlot + h * kHalf * 128 + (lane & 7) * 16;
+    // through p = 0: they are zeroed, a quarter by each warp of the key half
+    if ((kmask.x & kmask.y) != 0xffffffffu && (h == 0 || x.seg_start + g * kKeys + kHalf < x.seg_end)) {
+      uint8_t* box = x.smem + box_of(g, 2, x.rank).off + ((lane >> 3) & 1) * kSlot + kHalf * h * 128 + (lane & 7) * 16;
       for (int j = q4 + 4 * (lane >> 4); j < kHalf; j += 8)
-        if (!((kmask >> j) & 1ull)) *reinterpret_cast<uint4*>(box + j * 128) = make_uint4(0u, 0u, 0u, 0u);
+        if (!(((j < 32 ? kmask.x : kmask.y) >> (j & 31)) & 1u))
+          *reinterpret_cast<uint4*>(box + j * 128) = make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kPFull));
+    if (lane == 0) mbar_arrive(x.bar(kPFull + grp));
   }
 
   // ---------------------------------------------------------------- epilogue
+  if (ok && n > 0 && ((n - 1) & 1) != grp) ok = follow_other(n - 1);  // the last chunk was the other group's
+  // sums by group and key half, where the maxima of chunks n - 4 and n - 3 were
+  auto lsum = [&](int i) { return xmax + ((n + (i >> 1)) & 3) * 2 * kRows + (i & 1) * kRows; };
   if (ok) {
-    lsum[h * kRows + r] = l;
+    *lsum(kq) = l;
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kX + q4));
-    ok = warp_wait(x, x.bar(kX + q4), x.n_chunks & 1, 34);
+    if (lane == 0) mbar_arrive(x.bar(kXL + q4));
+    ok = warp_wait(x, x.bar(kXL + q4), 0, 34);
   }
-  if (ok && x.n_chunks > 0) {
-    ok = warp_wait(x, x.bar(kPFree), (x.n_chunks - 1) & 1, 35);
+  if (ok && n > 0) {
+    ok = warp_wait(x, x.bar(kPFree + ((n - 1) & 1)), ((n - 1) >> 1) & 1, 35);
     fence_after_sync();
   }
   if (!ok) return;
   float mult = 0.f;
   if (row_ok) {
-    const float L = lsum[r] + lsum[kRows + r];
+    const float L = (*lsum(0) + *lsum(1)) + (*lsum(2) + *lsum(3));
     const float base = m_ref == -INFINITY ? 0.f : m_ref - kPBias;  // the sums' reference
     const int head = rho % H;
     const int64_t th = static_cast<int64_t>(x.tok0 + rho / H) * H + head;
-    const bool writes = x.rank == 0 && h == 0;
+    const bool writes = x.rank == 0 && kq == 0;
     if (x.fin) {
       float lse = -INFINITY;
       if (p.sinks != nullptr) {
@@ -626,25 +853,21 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
       }
     }
   }
-  // Each warp scales its 32 rows x 128 columns and stages them, 128 bytes of
-  // each row at a time, in the 128-byte swizzle, in the ring (which holds no
+  // Each warp scales its 32 rows x 64 columns and stages them, 128 bytes of
+  // each row at a time, in the 128-byte swizzle, in the rings (which hold no
   // more boxes in use). When all 32 rows are valid one TMA tensor store writes
-  // each staged tile (two in flight); otherwise every store instruction covers
-  // four 128-byte row pieces. (TMEM loads are warp-collective.)
-  const int col0 = 256 * x.rank + 128 * h;
+  // each staged tile; otherwise every store instruction covers four 128-byte
+  // row pieces. (TMEM loads are warp-collective.)
+  const int col0 = 256 * x.rank + 64 * kq;
   const int wr = x.row0 + 32 * q4;          // the warp's first row within the unit
   if (wr >= x.rows_total) return;
   const bool whole = wr + 32 <= x.rows_total;
   const int z0 = x.fin || x.pslot < 0 ? x.tok0 * H + wr : x.pslot * p.slot_rows + 32 * q4;
   const int y0 = x.fin || x.pslot >= 0 ? 0 : x.seg;
   const CUtensorMap* map = x.fin ? &maps.out : &maps.part;
-  uint8_t* stage = x.smem + kOffRing + sw * 8192;
   const int qc = lane & 7;                  // 16-byte piece of a 128-byte row piece
-  int staged = 0;
-  auto store = [&](const uint32_t (&w)[32], int col) {
-    uint8_t* buf = stage + (staged & 1) * 4096;
-    if (whole && staged >= 2 && lane == 0) bulk_wait_read<1>();  // the store that read this buffer
-    __syncwarp();
+  auto store = [&](const uint32_t (&w)[32], int col, int tile) {
+    uint8_t* buf = x.smem + kOffKey + sw * 8192 + tile * 4096;
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
@@ -671,43 +894,49 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
                              : reinterpret_cast<uint8_t*>(p.segm_out + ts * kRank + col);
         *reinterpret_cast<uint4*>(dst + qc * 16) = v;
       }
-      __syncwarp();
     }
-    ++staged;
   };
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    uint32_t o[64];
-    if (x.n_chunks > 0) {
-      tmem_ld_32x32b_x64(x.tbase + lane_off + kTmemO + 128 * h + 64 * c, o);
-      tmem_ld_wait();
-    } else {
-#pragma unroll
-      for (int j = 0; j < 64; ++j) o[j] = 0u;
-    }
+  if (x.fin) {
     uint32_t w[32];
-    if (x.fin) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+    for (int c = 0; c < 2; ++c) {
+      uint32_t o[32];
+      if (x.n_chunks > 0) {
+        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * kq + 32 * c, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * mult, __uint_as_float(o[2 * j + 1]) * mult);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      store(w, col0 + 64 * c);
-    } else {
+    }
+    store(w, col0, 0);
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      uint32_t o[32];
+      if (x.n_chunks > 0) {
+        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * kq + 32 * c, o);
+        tmem_ld_wait();
+      } else {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(o[32 * hf + j]) * mult);
-        store(w, col0 + 64 * c + 32 * hf);
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
       }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mult);
+      store(o, col0 + 32 * c, c);
     }
   }
   if (lane == 0) bulk_wait_all();  // tiles read and written before the CTA exits
   __syncwarp();
 }
 
-template <bool SPARSE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool SPARSE, bool UNI>
+__global__ void __launch_bounds__(kThreads, 1)
     decode_vs_kernel(const __grid_constant__ VsMaps maps, const DecodeParams p, int* status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -717,14 +946,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   x.status = status;
   x.limit_ns = p.wait_ns != 0 ? p.wait_ns : kDefaultWaitNs;
   x.tid = threadIdx.x;
-  x.warp = x.tid >> 5;
+  x.warp = __shfl_sync(0xffffffffu, x.tid >> 5, 0);  // uniform, for the compiler too
   x.lane = x.tid & 31;
-  x.rank = static_cast<int>(cluster_ctarank());
+  x.rank = static_cast<int>(blockIdx.x & 1);
   int tile, item_begin = 0, item_end = 0;
   x.pslot = -1;
   if (p.items != nullptr) {
-    // balanced schedule: both CTAs read the same item, once the grid that
-    // wrote the list has completed; the merge may launch once every CTA has started
+    // balanced schedule: both CTAs of a tile read the same item, once the grid
+    // that wrote the list has completed; the merge may launch once every CTA
+    // has started
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int item = blockIdx.x >> 1;
@@ -765,7 +995,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   x.rows_total = x.qlen * x.H;
   x.row0 = tile * kRows;
-  if (x.row0 >= x.rows_total) return;  // both CTAs take this branch together
+  if (x.row0 >= x.rows_total) return;
   if (p.items != nullptr) {
     x.seg_start = item_begin;
     x.seg_end = min(item_end, x.part_len);
@@ -783,49 +1013,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   x.abort = reinterpret_cast<volatile int*>(smem + kOffAbort);
   if (x.tid == 0) {
     *x.abort = 0;
-    const uint32_t sharers = SPARSE ? 1 : 2;
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(x.bar(kFull + s), 1);
-      mbar_init(x.bar(kEmpty + s), sharers);
-    }
-    for (int s = 0; s < kRSlots; ++s) {
-      mbar_init(x.bar(kRFull + s), 1);
-      mbar_init(x.bar(kREmpty + s), sharers);
-    }
+    for (int i = 0; i < 2 * kAllSlots; ++i) mbar_init(x.bar(i), 1);
     mbar_init(x.bar(kQFull), 1);
-    mbar_init(x.bar(kQTmem), 2 * kSoftWarps);
-    mbar_init(x.bar(kSFull), 1);
-    mbar_init(x.bar(kSFree), kSoftWarps);
-    mbar_init(x.bar(kPFull), kSoftWarps);
-    mbar_init(x.bar(kPFree), 1);
-    for (int q = 0; q < 4; ++q) mbar_init(x.bar(kX + q), 2);
+    mbar_init(x.bar(kQTmem), kSoftWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(x.bar(kSFull + b), 2);  // Q K^T and the key scales
+      mbar_init(x.bar(kSFree + b), kGroupWarps);
+      mbar_init(x.bar(kPFull + b), kGroupWarps);
+      mbar_init(x.bar(kPFree + b), 1);
+    }
+    for (int q = 0; q < 8; ++q) mbar_init(x.bar(kX + q), 2);
+    for (int q = 0; q < 4; ++q) mbar_init(x.bar(kXL + q), 4);
     mbar_init(x.bar(kDrain), 1);
     mbar_init(x.bar(kDrainPV), 1);
     fence_barrier_init();
   }
-  if (x.tid < kSlots + kRSlots) reinterpret_cast<int*>(smem + kOffIssued)[x.tid] = -1;
+  if (x.tid < kAllSlots) reinterpret_cast<int*>(smem + kOffIssued)[x.tid] = -1;
   if (x.warp == 1) {
     tmem_alloc(smem_u32(tslot), kTmemCols);
     tmem_relinquish();
   }
   fence_before_sync();
   __syncthreads();
-  cluster_sync();  // the peer's barriers exist before any remote arrive or load
   fence_after_sync();
   x.tbase = *tslot;
 
-  if (x.warp >= 4 && x.warp < 12) {
-    softmax_rows<SPARSE>(x, maps, p);
+  // registers: 640 threads start with 96 each; the four control warps give 40
+  // up and the softmax warps take 8 more (128 * 56 + 512 * 104 <= 640 * 96)
+  static_assert(128 * kControlRegs + 512 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
+  if (x.warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kControlRegs));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+  if (x.warp >= 4) {
+    softmax_rows<SPARSE, UNI>(x, maps, p);
   } else if (x.warp == 1) {
-    qk_issue<SPARSE>(x, maps);
+    qk_issue(x, maps);
   } else if (x.warp == 3) {
-    pv_issue<SPARSE>(x);
-  } else {
-    const int pidx = x.warp == 0 ? 0 : (x.warp == 2 ? 1 : x.warp - 10);
+    pv_issue(x);
+  } else if (x.warp == 0) {
     if constexpr (SPARSE)
-      produce_sparse(x, maps, p, pidx);
+      produce_sparse<true>(x, maps, p);
     else
-      produce_dense(x, maps, p, pidx);
+      produce_dense(x, maps, p);
+  } else {
+    if constexpr (SPARSE)
+      produce_sparse<false>(x, maps, p);
+    else
+      scales_dense<UNI>(x, p);
   }
 
   // ------------------------------------------------------------ teardown
@@ -834,25 +1069,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (x.warp == 1) tmem_dealloc(x.tbase, kTmemCols);
-  // every load into this CTA's shared memory must have landed before it
-  // exits: per slot, the latest use issued here or by the peer, whose record
-  // is read once it has stopped issuing (all were consumed unless a wait gave
-  // up); then q
-  cluster_sync();
+  // every load must have landed before the CTA exits: per slot, the latest use
+  // issued (all were consumed unless a wait gave up); then q
   if (x.tid == 0 && x.n_chunks > 0) {
     const volatile int* issued = reinterpret_cast<const volatile int*>(smem + kOffIssued);
-    for (int e = 0; e < kSlots + kRSlots; ++e) {
-      int last = issued[e];
-      if constexpr (!SPARSE)
-        last = max(last, ld_cluster_s32(map_to_rank(smem_u32(smem + kOffIssued + 4 * e), x.rank ^ 1)));
-      if (last >= 0) drain_wait(x, x.bar(e < kSlots ? kFull + e : kRFull + e - kSlots), last & 1, 12);
-    }
+    for (int e = 0; e < kAllSlots; ++e)
+      if (issued[e] >= 0) drain_wait(x, x.bar(kFull + e), issued[e] & 1, 12);
     drain_wait(x, x.bar(kQFull), 0, 13);
   }
-  cluster_sync();  // no CTA exits while loads into the other may still land
 }
 
-template <bool SPARSE>
+template <bool SPARSE, bool UNI>
 cudaError_t launch_variant(const VsMaps& maps, const DecodeParams& p, dim3 grid, int* status, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -860,11 +1087,11 @@ cudaError_t launch_variant(const VsMaps& maps, const DecodeParams& p, dim3 grid,
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(decode_vs_kernel<SPARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(decode_vs_kernel<SPARSE, UNI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  decode_vs_kernel<SPARSE><<<grid, kThreads, kSmem, stream>>>(maps, p, status);
+  decode_vs_kernel<SPARSE, UNI><<<grid, kThreads, kSmem, stream>>>(maps, p, status);
   return cudaGetLastError();
 }
 
@@ -887,8 +1114,11 @@ cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_r
             : make_out_map(&maps.part, p.segm_out, static_cast<uint64_t>(q_rows),
                            static_cast<uint64_t>(p.num_segments), false, 32, 32, true);
   if (e != cudaSuccess) return e;
-  return sparse ? launch_variant<true>(maps, p, grid, status, stream)
-                : launch_variant<false>(maps, p, grid, status, stream);
+  if (sparse) return launch_variant<true, false>(maps, p, grid, status, stream);
+  // groups of a multiple of 32 slots: the 32 keys of a softmax warp (32-aligned
+  // positions of one block) share their scale
+  return p.scale_group % kPart == 0 ? launch_variant<false, true>(maps, p, grid, status, stream)
+                                    : launch_variant<false, false>(maps, p, grid, status, stream);
 }
 
 }  // namespace mla

@@ -52,6 +52,8 @@ struct DecodeParams {
   // slot s is scaled by kv_scales[s / scale_group]; null: kv_scale alone
   const float* kv_scales;
   int32_t scale_group;
+  uint32_t scale_magic, scale_shift;  // s / scale_group = mulhi(s, magic) >> shift (0 <= s < 2^31;
+                                      // magic 0: s >> shift)
   int32_t slot_rows;             // rows of a partial slot (balanced schedule)
 };
 

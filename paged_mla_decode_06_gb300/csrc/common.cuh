@@ -113,6 +113,20 @@ __device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32
   lo = l16;
 }
 
+// Four weights (in order from the low byte) as two words of e4m3 codes, hi and
+// lo as in p_terms.
+__device__ __forceinline__ void p_terms4(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b16 h0, h1, l0, l1;\n .reg .b32 a, b, c, d;\n"
+      " cvt.rn.f16x2.f32 a, %3, %2;\n cvt.rn.f16x2.f32 b, %5, %4;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h0, a;\n cvt.rn.satfinite.e4m3x2.f16x2 h1, b;\n"
+      " cvt.rn.f16x2.e4m3x2 c, h0;\n cvt.rn.f16x2.e4m3x2 d, h1;\n"
+      " sub.f16x2 a, a, c;\n sub.f16x2 b, b, d;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, a;\n cvt.rn.satfinite.e4m3x2.f16x2 l1, b;\n"
+      " mov.b32 %0, {h0, h1};\n mov.b32 %1, {l0, l1};\n}\n"
+      : "=r"(hi), "=r"(lo)
+      : "f"(p0), "f"(p1), "f"(p2), "f"(p3));
+}
+
 // A key of a cache with group scales, as the softmax takes it. With s the
 // group's scale, s2 the key's base-2 score factor times the raw score q . c
 // (c the codes), and t = s2 s + log2 s, the weights 2^(t - m) multiply the

@@ -62,42 +62,43 @@ constexpr int kKeys = 128;               // keys per chunk: N of Q K^T, K of P V
 constexpr int kHalf = 64;                // keys per TMA box, and per softmax warp
 constexpr int kSlot = kKeys * 128;       // ring slot: a 128-byte column box of a chunk (or of q)
 constexpr int kRSlot = kKeys * 64;       // rope ring slot
-constexpr int kKSlots = 4;               // latent boxes of the other CTA's value columns
-constexpr int kVSlots = 6;               // latent boxes of the own value columns
-constexpr int kRSlots = 2;
-constexpr int kAllSlots = kKSlots + kVSlots + kRSlots;
-constexpr int kQStage = 2;               // q's latent boxes land in value slots 2..5
-constexpr int kSoftWarps = 16;           // warps 4-19: two groups (even and odd chunks) of four
-                                         // TMEM lane quarters x two key halves
+constexpr int kKChunks = 2;              // ring of the other CTA's value columns (two boxes) and the
+                                         // rope box: chunks
+constexpr int kVChunks = 3;              // ring of the own value columns (two boxes): chunks
+constexpr int kQStage = 2;               // q's latent boxes land in value slots 2..5 (chunks 1 and 2)
+constexpr int kSoftWarps = 16;           // warps 4-19: two groups (even and odd half-chunks) of four
+                                         // TMEM lane quarters x two key quarters
 constexpr int kGroupWarps = 8;
-constexpr int kPart = 32;                // keys that share a scale where groups are multiples of it
+constexpr int kPart = 32;                // keys of a softmax warp; they share their scale where the
+                                         // groups are multiples of it
 constexpr int kThreads = 32 * (4 + kSoftWarps);
-constexpr int kLaunchRegs = 96;          // 65536 / 640, by allocation unit
-constexpr int kControlRegs = 56;
-constexpr int kSoftRegs = 104;
-constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P for 64 keys
+constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P of a half-chunk
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;           // 256 columns
-constexpr uint32_t kTmemS = 256;         // 128
+constexpr uint32_t kTmemS = 256;         // 2 x 64
 constexpr uint32_t kTmemQ = 384;         // 128: 512 latent dims, four to a column
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
-constexpr float kPBias = 4.f;            // p = 2^(t - m_ref + kPBias) <= 2^(2 kPBias)
-constexpr float kMove = 4.f;             // m_ref moves when a chunk max exceeds it by more
+// p = 2^(t - ref + kPBias); the reference moves when a half-chunk's maximum
+// exceeds it by more than kMove, so that p <= 2^8.75 = 431 (e4m3 ends at 448)
+// and a row's largest weight is at 2^4 or more.
+constexpr float kPBias = 4.f;
+constexpr float kMove = 4.75f;
 
 enum : int {
-  kFull = 0,                 // [kAllSlots] slot loaded (key ring, value ring, rope ring)
-  kEmpty = kAllSlots,        // [kAllSlots] slot released
-  kQFull = 2 * kAllSlots,    // q staged
+  kFull = 0,                 // [kVChunks] chunk c loaded, at c % kVChunks: both kinds of boxes
+  kKEmpty = kFull + kVChunks,   // [kKChunks] key and rope boxes released
+  kVEmpty = kKEmpty + kKChunks,  // [kVChunks] value boxes released
+  kQFull = kVEmpty + kVChunks,  // q staged
   kQTmem,                    // q copied to TMEM: the staging slots are free
-  // by the parity of the chunk (each phase is then waited for by all that
-  // wait on the barrier at all):
-  kSFull,                    // [2] S written, key scales ready
+  // of half-chunk g, at index g % 2:
+  kSFull,                    // [2] S written and key scales ready
   kSFree = kSFull + 2,       // [2] S read
   kPFull = kSFree + 2,       // [2] P written
-  kPFree = kPFull + 2,       // [2] P V complete: P may be replaced, O holds the chunk
-  kX = kPFree + 2,           // [2][4] the two warps of a row quarter have posted their maxima
-  kXL = kX + 8,              // [4] the four warps of a row quarter have posted their sums
+  kPFree = kPFull + 2,       // [2] P V complete: P may be replaced, O holds the half-chunk
+  kX = kPFree + 2,           // [4][4] (at g % 4) the two warps of a row quarter have posted their maxima
+  kScFree = kX + 16,         // [2] key scales of a chunk read
+  kXL = kScFree + 2,         // [4] the four warps of a row quarter have posted their sums
   kDrain = kXL + 4,          // the Q K^T issuer's MMAs complete
   kDrainPV,
   kNumBars
@@ -105,53 +106,31 @@ enum : int {
 
 // Shared memory: header, q's rope columns, P, the three rings.
 constexpr int kOffBar = 0;
-constexpr int kOffTslot = 384;
-constexpr int kOffAbort = 388;
-constexpr int kOffIssued = 448;           // [kAllSlots] int: last use issued per slot
-constexpr int kOffXMax = 1024;            // [4][2][128] maxima of chunk g (at g % 4) by key half;
-                                          // at the end the row sums, in the two oldest
-constexpr int kOffScale = 5120;           // [2][mul, add, inv][128] of chunk g (at g % 2)
-constexpr int kOffMask = kOffScale + 2 * 3 * kKeys * 4;  // [2][4] bits of existing keys
+constexpr int kOffTslot = 512;
+constexpr int kOffAbort = 516;
+constexpr int kOffIssued = 576;           // [2][kVChunks] int: last chunk issued, by kind of boxes
+constexpr int kOffMask = 640;             // [2][4] bits of existing keys of chunk c (at c % 2)
+constexpr int kOffXMax = 768;             // [4][2][128] maxima of half-chunk g (at g % 4) by key quarter
+constexpr int kOffScale = 4864;           // [2][mul, add, inv][128] of chunk c (at c % 2)
+constexpr int kOffLsum = 7936;            // [4][128] row sums by group and key quarter
 constexpr int kOffQR = 10240;             // 128 rows x 64 bytes, 64-byte swizzle
-constexpr int kOffP = kOffQR + kRSlot;    // [key half][hi, lo] tiles, 64-byte swizzle
+constexpr int kOffP = kOffQR + kRSlot;    // [g % 2][hi, lo] tiles of half-chunk g, 64-byte swizzle
 constexpr int kOffRope = kOffP + 4 * kPTile;
-constexpr int kOffKey = kOffRope + kRSlots * kRSlot;
-constexpr int kOffVal = kOffKey + kKSlots * kSlot;
-constexpr int kSmem = kOffVal + kVSlots * kSlot + 1024;  // + alignment slack
-static_assert(kNumBars * 8 <= kOffTslot && kOffIssued + 4 * kAllSlots <= kOffXMax, "header space");
-static_assert(kOffMask + 32 <= kOffQR, "scale space");
-static_assert(kVSlots % 2 == 0 && kKSlots % 2 == 0 && kSmem <= 232448, "shared memory budget");
+constexpr int kOffKey = kOffRope + kKChunks * kRSlot;
+constexpr int kOffVal = kOffKey + kKChunks * 2 * kSlot;
+constexpr int kSmem = kOffVal + kVChunks * 2 * kSlot + 1024;  // + alignment slack
+static_assert(kNumBars * 8 <= kOffTslot && kOffIssued + 8 * kVChunks <= kOffMask && kOffLsum + 2048 <= kOffQR,
+              "header space");
+static_assert(kSmem <= 232448, "shared memory budget");
 
-// Box b of chunk g (in the order Q K^T takes them: two of the other CTA's
-// value columns, two of the own, the rope columns): its barrier index, shared
-// memory, use of the slot and first column.
+// Box j of chunk c: 0, 1 of the other CTA's value columns, 2, 3 of the own, 4 the rope columns.
 struct Box {
-  int index, use, col, off;
-  bool rope;
+  int col, off;  // first column, shared memory
 };
-__device__ __forceinline__ Box box_of(int g, int b, int rank) {
-  Box x;
-  x.rope = b == 4;
-  if (b < 2) {
-    const int i = 2 * g + b, s = i % kKSlots;
-    x.index = s;
-    x.use = i / kKSlots;
-    x.col = 128 * (2 * (rank ^ 1) + b);
-    x.off = kOffKey + s * kSlot;
-  } else if (b < 4) {
-    const int i = 2 * g + b - 2, s = i % kVSlots;
-    x.index = kKSlots + s;
-    x.use = i / kVSlots;
-    x.col = 128 * (2 * rank + b - 2);
-    x.off = kOffVal + s * kSlot;
-  } else {
-    const int s = g % kRSlots;
-    x.index = kKSlots + kVSlots + s;
-    x.use = g / kRSlots;
-    x.col = kRank;
-    x.off = kOffRope + s * kRSlot;
-  }
-  return x;
+__device__ __forceinline__ Box box_of(int c, int j, int rank) {
+  if (j < 2) return Box{128 * (2 * (rank ^ 1) + j), kOffKey + (2 * (c % kKChunks) + j) * kSlot};
+  if (j < 4) return Box{128 * (2 * rank + j - 2), kOffVal + (2 * (c % kVChunks) + j - 2) * kSlot};
+  return Box{kRank, kOffRope + c % kKChunks * kRSlot};
 }
 
 struct VsMaps {
@@ -173,7 +152,7 @@ struct Ctx {
   int tid, warp, lane, rank;
   int H, unit, tok0, qlen, row0, rows_total, part_len;
   int64_t list_base;
-  int seg, seg_start, seg_end, n_chunks;
+  int seg, seg_start, seg_end, n_chunks, n_half;  // chunks of 128 keys, half-chunks of 64
   int pslot;  // partial slot of a balanced piece, -1: write out/lse
   bool fin;
   __device__ uint32_t bar(int i) const { return bar0 + 8u * i; }
@@ -249,12 +228,24 @@ __device__ __forceinline__ int key_slot(const Ctx& x, const DecodeParams& p, con
 }
 
 // ------------------------------------------------------------------ producers
-// The slot of box x may be filled: its last use is released, or (first use) q
-// has left the value slots that stage it.
-__device__ __forceinline__ bool slot_ready(const Ctx& x, const Box& b) {
-  if (b.use >= 1) return wait_phase(x, x.bar(kEmpty + b.index), (b.use - 1) & 1, 11);
-  const bool staged = b.index >= kKSlots + kQStage && b.index < kKSlots + kQStage + 4;
-  return !staged || wait_phase(x, x.bar(kQTmem), 0, 10);
+// The slots of a chunk's value boxes (or its others) may be filled: their last
+// use is released and, where q is staged there, q has left. Uniform in the warp.
+template <bool VALUES>
+__device__ __forceinline__ bool slots_ready(const Ctx& x, int c) {
+  constexpr int kRing = VALUES ? kVChunks : kKChunks;
+  if (c >= kRing) return warp_wait(x, x.bar((VALUES ? kVEmpty : kKEmpty) + c % kRing), (c / kRing - 1) & 1, 11);
+  return !VALUES || c == 0 || warp_wait(x, x.bar(kQTmem), 0, 10);
+}
+// One arrival for either kind, with the bytes to come, on the chunk's barrier.
+template <bool VALUES>
+__device__ __forceinline__ uint32_t announce(const Ctx& x, int c, uint32_t bytes) {
+  const uint32_t full = x.bar(kFull + c % kVChunks);
+  if (x.lane == 0) {
+    mbar_arrive_expect_tx(full, bytes);
+    reinterpret_cast<volatile int*>(x.smem + kOffIssued)[(VALUES ? kVChunks : 0) + c % kVChunks] = c;
+  }
+  __syncwarp();
+  return full;
 }
 
 // Dense: warp 0 loads a chunk's boxes, first those that wait for Q K^T alone,
@@ -263,46 +254,36 @@ __device__ __forceinline__ bool slot_ready(const Ctx& x, const Box& b) {
 // them in turn takes about 350 cycles each, which alone held the loop at 4240
 // cycles a chunk).
 template <bool VALUES>
-__device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int g, int row0, int row1) {
+__device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int c, int row0, int row1) {
   constexpr int kCount = VALUES ? 2 : 3;
   const int lane = x.lane;
-  const int j = VALUES ? 2 + (lane >> 1) : (lane >> 1) < 2 ? (lane >> 1) : 4;
-  const bool two = x.seg_start + g * kKeys + kHalf < x.seg_end;
-  bool ok = true;
-  if (lane < 2 * kCount) {
-    const Box b = box_of(g, j, x.rank);
-    ok = slot_ready(x, b);
-    if (ok && ((lane & 1) == 0 || two)) {
-      const int half = (b.rope ? kRSlot : kSlot) / 2;
-      const uint32_t full = x.bar(kFull + b.index);
-      if ((lane & 1) == 0) {
-        mbar_arrive_expect_tx(full, two ? 2 * half : half);
-        reinterpret_cast<volatile int*>(x.smem + kOffIssued)[b.index] = b.use;
-      }
-      tma_load_2d(smem_u32(x.smem + b.off + (lane & 1) * half), b.rope ? &maps.kvr : &maps.kv, b.col,
-                  (lane & 1) != 0 ? row1 : row0, full);
-    }
+  const bool two = 2 * c + 1 < x.n_half;
+  if (!slots_ready<VALUES>(x, c)) return false;
+  const uint32_t full = announce<VALUES>(x, c, (2 * kSlot + (VALUES ? 0 : kRSlot)) >> (two ? 0 : 1));
+  if (lane < 2 * kCount && ((lane & 1) == 0 || two)) {
+    const int i = lane >> 1;
+    const bool rope = i == 2;
+    const Box b = box_of(c, VALUES ? 2 + i : rope ? 4 : i, x.rank);
+    tma_load_2d(smem_u32(x.smem + b.off + (lane & 1) * ((rope ? kRSlot : kSlot) / 2)), rope ? &maps.kvr : &maps.kv,
+                b.col, (lane & 1) != 0 ? row1 : row0, full);
   }
-  return __all_sync(0xffffffffu, ok) != 0;
+  __syncwarp();
+  return true;
 }
 
 // Sparse: lane l issues one gather4 of the rows of keys 4 l .. 4 l + 3 of each
 // box. A key without a slot reads row 0: its score is masked and its value
 // row zeroed by the softmax warps, whatever the row holds.
 template <bool VALUES>
-__device__ __forceinline__ bool gather_boxes(const Ctx& x, const VsMaps& maps, int g, const int (&r)[4]) {
+__device__ __forceinline__ bool gather_boxes(const Ctx& x, const VsMaps& maps, int c, const int (&r)[4]) {
+  if (!slots_ready<VALUES>(x, c)) return false;
+  const uint32_t full = announce<VALUES>(x, c, 2 * kSlot + (VALUES ? 0 : kRSlot));
 #pragma unroll
   for (int i = 0; i < (VALUES ? 2 : 3); ++i) {
-    const Box b = box_of(g, VALUES ? 2 + i : (i < 2 ? i : 4), x.rank);
-    if (!__all_sync(0xffffffffu, slot_ready(x, b))) return false;
-    const uint32_t full = x.bar(kFull + b.index);
-    if (x.lane == 0) {
-      mbar_arrive_expect_tx(full, b.rope ? kRSlot : kSlot);
-      reinterpret_cast<volatile int*>(x.smem + kOffIssued)[b.index] = b.use;
-    }
-    __syncwarp();
-    tma_gather4(smem_u32(x.smem + b.off + (b.rope ? 256 : 512) * x.lane), b.rope ? &maps.kvr : &maps.kv, b.col, r[0],
-                r[1], r[2], r[3], full);
+    const bool rope = i == 2;
+    const Box b = box_of(c, VALUES ? 2 + i : rope ? 4 : i, x.rank);
+    tma_gather4(smem_u32(x.smem + b.off + (rope ? 256 : 512) * x.lane), rope ? &maps.kvr : &maps.kv, b.col, r[0], r[1],
+                r[2], r[3], full);
   }
   return true;
 }
@@ -355,16 +336,17 @@ __device__ __forceinline__ float scale_of_slot(const DecodeParams& p, int s) {
   return __ldg(p.kv_scales + g);
 }
 
-// Posts the key scales of chunk g (part i of 32 keys: lane's key 32 i + lane;
+// Posts the key scales of chunk c (part i of 32 keys: lane's key 32 i + lane;
 // UNI: lane i < 4 has the scale of part i) and the bits of the keys that exist,
-// once the softmax is done with those two chunks back (it has posted P).
+// once the softmax has read those two chunks back. The half-chunks' S barriers
+// count the post as well as Q K^T.
 template <bool UNI>
-__device__ __forceinline__ bool post_scales(const Ctx& x, const DecodeParams& p, int g, const float (&sc)[4],
+__device__ __forceinline__ bool post_scales(const Ctx& x, const DecodeParams& p, int c, const float (&sc)[4],
                                             uint32_t bits) {
   const int lane = x.lane;
-  if (g >= 2 && !warp_wait(x, x.bar(kPFull + (g & 1)), ((g >> 1) - 1) & 1, 27)) return false;
-  float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + (g & 1) * 3 * kKeys;
-  if (lane < 4) reinterpret_cast<uint32_t*>(x.smem + kOffMask)[(g & 1) * 4 + lane] = bits;
+  if (c >= 2 && !warp_wait(x, x.bar(kScFree + (c & 1)), ((c >> 1) - 1) & 1, 27)) return false;
+  float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + (c & 1) * 3 * kKeys;
+  if (lane < 4) reinterpret_cast<uint32_t*>(x.smem + kOffMask)[(c & 1) * 4 + lane] = bits;
 #pragma unroll
   for (int i = 0; i < (UNI ? 1 : 4); ++i) {
     const KeyScale k = key_scale(sc[i], p.score_scale_log2);
@@ -376,7 +358,12 @@ __device__ __forceinline__ bool post_scales(const Ctx& x, const DecodeParams& p,
     }
   }
   __syncwarp();
-  if (lane == 0) mbar_arrive(x.bar(kSFull + (g & 1)));
+  const int nh = min(2, x.n_half - 2 * c);
+  for (int h = 0; h < nh; ++h) {
+    const uint32_t bar = x.bar(kSFull + h);
+    if (c >= 1 && !warp_wait(x, bar, (c - 1) & 1, 28)) return false;  // S of the chunk before
+    if (lane == 0) mbar_arrive(bar);
+  }
   return true;
 }
 
@@ -505,7 +492,7 @@ struct RingPos {
 
 __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   if (x.n_chunks == 0) return;
-  constexpr uint32_t kId = instr_desc(kRows, kKeys, 0, 0, false, false);
+  constexpr uint32_t kId = instr_desc(kRows, kHalf, 0, 0, false, false);
   const uint32_t base = smem_u32(x.smem);
   const uint64_t k_desc = smem_desc_sw128(base, 16, 1024);
   const uint64_t r_desc = smem_desc_sw64(base + kOffRope, 512);
@@ -522,40 +509,36 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   }
   __syncwarp();
   bool ok = warp_wait(x, x.bar(kQFull), 0, 20) && warp_wait(x, x.bar(kQTmem), 0, 21);
-  const uint32_t d = x.tbase + kTmemS;
   const uint32_t a_key = x.tbase + kTmemQ + 64u * (x.rank ^ 1), a_val = x.tbase + kTmemQ + 64u * x.rank;
-  RingPos<kKSlots / 2> kr;
-  RingPos<kVSlots / 2> vr;
-  RingPos<kRSlots> rr;
-  for (int g = 0; g < x.n_chunks && ok; ++g) {
-    ok = g == 0 || warp_wait(x, x.bar(kSFree + ((g - 1) & 1)), ((g - 1) >> 1) & 1, 22);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int slot = j < 2 ? 2 * kr.at + j : kKSlots + 2 * vr.at + j - 2;
-      ok = ok && warp_wait(x, x.bar(kFull + slot), j < 2 ? kr.phase : vr.phase, 23);
-      if (!ok) break;
-      const uint32_t lo = k_lo + ((kOffKey + slot * kSlot) >> 4);  // (the value ring follows the key ring)
-      fence_after_sync();
-      if (one) {
-        mma_box(d, (j < 2 ? a_key : a_val) + 32u * (j & 1), lo, k_hi, kId, j != 0 ? 1u : 0u);
-        if (j < 2) mma_commit(x.bar(kEmpty + slot));  // its only read
-      }
-      __syncwarp();
-    }
-    ok = ok && warp_wait(x, x.bar(kFull + kKSlots + kVSlots + rr.at), rr.phase, 23);
+  RingPos<kKChunks> kr;
+  RingPos<kVChunks> vr;
+  for (int g = 0; g < x.n_half && ok; ++g) {
+    const int h = g & 1;
+    const bool last = h == 1 || g + 1 == x.n_half;  // of the chunk's half-chunks
+    const uint32_t d = x.tbase + kTmemS + kHalf * h;
+    if (h == 0) ok = warp_wait(x, x.bar(kFull + vr.at), vr.phase, 23);
+    ok = ok && (g < 2 || warp_wait(x, x.bar(kSFree + h), ((g >> 1) - 1) & 1, 22));
     if (!ok) break;
     fence_after_sync();
-    const uint64_t rd = r_desc + static_cast<uint64_t>(rr.at * (kRSlot >> 4));
+    // (64 rows of 128 bytes a half, of 64 bytes the rope columns)
+    const uint32_t lo_k = k_lo + ((kOffKey + kr.at * 2 * kSlot + h * kHalf * 128) >> 4);
+    const uint32_t lo_v = k_lo + ((kOffVal + vr.at * 2 * kSlot + h * kHalf * 128) >> 4);
+    const uint64_t rd = r_desc + static_cast<uint64_t>((kr.at * kRSlot + h * kHalf * 64) >> 4);
     if (one) {
+      mma_box(d, a_key, lo_k, k_hi, kId, 0u);
+      mma_box(d, a_key + 32u, lo_k + (kSlot >> 4), k_hi, kId, 1u);
+      mma_box(d, a_val, lo_v, k_hi, kId, 1u);
+      mma_box(d, a_val + 32u, lo_v + (kSlot >> 4), k_hi, kId, 1u);
       mma_ss_f8(d, q_desc, rd, kId, 1u);
       mma_ss_f8(d, q_desc + 2, rd + 2, kId, 1u);
-      mma_commit(x.bar(kEmpty + kKSlots + kVSlots + rr.at));
-      mma_commit(x.bar(kSFull + (g & 1)));
+      mma_commit(x.bar(kSFull + h));
+      if (last) mma_commit(x.bar(kKEmpty + kr.at));  // the key and rope boxes' only reads
     }
     __syncwarp();
-    kr.next();
-    vr.next();
-    rr.next();
+    if (last) {
+      kr.next();
+      vr.next();
+    }
   }
   if (one) {
     mma_commit(x.bar(kDrain));
@@ -563,7 +546,6 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   }
   __syncwarp();
 }
-static_assert(kOffVal == kOffKey + kKSlots * kSlot, "one descriptor base for both rings");
 
 __device__ void pv_issue(const Ctx& x) {
   if (x.n_chunks == 0) return;
@@ -572,28 +554,28 @@ __device__ void pv_issue(const Ctx& x) {
   const uint64_t p_desc = smem_desc_sw64(smem_u32(x.smem + kOffP), 512);
   const uint32_t d = x.tbase + kTmemO;
   const bool one = elect_one();
-  RingPos<kVSlots / 2> vr;
-  for (int g = 0; g < x.n_chunks; ++g) {
+  RingPos<kVChunks> vr;
+  for (int g = 0; g < x.n_half; ++g) {
+    const int h = g & 1;
+    const bool last = h == 1 || g + 1 == x.n_half;
     // P written; the softmax waited for S, whose Q K^T waited for these boxes
-    if (!warp_wait(x, x.bar(kPFull + (g & 1)), (g >> 1) & 1, 24)) break;
+    if (!warp_wait(x, x.bar(kPFull + h), (g >> 1) & 1, 24)) break;
     fence_after_sync();
-    const uint64_t vb = v_desc + static_cast<uint64_t>(vr.at * (2 * kSlot >> 4));
-    const bool two = x.seg_start + g * kKeys + kHalf < x.seg_end;  // else the second half holds no key
+    const uint64_t vb = v_desc + static_cast<uint64_t>((vr.at * 2 * kSlot + h * kHalf * 128) >> 4);
+    const uint64_t pb = p_desc + static_cast<uint64_t>((h * 2 * kPTile) >> 4);
     if (one) {
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 32; ++ks) {
-        if (ks >= 2 && !two) break;
-        const uint64_t av = p_desc + static_cast<uint64_t>(((ks >> 1) * 2 * kPTile + (ks & 1) * 32) >> 4);
+      for (int ks = 0; ks < kHalf / 32; ++ks) {
+        const uint64_t av = pb + static_cast<uint64_t>((ks * 32) >> 4);
         const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
         mma_ss_f8(d, av, bv, kId, (g | ks) != 0 ? 1u : 0u);
         mma_ss_f8(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kId, 1u);
       }
-      mma_commit(x.bar(kEmpty + kKSlots + 2 * vr.at));
-      mma_commit(x.bar(kEmpty + kKSlots + 2 * vr.at + 1));
-      mma_commit(x.bar(kPFree + (g & 1)));
+      if (last) mma_commit(x.bar(kVEmpty + vr.at));
+      mma_commit(x.bar(kPFree + h));
     }
     __syncwarp();
-    vr.next();
+    if (last) vr.next();
   }
   if (one) {
     mma_commit(x.bar(kDrainPV));
@@ -608,16 +590,16 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   const int lane = x.lane;
   const int sw = x.warp - 4;
   const int q4 = x.warp & 3;               // TMEM lane quarter of this warp
-  const int grp = sw >> 3;                 // chunks g with g % 2 == grp
-  const int h = (sw >> 2) & 1;             // its half of a chunk's keys
-  const int kq = sw >> 2;                  // its box of q, and quarter of the CTA's value columns at the end
+  const int h = sw >> 3;                   // half-chunks g with g % 2 == h: half of its chunk, and buffer
+  const int kh = (sw >> 2) & 1;            // its 32 keys of a half-chunk
+  const int cq = sw >> 2;                  // its box of q, and quarter of the CTA's value columns at the end
   const int r = q4 * 32 + lane;            // row within the tile
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const int H = x.H;
   const int rho = x.row0 + r;
   const bool row_ok = rho < x.rows_total;
   const int vis = !row_ok ? 0 : (SPARSE ? INT_MAX : x.part_len - x.qlen + rho / H + 1);
-  const int n = x.n_chunks;
+  const int n = x.n_half;
   bool ok = true;
 
   // this row of q, staged in the value ring, into TMEM (one of the four
@@ -625,7 +607,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   if (n > 0) {
     ok = warp_wait(x, x.bar(kQFull), 0, 30);
     if (ok) {
-      const uint8_t* src = x.smem + kOffVal + (kQStage + kq) * kSlot + r * 128;
+      const uint8_t* src = x.smem + kOffVal + (kQStage + cq) * kSlot + r * 128;
       uint32_t v[32];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -635,7 +617,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
         v[4 * q + 2] = t.z;
         v[4 * q + 3] = t.w;
       }
-      tmem_st_32x32b_x32(x.tbase + lane_off + kTmemQ + 32 * kq, v);
+      tmem_st_32x32b_x32(x.tbase + lane_off + kTmemQ + 32 * cq, v);
       tmem_st_wait();
       fence_before_sync();
       __syncwarp();
@@ -644,54 +626,58 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   }
 
   float* xmax = reinterpret_cast<float*>(x.smem + kOffXMax) + r;
-  // the warp's keys in P: the row's 64 bytes of either tile, 64-byte swizzle
+  // the warp's keys in P: two 16-byte chunks of the row's 64 bytes of either
+  // tile, 64-byte swizzle
   uint8_t* prow = x.smem + kOffP + h * 2 * kPTile + r * 64;
-  const int pswz = (r >> 1) & 3;
-  const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + grp * 3 * kKeys + kHalf * h;
+  const int c0 = ((2 * kh) ^ ((r >> 1) & 3)) << 4, c1 = ((2 * kh + 1) ^ ((r >> 1) & 3)) << 4;
+  const uint32_t ts = x.tbase + lane_off + kTmemS + kHalf * h + kPart * kh;
 
-  float m_ref = -INFINITY, m_true = -INFINITY, l = 0.f;
-  // Every thread follows its row's reference through the maxima of all chunks:
-  // the reference moves to a chunk's maximum that exceeds it by more than
-  // kMove. Returns the factor of what was formed before.
+  // Every thread follows its row's reference through the maxima of all
+  // half-chunks: it moves to one that exceeds it by more than kMove. Returns
+  // the factor of what was formed before.
+  float ref = -INFINITY, l = 0.f;
   auto follow = [&](float mx) {
-    m_true = fmaxf(m_true, mx);
-    if (!(mx > m_ref + kMove)) return 1.f;  // (true also for a row's first visible key)
-    const float a = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - mx);
-    m_ref = mx;
+    if (!(mx > ref + kMove)) return 1.f;  // (moves also when a row's first visible key arrives)
+    const float a = ref == -INFINITY ? 1.f : fast_exp2(ref - mx);
+    ref = mx;
     l *= a;
     return a;
   };
-  // the maximum of chunk g, which the two warps of the other group posted
+  // the maximum of half-chunk g, which two warps of the other group posted. A
+  // group looks at it before it posts its own of g + 1, which the other waits
+  // for before it posts that of g + 4: neither the barrier's phase nor the four
+  // buffers are passed over.
   auto follow_other = [&](int g) {
-    if (!warp_wait(x, x.bar(kX + 4 * (g & 1) + q4), (g >> 1) & 1, 33)) return false;
+    if (!warp_wait(x, x.bar(kX + 4 * (g & 3) + q4), (g >> 2) & 1, 33)) return false;
     const float* xm = xmax + (g & 3) * 2 * kRows;
     follow(fmaxf(xm[0], xm[kRows]));
     return true;
   };
-  for (int g = grp; g < n && ok; g += 2) {
+  for (int g = h; g < n && ok; g += 2) {
     const int ph = (g >> 1) & 1;
-    ok = warp_wait(x, x.bar(kSFull + grp), ph, 31);
+    ok = warp_wait(x, x.bar(kSFull + h), ph, 31);
     if (!ok) break;
     fence_after_sync();
-    float s[kHalf];
+    float s[kPart];
     {
-      uint32_t sr[kHalf];
-      tmem_ld_32x32b_x64(x.tbase + lane_off + kTmemS + kHalf * h, sr);
+      uint32_t sr[kPart];
+      tmem_ld_32x32b_x32(ts, sr);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j) s[j] = __uint_as_float(sr[j]);
+      for (int j = 0; j < kPart; ++j) s[j] = __uint_as_float(sr[j]);
     }
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kSFree + grp));  // the next chunk's Q K^T may overwrite S
-    const uint2 kmask = reinterpret_cast<const uint2*>(x.smem + kOffMask)[2 * grp + h];
-    KeyScale part[2] = {};  // UNI: the scales of the warp's first and second 32 keys
+    if (lane == 0) mbar_arrive(x.bar(kSFree + h));  // Q K^T two half-chunks on may overwrite S
+    const int sst = (g >> 1) & 1;                   // stage of the chunk's scales
+    const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + sst * 3 * kKeys + kHalf * h + kPart * kh;
+    const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * sst + 2 * h + kh];
+    KeyScale part{};
     if constexpr (UNI) {
-      part[0] = KeyScale{ks[0], ks[kKeys], ks[2 * kKeys]};
-      part[1] = KeyScale{ks[kPart], ks[kKeys + kPart], ks[2 * kKeys + kPart]};
+      part = KeyScale{ks[0], ks[kKeys], ks[2 * kKeys]};
     } else {
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 4) {
+      for (int j = 0; j < kPart; j += 4) {
         const float4 mu = *reinterpret_cast<const float4*>(ks + j);
         const float4 ad = *reinterpret_cast<const float4*>(ks + kKeys + j);
         const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(mu.x, mu.y), make_float2(ad.x, ad.y));
@@ -703,48 +689,44 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
       }
     }
     // keys that exist and that the row may see
-    const int lim = min(vis, x.seg_end) - (x.seg_start + g * kKeys + kHalf * h);
-    if (lim < kHalf || (kmask.x & kmask.y) != 0xffffffffu) {
+    const int lim = min(vis, x.seg_end) - (x.seg_start + g * kHalf + kPart * kh);
+    if (lim < kPart || kmask != 0xffffffffu) {
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j)
-        if (!(j < lim && (((j < 32 ? kmask.x : kmask.y) >> (j & 31)) & 1u))) s[j] = -INFINITY;
+      for (int j = 0; j < kPart; ++j)
+        if (!(j < lim && ((kmask >> j) & 1u))) s[j] = -INFINITY;
     }
-    float mine = -INFINITY;
+    float m4[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* v = s + kPart * i;
-      float m4[4];
+    for (int i = 0; i < 4; ++i) m4[i] = max3(s[i], s[i + 4], s[i + 8]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m4[j] = max3(v[j], v[j + 4], v[j + 8]);
+    for (int j = 12; j < kPart - 4; j += 8)
 #pragma unroll
-      for (int j = 12; j < kPart - 4; j += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], v[j + k], v[j + 4 + k]);
-      const float m = max3(fmaxf(m4[0], v[kPart - 4]), max3(m4[1], v[kPart - 3], m4[2]),
-                           max3(v[kPart - 2], m4[3], v[kPart - 1]));
-      mine = fmaxf(mine, UNI ? fmaf(m, part[i].mul, part[i].add) : m);  // (mul > 0; -inf stays)
-    }
+      for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[j + i], s[j + 4 + i]);
     static_assert((kPart - 12) % 8 == 4, "the last four scores");
-    // the row's maximum over both key halves; the previous chunk's before it
-    float* xm = xmax + (g & 3) * 2 * kRows;
-    xm[h * kRows] = mine;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kX + 4 * grp + q4));
-    ok = (g == 0 || follow_other(g - 1)) && warp_wait(x, x.bar(kX + 4 * grp + q4), ph, 32);
+    float mine = max3(fmaxf(m4[0], s[kPart - 4]), max3(m4[1], s[kPart - 3], m4[2]),
+                      max3(s[kPart - 2], m4[3], s[kPart - 1]));
+    if constexpr (UNI) mine = fmaf(mine, part.mul, part.add);  // (mul > 0; -inf stays)
+    // the row's maximum over both key quarters; the previous half-chunk's before it
+    ok = g == 0 || follow_other(g - 1);
     if (!ok) break;
-    const float alpha = follow(fmaxf(mine, xm[(h ^ 1) * kRows]));
+    float* xm = xmax + (g & 3) * 2 * kRows;
+    xm[kh * kRows] = mine;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.bar(kX + 4 * (g & 3) + q4));
+    ok = warp_wait(x, x.bar(kX + 4 * (g & 3) + q4), (g >> 2) & 1, 32);
+    if (!ok) break;
+    const float alpha = follow(fmaxf(mine, xm[(kh ^ 1) * kRows]));
     // p as hi + lo e4m3 terms, 16 keys to a 16-byte chunk of each tile
-    const float base = m_ref == -INFINITY ? 0.f : m_ref - kPBias;
-    uint32_t hi[kHalf / 4], lo[kHalf / 4];
+    const float base = ref == -INFINITY ? 0.f : ref - kPBias;
+    const float sh = UNI ? part.add - base : -base;
+    const float2 mul2 = make_float2(part.mul, part.mul), shift2 = make_float2(sh, sh);
+    float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 mul2 = make_float2(part[i].mul, part[i].mul);
-      const float sh = UNI ? part[i].add - base : -base;
-      const float2 shift2 = make_float2(sh, sh);
-#pragma unroll
-      for (int j = kPart / 4 * i; j < kPart / 4 * (i + 1); ++j) {
-        float2 a = make_float2(s[4 * j], s[4 * j + 1]), b = make_float2(s[4 * j + 2], s[4 * j + 3]);
+    for (int j = 0; j < 8; ++j) {
+      {
+        const int e = 4 * j;
+        float2 a = make_float2(s[e], s[e + 1]), b = make_float2(s[e + 2], s[e + 3]);
         a = UNI ? fma2(a, mul2, shift2) : add2(a, shift2);
         b = UNI ? fma2(b, mul2, shift2) : add2(b, shift2);
         a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
@@ -753,71 +735,75 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
           ps[0] = add2(ps[0], a);
           ps[1] = add2(ps[1], b);
         } else {
-          const float4 iv = *reinterpret_cast<const float4*>(ks + 2 * kKeys + 4 * j);
+          const float4 iv = *reinterpret_cast<const float4*>(ks + 2 * kKeys + e);
           ps[0] = fma2(a, make_float2(iv.x, iv.y), ps[0]);
           ps[1] = fma2(b, make_float2(iv.z, iv.w), ps[1]);
         }
-        uint32_t h0, h1, l0, l1;
-        p_terms(a.x, a.y, h0, l0);
-        p_terms(b.x, b.y, h1, l1);
-        hi[j] = h0 | (h1 << 16);
-        lo[j] = l0 | (l1 << 16);
+        p_terms4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
       }
-      const float psum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-      l = UNI ? fmaf(psum, part[i].inv, l) : l + psum;
     }
-    // the previous chunk's P V has read P and O is complete up to it
-    if (g >= 1) {
-      ok = warp_wait(x, x.bar(kPFree + (grp ^ 1)), ((g - 1) >> 1) & 1, 37);
+    const float psum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+    l = UNI ? fmaf(psum, part.inv, l) : l + psum;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.bar(kScFree + sst));
+    // P V two half-chunks back has read this buffer of P
+    ok = g < 2 || warp_wait(x, x.bar(kPFree + h), ph ^ 1, 37);
+    if (!ok) break;
+    *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+    *reinterpret_cast<uint4*>(prow + kPTile + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(prow + kPTile + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+      // some rows moved their reference: once O is complete up to the previous
+      // half-chunk, this warp rescales its rows of its half of the value
+      // columns. (This barrier's phase before, P V of g - 3, completed with that
+      // of g - 2, as P V is issued in order: the parity cannot be taken for it.)
+      ok = warp_wait(x, x.bar(kPFree + (h ^ 1)), ((g - 1) >> 1) & 1, 38);
       if (!ok) break;
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
-        // some rows moved their reference: this warp rescales its rows of its
-        // half of the value columns
-        fence_after_sync();
+      fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * h + 16 * c;
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(ta, o);
-          tmem_ld_wait();
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * kh + 64 * c;
+        uint32_t o[32], o2[32];
+        tmem_ld_32x32b_x32(ta, o);
+        tmem_ld_32x32b_x32(ta + 32, o2);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st_32x32b_x16(ta, o);
+        for (int i = 0; i < 32; ++i) {
+          o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          o2[i] = __float_as_uint(__uint_as_float(o2[i]) * alpha);
         }
-        tmem_st_wait();
+        tmem_st_32x32b_x32(ta, o);
+        tmem_st_32x32b_x32(ta + 32, o2);
       }
+      tmem_st_wait();
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint8_t* dst = prow + ((c ^ pswz) << 4);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-      *reinterpret_cast<uint4*>(dst + kPTile) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-    }
-    // value rows of keys that do not exist (stale or unloaded ring contents,
-    // cache rows past the sequence, unused list entries) must not reach O
-    // through p = 0: they are zeroed, a quarter by each warp of the key half
-    if ((kmask.x & kmask.y) != 0xffffffffu && (h == 0 || x.seg_start + g * kKeys + kHalf < x.seg_end)) {
-      uint8_t* box = x.smem + box_of(g, 2, x.rank).off + ((lane >> 3) & 1) * kSlot + kHalf * h * 128 + (lane & 7) * 16;
-      for (int j = q4 + 4 * (lane >> 4); j < kHalf; j += 8)
-        if (!(((j < 32 ? kmask.x : kmask.y) >> (j & 31)) & 1u))
-          *reinterpret_cast<uint4*>(box + j * 128) = make_uint4(0u, 0u, 0u, 0u);
+    // value rows of keys that do not exist (stale ring contents, cache rows past
+    // the sequence, unused list entries) must not reach O through p = 0: they
+    // are zeroed, a quarter by each warp
+    if (kmask != 0xffffffffu) {
+      uint8_t* box = x.smem + box_of(g >> 1, 2, x.rank).off + ((lane >> 3) & 1) * kSlot +
+                     (kHalf * h + kPart * kh) * 128 + (lane & 7) * 16;
+      for (int j = q4 + 4 * (lane >> 4); j < kPart; j += 8)
+        if (!((kmask >> j) & 1u)) *reinterpret_cast<uint4*>(box + j * 128) = make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kPFull + grp));
+    if (lane == 0) mbar_arrive(x.bar(kPFull + h));
   }
 
   // ---------------------------------------------------------------- epilogue
-  if (ok && n > 0 && ((n - 1) & 1) != grp) ok = follow_other(n - 1);  // the last chunk was the other group's
-  // sums by group and key half, where the maxima of chunks n - 4 and n - 3 were
-  auto lsum = [&](int i) { return xmax + ((n + (i >> 1)) & 3) * 2 * kRows + (i & 1) * kRows; };
+  if (ok && n > 0 && ((n - 1) & 1) != h) ok = follow_other(n - 1);  // the last one was the other group's
+  float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum) + r;
   if (ok) {
-    *lsum(kq) = l;
+    lsum[cq * kRows] = l;
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kXL + q4));
     ok = warp_wait(x, x.bar(kXL + q4), 0, 34);
   }
+  // O is complete with the last half-chunk (the phase before of its barrier, P V
+  // of n - 3, was waited for by its group before it posted its sum)
   if (ok && n > 0) {
     ok = warp_wait(x, x.bar(kPFree + ((n - 1) & 1)), ((n - 1) >> 1) & 1, 35);
     fence_after_sync();
@@ -825,11 +811,11 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   if (!ok) return;
   float mult = 0.f;
   if (row_ok) {
-    const float L = (*lsum(0) + *lsum(1)) + (*lsum(2) + *lsum(3));
-    const float base = m_ref == -INFINITY ? 0.f : m_ref - kPBias;  // the sums' reference
+    const float L = (lsum[0] + lsum[kRows]) + (lsum[2 * kRows] + lsum[3 * kRows]);
+    const float base = ref == -INFINITY ? 0.f : ref - kPBias;  // the reference of O and the sum
     const int head = rho % H;
     const int64_t th = static_cast<int64_t>(x.tok0 + rho / H) * H + head;
-    const bool writes = x.rank == 0 && kq == 0;
+    const bool writes = x.rank == 0 && cq == 0;
     if (x.fin) {
       float lse = -INFINITY;
       if (p.sinks != nullptr) {
@@ -848,8 +834,9 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
       mult = L > 0.f ? 1.f / L : 0.f;
       if (writes) {
         const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * p.slot_rows + r : th * p.num_segments + x.seg;
-        p.segm_max[ts] = L > 0.f ? m_true : -INFINITY;
-        p.segm_expsum[ts] = L > 0.f ? L * exp2f(base - m_true) : 0.f;
+        // (any reference of the partial serves the merge)
+        p.segm_max[ts] = L > 0.f ? base : -INFINITY;
+        p.segm_expsum[ts] = L;
       }
     }
   }
@@ -858,7 +845,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   // more boxes in use). When all 32 rows are valid one TMA tensor store writes
   // each staged tile; otherwise every store instruction covers four 128-byte
   // row pieces. (TMEM loads are warp-collective.)
-  const int col0 = 256 * x.rank + 64 * kq;
+  const int col0 = 256 * x.rank + 64 * cq;
   const int wr = x.row0 + 32 * q4;          // the warp's first row within the unit
   if (wr >= x.rows_total) return;
   const bool whole = wr + 32 <= x.rows_total;
@@ -902,7 +889,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     for (int c = 0; c < 2; ++c) {
       uint32_t o[32];
       if (x.n_chunks > 0) {
-        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * kq + 32 * c, o);
+        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * cq + 32 * c, o);
         tmem_ld_wait();
       } else {
 #pragma unroll
@@ -920,7 +907,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     for (int c = 0; c < 2; ++c) {
       uint32_t o[32];
       if (x.n_chunks > 0) {
-        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * kq + 32 * c, o);
+        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * cq + 32 * c, o);
         tmem_ld_wait();
       } else {
 #pragma unroll
@@ -1006,14 +993,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     x.seg_start = x.seg * seg_len;
     x.seg_end = min(x.seg_start + seg_len, x.part_len);
   }
-  x.n_chunks = x.seg_end > x.seg_start ? cdiv(x.seg_end - x.seg_start, kKeys) : 0;
+  x.n_half = x.seg_end > x.seg_start ? cdiv(x.seg_end - x.seg_start, kHalf) : 0;
+  x.n_chunks = cdiv(x.n_half, 2);
 
   x.bar0 = smem_u32(smem + kOffBar);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + kOffTslot);
   x.abort = reinterpret_cast<volatile int*>(smem + kOffAbort);
   if (x.tid == 0) {
     *x.abort = 0;
-    for (int i = 0; i < 2 * kAllSlots; ++i) mbar_init(x.bar(i), 1);
+    for (int i = 0; i < kVChunks; ++i) {
+      mbar_init(x.bar(kFull + i), 2);
+      mbar_init(x.bar(kVEmpty + i), 1);
+    }
+    for (int i = 0; i < kKChunks; ++i) mbar_init(x.bar(kKEmpty + i), 1);
     mbar_init(x.bar(kQFull), 1);
     mbar_init(x.bar(kQTmem), kSoftWarps);
     for (int b = 0; b < 2; ++b) {
@@ -1021,14 +1013,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(x.bar(kSFree + b), kGroupWarps);
       mbar_init(x.bar(kPFull + b), kGroupWarps);
       mbar_init(x.bar(kPFree + b), 1);
+      mbar_init(x.bar(kScFree + b), 2 * kGroupWarps);
     }
-    for (int q = 0; q < 8; ++q) mbar_init(x.bar(kX + q), 2);
+    for (int q = 0; q < 16; ++q) mbar_init(x.bar(kX + q), 2);
     for (int q = 0; q < 4; ++q) mbar_init(x.bar(kXL + q), 4);
     mbar_init(x.bar(kDrain), 1);
     mbar_init(x.bar(kDrainPV), 1);
     fence_barrier_init();
   }
-  if (x.tid < kAllSlots) reinterpret_cast<int*>(smem + kOffIssued)[x.tid] = -1;
+  if (x.tid < 2 * kVChunks) reinterpret_cast<int*>(smem + kOffIssued)[x.tid] = -1;
   if (x.warp == 1) {
     tmem_alloc(smem_u32(tslot), kTmemCols);
     tmem_relinquish();
@@ -1038,13 +1031,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   x.tbase = *tslot;
 
-  // registers: 640 threads start with 96 each; the four control warps give 40
-  // up and the softmax warps take 8 more (128 * 56 + 512 * 104 <= 640 * 96)
-  static_assert(128 * kControlRegs + 512 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
-  if (x.warp < 4)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kControlRegs));
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
   if (x.warp >= 4) {
     softmax_rows<SPARSE, UNI>(x, maps, p);
   } else if (x.warp == 1) {
@@ -1069,12 +1055,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (x.warp == 1) tmem_dealloc(x.tbase, kTmemCols);
-  // every load must have landed before the CTA exits: per slot, the latest use
-  // issued (all were consumed unless a wait gave up); then q
+  // every load must have landed before the CTA exits: of each chunk's barrier,
+  // the last chunk issued (all were consumed unless a wait gave up; where it
+  // did between a chunk's two kinds of boxes, the missing arrival is made here,
+  // so that the phase completes with the bytes); then q
   if (x.tid == 0 && x.n_chunks > 0) {
     const volatile int* issued = reinterpret_cast<const volatile int*>(smem + kOffIssued);
-    for (int e = 0; e < kAllSlots; ++e)
-      if (issued[e] >= 0) drain_wait(x, x.bar(kFull + e), issued[e] & 1, 12);
+    for (int e = 0; e < kVChunks; ++e) {
+      const int k = issued[e], v = issued[kVChunks + e], c = max(k, v);
+      if (c < 0) continue;
+      if (k != v) mbar_arrive(x.bar(kFull + e));
+      drain_wait(x, x.bar(kFull + e), (c / kVChunks) & 1, 12);
+    }
     drain_wait(x, x.bar(kQFull), 0, 13);
   }
 }

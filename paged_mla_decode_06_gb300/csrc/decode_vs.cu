@@ -492,7 +492,7 @@ struct RingPos {
 
 __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   if (x.n_chunks == 0) return;
-  constexpr uint32_t kId = instr_desc(kRows, kHalf, 0, 0, false, false);
+  constexpr uint32_t kId = instr_desc(kRows, kKeys, 0, 0, false, false);
   const uint32_t base = smem_u32(x.smem);
   const uint64_t k_desc = smem_desc_sw128(base, 16, 1024);
   const uint64_t r_desc = smem_desc_sw64(base + kOffRope, 512);
@@ -512,18 +512,19 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   const uint32_t a_key = x.tbase + kTmemQ + 64u * (x.rank ^ 1), a_val = x.tbase + kTmemQ + 64u * x.rank;
   RingPos<kKChunks> kr;
   RingPos<kVChunks> vr;
-  for (int g = 0; g < x.n_half && ok; ++g) {
-    const int h = g & 1;
-    const bool last = h == 1 || g + 1 == x.n_half;  // of the chunk's half-chunks
-    const uint32_t d = x.tbase + kTmemS + kHalf * h;
-    if (h == 0) ok = warp_wait(x, x.bar(kFull + vr.at), vr.phase, 23);
-    ok = ok && (g < 2 || warp_wait(x, x.bar(kSFree + h), ((g >> 1) - 1) & 1, 22));
+  const uint32_t d = x.tbase + kTmemS;
+  for (int c = 0; c < x.n_chunks; ++c) {
+    // (a last chunk of one half multiplies whatever the rows of the other hold:
+    // nobody reads those scores)
+    const bool two = 2 * c + 1 < x.n_half;
+    ok = ok && warp_wait(x, x.bar(kFull + vr.at), vr.phase, 23);
+    ok = ok && (c < 1 || (warp_wait(x, x.bar(kSFree), (c - 1) & 1, 22) &&
+                          warp_wait(x, x.bar(kSFree + 1), (c - 1) & 1, 29)));
     if (!ok) break;
     fence_after_sync();
-    // (64 rows of 128 bytes a half, of 64 bytes the rope columns)
-    const uint32_t lo_k = k_lo + ((kOffKey + kr.at * 2 * kSlot + h * kHalf * 128) >> 4);
-    const uint32_t lo_v = k_lo + ((kOffVal + vr.at * 2 * kSlot + h * kHalf * 128) >> 4);
-    const uint64_t rd = r_desc + static_cast<uint64_t>((kr.at * kRSlot + h * kHalf * 64) >> 4);
+    const uint32_t lo_k = k_lo + ((kOffKey + kr.at * 2 * kSlot) >> 4);
+    const uint32_t lo_v = k_lo + ((kOffVal + vr.at * 2 * kSlot) >> 4);
+    const uint64_t rd = r_desc + static_cast<uint64_t>((kr.at * kRSlot) >> 4);
     if (one) {
       mma_box(d, a_key, lo_k, k_hi, kId, 0u);
       mma_box(d, a_key + 32u, lo_k + (kSlot >> 4), k_hi, kId, 1u);
@@ -531,14 +532,13 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
       mma_box(d, a_val + 32u, lo_v + (kSlot >> 4), k_hi, kId, 1u);
       mma_ss_f8(d, q_desc, rd, kId, 1u);
       mma_ss_f8(d, q_desc + 2, rd + 2, kId, 1u);
-      mma_commit(x.bar(kSFull + h));
-      if (last) mma_commit(x.bar(kKEmpty + kr.at));  // the key and rope boxes' only reads
+      mma_commit(x.bar(kSFull));
+      if (two) mma_commit(x.bar(kSFull + 1));
+      mma_commit(x.bar(kKEmpty + kr.at));  // the key and rope boxes' only reads
     }
     __syncwarp();
-    if (last) {
-      kr.next();
-      vr.next();
-    }
+    kr.next();
+    vr.next();
   }
   if (one) {
     mma_commit(x.bar(kDrain));

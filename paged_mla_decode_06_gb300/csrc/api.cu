@@ -119,6 +119,27 @@ mla_status_t check_group_scales(const mla_plan_t* plan, const float* kv_scales, 
   return MLA_OK;
 }
 
+// Whether a call with group scales runs on the value-split kernel, whatever
+// kernel the plan names for the same problem with one scale: every row tile
+// of more than 64 rows the plan gives to a tensor-core kernel, and sparse lists.
+bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
+  if (kv_scales == nullptr) return false;
+  if (plan->prob.topk > 0) return true;
+  return plan->kernel == mla::kTcPair128 || (plan->kernel == mla::kTcRowsN && plan->tile_rows > 64);
+}
+
+// Segments of a fixed schedule. The planner's own choice for sparse lists (about
+// two of its CTAs per SM) suits the warp-MMA kernel; the value-split kernel, two
+// CTAs a tile and one an SM, takes no more of them than one wave of CTAs (32
+// tokens x 2048 keys, 128 heads: MEAS).
+int32_t segments_of(const mla_plan_t* plan, const float* kv_scales) {
+  const mla_problem_t& p = plan->prob;
+  if (p.num_segments != 0 || p.topk == 0 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
+  const int64_t ctas = 2 * static_cast<int64_t>(p.num_tokens) * ((p.num_heads + 127) / 128);
+  const int64_t fit = ctas > 0 ? plan->num_sms / ctas : 1;
+  return static_cast<int32_t>(fit < 1 ? 1 : fit < plan->num_segments ? fit : plan->num_segments);
+}
+
 mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   const mla_problem_t& p = plan->prob;
   mla::DecodeParams d{};
@@ -135,7 +156,7 @@ mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   d.num_heads = p.num_heads;
   d.block_size = p.block_size;
   d.topk = p.topk;
-  d.num_segments = plan->num_segments;
+  d.num_segments = segments_of(plan, in.kv_scales);
   d.tile_size = plan->tile_size;
   d.row_tiles = plan->row_tiles;
   d.score_scale_log2 = in.softmax_scale * in.q_scale * in.kv_scale * 1.4426950408889634f;
@@ -209,15 +230,6 @@ SchedLayout sched_layout(const mla_plan_t* plan) {
   return l;
 }
 
-// Whether a call with group scales runs on the value-split cluster, whatever
-// kernel the plan names for the same problem with one scale: every row tile
-// of more than 64 rows the plan gives to a tensor-core kernel, and sparse lists.
-bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
-  if (kv_scales == nullptr) return false;
-  if (plan->prob.topk > 0) return true;
-  return plan->kernel == mla::kTcPair128 || (plan->kernel == mla::kTcRowsN && plan->tile_rows > 64);
-}
-
 // d.items selects the balanced grid: one CTA pair per item slot (CTA-pair
 // kernel), one CTA or cluster per worker (rows-as-N kernel).
 mla_status_t launch_decode(const mla_plan_t* plan, const mla::DecodeParams& d, int* status,
@@ -231,7 +243,7 @@ mla_status_t launch_decode(const mla_plan_t* plan, const mla::DecodeParams& d, i
     const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
     const unsigned tiles = static_cast<unsigned>((rows + 127) / 128);
     const dim3 grid = d.items != nullptr ? dim3(2u * items, 1u, 1u)
-                                         : dim3(2u * tiles, static_cast<unsigned>(plan->num_segments),
+                                         : dim3(2u * tiles, static_cast<unsigned>(d.num_segments),
                                                 static_cast<unsigned>(plan->grid_z));
     return cuda_status(mla::launch_decode_vs(d, q_rows, kv_rows, grid, status, stream));
   }
@@ -359,7 +371,7 @@ mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* s
     if (s == MLA_OK) s = run_merge_items(plan, in, sinks, ws, out, lse, stream);
     return s;
   }
-  if (plan->num_segments == 1) {
+  if (d.num_segments == 1) {
     d.final_mode = 1;
     d.sinks = sinks;
     d.out = out;
@@ -379,7 +391,7 @@ mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* s
   m.part = part_lens_for(plan, in);
   m.num_tokens = p.num_tokens;
   m.num_heads = p.num_heads;
-  m.num_segments = plan->num_segments;
+  m.num_segments = d.num_segments;
   m.rank = kRank;
   m.tile_size = plan->tile_size;
   m.sinks = sinks;

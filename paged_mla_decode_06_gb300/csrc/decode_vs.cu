@@ -271,21 +271,44 @@ __device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int
   return true;
 }
 
-// Sparse: lane l issues one gather4 of the rows of keys 4 l .. 4 l + 3 of each
-// box. A key without a slot reads row 0: its score is masked and its value
-// row zeroed by the softmax warps, whatever the row holds.
+// Sparse: the rows of a chunk's keys into the own value boxes (VALUES) or the
+// other boxes, in their swizzles, by 16-byte asynchronous copies: an
+// instruction takes 128 bytes of four rows (of the rope columns: 64 of eight).
+// v[k] of lane l is the cache slot of key 32 k + l; a key without one is
+// filled with zeros. (TMA's row gathers move a chunk in 8500 cycles at best:
+// about 13 a row of 128 bytes.)
 template <bool VALUES>
-__device__ __forceinline__ bool gather_boxes(const Ctx& x, const VsMaps& maps, int c, const int (&r)[4]) {
-  if (!slots_ready<VALUES>(x, c)) return false;
-  const uint32_t full = announce<VALUES>(x, c, 2 * kSlot + (VALUES ? 0 : kRSlot));
+__device__ __forceinline__ void copy_rows(const Ctx& x, const DecodeParams& p, int c, const int (&v)[4]) {
+  const int lane = x.lane;
+  const uint8_t* src = static_cast<const uint8_t*>(p.kv);
+  {
+    const Box b = box_of(c, VALUES ? 2 : 0, x.rank);  // and the box after it
+    const uint8_t* from = src + b.col + 16 * (lane & 7);
+    const uint32_t to = smem_u32(x.smem + b.off) + 128 * (lane >> 3) + (((lane & 7) ^ (lane >> 3)) << 4);
 #pragma unroll
-  for (int i = 0; i < (VALUES ? 2 : 3); ++i) {
-    const bool rope = i == 2;
-    const Box b = box_of(c, VALUES ? 2 + i : rope ? 4 : i, x.rank);
-    tma_gather4(smem_u32(x.smem + b.off + (rope ? 256 : 512) * x.lane), rope ? &maps.kvr : &maps.kv, b.col, r[0], r[1],
-                r[2], r[3], full);
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int s = __shfl_sync(0xffffffffu, v[k], 4 * j + (lane >> 3));
+        const uint8_t* row = from + static_cast<int64_t>(max(s, 0)) * kHeadDim;
+        const uint32_t n = s >= 0 ? 16u : 0u;
+        const uint32_t at = (to ^ ((j & 1) << 6)) + 512 * (8 * k + j);
+        cp_async_16(at, row, n);
+        cp_async_16(at + kSlot, row + 128, n);
+      }
   }
-  return true;
+  if constexpr (!VALUES) {
+    const uint8_t* from = src + kRank + 16 * (lane & 3);
+    const uint32_t to =
+        smem_u32(x.smem + box_of(c, 4, x.rank).off) + 64 * (lane >> 2) + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = __shfl_sync(0xffffffffu, v[k], 8 * j + (lane >> 2));
+        cp_async_16(to + 512 * (4 * k + j), from + static_cast<int64_t>(max(s, 0)) * kHeadDim, s >= 0 ? 16u : 0u);
+      }
+  }
 }
 
 // Cache rows of the 64-key halves of a dense request's chunks: looked up by
@@ -395,23 +418,12 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
   __syncwarp();
 }
 
-// Sparse: warp 0 (VALUES) gathers the value boxes, warp 2 the others, and
-// prepares the scales: the slots of a lane's keys are read two chunks ahead
-// and their scales one.
+// Sparse: warp 0 (VALUES) copies the value boxes, warp 2 the others, and
+// prepares the scales. The slots of a lane's keys are read two chunks ahead and
+// their scales one. A chunk is posted once the next one's copies are under way.
 template <bool VALUES>
-__device__ void produce_sparse(const Ctx& x, const VsMaps& maps, const DecodeParams& p) {
+__device__ void produce_sparse(const Ctx& x, const DecodeParams& p) {
   const int lane = x.lane;
-  if (lane == 0) {
-    tma_prefetch_desc(&maps.kv);
-    tma_prefetch_desc(&maps.kvr);
-  }
-  int rows[4];
-  auto gather_rows = [&](int g) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      rows[k] = g < x.n_chunks ? key_slot<true>(x, p, nullptr, x.seg_start + g * kKeys + 4 * lane + k) : 0;
-  };
-  gather_rows(0);
   int slot[4], next[4];
   float sc[4];
   auto slots_of = [&](int g, int (&v)[4]) {
@@ -423,17 +435,23 @@ __device__ void produce_sparse(const Ctx& x, const VsMaps& maps, const DecodePar
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = v[i] >= 0 ? scale_of_slot(p, v[i]) : 1.f;
   };
-  if constexpr (!VALUES) {
-    slots_of(0, slot);
-    scales_of(slot);
-    slots_of(1, next);
-  }
-  for (int g = 0; g < x.n_chunks; ++g) {
-    int r[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = rows[k] >= 0 ? rows[k] : 0;
-    gather_rows(g + 1);
-    if (!gather_boxes<VALUES>(x, maps, g, r)) break;
+  auto post = [&](int g) {  // the copies are complete: make them visible to the MMAs
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.bar(kFull + g % kVChunks));
+  };
+  slots_of(0, slot);
+  if constexpr (!VALUES) scales_of(slot);
+  slots_of(1, next);
+  int g = 0;
+  for (; g < x.n_chunks; ++g) {
+    if (!slots_ready<VALUES>(x, g)) break;
+    copy_rows<VALUES>(x, p, g, slot);
+    cp_async_commit();
+    if (g > 0) {
+      cp_async_wait<1>();
+      post(g - 1);
+    }
     if constexpr (!VALUES) {
       uint32_t bits = 0u;
 #pragma unroll
@@ -442,12 +460,14 @@ __device__ void produce_sparse(const Ctx& x, const VsMaps& maps, const DecodePar
         if (lane == i) bits = b;
       }
       if (!post_scales<false>(x, p, g, sc, bits)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) slot[i] = next[i];
-      scales_of(slot);
-      slots_of(g + 2, next);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slot[i] = next[i];
+    if constexpr (!VALUES) scales_of(slot);
+    slots_of(g + 2, next);
   }
+  cp_async_wait<0>();  // also where a wait gave up: no copy outlives the CTA
+  if (g > 0 && g == x.n_chunks) post(g - 1);
   __syncwarp();
 }
 
@@ -781,7 +801,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     // value rows of keys that do not exist (stale ring contents, cache rows past
     // the sequence, unused list entries) must not reach O through p = 0: they
     // are zeroed, a quarter by each warp
-    if (kmask != 0xffffffffu) {
+    if (!SPARSE && kmask != 0xffffffffu) {
       uint8_t* box = x.smem + box_of(g >> 1, 2, x.rank).off + ((lane >> 3) & 1) * kSlot +
                      (kHalf * h + kPart * kh) * 128 + (lane & 7) * 16;
       for (int j = q4 + 4 * (lane >> 4); j < kPart; j += 8)
@@ -1039,12 +1059,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     pv_issue(x);
   } else if (x.warp == 0) {
     if constexpr (SPARSE)
-      produce_sparse<true>(x, maps, p);
+      produce_sparse<true>(x, p);
     else
       produce_dense(x, maps, p);
   } else {
     if constexpr (SPARSE)
-      produce_sparse<false>(x, maps, p);
+      produce_sparse<false>(x, p);
     else
       scales_dense<UNI>(x, p);
   }
@@ -1096,8 +1116,8 @@ cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_r
   VsMaps maps{};
   cudaError_t e = make_row_map(&maps.q, p.q, static_cast<uint64_t>(q_rows), kRows, true);
   if (e == cudaSuccess) e = make_row_map(&maps.qr, p.q, static_cast<uint64_t>(q_rows), kRows, true, 64);
-  if (e == cudaSuccess) e = make_row_map(&maps.kv, p.kv, static_cast<uint64_t>(kv_rows), sparse ? 1 : kHalf, true);
-  if (e == cudaSuccess) e = make_row_map(&maps.kvr, p.kv, static_cast<uint64_t>(kv_rows), sparse ? 1 : kHalf, true, 64);
+  if (e == cudaSuccess) e = make_row_map(&maps.kv, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true);
+  if (e == cudaSuccess) e = make_row_map(&maps.kvr, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true, 64);
   if (e == cudaSuccess && p.out != nullptr)
     e = make_out_map(&maps.out, p.out, static_cast<uint64_t>(q_rows), 1, true, 64, 32, true);
   if (e == cudaSuccess && p.segm_out != nullptr)

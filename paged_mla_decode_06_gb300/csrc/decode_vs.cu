@@ -271,44 +271,36 @@ __device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int
   return true;
 }
 
-// Sparse: the rows of a chunk's keys into the own value boxes (VALUES) or the
-// other boxes, in their swizzles, by 16-byte asynchronous copies: an
-// instruction takes 128 bytes of four rows (of the rope columns: 64 of eight).
-// v[k] of lane l is the cache slot of key 32 k + l; a key without one is
-// filled with zeros. (TMA's row gathers move a chunk in 8500 cycles at best:
-// about 13 a row of 128 bytes.)
-template <bool VALUES>
+// Sparse: the rows of a chunk's keys into its boxes, in their swizzles, by
+// 16-byte asynchronous copies: an instruction takes 128 bytes of four rows (of
+// the rope columns: 64 of eight). v[k] of lane l is the cache slot of key
+// 32 k + l; a key without one is filled with zeros. (TMA's row gathers take
+// about 13 cycles a row of 128 bytes: 8500 cycles a chunk.)
+enum : int { kOther = 0, kOwn = 2, kRope = 4 };  // first box (box_of) of a share
+template <int FIRST>
 __device__ __forceinline__ void copy_rows(const Ctx& x, const DecodeParams& p, int c, const int (&v)[4]) {
-  const int lane = x.lane;
-  const uint8_t* src = static_cast<const uint8_t*>(p.kv);
-  {
-    const Box b = box_of(c, VALUES ? 2 : 0, x.rank);  // and the box after it
-    const uint8_t* from = src + b.col + 16 * (lane & 7);
-    const uint32_t to = smem_u32(x.smem + b.off) + 128 * (lane >> 3) + (((lane & 7) ^ (lane >> 3)) << 4);
+  constexpr int kLanes = FIRST == kRope ? 4 : 8;  // of a row
+  constexpr int kStep = 32 / kLanes;              // keys an instruction
+  const int key = x.lane / kLanes, piece = x.lane % kLanes;
+  const Box b = box_of(c, FIRST, x.rank);
+  const uint8_t* from = static_cast<const uint8_t*>(p.kv) + b.col + 16 * piece;
+  const uint32_t to = smem_u32(x.smem + b.off) + 16 * kLanes * key +
+                      ((FIRST == kRope ? piece ^ ((key >> 1) & 3) : piece ^ key) << 4);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int s = __shfl_sync(0xffffffffu, v[k], 4 * j + (lane >> 3));
-        const uint8_t* row = from + static_cast<int64_t>(max(s, 0)) * kHeadDim;
-        const uint32_t n = s >= 0 ? 16u : 0u;
-        const uint32_t at = (to ^ ((j & 1) << 6)) + 512 * (8 * k + j);
+    for (int j = 0; j < kLanes; ++j) {
+      const int s = __shfl_sync(0xffffffffu, v[k], kStep * j + key);
+      const uint8_t* row = from + static_cast<int64_t>(max(s, 0)) * kHeadDim;
+      const uint32_t n = s >= 0 ? 16u : 0u;
+      if constexpr (FIRST == kRope) {
+        cp_async_16(to + 512 * (kLanes * k + j), row, n);
+      } else {  // (odd steps have bit 2 of the key set)
+        const uint32_t at = (to ^ ((j & 1) << 6)) + 512 * (kLanes * k + j);
         cp_async_16(at, row, n);
         cp_async_16(at + kSlot, row + 128, n);
       }
-  }
-  if constexpr (!VALUES) {
-    const uint8_t* from = src + kRank + 16 * (lane & 3);
-    const uint32_t to =
-        smem_u32(x.smem + box_of(c, 4, x.rank).off) + 64 * (lane >> 2) + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int s = __shfl_sync(0xffffffffu, v[k], 8 * j + (lane >> 2));
-        cp_async_16(to + 512 * (4 * k + j), from + static_cast<int64_t>(max(s, 0)) * kHeadDim, s >= 0 ? 16u : 0u);
-      }
-  }
+    }
 }
 
 // Cache rows of the 64-key halves of a dense request's chunks: looked up by
@@ -418,9 +410,10 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
   __syncwarp();
 }
 
-// Sparse: warp 0 (VALUES) copies the value boxes, warp 2 the others, and
-// prepares the scales. The slots of a lane's keys are read two chunks ahead and
-// their scales one. A chunk is posted once the next one's copies are under way.
+// Sparse: warp 0 (VALUES) copies the own value boxes and the rope columns,
+// warp 2 the other boxes, and prepares the scales. The slots of a lane's keys
+// are read a chunk ahead. A chunk is posted when its copies, issued an
+// iteration before, have landed.
 template <bool VALUES>
 __device__ void produce_sparse(const Ctx& x, const DecodeParams& p) {
   const int lane = x.lane;
@@ -435,23 +428,24 @@ __device__ void produce_sparse(const Ctx& x, const DecodeParams& p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sc[i] = v[i] >= 0 ? scale_of_slot(p, v[i]) : 1.f;
   };
-  auto post = [&](int g) {  // the copies are complete: make them visible to the MMAs
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kFull + g % kVChunks));
-  };
-  slots_of(0, slot);
-  if constexpr (!VALUES) scales_of(slot);
-  slots_of(1, next);
-  int g = 0;
-  for (; g < x.n_chunks; ++g) {
-    if (!slots_ready<VALUES>(x, g)) break;
-    copy_rows<VALUES>(x, p, g, slot);
-    cp_async_commit();
-    if (g > 0) {
-      cp_async_wait<1>();
-      post(g - 1);
+  slots_of(0, next);
+  for (int g = 0; g <= x.n_chunks; ++g) {
+    if (g > 0) {  // the copies of g - 1 are complete: make them visible to the MMAs
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.bar(kFull + (g - 1) % kVChunks));
     }
+    if (g == x.n_chunks) break;
+    // (after the fence, which waits for loads)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) slot[i] = next[i];
+    if constexpr (!VALUES) scales_of(slot);
+    slots_of(g + 1, next);
+    if (!slots_ready<VALUES>(x, g) || (VALUES && !slots_ready<false>(x, g))) break;
+    copy_rows<VALUES ? kOwn : kOther>(x, p, g, slot);
+    if constexpr (VALUES) copy_rows<kRope>(x, p, g, slot);
+    cp_async_commit();
     if constexpr (!VALUES) {
       uint32_t bits = 0u;
 #pragma unroll
@@ -461,13 +455,8 @@ __device__ void produce_sparse(const Ctx& x, const DecodeParams& p) {
       }
       if (!post_scales<false>(x, p, g, sc, bits)) break;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) slot[i] = next[i];
-    if constexpr (!VALUES) scales_of(slot);
-    slots_of(g + 2, next);
   }
   cp_async_wait<0>();  // also where a wait gave up: no copy outlives the CTA
-  if (g > 0 && g == x.n_chunks) post(g - 1);
   __syncwarp();
 }
 

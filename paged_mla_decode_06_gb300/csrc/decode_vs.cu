@@ -69,8 +69,8 @@ constexpr int kQStage = 2;               // q's latent boxes land in value slots
 constexpr int kSoftWarps = 16;           // warps 4-19: two groups (even and odd half-chunks) of four
                                          // TMEM lane quarters x two key quarters
 constexpr int kGroupWarps = 8;
-constexpr int kPart = 32;                // keys of a softmax warp; they share their scale where the
-                                         // groups are multiples of it
+constexpr int kPart = 32;                // keys of a softmax warp
+constexpr int kUni = 16;                 // keys that share their scale where the groups are multiples of it
 constexpr int kThreads = 32 * (4 + kSoftWarps);
 constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P of a half-chunk
 constexpr uint32_t kTmemCols = 512;
@@ -352,7 +352,7 @@ __device__ __forceinline__ float scale_of_slot(const DecodeParams& p, int s) {
 }
 
 // Posts the key scales of chunk c (part i of 32 keys: lane's key 32 i + lane;
-// UNI: lane i < 4 has the scale of part i) and the bits of the keys that exist,
+// UNI: lane i < 8 has the scale of the 16 keys from 16 i) and the bits of the keys that exist,
 // once the softmax has read those two chunks back. The half-chunks' S barriers
 // count the post as well as Q K^T.
 template <bool UNI>
@@ -365,8 +365,8 @@ __device__ __forceinline__ bool post_scales(const Ctx& x, const DecodeParams& p,
 #pragma unroll
   for (int i = 0; i < (UNI ? 1 : 4); ++i) {
     const KeyScale k = key_scale(sc[i], p.score_scale_log2);
-    const int at = UNI ? 32 * lane : 32 * i + lane;
-    if (!UNI || lane < 4) {
+    const int at = UNI ? kUni * lane : 32 * i + lane;
+    if (!UNI || lane < kKeys / kUni) {
       ks[at] = k.mul;
       ks[kKeys + at] = k.add;
       ks[2 * kKeys + at] = k.inv;
@@ -396,7 +396,7 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
     const int n = x.seg_end - (x.seg_start + g * kKeys);
 #pragma unroll
     for (int i = 0; i < (UNI ? 1 : 4); ++i) {
-      const int j = UNI ? 32 * lane : 32 * i + lane;
+      const int j = UNI ? kUni * lane : 32 * i + lane;
       sc[i] = j < n && j < kKeys ? scale_of_slot(p, (j < kHalf ? row0 : row1) + (j & (kHalf - 1))) : 1.f;
     }
   };
@@ -681,10 +681,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     const int sst = (g >> 1) & 1;                   // stage of the chunk's scales
     const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + sst * 3 * kKeys + kHalf * h + kPart * kh;
     const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * sst + 2 * h + kh];
-    KeyScale part{};
-    if constexpr (UNI) {
-      part = KeyScale{ks[0], ks[kKeys], ks[2 * kKeys]};
-    } else {
+    if constexpr (!UNI) {
 #pragma unroll
       for (int j = 0; j < kPart; j += 4) {
         const float4 mu = *reinterpret_cast<const float4*>(ks + j);
@@ -704,17 +701,15 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
       for (int j = 0; j < kPart; ++j)
         if (!(j < lim && ((kmask >> j) & 1u))) s[j] = -INFINITY;
     }
-    float m4[4];
+    float m[2];  // of either half of the keys
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m4[i] = max3(s[i], s[i + 4], s[i + 8]);
-#pragma unroll
-    for (int j = 12; j < kPart - 4; j += 8)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[j + i], s[j + 4 + i]);
-    static_assert((kPart - 12) % 8 == 4, "the last four scores");
-    float mine = max3(fmaxf(m4[0], s[kPart - 4]), max3(m4[1], s[kPart - 3], m4[2]),
-                      max3(s[kPart - 2], m4[3], s[kPart - 1]));
-    if constexpr (UNI) mine = fmaf(mine, part.mul, part.add);  // (mul > 0; -inf stays)
+    for (int i = 0; i < 2; ++i) {
+      const float* e = s + kUni * i;
+      m[i] = fmaxf(max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), max3(e[6], e[7], e[8])),
+                   max3(max3(e[9], e[10], e[11]), max3(e[12], e[13], e[14]), e[15]));
+      if constexpr (UNI) m[i] = fmaf(m[i], ks[kUni * i], ks[kKeys + kUni * i]);  // (mul > 0; -inf stays)
+    }
+    const float mine = fmaxf(m[0], m[1]);
     // the row's maximum over both key quarters; the previous half-chunk's before it
     ok = g == 0 || follow_other(g - 1);
     if (!ok) break;
@@ -727,13 +722,15 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     const float alpha = follow(fmaxf(mine, xm[(kh ^ 1) * kRows]));
     // p as hi + lo e4m3 terms, 16 keys to a 16-byte chunk of each tile
     const float base = ref == -INFINITY ? 0.f : ref - kPBias;
-    const float sh = UNI ? part.add - base : -base;
-    const float2 mul2 = make_float2(part.mul, part.mul), shift2 = make_float2(sh, sh);
-    float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float psum = 0.f;
     uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      {
+    for (int i = 0; i < 2; ++i) {
+      const float mu = UNI ? ks[kUni * i] : 1.f, sh = UNI ? ks[kKeys + kUni * i] - base : -base;
+      const float2 mul2 = make_float2(mu, mu), shift2 = make_float2(sh, sh);
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int j = 4 * i; j < 4 * i + 4; ++j) {
         const int e = 4 * j;
         float2 a = make_float2(s[e], s[e + 1]), b = make_float2(s[e + 2], s[e + 3]);
         a = UNI ? fma2(a, mul2, shift2) : add2(a, shift2);
@@ -750,9 +747,10 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
         }
         p_terms4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
       }
+      const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+      psum = UNI ? fmaf(sum, ks[2 * kKeys + kUni * i], psum) : psum + sum;
     }
-    const float psum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-    l = UNI ? fmaf(psum, part.inv, l) : l + psum;
+    l += psum;
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kScFree + sst));
     // P V two half-chunks back has read this buffer of P
@@ -1116,9 +1114,10 @@ cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_r
                            static_cast<uint64_t>(p.num_segments), false, 32, 32, true);
   if (e != cudaSuccess) return e;
   if (sparse) return launch_variant<true, false>(maps, p, grid, status, stream);
-  // groups of a multiple of 32 slots: the 32 keys of a softmax warp (32-aligned
-  // positions of one block) share their scale
-  return p.scale_group % kPart == 0 ? launch_variant<false, true>(maps, p, grid, status, stream)
+  // groups of a multiple of 16 slots: 16 keys from a 16-aligned position (of one
+  // block) share their scale, and a softmax thread reads two for its 32 keys
+  // instead of 32 (MEAS)
+  return p.scale_group % kUni == 0 ? launch_variant<false, true>(maps, p, grid, status, stream)
                                     : launch_variant<false, false>(maps, p, grid, status, stream);
 }
 

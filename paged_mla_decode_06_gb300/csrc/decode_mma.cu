@@ -60,14 +60,16 @@ struct Cfg {
   static constexpr int kComputeBytes = FP8 ? kKC * kQStride * 2 : 0;
   static constexpr int kPBytes = kRows * kPStride * 2;
   static constexpr int kRedBytes = RG * kCS * 16 * 4;
-  static constexpr int kOkBytes = kStages * kKC * 4;
+  static constexpr int kSlotStages = kStages + 1;    // slots are looked up a chunk before its copies
+  static constexpr int kSlotBytes = kSlotStages * kKC * 8;
+  static_assert(kStages * kKC <= kThreads, "a thread looks up one key ahead of the loop");
   static constexpr int kOffStage = kQBytes;
   static constexpr int kOffCompute = kOffStage + kStages * kStageBytes;
   static constexpr int kOffP = kOffCompute + kComputeBytes;
   static constexpr int kOffRed = kOffP + kPBytes;
-  static constexpr int kOffOk = kOffRed + kRedBytes;
-  static constexpr int kOffScale = kOffOk + kOkBytes;  // GS: the scale of each ring key
-  static constexpr int kSmem = kOffScale + (GS ? kOkBytes : 0);
+  static constexpr int kOffSlot = kOffRed + kRedBytes;
+  static constexpr int kOffScale = kOffSlot + kSlotBytes;  // GS: the scale of each ring key
+  static constexpr int kSmem = kOffScale + (GS ? kStages * kKC * 4 : 0);
   static_assert(kNTS >= 1 && kKW % 8 == 0, "key slice per warp must be whole n-tiles");
   static_assert(kNTV % 2 == 0, "value slice must be an even number of n-tiles");
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
   uint8_t* sQ = smem;
   uint8_t* sP = smem + C::kOffP;
   float* red = reinterpret_cast<float*>(smem + C::kOffRed);
-  int* key_ok = reinterpret_cast<int*>(smem + C::kOffOk);
+  int64_t* key_slot = reinterpret_cast<int64_t*>(smem + C::kOffSlot);  // -1: no key
   float* key_sc = reinterpret_cast<float*>(smem + C::kOffScale);
 
   // Rows of this thread: r_a = rg*16 + lane/4 and r_a + 8 (within the tile).
@@ -134,7 +136,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
     vis[i] = (rho >= rows_total) ? 0 : (sparse ? INT_MAX : part_len - qlen + j + 1);
   }
 
-  // ---------------------------------------------------------------- Q
+  // ---------------------------------------------------------------- KV gather
+  const uint8_t* kvbytes = static_cast<const uint8_t*>(p.kv);
+  const int64_t row_bytes = FP8 ? kHeadDim : kHeadDim * 2;
+  const int bs = p.block_size;
+  // The cache slot of key k of chunk c, by one thread, a chunk before the copies
+  // that need it: a copy that looked its own up waited for the block table each
+  // time (2 requests x 37 to 130 keys, 16 heads: MEAS).
+  auto find_slot = [&](int c, int k) -> int64_t {
+    const int pos = seg_start + c * C::kKC + k;
+    if (c >= n_chunks || pos >= seg_end) return -1;
+    if (sparse) return p.slots[list_base + pos];
+    const int blk = pos / bs;
+    return static_cast<int64_t>(bt_row[blk]) * bs + (pos - blk * bs);
+  };
+  auto load_chunk = [&](int c, int stage) {
+    const int64_t* slots = key_slot + c % C::kSlotStages * C::kKC;
+    uint8_t* dst = smem + C::kOffStage + stage * C::kStageBytes;
+    constexpr int kRowStrideB = FP8 ? kRawStride : kQStride * 2;
+#pragma unroll 3
+    for (int i = tid; i < C::kKC * C::kPieces; i += kThreads) {
+      const int k = i / C::kPieces, part = i % C::kPieces;
+      const int64_t slot = slots[k];
+      const bool live = slot >= 0;
+      cp_async_16(smem_u32(dst + k * kRowStrideB + part * 16),
+                  live ? kvbytes + slot * row_bytes + part * 16 : kvbytes, live ? 16u : 0u);
+      if constexpr (GS)
+        if (part == 1)
+          cp_async_4(smem_u32(key_sc + stage * C::kKC + k),
+                     live ? p.kv_scales + static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.scale_group)
+                          : p.kv_scales,
+                     live ? 4u : 0u);
+    }
+  };
+
+  if (tid < C::kStages * C::kKC) key_slot[tid] = find_slot(tid / C::kKC, tid % C::kKC);
+  __syncthreads();
+  // Q: bf16 with the first chunk's copies, e4m3 widened while the first chunks arrive
   const uint8_t* qbytes = static_cast<const uint8_t*>(p.q);
   if constexpr (!FP8) {
     for (int i = tid; i < C::kRows * 72; i += kThreads) {
@@ -145,8 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       cp_async_16(smem_u32(sQ + r * kQStride * 2 + part * 16), qbytes + qrow * kHeadDim * 2 + part * 16,
                   ok ? 16u : 0u);
     }
+  }
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) {
+    if (s < n_chunks) load_chunk(s, s);
     cp_async_commit();
-  } else {
+  }
+  if constexpr (FP8) {
     for (int i = tid; i < C::kRows * 36; i += kThreads) {
       const int r = i / 36, part = i % 36;
       const int rho = row0 + r;
@@ -168,46 +211,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
     }
   }
 
-  // ---------------------------------------------------------------- KV gather
-  const uint8_t* kvbytes = static_cast<const uint8_t*>(p.kv);
-  const int64_t row_bytes = FP8 ? kHeadDim : kHeadDim * 2;
-  const int bs = p.block_size;
-  auto load_chunk = [&](int c, int stage) {
-    const int c0 = seg_start + c * C::kKC;
-    uint8_t* dst = smem + C::kOffStage + stage * C::kStageBytes;
-    int* ok = key_ok + stage * C::kKC;
-    constexpr int kRowStrideB = FP8 ? kRawStride : kQStride * 2;
-    for (int i = tid; i < C::kKC * C::kPieces; i += kThreads) {
-      const int k = i / C::kPieces, part = i % C::kPieces;
-      const int pos = c0 + k;
-      int64_t slot = -1;
-      if (pos < seg_end) {
-        if (!sparse) {
-          const int blk = pos / bs;
-          slot = static_cast<int64_t>(bt_row[blk]) * bs + (pos - blk * bs);
-        } else {
-          slot = p.slots[list_base + pos];
-        }
-      }
-      const bool live = slot >= 0;
-      cp_async_16(smem_u32(dst + k * kRowStrideB + part * 16),
-                  live ? kvbytes + slot * row_bytes + part * 16 : kvbytes, live ? 16u : 0u);
-      if (part == 0) ok[k] = live ? 1 : 0;
-      if constexpr (GS)
-        if (part == 1)
-          cp_async_4(smem_u32(key_sc + stage * C::kKC + k),
-                     live ? p.kv_scales + static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.scale_group)
-                          : p.kv_scales,
-                     live ? 4u : 0u);
-    }
-  };
-
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) {
-    if (s < n_chunks) load_chunk(s, s);
-    cp_async_commit();
-  }
-
   float o[C::kNTV][4];
 #pragma unroll
   for (int n = 0; n < C::kNTV; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
@@ -227,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       if (nc < n_chunks) load_chunk(nc, nc % C::kStages);
       cp_async_commit();
     }
+    int64_t ahead = -1;  // of the chunk that the next iteration copies
+    if (tid < C::kKC) ahead = find_slot(c + C::kStages, tid);
     const uint8_t* kvs;
     if constexpr (FP8) {
       const uint8_t* raw = smem + C::kOffStage + stage * C::kStageBytes;
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       kvs = smem + C::kOffStage + stage * C::kStageBytes;
     }
     const uint32_t kv_u32 = smem_u32(kvs);
-    const int* ok = key_ok + stage * C::kKC;
+    const int64_t* slots = key_slot + c % C::kSlotStages * C::kKC;
 
     // ---- S = Q K^T for rows of group rg, keys [cs*KW, cs*KW + KW)
     float sacc[C::kNTS][4];
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       for (int e = 0; e < 2; ++e) {
         const int kl = cs * C::kKW + n * 8 + 2 * (lane & 3) + e;
         const int pos = c0 + kl;
-        const bool live = ok[kl] != 0;
+        const bool live = slots[kl] >= 0;
         float f0 = sacc[n][e] * scale2, f1 = sacc[n][2 + e] * scale2;
         if constexpr (GS) {
           const KeyScale ks = key_scale(live ? key_sc[stage * C::kKC + kl] : 1.f, scale2);
@@ -347,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       o[n][2] *= alpha[1];
       o[n][3] *= alpha[1];
     }
+    if (tid < C::kKC) key_slot[(c + C::kStages) % C::kSlotStages * C::kKC + tid] = ahead;
     __syncthreads();
 
     // ---- O += P V for value columns [cs*VW, cs*VW + VW)

@@ -449,7 +449,10 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * Everything else is mla_decode_fwd's: dense requests of one or more tokens,
  * sparse slot lists, sinks, the balanced schedule or a fixed num_segments,
  * the workspace and its status word. The plan is one for kv_dtype =
- * MLA_DTYPE_FP8_E4M3 (mla_decode_plan chooses among the same kernels).
+ * MLA_DTYPE_FP8_E4M3. Row tiles of more than 64 rows that it gives to a
+ * tensor-core kernel, and sparse lists, run on a kernel of their own here, in
+ * the same workspace; where the planner chose the number of segments of a
+ * sparse call, that kernel may use fewer. A sink of -inf counts as none.
  *   kv_scales    [num_blocks * block_size / scale_group] fp32. The scales of
  *                groups that hold visible keys must lie in [2^-60, 2^60]
  *                (mla_cache_append writes such); others are not used.

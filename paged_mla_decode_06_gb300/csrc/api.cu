@@ -135,7 +135,7 @@ bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
 int32_t segments_of(const mla_plan_t* plan, const float* kv_scales) {
   const mla_problem_t& p = plan->prob;
   if (p.num_segments != 0 || p.topk == 0 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
-  const int64_t ctas = 2 * static_cast<int64_t>(p.num_tokens) * ((p.num_heads + 127) / 128);
+  const int64_t ctas = 2 * static_cast<int64_t>(p.num_tokens);  // (a token's heads are one row tile)
   const int64_t fit = ctas > 0 ? plan->num_sms / ctas : 1;
   return static_cast<int32_t>(fit < 1 ? 1 : fit < plan->num_segments ? fit : plan->num_segments);
 }
@@ -284,7 +284,7 @@ mla::SchedParams sched_params(const mla_plan_t* plan, const Inputs& in, uint8_t*
   sp.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
   sp.workers = plan_workers(plan);
   // workers run contiguous runs of items (the value-split kernel takes one
-  // item a cluster, longest first, also under a rows-as-N plan)
+  // item a pair of CTAs, longest first, also under a rows-as-N plan)
   if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales))
     sp.worker_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
   return sp;

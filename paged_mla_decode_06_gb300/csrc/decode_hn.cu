@@ -772,9 +772,11 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
               const float s2 = p.sinks[head] * kLog2e;
               const float M = fmaxf(L > 0.f ? base : -INFINITY, s2);
               const float e = L > 0.f ? exp2f(base - M) : 0.f;
-              const float W = L * e + exp2f(s2 - M);
-              f = e / W;
-              lse = kLn2 * (M + log2f(W));
+              const float W = L * e + (s2 > -INFINITY ? exp2f(s2 - M) : 0.f);  // (-inf: no sink)
+              if (W > 0.f) {
+                f = e / W;
+                lse = kLn2 * (M + log2f(W));
+              }
             } else if (L > 0.f) {
               f = 1.f / L;
               lse = kLn2 * (base + log2f(L));
@@ -1058,15 +1060,14 @@ cudaError_t launch_rows(const HnMaps& maps, const DecodeParams& p, dim3 grid, in
   return cudaLaunchKernelEx(&cfg, decode_hn_kernel<NR, CL, GS>, maps, p, status);
 }
 
-template <int NR, int CL>
-cudaError_t launch_scaled(const HnMaps& maps, const DecodeParams& p, dim3 grid, int* status,
+// (group scales: up to 64 rows, on one CTA)
+template <int NR>
+cudaError_t launch_single(const HnMaps& maps, const DecodeParams& p, dim3 grid, int* status,
                           cudaStream_t stream) {
-  return p.kv_scales != nullptr ? launch_rows<NR, CL, true>(maps, p, grid, status, stream)
-                                : launch_rows<NR, CL, false>(maps, p, grid, status, stream);
+  return p.kv_scales != nullptr ? launch_rows<NR, 1, true>(maps, p, grid, status, stream)
+                                : launch_rows<NR, 1, false>(maps, p, grid, status, stream);
 }
 
-// (the group-scaled variant has the same threads, shared memory and cluster,
-// and registers for one CTA per SM either way)
 template <int NR>
 cudaError_t max_pairs(int* n) {
   int smem = 0;
@@ -1111,17 +1112,17 @@ cudaError_t launch_decode_hn(const DecodeParams& p, int rows, int cluster, int64
   }
   if (cluster == 1) {
     switch (rows) {
-      case 16: return launch_scaled<16, 1>(maps, p, grid, status, stream);
-      case 32: return launch_scaled<32, 1>(maps, p, grid, status, stream);
-      case 48: return launch_scaled<48, 1>(maps, p, grid, status, stream);
-      case 64: return launch_scaled<64, 1>(maps, p, grid, status, stream);
+      case 16: return launch_single<16>(maps, p, grid, status, stream);
+      case 32: return launch_single<32>(maps, p, grid, status, stream);
+      case 48: return launch_single<48>(maps, p, grid, status, stream);
+      case 64: return launch_single<64>(maps, p, grid, status, stream);
       default: return cudaErrorInvalidValue;
     }
   }
-  if (cluster == 2) {
+  if (cluster == 2 && p.kv_scales == nullptr) {
     switch (rows) {
-      case 48: return launch_scaled<48, 2>(maps, p, grid, status, stream);
-      case 64: return launch_scaled<64, 2>(maps, p, grid, status, stream);
+      case 48: return launch_rows<48, 2, false>(maps, p, grid, status, stream);
+      case 64: return launch_rows<64, 2, false>(maps, p, grid, status, stream);
       default: return cudaErrorInvalidValue;
     }
   }

@@ -6,44 +6,50 @@
 // memory, so a row tile takes two SMs. Here each CTA owns all 128 rows and 256
 // of the value columns; both compute all scores and the same softmax. That
 // doubles Q K^T, but nothing crosses between the SMs (probabilities would:
-// distributed shared memory moves about 20 bytes a clock), a row's softmax is
-// in four threads that exchange one maximum, and the epilogue is halved. Per
-// chunk of 128 keys a CTA issues
+// distributed shared memory moves about 20 bytes a clock) and the epilogue is
+// halved. Per chunk of 128 keys a CTA issues
 //   S[rows, keys]  = Q K^T   M = 128 rows, N = 128 keys, K = 576: A = q from
 //                            TMEM (512 latent dims) and shared memory (64 rope
 //                            dims), B = the key rows of the rings, K-major:
-//                            18 kind::f8f6f4 instructions of 64 cycles;
-//   O[rows, 256]  += P V     M = 128 rows, N = 256 columns, K = 128 keys, P as
-//                            two e4m3 terms (hi, lo), V = the same key rows
-//                            read MN-major: 8 instructions of 128 cycles.
-// That is 2176 tensor cycles a chunk, close to what the shared memory's 128
+//                            18 kind::f8f6f4 instructions of 64.5 cycles;
+//   O[rows, 256]  += P V     for each half of 64 keys: M = 128 rows, N = 256
+//                            columns, K = 64, P as two e4m3 terms (hi, lo), V =
+//                            the same key rows read MN-major: 8 instructions a
+//                            chunk of 128 cycles.
+// That is 2180 tensor cycles a chunk, close to what the shared memory's 128
 // bytes a clock allow for the operands, the copies in and P (284 KB, 2220
-// cycles). The softmax runs beside them: S is read into registers at once, so
-// that the next chunk's Q K^T can overwrite it while its weights are formed,
-// and one buffer of S and one of P are enough.
+// cycles). Measured: 3100 to 3400 (52 x 16384 keys, 128 heads), bound by the
+// chain S -> maxima -> weights -> P of a half-chunk (2600 cycles) and its
+// hand-overs; at 1.7 GHz, as the SMs clock under this load, 180 us.
+//
+// The softmax works on half-chunks of 64 keys: one group of eight warps takes
+// the even ones, another the odd ones, so that each has two of them in
+// flight. A warp reads its 32 rows x 32 keys of S into registers and frees
+// them at once: the next chunk's Q K^T runs while the weights are formed, and
+// one buffer of S is enough. P has one for each half. (Groups on
+// alternate whole chunks, with two buffers of S: 191 us against 183.)
 //
 // Rings: the two latent boxes of the own value columns stay until P V, the
 // other two and the rope box only until Q K^T. They have rings of their own, of
 // three, two and two chunks: what limits the loop is a box's lifetime (load,
 // Q K^T, softmax, P V: about 8000 cycles for a value box), and in one ring of
-// ten slots the short-lived boxes would wait behind the long-lived ones
-// (4470 cycles a chunk, measured). The two CTAs of a tile read each key row
-// once from memory between them: the later one finds it in L2. Multicasting
-// each box to both, from one read of L2, ties each slot to the slower CTA and
-// measured 5930 cycles a chunk against 4730 (one ring).
+// ten slots the short-lived boxes would wait behind the long-lived ones. The
+// two CTAs of a tile read each key row once from memory between them: the later
+// one finds it in L2. (Multicasting each box to both, from one read of L2, ties
+// each slot to the slower CTA: 5930 cycles a chunk against 4730 without, when
+// both had one ring.)
 //
 // Weights: with group scales the thread's scores become t = score + log2 s and
 // the weights 2^(t - m) multiply the codes (KeyScale). They are formed as
-// p = 2^(t - m_ref + 4) with a reference that moves only when a chunk maximum
-// exceeds it by more than 4 (O is then rescaled in TMEM), so p <= 2^8 fits
-// e4m3 and hi + lo carry 8 bits of it.
+// p = 2^(t - m_ref + 4) with a reference that moves only when a half-chunk's
+// maximum exceeds it by more than 4.75 (O is then rescaled in TMEM), so p <=
+// 2^8.75 fits e4m3 and hi + lo carry 8 bits of it.
 //
-// Warps: 0 and 20-22 load (sparse: gather), 1 issues Q K^T, 2 prepares the
-// keys' scales, 3 issues P V, 4-19 softmax and epilogue (a TMEM lane quarter
-// of the rows and a quarter of the chunk's keys each: four warps to a
-// scheduler hide each other's latencies). Every wait is bounded: a timeout
-// records a code in the status word, stops the CTA's work, drains what was
-// issued and exits.
+// Warps: 0 loads, 1 issues Q K^T, 2 prepares the keys' scales (sparse lists: 0
+// and 2 share the copies), 3 issues P V, 4-19 softmax and epilogue (of either
+// group: a TMEM lane quarter of the rows and half of the half-chunk's keys
+// each). Every wait is bounded: a timeout records a code in the status word,
+// stops the CTA's work, drains what was issued and exits.
 #include <atomic>
 #include <climits>
 
@@ -58,8 +64,8 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;               // query rows of a tile: M
-constexpr int kKeys = 128;               // keys per chunk: N of Q K^T, K of P V
-constexpr int kHalf = 64;                // keys per TMA box, and per softmax warp
+constexpr int kKeys = 128;               // keys per chunk: N of Q K^T
+constexpr int kHalf = 64;                // keys per half-chunk: of a TMA box, K of P V
 constexpr int kSlot = kKeys * 128;       // ring slot: a 128-byte column box of a chunk (or of q)
 constexpr int kRSlot = kKeys * 64;       // rope ring slot
 constexpr int kKChunks = 2;              // ring of the other CTA's value columns (two boxes) and the
@@ -75,7 +81,7 @@ constexpr int kThreads = 32 * (4 + kSoftWarps);
 constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P of a half-chunk
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;           // 256 columns
-constexpr uint32_t kTmemS = 256;         // 2 x 64
+constexpr uint32_t kTmemS = 256;         // 128: S of a chunk
 constexpr uint32_t kTmemQ = 384;         // 128: 512 latent dims, four to a column
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
@@ -188,13 +194,13 @@ __device__ __forceinline__ void report(int* status, int code) {
 
 // Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or abort.
 __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t nap = x.limit_ns < kSleepNs ? static_cast<uint32_t>(x.limit_ns) : kSleepNs;
+  const bool brief = x.limit_ns < kSleepNs;  // (a sleep may last longer than the limit: poll)
+  if (brief ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
   // one sleep before the clock is read for the first time: nearly every wait
   // ends in it, and reading the global timer takes longer than most waits
-  if (mbar_try_wait_sleep(bar, parity, nap)) return true;
+  if (!brief && mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, nap)) {
+  while (!(brief ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepNs))) {
     if (*x.abort) return false;
     if (global_timer_ns() - t0 > x.limit_ns) {
       report(x.status, code);
@@ -677,7 +683,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     }
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kSFree + h));  // Q K^T two half-chunks on may overwrite S
+    if (lane == 0) mbar_arrive(x.bar(kSFree + h));  // the next chunk's Q K^T may overwrite it
     const int sst = (g >> 1) & 1;                   // stage of the chunk's scales
     const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + sst * 3 * kKeys + kHalf * h + kPart * kh;
     const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * sst + 2 * h + kh];
@@ -829,9 +835,11 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
         const float s2 = p.sinks[head] * kLog2e;
         const float M = fmaxf(L > 0.f ? base : -INFINITY, s2);
         const float e = L > 0.f ? exp2f(base - M) : 0.f;
-        const float W = L * e + exp2f(s2 - M);
-        mult = e / W;
-        lse = kLn2 * (M + log2f(W));
+        const float W = L * e + (s2 > -INFINITY ? exp2f(s2 - M) : 0.f);  // (-inf: no sink)
+        if (W > 0.f) {
+          mult = e / W;
+          lse = kLn2 * (M + log2f(W));
+        }
       } else if (L > 0.f) {
         mult = 1.f / L;
         lse = kLn2 * (base + log2f(L));

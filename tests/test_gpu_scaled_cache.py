@@ -415,10 +415,22 @@ def test_decode_zero_groups():
         check_decode(c)
 
 
-def test_decode_sinks_of_minus_infinity_and_large():
+def test_decode_sinks_large_and_small():
     c = decode_case(12, [0, 40, 300], 16, 64, 64, sinks=True)
     c["sinks"][:4] = [60.0, -60.0, 0.0, 12.0]
     check_decode(c)
+
+
+def test_decode_a_sink_of_minus_infinity_is_none():
+    """Also for rows without keys: the bits of the call without sinks."""
+    for heads, bs, q, lens in ((16, 64, None, [0, 40, 300]), (128, 64, None, [0, 40, 6000]), (128, 64, [2, 3, 1], [0, 40, 300]),
+                               (16, 16, None, [0, 40, 300])):
+        c = decode_case(15, lens, heads, bs, 16, qlens=q, sinks=True)
+        c["sinks"][:] = -np.inf
+        a = run_decode(c)
+        c["sinks"] = None
+        b = run_decode(c)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
 def test_decode_split_rows_and_stages():
@@ -608,3 +620,98 @@ def test_cache_beyond_32_bit_offsets():
         lists = S.token_slots(np.arange(4)[None], [n], bs, [0, q])
         compare(out.double().cpu().numpy(), lse.double().cpu().numpy(),
                 *S.decode(qc, QS, small_c, small_s, g, lists, SCALE, bounds=True))
+
+
+@pytest.mark.parametrize("heads,g", [(1, 64), (128, 1), (100, 16)])
+def test_decode_sparse_ragged_lists(heads, g):
+    """Slot lists of their own lengths, with holes, a slot listed twice and a
+    list without slots."""
+    rng = np.random.default_rng(heads)
+    bs, nb = 64, 24
+    codes, scales = filled(rng, nb * bs, g)
+    lists = []
+    for n in (0, 1, 2, 127, 128, 129, 500, 512):
+        s = rng.choice(nb * bs, n, replace=False)
+        s[rng.random(n) < 0.1] = -1
+        if n > 2:
+            s[-1] = s[0] = 5
+        lists.append(s)
+    lists.append(np.full(40, -1))
+    T, topk = len(lists), 512
+    indptr = np.concatenate([[0], np.cumsum([len(s) for s in lists])])
+    qc = I.float32_to_e4m3_codes(rng.standard_normal((T, heads, 576)).astype(np.float32) / QS)
+    for ns in (0, 1, 4):
+        plan = B.mla_decode_plan(B.make_problem(num_tokens=T, num_heads=heads, block_size=bs, num_blocks=nb, num_reqs=0,
+                                                max_blocks_per_req=0, max_seq_len=0, topk=topk, dtype="fp8", num_segments=ns))
+        ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty((T, heads, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((T, heads), device="cuda")
+        B.mla_decode_fwd_scaled(plan, dev(qc), dev(codes).view(nb, bs, 576), dev(scales, np.float32), scale_group=g,
+                                sparse_slots=dev(np.concatenate(lists), np.int32), sparse_indptr=dev(indptr, np.int32),
+                                softmax_scale=SCALE, q_scale=QS, workspace=ws, out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert B.mla_workspace_status(plan, ws) == 0
+        compare(out.double().cpu().numpy(), lse.double().cpu().numpy(),
+                *S.decode(qc, QS, codes, scales, g, lists, SCALE, bounds=True))
+
+
+def test_sparse_beyond_32_bit_offsets():
+    bs, g, heads, topk = 64, 1, 128, 256
+    nb = (1 << 32) // (576 * bs) + 40
+    rng = np.random.default_rng(32)
+    rows = np.concatenate([rng.choice(nb * bs, 100, replace=False), np.arange(nb * bs - 100, nb * bs)])
+    codes, scales = filled(rng, len(rows), g)
+    cache = torch.zeros((nb, bs, 576), dtype=torch.uint8, device="cuda")
+    sc = torch.full((nb * bs,), float("nan"), device="cuda")
+    cache.view(-1, 576)[dev(rows, np.int64)] = dev(codes)
+    sc[dev(rows, np.int64)] = dev(scales, np.float32)
+    slots = np.full((1, topk), -1)
+    slots[0, 30:230] = rows
+    lists = [np.where(slots[0] >= 0, np.arange(topk) - 30, -1)]
+    qc = I.float32_to_e4m3_codes(rng.standard_normal((1, heads, 576)).astype(np.float32) / QS)
+    plan = B.mla_decode_plan(B.make_problem(num_tokens=1, num_heads=heads, block_size=bs, num_blocks=nb, num_reqs=0,
+                                            max_blocks_per_req=0, max_seq_len=0, topk=topk, dtype="fp8"))
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((1, heads, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((1, heads), device="cuda")
+    B.mla_decode_fwd_scaled(plan, dev(qc), cache, sc, scale_group=g, sparse_slots=dev(slots, np.int32), softmax_scale=SCALE,
+                            q_scale=QS, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    compare(out.double().cpu().numpy(), lse.double().cpu().numpy(),
+            *S.decode(qc, QS, codes, scales, g, lists, SCALE, bounds=True))
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its workspace: the bits of
+    the calls made alone."""
+    cases = [decode_case(41, [3000, 70, 900], 128, 64, 16), decode_case(42, [2000, 1, 640], 16, 64, 64)]
+    alone = [run_decode(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _, _, (args, kw, _) in alone:
+        kw["out"].fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, (_, _, (args, kw, _)) in zip(streams, alone):
+            B.mla_decode_fwd_scaled(*args, **kw, stream=s)
+    torch.cuda.synchronize()
+    for out, lse, (_, kw, _) in alone:
+        assert np.array_equal(out, kw["out"].double().cpu().numpy())
+        assert np.array_equal(lse, kw["lse"].double().cpu().numpy())
+
+
+@pytest.mark.parametrize("heads,qlens,topk", [(128, None, 0), (128, [3, 2], 0), (128, None, 512), (16, None, 0)])
+def test_bounded_wait_runs_out_and_is_reported(heads, qlens, topk):
+    """With a limit of a microsecond the kernel's waits give up: it drains what
+    it issued, exits and leaves a code; the next call is right."""
+    c = decode_case(43, [2000, 900], heads, 64, 16, qlens=qlens, topk=topk)
+    _, _, (args, kw, plan) = check_decode(c)
+    plan.wait_limit_us = 1
+    B.mla_decode_fwd_scaled(*args, **kw)
+    torch.cuda.synchronize()
+    code = B.mla_workspace_status(plan, kw["workspace"], clear=True)
+    assert code != 0
+    plan.wait_limit_us = 0
+    B.mla_decode_fwd_scaled(*args, **kw)
+    torch.cuda.synchronize()
+    assert B.mla_workspace_status(plan, kw["workspace"]) == 0
+    lists = list(c["slots"]) if topk else S.token_slots(c["table"], c["lens"], c["bs"], c["qo"])
+    compare(kw["out"].double().cpu().numpy(), kw["lse"].double().cpu().numpy(),
+            *S.decode(c["q"], QS, c["codes"], c["scales"], c["g"], lists, SCALE, c["sinks"], bounds=True))

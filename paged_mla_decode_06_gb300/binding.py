@@ -374,12 +374,11 @@ def _refuse(fn: str, device: int, tensors, rules):
     need(False, "bad arguments")
 
 
-def _dense_rows(t, min_cols: int) -> bool:
-    """``t`` is a matrix of rows that are dense and do not overlap."""
-    rows, cols = t.shape
-    row_stride, col_stride = t.stride()
-    return cols >= min_cols and (rows == 0 or ((col_stride == 1 or cols == 1)
-                                               and (rows == 1 or row_stride >= cols)))
+def _dense_rows(shape, strides, min_cols: int) -> bool:
+    """A matrix's rows are dense and do not overlap."""
+    rows, cols = shape
+    return cols >= min_cols and (rows == 0 or ((strides[1] == 1 or cols == 1)
+                                               and (rows == 1 or strides[0] >= cols)))
 
 
 def _scaled_args(fn: str, plan: Plan, q, kv_cache, kv_scales, scale_group, block_table,
@@ -417,7 +416,8 @@ def _scaled_args(fn: str, plan: Plan, q, kv_cache, kv_scales, scale_group, block
                                            and qo_indptr.numel() == R + 1 and qo_indptr.is_contiguous()))
         ok = ok and (block_table is None
                      or (block_table.dtype is i32 and block_table.get_device() == dev and block_table.dim() == 2
-                         and block_table.size(0) == R and _dense_rows(block_table, pr.max_blocks_per_req)))
+                         and block_table.shape[0] == R
+                         and _dense_rows(block_table.shape, block_table.stride(), pr.max_blocks_per_req)))
     if not ok:
         if pr.kv_dtype != MLA_DTYPE_FP8_E4M3:
             raise MLAError(fn, MLA_ERR_UNSUPPORTED, "the plan's cache is not e4m3")
@@ -485,23 +485,31 @@ def mla_block_tables(query_start_loc, seq_lens, free_blocks, block_table, *, blo
     the step takes."""
     lib = _lib or load_library()
     torch = _torch or _load_torch()
-    fn = "mla_block_tables"
     i32 = torch.int32
     dev = query_start_loc.get_device()
-    R, T = seq_lens.numel(), slot_mapping.numel()
-    if not (dev >= 0 and dev == torch._C._cuda_getDevice()
-            and query_start_loc.dtype is i32 and query_start_loc.numel() == R + 1 and query_start_loc.is_contiguous()
-            and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous()
-            and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
-            and taken.dtype is i32 and taken.get_device() == dev and taken.numel() == 1
-            and (free_blocks is None or (free_blocks.dtype is i32 and free_blocks.get_device() == dev
-                                         and free_blocks.is_contiguous()))
-            and (req_id is None or (req_id.dtype is i32 and req_id.get_device() == dev
-                                    and req_id.numel() == T and req_id.is_contiguous()))
-            and (positions is None or (positions.dtype is i32 and positions.get_device() == dev
-                                       and positions.numel() == T and positions.is_contiguous()))
-            and block_table.dtype is i32 and block_table.get_device() == dev and block_table.dim() == 2
-            and block_table.size(0) == R and _dense_rows(block_table, 1)):
+    R, T, shape = seq_lens.numel(), slot_mapping.numel(), block_table.shape
+    ok = (dev >= 0 and dev == torch._C._cuda_getDevice()
+          and query_start_loc.dtype is i32 and query_start_loc.numel() == R + 1 and query_start_loc.is_contiguous()
+          and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous()
+          and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
+          and taken.dtype is i32 and taken.get_device() == dev and taken.numel() == 1
+          and block_table.dtype is i32 and block_table.get_device() == dev and len(shape) == 2 and shape[0] == R
+          and _dense_rows(shape, block_table.stride(), 1))
+    free = reqs = pos = None
+    num_free = 0
+    if free_blocks is not None:
+        ok = ok and free_blocks.dtype is i32 and free_blocks.get_device() == dev and free_blocks.is_contiguous()
+        free, num_free = free_blocks.data_ptr(), free_blocks.numel()
+    if req_id is not None:
+        ok = (ok and req_id.dtype is i32 and req_id.get_device() == dev and req_id.numel() == T
+              and req_id.is_contiguous())
+        reqs = req_id.data_ptr()
+    if positions is not None:
+        ok = (ok and positions.dtype is i32 and positions.get_device() == dev and positions.numel() == T
+              and positions.is_contiguous())
+        pos = positions.data_ptr()
+    if not ok:
+        fn = "mla_block_tables"
         named = [("query_start_loc", query_start_loc), ("seq_lens", seq_lens), ("slot_mapping", slot_mapping),
                  ("free_blocks", free_blocks), ("req_id", req_id), ("positions", positions)]
         _refuse(fn, dev, [(n, t, (i32,)) for n, t in named + [("taken", taken), ("block_table", block_table)]],
@@ -511,12 +519,13 @@ def mla_block_tables(query_start_loc, seq_lens, free_blocks, block_table, *, blo
                  (req_id is None or req_id.numel() == T, "req_id must be [num_tokens]"),
                  (positions is None or positions.numel() == T, "positions must be [num_tokens]"),
                  (False, "block_table must be [num_reqs, columns] with dense rows that do not overlap")])
-    cols = block_table.size(1)
-    _check(fn, lib.mla_block_tables(
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, block_size, _ptr(free_blocks),
-        0 if free_blocks is None else free_blocks.numel(), block_table.data_ptr(),
-        block_table.stride(0) if R > 1 else cols, cols, slot_mapping.data_ptr(), _ptr(req_id), _ptr(positions),
-        taken.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
+    cols = shape[1]
+    status = lib.mla_block_tables(
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), R, T, block_size, free, num_free, block_table.data_ptr(),
+        block_table.stride()[0] if R > 1 else cols, cols, slot_mapping.data_ptr(), reqs, pos, taken.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check("mla_block_tables", status)
 
 
 def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_group: int,
@@ -525,21 +534,22 @@ def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_gro
     ``slot_mapping``, as e4m3 codes under their groups' scales."""
     lib = _lib or load_library()
     torch = _torch or _load_torch()
-    fn = "mla_cache_append"
-    i32, f32, b16, codes = torch.int32, torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
-    dev = kv_cache.get_device()
-    T = slot_mapping.numel()
+    i32, f32, b16 = torch.int32, torch.float32, torch.bfloat16
+    dev, T, shape, code = kv_cache.get_device(), slot_mapping.numel(), kv_cache.shape, kv_cache.dtype
+    nb, bs, width = shape if len(shape) == 3 else (0, 0, 0)
     rope = HEAD_DIM - KV_LORA_RANK
-    ok = (dev >= 0 and dev == torch._C._cuda_getDevice() and kv_cache.dtype in codes and kv_cache.dim() == 3
-          and kv_cache.is_contiguous()
-          and kv_scales.dtype is f32 and kv_scales.get_device() == dev and kv_scales.is_contiguous()
-          and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
-          and c_kv.dtype is b16 and c_kv.get_device() == dev and c_kv.shape == (T, KV_LORA_RANK)
-          and k_pe.dtype is b16 and k_pe.get_device() == dev and k_pe.shape == (T, rope)
-          and _dense_rows(c_kv, 1) and _dense_rows(k_pe, 1))
-    nb, bs, width = kv_cache.shape if kv_cache.dim() == 3 else (0, 0, 0)
-    if not (ok and width == HEAD_DIM and scale_group > 0 and bs % scale_group == 0
-            and kv_scales.numel() == nb * bs // scale_group):
+    c_shape, p_shape = c_kv.shape, k_pe.shape
+    c_stride, p_stride = c_kv.stride(), k_pe.stride()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and (code is torch.uint8 or code is torch.float8_e4m3fn)
+            and width == HEAD_DIM and kv_cache.is_contiguous()
+            and scale_group > 0 and bs % scale_group == 0
+            and kv_scales.dtype is f32 and kv_scales.get_device() == dev and kv_scales.is_contiguous()
+            and kv_scales.numel() == nb * bs // scale_group
+            and slot_mapping.dtype is i32 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
+            and c_kv.dtype is b16 and c_kv.get_device() == dev and c_shape == (T, KV_LORA_RANK)
+            and k_pe.dtype is b16 and k_pe.get_device() == dev and p_shape == (T, rope)
+            and _dense_rows(c_shape, c_stride, 1) and _dense_rows(p_shape, p_stride, 1)):
+        fn, codes = "mla_cache_append", (torch.float8_e4m3fn, torch.uint8)
         _refuse(fn, dev, [("kv_cache", kv_cache, codes), ("kv_scales", kv_scales, (f32,)),
                           ("slot_mapping", slot_mapping, (i32,)), ("c_kv", c_kv, (b16,)), ("k_pe", k_pe, (b16,))],
                 [(t.is_contiguous(), f"{n} must be contiguous") for n, t in
@@ -552,11 +562,12 @@ def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_gro
                   "kv_scales must hold num_blocks * block_size / scale_group scales"),
                  (False, "the rows of c_kv and k_pe must be dense and must not overlap")])
     many = T > 1
-    _check(fn, lib.mla_cache_append(
-        c_kv.data_ptr(), c_kv.stride(0) if many else KV_LORA_RANK, k_pe.data_ptr(),
-        k_pe.stride(0) if many else rope, slot_mapping.data_ptr(), T, nb, bs, scale_group,
-        kv_cache.data_ptr(), kv_scales.data_ptr(),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)))
+    status = lib.mla_cache_append(
+        c_kv.data_ptr(), c_stride[0] if many else KV_LORA_RANK, k_pe.data_ptr(), p_stride[0] if many else rope,
+        slot_mapping.data_ptr(), T, nb, bs, scale_group, kv_cache.data_ptr(), kv_scales.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check("mla_cache_append", status)
 
 
 def mla_fit_kpool_indices(token_indices, *, topk: int, out, stream=None) -> None:

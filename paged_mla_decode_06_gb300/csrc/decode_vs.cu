@@ -195,7 +195,7 @@ __device__ __forceinline__ void report(int* status, int code) {
 // Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or abort.
 __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
   const bool brief = x.limit_ns < kSleepNs;  // (a sleep may last longer than the limit: poll)
-  if (brief ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (mbar_test_wait(bar, parity)) return true;
   // one sleep before the clock is read for the first time: nearly every wait
   // ends in it, and reading the global timer takes longer than most waits
   if (!brief && mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;

@@ -17,6 +17,10 @@
 // is larger than its latency (slots, then rows, then codes: three trips). The
 // rows of a run are read once and stay in registers between the maximum and
 // the rounding; the rows of a longer run past those are read again, from L2.
+// (16 prompts of 2047 tokens, groups of 64: 14.5 us, 3.9 TB/s of reads and
+// writes; without either the same call takes 9.9 us. Asking for a CTA's rows in
+// L2 before its slots are known 17.4 us; batches of 32 rows at more CTAs an SM,
+// all but the last read twice, 15.4.)
 // A CTA has four threads for each 16-byte piece of a row (4 x 72), so that a
 // thread walks down one column with a constant stride, 16 pieces in flight for
 // 64 rows; a warp, whose runs are short, takes the pieces row after row.
@@ -36,7 +40,8 @@ constexpr int kWarpGroup = 8;              // largest group a warp takes
 constexpr int kMaxWindow = 256;            // tokens of a CTA's window
 constexpr int kSlotCache = 512;            // slots a CTA keeps in shared memory
 constexpr int kMinExp = -60;               // the smallest scale is 2^-60
-constexpr int kWindowCtas = 608;            // CTAs of a long call: two an SM, twice over
+constexpr int kWindowCtas = 304;           // CTAs of a long call: two an SM, once over (twice over:
+                                           // 16 prompts of 2047 tokens 15.6 us against 14.5)
 
 // Row t's piece (the caller's pointer to it advances by the part's stride).
 struct Column {
@@ -83,16 +88,18 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
   return __int_as_float((e + 127) << 23);
 }
 
+// Eight bf16 values, times inv, as e4m3 codes.
 __device__ __forceinline__ uint2 quantise(uint4 v, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t out[2] = {0u, 0u};
+  uint16_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(f.x * inv, f.y * inv), __NV_SATFINITE, __NV_E4M3);
-    out[i >> 1] |= (c & 0xFFFFu) << ((i & 1) * 16);
-  }
-  return make_uint2(out[0], out[1]);
+  for (int i = 0; i < 4; ++i)
+    asm("{\n .reg .b32 a, b;\n .reg .b64 x, y;\n shl.b32 a, %1, 16;\n and.b32 b, %1, 0xffff0000;\n"
+        " mov.b64 x, {a, b};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {a, b}, x;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 %0, b, a;\n}\n"
+        : "=h"(c[i])
+        : "r"(w[i]), "f"(inv));
+  return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
 }
 
 __device__ __forceinline__ uint32_t requantise(uint32_t codes, float ratio) {

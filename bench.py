@@ -133,13 +133,13 @@ PROFILED_TRAFFIC = {
     },
     (5, "fp8", 16): {  # decode_hn.cu, e4m3 batch at 16 heads (profiles/decode_hn_fp8.md)
         "source": "decode_hn.cu",
-        "code_sha256": "b27dd235d6d48fcd1daf6457f627d20b78edd5858b4d37eb289261f2ff1ad65b",
-        "dram_per_alg_byte": (226.828800 + 3.769344) / 226.738272,
+        "code_sha256": "9c55d39260e037ff5ac4be0a01ef275a216cf3b3140883c7cca3e7447448610d",
+        "dram_per_alg_byte": (226.829312 + 3.374848) / 226.738272,
     },
     (5, "fp8", 128): {  # decode_hn.cu on CTA-pair clusters, e4m3 batch at 128 heads (same file)
         "source": "decode_hn.cu",
-        "code_sha256": "b27dd235d6d48fcd1daf6457f627d20b78edd5858b4d37eb289261f2ff1ad65b",
-        "dram_per_alg_byte": (228.402432 + 4.709632) / 228.286560,
+        "code_sha256": "9c55d39260e037ff5ac4be0a01ef275a216cf3b3140883c7cca3e7447448610d",
+        "dram_per_alg_byte": (228.407552 + 4.732160) / 228.286560,
     },
 }
 

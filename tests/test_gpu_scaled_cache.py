@@ -535,11 +535,12 @@ def test_serving_steps(heads, bs, g):
                 *S.decode(qc, QS, codes, scales, g, lists, SCALE, bounds=True))
 
 
-def test_step_captured_and_replayed():
+@pytest.mark.parametrize("H", [16, 128])
+def test_step_captured_and_replayed(H):
     """One decode step captured in a graph on a side stream and replayed with
     other lengths, rows and queries in the same buffers."""
     rng = np.random.default_rng(21)
-    R, cols, nb, bs, g, H = 3, 8, 32, 64, 64, 16
+    R, cols, nb, bs, g = 3, 8, 32, 64, 64
     codes0, scales0 = filled(rng, nb * bs, g)
     ids = rng.permutation(nb)
     buf = dict(qsl=dev(np.arange(R + 1), np.int32), lens=dev(np.ones(R), np.int32), free=dev(ids[20:], np.int32),

@@ -133,13 +133,13 @@ PROFILED_TRAFFIC = {
     },
     (5, "fp8", 16): {  # decode_hn.cu, e4m3 batch at 16 heads (profiles/decode_hn_fp8.md)
         "source": "decode_hn.cu",
-        "code_sha256": "9c55d39260e037ff5ac4be0a01ef275a216cf3b3140883c7cca3e7447448610d",
-        "dram_per_alg_byte": (226.829312 + 3.374848) / 226.738272,
+        "code_sha256": "c94a8a98566852ff49137bdd25f14266eec37a09946714c21ece6ebbcbc73fb3",
+        "dram_per_alg_byte": (226.829568 + 3.854336) / 226.738272,
     },
     (5, "fp8", 128): {  # decode_hn.cu on CTA-pair clusters, e4m3 batch at 128 heads (same file)
         "source": "decode_hn.cu",
-        "code_sha256": "9c55d39260e037ff5ac4be0a01ef275a216cf3b3140883c7cca3e7447448610d",
-        "dram_per_alg_byte": (228.407552 + 4.732160) / 228.286560,
+        "code_sha256": "c94a8a98566852ff49137bdd25f14266eec37a09946714c21ece6ebbcbc73fb3",
+        "dram_per_alg_byte": (228.464384 + 4.723200) / 228.286560,
     },
 }
 

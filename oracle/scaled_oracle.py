@@ -123,12 +123,17 @@ def decode(q_codes, q_scale, codes, scales, group, lists, softmax_scale, sinks=N
 
 def _bounds(q, c, s, softmax_scale, out, lse, sinks):
     """Largest error of a kernel that keeps scores, sums and accumulators in
-    fp32, rounds each weight p'_j ~ w_j s_j (w the softmax weights) to two e4m3
-    terms and the output to bf16:
-      * a weight: two 4-bit terms leave half a step of the second, 2^-8 of the
-        weight, and 2^-14 of the row's largest weight where the second term is
-        below e4m3's smallest step (2^-9, half of it, with the largest weight
-        kept at 2^4 or more);
+    fp32, rounds each weight p'_j ~ w_j s_j (w the softmax weights, the row's
+    largest kept at p' >= 2^4) to an e4m3 term and a rest in e5m2 or, 32 times
+    itself, in e4m3, and the output to bf16:
+      * a weight: half a step of e4m3 leaves a rest of 2^-4 of it at most, half
+        a step of e5m2 2^-3 of that: 2^-7. The f16 that both are taken from
+        adds 2^-11. Below 2^-6 the first term's half step is 2^-10 and 2^-3 of
+        the rest at most 2^-13, 2^-17 of the largest weight, and at most 2^-3
+        of the weight, as the rest is no larger than it. A rest below the
+        second term's normal range is off by half its smallest step: 2^-17 in
+        e5m2, 2^-10 / 32 in the other, 2^-19 of the largest weight, and at most
+        the weight itself;
       * a score: 576 fp32 additions, each off by at most 2^-23 (truncated
         alignment in the matrix unit) of the sum of magnitudes;
       * the exponent: its argument t = score log2 e + log2 s rounded a few
@@ -143,8 +148,10 @@ def _bounds(q, c, s, softmax_scale, out, lse, sinks):
     gamma = 576 * 2.0 ** -23 * mags.max(1) + (t.max(1) + 8.0) * 2.0 ** -21 + n * 2.0 ** -25
     v = np.abs(c[:, :KV_LORA_RANK])
     ws = w * s
-    tol_o = (2.0 ** -8 + 2.0 * gamma)[:, None] * (ws @ v)
-    tol_o += 2.0 ** -14 * ws.max(1)[:, None] * v.sum(0)[None, :]
+    top = ws.max(1)[:, None]
+    err = (2.0 ** -7 + 2.0 ** -11) * ws
+    err += np.minimum(2.0 ** -17 * top, 2.0 ** -3 * ws) + np.minimum(2.0 ** -19 * top, ws)
+    tol_o = (err + 2.0 * gamma[:, None] * ws) @ v
     tol_o = tol_o * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(out)
     tol_l = gamma + np.abs(lse) * 2.0 ** -22
     if sinks is not None:

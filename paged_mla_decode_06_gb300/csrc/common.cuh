@@ -98,8 +98,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 
-// Two weights as two e4m3 code pairs: hi = e4m3(p), lo = e4m3(p - hi),
-// formed in f16 (p rounded to 11 bits first; the difference is then exact).
+// Two weights as two code pairs: hi = e4m3(p) and lo, the rest p - hi, formed
+// in f16 (p rounded to 11 bits first; the difference is then exact). The rest
+// is taken as e4m3 (8 bits of p, nothing below 2^-10), as e5m2 (7 bits, down to
+// 2^-17), or as 32 times it in e4m3, for products that are summed apart (8
+// bits, down to 2^-15; the rest is at most 8 where p <= 2^8). The last two are
+// for rows of which one key outweighs a long context: with p = 2^4 at the
+// largest weight, keys 2^-14 below it would be left out of the first.
+enum class Rest { kE4m3, kE5m2, kE4m3Times32 };
+template <Rest R>
 __device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32_t& lo) {
   const __half2 ph = __floats2half2_rn(p0, p1);
   const uint32_t phb = *reinterpret_cast<const uint32_t*>(&ph);
@@ -107,21 +114,26 @@ __device__ __forceinline__ void p_terms(float p0, float p1, uint32_t& hi, uint32
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(h16) : "r"(phb));
   uint32_t back;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(back) : "h"(h16));
-  const __half2 d = __hsub2(ph, *reinterpret_cast<const __half2*>(&back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(l16) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
+  __half2 d = __hsub2(ph, *reinterpret_cast<const __half2*>(&back));
+  if constexpr (R == Rest::kE4m3Times32) d = __hmul2(d, __floats2half2_rn(32.f, 32.f));
+  const uint32_t db = *reinterpret_cast<const uint32_t*>(&d);
+  if constexpr (R == Rest::kE5m2)
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;\n" : "=h"(l16) : "r"(db));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(l16) : "r"(db));
   hi = h16;
   lo = l16;
 }
 
-// Four weights (in order from the low byte) as two words of e4m3 codes, hi and
-// lo as in p_terms.
+// Four weights (in order from the low byte) as two words of codes, the rest in
+// e5m2.
 __device__ __forceinline__ void p_terms4(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
   asm("{\n .reg .b16 h0, h1, l0, l1;\n .reg .b32 a, b, c, d;\n"
       " cvt.rn.f16x2.f32 a, %3, %2;\n cvt.rn.f16x2.f32 b, %5, %4;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 h0, a;\n cvt.rn.satfinite.e4m3x2.f16x2 h1, b;\n"
       " cvt.rn.f16x2.e4m3x2 c, h0;\n cvt.rn.f16x2.e4m3x2 d, h1;\n"
       " sub.f16x2 a, a, c;\n sub.f16x2 b, b, d;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l0, a;\n cvt.rn.satfinite.e4m3x2.f16x2 l1, b;\n"
+      " cvt.rn.satfinite.e5m2x2.f16x2 l0, a;\n cvt.rn.satfinite.e5m2x2.f16x2 l1, b;\n"
       " mov.b32 %0, {h0, h1};\n mov.b32 %1, {l0, l1};\n}\n"
       : "=r"(hi), "=r"(lo)
       : "f"(p0), "f"(p1), "f"(p2), "f"(p3));

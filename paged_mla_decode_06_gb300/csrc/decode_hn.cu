@@ -29,7 +29,8 @@
 // TMEM), so p <= 2^8 fits e4m3 and the bulk of the weights stays in its
 // normal range; the true max is kept for the partials. With group scales (GS)
 // the thread's key has one scale, which enters its scores and the row sums
-// (KeyScale); everything else is the same.
+// (KeyScale), and the rest of P has more range (Rest); everything else is the
+// same.
 //
 // Requests of 65..128 rows run on a thread-block cluster of CL = 2 CTAs, CTA
 // r owning rows [r NR, (r + 1) NR) of the row tile: every key box is read
@@ -465,11 +466,12 @@ __device__ void qk_issue(const Ctx& x, const HnMaps& maps, const DecodeParams& p
   drain_wait(x, x.bar(kDrain), 0, 25);
 }
 
-template <int NR, int CL>
+template <int NR, int CL, bool GS>
 __device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
   using C = HnCfg<NR>;
   if (x.lane != 0) return;
   constexpr uint32_t kIdPV = instr_desc(128, C::kNpv, 0, 0, true, true);
+  constexpr uint32_t kIdLo = instr_desc(128, C::kNpv, 0, GS ? 1 : 0, true, true);  // (GS: the rest as e5m2)
   const uint64_t v_desc = smem_desc_sw128(smem_u32(x.smem + C::kOffRing), kSlot, 1024);   // MN-major
   const uint64_t p_desc = smem_desc_interleave(smem_u32(x.smem + C::kOffP), C::kPLbo, 128);
   int g = 0, ne = 0;
@@ -503,7 +505,7 @@ __device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
           const uint64_t bv = pb + static_cast<uint64_t>((ks * 4 * C::kPLbo) >> 4);
           mma_ss_f8(dm, av, bv, kIdPV, (c | ks) != 0 ? 1u : 0u);
           if constexpr (!C::kConcat)  // the lo term: the next NR / 16 core matrices
-            mma_ss_f8(dm, av, bv + static_cast<uint64_t>((NR / 16 * 128) >> 4), kIdPV, 1u);
+            mma_ss_f8(dm, av, bv + static_cast<uint64_t>((NR / 16 * 128) >> 4), kIdLo, 1u);
         }
         release<CL>(x.bar(kEmpty + slot));  // the value box's last read
       }
@@ -538,6 +540,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[NW]) {
 template <int NR, int CL, bool GS>
 __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParams& p) {
   using C = HnCfg<NR>;
+  constexpr Rest kRest = !GS ? Rest::kE4m3 : C::kConcat ? Rest::kE4m3Times32 : Rest::kE5m2;
   constexpr int NH = NR / 2;
   const int lane = x.lane;
   const int sw = x.warp - 4;                    // softmax warp 0..7
@@ -707,7 +710,7 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
             const float p1 = fast_exp2(GS ? s[n + 1] - b1 : fmaf(s[n + 1], scale2, -b1));
             l[n] = GS ? fmaf(p0, kq.inv, l[n]) : l[n] + p0;
             l[n + 1] = GS ? fmaf(p1, kq.inv, l[n + 1]) : l[n + 1] + p1;
-            p_terms(p0, p1, hc[e], lc[e]);
+            p_terms<kRest>(p0, p1, hc[e], lc[e]);
           }
           hw[q] = hc[0] | (hc[1] << 16);
           lw[q] = lc[0] | (lc[1] << 16);
@@ -823,7 +826,7 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
             tmem_ld_cols<8>(x.tbase + lane_off + m * C::kNpv + NR + ru, o2);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += o2[i];
+            for (int i = 0; i < 8; ++i) o[i] = GS ? fmaf(o2[i], 1.f / 32.f, o[i]) : o[i] + o2[i];
           } else {
             tmem_ld_wait();
           }
@@ -980,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (x.warp == 1) {
     qk_issue<NR, CL>(x, maps, p);
   } else if (x.warp == 3) {
-    pv_issue<NR, CL>(x, p);
+    pv_issue<NR, CL, GS>(x, p);
   } else {
     softmax_rows<NR, CL, GS>(x, maps, p);
   }

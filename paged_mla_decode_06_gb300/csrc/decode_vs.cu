@@ -13,14 +13,14 @@
 //                            dims), B = the key rows of the rings, K-major:
 //                            18 kind::f8f6f4 instructions of 64.5 cycles;
 //   O[rows, 256]  += P V     for each half of 64 keys: M = 128 rows, N = 256
-//                            columns, K = 64, P as two e4m3 terms (hi, lo), V =
-//                            the same key rows read MN-major: 8 instructions a
-//                            chunk of 128 cycles.
+//                            columns, K = 64, P as two terms (hi in e4m3, lo in
+//                            e5m2), V = the same key rows read MN-major: 8
+//                            instructions a chunk of 128 cycles.
 // That is 2180 tensor cycles a chunk, close to what the shared memory's 128
 // bytes a clock allow for the operands, the copies in and P (284 KB, 2220
 // cycles). Measured: 3100 to 3400 (52 x 16384 keys, 128 heads), bound by the
 // chain S -> maxima -> weights -> P of a half-chunk (2600 cycles) and its
-// hand-overs; at 1.7 GHz, as the SMs clock under this load, 180 us.
+// hand-overs; at 1.7 GHz, as the SMs clock under this load, 188 us.
 //
 // The softmax works on half-chunks of 64 keys: one group of eight warps takes
 // the even ones, another the odd ones, so that each has two of them in
@@ -43,7 +43,9 @@
 // the weights 2^(t - m) multiply the codes (KeyScale). They are formed as
 // p = 2^(t - m_ref + 4) with a reference that moves only when a half-chunk's
 // maximum exceeds it by more than 4.75 (O is then rescaled in TMEM), so p <=
-// 2^8.75 fits e4m3 and hi + lo carry 8 bits of it.
+// 2^8.75 fits e4m3; hi + lo carry 7 bits of it, and the rest of a weight down to
+// 2^-21 of the row's largest (Rest: rows of which one key outweighs a long
+// context).
 //
 // Warps: 0 loads, 1 issues Q K^T, 2 prepares the keys' scales (sparse lists: 0
 // and 2 share the copies), 3 issues P V, 4-19 softmax and epilogue (of either
@@ -78,7 +80,7 @@ constexpr int kGroupWarps = 8;
 constexpr int kPart = 32;                // keys of a softmax warp
 constexpr int kUni = 16;                 // keys that share their scale where the groups are multiples of it
 constexpr int kThreads = 32 * (4 + kSoftWarps);
-constexpr int kPTile = kRows * kHalf;    // one e4m3 term of P of a half-chunk
+constexpr int kPTile = kRows * kHalf;    // one term of P of a half-chunk
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;           // 256 columns
 constexpr uint32_t kTmemS = 256;         // 128: S of a chunk
@@ -564,7 +566,8 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
 
 __device__ void pv_issue(const Ctx& x) {
   if (x.n_chunks == 0) return;
-  constexpr uint32_t kId = instr_desc(kRows, 256, 0, 0, false, true);
+  constexpr uint32_t kIdHi = instr_desc(kRows, 256, 0, 0, false, true);
+  constexpr uint32_t kIdLo = instr_desc(kRows, 256, 1, 0, false, true);
   const uint64_t v_desc = smem_desc_sw128(smem_u32(x.smem + kOffVal), kSlot, 1024);  // MN-major, two boxes
   const uint64_t p_desc = smem_desc_sw64(smem_u32(x.smem + kOffP), 512);
   const uint32_t d = x.tbase + kTmemO;
@@ -583,8 +586,8 @@ __device__ void pv_issue(const Ctx& x) {
       for (int ks = 0; ks < kHalf / 32; ++ks) {
         const uint64_t av = pb + static_cast<uint64_t>((ks * 32) >> 4);
         const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
-        mma_ss_f8(d, av, bv, kId, (g | ks) != 0 ? 1u : 0u);
-        mma_ss_f8(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kId, 1u);
+        mma_ss_f8(d, av, bv, kIdHi, (g | ks) != 0 ? 1u : 0u);
+        mma_ss_f8(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kIdLo, 1u);
       }
       if (last) mma_commit(x.bar(kVEmpty + vr.at));
       mma_commit(x.bar(kPFree + h));
@@ -726,7 +729,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     ok = warp_wait(x, x.bar(kX + 4 * (g & 3) + q4), (g >> 2) & 1, 32);
     if (!ok) break;
     const float alpha = follow(fmaxf(mine, xm[(kh ^ 1) * kRows]));
-    // p as hi + lo e4m3 terms, 16 keys to a 16-byte chunk of each tile
+    // p as hi + lo terms, 16 keys to a 16-byte chunk of each tile
     const float base = ref == -INFINITY ? 0.f : ref - kPBias;
     float psum = 0.f;
     uint32_t hi[8], lo[8];

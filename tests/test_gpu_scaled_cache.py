@@ -402,6 +402,26 @@ def test_decode_scales_far_apart(heads, bs, qlens, exps):
     check_decode(c)
 
 
+@pytest.mark.parametrize("heads,bs,qlens", [(16, 64, None), (64, 64, None), (128, 64, None), (128, 64, [2]), (16, 16, None)])
+def test_decode_one_key_outweighs_a_long_context(heads, bs, qlens):
+    """One key without a value weighs 2^16 times as much as each of 9000 others
+    whose values agree in sign: together they are the result."""
+    c = decode_case(17, [9000], heads, bs, 1, qlens=qlens)
+    rng = np.random.default_rng(18)
+    q = np.tile(rng.standard_normal(576) * 2.0 ** -8, (c["T"], heads, 1)).astype(np.float32) / QS
+    c["q"] = I.float32_to_e4m3_codes(q)
+    c["codes"] &= 0x7F                                     # (poisoned slots stay NaN)
+    at = S.row_slots(c["table"][0], bs, 9000)
+    c["codes"][at] = I.float32_to_e4m3_codes(np.abs(rng.standard_normal((9000, 576))).astype(np.float32))
+    c["scales"][at] = 1.0
+    first = int(at[4000])
+    rope = O.decode_e4m3fn(c["q"])[0, 0, 512:] * QS
+    c["codes"][first, :512] = 0                            # it has no value of its own
+    c["codes"][first, 512:] = I.float32_to_e4m3_codes(448 * np.sign(rope).astype(np.float32))
+    c["scales"][first] = np.float32(16 * np.log(2.0) / (448 * SCALE * np.abs(rope).sum()))
+    check_decode(c)
+
+
 def test_decode_zero_groups():
     """Rows of zeros, written by the append under the smallest scale, weigh
     e^0 in the softmax beside keys of ordinary and of very negative score."""

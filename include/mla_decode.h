@@ -453,8 +453,9 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * tensor-core kernel, and sparse lists, run on a kernel of their own here, in
  * the same workspace; where the planner chose the number of segments of a
  * sparse call, that kernel may use fewer. A sink of -inf counts as none.
- * A weight enters the product with the values rounded to 7 bits or more, and to
- * steps of 2^-19 of the row's largest (weight times scale) or less.
+ * A weight times its scale enters the product with the codes rounded to 7 bits
+ * or more, below 2^-10 of the row's largest to 3 or more, and is off by 2^-19 of
+ * the largest at most where it is smaller still.
  *   kv_scales    [num_blocks * block_size / scale_group] fp32. The scales of
  *                groups that hold visible keys must lie in [2^-60, 2^60]
  *                (mla_cache_append writes such); others are not used.

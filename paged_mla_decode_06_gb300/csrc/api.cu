@@ -120,22 +120,33 @@ mla_status_t check_group_scales(const mla_plan_t* plan, const float* kv_scales, 
 }
 
 // Whether a call with group scales runs on the value-split kernel, whatever
-// kernel the plan names for the same problem with one scale: every row tile
-// of more than 64 rows the plan gives to a tensor-core kernel, and sparse lists.
+// kernel the plan names for the same problem with one scale: row tiles of more
+// than 64 rows of a tensor-core plan, and what the planner leaves to the
+// warp-MMA kernel (sparse lists, block sizes that are not a multiple of 64) but
+// for one row group of 16 over at most two of its chunks of 64 keys: 2 requests
+// of 128 keys, 16 heads take 10.8 us there and 11.5 here, of 192 keys 14.2 and
+// 13.1; 32 of 4000 keys, 128 heads 300 and 68; 32 x 2048 sparse slots, 32 heads
+// 52.6 and 33.6.
 bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
   if (kv_scales == nullptr) return false;
-  if (plan->prob.topk > 0) return true;
-  return plan->kernel == mla::kTcPair128 || (plan->kernel == mla::kTcRowsN && plan->tile_rows > 64);
+  const mla_problem_t& p = plan->prob;
+  if (plan->kernel == mla::kTcPair128) return true;
+  if (plan->kernel == mla::kTcRowsN) return plan->tile_rows > 64;
+  if (p.kernel != MLA_KERNEL_AUTO) return false;
+  const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
+  return rows > 16 || (p.topk > 0 ? p.topk : p.max_seq_len) > 128;
 }
 
-// Segments of a fixed schedule. The planner's own choice for sparse lists (about
-// two of its CTAs per SM) suits the warp-MMA kernel; the value-split kernel, two
-// CTAs a tile and one an SM, takes no more of them than one wave of CTAs (32
-// tokens x 2048 keys, 128 heads: 61 us with the four of the planner, 38 with two).
+// Segments of a fixed schedule. The planner's own choice (about two of its CTAs
+// per SM) suits the warp-MMA kernel; the value-split kernel, two CTAs a tile and
+// one an SM, takes no more of them than one wave of CTAs (32 tokens x 2048 keys,
+// 128 heads: 61 us with the four of the planner, 38 with two).
 int32_t segments_of(const mla_plan_t* plan, const float* kv_scales) {
   const mla_problem_t& p = plan->prob;
-  if (p.num_segments != 0 || p.topk == 0 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
-  const int64_t ctas = 2 * static_cast<int64_t>(p.num_tokens);  // (a token's heads are one row tile)
+  if (p.num_segments != 0 || plan->num_segments == 1 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
+  const int64_t units = p.topk > 0 ? p.num_tokens : p.num_reqs;
+  const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
+  const int64_t ctas = 2 * units * ((rows + 127) / 128);
   const int64_t fit = ctas > 0 ? plan->num_sms / ctas : 1;
   return static_cast<int32_t>(fit < 1 ? 1 : fit < plan->num_segments ? fit : plan->num_segments);
 }

@@ -47,8 +47,8 @@
 // 2^-21 of the row's largest (Rest: rows of which one key outweighs a long
 // context).
 //
-// Warps: 0 loads, 1 issues Q K^T, 2 prepares the keys' scales (sparse lists: 0
-// and 2 share the copies), 3 issues P V, 4-19 softmax and epilogue (of either
+// Warps: 0 loads, 1 issues Q K^T, 2 prepares the keys' scales (keys copied row by
+// row: 0 and 2 share the copies), 3 issues P V, 4-19 softmax and epilogue (of either
 // group: a TMEM lane quarter of the rows and half of the half-chunk's keys
 // each). Every wait is bounded: a timeout records a code in the status word,
 // stops the CTA's work, drains what was issued and exits.
@@ -141,10 +141,14 @@ __device__ __forceinline__ Box box_of(int c, int j, int rank) {
   return Box{kRank, kOffRope + c % kKChunks * kRSlot};
 }
 
+// Where the keys of a row tile are: in blocks of a multiple of 64 slots (TMA
+// boxes), in blocks of any size, or in a list of slots (both copied row by row).
+enum class Keys { kBoxes, kBlocks, kList };
+
 struct VsMaps {
   CUtensorMap q;     // q as [T*H rows, 576] e4m3, box 128 bytes x 128 rows
   CUtensorMap qr;    // the same, box 64 bytes (the rope columns)
-  CUtensorMap kv;    // cache as [NB*BS rows, 576], box 128 bytes x 64 rows; sparse: x 1 row
+  CUtensorMap kv;    // cache as [NB*BS rows, 576], box 128 bytes x 64 rows (Keys::kBoxes)
   CUtensorMap kvr;   // the same, box 64 bytes
   CUtensorMap out;   // out as [T*H, 1, 512] bf16, box 32 rows x 64 columns, 128-byte swizzle
   CUtensorMap part;  // partials as [slot rows, 1, 512] or [T*H, NS, 512] fp32, box 32 x 32
@@ -227,10 +231,10 @@ __device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code
 }
 
 // Cache slot of key position pos (-1 past the segment or for an unused list entry).
-template <bool SPARSE>
+template <bool LIST>
 __device__ __forceinline__ int key_slot(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int pos) {
   if (pos >= x.seg_end) return -1;
-  if constexpr (SPARSE) return p.slots[x.list_base + pos];
+  if constexpr (LIST) return p.slots[x.list_base + pos];
   const int blk = pos / p.block_size;
   return bt_row[blk] * p.block_size + (pos - blk * p.block_size);
 }
@@ -279,7 +283,7 @@ __device__ __forceinline__ bool load_boxes(const Ctx& x, const VsMaps& maps, int
   return true;
 }
 
-// Sparse: the rows of a chunk's keys into its boxes, in their swizzles, by
+// The rows of a chunk's keys into its boxes, in their swizzles, by
 // 16-byte asynchronous copies: an instruction takes 128 bytes of four rows (of
 // the rope columns: 64 of eight). v[k] of lane l is the cache slot of key
 // 32 k + l; a key without one is filled with zeros. (TMA's row gathers take
@@ -418,19 +422,20 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
   __syncwarp();
 }
 
-// Sparse: warp 0 (VALUES) copies the own value boxes and the rope columns,
-// warp 2 the other boxes, and prepares the scales. The slots of a lane's keys
+// Keys copied row by row: warp 0 (VALUES) copies the own value boxes and the
+// rope columns, warp 2 the other boxes, and prepares the scales. The slots of a lane's keys
 // are read a chunk ahead. A chunk is posted when its copies, issued an
 // iteration before, have landed.
-template <bool VALUES>
-__device__ void produce_sparse(const Ctx& x, const DecodeParams& p) {
+template <bool LIST, bool VALUES>
+__device__ void produce_rows(const Ctx& x, const DecodeParams& p) {
   const int lane = x.lane;
+  const int32_t* bt_row = LIST ? nullptr : p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   int slot[4], next[4];
   float sc[4];
   auto slots_of = [&](int g, int (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = g < x.n_chunks ? key_slot<true>(x, p, nullptr, x.seg_start + g * kKeys + 32 * i + lane) : -1;
+      v[i] = g < x.n_chunks ? key_slot<LIST>(x, p, bt_row, x.seg_start + g * kKeys + 32 * i + lane) : -1;
   };
   auto scales_of = [&](const int (&v)[4]) {
 #pragma unroll
@@ -603,7 +608,7 @@ __device__ void pv_issue(const Ctx& x) {
 }
 
 // ------------------------------------------------------------------ softmax + epilogue
-template <bool SPARSE, bool UNI>
+template <Keys KEYS, bool UNI>
 __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParams& p) {
   const int lane = x.lane;
   const int sw = x.warp - 4;
@@ -616,7 +621,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   const int H = x.H;
   const int rho = x.row0 + r;
   const bool row_ok = rho < x.rows_total;
-  const int vis = !row_ok ? 0 : (SPARSE ? INT_MAX : x.part_len - x.qlen + rho / H + 1);
+  const int vis = !row_ok ? 0 : (KEYS == Keys::kList ? INT_MAX : x.part_len - x.qlen + rho / H + 1);
   const int n = x.n_half;
   bool ok = true;
 
@@ -797,7 +802,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
     // value rows of keys that do not exist (stale ring contents, cache rows past
     // the sequence, unused list entries) must not reach O through p = 0: they
     // are zeroed, a quarter by each warp
-    if (!SPARSE && kmask != 0xffffffffu) {
+    if (KEYS == Keys::kBoxes && kmask != 0xffffffffu) {
       uint8_t* box = x.smem + box_of(g >> 1, 2, x.rank).off + ((lane >> 3) & 1) * kSlot +
                      (kHalf * h + kPart * kh) * 128 + (lane & 7) * 16;
       for (int j = q4 + 4 * (lane >> 4); j < kPart; j += 8)
@@ -940,7 +945,7 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
   __syncwarp();
 }
 
-template <bool SPARSE, bool UNI>
+template <Keys KEYS, bool UNI>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_vs_kernel(const __grid_constant__ VsMaps maps, const DecodeParams p, int* status) {
   extern __shared__ uint8_t smem_raw[];
@@ -983,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   x.qlen = 1;
   x.tok0 = x.unit;
   x.list_base = 0;
-  if constexpr (SPARSE) {
+  if constexpr (KEYS == Keys::kList) {
     if (p.slot_indptr != nullptr) {
       x.list_base = p.slot_indptr[x.unit];
       x.part_len = p.slot_indptr[x.unit + 1] - p.slot_indptr[x.unit];
@@ -1050,21 +1055,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   x.tbase = *tslot;
 
   if (x.warp >= 4) {
-    softmax_rows<SPARSE, UNI>(x, maps, p);
+    softmax_rows<KEYS, UNI>(x, maps, p);
   } else if (x.warp == 1) {
     qk_issue(x, maps);
   } else if (x.warp == 3) {
     pv_issue(x);
   } else if (x.warp == 0) {
-    if constexpr (SPARSE)
-      produce_sparse<true>(x, p);
-    else
+    if constexpr (KEYS == Keys::kBoxes)
       produce_dense(x, maps, p);
-  } else {
-    if constexpr (SPARSE)
-      produce_sparse<false>(x, p);
     else
+      produce_rows<KEYS == Keys::kList, true>(x, p);
+  } else {
+    if constexpr (KEYS == Keys::kBoxes)
       scales_dense<UNI>(x, p);
+    else
+      produce_rows<KEYS == Keys::kList, false>(x, p);
   }
 
   // ------------------------------------------------------------ teardown
@@ -1089,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool SPARSE, bool UNI>
+template <Keys KEYS, bool UNI>
 cudaError_t launch_variant(const VsMaps& maps, const DecodeParams& p, dim3 grid, int* status, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -1097,11 +1102,11 @@ cudaError_t launch_variant(const VsMaps& maps, const DecodeParams& p, dim3 grid,
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(decode_vs_kernel<SPARSE, UNI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(decode_vs_kernel<KEYS, UNI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  decode_vs_kernel<SPARSE, UNI><<<grid, kThreads, kSmem, stream>>>(maps, p, status);
+  decode_vs_kernel<KEYS, UNI><<<grid, kThreads, kSmem, stream>>>(maps, p, status);
   return cudaGetLastError();
 }
 
@@ -1110,12 +1115,12 @@ cudaError_t launch_variant(const VsMaps& maps, const DecodeParams& p, dim3 grid,
 cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, dim3 grid, int* status,
                              cudaStream_t stream) {
   if (p.kv_scales == nullptr) return cudaErrorInvalidValue;
-  const bool sparse = p.slots != nullptr;
+  const bool boxes = p.slots == nullptr && p.block_size % kHalf == 0;
   VsMaps maps{};
   cudaError_t e = make_row_map(&maps.q, p.q, static_cast<uint64_t>(q_rows), kRows, true);
   if (e == cudaSuccess) e = make_row_map(&maps.qr, p.q, static_cast<uint64_t>(q_rows), kRows, true, 64);
-  if (e == cudaSuccess) e = make_row_map(&maps.kv, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true);
-  if (e == cudaSuccess) e = make_row_map(&maps.kvr, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true, 64);
+  if (e == cudaSuccess && boxes) e = make_row_map(&maps.kv, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true);
+  if (e == cudaSuccess && boxes) e = make_row_map(&maps.kvr, p.kv, static_cast<uint64_t>(kv_rows), kHalf, true, 64);
   if (e == cudaSuccess && p.out != nullptr)
     e = make_out_map(&maps.out, p.out, static_cast<uint64_t>(q_rows), 1, true, 64, 32, true);
   if (e == cudaSuccess && p.segm_out != nullptr)
@@ -1124,12 +1129,13 @@ cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_r
             : make_out_map(&maps.part, p.segm_out, static_cast<uint64_t>(q_rows),
                            static_cast<uint64_t>(p.num_segments), false, 32, 32, true);
   if (e != cudaSuccess) return e;
-  if (sparse) return launch_variant<true, false>(maps, p, grid, status, stream);
+  if (p.slots != nullptr) return launch_variant<Keys::kList, false>(maps, p, grid, status, stream);
+  if (!boxes) return launch_variant<Keys::kBlocks, false>(maps, p, grid, status, stream);
   // groups of a multiple of 16 slots: 16 keys from a 16-aligned position (of one
   // block) share their scale, and a softmax thread reads two for its 32 keys
   // instead of 32 (32 requests of 1 to 3 tokens, groups of 16: 97 against 90 us)
-  return p.scale_group % kUni == 0 ? launch_variant<false, true>(maps, p, grid, status, stream)
-                                    : launch_variant<false, false>(maps, p, grid, status, stream);
+  return p.scale_group % kUni == 0 ? launch_variant<Keys::kBoxes, true>(maps, p, grid, status, stream)
+                                    : launch_variant<Keys::kBoxes, false>(maps, p, grid, status, stream);
 }
 
 }  // namespace mla

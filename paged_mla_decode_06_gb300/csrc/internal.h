@@ -194,8 +194,7 @@ cudaError_t launch_decode_hn(const DecodeParams& p, int rows, int cluster, int64
 cudaError_t decode_hn_max_pairs(int rows, int* n);
 
 // tcgen05 kernel of the group-scaled cache for row tiles of up to 128 rows, two
-// CTAs that split the value columns: dense (block size a multiple of 64) or
-// sparse. grid.x counts CTAs: two per item or row tile.
+// CTAs that split the value columns: dense or sparse. grid.x counts CTAs: two per item or row tile.
 cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, dim3 grid, int* status,
                              cudaStream_t stream);
 

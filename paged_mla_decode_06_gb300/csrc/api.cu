@@ -14,6 +14,7 @@ namespace {
 constexpr int kHeadDim = 576;
 constexpr int kRank = 512;
 constexpr int kMaxHeads = 128;
+constexpr int kShortKeys = 512;  // requests that a call with group scales does not split
 constexpr int kMaxSegments = 64;
 constexpr int kSparseTile = 64;
 constexpr int64_t kRowsNMax = 128;  // query rows per request the rows-as-N kernel takes (a CTA pair)
@@ -119,22 +120,47 @@ mla_status_t check_group_scales(const mla_plan_t* plan, const float* kv_scales, 
   return MLA_OK;
 }
 
+// CTAs of the value-split kernel, two a row tile of 128, over unsplit requests.
+int64_t value_split_ctas(const mla_plan_t* plan) {
+  const mla_problem_t& p = plan->prob;
+  const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
+  return 2 * ((rows + 127) / 128) * (p.topk > 0 ? p.num_tokens : p.num_reqs);
+}
+
 // Whether a call with group scales runs on the value-split kernel, whatever
-// kernel the plan names for the same problem with one scale: row tiles of more
-// than 64 rows of a tensor-core plan, and what the planner leaves to the
-// warp-MMA kernel (sparse lists, block sizes that are not a multiple of 64) but
-// for one row group of 16 over at most two of its chunks of 64 keys: 2 requests
-// of 128 keys, 16 heads take 10.8 us there and 11.5 here, of 192 keys 14.2 and
-// 13.1; 32 of 4000 keys, 128 heads 300 and 68; 32 x 2048 sparse slots, 32 heads
-// 52.6 and 33.6.
+// kernel the plan names for the same problem with one scale:
+// * of a rows-as-N plan, tiles of more than 64 rows, and of more than 16 in a
+//   call of one wave over short requests (32 x 512 keys, 64 heads: 15.8 us
+//   against 25.7, 48 heads 22.1; 16 heads 15.0; over long ones the rows-as-N
+//   kernel is ahead: 52 x 16384 keys, 48 heads 121 us against 186);
+// * of a warp-MMA plan (sparse lists, block sizes that are not a multiple of 64)
+//   all but one row group of 16 over at most two of its chunks of 64 keys: 2
+//   requests of 128 keys, 16 heads take 10.8 us there and 11.5 here, of 192 keys
+//   14.2 and 13.1; 32 of 4000 keys, 128 heads 300 and 68; 32 x 2048 sparse
+//   slots, 32 heads 52.6 and 33.6.
 bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
   if (kv_scales == nullptr) return false;
   const mla_problem_t& p = plan->prob;
   if (plan->kernel == mla::kTcPair128) return true;
-  if (plan->kernel == mla::kTcRowsN) return plan->tile_rows > 64;
-  if (p.kernel != MLA_KERNEL_AUTO) return false;
+  const bool asked = p.kernel != MLA_KERNEL_AUTO;
+  if (plan->kernel == mla::kTcRowsN) {
+    const bool one_wave = plan->schedule == 1 && p.max_seq_len <= kShortKeys && value_split_ctas(plan) <= plan->num_sms;
+    return plan->tile_rows > 64 || (!asked && plan->tile_rows > 16 && one_wave);
+  }
+  if (asked) return false;
   const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
   return rows > 16 || (p.topk > 0 ? p.topk : p.max_seq_len) > 128;
+}
+
+// Whether a whole call with group scales leaves a balanced plan's schedule and
+// merge out: short requests, and a CTA (pair) for each row tile in one wave (32
+// x 128 keys, 128 heads: 10.2 us against 14.4, 512 keys 15.8 against 20.9; one
+// request of 512 keys 15.4 against 15.6, of 768 18.9 against 16.4).
+bool runs_unsplit(const mla_plan_t* plan, const float* kv_scales) {
+  const mla_problem_t& p = plan->prob;
+  if (kv_scales == nullptr || plan->schedule != 1 || p.max_seq_len > kShortKeys) return false;
+  return (runs_value_split(plan, kv_scales) ? value_split_ctas(plan)
+                                            : static_cast<int64_t>(plan->row_tiles) * p.num_reqs) <= plan->num_sms;
 }
 
 // Segments of a fixed schedule. The planner's own choice (about two of its CTAs
@@ -144,9 +170,7 @@ bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
 int32_t segments_of(const mla_plan_t* plan, const float* kv_scales) {
   const mla_problem_t& p = plan->prob;
   if (p.num_segments != 0 || plan->num_segments == 1 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
-  const int64_t units = p.topk > 0 ? p.num_tokens : p.num_reqs;
-  const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
-  const int64_t ctas = 2 * units * ((rows + 127) / 128);
+  const int64_t ctas = value_split_ctas(plan);
   const int64_t fit = ctas > 0 ? plan->num_sms / ctas : 1;
   return static_cast<int32_t>(fit < 1 ? 1 : fit < plan->num_segments ? fit : plan->num_segments);
 }
@@ -376,7 +400,7 @@ mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* s
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* status = reinterpret_cast<int*>(ws + plan->status_offset);
   mla::DecodeParams d = make_params(plan, in);
-  if (plan->schedule == 1) {
+  if (plan->schedule == 1 && !runs_unsplit(plan, in.kv_scales)) {
     s = run_schedule(plan, in, ws, stream);
     if (s == MLA_OK) s = run_items(plan, in, sinks, ws, out, lse, stream);
     if (s == MLA_OK) s = run_merge_items(plan, in, sinks, ws, out, lse, stream);

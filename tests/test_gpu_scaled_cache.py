@@ -736,3 +736,17 @@ def test_bounded_wait_runs_out_and_is_reported(heads, qlens, topk):
     lists = list(c["slots"]) if topk else S.token_slots(c["table"], c["lens"], c["bs"], c["qo"])
     compare(kw["out"].double().cpu().numpy(), kw["lse"].double().cpu().numpy(),
             *S.decode(c["q"], QS, c["codes"], c["scales"], c["g"], lists, SCALE, c["sinks"], bounds=True))
+
+
+@pytest.mark.parametrize("heads,qlens,longest", [(16, None, 512), (17, None, 512), (48, None, 511), (64, [1, 3, 0, 2, 1, 1, 1], 300),
+                                                 (128, None, 512), (128, [2, 3, 0, 3, 1, 1, 2], 512), (128, None, 513)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_decode_short_requests(heads, qlens, longest, sinks):
+    """Short requests, which a whole call does not split, and the three stages
+    over the same ones, which do; also in so many requests that neither kernel
+    takes them in one wave."""
+    lens = [longest, 64, 5, 129, 300, 2, 256]
+    c = decode_case(51, lens, heads, 64, 16, qlens=qlens, sinks=sinks)
+    check_decode(c)
+    check_decode(c, stages=True)
+    check_decode(decode_case(52, [33] * 40 + [100] * 40 + [0] * 80, heads, 64, 64, sinks=sinks))

@@ -14,7 +14,8 @@ namespace {
 constexpr int kHeadDim = 576;
 constexpr int kRank = 512;
 constexpr int kMaxHeads = 128;
-constexpr int kShortKeys = 512;  // requests that a call with group scales does not split
+constexpr int64_t kFewKeys = 32768;  // of all requests: runs_value_split
+constexpr int kShortKeys = 512;      // requests that a call with group scales does not split
 constexpr int kMaxSegments = 64;
 constexpr int kSparseTile = 64;
 constexpr int64_t kRowsNMax = 128;  // query rows per request the rows-as-N kernel takes (a CTA pair)
@@ -131,8 +132,10 @@ int64_t value_split_ctas(const mla_plan_t* plan) {
 // kernel the plan names for the same problem with one scale:
 // * of a rows-as-N plan, tiles of more than 64 rows, and of more than 16 in a
 //   call of one wave over short requests (32 x 512 keys, 64 heads: 15.8 us
-//   against 25.7, 48 heads 22.1; 16 heads 15.0; over long ones the rows-as-N
-//   kernel is ahead: 52 x 16384 keys, 48 heads 121 us against 186);
+//   against 25.7, 48 heads 22.1; 16 heads 15.0) or over few keys (1 x 32768, 32
+//   heads: 32 us against 57, 16 x 2048: 22 and 23; over more the rows-as-N kernel
+//   is ahead: 16 x 4096, 32 heads 32 us against 28, 52 x 16384, 48 heads 186
+//   against 121);
 // * of a warp-MMA plan (sparse lists, block sizes that are not a multiple of 64)
 //   all but one row group of 16 over at most two of its chunks of 64 keys: 2
 //   requests of 128 keys, 16 heads take 10.8 us there and 11.5 here, of 192 keys
@@ -145,7 +148,8 @@ bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
   const bool asked = p.kernel != MLA_KERNEL_AUTO;
   if (plan->kernel == mla::kTcRowsN) {
     const bool one_wave = plan->schedule == 1 && p.max_seq_len <= kShortKeys && value_split_ctas(plan) <= plan->num_sms;
-    return plan->tile_rows > 64 || (!asked && plan->tile_rows > 16 && one_wave);
+    const bool few_keys = plan->schedule == 1 && static_cast<int64_t>(p.max_seq_len) * p.num_reqs <= kFewKeys;
+    return plan->tile_rows > 64 || (!asked && plan->tile_rows > 16 && (one_wave || few_keys));
   }
   if (asked) return false;
   const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
@@ -318,6 +322,9 @@ mla::SchedParams sched_params(const mla_plan_t* plan, const Inputs& in, uint8_t*
   sp.n_items = reinterpret_cast<int32_t*>(ws + l.n_items);
   sp.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
   sp.workers = plan_workers(plan);
+  // (a rows-as-N plan of up to 64 rows has a worker an SM, the value-split kernel a pair)
+  if (plan->kernel == mla::kTcRowsN && plan->tile_rows <= 64 && runs_value_split(plan, in.kv_scales) && sp.workers > 1)
+    sp.workers /= 2;
   // workers run contiguous runs of items (the value-split kernel takes one
   // item a pair of CTAs, longest first, also under a rows-as-N plan)
   if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales))

@@ -1,7 +1,7 @@
 // merge.cu -- merge split-K segment partials into the output and a
 // natural-log LSE (rocm_aiter_mla_merge page, merge_mla_segments_triton).
 //
-// One warp per (token, head). The token's partition length and the tile size
+// One warp per (token, head), or four. The token's partition length and the tile size
 // give the segments that exist (start < len, tiles_per_segment =
 // cdiv(len, NS * tile)); of those, segments with expsum > 0 contribute.
 // Under the balanced schedule the row's pieces come from the unit table
@@ -41,10 +41,14 @@ __device__ __forceinline__ int part_len_of(const PartLens& pl, int t) {
   }
 }
 
-template <int VPL>  // float4 values per lane: rank / 128
+// A row's rank / 128 float4 values per lane, by one warp or (SLICED, few rows)
+// a fourth each by the block's four warps.
+template <int WIDTH, bool SLICED>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5);
+  constexpr int VPL = SLICED ? WIDTH / kWarpsPerBlock : WIDTH;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t gw = SLICED ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + warp;
+  const int slice = SLICED ? warp : 0;
   const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   if (gw >= total) return;
   const int t = static_cast<int>(gw / p.num_heads);
@@ -71,8 +75,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
       e = reinterpret_cast<const int2*>(p.unit_tab)[static_cast<int64_t>(u) * p.tiles_max + r / tr];
     if (e.y <= 1) return;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    merge_row<VPL, true>(p.segm_out, p.segm_max, p.segm_expsum, static_cast<int64_t>(e.x) * tr + r % tr,
-                         tr, e.y, sink2, out, p.lse + gw, lane);
+    merge_row<VPL, WIDTH, true>(p.segm_out, p.segm_max, p.segm_expsum, static_cast<int64_t>(e.x) * tr + r % tr,
+                         tr, e.y, sink2, out, p.lse + gw, lane, slice);
     return;
   }
   // uniform partition: an ordinary launch (the wait is a no-op)
@@ -83,8 +87,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
   const int tps = len > 0 ? cdiv(len, span) : 0;
   const int seg = tps * p.tile_size;
   const int live = len > 0 ? min(NS, cdiv(len, seg)) : 0;
-  merge_row<VPL, false>(p.segm_out, p.segm_max, p.segm_expsum, gw * NS, 1, live, sink2, out, p.lse + gw,
-                        lane);
+  merge_row<VPL, WIDTH, false>(p.segm_out, p.segm_max, p.segm_expsum, gw * NS, 1, live, sink2, out, p.lse + gw,
+                        lane, slice);
 }
 
 // Natural-log (out, lse) pairs of W key shards of the same rows: weights
@@ -162,7 +166,12 @@ cudaError_t launch_merge_lse(const LseMergeParams& p, cudaStream_t stream) {
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   const int64_t warps = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   if (warps == 0) return cudaSuccess;
-  const unsigned blocks = static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock);
+  // four warps a row while the rows are few: a warp alone is bound by the round
+  // trips of a row's partials (the whole call over 1 request of 32768 keys, e4m3
+  // with group scales, 32 heads: 95 us by one warp that also read the partials'
+  // weights in turn, 57 so)
+  const bool sliced = p.rank == 512 && warps <= 512;
+  const unsigned blocks = static_cast<unsigned>(sliced ? warps : (warps + kWarpsPerBlock - 1) / kWarpsPerBlock);
   if (p.unit_tab != nullptr) {
     // balanced schedule: programmatic dependent launch after the decode, so
     // that the grid is in place when the decode completes
@@ -176,12 +185,18 @@ cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_kernel<4>, p);
+    return sliced ? cudaLaunchKernelEx(&cfg, merge_kernel<4, true>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<4, false>, p);
   }
   switch (p.rank / 128) {
-    case 1: merge_kernel<1><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p); break;
-    case 2: merge_kernel<2><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p); break;
-    case 4: merge_kernel<4><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p); break;
+    case 1: merge_kernel<1, false><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p); break;
+    case 2: merge_kernel<2, false><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p); break;
+    case 4:
+      if (sliced)
+        merge_kernel<4, true><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p);
+      else
+        merge_kernel<4, false><<<blocks, kWarpsPerBlock * 32, 0, stream>>>(p);
+      break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

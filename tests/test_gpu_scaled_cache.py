@@ -750,3 +750,10 @@ def test_decode_short_requests(heads, qlens, longest, sinks):
     check_decode(c)
     check_decode(c, stages=True)
     check_decode(decode_case(52, [33] * 40 + [100] * 40 + [0] * 80, heads, 64, 64, sinks=sinks))
+
+
+@pytest.mark.parametrize("heads,qlens", [(1, None), (16, None), (32, [2]), (128, None), (128, [3])])
+def test_decode_one_long_request(heads, qlens):
+    """A row of many partials: more than 40 pieces, merged by four warps a row."""
+    check_decode(decode_case(61, [19999], heads, 64, 64, qlens=qlens, sinks=True))
+    check_decode(decode_case(62, [9001, 1], heads, 16, 8, qlens=None if qlens is None else qlens + [1]), num_segments=40)

@@ -450,9 +450,11 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * sparse slot lists, sinks, the balanced schedule or a fixed num_segments,
  * the workspace and its status word. The plan is one for kv_dtype =
  * MLA_DTYPE_FP8_E4M3. Row tiles of more than 64 rows that it gives to a
- * tensor-core kernel, and most of what it gives to the warp-MMA kernel without
- * being asked to, run on a kernel of their own here, in the same workspace;
- * where the planner chose the number of segments, that kernel may use fewer. A sink of -inf counts as none.
+ * tensor-core kernel (of more than 16 over few keys), and most of what it gives
+ * to the warp-MMA kernel without being asked to, run on a kernel of their own
+ * here, in the same workspace; where the planner chose the number of segments,
+ * that kernel may use fewer, and a whole call over few short requests may leave
+ * a balanced plan's schedule and merge out. A sink of -inf counts as none.
  * A weight times its scale enters the product with the codes rounded to 7 bits
  * or more, below 2^-10 of the row's largest to 3 or more, and is off by 2^-19 of
  * the largest at most where it is smaller still.

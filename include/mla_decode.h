@@ -39,7 +39,8 @@
  *     are 576 elements; q, kv_cache and out must be 16-byte aligned,
  *     workspace 256-byte aligned, lse and the float/int arrays 4-byte aligned.
  *   - Values the host cannot see (block-table entries, seq_lens, slots) are
- *     trusted to be in range: block_table entries in [0, num_blocks),
+ *     trusted to be in range: block_table entries in [0, num_blocks) (over a
+ *     cache with group scales also below 0: no block),
  *     0 <= seq_lens[r] <= max_blocks_per_req * block_size, seq_lens[r] >=
  *     qlen_r, slots in [-1, num_blocks * block_size).
  */
@@ -455,6 +456,8 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * here, in the same workspace; where the planner chose the number of segments,
  * that kernel may use fewer, and a whole call over few short requests may leave
  * a balanced plan's schedule and merge out. A sink of -inf counts as none.
+ * Keys of a negative block_table entry are skipped, as unused list entries are:
+ * mla_block_tables leaves -1 where the free list was too short (*taken tells).
  * A weight times its scale enters the product with the codes rounded to 7 bits
  * or more, below 2^-10 of the row's largest to 3 or more, and is off by 2^-19 of
  * the largest at most where it is smaller still.

@@ -570,7 +570,9 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
 #pragma unroll
     for (int n = 0; n < NH; ++n) l[n] = 0.f;
     // GS: the cache row of this thread's key two chunks ahead and the scale
-    // of its group one chunk ahead, so that neither read is waited for
+    // of its group one chunk ahead, so that neither read is waited for. A
+    // negative row is a key past the segment or of a table cell without a
+    // block (whose box TMA fills with zeros): there is none.
     const int32_t* bt_row = p.block_table + static_cast<int64_t>(it.unit) * p.bt_stride;
     auto key_row = [&](int ch) {
       const int kp = it.seg_start + ch * kKeys + k;
@@ -581,15 +583,20 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
     };
     float sc_next = 1.f;
     int row_next = -1;
+    bool here_next = false;
     if constexpr (GS) {
-      sc_next = row_scale(key_row(0));
+      const int row = key_row(0);
+      sc_next = row_scale(row);
+      here_next = row >= 0;
       row_next = key_row(1);
     }
     for (int c = 0; c < it.n_chunks && ok; ++c, ++g) {
       KeyScale kq{};
+      const bool here = here_next;  // (GS)
       if constexpr (GS) {
         kq = key_scale(sc_next, scale2);
         sc_next = row_scale(row_next);
+        here_next = row_next >= 0;
         row_next = key_row(c + 2);
       }
       const int b = g & 1;
@@ -607,13 +614,14 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
 #pragma unroll
         for (int n = 0; n < NH; ++n) s[n] = fmaf(s[n], kq.mul, kq.add);
       }
-      // keys that exist (inside the segment) and that each row may see; a
-      // chunk inside the segment and before every row's causal end needs no mask
+      // keys that exist (inside the segment; GS: in a block) and that each row
+      // may see; a chunk inside the segment and before every row's causal end
+      // needs no mask
       const int pos = it.seg_start + c * kKeys + k;
-      const bool key_ok = pos < it.seg_end;
+      const bool key_ok = GS ? here : pos < it.seg_end;
       const int chunk_end = it.seg_start + (c + 1) * kKeys;
       const bool causal = it.qlen > 1 && chunk_end > vis_min;
-      if (chunk_end > it.seg_end || causal) {
+      if ((GS ? !__all_sync(0xffffffffu, here) : chunk_end > it.seg_end) || causal) {
 #pragma unroll
         for (int n = 0; n < NH; ++n)
           if (!(key_ok && (!causal || pos < vis[r0 + n]))) s[n] = -INFINITY;
@@ -720,7 +728,7 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
         *reinterpret_cast<uint2*>(dst + (NR / 16) * 128) = make_uint2(lw[0], lw[1]);
       }
       if (!key_ok) {
-        // a key past the segment: its value row (stale or unloaded ring
+        // a key that does not exist: its value row (stale or unloaded ring
         // contents, or cache rows past the sequence) must not reach O^T
         // through p = 0, so it is zeroed; each row half zeroes two of the
         // chunk's four value boxes

@@ -230,7 +230,8 @@ __device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code
   }
 }
 
-// Cache slot of key position pos (-1 past the segment or for an unused list entry).
+// Cache slot of key position pos (-1 past the segment; negative for an unused list
+// entry and where the table has no block).
 template <bool LIST>
 __device__ __forceinline__ int key_slot(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int pos) {
   if (pos >= x.seg_end) return -1;
@@ -316,13 +317,14 @@ __device__ __forceinline__ void copy_rows(const Ctx& x, const DecodeParams& p, i
 }
 
 // Cache rows of the 64-key halves of a dense request's chunks: looked up by
-// the whole warp, 16 chunks at a time and a window ahead.
+// the whole warp, 16 chunks at a time and a window ahead. A half past the end or
+// without a block has row -64, whose box is filled with zeros.
 struct RowWindow {
   int cur, nxt;
   __device__ __forceinline__ void load(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int w0, int& v) {
     const int s =
         key_slot<false>(x, p, bt_row, x.seg_start + (w0 + (x.lane >> 1)) * kKeys + (x.lane & 1) * kHalf);
-    v = s < 0 ? 0 : s;
+    v = s < 0 ? -kHalf : s;
   }
   __device__ __forceinline__ void start(const Ctx& x, const DecodeParams& p, const int32_t* bt_row) {
     load(x, p, bt_row, 0, cur);
@@ -402,6 +404,7 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
   RowWindow w;
   w.start(x, p, bt_row);
   float sc[4];
+  uint32_t bits = 0u;  // lane i < 4: the keys of part i that exist
   auto read = [&](int g) {  // 1 for keys that do not exist
     w.at(x, p, bt_row, g);
     const int row0 = w.row(g, 0), row1 = w.row(g, 1);
@@ -409,13 +412,14 @@ __device__ void scales_dense(const Ctx& x, const DecodeParams& p) {
 #pragma unroll
     for (int i = 0; i < (UNI ? 1 : 4); ++i) {
       const int j = UNI ? kUni * lane : 32 * i + lane;
-      sc[i] = j < n && j < kKeys ? scale_of_slot(p, (j < kHalf ? row0 : row1) + (j & (kHalf - 1))) : 1.f;
+      const int row = j < kHalf ? row0 : row1;
+      sc[i] = j < n && j < kKeys && row >= 0 ? scale_of_slot(p, row + (j & (kHalf - 1))) : 1.f;
     }
+    const int left = (lane < 2 ? row0 : row1) >= 0 ? n - 32 * lane : 0;
+    bits = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
   };
   if (x.n_chunks > 0) read(0);
   for (int g = 0; g < x.n_chunks; ++g) {
-    const int n = x.seg_end - (x.seg_start + g * kKeys) - 32 * lane;
-    const uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
     if (!post_scales<UNI>(x, p, g, sc, bits)) break;
     if (g + 1 < x.n_chunks) read(g + 1);
   }

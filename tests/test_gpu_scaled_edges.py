@@ -1,0 +1,150 @@
+"""The serving step over a cache with group scales at its edges: table cells
+without a block, rows behind the last request, sinks and keys that are no
+numbers, work lists shared between calls, and every kernel a scaled call can
+run on, each against the oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scaled_oracle as S
+from paged_mla_decode_06_gb300 import binding as B
+from paged_mla_decode_06_gb300 import build as BUILD
+from paged_mla_decode_06_gb300 import inputs as I
+from tests.test_gpu_scaled_cache import QS, SCALE, compare, decode_case, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    BUILD.build()
+    B.load_library()
+
+
+class Call:
+    """A decode over the case's tensors. ``bound``: the host's bound of the
+    lengths, where it is not the longest; ``behind``: rows of q, out and lse
+    past the last request."""
+
+    def __init__(self, c, bound=None, behind=0, num_segments=0, kernel=B.MLA_KERNEL_AUTO):
+        self.c = c
+        table = c["table"]
+        if bound is not None:  # columns that no request fills
+            cols = max(table.shape[1], -(-bound // c["bs"]))
+            table = np.concatenate([table, np.full((len(table), cols - table.shape[1]), table[0, -1])], 1)
+        T = c["T"] + behind
+        self.plan = B.mla_decode_plan(B.make_problem(
+            num_tokens=T, num_heads=c["H"], block_size=c["bs"], num_blocks=c["nb"], num_reqs=len(c["lens"]),
+            max_blocks_per_req=table.shape[1], max_seq_len=int(bound if bound is not None else c["lens"].max()),
+            max_qlen=c["max_qlen"], dtype="fp8", has_sinks=c["sinks"] is not None, num_segments=num_segments,
+            kernel=kernel))
+        q = np.concatenate([c["q"], np.full((behind, c["H"], 576), 0x7F, np.uint8)])
+        self.args = (self.plan, dev(q), dev(c["codes"]).view(c["nb"], c["bs"], 576))
+        self.scales = dev(c["scales"], np.float32)
+        self.seq = dev(c["lens"], np.int32)
+        self.qo = None if c["qo"] is None else dev(c["qo"], np.int32)
+        self.sinks = None if c["sinks"] is None else dev(c["sinks"])
+        self.ws = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        self.out = torch.empty((T, c["H"], 512), dtype=torch.bfloat16, device="cuda")
+        self.lse = torch.empty((T, c["H"]), device="cuda")
+        self.kw = dict(block_table=dev(table, np.int32), seq_lens=self.seq, qo_indptr=self.qo, softmax_scale=SCALE,
+                       q_scale=QS, sinks=self.sinks, workspace=self.ws, out=self.out, lse=self.lse)
+
+    def clear(self):
+        self.out.fill_(-7.0)
+        self.lse.fill_(-7.0)
+
+    def result(self):
+        torch.cuda.synchronize()
+        assert B.mla_workspace_status(self.plan, self.ws) == 0
+        return self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
+
+    def schedule(self):
+        B.mla_decode_schedule(self.plan, seq_lens=self.seq, qo_indptr=self.qo, workspace=self.ws)
+
+    def merge(self):
+        B.mla_merge_items(self.plan, qo_indptr=self.qo, sinks=self.sinks, workspace=self.ws, out=self.out, lse=self.lse)
+
+    def fwd_scaled(self):
+        self.clear()
+        B.mla_decode_fwd_scaled(*self.args, self.scales, scale_group=self.c["g"], **self.kw)
+        return self.result()
+
+    def stages_scaled(self):
+        self.clear()
+        self.schedule()
+        B.mla_decode_items_scaled(*self.args, self.scales, scale_group=self.c["g"], **self.kw)
+        self.merge()
+        return self.result()
+
+    def items(self, kv_scale):
+        """The unscaled decode over the list in the workspace, and its merge."""
+        self.clear()
+        B.mla_decode_items(*self.args, kv_scale=kv_scale, **self.kw)
+        self.merge()
+        return self.result()
+
+
+def reference(c):
+    lists = S.token_slots(c["table"], c["lens"], c["bs"], c["qo"])
+    return S.decode(c["q"], QS, c["codes"], c["scales"], c["g"], lists, SCALE, c["sinks"], bounds=True)
+
+
+# (heads, block size, group, tokens of the requests): the rows-as-N kernel at
+# 16 rows, the value-split kernel with shared scales and with one a key, over
+# blocks that boxes do not fit, and the warp-MMA kernel
+SHAPES = [(16, 64, 64, None), (16, 128, 1, [2, 1, 3, 1, 2]), (48, 64, 16, None), (128, 64, 64, None), (128, 128, 1, None),
+          (128, 64, 16, [2, 3, 1, 1, 2]), (128, 48, 24, None), (16, 16, 16, None)]
+
+
+@pytest.mark.parametrize("heads,bs,g,qlens", SHAPES)
+@pytest.mark.parametrize("bound", [None, 60000])
+def test_keys_without_a_block_are_skipped(heads, bs, g, qlens, bound):
+    """Cells below 0 in the middle, at either end and over all of a request's
+    columns, as a free list that was too short leaves them: no key of theirs
+    counts, and none of another request's is read in their place."""
+    c = decode_case(71, [300, 2 * bs, 700, 5000, 65], heads, bs, g, qlens=qlens, sinks=heads == 48)
+    t = c["table"]
+    t[0, 1] = -1
+    t[1, :2] = -1
+    t[2, 0] = t[2, -(-700 // bs) - 1] = -1
+    t[3, [3, 4, 5, 20]] = -1
+    t[3, 7] = -5
+    call = Call(c, bound=bound)
+    compare(*call.fwd_scaled(), *reference(c))
+    if call.plan.schedule == 1:
+        compare(*call.stages_scaled(), *reference(c))
+
+
+def test_a_step_on_a_short_free_list():
+    """Tables, append and decode of one step on one stream, three blocks short:
+    the tokens without a slot are not written and not attended to."""
+    rng = np.random.default_rng(72)
+    R, cols, nb, bs, g, H = 3, 8, 16, 64, 64, 128
+    q = np.array([200, 150, 100])
+    qsl, T = np.concatenate([[0], np.cumsum(q)]), int(q.sum())
+    free = rng.permutation(nb)[:6]                          # of the nine that the step takes
+    rows = torch.from_numpy(rng.standard_normal((T, 576)).astype(np.float32)).bfloat16()
+    table, slots, _, _, taken = S.block_tables(qsl, q, free, np.full((R, cols), -1), bs, T)
+    codes, scales = S.cache_append(rows.double().numpy(), slots, np.full((nb * bs, 576), 0x7F, np.uint8), np.full(nb, np.nan), g)
+    kv, d_table = rows.cuda(), dev(np.full((R, cols), -1), np.int32)
+    cache, sc = dev(np.full((nb, bs, 576), 0x7F, np.uint8)), dev(np.full(nb, np.nan), np.float32)
+    d_qsl, d_lens = dev(qsl, np.int32), dev(q, np.int32)
+    d_slots, d_taken = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    plan = B.mla_decode_plan(B.make_problem(num_tokens=T, num_heads=H, block_size=bs, num_blocks=nb, num_reqs=R,
+                                            max_blocks_per_req=cols, max_seq_len=cols * bs, max_qlen=200, dtype="fp8"))
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    qc = I.float32_to_e4m3_codes(rng.standard_normal((T, H, 576)).astype(np.float32) / QS)
+    out, lse = torch.empty((T, H, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((T, H), device="cuda")
+    B.mla_block_tables(d_qsl, d_lens, dev(free, np.int32), d_table, block_size=bs, slot_mapping=d_slots, taken=d_taken)
+    B.mla_cache_append(kv[:, :512], kv[:, 512:], d_slots, cache, sc, scale_group=g)
+    B.mla_decode_fwd_scaled(plan, dev(qc), cache, sc, scale_group=g, block_table=d_table, seq_lens=d_lens, qo_indptr=d_qsl,
+                            softmax_scale=SCALE, q_scale=QS, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert int(d_taken[0]) == taken == 9 and np.array_equal(d_table.cpu().numpy(), table)
+    pick = np.concatenate([np.arange(0, T, 37), [T - 1]])   # (the oracle at 450 tokens x 128 heads is slow)
+    lists = S.token_slots(table, q, bs, qsl)
+    compare(out.double().cpu().numpy()[pick], lse.double().cpu().numpy()[pick],
+            *S.decode(qc[pick], QS, codes, scales, g, [lists[t] for t in pick], SCALE, bounds=True))

@@ -229,8 +229,10 @@ MLA_API mla_status_t mla_decode_plan(const mla_problem_t* prob, mla_plan_t* plan
  *                with mla_workspace_status). The rest needs no
  *                initialisation.
  *   out          [T, H, 512] bf16; lse [T, H] fp32 natural log. Every element
- *                is written; a row with no visible key gets out = 0 and
- *                lse = -inf (or its sink).
+ *                of a request's rows is written; a row with no visible key
+ *                gets out = 0 and lse = -inf (or its sink). Tokens before
+ *                qo_indptr[0] or at or past qo_indptr[R] (the padding of a
+ *                captured batch) are left as they were.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
  */
 MLA_API mla_status_t mla_decode_fwd(const mla_plan_t* plan, const void* q, const void* kv_cache,

@@ -6,7 +6,8 @@
 // cdiv(len, NS * tile)); of those, segments with expsum > 0 contribute.
 // Under the balanced schedule the row's pieces come from the unit table
 // instead, and rows whose unit was not split are left as the decode kernel
-// wrote them.
+// wrote them; so are rows of no request (a padded batch), which have no
+// partials.
 // Pass 1 reads the base-2 maxima, pass 2 streams each live segment's
 // normalised output coalesced (lane i reads float4 i, i + 32, ...) and
 // accumulates it with weight l_s * 2^(m2_s - M). The sink logit, when given,
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
   if (gw >= total) return;
   const int t = static_cast<int>(gw / p.num_heads);
   const int h = static_cast<int>(gw % p.num_heads);
+  if (p.part.qo_indptr != nullptr && (t < p.part.qo_indptr[0] || t >= p.part.qo_indptr[p.part.num_reqs])) return;
   const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + gw * p.rank;
   if (p.unit_tab != nullptr) {

@@ -25,26 +25,27 @@ def _lib():
 
 class Call:
     """A decode over the case's tensors. ``bound``: the host's bound of the
-    lengths, where it is not the longest; ``behind``: rows of q, out and lse
-    past the last request."""
+    lengths, where it is not the longest; ``ahead`` and ``behind``: rows of q,
+    out and lse before the first request and past the last."""
 
-    def __init__(self, c, bound=None, behind=0, num_segments=0, kernel=B.MLA_KERNEL_AUTO):
+    def __init__(self, c, bound=None, ahead=0, behind=0, num_segments=0, kernel=B.MLA_KERNEL_AUTO):
         self.c = c
         table = c["table"]
         if bound is not None:  # columns that no request fills
             cols = max(table.shape[1], -(-bound // c["bs"]))
             table = np.concatenate([table, np.full((len(table), cols - table.shape[1]), table[0, -1])], 1)
-        T = c["T"] + behind
+        T = ahead + c["T"] + behind
         self.plan = B.mla_decode_plan(B.make_problem(
             num_tokens=T, num_heads=c["H"], block_size=c["bs"], num_blocks=c["nb"], num_reqs=len(c["lens"]),
             max_blocks_per_req=table.shape[1], max_seq_len=int(bound if bound is not None else c["lens"].max()),
             max_qlen=c["max_qlen"], dtype="fp8", has_sinks=c["sinks"] is not None, num_segments=num_segments,
             kernel=kernel))
-        q = np.concatenate([c["q"], np.full((behind, c["H"], 576), 0x7F, np.uint8)])
+        q = np.concatenate([np.full((n, c["H"], 576), 0x7F, np.uint8) if x is None else x
+                            for n, x in ((ahead, None), (0, c["q"]), (behind, None))])
         self.args = (self.plan, dev(q), dev(c["codes"]).view(c["nb"], c["bs"], 576))
         self.scales = dev(c["scales"], np.float32)
         self.seq = dev(c["lens"], np.int32)
-        self.qo = None if c["qo"] is None else dev(c["qo"], np.int32)
+        self.qo = None if c["qo"] is None else dev(c["qo"] + ahead, np.int32)
         self.sinks = None if c["sinks"] is None else dev(c["sinks"])
         self.ws = torch.zeros(self.plan.workspace_bytes, dtype=torch.uint8, device="cuda")
         self.out = torch.empty((T, c["H"], 512), dtype=torch.bfloat16, device="cuda")
@@ -148,3 +149,21 @@ def test_a_step_on_a_short_free_list():
     lists = S.token_slots(table, q, bs, qsl)
     compare(out.double().cpu().numpy()[pick], lse.double().cpu().numpy()[pick],
             *S.decode(qc[pick], QS, codes, scales, g, [lists[t] for t in pick], SCALE, bounds=True))
+
+
+# ---------------------------------------------------------------- rows of no request
+
+@pytest.mark.parametrize("heads,bs,ns,bound", [(16, 64, 0, None), (16, 64, 0, 60000), (128, 64, 0, None), (128, 64, 3, None),
+                                               (16, 64, 3, None), (16, 16, 0, None), (128, 48, 2, None)])
+@pytest.mark.parametrize("ahead", [0, 2])
+def test_rows_of_no_request_stay_as_they_were(heads, bs, ns, bound, ahead):
+    """A padded batch: the last request, split into pieces, has fewer tokens
+    than the longest, and the tensors more rows than there are tokens."""
+    c = decode_case(73, [9000, 900, 9000], heads, bs, 16, qlens=[1, 3, 1], sinks=True)
+    call = Call(c, ahead=ahead, behind=4, num_segments=ns, bound=bound)
+    mine = slice(ahead, ahead + c["T"])
+    other = np.r_[0:ahead, ahead + c["T"]:ahead + c["T"] + 4]
+    for run in (call.fwd_scaled,) + ((call.stages_scaled,) if call.plan.schedule == 1 else ()):
+        out, lse = run()
+        assert (out[other] == -7.0).all() and (lse[other] == -7.0).all()
+        compare(out[mine], lse[mine], *reference(c))

@@ -327,8 +327,12 @@ mla::SchedParams sched_params(const mla_plan_t* plan, const Inputs& in, uint8_t*
     sp.workers /= 2;
   // workers run contiguous runs of items (the value-split kernel takes one
   // item a pair of CTAs, longest first, also under a rows-as-N plan)
-  if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales))
+  if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales)) {
     sp.worker_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
+  } else if (plan->kernel == mla::kTcRowsN) {
+    sp.even_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
+    sp.even_workers = plan_workers(plan);
+  }
   return sp;
 }
 

@@ -73,6 +73,11 @@ struct SchedParams {
   // worker_first[w] ([workers + 1]); else longest first for one-item CTAs
   int32_t* worker_first;
   int32_t workers;               // the share of the groups is cdiv(total, workers)
+  // a list that is not contiguous, in a workspace whose plan has workers: their
+  // first items ([even_workers + 1], null: no such workers), the list dealt
+  // evenly in its order, so that it also serves the kernel that runs by workers
+  int32_t* even_first;
+  int32_t even_workers;
 };
 
 cudaError_t launch_schedule(const SchedParams& p, cudaStream_t stream);

@@ -36,6 +36,12 @@
 // written in sequence order with worker_first[w] = the first item of worker
 // w (a piece belongs to the worker its first group falls to; an empty row,
 // to the worker of its position).
+//
+// A longest-first list in the workspace of such a plan (the value-split kernel
+// runs it, over a cache with group scales) is dealt evenly to the plan's
+// workers: worker_first is right for the list that is there, whichever call
+// wrote it. (Left over from another list, it would have the rows-as-N kernel
+// leave items out.)
 #include "common.cuh"
 #include "internal.h"
 
@@ -139,6 +145,13 @@ __device__ int unit_bounds(I a, int g, int T, I W, F f) {
   return c.count;
 }
 
+// Deals n items evenly to the workers of the plan, where it has any.
+__device__ void deal_items(const SchedParams& p, long long n) {
+  if (p.even_first == nullptr) return;
+  for (int w = threadIdx.x; w <= p.even_workers; w += kThreads)
+    p.even_first[w] = static_cast<int32_t>(n * w / p.even_workers);
+}
+
 // The histogram, the ranking and the items, with positions of type I. The
 // T items of a piece (one per row tile) are written next to each other, so
 // that the CTA pairs that read the same keys start together and the keys
@@ -229,6 +242,7 @@ __device__ void schedule_items(const SchedParams& p, Info info, I W, long long* 
     }
   }
   n_items = block_sum(n_items, red);
+  deal_items(p, n_items);
   if (tid == 0) *p.n_items = static_cast<int32_t>(n_items);
 }
 
@@ -356,6 +370,7 @@ __device__ bool schedule_items_small(const SchedParams& p, UnitInfo i, I W, long
       it[1] = make_int4(km > 1 ? slot0 + t * km + me.w : -1, 0, 0, 0);
     }
   }
+  deal_items(p, tot.z);
   if (tid == 0) *p.n_items = tot.z;
   return true;
 }

@@ -10,6 +10,7 @@ from oracle import scaled_oracle as S
 from paged_mla_decode_06_gb300 import binding as B
 from paged_mla_decode_06_gb300 import build as BUILD
 from paged_mla_decode_06_gb300 import inputs as I
+from tests.gpu_helpers import assert_close
 from tests.test_gpu_scaled_cache import QS, SCALE, compare, decode_case, dev
 
 pytestmark = pytest.mark.gpu
@@ -167,3 +168,25 @@ def test_rows_of_no_request_stay_as_they_were(heads, bs, ns, bound, ahead):
         out, lse = run()
         assert (out[other] == -7.0).all() and (lse[other] == -7.0).all()
         compare(out[mine], lse[mine], *reference(c))
+
+
+# ---------------------------------------------------------------- a list in a shared workspace
+
+@pytest.mark.parametrize("heads,qlens", [(48, None), (128, None), (16, [3, 2, 2, 3, 1]), (16, None)])
+def test_the_unscaled_items_run_over_the_list_of_a_scaled_call(heads, qlens):
+    """One list serves any number of calls: the one that a scaled whole call
+    leaves in the workspace is as good for mla_decode_items as that of
+    mla_decode_schedule, before it or not. Rows that are split and rows that
+    are not; no partial of the scaled call is left."""
+    c = decode_case(74, [1500, 6500, 100, 2500, 64], heads, 64, 64, qlens=qlens)
+    c["scales"][:] = 2.0 ** -7                              # values of about unit variance, as assert_close has them
+    ref = reference(c)
+    seen = np.array([len(s) for s in S.token_slots(c["table"], c["lens"], c["bs"], c["qo"])])
+    for scheduled in (False, True):
+        call = Call(c)
+        assert call.plan.schedule == 1 and call.plan.kernel == 5
+        if scheduled:
+            call.schedule()
+        compare(*call.fwd_scaled(), *ref)
+        call.ws[call.plan.segm_output_offset:] = 0xFF       # NaN
+        assert_close(*call.items(2.0 ** -7), *ref[:2], "fp8", f"scheduled {scheduled}", keys=seen)

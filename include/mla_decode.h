@@ -457,7 +457,8 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * to the warp-MMA kernel without being asked to, run on a kernel of their own
  * here, in the same workspace; where the planner chose the number of segments,
  * that kernel may use fewer, and a whole call over few short requests may leave
- * a balanced plan's schedule and merge out. A sink of -inf counts as none.
+ * a balanced plan's schedule and merge out. A sink of -inf counts as none, one
+ * that is NaN makes its head's rows NaN.
  * Keys of a negative block_table entry are skipped, as unused list entries are:
  * mla_block_tables leaves -1 where the free list was too short (*taken tells).
  * A weight times its scale enters the product with the codes rounded to 7 bits

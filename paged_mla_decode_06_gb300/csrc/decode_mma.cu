@@ -431,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
         const float s2 = p.sinks[head] * kLog2e;
         const float M = fmaxf(m, s2);
         const float wk = L > 0.f ? L * exp2f(m - M) : 0.f;
-        const float W = wk + (s2 > -INFINITY ? exp2f(s2 - M) : 0.f);  // (-inf: no sink)
+        const float W = wk + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));  // (-inf: no sink; NaN stays)
         mult = L > 0.f ? exp2f(m - M) / W : 0.f;
-        lse = W > 0.f ? kLn2 * (M + log2f(W)) : -INFINITY;
+        lse = W != 0.f ? kLn2 * (M + log2f(W)) : -INFINITY;
       } else if (L > 0.f) {
         mult = 1.f / L;
         lse = kLn2 * (m + log2f(L));

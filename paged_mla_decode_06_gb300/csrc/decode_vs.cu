@@ -847,8 +847,8 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
         const float s2 = p.sinks[head] * kLog2e;
         const float M = fmaxf(L > 0.f ? base : -INFINITY, s2);
         const float e = L > 0.f ? exp2f(base - M) : 0.f;
-        const float W = L * e + (s2 > -INFINITY ? exp2f(s2 - M) : 0.f);  // (-inf: no sink)
-        if (W > 0.f) {
+        const float W = L * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));  // (-inf: no sink; NaN stays)
+        if (W != 0.f) {
           mult = e / W;
           lse = kLn2 * (M + log2f(W));
         }

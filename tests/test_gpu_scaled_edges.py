@@ -190,3 +190,29 @@ def test_the_unscaled_items_run_over_the_list_of_a_scaled_call(heads, qlens):
         compare(*call.fwd_scaled(), *ref)
         call.ws[call.plan.segm_output_offset:] = 0xFF       # NaN
         assert_close(*call.items(2.0 ** -7), *ref[:2], "fp8", f"scheduled {scheduled}", keys=seen)
+
+
+# ---------------------------------------------------------------- values that are no numbers
+
+@pytest.mark.parametrize("heads,bs,lens", [(16, 64, [0, 40, 9000]), (128, 64, [0, 40, 9000]), (16, 16, [0, 40, 300])])
+@pytest.mark.parametrize("scaled", [True, False])
+def test_a_sink_that_is_no_number_is_not_dropped(heads, bs, lens, scaled):
+    """Its head is NaN in every row, split or not; the other heads keep their
+    bits."""
+    c = decode_case(75, lens, heads, bs, 16, sinks=True)
+    got = []
+    for sink in (0.5, np.nan):
+        c["sinks"][5] = sink
+        call = Call(c)
+        call.clear()
+        if scaled:
+            got.append(call.fwd_scaled())
+        else:
+            B.mla_decode_fwd(*call.args, kv_scale=0.125, **call.kw)
+            got.append(call.result())
+    (out0, lse0), (out, lse) = got
+    assert np.isfinite(out0).all() and np.isfinite(lse0).all()
+    assert np.isnan(lse[:, 5]).all()
+    assert np.isnan(out[1:, 5]).all()                       # (0 x NaN where there is no key: unspecified)
+    rest = np.arange(heads) != 5
+    assert np.array_equal(out[:, rest], out0[:, rest]) and np.array_equal(lse[:, rest], lse0[:, rest])

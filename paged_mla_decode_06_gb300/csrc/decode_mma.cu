@@ -376,6 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       o[n][2] *= alpha[1];
       o[n][3] *= alpha[1];
     }
+    if constexpr (GS) {
+      // values of keys that only the later tokens of the tile see (S is complete)
+      const int lo = part_len - qlen + row0 / H + 1 - c0;
+      if (qlen > 1 && lo < C::kKC) {
+        for (int i = max(lo, 0) * 64 + tid; i < C::kKC * 64; i += kThreads) {
+          uint4* v = reinterpret_cast<uint4*>(smem + C::kOffCompute + i / 64 * (kQStride * 2) + i % 64 * 16);
+          const uint4 w = *v;
+          *v = make_uint4(f16x2_without_nan(w.x), f16x2_without_nan(w.y), f16x2_without_nan(w.z), f16x2_without_nan(w.w));
+        }
+      }
+    }
     if (tid < C::kKC) key_slot[(c + C::kStages) % C::kSlotStages * C::kKC + tid] = ahead;
     __syncthreads();
 

@@ -573,7 +573,20 @@ __device__ void qk_issue(const Ctx& x, const VsMaps& maps) {
   __syncwarp();
 }
 
-__device__ void pv_issue(const Ctx& x) {
+// The own value rows of keys [first, end) of half-chunk g, without NaNs.
+__device__ __forceinline__ void drop_nans(const Ctx& x, int g, int first, int end) {
+  uint8_t* box = x.smem + box_of(g >> 1, 2, x.rank).off + (g & 1) * kHalf * 128;
+#pragma unroll 1
+  for (int i = first * 16 + x.lane; i < end * 16; i += 32) {
+    uint4* at = reinterpret_cast<uint4*>(box + ((i >> 3) & 1) * kSlot + (i >> 4) * 128 + (i & 7) * 16);
+    const uint4 v = *at;
+    *at = make_uint4(e4m3x4_without_nan(v.x), e4m3x4_without_nan(v.y), e4m3x4_without_nan(v.z), e4m3x4_without_nan(v.w));
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+__device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
   if (x.n_chunks == 0) return;
   constexpr uint32_t kIdHi = instr_desc(kRows, 256, 0, 0, false, true);
   constexpr uint32_t kIdLo = instr_desc(kRows, 256, 1, 0, false, true);
@@ -582,11 +595,11 @@ __device__ void pv_issue(const Ctx& x) {
   const uint32_t d = x.tbase + kTmemO;
   const bool one = elect_one();
   RingPos<kVChunks> vr;
-  for (int g = 0; g < x.n_half; ++g) {
+  auto step = [&](int g) {
     const int h = g & 1;
     const bool last = h == 1 || g + 1 == x.n_half;
     // P written; the softmax waited for S, whose Q K^T waited for these boxes
-    if (!warp_wait(x, x.bar(kPFull + h), (g >> 1) & 1, 24)) break;
+    if (!warp_wait(x, x.bar(kPFull + h), (g >> 1) & 1, 24)) return false;
     fence_after_sync();
     const uint64_t vb = v_desc + static_cast<uint64_t>((vr.at * 2 * kSlot + h * kHalf * 128) >> 4);
     const uint64_t pb = p_desc + static_cast<uint64_t>((h * 2 * kPTile) >> 4);
@@ -603,6 +616,24 @@ __device__ void pv_issue(const Ctx& x) {
     }
     __syncwarp();
     if (last) vr.next();
+    return true;
+  };
+  // keys before all_see are seen by every row of the tile; of those from it on a
+  // NaN must not reach the rows that do not see them through p = 0. (A loop of
+  // their own, from lengths read again: a test in the other loop cost 2 % of
+  // every call, the values kept in registers spilled the softmax's.)
+  const int qlen = p.qo_indptr != nullptr ? p.qo_indptr[x.unit + 1] - p.qo_indptr[x.unit] : 1;
+  const int all_see = qlen > 1 ? p.seq_lens[x.unit] - qlen + x.row0 / p.num_heads + 1 - x.seg_start : 0;
+  const int tail = qlen > 1 ? min(max(all_see, 0) / kHalf, x.n_half) : x.n_half;
+  bool ok = true;
+  for (int g = 0; g < tail && ok; ++g) ok = step(g);
+#pragma unroll 1
+  for (int g = tail; g < x.n_half && ok; ++g) {
+    ok = warp_wait(x, x.bar(kPFull + (g & 1)), (g >> 1) & 1, 24) &&
+         warp_wait(x, x.bar(kFull + vr.at), vr.phase, 39);  // (the box has landed; this shows its writes)
+    if (!ok) break;
+    drop_nans(x, g, max(all_see - g * kHalf, 0), min(x.seg_end - x.seg_start - g * kHalf, kHalf));
+    ok = step(g);
   }
   if (one) {
     mma_commit(x.bar(kDrainPV));
@@ -1063,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (x.warp == 1) {
     qk_issue(x, maps);
   } else if (x.warp == 3) {
-    pv_issue(x);
+    pv_issue(x, p);
   } else if (x.warp == 0) {
     if constexpr (KEYS == Keys::kBoxes)
       produce_dense(x, maps, p);

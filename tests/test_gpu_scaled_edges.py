@@ -216,3 +216,19 @@ def test_a_sink_that_is_no_number_is_not_dropped(heads, bs, lens, scaled):
     assert np.isnan(out[1:, 5]).all()                       # (0 x NaN where there is no key: unspecified)
     rest = np.arange(heads) != 5
     assert np.array_equal(out[:, rest], out0[:, rest]) and np.array_equal(lse[:, rest], lse0[:, rest])
+
+
+@pytest.mark.parametrize("heads,bs,g,bound", [(16, 64, 64, None), (8, 64, 1, 60000), (128, 64, 16, None), (128, 64, 1, None),
+                                              (128, 48, 48, None), (16, 16, 16, None), (5, 16, 1, None)])
+@pytest.mark.parametrize("last", [65, 130, 3000])
+def test_a_nan_key_reaches_only_the_tokens_that_see_it(heads, bs, g, bound, last):
+    """The last token of a request left NaN in its row: the earlier tokens, in
+    whose softmax the key is masked, keep their results."""
+    c = decode_case(76, [last, 200], heads, bs, g, qlens=[3, 2])
+    ref = reference(c)
+    bad = S.row_slots(c["table"][0], bs, last)[-1]
+    c["codes"][bad, 3::7] = 0x7F
+    c["codes"][bad, 4::7] = 0xFF
+    out, lse = Call(c, bound=bound).fwd_scaled()
+    keep = np.array([0, 1, 3, 4])
+    compare(out[keep], lse[keep], *(x[keep] for x in ref))

@@ -461,7 +461,8 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * that is NaN makes its head's rows NaN.
  * Keys of a negative block_table entry are skipped, as unused list entries are:
  * mla_block_tables leaves -1 where the free list was too short (*taken tells).
- * NaN codes of a key reach the rows that see the key, and no others.
+ * NaN codes of a key reach the rows that see the key, and no others; these rows,
+ * and those of a query with a NaN, have a NaN output and LSE.
  * A weight times its scale enters the product with the codes rounded to 7 bits
  * or more, below 2^-10 of the row's largest to 3 or more, and is off by 2^-19 of
  * the largest at most where it is smaller still.

@@ -170,6 +170,13 @@ __device__ __forceinline__ KeyScale key_scale(float s, float score_scale_log2) {
   return k;
 }
 
+// The (max, sum) of a partial for the merge, which passes over sums that are not
+// positive: a sum that is no number (a key or a query with a NaN) goes on as
+// (inf, 1), whose weight in the merge is NaN, as the whole row's is.
+__device__ __forceinline__ float2 partial_sums(float max, float sum) {
+  return sum != sum ? make_float2(INFINITY, 1.f) : make_float2(max, sum);
+}
+
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 }  // namespace mla

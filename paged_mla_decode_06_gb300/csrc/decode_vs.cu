@@ -883,18 +883,19 @@ __device__ void softmax_rows(const Ctx& x, const VsMaps& maps, const DecodeParam
           mult = e / W;
           lse = kLn2 * (M + log2f(W));
         }
-      } else if (L > 0.f) {
+      } else if (L != 0.f) {
         mult = 1.f / L;
         lse = kLn2 * (base + log2f(L));
       }
       if (writes) p.lse[th] = lse;
     } else {
-      mult = L > 0.f ? 1.f / L : 0.f;
+      mult = L != 0.f ? 1.f / L : 0.f;
       if (writes) {
         const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * p.slot_rows + r : th * p.num_segments + x.seg;
         // (any reference of the partial serves the merge)
-        p.segm_max[ts] = L > 0.f ? base : -INFINITY;
-        p.segm_expsum[ts] = L;
+        const float2 part = partial_sums(L > 0.f ? base : -INFINITY, L);
+        p.segm_max[ts] = part.x;
+        p.segm_expsum[ts] = part.y;
       }
     }
   }

@@ -232,3 +232,23 @@ def test_a_nan_key_reaches_only_the_tokens_that_see_it(heads, bs, g, bound, last
     out, lse = Call(c, bound=bound).fwd_scaled()
     keep = np.array([0, 1, 3, 4])
     compare(out[keep], lse[keep], *(x[keep] for x in ref))
+
+
+@pytest.mark.parametrize("heads,bs,g,bound", [(16, 64, 64, None), (16, 64, 1, 60000), (40, 64, 16, 60000), (64, 64, 64, 60000),
+                                              (128, 64, 16, None), (128, 64, 1, None), (128, 48, 48, None), (16, 16, 16, None)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_rows_that_see_a_nan_are_nan_split_or_not(heads, bs, g, bound, sinks):
+    """A key with a NaN, a query of one head with a NaN and an ordinary
+    request, whole and in pieces: every row is NaN in its output and its LSE
+    or right, wherever the NaN lies."""
+    c = decode_case(77, [65, 8000, 300, 8000], heads, bs, g, sinks=sinks)
+    ref = reference(c)
+    c["codes"][S.row_slots(c["table"][0], bs, 65)[3], 511] = 0x7F
+    c["codes"][S.row_slots(c["table"][1], bs, 8000)[4001], 530] = 0xFF
+    c["q"][2:, 7, 100] = 0x7F
+    bad = np.zeros((4, heads), bool)
+    bad[:2] = bad[2:, 7] = True
+    for ns in (0, 3):
+        out, lse = Call(c, bound=bound, num_segments=ns).fwd_scaled()
+        assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+        compare(out[~bad], lse[~bad], *(x[~bad] for x in ref))

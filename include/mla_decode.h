@@ -543,10 +543,11 @@ MLA_API mla_status_t mla_block_tables(const int32_t* query_start_loc, const int3
  * the rows of its group before its first slot are taken to be in use, those
  * behind its last are left as they are. With a the largest finite |x| of the
  * run's rows x = c_kv || k_pe, its group's scale becomes
- *   s = max(2^k, 2^-60) with the least k for which a <= 448 * 2^k,
+ *   s = min(max(2^k, 2^-60), 2^60) with the least k for which a <= 448 * 2^k,
  * or the old scale where that is larger and the run does not start its group;
  * the rows are stored as e4m3 codes of x / s (times the fp32 reciprocal),
- * rounded to nearest even, infinities as +-448, NaN as NaN. Where s exceeds
+ * rounded to nearest even, infinities and values beyond 448 * 2^60 as +-448,
+ * NaN as NaN. Where s exceeds
  * the old scale, the group's rows before the run are requantised by
  * old / s: exact but for codes that become subnormal, as long as every scale
  * is a power of two.

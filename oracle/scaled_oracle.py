@@ -13,7 +13,7 @@ import numpy as np
 
 from .mla_oracle import HEAD_DIM, KV_LORA_RANK, attend, decode_e4m3fn, encode_e4m3fn
 
-MIN_SCALE = 2.0 ** -60
+MIN_SCALE, MAX_SCALE = 2.0 ** -60, 2.0 ** 60
 
 
 def block_tables(query_start_loc, seq_lens, free_blocks, table, block_size, num_tokens):
@@ -40,9 +40,9 @@ def block_tables(query_start_loc, seq_lens, free_blocks, table, block_size, num_
 
 
 def group_scale(amax: float) -> float:
-    """The least power of two s with amax <= 448 s, at least MIN_SCALE."""
+    """The least power of two s with amax <= 448 s, within [MIN_SCALE, MAX_SCALE]."""
     s = MIN_SCALE
-    while amax > 448.0 * s:
+    while amax > 448.0 * s and s < MAX_SCALE:
         s *= 2.0
     return s
 

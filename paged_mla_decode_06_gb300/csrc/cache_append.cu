@@ -5,10 +5,12 @@
 // group; its team (a warp for groups of at most 8 slots, else a CTA) is the
 // only one that touches the group. With a the largest finite magnitude of the
 // run's rows, the group's scale becomes
-//   s = max(2^k, 2^-60, s_old if the run starts behind rows of its group),
+//   s = max(min(2^k, 2^60), 2^-60, s_old if the run starts behind rows of its
+//       group),
 // k the least integer with a <= 448 2^k, and the rows are stored as
-// e4m3(x / s). Where s grew, the rows before the run are requantised by
-// s_old / s. Scales made here are powers of two, so that this changes no code
+// e4m3(x / s), saturating. (The decode weighs groups against each other in
+// fp32, which scales within 2^60 of one on either side allow.) Where s grew,
+// the rows before the run are requantised by s_old / s. Scales made here are powers of two, so that this changes no code
 // but those that fall below e4m3's normal range: a group that grows again and
 // again loses no more than one that grew once. (A floating-point format gains
 // nothing from a finer scale but part of a binade of range.)
@@ -39,7 +41,7 @@ constexpr int kWarpThreads = 256;          // warp kernel
 constexpr int kWarpGroup = 8;              // largest group a warp takes
 constexpr int kMaxWindow = 256;            // tokens of a CTA's window
 constexpr int kSlotCache = 512;            // slots a CTA keeps in shared memory
-constexpr int kMinExp = -60;               // the smallest scale is 2^-60
+constexpr int kMaxExp = 60;                // scales lie in [2^-60, 2^60]
 constexpr int kWindowCtas = 304;           // CTAs of a long call: two an SM, once over (twice over:
                                            // 16 prompts of 2047 tokens 15.6 us against 14.5)
 
@@ -80,11 +82,11 @@ __device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
   return max(lo > 0x7F80u ? 0u : lo, hi > 0x7F80u ? 0u : hi);
 }
 
-// The power of two that brings a bf16 magnitude (its bits) to 448 or below:
-// 448 = 1.75 * 2^8, and the mantissa of 1.75 is 0x60.
+// The power of two that brings a bf16 magnitude (its bits) to 448 or below,
+// within the range of scales: 448 = 1.75 * 2^8, and the mantissa of 1.75 is 0x60.
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
   int e = static_cast<int>(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7Fu) > 0x60u ? 1 : 0);
-  e = max(e, kMinExp);
+  e = min(max(e, -kMaxExp), kMaxExp);
   return __int_as_float((e + 127) << 23);
 }
 

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from oracle import scaled_oracle as S
 from paged_mla_decode_06_gb300 import binding as B
 from paged_mla_decode_06_gb300 import build as BUILD
@@ -252,3 +253,43 @@ def test_rows_that_see_a_nan_are_nan_split_or_not(heads, bs, g, bound, sinks):
         out, lse = Call(c, bound=bound, num_segments=ns).fwd_scaled()
         assert np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
         compare(out[~bad], lse[~bad], *(x[~bad] for x in ref))
+
+
+@pytest.mark.parametrize("g", [1, 8, 64])
+@pytest.mark.parametrize("heads,bs", [(16, 64), (128, 64)])
+def test_the_largest_and_smallest_rows_an_append_takes(heads, bs, g):
+    """Rows of bf16's largest values, of 448 * 2^60, just beyond, and of zeros,
+    appended: the scales stay in the decode's range, what is beyond saturates,
+    and the decode over that cache is right."""
+    rng = np.random.default_rng(78)
+    n = 5 * 64
+    rows = np.exp2(rng.uniform(-3, 3, (n, 576))) * rng.choice([-1.0, 1.0], (n, 576))
+    rows[0:64] = 0.0
+    rows[64, 7], rows[65, 3] = 3.38e38, -3.0e38
+    rows[128, 0] = 448.0 * 2.0 ** 60
+    rows[192, 0] = 452.0 * 2.0 ** 60
+    t = torch.from_numpy(rows.astype(np.float32)).bfloat16()
+    cache, sc = torch.zeros((5, bs, 576), dtype=torch.uint8, device="cuda"), torch.zeros(n // g, device="cuda")
+    kv = t.cuda()
+    B.mla_cache_append(kv[:, :512], kv[:, 512:], dev(np.arange(n), np.int32), cache, sc, scale_group=g)
+    torch.cuda.synchronize()
+    got_s, codes = sc.double().cpu().numpy(), cache.view(-1, 576).cpu().numpy()
+    assert (got_s >= 2.0 ** -60).all() and (got_s <= 2.0 ** 60).all()
+    want_c, want_s = S.cache_append(t.double().numpy(), np.arange(n), np.zeros((n, 576), np.uint8), np.zeros(n // g), g)
+    assert np.array_equal(got_s, want_s)
+    assert np.array_equal(O.decode_e4m3fn(codes), O.decode_e4m3fn(want_c))
+    assert O.decode_e4m3fn(codes[64, 7]) == 448.0 and O.decode_e4m3fn(codes[65, 3]) == -448.0
+    # the queries are orthogonal to the columns that differ by many binades, so
+    # that the softmax weighs all keys
+    qc = I.float32_to_e4m3_codes(rng.standard_normal((1, heads, 576)).astype(np.float32) * 2.0 ** -6 / QS)
+    qc[..., [0, 3, 7]] = 0
+    plan = B.mla_decode_plan(B.make_problem(num_tokens=1, num_heads=heads, block_size=bs, num_blocks=5, num_reqs=1,
+                                            max_blocks_per_req=5, max_seq_len=n, dtype="fp8"))
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((1, heads, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((1, heads), device="cuda")
+    table = np.arange(5)[None]
+    B.mla_decode_fwd_scaled(plan, dev(qc), cache, sc, scale_group=g, block_table=dev(table, np.int32),
+                            seq_lens=dev([n], np.int32), softmax_scale=SCALE, q_scale=QS, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    compare(out.double().cpu().numpy(), lse.double().cpu().numpy(),
+            *S.decode(qc, QS, codes, got_s, g, S.token_slots(table, [n], bs), SCALE, bounds=True))

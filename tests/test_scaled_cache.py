@@ -175,3 +175,13 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(B.MLAError, match="CUDA device"):
         B.mla_decode_fwd_scaled(_plan(), torch.zeros((4, 16, 576), dtype=torch.uint8), cache, sc, scale_group=4,
                                 softmax_scale=1.0, out=kv, lse=sc)
+
+
+@pytest.mark.parametrize("amax,scale", [(448.0 * 2.0 ** 60, 2.0 ** 60), (449.0 * 2.0 ** 60, 2.0 ** 60), (3.38e38, 2.0 ** 60),
+                                        (448.0 * 2.0 ** 59, 2.0 ** 59), (225.0 * 2.0 ** 60, 2.0 ** 60)])
+def test_group_scale_stays_in_the_decodes_range(amax, scale):
+    """Scales lie in [2^-60, 2^60]; what is beyond 448 * 2^60 saturates."""
+    assert S.group_scale(amax) == scale
+    codes, scales = S.cache_append(np.full((1, 576), amax), [0], np.zeros((2, 576), np.uint8), np.zeros(1), 2)
+    assert scales[0] == scale
+    assert O.decode_e4m3fn(codes[0, 0]) == O.decode_e4m3fn(O.encode_e4m3fn(np.array(min(amax / scale, 448.0))))

@@ -113,7 +113,7 @@ typedef enum {
                                   sparse bf16 */
   MLA_KERNEL_TCGEN05_ROWS_N = 3 /* tcgen05/TMEM kernel with the query rows as
                                   the MMA N dimension, one CTA per 16..64 rows
-                                  (a cluster of two CTAs sharing each key box
+                                  (a cluster of two CTAs over the same keys
                                   for 65..128 rows):
                                   dense e4m3 with block_size a multiple of 64
                                   and num_heads * max_qlen <= 128 */

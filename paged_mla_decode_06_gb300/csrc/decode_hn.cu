@@ -33,13 +33,12 @@
 // same.
 //
 // Requests of 65..128 rows run on a thread-block cluster of CL = 2 CTAs, CTA
-// r owning rows [r NR, (r + 1) NR) of the row tile: every key box is read
-// from memory once, by one CTA of the cluster, and multicast by TMA to the
-// ring slot of both, so that all heads of a request share one pass over its
-// keys. A slot is refilled only after the consumers of every CTA released it
-// (each commit arrives on the empty barrier of every CTA of the cluster); the
-// loading CTA also arms the peer's full barrier with the box's bytes, so each
-// CTA can tell, at teardown, when every box meant for it has landed.
+// r owning rows [r NR, (r + 1) NR) of the row tile. The two start together
+// and walk the same keys, each with boxes and barriers of its own: the later
+// one of a box finds it in L2, so that all heads of a request still share one
+// pass over its keys in memory. (Boxes loaded once for both tie each slot to
+// the slower CTA: 52 x 16384 keys, 96 heads 230 us a call against 197, 128
+// heads 269 either way; loads that ask L2 to evict them first 194 and 276.)
 //
 // Work: with the balanced schedule, a worker (a CTA, or a cluster) walks a
 // contiguous run of items (key ranges of row tiles) of about equal length,
@@ -83,9 +82,9 @@ constexpr float kMove = 4.f;             // m_ref moves when a chunk max exceeds
 
 enum : int {
   kFull = 0,                    // [kMaxSlots] ring slot loaded
-  kEmpty = kMaxSlots,           // [kMaxSlots] ring slot released by every CTA of the cluster
+  kEmpty = kMaxSlots,           // [kMaxSlots] ring slot released
   kRFull = 2 * kMaxSlots,       // [kMaxRSlots] rope slot loaded
-  kREmpty = kRFull + kMaxRSlots,  // [kMaxRSlots] rope slot released by every CTA of the cluster
+  kREmpty = kRFull + kMaxRSlots,  // [kMaxRSlots] rope slot released
   kQFull = kREmpty + kMaxRSlots,  // q of the current item loaded
   kQFree,                       // QK^T of the item complete: q may be replaced
   kSFull,                       // [2] S^T buffer written
@@ -255,15 +254,12 @@ __device__ __forceinline__ void report(int* status, int code) {
 // Bounded wait on a barrier phase; false on timeout (recorded) or abort. The
 // thread sleeps in the wait (up to kSleepNs at a time, woken by the phase)
 // rather than spinning, which would take issue slots from the MMA issuer.
-// `cluster` selects cluster-scope acquire, for barriers that other CTAs of
-// the cluster arrive on.
 constexpr uint32_t kSleepNs = 20000;
-template <bool kCluster = false>
 __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   const uint32_t nap = x.limit_ns < kSleepNs ? static_cast<uint32_t>(x.limit_ns) : kSleepNs;
-  while (!(kCluster ? mbar_try_wait_cluster_sleep(bar, parity, nap) : mbar_try_wait_sleep(bar, parity, nap))) {
+  while (!mbar_try_wait_sleep(bar, parity, nap)) {
     if (*x.abort) return false;
     if (global_timer_ns() - t0 > x.limit_ns) {
       report(x.status, code);
@@ -282,7 +278,7 @@ __device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t p
 // Wait that ignores the abort flag (teardown drains), bounded by the default limit.
 __device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_cluster_sleep(bar, parity, kSleepNs)) {
+  while (!mbar_try_wait_sleep(bar, parity, kSleepNs)) {
     if (global_timer_ns() - t0 > kDefaultWaitNs) {
       report(x.status, code);
       return;
@@ -298,16 +294,6 @@ __device__ __forceinline__ bool cross_sync(const Ctx& x, int idx, uint32_t parit
   return warp_wait(x, x.bar(idx), parity, code);
 }
 
-// Release of a ring slot (or any barrier every CTA of the cluster counts) by
-// this CTA's MMAs, once they complete.
-template <int CL>
-__device__ __forceinline__ void release(uint32_t bar) {
-  if constexpr (CL == 1)
-    mma_commit(bar);
-  else
-    mma_commit_mc(bar, static_cast<uint16_t>((1u << CL) - 1u));
-}
-
 // Cache row of key position pos (64 keys from a 64-aligned position lie in
 // one block: the block size is a multiple of 64).
 __device__ __forceinline__ int cache_row(const DecodeParams& p, const int32_t* bt_row, int pos) {
@@ -320,9 +306,8 @@ __device__ __forceinline__ int cache_row(const DecodeParams& p, const int32_t* b
 // Latent box j < 4 of the worker's g-th chunk (two 64-row TMA boxes from
 // their blocks) goes to ring slot i % kSlots, i = 4 g + j, its rope box to
 // rope slot g % kRSlots, the counts running on across the worker's items.
-// Box b = 5 g + j is loaded by CTA b % CL of the cluster (the only one in a
-// cluster of one) and there by producer warp (b / CL) % 2, which records
-// the latest use issued per slot (the teardown waits for those loads). The whole warp looks up the cache rows of 16 chunks at a time
+// Box b = 5 g + j is loaded by producer warp b % 2, which records the latest
+// use issued per slot (the teardown waits for those loads). The whole warp looks up the cache rows of 16 chunks at a time
 // (lane l: chunk l / 2, half l % 2), one window ahead of the chunks it
 // issues, so that no TMA issue waits on a block-table read; lane 0 issues.
 template <int NR, int CL>
@@ -334,7 +319,7 @@ __device__ void produce(const Ctx& x, const HnMaps& maps, const DecodeParams& p,
     tma_prefetch_desc(&maps.kv);
     tma_prefetch_desc(&maps.kvr);
   }
-  const uint64_t pol = l2_evict_first();  // each key row is read once
+  const uint64_t pol = l2_evict_first();  // each key row is read once (CL = 1)
   int gb = 0;                             // the worker's box count
   bool ok = true;
   for (int idx = x.it_begin; idx < x.it_end && ok; ++idx) {
@@ -358,14 +343,14 @@ __device__ void produce(const Ctx& x, const HnMaps& maps, const DecodeParams& p,
       if (lane == 0) {
         for (int j = 0; j < kBoxes; ++j) {
           const int bi = gb + j;
-          if (bi % CL != x.rank || (bi / CL) % kProducers != pidx) continue;
+          if (bi % kProducers != pidx) continue;
           const bool rope = j == kBoxes - 1;
           const int i = rope ? gb / kBoxes : (gb / kBoxes) * (kBoxes - 1) + j;
           const int nslots = rope ? C::kRSlots : C::kSlots;
           const int slot = i % nslots;
           const int use = i / nslots;
           const int empty = rope ? kREmpty + slot : kEmpty + slot;
-          if (use >= 1 && !wait_phase<(CL > 1)>(x, x.bar(empty), (use - 1) & 1, 11)) {
+          if (use >= 1 && !wait_phase(x, x.bar(empty), (use - 1) & 1, 11)) {
             ok = false;
             break;
           }
@@ -378,13 +363,9 @@ __device__ void produce(const Ctx& x, const HnMaps& maps, const DecodeParams& p,
           if constexpr (CL == 1) {
             tma_load_2d_hint(dst, map, 128 * j, row0, full, pol);
             if (two) tma_load_2d_hint(dst + box / 2, map, 128 * j, row1, full, pol);
-          } else {
-            // the peers' phases of this slot also wait for the box
-            for (int r = 0; r < CL; ++r)
-              if (r != x.rank) mbar_arrive_expect_tx_cluster(map_to_rank(full, r), bytes);
-            constexpr uint16_t kAll = static_cast<uint16_t>((1u << CL) - 1u);
-            tma_load_2d_mc_hint(dst, map, 128 * j, row0, full, kAll, pol);
-            if (two) tma_load_2d_mc_hint(dst + box / 2, map, 128 * j, row1, full, kAll, pol);
+          } else {  // (the other CTA's rows need it too)
+            tma_load_2d(dst, map, 128 * j, row0, full);
+            if (two) tma_load_2d(dst + box / 2, map, 128 * j, row1, full);
           }
           atomicMax(const_cast<int*>(issued + (rope ? kMaxSlots + slot : slot)), use);
         }
@@ -441,7 +422,7 @@ __device__ void qk_issue(const Ctx& x, const HnMaps& maps, const DecodeParams& p
         const int i = rope ? g : g * (kBoxes - 1) + j;
         const int slot = i % (rope ? C::kRSlots : C::kSlots);
         const int use = i / (rope ? C::kRSlots : C::kSlots);
-        if (!wait_phase<(CL > 1)>(x, x.bar(rope ? kRFull + slot : kFull + slot), use & 1, 23)) {
+        if (!wait_phase(x, x.bar(rope ? kRFull + slot : kFull + slot), use & 1, 23)) {
           ok = false;
           break;
         }
@@ -453,7 +434,7 @@ __device__ void qk_issue(const Ctx& x, const HnMaps& maps, const DecodeParams& p
 #pragma unroll
         for (int s = 0; s < (rope ? 2 : 4); ++s)
           mma_ss_f8(d, a + 2 * s, qb + 2 * s, kIdQK, (j | s) != 0 ? 1u : 0u);
-        if (rope) release<CL>(x.bar(kREmpty + slot));  // the rope box's only read
+        if (rope) mma_commit(x.bar(kREmpty + slot));  // the rope box's only read
       }
       if (!ok) break;
       mma_commit(x.bar(kSFull + b));
@@ -507,7 +488,7 @@ __device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
           if constexpr (!C::kConcat)  // the lo term: the next NR / 16 core matrices
             mma_ss_f8(dm, av, bv + static_cast<uint64_t>((NR / 16 * 128) >> 4), kIdLo, 1u);
         }
-        release<CL>(x.bar(kEmpty + slot));  // the value box's last read
+        mma_commit(x.bar(kEmpty + slot));  // the value box's last read
       }
       mma_commit(x.bar(kPFree + b));
     }
@@ -972,11 +953,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *x.abort = 0;
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(x.bar(kFull + s), 1);
-      mbar_init(x.bar(kEmpty + s), CL);
+      mbar_init(x.bar(kEmpty + s), 1);
     }
     for (int s = 0; s < C::kRSlots; ++s) {
       mbar_init(x.bar(kRFull + s), 1);
-      mbar_init(x.bar(kREmpty + s), CL);
+      mbar_init(x.bar(kREmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(x.bar(kSFull + b), 1);
@@ -1013,7 +994,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if constexpr (CL > 1) cluster_sync();  // the peers' barriers exist before any remote arrive or load
   x.tbase = *tslot;
 
   if (x.warp == 0 || x.warp == 2) {
@@ -1031,29 +1011,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   if (x.warp == 1) tmem_dealloc(x.tbase, C::kTmemAlloc);
-  // every TMA load into this CTA's shared memory must have landed before the
-  // CTA exits: per slot, the latest use armed here (by this CTA's loads or,
-  // in a cluster, the peers', whose issue records are read once every CTA
-  // has stopped issuing); all are consumed unless a wait gave up. Then q.
-  if constexpr (CL > 1) cluster_sync();
+  // every TMA load must have landed before the CTA exits: per slot, the latest
+  // use issued (all are consumed unless a wait gave up). Then q.
   if (x.tid == 0) {
     const volatile int* issued = reinterpret_cast<const volatile int*>(smem + kOffIssued);
     for (int e = 0; e < kMaxSlots + kMaxRSlots; ++e) {
       const bool rope = e >= kMaxSlots;
       const int s = rope ? e - kMaxSlots : e;
-      if (s >= (rope ? C::kRSlots : C::kSlots)) continue;
-      int last = issued[e];
-      if constexpr (CL > 1) {
-        const uint32_t rec = smem_u32(smem + kOffIssued + 4 * e);
-        for (int r = 0; r < CL; ++r)
-          if (r != x.rank) last = max(last, ld_cluster_s32(map_to_rank(rec, r)));
-      }
-      if (last >= 0) drain_wait(x, x.bar(rope ? kRFull + s : kFull + s), last & 1, 12);
+      if (s >= (rope ? C::kRSlots : C::kSlots) || issued[e] < 0) continue;
+      drain_wait(x, x.bar(rope ? kRFull + s : kFull + s), issued[e] & 1, 12);
     }
     if (issued[kIssuedQ] >= 0) drain_wait(x, x.bar(kQFull), issued[kIssuedQ] & 1, 13);
   }
-  // no CTA of the cluster exits while loads into another may still land
-  if constexpr (CL > 1) cluster_sync();
 }
 
 template <int NR, int CL, bool GS>

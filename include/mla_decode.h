@@ -484,6 +484,15 @@ MLA_API mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q
                                            float* lse, cudaStream_t stream);
 
 /*
+ * mla_decode_scaled_kernel -- the decode kernel that the scaled calls of a plan
+ * run on: *kernel receives plan->kernel, or 6 for the kernel of their own
+ * (two CTAs to a tile of 128 query rows). Host only, no device call. Errors:
+ * MLA_ERR_INVALID_ARG for NULL or a bad plan, MLA_ERR_UNSUPPORTED for one whose
+ * cache is not e4m3.
+ */
+MLA_API mla_status_t mla_decode_scaled_kernel(const mla_plan_t* plan, int32_t* kernel);
+
+/*
  * mla_decode_items_scaled -- mla_decode_items over a cache with group scales,
  * between mla_decode_schedule and mla_merge_items, for callers that compute
  * the work list once per step. Arguments as mla_decode_fwd_scaled.

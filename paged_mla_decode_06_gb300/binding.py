@@ -129,6 +129,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mla_decode_fwd_scaled.restype = st
         lib.mla_decode_items_scaled.argtypes = scaled
         lib.mla_decode_items_scaled.restype = st
+        lib.mla_decode_scaled_kernel.argtypes = [ctypes.POINTER(Plan), ctypes.POINTER(i32)]
+        lib.mla_decode_scaled_kernel.restype = st
         lib.mla_block_tables.argtypes = [_vp, _vp, i32, i32, i32, _vp, i32, _vp, i64, i32, _vp, _vp,
                                          _vp, _vp, _vp]
         lib.mla_block_tables.restype = st
@@ -475,6 +477,15 @@ def mla_decode_items_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: 
         fn, plan, q, kv_cache, kv_scales, scale_group, block_table, block_table_stride, seq_lens,
         qo_indptr, sparse_slots, sparse_indptr, softmax_scale, q_scale, sinks, workspace, out, lse,
         stream)))
+
+
+def mla_decode_scaled_kernel(plan: Plan) -> int:
+    """The decode kernel that the scaled calls of ``plan`` run on (``plan.kernel``,
+    or 6 for the kernel of their own)."""
+    lib = _lib or load_library()
+    kernel = ctypes.c_int32(0)
+    _check("mla_decode_scaled_kernel", lib.mla_decode_scaled_kernel(ctypes.byref(plan), ctypes.byref(kernel)))
+    return kernel.value
 
 
 def mla_block_tables(query_start_loc, seq_lens, free_blocks, block_table, *, block_size: int,

@@ -657,6 +657,16 @@ mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q, const 
   return decode_fwd(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
 }
 
+mla_status_t mla_decode_scaled_kernel(const mla_plan_t* plan, int32_t* kernel) {
+  if (plan == nullptr || kernel == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla_status_t s = check_problem(plan->prob);
+  if (s != MLA_OK) return s;
+  if (plan->prob.kv_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
+  static const float scales = 1.f;  // (the rule asks whether there are any)
+  *kernel = runs_value_split(plan, &scales) ? mla::kValueSplit : plan->kernel;
+  return MLA_OK;
+}
+
 mla_status_t mla_workspace_status(const mla_plan_t* plan, const void* workspace, int32_t* code,
                                   int32_t clear, cudaStream_t stream) {
   if (plan == nullptr || workspace == nullptr || code == nullptr) return MLA_ERR_INVALID_ARG;

@@ -14,6 +14,7 @@ enum KernelId : int32_t {
   kMmaRows64 = 3,   // 64 rows per CTA
   kTcPair128 = 4,   // tcgen05 CTA-pair kernel, 128 rows per pair
   kTcRowsN = 5,     // tcgen05 kernel with the query rows as N, 16..64 rows per CTA, 1-2 CTAs per tile
+  kValueSplit = 6,  // tcgen05 kernel of the group-scaled cache, two CTAs per row tile (never a plan's: decode_vs.cu)
 };
 
 struct DecodeParams {

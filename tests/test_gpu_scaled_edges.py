@@ -293,3 +293,73 @@ def test_the_largest_and_smallest_rows_an_append_takes(heads, bs, g):
     torch.cuda.synchronize()
     compare(out.double().cpu().numpy(), lse.double().cpu().numpy(),
             *S.decode(qc, QS, codes, got_s, g, S.token_slots(table, [n], bs), SCALE, bounds=True))
+
+
+# ---------------------------------------------------------------- the rows-as-N kernel at 17 to 64 rows
+
+# (heads, tokens of the requests, group): 32, 48 and 64 rows a CTA, part filled or full
+ROWS_N = [(17, None, 64), (32, None, 1), (48, None, 16), (57, None, 2), (64, None, 64), (64, None, 1),
+          (8, [3, 1, 2, 3, 1, 2], 32), (16, [1, 3, 3, 2, 1, 3], 8), (21, [2, 3, 1, 3, 3, 1], 64), (16, [4, 2, 4, 1, 4, 3], 16)]
+
+
+@pytest.mark.parametrize("heads,qlens,g", ROWS_N)
+@pytest.mark.parametrize("sinks", [False, True])
+def test_rows_as_n_over_long_contexts(heads, qlens, g, sinks):
+    """Requests that are split among many workers, and short and empty ones; the
+    stages apart give the bits of the whole call (one list for both)."""
+    lens = [9001, 4, 129, 24000, 64, 777] if qlens else [9001, 0, 129, 24000, 1, 777]
+    c = decode_case(81 + heads, lens, heads, 64, g, qlens=qlens, sinks=sinks)
+    call = Call(c)
+    assert B.mla_decode_scaled_kernel(call.plan) == 5 and call.plan.tile_rows in (32, 48, 64)
+    a = call.fwd_scaled()
+    compare(*a, *reference(c))
+    b = call.stages_scaled()
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("heads,qlens,g", ROWS_N)
+@pytest.mark.parametrize("ns", [1, 3])
+def test_rows_as_n_with_a_fixed_partition(heads, qlens, g, ns):
+    lens = [300, 4, 129, 1500, 64, 777] if qlens else [300, 0, 129, 1500, 1, 777]
+    c = decode_case(82 + heads, lens, heads, 64, g, qlens=qlens, sinks=ns == 3)
+    call = Call(c, num_segments=ns)
+    assert B.mla_decode_scaled_kernel(call.plan) == 5
+    compare(*call.fwd_scaled(), *reference(c))
+
+
+@pytest.mark.parametrize("heads", [32, 48, 64])
+@pytest.mark.parametrize("exps", [(-6, 6), (-40, -36), (10, 14), (-50, 3)])
+def test_rows_as_n_with_scales_far_apart(heads, exps):
+    c = decode_case(83, [5, 300, 1100, 64], heads, 64, 8, scale_exp=exps, sinks=exps[0] == -6)
+    call = Call(c, bound=60000)
+    assert B.mla_decode_scaled_kernel(call.plan) == 5
+    compare(*call.fwd_scaled(), *reference(c))
+
+
+@pytest.mark.parametrize("heads,qlens", [(16, None), (32, None), (48, None), (64, None), (20, [3])])
+def test_rows_as_n_where_one_key_outweighs_a_long_context(heads, qlens):
+    """One key without a value weighs 2^16 times as much as each of 9000 others
+    whose values agree in sign: together they are the result."""
+    c = decode_case(84, [9000], heads, 64, 1, qlens=qlens)
+    rng = np.random.default_rng(85)
+    q = np.tile(rng.standard_normal(576) * 2.0 ** -8, (c["T"], heads, 1)).astype(np.float32) / QS
+    c["q"] = I.float32_to_e4m3_codes(q)
+    at = S.row_slots(c["table"][0], 64, 9000)
+    c["codes"][at] = I.float32_to_e4m3_codes(np.abs(rng.standard_normal((9000, 576))).astype(np.float32))
+    c["scales"][at] = 1.0
+    first = int(at[4000])
+    rope = O.decode_e4m3fn(c["q"])[0, 0, 512:] * QS
+    c["codes"][first, :512] = 0
+    c["codes"][first, 512:] = I.float32_to_e4m3_codes(448 * np.sign(rope).astype(np.float32))
+    c["scales"][first] = np.float32(16 * np.log(2.0) / (448 * SCALE * np.abs(rope).sum()))
+    call = Call(c, bound=60000)
+    assert B.mla_decode_scaled_kernel(call.plan) == 5
+    compare(*call.fwd_scaled(), *reference(c))
+
+
+@pytest.mark.parametrize("heads", [17, 48, 64])
+def test_rows_as_n_over_more_short_requests_than_one_wave(heads):
+    c = decode_case(86, [33] * 40 + [100] * 40 + [0] * 80, heads, 64, 64)
+    call = Call(c, bound=512)
+    assert B.mla_decode_scaled_kernel(call.plan) == 5
+    compare(*call.fwd_scaled(), *reference(c))

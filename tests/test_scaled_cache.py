@@ -185,3 +185,34 @@ def test_group_scale_stays_in_the_decodes_range(amax, scale):
     codes, scales = S.cache_append(np.full((1, 576), amax), [0], np.zeros((2, 576), np.uint8), np.zeros(1), 2)
     assert scales[0] == scale
     assert O.decode_e4m3fn(codes[0, 0]) == O.decode_e4m3fn(O.encode_e4m3fn(np.array(min(amax / scale, 448.0))))
+
+
+# ---------------------------------------------------------------- the kernel that a scaled call runs on
+
+# plans of 152 SMs: 1-3 warp MMA, 5 rows as N, 6 the scaled calls' own
+@pytest.mark.parametrize("heads,reqs,bound,kw,kernel", [
+    (16, 52, 16384, {}, 5), (16, 1, 64, {}, 5), (17, 52, 16384, {}, 5), (32, 52, 16384, {}, 5), (64, 52, 16384, {}, 5),
+    (65, 52, 16384, {}, 6), (128, 1, 64, {}, 6), (16, 8, 4096, dict(qlen=5), 6), (16, 64, 4096, dict(qlen=4), 5),
+    (17, 1, 32768, {}, 6), (17, 1, 32832, {}, 5), (64, 8, 4096, {}, 6), (64, 9, 4096, {}, 5),        # few keys
+    (64, 76, 512, {}, 6), (64, 77, 512, {}, 5), (64, 76, 576, {}, 5), (16, 76, 512, {}, 5),          # one wave, short
+    (16, 9, 4096, dict(block=16), 6), (16, 9, 128, dict(block=16), 1), (17, 9, 128, dict(block=16), 6),
+    (128, 9, 4096, dict(block=48), 6), (16, 9, 0, dict(topk=128), 1), (16, 9, 0, dict(topk=256), 6),
+    (16, 9, 4096, dict(kernel=B.MLA_KERNEL_WARP_MMA), 1), (128, 9, 4096, dict(kernel=B.MLA_KERNEL_WARP_MMA), 3),
+    (16, 9, 4096, dict(kernel=B.MLA_KERNEL_TCGEN05), 6), (64, 9, 512, dict(kernel=B.MLA_KERNEL_TCGEN05_ROWS_N), 5),
+    (64, 9, 512, dict(num_segments=2), 5), (128, 9, 512, dict(num_segments=2), 6)])
+def test_kernel_of_a_scaled_call(lib, heads, reqs, bound, kw, kernel):
+    kw = dict(kw)
+    qlen, block, topk = kw.pop("qlen", 1), kw.pop("block", 64), kw.get("topk", 0)
+    plan = B.mla_decode_plan(B.make_problem(
+        num_tokens=reqs * qlen, num_reqs=0 if topk else reqs, num_heads=heads, block_size=block, num_blocks=100,
+        max_blocks_per_req=-(-bound // block), max_seq_len=bound, max_qlen=qlen, num_sms=152, dtype="fp8", **kw))
+    assert B.mla_decode_scaled_kernel(plan) == kernel
+
+
+def test_kernel_of_a_scaled_call_refuses(lib):
+    k = ctypes.c_int32(0)
+    assert lib.mla_decode_scaled_kernel(None, ctypes.byref(k)) == B.MLA_ERR_INVALID_ARG
+    assert lib.mla_decode_scaled_kernel(ctypes.byref(_plan()), None) == B.MLA_ERR_INVALID_ARG
+    with pytest.raises(B.MLAError) as e:
+        B.mla_decode_scaled_kernel(_plan(dtype="bf16"))
+    assert e.value.status == B.MLA_ERR_UNSUPPORTED

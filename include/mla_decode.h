@@ -457,8 +457,14 @@ MLA_API mla_status_t mla_concat_quant_q(const void* ql_nope, int64_t nope_stride
  * to the warp-MMA kernel without being asked to, run on a kernel of their own
  * here, in the same workspace; where the planner chose the number of segments,
  * that kernel may use fewer, and a whole call over few short requests may leave
- * a balanced plan's schedule and merge out. A sink of -inf counts as none, one
- * that is NaN makes its head's rows NaN.
+ * a balanced plan's schedule and merge out. These choices (few keys: max_seq_len
+ * times num_reqs at most 32768; short: max_seq_len at most 512) go by the
+ * plan's max_seq_len, not by the lengths: a captured call whose plan has the
+ * model's longest context takes the kernels for long ones, right but slower
+ * over short requests (32 of 512 keys: 64 heads 26 us instead of 16, 128 heads
+ * 21 instead of 16), so a server that captures per batch size may capture
+ * per length bound as well. mla_decode_scaled_kernel tells the kernel. A sink
+ * of -inf counts as none, one that is NaN makes its head's rows NaN.
  * Keys of a negative block_table entry are skipped, as unused list entries are:
  * mla_block_tables leaves -1 where the free list was too short (*taken tells).
  * NaN codes of a key reach the rows that see the key, and no others; these rows,
@@ -493,10 +499,24 @@ MLA_API mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q
 MLA_API mla_status_t mla_decode_scaled_kernel(const mla_plan_t* plan, int32_t* kernel);
 
 /*
- * mla_decode_items_scaled -- mla_decode_items over a cache with group scales,
- * between mla_decode_schedule and mla_merge_items, for callers that compute
- * the work list once per step. Arguments as mla_decode_fwd_scaled.
+ * mla_decode_schedule_scaled, mla_decode_items_scaled -- the first two stages of
+ * mla_decode_fwd_scaled under a balanced plan, mla_merge_items being the third:
+ * mla_decode_schedule with the list of the kernel that scaled calls run on, and
+ * mla_decode_items over a cache with group scales. Arguments as there and as
+ * mla_decode_fwd_scaled. The stages give the bits of a whole call that splits
+ * its rows the same way (that is, of any but one over few short requests, which
+ * makes no list). Over the list of mla_decode_schedule the items are right too;
+ * where they run on a kernel other than the plan's (mla_decode_scaled_kernel:
+ * 6), its pieces are not that kernel's (52 x 16384 keys, 128 heads: 227 us
+ * against 160), and the bits are others. Any call's list serves all calls of
+ * the same lengths, mla_decode_items among them, until another replaces it.
+ * Errors: as mla_decode_schedule and mla_decode_fwd_scaled.
  */
+MLA_API mla_status_t mla_decode_schedule_scaled(const mla_plan_t* plan, const int32_t* seq_lens,
+                                                const int32_t* qo_indptr, const int32_t* sparse_indptr,
+                                                void* workspace, size_t workspace_bytes,
+                                                cudaStream_t stream);
+
 MLA_API mla_status_t mla_decode_items_scaled(const mla_plan_t* plan, const void* q,
                                              const void* kv_cache, const float* kv_scales,
                                              int32_t scale_group, const int32_t* block_table,

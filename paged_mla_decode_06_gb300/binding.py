@@ -129,6 +129,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mla_decode_fwd_scaled.restype = st
         lib.mla_decode_items_scaled.argtypes = scaled
         lib.mla_decode_items_scaled.restype = st
+        lib.mla_decode_schedule_scaled.argtypes = lib.mla_decode_schedule.argtypes
+        lib.mla_decode_schedule_scaled.restype = st
         lib.mla_decode_scaled_kernel.argtypes = [ctypes.POINTER(Plan), ctypes.POINTER(i32)]
         lib.mla_decode_scaled_kernel.restype = st
         lib.mla_block_tables.argtypes = [_vp, _vp, i32, i32, i32, _vp, i32, _vp, i64, i32, _vp, _vp,
@@ -464,13 +466,22 @@ def mla_decode_fwd_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: in
         stream)))
 
 
+def mla_decode_schedule_scaled(plan: Plan, *, seq_lens=None, qo_indptr=None, sparse_indptr=None,
+                               workspace, stream=None) -> None:
+    """Balanced plans: the work list of mla_decode_items_scaled into ``workspace``."""
+    lib = _lib or load_library()
+    _check("mla_decode_schedule_scaled", lib.mla_decode_schedule_scaled(
+        ctypes.byref(plan), _ptr(seq_lens), _ptr(qo_indptr), _ptr(sparse_indptr),
+        _ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
 def mla_decode_items_scaled(plan: Plan, q, kv_cache, kv_scales, *, scale_group: int,
                             block_table=None, block_table_stride=None, seq_lens=None,
                             qo_indptr=None, sparse_slots=None, sparse_indptr=None,
                             softmax_scale: float, q_scale: float = 1.0, sinks=None, workspace,
                             out, lse, stream=None) -> None:
     """Balanced plans: the decode kernel of mla_decode_fwd_scaled over the work
-    list in ``workspace``."""
+    list in ``workspace`` (mla_decode_schedule_scaled's)."""
     lib = _lib or load_library()
     fn = "mla_decode_items_scaled"
     _check(fn, lib.mla_decode_items_scaled(*_scaled_args(

@@ -82,6 +82,7 @@ struct Inputs {
   float softmax_scale, q_scale, kv_scale;
   const float* kv_scales = nullptr;  // group scales of the cache, or null
   int32_t scale_group = 0;
+  bool scaled() const { return scale_group > 0; }
 };
 
 mla_status_t check_inputs(const mla_plan_t* plan, const Inputs& in) {
@@ -141,8 +142,8 @@ int64_t value_split_ctas(const mla_plan_t* plan) {
 //   requests of 128 keys, 16 heads take 10.8 us there and 11.5 here, of 192 keys
 //   14.2 and 13.1; 32 of 4000 keys, 128 heads 300 and 68; 32 x 2048 sparse
 //   slots, 32 heads 52.6 and 33.6.
-bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
-  if (kv_scales == nullptr) return false;
+bool runs_value_split(const mla_plan_t* plan, bool scaled) {
+  if (!scaled) return false;
   const mla_problem_t& p = plan->prob;
   if (plan->kernel == mla::kTcPair128) return true;
   const bool asked = p.kernel != MLA_KERNEL_AUTO;
@@ -160,20 +161,20 @@ bool runs_value_split(const mla_plan_t* plan, const float* kv_scales) {
 // merge out: short requests, and a CTA (pair) for each row tile in one wave (32
 // x 128 keys, 128 heads: 10.2 us against 14.4, 512 keys 15.8 against 20.9; one
 // request of 512 keys 15.4 against 15.6, of 768 18.9 against 16.4).
-bool runs_unsplit(const mla_plan_t* plan, const float* kv_scales) {
+bool runs_unsplit(const mla_plan_t* plan, bool scaled) {
   const mla_problem_t& p = plan->prob;
-  if (kv_scales == nullptr || plan->schedule != 1 || p.max_seq_len > kShortKeys) return false;
-  return (runs_value_split(plan, kv_scales) ? value_split_ctas(plan)
-                                            : static_cast<int64_t>(plan->row_tiles) * p.num_reqs) <= plan->num_sms;
+  if (!scaled || plan->schedule != 1 || p.max_seq_len > kShortKeys) return false;
+  return (runs_value_split(plan, scaled) ? value_split_ctas(plan)
+                                         : static_cast<int64_t>(plan->row_tiles) * p.num_reqs) <= plan->num_sms;
 }
 
 // Segments of a fixed schedule. The planner's own choice (about two of its CTAs
 // per SM) suits the warp-MMA kernel; the value-split kernel, two CTAs a tile and
 // one an SM, takes no more of them than one wave of CTAs (32 tokens x 2048 keys,
 // 128 heads: 61 us with the four of the planner, 38 with two).
-int32_t segments_of(const mla_plan_t* plan, const float* kv_scales) {
+int32_t segments_of(const mla_plan_t* plan, bool scaled) {
   const mla_problem_t& p = plan->prob;
-  if (p.num_segments != 0 || plan->num_segments == 1 || !runs_value_split(plan, kv_scales)) return plan->num_segments;
+  if (p.num_segments != 0 || plan->num_segments == 1 || !runs_value_split(plan, scaled)) return plan->num_segments;
   const int64_t ctas = value_split_ctas(plan);
   const int64_t fit = ctas > 0 ? plan->num_sms / ctas : 1;
   return static_cast<int32_t>(fit < 1 ? 1 : fit < plan->num_segments ? fit : plan->num_segments);
@@ -195,7 +196,7 @@ mla::DecodeParams make_params(const mla_plan_t* plan, const Inputs& in) {
   d.num_heads = p.num_heads;
   d.block_size = p.block_size;
   d.topk = p.topk;
-  d.num_segments = segments_of(plan, in.kv_scales);
+  d.num_segments = segments_of(plan, in.scaled());
   d.tile_size = plan->tile_size;
   d.row_tiles = plan->row_tiles;
   d.score_scale_log2 = in.softmax_scale * in.q_scale * in.kv_scale * 1.4426950408889634f;
@@ -278,7 +279,7 @@ mla_status_t launch_decode(const mla_plan_t* plan, const mla::DecodeParams& d, i
   const int64_t q_rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   const int64_t kv_rows = static_cast<int64_t>(p.num_blocks) * p.block_size;
   const unsigned items = static_cast<unsigned>(plan->max_items);
-  if (runs_value_split(plan, d.kv_scales)) {
+  if (runs_value_split(plan, d.scale_group > 0)) {
     const int64_t rows = static_cast<int64_t>(p.num_heads) * (p.topk > 0 ? 1 : p.max_qlen);
     const unsigned tiles = static_cast<unsigned>((rows + 127) / 128);
     const dim3 grid = d.items != nullptr ? dim3(2u * items, 1u, 1u)
@@ -323,11 +324,11 @@ mla::SchedParams sched_params(const mla_plan_t* plan, const Inputs& in, uint8_t*
   sp.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
   sp.workers = plan_workers(plan);
   // (a rows-as-N plan of up to 64 rows has a worker an SM, the value-split kernel a pair)
-  if (plan->kernel == mla::kTcRowsN && plan->tile_rows <= 64 && runs_value_split(plan, in.kv_scales) && sp.workers > 1)
+  if (plan->kernel == mla::kTcRowsN && plan->tile_rows <= 64 && runs_value_split(plan, in.scaled()) && sp.workers > 1)
     sp.workers /= 2;
   // workers run contiguous runs of items (the value-split kernel takes one
   // item a pair of CTAs, longest first, also under a rows-as-N plan)
-  if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.kv_scales)) {
+  if (plan->kernel == mla::kTcRowsN && !runs_value_split(plan, in.scaled())) {
     sp.worker_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
   } else if (plan->kernel == mla::kTcRowsN) {
     sp.even_first = reinterpret_cast<int32_t*>(ws + l.worker_first);
@@ -411,7 +412,7 @@ mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* s
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* status = reinterpret_cast<int*>(ws + plan->status_offset);
   mla::DecodeParams d = make_params(plan, in);
-  if (plan->schedule == 1 && !runs_unsplit(plan, in.kv_scales)) {
+  if (plan->schedule == 1 && !runs_unsplit(plan, in.scaled())) {
     s = run_schedule(plan, in, ws, stream);
     if (s == MLA_OK) s = run_items(plan, in, sinks, ws, out, lse, stream);
     if (s == MLA_OK) s = run_merge_items(plan, in, sinks, ws, out, lse, stream);
@@ -444,6 +445,28 @@ mla_status_t decode_fwd(const mla_plan_t* plan, const Inputs& in, const float* s
   m.out = out;
   m.lse = lse;
   return cuda_status(mla::launch_merge(m, stream));
+}
+
+// the schedule stage, for the plan's kernel or a scaled call's
+mla_status_t decode_schedule(const mla_plan_t* plan, bool scaled, const int32_t* seq_lens, const int32_t* qo_indptr,
+                             const int32_t* sparse_indptr, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  mla_status_t s = check_scheduled(plan, workspace, workspace_bytes);
+  if (s != MLA_OK) return s;
+  s = check_problem(plan->prob);
+  if (s != MLA_OK) return s;
+  const mla_problem_t& p = plan->prob;
+  if (p.num_tokens == 0) return MLA_OK;
+  if (p.topk == 0) {
+    if (seq_lens == nullptr || !aligned(seq_lens, 4)) return MLA_ERR_INVALID_ARG;
+    if (p.max_qlen > 1 && qo_indptr == nullptr) return MLA_ERR_INVALID_ARG;
+  }
+  Inputs in{};
+  in.scale_group = scaled ? 1 : 0;  // (any: the list does not depend on it)
+  in.seq_lens = seq_lens;
+  in.qo_indptr = p.topk > 0 ? nullptr : qo_indptr;
+  in.slot_indptr = p.topk > 0 ? sparse_indptr : nullptr;
+  return run_schedule(plan, in, static_cast<uint8_t*>(workspace), stream);
 }
 
 mla_status_t decode_items(const mla_plan_t* plan, const Inputs& in, const float* sinks, void* workspace,
@@ -662,8 +685,7 @@ mla_status_t mla_decode_scaled_kernel(const mla_plan_t* plan, int32_t* kernel) {
   const mla_status_t s = check_problem(plan->prob);
   if (s != MLA_OK) return s;
   if (plan->prob.kv_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
-  static const float scales = 1.f;  // (the rule asks whether there are any)
-  *kernel = runs_value_split(plan, &scales) ? mla::kValueSplit : plan->kernel;
+  *kernel = runs_value_split(plan, true) ? mla::kValueSplit : plan->kernel;
   return MLA_OK;
 }
 
@@ -684,21 +706,14 @@ mla_status_t mla_workspace_status(const mla_plan_t* plan, const void* workspace,
 mla_status_t mla_decode_schedule(const mla_plan_t* plan, const int32_t* seq_lens,
                                  const int32_t* qo_indptr, const int32_t* sparse_indptr,
                                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  mla_status_t s = check_scheduled(plan, workspace, workspace_bytes);
-  if (s != MLA_OK) return s;
-  s = check_problem(plan->prob);
-  if (s != MLA_OK) return s;
-  const mla_problem_t& p = plan->prob;
-  if (p.num_tokens == 0) return MLA_OK;
-  if (p.topk == 0) {
-    if (seq_lens == nullptr || !aligned(seq_lens, 4)) return MLA_ERR_INVALID_ARG;
-    if (p.max_qlen > 1 && qo_indptr == nullptr) return MLA_ERR_INVALID_ARG;
-  }
-  Inputs in{};
-  in.seq_lens = seq_lens;
-  in.qo_indptr = p.topk > 0 ? nullptr : qo_indptr;
-  in.slot_indptr = p.topk > 0 ? sparse_indptr : nullptr;
-  return run_schedule(plan, in, static_cast<uint8_t*>(workspace), stream);
+  return decode_schedule(plan, false, seq_lens, qo_indptr, sparse_indptr, workspace, workspace_bytes, stream);
+}
+
+mla_status_t mla_decode_schedule_scaled(const mla_plan_t* plan, const int32_t* seq_lens,
+                                        const int32_t* qo_indptr, const int32_t* sparse_indptr,
+                                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (plan != nullptr && plan->prob.kv_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
+  return decode_schedule(plan, true, seq_lens, qo_indptr, sparse_indptr, workspace, workspace_bytes, stream);
 }
 
 mla_status_t mla_decode_items(const mla_plan_t* plan, const void* q, const void* kv_cache,

@@ -64,8 +64,8 @@ class Call:
         assert B.mla_workspace_status(self.plan, self.ws) == 0
         return self.out.double().cpu().numpy(), self.lse.double().cpu().numpy()
 
-    def schedule(self):
-        B.mla_decode_schedule(self.plan, seq_lens=self.seq, qo_indptr=self.qo, workspace=self.ws)
+    def schedule(self, of=None):
+        (of or B.mla_decode_schedule)(self.plan, seq_lens=self.seq, qo_indptr=self.qo, workspace=self.ws)
 
     def merge(self):
         B.mla_merge_items(self.plan, qo_indptr=self.qo, sinks=self.sinks, workspace=self.ws, out=self.out, lse=self.lse)
@@ -75,9 +75,9 @@ class Call:
         B.mla_decode_fwd_scaled(*self.args, self.scales, scale_group=self.c["g"], **self.kw)
         return self.result()
 
-    def stages_scaled(self):
+    def stages_scaled(self, of=None):
         self.clear()
-        self.schedule()
+        self.schedule(of)
         B.mla_decode_items_scaled(*self.args, self.scales, scale_group=self.c["g"], **self.kw)
         self.merge()
         return self.result()
@@ -363,3 +363,43 @@ def test_rows_as_n_over_more_short_requests_than_one_wave(heads):
     call = Call(c, bound=512)
     assert B.mla_decode_scaled_kernel(call.plan) == 5
     compare(*call.fwd_scaled(), *reference(c))
+
+
+# ---------------------------------------------------------------- whole calls and stages
+
+@pytest.mark.parametrize("heads,lens,qlens", [
+    (128, [40000, 3000, 17, 30000, 9000], None), (113, [9000, 20000, 1, 33000, 700, 23000], None),
+    (128, [30000, 300, 9000], [2, 3, 1]), (64, [10000, 300, 2000], None), (32, [10000, 1, 900], None),
+    (17, [5000, 5000, 0, 70, 6100], None), (16, [9000, 9000, 500], [2, 3, 1])])
+def test_stages_and_whole_calls(heads, lens, qlens):
+    """Rows of many pieces on the value-split kernel: the three stages give a
+    whole call's bits; over the list of mla_decode_schedule, which is that of the
+    plan's own kernel (a cut at every worker's share, slivers too), other bits,
+    as right."""
+    c = decode_case(91, lens, heads, 64, 64, qlens=qlens, sinks=heads == 64)
+    call = Call(c)
+    assert B.mla_decode_scaled_kernel(call.plan) == 6 and call.plan.schedule == 1
+    ref = reference(c)
+    a = call.fwd_scaled()
+    compare(*a, *ref)
+    b = call.stages_scaled(B.mla_decode_schedule_scaled)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    mine = call.ws[256:call.plan.segm_output_offset].clone()
+    compare(*call.stages_scaled(), *ref)
+    if call.plan.kernel == 5:
+        assert not torch.equal(mine, call.ws[256:call.plan.segm_output_offset])
+
+
+def test_a_list_serves_calls_until_another_replaces_it():
+    """Stages over one list, twice, around an unsplit whole call, which leaves
+    the list alone."""
+    c = decode_case(92, [300, 5, 129, 512], 128, 64, 16)
+    call = Call(c)
+    a = call.stages_scaled()
+    compare(*a, *reference(c))
+    compare(*call.fwd_scaled(), *reference(c))
+    call.clear()
+    B.mla_decode_items_scaled(*call.args, call.scales, scale_group=c["g"], **call.kw)
+    call.merge()
+    b = call.result()
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])

@@ -216,3 +216,15 @@ def test_kernel_of_a_scaled_call_refuses(lib):
     with pytest.raises(B.MLAError) as e:
         B.mla_decode_scaled_kernel(_plan(dtype="bf16"))
     assert e.value.status == B.MLA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(sl=None), 1), (dict(sl=P + 2), 1), (dict(ws=None), 3), (dict(nbytes=8), 3), (dict(ws=P + 16), 1)])
+def test_schedule_scaled_refuses(lib, kw, status):
+    a = dict(sl=P, ws=P, nbytes=1 << 40)
+    a.update(kw)
+    call = lambda p: lib.mla_decode_schedule_scaled(p, a["sl"], None, None, a["ws"], a["nbytes"], None)
+    assert call(ctypes.byref(_plan())) == status
+    assert call(None) == B.MLA_ERR_INVALID_ARG
+    assert call(ctypes.byref(_plan(num_segments=2))) == B.MLA_ERR_INVALID_ARG
+    assert call(ctypes.byref(_plan(dtype="bf16"))) == B.MLA_ERR_UNSUPPORTED

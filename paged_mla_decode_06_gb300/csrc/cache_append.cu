@@ -10,10 +10,13 @@
 // k the least integer with a <= 448 2^k, and the rows are stored as
 // e4m3(x / s), saturating. (The decode weighs groups against each other in
 // fp32, which scales within 2^60 of one on either side allow.) Where s grew,
-// the rows before the run are requantised by s_old / s. Scales made here are powers of two, so that this changes no code
-// but those that fall below e4m3's normal range: a group that grows again and
-// again loses no more than one that grew once. (A floating-point format gains
-// nothing from a finer scale but part of a binade of range.)
+// the rows before the run are requantised by s_old / s. Scales made here are
+// powers of two, so that this changes no code but those that fall below e4m3's
+// normal range. Those are rounded once more at each growth, by half of the
+// smallest step of the scale of the time: however often a group grows, what is
+// stored stays within one smallest step (2^-9 of the scale) of the row, where
+// one rounding leaves half a step. (A floating-point format gains nothing from
+// a finer scale but part of a binade of range.)
 //
 // What bounds it: memory, 1152 bytes read and 576 written a token, once a call
 // is larger than its latency (slots, then rows, then codes: three trips). The

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
     // ---- mask, chunk max
     const int c0 = seg_start + c * C::kKC;
     float mx[2] = {-INFINITY, -INFINITY};
-    float inv[C::kNTS][2];  // GS: 1 / scale of this thread's keys, 0 where there is none
+    float inv[C::kNTS][2];  // GS: 1 / scale of this thread's keys (1 where there is none: its weight is 0)
 #pragma unroll
     for (int n = 0; n < C::kNTS; ++n) {
 #pragma unroll

@@ -403,3 +403,29 @@ def test_a_list_serves_calls_until_another_replaces_it():
     call.merge()
     b = call.result()
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+# ---------------------------------------------------------------- groups that grow
+
+@pytest.mark.parametrize("g,rise", [(8, 0.5), (8, 2.0), (64, 0.125), (64, 0.4)])
+def test_append_groups_that_grow_keep_within_a_smallest_step(g, rise):
+    """Rows of rising size, one call each. A value that ends in the normal range
+    was rounded once: 2^-4 of it. One that ends below was rounded to a grid of
+    its own at first and then to the smallest step of each later scale, half a
+    step each time, of steps that are different powers of two up to the last
+    one's u: u/2 + u/4 + ... < u = 2^-9 of the scale."""
+    rng = np.random.default_rng(95)
+    n = min(g, 40)
+    rows = rng.standard_normal((n, 576)) * np.exp2(rise * np.arange(n))[:, None]
+    t = torch.from_numpy(rows.astype(np.float32)).bfloat16()
+    x, kv = t.double().numpy(), t.cuda()
+    cache, sc = torch.zeros((1, 64, 576), dtype=torch.uint8, device="cuda"), torch.zeros(64 // g, device="cuda")
+    for i in range(n):
+        B.mla_cache_append(kv[i:i + 1, :512], kv[i:i + 1, 512:], dev([i], np.int32), cache, sc, scale_group=g)
+    torch.cuda.synchronize()
+    s = float(sc[0])
+    assert s >= np.abs(x).max() / 448.0
+    off = np.abs(O.decode_e4m3fn(cache.view(-1, 576)[:n].cpu().numpy()) * s - x)
+    assert (off <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -9 * s)).all()
+    small = np.abs(x) < 2.0 ** -6 * s
+    assert rise < 0.3 or (off[small] > 2.0 ** -10 * s).any()   # (more than one rounding leaves: the case is met)

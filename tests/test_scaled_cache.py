@@ -228,3 +228,18 @@ def test_schedule_scaled_refuses(lib, kw, status):
     assert call(None) == B.MLA_ERR_INVALID_ARG
     assert call(ctypes.byref(_plan(num_segments=2))) == B.MLA_ERR_INVALID_ARG
     assert call(ctypes.byref(_plan(dtype="bf16"))) == B.MLA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("g,rise", [(8, 2.0), (64, 0.4)])
+def test_groups_that_grow_keep_within_a_smallest_step(g, rise):
+    """Rounded again at each growth: half a smallest step of every scale since,
+    less than one of the last in all."""
+    rng = np.random.default_rng(95)
+    n = min(g, 40)
+    x = rng.standard_normal((n, 576)) * np.exp2(rise * np.arange(n))[:, None]
+    codes, scales = np.zeros((64, 576), np.uint8), np.zeros(64 // g)
+    for i in range(n):
+        codes, scales = S.cache_append(x[i:i + 1], [i], codes, scales, g)
+    off = np.abs(O.decode_e4m3fn(codes[:n]) * scales[0] - x)
+    assert (off <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -9 * scales[0])).all()
+    assert (off[np.abs(x) < 2.0 ** -6 * scales[0]] > 2.0 ** -10 * scales[0]).any()   # (the case is met)

@@ -133,13 +133,13 @@ PROFILED_TRAFFIC = {
     },
     (5, "fp8", 16): {  # decode_hn.cu, e4m3 batch at 16 heads (profiles/decode_hn_fp8.md)
         "source": "decode_hn.cu",
-        "code_sha256": "c94a8a98566852ff49137bdd25f14266eec37a09946714c21ece6ebbcbc73fb3",
-        "dram_per_alg_byte": (226.829568 + 3.854336) / 226.738272,
+        "code_sha256": "83249ff255d7f132f4904c3ba508e1279cadc75e47b6643e91502954249c9e33",
+        "dram_per_alg_byte": (226.828800 + 3.382784) / 226.738272,
     },
-    (5, "fp8", 128): {  # decode_hn.cu on CTA-pair clusters, e4m3 batch at 128 heads (same file)
+    (5, "fp8", 128): {  # decode_hn.cu on clusters of two CTAs, e4m3 batch at 128 heads (same file)
         "source": "decode_hn.cu",
-        "code_sha256": "c94a8a98566852ff49137bdd25f14266eec37a09946714c21ece6ebbcbc73fb3",
-        "dram_per_alg_byte": (228.464384 + 4.723200) / 228.286560,
+        "code_sha256": "83249ff255d7f132f4904c3ba508e1279cadc75e47b6643e91502954249c9e33",
+        "dram_per_alg_byte": (229.603072 + 7.410944) / 228.286560,
     },
 }
 

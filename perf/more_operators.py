@@ -273,7 +273,7 @@ def _prepare_pages(c, rng, gen):
                  count=torch.empty(1, dtype=torch.int32, device="cuda"))
         if own:
             from paged_mla_decode_06_gb300 import binding as B
-            s["workspace"] = torch.empty(B.mla_cache_workspace(N), dtype=torch.uint8, device="cuda")
+            s["workspace"] = torch.zeros(B.mla_cache_workspace(N), dtype=torch.uint8, device="cuda")
         return s
     parent = np.repeat(np.arange(P), S)
     s.update(parent=_i32(parent), child=_i32(P + rng.permutation(P * S)), lens=_i32(ctx[parent]),
@@ -283,7 +283,7 @@ def _prepare_pages(c, rng, gen):
                  count=torch.empty(1, dtype=torch.int32, device="cuda"))
         if own:
             from paged_mla_decode_06_gb300 import binding as B
-            s["workspace"] = torch.empty(B.mla_cache_workspace(N), dtype=torch.uint8, device="cuda")
+            s["workspace"] = torch.zeros(B.mla_cache_workspace(N), dtype=torch.uint8, device="cuda")
     return s
 
 

@@ -598,6 +598,169 @@ MLA_API mla_status_t mla_cache_append(const void* c_kv, int64_t c_kv_stride, con
                                       int32_t scale_group, void* kv_cache, float* kv_scales,
                                       cudaStream_t stream);
 
+/*
+ * mla_rope_plan -- the rotary frequencies of a model, made once on the host.
+ * Pair i of the dim / 2 turns by p * f_i at position p:
+ *   NONE    f_i = base^(-2 i / dim)
+ *   LINEAR  f_i / factor (positions interpolated)
+ *   YARN    f_i / factor * r_i + f_i * (1 - r_i), r_i rising linearly from 0 at pair
+ *           floor(c(beta_fast)) (at least 0) to 1 at pair ceil(c(beta_slow)) (at
+ *           most dim - 1), c(b) = dim ln(original_max_position / (2 pi b)) / (2 ln
+ *           base) the pair that makes b turns over the original context; cosine
+ *           and sine times g(mscale) / g(mscale_all_dim), g(m) = 0.1 m ln factor + 1
+ *           (1 where factor <= 1)
+ * Host only. Errors: MLA_ERR_INVALID_ARG for NULL, an odd dim or one outside 2 ..
+ * 64, a bad enum, base <= 1, and, where they are used, factors, betas or an
+ * original_max_position that are not positive, beta_fast < beta_slow, a negative
+ * mscale.
+ */
+typedef enum {
+  MLA_ROPE_INTERLEAVED = 0,    /* pair i: columns 2 i and 2 i + 1 */
+  MLA_ROPE_HALF = 1            /* pair i: columns i and i + dim / 2 */
+} mla_rope_layout_t;
+
+typedef enum {
+  MLA_ROPE_SCALING_NONE = 0,
+  MLA_ROPE_SCALING_LINEAR = 1,
+  MLA_ROPE_SCALING_YARN = 2
+} mla_rope_scaling_t;
+
+typedef struct {
+  int32_t dim;                 /* rotated columns of the 64: the first dim, even */
+  int32_t layout;              /* mla_rope_layout_t */
+  int32_t scaling;             /* mla_rope_scaling_t */
+  int32_t original_max_position; /* YARN: context that the model was trained on */
+  double base;
+  double factor;               /* LINEAR, YARN */
+  double beta_fast, beta_slow; /* YARN: commonly 32 and 1 */
+  double mscale, mscale_all_dim; /* YARN: 0 for none */
+} mla_rope_problem_t;
+
+typedef struct {
+  mla_rope_problem_t prob;
+  float mscale;                /* factor of cosine and sine */
+  double turns[32];            /* f_i / (2 pi) */
+} mla_rope_t;
+
+MLA_API mla_status_t mla_rope_plan(const mla_rope_problem_t* prob, mla_rope_t* rope);
+
+/*
+ * mla_rope_qk -- the rotary positions of a step, queries and keys, and with them
+ * the q pre-step of mla_concat_quant_q:
+ *   q_out[t, h, 0:512]   = ql_nope[t, h, :]
+ *   q_out[t, h, 512:576] = rotation of q_pe[t, h, :] by positions[t]
+ * as bf16, or as e4m3 codes of (value * (1 / q_scale)) rounded to nearest even
+ * with magnitudes above 448 saturated; and k_out[t, :] = rotation of k_pe[t, :] in
+ * bf16, the k_pe of mla_cache_append. Angles are formed in 64 bits, whatever the
+ * position; the rotation in fp32, rounded once. Columns from dim on pass. Tokens with a negative
+ * position (mla_block_tables gives the padding of a captured batch -1) are
+ * left as they were in q_out and k_out.
+ *   positions [T] int32
+ *   ql_nope [T, H, 512], q_pe [T, H, 64] bf16 in any strides (elements): the
+ *           absorbed queries as a product over heads leaves them, a slice of the
+ *           projection's rows; num_heads 0: no queries
+ *   q_out   [T, H, 576] contiguous, in out_dtype, not overlapping the inputs
+ *   k_pe    [T, 64] bf16, row stride k_pe_stride, or NULL: no keys; k_out [T, 64]
+ *           bf16, row stride k_out_stride: k_pe itself, or not overlapping it
+ * The last dims are contiguous; ql_nope and q_out 16-byte aligned, the strides of
+ * ql_nope multiples of 8; q_pe, k_pe and k_out 4-byte aligned, their strides
+ * even. One launch on `stream`. Errors: MLA_ERR_INVALID_ARG (also where neither
+ * queries nor keys are given), MLA_ERR_CUDA.
+ */
+MLA_API mla_status_t mla_rope_qk(const mla_rope_t* rope, const int32_t* positions, int32_t num_tokens,
+                                 int32_t num_heads, const void* ql_nope, int64_t nope_stride_t,
+                                 int64_t nope_stride_h, const void* q_pe, int64_t pe_stride_t,
+                                 int64_t pe_stride_h, int32_t out_dtype, float q_scale, void* q_out,
+                                 const void* k_pe, int64_t k_pe_stride, void* k_out, int64_t k_out_stride,
+                                 cudaStream_t stream);
+
+/*
+ * The pages of requests that share them. ref_counts [num_blocks] int32 holds, for
+ * each physical block, the number of table cells that hold it: 0 for a free block, 1
+ * for one that mla_block_tables took from the free list (the caller sets that), more
+ * after forks. A block with more than one reference is only read: the
+ * step's tokens go into a request's own last block, which forking copies. The four
+ * calls take the cache as kv_cache [num_blocks, block_size, 576] in kv_dtype with
+ * kv_scales [num_blocks * block_size / scale_group] fp32, or NULL and scale_group 0
+ * for a cache without group scales.
+ *
+ * mla_cache_fork -- fork i makes table row child[i] a copy of row parent[i] for the
+ * first lens[i] tokens: its whole blocks (lens[i] / block_size of them) are shared,
+ * their counts raised by one; a partly filled last block is copied into the next
+ * entry of free_blocks (forks in order, from entry 0; its count becomes 1): its
+ * rows lens[i] % block_size and the scales of the groups that hold them, nothing
+ * behind. Cells behind, and the rows of other requests, are left as they were.
+ * Where the list is too short the last cell becomes -1 and nothing is copied; where
+ * the parent's cell is negative the child's is -1 and no entry is taken. *taken
+ * receives the number of entries wanted, as mla_block_tables' does. Forks whose parent or child is
+ * outside [0, num_rows) are passed over. A parent may be forked many times; the children must
+ * be distinct, free rows (mla_cache_free), none of them a parent of the same call.
+ *   parent, child, lens [num_forks] int32; block_table [num_rows,
+ *   max_blocks_per_req] int32, row stride block_table_stride; taken [1]
+ * One launch. Errors of all four: MLA_ERR_INVALID_ARG for bad sizes, strides or
+ * enums, NULL or misaligned pointers (kv_cache 16-byte, workspace 256-byte
+ * aligned), scales without e4m3 or without a group that divides the block;
+ * MLA_ERR_UNSUPPORTED for more than INT32_MAX slots; MLA_ERR_WORKSPACE.
+ */
+MLA_API mla_status_t mla_cache_fork(const int32_t* parent, const int32_t* child, const int32_t* lens,
+                                    int32_t num_forks, const int32_t* free_blocks, int32_t num_free,
+                                    int32_t* block_table, int64_t block_table_stride, int32_t num_rows,
+                                    int32_t max_blocks_per_req, int32_t* ref_counts, int32_t num_blocks,
+                                    int32_t block_size, int32_t kv_dtype, int32_t scale_group, void* kv_cache,
+                                    float* kv_scales, int32_t* taken, cudaStream_t stream);
+
+/*
+ * mla_cache_copy_blocks -- whole blocks src[i] to dst[i], with their scales. Pairs
+ * with a member outside [0, num_blocks) are passed over; the dst must be distinct and none of them
+ * a src. src, dst [num_pairs] int32. One launch.
+ */
+MLA_API mla_status_t mla_cache_copy_blocks(const int32_t* src, const int32_t* dst, int32_t num_pairs,
+                                           int32_t num_blocks, int32_t block_size, int32_t kv_dtype,
+                                           int32_t scale_group, void* kv_cache, float* kv_scales,
+                                           cudaStream_t stream);
+
+/* Workspace bytes of mla_cache_free and mla_cache_compact for a pool of num_blocks;
+ * 0 for num_blocks <= 0. Zero it once after allocating. One call at a time may use
+ * a workspace; calls on one stream follow one another. */
+MLA_API size_t mla_cache_workspace(int32_t num_blocks);
+
+/*
+ * mla_cache_free -- gives up the table rows rows[i]: their cells become -1, the
+ * counts of the blocks in them fall, and the blocks that no cell holds any more go
+ * to freed, in ascending order. Row i's columns are the ceil(lens[i] /
+ * block_size) first ones, or all of them with lens NULL; negative cells are
+ * passed over, and so are row numbers outside [0, num_rows). A row that is listed
+ * twice is given up once. *num_freed receives the number of freed blocks; where it
+ * exceeds `capacity`, those beyond are not listed.
+ *   rows [num_listed] int32, lens [num_listed] int32 or NULL, freed [capacity]
+ *   int32, num_freed [1], workspace of mla_cache_workspace(num_blocks) bytes
+ * One launch.
+ */
+MLA_API mla_status_t mla_cache_free(const int32_t* rows, const int32_t* lens, int32_t num_listed,
+                                    int32_t* block_table, int64_t block_table_stride, int32_t num_rows,
+                                    int32_t max_blocks_per_req, int32_t* ref_counts, int32_t num_blocks,
+                                    int32_t block_size, int32_t* freed, int32_t capacity, int32_t* num_freed,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * mla_cache_compact -- moves the blocks in use (count above 0) together: with L of
+ * them, the used blocks from L on, in ascending order, go to the unused ones below L, in
+ * ascending order. Afterwards blocks [0, L) are in use and the free list is L,
+ * L + 1, ... block_table_out is block_table with the moved blocks' new numbers, every
+ * column of every row (cells that name no block in use are copied as they
+ * are); ref_counts_out the counts, 0 from L on. Both may be the inputs
+ * themselves, or must not overlap them. *num_live receives L. The contents of blocks
+ * from L on stay as they were.
+ * Two launches, the number of moves known to the GPU alone.
+ */
+MLA_API mla_status_t mla_cache_compact(const int32_t* ref_counts, int32_t* ref_counts_out,
+                                       const int32_t* block_table, int64_t block_table_stride,
+                                       int32_t* block_table_out, int64_t block_table_out_stride,
+                                       int32_t num_rows, int32_t max_blocks_per_req, int32_t num_blocks,
+                                       int32_t block_size, int32_t kv_dtype, int32_t scale_group,
+                                       void* kv_cache, float* kv_scales, int32_t* num_live, void* workspace,
+                                       size_t workspace_bytes, cudaStream_t stream);
+
 /* Largest plan->workspace_bytes that mla_decode_fwd_static accepts. */
 #define MLA_STATIC_SCRATCH_BYTES ((size_t)64 << 20) /* 64 MiB */
 

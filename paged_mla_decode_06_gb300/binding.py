@@ -28,6 +28,12 @@ MLA_KERNEL_WARP_MMA = 1
 MLA_KERNEL_TCGEN05 = 2
 MLA_KERNEL_TCGEN05_ROWS_N = 3
 
+MLA_ROPE_INTERLEAVED = 0
+MLA_ROPE_HALF = 1
+MLA_ROPE_SCALING_NONE = 0
+MLA_ROPE_SCALING_LINEAR = 1
+MLA_ROPE_SCALING_YARN = 2
+
 HEAD_DIM = 576
 KV_LORA_RANK = 512
 
@@ -56,6 +62,15 @@ class Plan(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t), ("status_offset", ctypes.c_size_t),
         ("segm_output_offset", ctypes.c_size_t), ("segm_max_offset", ctypes.c_size_t),
         ("segm_expsum_offset", ctypes.c_size_t)]
+
+
+class RopeProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dim", "layout", "scaling", "original_max_position")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow", "mscale", "mscale_all_dim")]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("prob", RopeProblem), ("mscale", ctypes.c_float), ("turns", ctypes.c_double * 32)]
 
 
 _lib = None
@@ -138,6 +153,24 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mla_block_tables.restype = st
         lib.mla_cache_append.argtypes = [_vp, i64, _vp, i64, _vp, i32, i32, i32, i32, _vp, _vp, _vp]
         lib.mla_cache_append.restype = st
+        lib.mla_rope_plan.argtypes = [ctypes.POINTER(RopeProblem), ctypes.POINTER(Rope)]
+        lib.mla_rope_plan.restype = st
+        lib.mla_rope_qk.argtypes = [ctypes.POINTER(Rope), _vp, i32, i32, _vp, i64, i64, _vp, i64, i64, i32, f32,
+                                    _vp, _vp, i64, _vp, i64, _vp]
+        lib.mla_rope_qk.restype = st
+        lib.mla_cache_fork.argtypes = [_vp, _vp, _vp, i32, _vp, i32, _vp, i64, i32, i32, _vp, i32, i32, i32, i32,
+                                       _vp, _vp, _vp, _vp]
+        lib.mla_cache_fork.restype = st
+        lib.mla_cache_copy_blocks.argtypes = [_vp, _vp, i32, i32, i32, i32, i32, _vp, _vp, _vp]
+        lib.mla_cache_copy_blocks.restype = st
+        lib.mla_cache_workspace.argtypes = [i32]
+        lib.mla_cache_workspace.restype = ctypes.c_size_t
+        lib.mla_cache_free.argtypes = [_vp, _vp, i32, _vp, i64, i32, i32, _vp, i32, i32, _vp, i32, _vp, _vp,
+                                       ctypes.c_size_t, _vp]
+        lib.mla_cache_free.restype = st
+        lib.mla_cache_compact.argtypes = [_vp, _vp, _vp, i64, _vp, i64, i32, i32, i32, i32, i32, i32, _vp, _vp, _vp,
+                                          _vp, ctypes.c_size_t, _vp]
+        lib.mla_cache_compact.restype = st
         lib.mla_workspace_status.argtypes = [ctypes.POINTER(Plan), _vp, ctypes.POINTER(ctypes.c_int32),
                                              ctypes.c_int32, _vp]
         lib.mla_workspace_status.restype = st
@@ -590,6 +623,213 @@ def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_gro
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status:
         _check("mla_cache_append", status)
+
+
+def mla_rope_plan(*, dim: int = 64, layout: str = "interleaved", base: float = 10000.0, scaling: str = "none",
+                  factor: float = 1.0, original_max_position: int = 4096, beta_fast: float = 32.0,
+                  beta_slow: float = 1.0, mscale: float = 0.0, mscale_all_dim: float = 0.0) -> Rope:
+    """The rotary frequencies of a model: ``layout`` "interleaved" or "half",
+    ``scaling`` "none", "linear" or "yarn"."""
+    lib = _lib or load_library()
+    layouts = {"interleaved": MLA_ROPE_INTERLEAVED, "half": MLA_ROPE_HALF}
+    scalings = {"none": MLA_ROPE_SCALING_NONE, "linear": MLA_ROPE_SCALING_LINEAR, "yarn": MLA_ROPE_SCALING_YARN}
+    for value, known in ((layout, layouts), (scaling, scalings)):
+        if value not in known:
+            raise MLAError("mla_rope_plan", MLA_ERR_INVALID_ARG, f"{value!r} is none of {sorted(known)}")
+    prob = RopeProblem(dim=dim, layout=layouts[layout], scaling=scalings[scaling],
+                       original_max_position=original_max_position, base=base, factor=factor,
+                       beta_fast=beta_fast, beta_slow=beta_slow, mscale=mscale, mscale_all_dim=mscale_all_dim)
+    rope = Rope()
+    _check("mla_rope_plan", lib.mla_rope_plan(ctypes.byref(prob), ctypes.byref(rope)))
+    return rope
+
+
+def _last_dense(t) -> bool:
+    return t.shape[-1] <= 1 or t.stride(-1) == 1
+
+
+def mla_rope_qk(rope: Rope, positions, *, ql_nope=None, q_pe=None, q_out=None, q_scale: float | None = None,
+                k_pe=None, k_out=None, stream=None) -> None:
+    """``q_out [T, H, 576]`` = ``ql_nope || rotated q_pe`` (bf16, or e4m3 codes of
+    q / ``q_scale`` when that is given), and ``k_out [T, 64]`` = rotated ``k_pe``
+    (which may be ``k_out`` itself); either may be left out."""
+    lib = _lib or load_library()
+    torch = _torch or _load_torch()
+    i32, b16 = torch.int32, torch.bfloat16
+    codes = (b16,) if q_scale is None else (torch.float8_e4m3fn, torch.uint8)
+    rope_cols = HEAD_DIM - KV_LORA_RANK
+    dev, T, H = positions.get_device(), positions.numel(), 0
+    ok = (dev >= 0 and dev == torch._C._cuda_getDevice() and positions.dtype is i32 and positions.is_contiguous()
+          and (ql_nope is None) == (q_pe is None) == (q_out is None) and (k_pe is None) == (k_out is None)
+          and (ql_nope is not None or k_pe is not None))
+    nope = pe = out = keys = kout = None
+    n_st = p_st = (0, 0, 0)
+    k_st = ko_st = rope_cols
+    if ok and ql_nope is not None:
+        H = ql_nope.shape[1] if ql_nope.dim() == 3 else 0
+        ok = (H > 0 and ql_nope.shape == (T, H, KV_LORA_RANK) and ql_nope.dtype is b16 and ql_nope.get_device() == dev
+              and _last_dense(ql_nope) and q_pe.shape == (T, H, rope_cols) and q_pe.dtype is b16
+              and q_pe.get_device() == dev and _last_dense(q_pe) and q_out.shape == (T, H, HEAD_DIM)
+              and q_out.dtype in codes and q_out.get_device() == dev and q_out.is_contiguous())
+        nope, pe, out, n_st, p_st = ql_nope.data_ptr(), q_pe.data_ptr(), q_out.data_ptr(), ql_nope.stride(), q_pe.stride()
+    if ok and k_pe is not None:
+        ok = (k_pe.shape == (T, rope_cols) and k_pe.dtype is b16 and k_pe.get_device() == dev and _last_dense(k_pe)
+              and k_out.shape == (T, rope_cols) and k_out.dtype is b16 and k_out.get_device() == dev
+              and _dense_rows(k_out.shape, k_out.stride(), 1))
+        keys, kout = k_pe.data_ptr(), k_out.data_ptr()
+        if T > 1:
+            k_st, ko_st = k_pe.stride(0), k_out.stride(0)
+    fn = "mla_rope_qk"
+    if not ok:
+        named = [("ql_nope", ql_nope, (b16,)), ("q_pe", q_pe, (b16,)), ("q_out", q_out, codes), ("k_pe", k_pe, (b16,)),
+                 ("k_out", k_out, (b16,))]
+        given = [t is not None for _, t, _ in named]
+        _refuse(fn, dev, [("positions", positions, (i32,))] + named,
+                [(positions.is_contiguous(), "positions must be contiguous"),
+                 (given[0] == given[1] == given[2], "ql_nope, q_pe and q_out go together"),
+                 (given[3] == given[4], "k_pe and k_out go together"),
+                 (given[0] or given[3], "neither queries nor keys")] +
+                [(t is None or _last_dense(t), f"the last dimension of {n} must be contiguous") for n, t, _ in named] +
+                [(False, f"the shapes must be [{T}, H, 512], [{T}, H, 64] and contiguous [{T}, H, 576]; [{T}, 64] with "
+                         "rows of k_out that do not overlap")])
+    status = lib.mla_rope_qk(
+        ctypes.byref(rope), positions.data_ptr(), T, H, nope, n_st[0], n_st[1], pe, p_st[0], p_st[1],
+        MLA_DTYPE_BF16 if q_scale is None else MLA_DTYPE_FP8_E4M3, 1.0 if q_scale is None else q_scale, out, keys, k_st,
+        kout, ko_st, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
+
+
+# The calls on the pages of a cache.
+
+def _pages_args(fn: str, kv_cache, kv_scales, scale_group):
+    """(device, num_blocks, block_size, dtype code) of a cache, checked."""
+    torch = _torch or _load_torch()
+    dev, shape, kind = kv_cache.get_device(), kv_cache.shape, kv_cache.dtype
+    fp8 = kind is torch.uint8 or kind is torch.float8_e4m3fn
+    nb, bs, width = shape if len(shape) == 3 else (0, 0, 0)
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and (fp8 or kind is torch.bfloat16) and width == HEAD_DIM
+            and kv_cache.is_contiguous() and (kv_scales is not None) == (scale_group > 0)
+            and (kv_scales is None
+                 or (fp8 and bs % scale_group == 0 and kv_scales.dtype is torch.float32
+                     and kv_scales.get_device() == dev and kv_scales.is_contiguous()
+                     and kv_scales.numel() == nb * bs // scale_group))):
+        _refuse(fn, dev, [("kv_cache", kv_cache, (torch.bfloat16, torch.float8_e4m3fn, torch.uint8)),
+                          ("kv_scales", kv_scales, (torch.float32,))],
+                [(width == HEAD_DIM, f"kv_cache must be [num_blocks, block_size, {HEAD_DIM}]"),
+                 (kv_cache.is_contiguous(), "kv_cache must be contiguous"),
+                 ((kv_scales is not None) == (scale_group > 0), "kv_scales and scale_group go together"),
+                 (kv_scales is None or fp8, "a cache with group scales is e4m3"),
+                 (scale_group <= 0 or bs % scale_group == 0, "scale_group must divide the block size"),
+                 (False, "kv_scales must be contiguous and hold num_blocks * block_size / scale_group scales")])
+    return dev, nb, bs, MLA_DTYPE_FP8_E4M3 if fp8 else MLA_DTYPE_BF16
+
+
+def _int_lists(fn: str, dev: int, tables, lists):
+    """``tables`` [(name, 2-D int32 tensor)], ``lists`` [(name, contiguous int32
+    tensor or None, size or None)] on device ``dev``."""
+    i32 = _torch.int32
+    for name, t, n in lists:
+        if t is not None and not (t.dtype is i32 and t.get_device() == dev and t.is_contiguous()
+                                  and (n is None or t.numel() == n)):
+            _refuse(fn, dev, [(name, t, (i32,))], [(t.is_contiguous(), f"{name} must be contiguous"),
+                                                   (False, f"{name} must hold {n} numbers")])
+    for name, t in tables:
+        if not (t.dtype is i32 and t.get_device() == dev and t.dim() == 2 and _dense_rows(t.shape, t.stride(), 1)):
+            _refuse(fn, dev, [(name, t, (i32,))],
+                    [(False, f"{name} must be [rows, columns] with dense rows that do not overlap")])
+
+
+def _table_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def mla_cache_workspace(num_blocks: int) -> int:
+    """Workspace bytes (zeroed once) of mla_cache_free and mla_cache_compact."""
+    return (_lib or load_library()).mla_cache_workspace(num_blocks)
+
+
+def mla_cache_fork(parent, child, lens, free_blocks, block_table, ref_counts, kv_cache, kv_scales=None, *,
+                   scale_group: int = 0, taken, stream=None) -> None:
+    """Table rows ``child`` as copies of rows ``parent`` for the first ``lens`` tokens:
+    whole blocks shared, a partly filled last one copied into the next entry of
+    ``free_blocks`` (None: no free block)."""
+    lib, fn = _lib or load_library(), "mla_cache_fork"
+    dev, nb, bs, code = _pages_args(fn, kv_cache, kv_scales, scale_group)
+    n = parent.numel()
+    _int_lists(fn, dev, [("block_table", block_table)],
+               [("parent", parent, n), ("child", child, n), ("lens", lens, n), ("free_blocks", free_blocks, None),
+                ("ref_counts", ref_counts, nb), ("taken", taken, 1)])
+    rows, cols = block_table.shape
+    status = lib.mla_cache_fork(
+        parent.data_ptr(), child.data_ptr(), lens.data_ptr(), n, _ptr(free_blocks),
+        0 if free_blocks is None else free_blocks.numel(), block_table.data_ptr(), _table_stride(block_table), rows, cols,
+        ref_counts.data_ptr(), nb, bs, code, scale_group, kv_cache.data_ptr(), _ptr(kv_scales), taken.data_ptr(),
+        _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
+
+
+def mla_cache_copy_blocks(src, dst, kv_cache, kv_scales=None, *, scale_group: int = 0, stream=None) -> None:
+    """Blocks ``src`` of the cache, with their scales, to blocks ``dst``."""
+    lib, fn = _lib or load_library(), "mla_cache_copy_blocks"
+    dev, nb, bs, code = _pages_args(fn, kv_cache, kv_scales, scale_group)
+    n = src.numel()
+    _int_lists(fn, dev, [], [("src", src, n), ("dst", dst, n)])
+    status = lib.mla_cache_copy_blocks(
+        src.data_ptr(), dst.data_ptr(), n, nb, bs, code, scale_group, kv_cache.data_ptr(), _ptr(kv_scales),
+        _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
+
+
+def mla_cache_free(rows, block_table, ref_counts, *, lens=None, block_size: int = 1, freed, num_freed, workspace,
+                   stream=None) -> None:
+    """Gives up the table rows ``rows``, all their columns or those of ``lens`` tokens
+    in blocks of ``block_size``; the blocks that no row holds any more go to
+    ``freed``, in ascending order, their number to ``num_freed``."""
+    lib, fn = _lib or load_library(), "mla_cache_free"
+    torch = _torch or _load_torch()
+    dev, n = block_table.get_device(), rows.numel()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and workspace.get_device() == dev
+            and workspace.is_contiguous()):
+        _refuse(fn, dev, [("workspace", workspace, (workspace.dtype,))], [(False, "workspace must be contiguous")])
+    _int_lists(fn, dev, [("block_table", block_table)],
+               [("rows", rows, n), ("lens", lens, n), ("ref_counts", ref_counts, None), ("freed", freed, None),
+                ("num_freed", num_freed, 1)])
+    num_rows, cols = block_table.shape
+    status = lib.mla_cache_free(
+        rows.data_ptr(), _ptr(lens), n, block_table.data_ptr(), _table_stride(block_table), num_rows, cols,
+        ref_counts.data_ptr(), ref_counts.numel(), block_size, freed.data_ptr(), freed.numel(), num_freed.data_ptr(),
+        workspace.data_ptr(), _ws_bytes(workspace),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
+
+
+def mla_cache_compact(ref_counts, block_table, kv_cache, kv_scales=None, *, scale_group: int = 0, refs_out=None,
+                      table_out=None, num_live, workspace, stream=None) -> None:
+    """Moves the blocks in use to the front of the pool. ``refs_out`` and
+    ``table_out`` receive the counts and the tables (None: in place), ``num_live``
+    the number of blocks in use."""
+    lib, fn = _lib or load_library(), "mla_cache_compact"
+    dev, nb, bs, code = _pages_args(fn, kv_cache, kv_scales, scale_group)
+    refs_out = ref_counts if refs_out is None else refs_out
+    table_out = block_table if table_out is None else table_out
+    if not (workspace.get_device() == dev and workspace.is_contiguous() and block_table.shape == table_out.shape):
+        _refuse(fn, dev, [("workspace", workspace, (workspace.dtype,))],
+                [(workspace.is_contiguous(), "workspace must be contiguous"),
+                 (False, "table_out must have block_table's shape")])
+    _int_lists(fn, dev, [("block_table", block_table), ("table_out", table_out)],
+               [("ref_counts", ref_counts, nb), ("refs_out", refs_out, nb), ("num_live", num_live, 1)])
+    rows, cols = block_table.shape
+    status = lib.mla_cache_compact(
+        ref_counts.data_ptr(), refs_out.data_ptr(), block_table.data_ptr(), _table_stride(block_table),
+        table_out.data_ptr(), _table_stride(table_out), rows, cols, nb, bs, code, scale_group, kv_cache.data_ptr(),
+        _ptr(kv_scales), num_live.data_ptr(), workspace.data_ptr(), _ws_bytes(workspace),
+        _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
 
 
 def mla_fit_kpool_indices(token_indices, *, topk: int, out, stream=None) -> None:

@@ -486,6 +486,10 @@ mla_status_t decode_items(const mla_plan_t* plan, const Inputs& in, const float*
 
 }  // namespace
 
+namespace mla {
+void record_cuda_error(cudaError_t e) { cuda_status(e); }
+}  // namespace mla
+
 extern "C" {
 
 const char* mla_status_string(mla_status_t s) {

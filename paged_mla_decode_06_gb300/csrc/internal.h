@@ -182,6 +182,87 @@ struct AppendParams {
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
 
+// Rotary positions and the q pre-step (rope.cu).
+struct RopeParams {
+  const int32_t* positions;    // [T]; negative: padding
+  int32_t num_tokens, num_heads;
+  const void* nope;            // [T, H, 512] bf16, strides in elements
+  int64_t nope_st, nope_sh;
+  const void* pe;              // [T, H, 64] bf16
+  int64_t pe_st, pe_sh;
+  int32_t fp8;                 // 1: e4m3 codes of q * q_inv; 0: bf16
+  float q_inv;
+  void* out;                   // [T, H, 576]
+  const void* k_pe;            // [T, 64] bf16 or null
+  int64_t k_st;
+  void* k_out;                 // [T, 64] bf16
+  int64_t k_out_st;
+  int32_t dim, half;           // rotated columns; 1: pairs (i, i + dim / 2)
+  float mscale;
+  int32_t shares, share_heads; // a token's warps and the heads of each (set by the launch)
+  double turns[32];            // turns per position of each pair
+};
+
+cudaError_t launch_rope(RopeParams p, cudaStream_t stream);
+
+// The pages of a cache (cache_pages.cu).
+struct PageCopy {
+  void* cache;                 // [num_blocks, block_units] of 16 bytes
+  int32_t num_blocks, block_units;
+  float* scales;               // [num_blocks, block_scales] or null
+  int32_t block_scales;        // 0: no scales
+};
+struct ForkParams {
+  const int32_t *parent, *child, *lens;  // [num_forks]
+  int32_t num_forks, block_size;
+  const int32_t* free_blocks;  // [num_free]
+  int32_t num_free;
+  int32_t* block_table;        // [num_rows, cols]
+  int64_t bt_stride;
+  int32_t num_rows, cols;
+  int32_t* ref_counts;         // [num_blocks]
+  int32_t* taken;              // [1]
+  PageCopy copy;
+};
+struct FreeParams {
+  const int32_t* rows;         // [num_listed]
+  const int32_t* lens;         // [num_listed] or null: all columns
+  int32_t num_listed, block_size;
+  int32_t* block_table;
+  int64_t bt_stride;
+  int32_t num_rows, cols;
+  int32_t* ref_counts;
+  int32_t num_blocks;
+  int32_t* freed;              // [capacity]
+  int32_t capacity;
+  int32_t* num_freed;          // [1]
+  int32_t* ticket;             // zero before and after
+  uint32_t* bitmap;            // [cdiv(num_blocks, 32)], zero before and after
+};
+struct CompactParams {
+  const int32_t* refs;         // [num_blocks]
+  int32_t* refs_out;
+  const int32_t* table;        // [num_rows, cols]
+  int64_t table_stride;
+  int32_t* table_out;
+  int64_t table_out_stride;
+  int32_t num_rows, cols;
+  int32_t* num_live;           // [1]
+  int32_t* head;               // {blocks in use, moves}
+  int32_t* holes;              // [num_blocks / 2]
+  int32_t* from;               // [num_blocks / 2]
+  int32_t* back;               // [num_blocks]
+  PageCopy copy;
+};
+
+cudaError_t launch_copy_blocks(const PageCopy& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream);
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
+cudaError_t launch_free(const FreeParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+// Records a CUDA error for mla_last_cuda_error (api.cu).
+void record_cuda_error(cudaError_t e);
+
 // tcgen05 CTA-pair kernel: q_rows / kv_rows are the row counts of the q
 // and cache tensors viewed as [rows, 576]; status (may be null) receives a
 // nonzero code if a bounded wait times out.

@@ -490,6 +490,62 @@ MLA_API mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q
                                            float* lse, cudaStream_t stream);
 
 /*
+ * mla_decode_fwd_shared -- the decode of a batch whose requests share prefixes:
+ * samples of one prompt (mla_cache_fork), requests behind one system prompt. The
+ * keys that a group of requests has in common are read and multiplied once, for
+ * the query rows of all its tokens together; each request's own keys follow, and the two
+ * are merged. The result is that of mla_decode_fwd (kv_scales NULL and scale_group 0) or of
+ * mla_decode_fwd_scaled on the same tables and lengths, up to the order of its sums and
+ * the roundings of its weights; arguments that have the same names mean the same.
+ *   prefix_lens  [num_groups] int32: tokens that all requests of a group have in common
+ *                from position 0 on; whole blocks of them, prefix_lens[g] / block_size,
+ *                are shared: the first cells of the table rows of the group's requests
+ *                (those that take part) must be equal there, or hold equal blocks
+ *   group_indptr [num_groups + 1] int32, nondecreasing: group g has requests
+ *                [group_indptr[g], group_indptr[g + 1]); NULL with one group: all
+ *                requests. Requests of no group share nothing.
+ * A request takes part in its group's prefix when every one of its tokens sees all of it:
+ * seq_lens[r] - qlen_r >= the shared keys. Others (padding with shorter
+ * lengths among them) and the only participant of a group are decoded on their own, right
+ * for any lengths. The rows of every token in a group are computed over its
+ * prefix, so that padding is better kept behind the last group.
+ * Prefixes are shared for e4m3 with a block size that is a multiple of 16, and bf16 with
+ * a multiple of 64; other plans, and plans that ask for a kernel or a number of
+ * segments, run as mla_decode_fwd(_scaled). Sparse lists have no prefix.
+ * Groups whose prefixes are shorter than a few hundred keys gain little: 4 requests
+ * of 16 heads over 200 common keys take as long either way.
+ * Three launches on `stream` (list, decode, merge).
+ *
+ * mla_decode_shared_plan -- the plan of such calls for up to num_groups groups; host only,
+ * as mla_decode_plan, whose problem it takes. plan.wait_limit_us and the status word of
+ * the workspace (at its start; zero it once) work as there: mla_workspace_status takes
+ * &plan->plan. Errors: as mla_decode_plan and mla_decode_fwd(_scaled);
+ * MLA_ERR_INVALID_ARG for num_groups < 1, NULL prefix_lens, a NULL
+ * group_indptr with more than one group, kv_scales without scale_group or with a
+ * kv_scale other than 1; MLA_ERR_UNSUPPORTED for sparse problems and more than 65535 groups.
+ */
+typedef struct {
+  mla_plan_t plan;             /* of the same calls without sharing */
+  int32_t num_groups;
+  int32_t workers;             /* CTA pairs that the list is made for */
+  int32_t max_items;           /* item slots of the list; 0: nothing is shared */
+  int32_t unit_tiles;          /* tiles of 128 query rows of a request, */
+  int32_t prefix_tiles;        /* and of all groups */
+  int32_t partial_rows;
+  size_t workspace_bytes;
+} mla_shared_plan_t;
+
+MLA_API mla_status_t mla_decode_shared_plan(const mla_problem_t* prob, int32_t num_groups, mla_shared_plan_t* plan);
+
+MLA_API mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q, const void* kv_cache,
+                                           const float* kv_scales, int32_t scale_group, const int32_t* block_table,
+                                           int64_t block_table_stride, const int32_t* seq_lens,
+                                           const int32_t* qo_indptr, const int32_t* prefix_lens,
+                                           const int32_t* group_indptr, float softmax_scale, float q_scale,
+                                           float kv_scale, const float* sinks, void* workspace,
+                                           size_t workspace_bytes, void* out, float* lse, cudaStream_t stream);
+
+/*
  * mla_decode_scaled_kernel -- the decode kernel that the scaled calls of a plan
  * run on: *kernel receives plan->kernel, or 6 for the kernel of their own
  * (two CTAs to a tile of 128 query rows). Host only, no device call. Errors:

@@ -64,6 +64,12 @@ class Plan(ctypes.Structure):
         ("segm_expsum_offset", ctypes.c_size_t)]
 
 
+class SharedPlan(ctypes.Structure):
+    _fields_ = [("plan", Plan)] + [(n, ctypes.c_int32) for n in (
+        "num_groups", "workers", "max_items", "unit_tiles", "prefix_tiles", "partial_rows")] + [
+        ("workspace_bytes", ctypes.c_size_t)]
+
+
 class RopeProblem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dim", "layout", "scaling", "original_max_position")] + [
         (n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow", "mscale", "mscale_all_dim")]
@@ -153,6 +159,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.mla_block_tables.restype = st
         lib.mla_cache_append.argtypes = [_vp, i64, _vp, i64, _vp, i32, i32, i32, i32, _vp, _vp, _vp]
         lib.mla_cache_append.restype = st
+        lib.mla_decode_shared_plan.argtypes = [ctypes.POINTER(Problem), i32, ctypes.POINTER(SharedPlan)]
+        lib.mla_decode_shared_plan.restype = st
+        lib.mla_decode_fwd_shared.argtypes = [ctypes.POINTER(SharedPlan), _vp, _vp, _vp, i32, _vp, i64, _vp, _vp, _vp,
+                                              _vp, f32, f32, f32, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp]
+        lib.mla_decode_fwd_shared.restype = st
         lib.mla_rope_plan.argtypes = [ctypes.POINTER(RopeProblem), ctypes.POINTER(Rope)]
         lib.mla_rope_plan.restype = st
         lib.mla_rope_qk.argtypes = [ctypes.POINTER(Rope), _vp, i32, i32, _vp, i64, i64, _vp, i64, i64, i32, f32,
@@ -623,6 +634,74 @@ def mla_cache_append(c_kv, k_pe, slot_mapping, kv_cache, kv_scales, *, scale_gro
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status:
         _check("mla_cache_append", status)
+
+
+def mla_decode_shared_plan(problem: Problem, *, num_groups: int = 1) -> SharedPlan:
+    """The plan of mla_decode_fwd_shared calls for up to ``num_groups`` groups."""
+    lib = _lib or load_library()
+    plan = SharedPlan()
+    _check("mla_decode_shared_plan",
+           lib.mla_decode_shared_plan(ctypes.byref(problem), num_groups, ctypes.byref(plan)))
+    return plan
+
+
+def mla_decode_fwd_shared(plan: SharedPlan, q, kv_cache, *, kv_scales=None, scale_group: int = 0, block_table,
+                          seq_lens, qo_indptr=None, prefix_lens, group_indptr=None, softmax_scale: float,
+                          q_scale: float = 1.0, kv_scale: float = 1.0, sinks=None, workspace, out, lse,
+                          stream=None) -> None:
+    """The decode of a batch whose requests share prefixes: ``prefix_lens [G]`` tokens
+    in common among the requests ``group_indptr[g]`` to ``group_indptr[g + 1]``."""
+    lib, fn = _lib or load_library(), "mla_decode_fwd_shared"
+    torch = _torch or _load_torch()
+    pr, G = plan.plan.prob, plan.num_groups
+    dev, T, H, R, nb, bs = q.get_device(), pr.num_tokens, pr.num_heads, pr.num_reqs, pr.num_blocks, pr.block_size
+    i32, f32 = torch.int32, torch.float32
+    kinds = (torch.float8_e4m3fn, torch.uint8) if pr.kv_dtype == MLA_DTYPE_FP8_E4M3 else (torch.bfloat16,)
+    lists = (("seq_lens", seq_lens, R), ("qo_indptr", qo_indptr, R + 1), ("prefix_lens", prefix_lens, G),
+             ("group_indptr", group_indptr, G + 1))
+    ok = (dev >= 0 and dev == torch._C._cuda_getDevice() and q.dtype in kinds and q.shape == (T, H, HEAD_DIM)
+          and q.is_contiguous() and kv_cache.dtype in kinds and kv_cache.get_device() == dev
+          and kv_cache.shape == (nb, bs, HEAD_DIM) and kv_cache.is_contiguous()
+          and (kv_scales is None) == (scale_group == 0)
+          and (kv_scales is None
+               or (scale_group > 0 and bs % scale_group == 0 and kv_scales.dtype is f32
+                   and kv_scales.get_device() == dev and kv_scales.numel() == nb * bs // scale_group
+                   and kv_scales.is_contiguous()))
+          and out.dtype is torch.bfloat16 and out.get_device() == dev and out.shape == (T, H, KV_LORA_RANK)
+          and out.is_contiguous() and lse.dtype is f32 and lse.get_device() == dev and lse.shape == (T, H)
+          and lse.is_contiguous() and workspace.get_device() == dev and workspace.is_contiguous()
+          and (sinks is None or (sinks.dtype is f32 and sinks.get_device() == dev and sinks.numel() == H
+                                 and sinks.is_contiguous()))
+          and block_table.dtype is i32 and block_table.get_device() == dev and block_table.dim() == 2
+          and block_table.shape[0] == R
+          and _dense_rows(block_table.shape, block_table.stride(), pr.max_blocks_per_req))
+    for _, t, n in lists:
+        ok = ok and (t is None or (t.dtype is i32 and t.get_device() == dev and t.numel() == n and t.is_contiguous()))
+    if not ok:
+        if kv_scales is not None and pr.kv_dtype != MLA_DTYPE_FP8_E4M3:
+            raise MLAError(fn, MLA_ERR_UNSUPPORTED, "the plan's cache is not e4m3")
+        dense = [("q", q), ("kv_cache", kv_cache), ("kv_scales", kv_scales), ("out", out), ("lse", lse),
+                 ("workspace", workspace), ("sinks", sinks)] + [(n, t) for n, t, _ in lists]
+        _refuse(fn, dev, [("q", q, kinds), ("kv_cache", kv_cache, kinds), ("kv_scales", kv_scales, (f32,)),
+                          ("out", out, (torch.bfloat16,)), ("lse", lse, (f32,)), ("sinks", sinks, (f32,)),
+                          ("block_table", block_table, (i32,)), ("workspace", workspace, (workspace.dtype,))] +
+                [(n, t, (i32,)) for n, t, _ in lists],
+                [(t is None or t.is_contiguous(), f"{n} must be contiguous") for n, t in dense] +
+                [(t is None or t.numel() == k, f"{n} must hold {k} numbers") for n, t, k in lists] +
+                [(q.shape == (T, H, HEAD_DIM), f"q must be [{T}, {H}, {HEAD_DIM}] for this plan"),
+                 (kv_cache.shape == (nb, bs, HEAD_DIM), f"kv_cache must be [{nb}, {bs}, {HEAD_DIM}] for this plan"),
+                 ((kv_scales is None) == (scale_group == 0), "kv_scales and scale_group go together"),
+                 (scale_group >= 0 and (scale_group == 0 or bs % scale_group == 0), "scale_group must divide the block size"),
+                 (out.shape == (T, H, KV_LORA_RANK), f"out must be [{T}, {H}, {KV_LORA_RANK}]"),
+                 (lse.shape == (T, H), f"lse must be [{T}, {H}]"),
+                 (False, "kv_scales, sinks or block_table do not have the plan's sizes")])
+    status = lib.mla_decode_fwd_shared(
+        ctypes.byref(plan), q.data_ptr(), kv_cache.data_ptr(), _ptr(kv_scales), scale_group, block_table.data_ptr(),
+        max(block_table.stride(0), block_table.size(1)), _ptr(seq_lens), _ptr(qo_indptr), _ptr(prefix_lens),
+        _ptr(group_indptr), softmax_scale, q_scale, kv_scale, _ptr(sinks), workspace.data_ptr(), _ws_bytes(workspace),
+        out.data_ptr(), lse.data_ptr(), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status:
+        _check(fn, status)
 
 
 def mla_rope_plan(*, dim: int = 64, layout: str = "interleaved", base: float = 10000.0, scaling: str = "none",

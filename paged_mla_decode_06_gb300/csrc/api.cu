@@ -20,8 +20,8 @@ constexpr int kMaxSegments = 64;
 constexpr int kSparseTile = 64;
 constexpr int64_t kRowsNMax = 128;  // query rows per request the rows-as-N kernel takes (a CTA pair)
 constexpr int32_t kMaxWorkers = 1024;  // workers of the contiguous schedule
-static_assert(sizeof(mla_problem_t) == 68 && sizeof(mla_plan_t) == 168,
-              "the plan layout the bindings mirror");
+static_assert(sizeof(mla_problem_t) == 68 && sizeof(mla_plan_t) == 168 && sizeof(mla_shared_plan_t) == 200,
+              "the plan layouts the bindings mirror");
 constexpr size_t kWsAlign = 256;
 
 thread_local const char* g_last_cuda_error = "";
@@ -484,6 +484,54 @@ mla_status_t decode_items(const mla_plan_t* plan, const Inputs& in, const float*
   return run_items(plan, in, sinks, static_cast<uint8_t*>(workspace), out, lse, stream);
 }
 
+// ---- batches that share prefixes
+
+// Whether a plan's calls compute a prefix once: dense, with the kernel and the
+// segments left to the planner, and blocks that the kernel's boxes fit (e4m3: of
+// a multiple of 16 slots, bf16: of 64). Others run as mla_decode_fwd.
+bool shares_prefixes(const mla_problem_t& p) {
+  const bool fp8 = p.kv_dtype == MLA_DTYPE_FP8_E4M3;
+  return p.kernel == MLA_KERNEL_AUTO && p.num_segments == 0 && p.block_size % (fp8 ? 16 : 64) == 0;
+}
+
+// Workspace pieces of a shared call, after the status block.
+struct SharedLayout {
+  size_t n_items, items, unit_tab, req_group, groups, group_pos, prefix_tab, segm_out, segm_max, segm_expsum, end;
+};
+SharedLayout shared_layout(const mla_shared_plan_t* sp) {
+  const mla_problem_t& p = sp->plan.prob;
+  const size_t R = static_cast<size_t>(p.num_reqs), G = static_cast<size_t>(sp->num_groups);
+  SharedLayout l;
+  size_t at = kWsAlign;
+  auto take = [&](size_t bytes) {
+    const size_t a = at;
+    at += align_up(bytes, kWsAlign);
+    return a;
+  };
+  l.n_items = take(4);
+  l.items = take(static_cast<size_t>(sp->max_items) * 32);
+  l.unit_tab = take(R * sp->unit_tiles * 8);
+  l.req_group = take(R * 4);
+  l.groups = take(G * 16);
+  l.group_pos = take(G * 8);
+  l.prefix_tab = take(static_cast<size_t>(sp->prefix_tiles) * 8);
+  l.segm_out = take(static_cast<size_t>(sp->partial_rows) * kRank * 4);
+  l.segm_max = take(static_cast<size_t>(sp->partial_rows) * 4);
+  l.segm_expsum = take(static_cast<size_t>(sp->partial_rows) * 4);
+  l.end = at;
+  return l;
+}
+
+mla_status_t check_shared(const mla_shared_plan_t* sp) {
+  if (sp == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla_status_t s = check_problem(sp->plan.prob);
+  if (s != MLA_OK) return s;
+  if (sp->num_groups < 1 || sp->workers < 0 || sp->max_items < 0 || sp->unit_tiles < 0 || sp->prefix_tiles < 0 ||
+      sp->partial_rows < 0)
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
 }  // namespace
 
 namespace mla {
@@ -682,6 +730,121 @@ mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q, const 
   const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr, sparse_slots,
                   sparse_indptr, softmax_scale, q_scale, 1.f, kv_scales, scale_group};
   return decode_fwd(plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
+}
+
+mla_status_t mla_decode_shared_plan(const mla_problem_t* prob, int32_t num_groups, mla_shared_plan_t* plan) {
+  if (prob == nullptr || plan == nullptr || num_groups < 1) return MLA_ERR_INVALID_ARG;
+  std::memset(plan, 0, sizeof(*plan));
+  const mla_status_t s = mla_decode_plan(prob, &plan->plan);
+  if (s != MLA_OK) return s;
+  const mla_problem_t& p = plan->plan.prob;
+  if (p.topk > 0) return MLA_ERR_UNSUPPORTED;
+  if (num_groups > 65535) return MLA_ERR_UNSUPPORTED;
+  plan->num_groups = num_groups;
+  plan->workspace_bytes = plan->plan.workspace_bytes;
+  if (!shares_prefixes(p)) return MLA_OK;
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
+  const int64_t unit_tiles = (static_cast<int64_t>(p.max_qlen) * p.num_heads + 127) / 128;
+  const int64_t prefix_tiles = (rows + 127) / 128 + num_groups;  // each group's last may be cut short
+  const int64_t workers = plan->plan.num_sms / 2 > 0 ? plan->plan.num_sms / 2 : 1;
+  // every cut that the schedule makes, in prefix tiles or own ones, ends a worker's
+  // share: at most `workers` of either
+  const int64_t items = prefix_tiles + unit_tiles * p.num_reqs + 2 * workers;
+  const int64_t partial = (prefix_tiles + 2 * workers) * 128 + rows;
+  if (items > (1 << 22) || partial > (1 << 24)) return MLA_OK;  // (runs as mla_decode_fwd)
+  plan->workers = static_cast<int32_t>(workers);
+  plan->max_items = static_cast<int32_t>(items);
+  plan->unit_tiles = static_cast<int32_t>(unit_tiles);
+  plan->prefix_tiles = static_cast<int32_t>(prefix_tiles);
+  plan->partial_rows = static_cast<int32_t>(partial);
+  const size_t bytes = shared_layout(plan).end;
+  if (bytes > plan->workspace_bytes) plan->workspace_bytes = bytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q, const void* kv_cache,
+                                   const float* kv_scales, int32_t scale_group, const int32_t* block_table,
+                                   int64_t block_table_stride, const int32_t* seq_lens, const int32_t* qo_indptr,
+                                   const int32_t* prefix_lens, const int32_t* group_indptr, float softmax_scale,
+                                   float q_scale, float kv_scale, const float* sinks, void* workspace,
+                                   size_t workspace_bytes, void* out, float* lse, cudaStream_t stream) {
+  mla_status_t s = check_shared(plan);
+  if (s != MLA_OK) return s;
+  const mla_problem_t& p = plan->plan.prob;
+  if ((kv_scales != nullptr) != (scale_group != 0)) return MLA_ERR_INVALID_ARG;
+  if (scale_group != 0) {
+    s = check_group_scales(&plan->plan, kv_scales, scale_group);
+    if (s != MLA_OK) return s;
+    if (kv_scale != 1.f) return MLA_ERR_INVALID_ARG;
+  }
+  const Inputs in{q, kv_cache, block_table, block_table_stride, seq_lens, qo_indptr, nullptr, nullptr,
+                  softmax_scale, q_scale, kv_scale, kv_scales, scale_group};
+  s = check_inputs(&plan->plan, in);
+  if (s != MLA_OK) return s;
+  if ((sinks != nullptr) != (p.has_sinks == 1)) return MLA_ERR_INVALID_ARG;
+  if (p.num_tokens == 0) return MLA_OK;
+  if (prefix_lens == nullptr || !aligned(prefix_lens, 4) || !aligned(group_indptr, 4)) return MLA_ERR_INVALID_ARG;
+  if (group_indptr == nullptr && plan->num_groups != 1) return MLA_ERR_INVALID_ARG;
+  if (out == nullptr || lse == nullptr || !aligned(out, 16) || !aligned(lse, 4)) return MLA_ERR_INVALID_ARG;
+  if (sinks != nullptr && !aligned(sinks, 4)) return MLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < plan->workspace_bytes) return MLA_ERR_WORKSPACE;
+  if (!aligned(workspace, kWsAlign)) return MLA_ERR_INVALID_ARG;
+  if (plan->max_items == 0)
+    return decode_fwd(&plan->plan, in, sinks, workspace, workspace_bytes, out, lse, stream);
+  const SharedLayout l = shared_layout(plan);
+  if (l.end > workspace_bytes) return MLA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  mla::PrefixParams x{};
+  x.seq_lens = seq_lens;
+  x.qo_indptr = qo_indptr;
+  x.prefix_lens = prefix_lens;
+  x.group_indptr = group_indptr;
+  x.num_reqs = p.num_reqs;
+  x.num_groups = plan->num_groups;
+  x.num_tokens = p.num_tokens;
+  x.num_heads = p.num_heads;
+  x.block_size = p.block_size;
+  x.cols = p.max_blocks_per_req;
+  x.workers = plan->workers > 0 ? plan->workers : 1;
+  x.tiles_max = plan->unit_tiles;
+  x.ptiles_max = plan->prefix_tiles;
+  x.max_items = plan->max_items;
+  x.items = reinterpret_cast<int32_t*>(ws + l.items);
+  x.n_items = reinterpret_cast<int32_t*>(ws + l.n_items);
+  x.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
+  x.req_group = reinterpret_cast<int32_t*>(ws + l.req_group);
+  x.groups = reinterpret_cast<int32_t*>(ws + l.groups);
+  x.group_pos = reinterpret_cast<int64_t*>(ws + l.group_pos);
+  x.prefix_tab = reinterpret_cast<int32_t*>(ws + l.prefix_tab);
+  x.segm_out = reinterpret_cast<float*>(ws + l.segm_out);
+  x.segm_max = reinterpret_cast<float*>(ws + l.segm_max);
+  x.segm_expsum = reinterpret_cast<float*>(ws + l.segm_expsum);
+  x.sinks = sinks;
+  x.out = out;
+  x.lse = lse;
+  s = cuda_status(mla::launch_prefix_schedule(x, stream));
+  if (s != MLA_OK) return s;
+  mla::DecodeParams d = make_params(&plan->plan, in);
+  d.items = x.items;
+  d.n_items = x.n_items;
+  d.shared = 1;
+  d.slot_rows = 1;  // the items name rows
+  d.sinks = sinks;
+  d.out = out;
+  d.lse = lse;
+  d.segm_out = reinterpret_cast<float*>(ws + l.segm_out);
+  d.segm_rows = plan->partial_rows;
+  d.segm_max = reinterpret_cast<float*>(ws + l.segm_max);
+  d.segm_expsum = reinterpret_cast<float*>(ws + l.segm_expsum);
+  const int64_t q_rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
+  const int64_t kv_rows = static_cast<int64_t>(p.num_blocks) * p.block_size;
+  const unsigned items = static_cast<unsigned>(plan->max_items);
+  int* status = reinterpret_cast<int*>(ws);
+  s = cuda_status(p.kv_dtype == MLA_DTYPE_FP8_E4M3
+                      ? mla::launch_decode_pair(d, q_rows, kv_rows, items, status, stream)
+                      : mla::launch_decode_tc(d, false, q_rows, kv_rows, dim3(2u * items), status, stream));
+  if (s != MLA_OK) return s;
+  return cuda_status(mla::launch_prefix_merge(x, stream));
 }
 
 mla_status_t mla_decode_scaled_kernel(const mla_plan_t* plan, int32_t* kernel) {

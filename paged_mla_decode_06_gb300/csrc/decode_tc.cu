@@ -620,7 +620,7 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
       if (x.fin) {
         p.lse[th] = lse;
       } else {
-        const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * kRows + r
+        const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * p.slot_rows + r
                                         : th * p.num_segments + x.seg;
         p.segm_max[ts] = l > 0.f ? m_true : -INFINITY;
         p.segm_expsum[ts] = l > 0.f ? l * exp2f(m_ref - m_true) : 0.f;
@@ -770,7 +770,7 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
       // the warp's rows are consecutive rows of out, of the item's partial
       // slot, or of the segment's partials
       const int wr = x.row0 + 32 * q4;
-      const int z0 = x.fin || x.pslot < 0 ? x.tok0 * H + wr : x.pslot * kRows + 32 * q4;
+      const int z0 = x.fin || x.pslot < 0 ? x.tok0 * H + wr : x.pslot * p.slot_rows + 32 * q4;
       const int y0 = x.fin || x.pslot >= 0 ? 0 : x.seg;
       const CUtensorMap* map = x.fin ? &maps.out : &maps.part;
       int staged = 0;
@@ -827,7 +827,7 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
       rbase[it] = nullptr;
       if (rr < x.rows_total) {
         const int64_t th = static_cast<int64_t>(x.tok0 + rr / H) * H + rr % H;
-        const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * kRows + (rr - x.row0)
+        const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * p.slot_rows + (rr - x.row0)
                                         : th * p.num_segments + x.seg;
         rbase[it] = x.fin ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + th * kRank)
                           : reinterpret_cast<uint4*>(p.segm_out + ts * kRank);
@@ -994,6 +994,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FP8, SPARSE>::kT
       x.qlen = p.qo_indptr[x.unit + 1] - x.tok0;
     }
     x.part_len = p.seq_lens[x.unit];
+    if (p.shared != 0) {  // tokens and visible keys of the item itself (of a prefix: all keys for all rows)
+      const int4 b = reinterpret_cast<const int4*>(p.items)[2 * (blockIdx.x >> 1) + 1];
+      x.tok0 = b.y;
+      x.qlen = b.z & kItemTokens;
+      x.part_len = (b.z & kItemPrefix) != 0 ? INT_MAX : b.w + x.qlen - 1;
+    }
   }
   x.rows_total = x.qlen * x.H;
   x.row0 = tile * kRows;

@@ -56,7 +56,12 @@ struct DecodeParams {
   uint32_t scale_magic, scale_shift;  // s / scale_group = mulhi(s, magic) >> shift (0 <= s < 2^31;
                                       // magic 0: s >> shift)
   int32_t slot_rows;             // rows of a partial slot (balanced schedule)
+  // the list is one of prefix_sched.cu: an item's second half is {first row of its
+  // partial, first token, tokens | kItemPrefix, keys that the first token sees}
+  int32_t shared;
 };
+constexpr int32_t kItemPrefix = 1 << 30;  // all rows of the item see all of its keys
+constexpr int32_t kItemTokens = kItemPrefix - 1;
 
 // Balanced work list (sched.cu).
 struct SchedParams {
@@ -284,6 +289,37 @@ cudaError_t decode_hn_max_pairs(int rows, int* n);
 // CTAs that split the value columns: dense or sparse. grid.x counts CTAs: two per item or row tile.
 cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, dim3 grid, int* status,
                              cudaStream_t stream);
+
+// tcgen05 kernel of a batch that shares prefixes (e4m3): tiles of 128 query rows on
+// two CTAs that share each instruction; block size a multiple of 16. `items`: item
+// slots of the list.
+cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, unsigned items, int* status,
+                               cudaStream_t stream);
+
+// Work list and merge of a batch that shares prefixes (prefix_sched.cu).
+struct PrefixParams {
+  const int32_t* seq_lens;       // [R]
+  const int32_t* qo_indptr;      // [R+1] or null
+  const int32_t* prefix_lens;    // [G]
+  const int32_t* group_indptr;   // [G+1] requests, or null (one group of all)
+  int32_t num_reqs, num_groups, num_tokens, num_heads, block_size, cols;
+  int32_t workers, tiles_max, ptiles_max, max_items;
+  int32_t* items;                // [max_items, 8]
+  int32_t* n_items;
+  int32_t* unit_tab;             // [R * tiles_max, 2]: first partial row (-1), pieces
+  int32_t* req_group;            // [R]: group whose prefix the request takes part in, or -1
+  int32_t* groups;               // [G, 4]: first request, shared keys, first token, first prefix tile
+  int64_t* group_pos;            // [G]
+  int32_t* prefix_tab;           // [ptiles_max, 2]: first partial row, pieces
+  const float* segm_out;         // [rows, 512]
+  const float* segm_max;
+  const float* segm_expsum;
+  const float* sinks;
+  void* out;
+  float* lse;
+};
+cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream);
 
 // Shared memory bytes a decode variant needs (host query for validation).
 int decode_mma_smem_bytes(int32_t kernel, bool fp8);

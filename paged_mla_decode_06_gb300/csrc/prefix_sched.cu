@@ -1,0 +1,405 @@
+// prefix_sched.cu -- the work list and the merge of a batch that shares prefixes.
+//
+// The keys of a request are those of its group's prefix (whole blocks, the same in
+// all its requests' tables) and its own behind them. The rows of all tokens of a
+// group make the tiles of its prefix, the rows of a request those of its own
+// keys; an item is a tile of 128 rows and a range of 128-key groups. With W =
+// cdiv(all tiles' groups, workers), the prefix tiles are laid end to end and
+// their sequence is cut at every multiple of W (a cut within W / 8 of a tile's
+// ends is dropped), and an own tile of more than W groups is cut into equal
+// pieces; items are handed out longest first, so that the own keys, short as a
+// rule, fill what the prefix pieces leave. A row's pieces, of either kind, write base-2
+// partials; rows of one piece in all write their output.
+//
+// A request takes part in its group's prefix when all its tokens see all of it
+// (seq_len - qlen >= prefix); the others, and the only participant of a
+// group, take all their keys as their own. So a call gives what mla_decode_fwd
+// gives for any lengths, and only the tables are trusted to share their blocks.
+//
+// One CTA; what it spends is a few dependent passes over the lengths.
+#include "common.cuh"
+#include "internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kGroupKeys = 128;
+constexpr int kTileRows = 128;
+constexpr int kBins = 512;
+constexpr int kCache = 256;   // groups whose records are kept in shared memory
+
+struct Shared {
+  long long red[kThreads / 32];
+  int hist[kBins];
+  int start[kBins];
+  int4 groups[kCache];
+  long long pos[kCache];
+  int count[kCache];
+};
+
+template <typename T>
+__device__ T block_scan(T v, long long* red, T* total) {  // exclusive
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  T before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const T s = static_cast<T>(red[w]);
+    if (w < warp) before += s;
+    all += s;
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// Last i in [0, n) with at(i) <= v (at does not decrease; 0 if none).
+template <typename F>
+__device__ __forceinline__ int last_at(int n, int v, F at) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at(mid) <= v) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int group_edge(const PrefixParams& p, int g) {  // first request of group g
+  return p.group_indptr == nullptr ? (g == 0 ? 0 : p.num_reqs) : min(max(p.group_indptr[g], 0), p.num_reqs);
+}
+__device__ __forceinline__ int token_edge(const PrefixParams& p, int r) {  // first token of request r
+  return p.qo_indptr == nullptr ? min(r, p.num_tokens) : min(max(p.qo_indptr[r], 0), p.num_tokens);
+}
+__device__ __forceinline__ int group_of_req(const PrefixParams& p, int r) {
+  if (p.group_indptr == nullptr) return 0;
+  const int g = last_at(p.num_groups, r, [&](int i) { return p.group_indptr[i]; });
+  return r >= p.group_indptr[g] && r < p.group_indptr[g + 1] ? g : -1;
+}
+
+struct Own {
+  int tok0, qlen, len, first, groups, tiles;
+};
+__device__ __forceinline__ Own own_keys(const PrefixParams& p, int r, int shared) {
+  Own o;
+  o.tok0 = token_edge(p, r);
+  o.qlen = max(token_edge(p, r + 1) - o.tok0, 0);
+  o.len = p.seq_lens[r];
+  o.first = shared;
+  const int n = o.len - shared;
+  o.groups = n > 0 ? n / kGroupKeys + (n % kGroupKeys != 0) : 0;
+  o.tiles = static_cast<int>(min((static_cast<int64_t>(o.qlen) * p.num_heads + kTileRows - 1) / kTileRows,
+                                 static_cast<int64_t>(p.tiles_max)));
+  return o;
+}
+__device__ __forceinline__ int group_tokens(const PrefixParams& p, int g) {
+  return max(token_edge(p, group_edge(p, g + 1)) - token_edge(p, group_edge(p, g)), 0);
+}
+__device__ __forceinline__ int tiles_of(int64_t rows) { return static_cast<int>((rows + kTileRows - 1) / kTileRows); }
+
+// f(b) for each cut of the tile at [a, a + g) of the sequence, as group offsets.
+template <typename F>
+__device__ __forceinline__ int tile_cuts(long long a, int g, int W, F f) {
+  const int d = W / 8;
+  const long long lo = a + d + 1, hi = a + g - d - 1;
+  if (hi < lo) return 0;
+  int n = 0;
+  for (long long c = (lo + W - 1) / W * W; c <= hi; c += W, ++n) f(static_cast<int>(c - a));
+  return n;
+}
+__device__ __forceinline__ int own_pieces(int groups, int W) {
+  return groups > W + W / 8 ? (groups + W - 1) / W : 1;
+}
+__device__ __forceinline__ int bin_of(int size) { return min(size, kBins - 1); }
+
+__global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixParams p) {
+  __shared__ Shared s;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int tid = threadIdx.x;
+  const int G = p.num_groups, R = p.num_reqs, H = p.num_heads;
+  int4* const out_groups = reinterpret_cast<int4*>(p.groups);
+  int4* const gr = G <= kCache ? s.groups : out_groups;  // {first request, keys, participants, -}, then as in PrefixParams
+  long long* const gp = G <= kCache ? s.pos : reinterpret_cast<long long*>(p.group_pos);
+  for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;
+  for (int g = tid; g < G; g += kThreads) {
+    const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
+    gr[g] = make_int4(INT32_MAX, whole * p.block_size, 0, 0);
+  }
+  __syncthreads();
+  for (int r = tid; r < R; r += kThreads) {
+    const int g = group_of_req(p, r);
+    bool part = false;
+    if (g >= 0) {
+      const int shared = gr[g].y;
+      const int qlen = token_edge(p, r + 1) - token_edge(p, r);
+      part = shared > 0 && qlen > 0 && p.seq_lens[r] - qlen >= shared;
+      if (part) {
+        atomicMin(&gr[g].x, r);
+        atomicAdd(&gr[g].z, 1);
+      }
+    }
+    p.req_group[r] = part ? g : -1;
+  }
+  __syncthreads();
+  // prefix tiles and their places in the sequence
+  int tile_carry = 0;
+  long long pos_carry = 0;
+  for (int g0 = 0; g0 < G; g0 += kThreads) {
+    const int g = g0 + tid;
+    int tiles = 0, keys = 0;
+    if (g < G && gr[g].z >= 2) {
+      keys = gr[g].y;
+      tiles = tiles_of(static_cast<int64_t>(group_tokens(p, g)) * H);
+    }
+    int tsum;
+    long long psum;
+    const int t = tile_carry + block_scan<int>(tiles, s.red, &tsum);
+    const long long a = pos_carry + block_scan<long long>(static_cast<long long>(tiles) * cdiv(keys, kGroupKeys), s.red, &psum);
+    tile_carry += tsum;
+    pos_carry += psum;
+    if (g < G) {
+      const int4 v = make_int4(gr[g].x, keys, token_edge(p, group_edge(p, g)), t);
+      gr[g] = v;
+      out_groups[g] = v;
+      gp[g] = a;
+    }
+  }
+  const int ptiles = min(tile_carry, p.ptiles_max);
+  __syncthreads();
+  long long mine = 0;
+  for (int r = tid; r < R; r += kThreads) {
+    int g = p.req_group[r];
+    if (g >= 0 && gr[g].y == 0) p.req_group[r] = g = -1;
+    const Own o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
+    mine += static_cast<long long>(o.tiles) * o.groups;
+  }
+  long long total;
+  block_scan<long long>(mine, s.red, &total);
+  total += pos_carry;
+  const int W = static_cast<int>(max((total + p.workers - 1) / p.workers, 1ll));
+  // sizes
+  auto tile_group = [&](int t) { return last_at(G, t, [&](int i) { return gr[i].w; }); };
+  for (int t = tid; t < ptiles; t += kThreads) {
+    const int g = tile_group(t), n = cdiv(gr[g].y, kGroupKeys);
+    int prev = 0;
+    tile_cuts(gp[g] + static_cast<long long>(t - gr[g].w) * n, n, W, [&](int b) {
+      atomicAdd(&s.hist[bin_of(b - prev)], 1);
+      prev = b;
+    });
+    atomicAdd(&s.hist[bin_of(n - prev)], 1);
+  }
+  for (int r = tid; r < R; r += kThreads) {
+    const int g = p.req_group[r];
+    const Own o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
+    if (o.tiles == 0) continue;
+    const int k = own_pieces(o.groups, W), size = cdiv(o.groups, k);
+    for (int j = 0; j < k; ++j)
+      atomicAdd(&s.hist[bin_of(max(min(size, o.groups - j * size), 0))], o.tiles);
+  }
+  __syncthreads();
+  {  // start[b] = items of the bins above b
+    const int b = kBins - 1 - tid;
+    int all;
+    const int v = s.hist[b];
+    s.start[b] = block_scan<int>(v, s.red, &all);
+    if (tid == 0) *p.n_items = min(all, p.max_items);
+    static_assert(kBins == kThreads, "a bin a thread");
+  }
+  __syncthreads();
+  auto emit = [&](int size, int unit, int tile, int kb, int ke, int4 second) {
+    const int at = atomicAdd(&s.start[bin_of(size)], 1);
+    if (at >= p.max_items) return;
+    int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
+    it[0] = make_int4(unit, tile, kb, ke);
+    it[1] = second;
+  };
+  int row_carry = 0;  // rows of the partials
+  for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
+    const int t = t0 + tid;
+    int g = 0, n = 0, k = 0;
+    long long a = 0;
+    if (t < ptiles) {
+      g = tile_group(t);
+      n = cdiv(gr[g].y, kGroupKeys);
+      a = gp[g] + static_cast<long long>(t - gr[g].w) * n;
+      k = 1 + tile_cuts(a, n, W, [](int) {});
+    }
+    int rows;
+    const int base = row_carry + block_scan<int>(k * kTileRows, s.red, &rows);
+    row_carry += rows;
+    if (t < ptiles) {
+      reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, k);
+      const int tokens = group_tokens(p, g) | kItemPrefix;
+      int prev = 0, j = 0;
+      auto piece = [&](int b) {
+        emit(b - prev, gr[g].x, t - gr[g].w, prev * kGroupKeys, min(b * kGroupKeys, gr[g].y),
+             make_int4(base + j * kTileRows, gr[g].z, tokens, 0));
+        prev = b;
+        ++j;
+      };
+      tile_cuts(a, n, W, piece);
+      piece(n);
+    }
+  }
+  for (int r0 = 0; r0 < R; r0 += kThreads) {
+    const int r = r0 + tid;
+    Own o{};
+    int k = 0, g = -1, rows = 0;
+    if (r < R) {
+      g = p.req_group[r];
+      o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
+      if (o.tiles > 0) {
+        k = own_pieces(o.groups, W);
+        if (g >= 0 || k > 1) rows = k * o.qlen * H;
+      }
+    }
+    int sum;
+    int base = row_carry + block_scan<int>(rows, s.red, &sum);
+    row_carry += sum;
+    const int size = k > 0 ? cdiv(o.groups, k) : 0;
+    for (int t = 0; t < o.tiles; ++t) {
+      const int tr = min(kTileRows, o.qlen * H - t * kTileRows);
+      reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(rows > 0 ? base : -1, k);
+      for (int j = 0; j < k; ++j) {
+        const int b0 = min(j * size, o.groups), b1 = min(b0 + size, o.groups);
+        emit(b1 - b0, r, t, o.first + b0 * kGroupKeys, j + 1 == k ? max(o.len, o.first) : o.first + b1 * kGroupKeys,
+             make_int4(rows > 0 ? base + j * tr : -1, o.tok0, o.qlen, o.len - o.qlen + 1));
+      }
+      base += rows > 0 ? k * tr : 0;
+    }
+  }
+}
+
+// One warp a row: its pieces over the prefix, then those over its own keys, in
+// their order, weighted as mla_merge_segments does.
+constexpr int kMergeWarps = 4;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
+  const int H = p.num_heads;
+  const int t = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(t) * H);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  int r = t, tok0 = t;
+  if (p.qo_indptr != nullptr) {
+    if (t < p.qo_indptr[0] || t >= p.qo_indptr[p.num_reqs]) return;  // padding of the batch
+    r = last_at(p.num_reqs, t, [&](int i) { return p.qo_indptr[i]; });
+    tok0 = p.qo_indptr[r];
+  }
+  const int own_row = (t - tok0) * H + h;
+  if (own_row / kTileRows >= p.tiles_max) return;
+  const int g = p.req_group[r];
+  const int2 own = reinterpret_cast<const int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + own_row / kTileRows];
+  if (own.x < 0) return;  // one piece in all: written by the decode
+  const int end = token_edge(p, r + 1);
+  const int own_stride = min(kTileRows, (end - tok0) * H - own_row / kTileRows * kTileRows);
+  int2 pre = make_int2(0, 0);
+  int pre_row = 0;
+  if (g >= 0) {
+    const int4 gi = reinterpret_cast<const int4*>(p.groups)[g];
+    pre_row = (t - gi.z) * H + h;
+    pre = reinterpret_cast<const int2*>(p.prefix_tab)[gi.w + pre_row / kTileRows];
+  }
+  const int live = pre.y + own.y;
+  auto at = [&](int s) {  // row of piece s among the partials
+    return s < pre.y ? static_cast<int64_t>(pre.x) + s * kTileRows + pre_row % kTileRows
+                     : static_cast<int64_t>(own.x) + static_cast<int64_t>(s - pre.y) * own_stride + own_row % kTileRows;
+  };
+  const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
+  float M = sink2;
+  float m0 = -INFINITY, l0 = 0.f;  // of piece `lane`
+  for (int s = lane; s < live; s += 32) {
+    const int64_t i = at(s);
+    const float l = p.segm_expsum[i], m = p.segm_max[i];
+    if (s == lane) {
+      l0 = l;
+      m0 = m;
+    }
+    if (l > 0.f) M = fmaxf(M, m);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kRank);
+  // (a sink that is NaN leaves M to the others and makes the sum NaN)
+  if (M == -INFINITY && !(sink2 != sink2)) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) out[v * 32 + lane] = make_uint2(0u, 0u);
+    if (lane == 0) p.lse[row] = -INFINITY;
+    return;
+  }
+  float acc[4][4] = {};
+  float sum = sink2 == -INFINITY ? 0.f : exp2f(sink2 - M);
+  for (int s0 = 0; s0 < live; s0 += 32) {
+    if (s0 > 0) {
+      const int s = s0 + lane;
+      l0 = s < live ? p.segm_expsum[at(s)] : 0.f;
+      m0 = s < live ? p.segm_max[at(s)] : -INFINITY;
+    }
+    const float mine = l0 > 0.f ? l0 * exp2f(m0 - M) : 0.f;
+    for (int k = 0; k < 32 && s0 + k < live; k += 4) {
+      float4 x[4][4];
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = __shfl_sync(0xffffffffu, mine, (k + u) & 31);
+        if (s0 + k + u >= live) w[u] = 0.f;
+        // (a piece without mass may hold anything)
+        const float4* src = reinterpret_cast<const float4*>(p.segm_out + at(min(s0 + k + u, live - 1)) * kRank);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[u][v] = w[u] != 0.f ? __ldcg(src + v * 32 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        sum += w[u];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (w[u] == 0.f) continue;
+          acc[v][0] += w[u] * x[u][v].x;
+          acc[v][1] += w[u] * x[u][v].y;
+          acc[v][2] += w[u] * x[u][v].z;
+          acc[v][3] += w[u] * x[u][v].w;
+        }
+      }
+    }
+  }
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[v][0] * inv, acc[v][1] * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[v][2] * inv, acc[v][3] * inv);
+    out[v * 32 + lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  if (lane == 0) p.lse[row] = kLn2 * (M + log2f(sum));
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t stream) {
+  prefix_schedule_kernel<<<1, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
+  if (rows == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, p);
+}
+
+}  // namespace mla

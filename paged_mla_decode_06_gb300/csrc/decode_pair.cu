@@ -16,7 +16,7 @@
 //                            instructions of 46 cycles (measured; of 32 at N = 256,
 //                            for whose keys the shared memory has no room);
 //   O[rows, 512]  += P V     for j = 0, 1: M = 128, N = 256, K = 128: CTA r has its
-//                            rows of P as two terms (hi e4m3, lo e5m2), and value
+//                            rows of P as two terms (hi e5m2, lo e4m3), and value
 //                            columns 256 j + 128 r .. + 127 of all 128 keys, read MN-major: 16
 //                            instructions of 64.3 cycles.
 // That is 1860 tensor cycles a chunk and pair. (The value-split kernel takes 2180,
@@ -29,9 +29,14 @@
 // The softmax works on chunks: one group of eight warps takes the even ones,
 // another the odd ones. TMEM lanes 0..63 hold the rows' scores of keys 0..63,
 // lanes 64..127 those of keys 64..127; a warp takes 32 rows x 32 keys, and four
-// warps exchange a row's maximum. Weights, references and rounding are those of
-// the value-split kernel: p = 2^(t - ref + 4), t = score + log2 s, the reference moving
-// when a maximum exceeds it by more than 4.75 (O is then rescaled in TMEM).
+// warps exchange a row's maximum. With t = score + log2 s (KeyScale), the weights
+// are p = 2^(t - ref + 4), in two terms: hi in e5m2, the upper byte of p's f16
+// rounded there (so that it needs no conversion, and the rest p - hi is exact in
+// f16), and the rest in e4m3. That is 7 bits of p down to 2^-3, 3 bits down to
+// 2^-14. The rest fits e4m3 while p < 2^11.8, so the reference moves only when
+// a maximum exceeds it by more than 7.75: O is then rescaled in TMEM, which P V
+// has to wait for. (hi in e4m3, as the value-split kernel has it, leaves 4.75, and most
+// chunks had a row that moved.)
 //
 // Rank 0 issues all matrix instructions; their completion is committed to the
 // barriers of both CTAs. Rank 1's copies complete on its own barriers, and two
@@ -78,7 +83,7 @@ constexpr uint32_t kTmemS = 256;          // [2] 64: S of chunk c at c % 2
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
 constexpr float kPBias = 4.f;
-constexpr float kMove = 4.75f;
+constexpr float kMove = 7.75f;
 
 enum : int {
   kKFull = 0,                  // [kKRing] this CTA's keys of a chunk have landed
@@ -170,6 +175,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// Four weights (in order from the low byte) as two words of codes, the first
+// in e5m2, the rest in e4m3. (p is positive and below 2^12: the carry of the
+// rounding stays in its half. A NaN goes on in the rest.)
+__device__ __forceinline__ void split4(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b16 l0, l1;\n .reg .b32 a, b, c, d;\n"
+      " cvt.rn.f16x2.f32 a, %3, %2;\n cvt.rn.f16x2.f32 b, %5, %4;\n"
+      " add.u32 c, a, 0x00800080;\n add.u32 d, b, 0x00800080;\n"
+      " and.b32 c, c, 0xff00ff00;\n and.b32 d, d, 0xff00ff00;\n"
+      " prmt.b32 %0, c, d, 0x7531;\n"
+      " sub.f16x2 a, a, c;\n sub.f16x2 b, b, d;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, a;\n cvt.rn.satfinite.e4m3x2.f16x2 l1, b;\n"
+      " mov.b32 %1, {l0, l1};\n}\n"
+      : "=r"(hi), "=r"(lo)
+      : "f"(p0), "f"(p1), "f"(p2), "f"(p3));
+}
+
 // ------------------------------------------------------------------ pair instructions
 __device__ __forceinline__ void pair_alloc(uint32_t dst_saddr, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_saddr), "r"(ncols)
@@ -208,17 +229,17 @@ __device__ __forceinline__ void report(int* status, int code) {
 }
 
 // Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or
-// abort. CLUSTER: the other CTA arrives on it.
-template <bool CLUSTER>
+// abort. Barriers that the other CTA arrives on are waited for as the CTA's own:
+// no thread reads what one of the other CTA wrote through the generic proxy (P,
+// S and O are read by the tensor core of the SM that holds them, after proxy and
+// tcgen05 fences), and acquire and release at cluster scope took 1000 to 2000 cycles
+// each (168 us against 192 for 64 requests over 8192 common keys, 128 heads).
 __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  const bool brief = x.limit_ns < kSleepNs;
-  auto poll = [&]() { return CLUSTER ? mbar_try_wait_cluster_sleep(bar, parity, 0) : mbar_test_wait(bar, parity); };
-  auto sleep = [&]() {
-    return CLUSTER ? mbar_try_wait_cluster_sleep(bar, parity, kSleepNs) : mbar_try_wait_sleep(bar, parity, kSleepNs);
-  };
-  if (!brief && sleep()) return true;
+  const bool brief = x.limit_ns < kSleepNs;  // (a sleep may last longer than the limit: poll)
+  if (mbar_test_wait(bar, parity)) return true;
+  if (!brief && mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (!(brief ? poll() : sleep())) {
+  while (!(brief ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepNs))) {
     if (*x.abort) return false;
     if (global_timer_ns() - t0 > x.limit_ns) {
       report(x.status, code);
@@ -228,14 +249,13 @@ __device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code
   }
   return true;
 }
-template <bool CLUSTER>
 __device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  return __all_sync(0xffffffffu, wait_phase<CLUSTER>(x, bar, parity, code)) != 0;
+  return __all_sync(0xffffffffu, wait_phase(x, bar, parity, code)) != 0;
 }
 // Wait that ignores the abort flag (teardown), still bounded.
 __device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_cluster_sleep(bar, parity, kSleepNs)) {
+  while (!mbar_try_wait_sleep(bar, parity, kSleepNs)) {
     if (global_timer_ns() - t0 > kDefaultWaitNs) {
       report(x.status, code);
       return;
@@ -275,58 +295,78 @@ struct RowWindow {
   }
 };
 
-// Warp 0: the keys (five column boxes of this CTA's 64 rows), then the values
-// (two column boxes of all 128 rows) of each chunk; the boxes of a kind
-// go out together, one lane each.
+// Warp 0: the keys of each chunk (five column boxes of this CTA's 64 rows) and its
+// values (two column boxes of all 128 rows, half after half), each as soon as
+// its slot is free; the boxes of a kind go out together, one lane each. (In
+// turn, the keys of a chunk waited behind the values of the one before, whose
+// slots P V frees late: 4600 cycles a chunk. A warp more for either would leave 80
+// registers a thread.)
 template <int BOX>
-__device__ void produce(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
+__device__ void load_boxes(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
   constexpr int kSub = kHalf / BOX;  // boxes high of 64 rows
-  const int lane = x.lane;
-  if (lane == 0) {
-    tma_prefetch_desc(&maps.kv);
-    tma_prefetch_desc(&maps.kvr);
-  }
+  const int box = x.lane / kSub, run = x.lane % kSub;
   const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   volatile int* issued = reinterpret_cast<volatile int*>(x.smem + kOffIssued);
   const uint32_t base = smem_u32(x.smem);
-  RowWindow<BOX> w;
-  w.start(x, p, bt_row);
-  bool ok = true;
-  for (int c = 0; c < x.n_chunks && ok; ++c) {
-    w.at(x, p, bt_row, c);
-    {  // keys: lane = box * kSub + run (the rope box is the fifth)
+  RowWindow<BOX> kw, vw;
+  kw.start(x, p, bt_row);
+  vw = kw;
+  uint64_t t0 = 0;
+  int polls = 0;
+  for (int c = 0, g = 0; g < 2 * x.n_chunks;) {
+    bool idle = true;
+    if (c < x.n_chunks) {
       const int s = c % kKRing;
-      ok = c < kKRing || warp_wait<true>(x, x.bar(kKEmpty + s), (c / kKRing - 1) & 1, 11);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(x.bar(kKFull + s), kKSlot);
-        issued[0] = c;
+      if (c < kKRing || __all_sync(0xffffffffu, mbar_test_wait(x.bar(kKEmpty + s), (c / kKRing - 1) & 1))) {
+        kw.at(x, p, bt_row, c);
+        if (x.lane == 0) {
+          mbar_arrive_expect_tx(x.bar(kKFull + s), kKSlot);
+          issued[0] = c;
+        }
+        __syncwarp();
+        const int row = kw.row(c, x.rank * kSub + run);
+        const uint32_t to = base + kOffK + s * kKSlot;
+        if (box < 4) tma_load_2d(to + box * kBox + run * BOX * 128, &maps.kv, 128 * box, row, x.bar(kKFull + s));
+        if (box == 4) tma_load_2d(to + 4 * kBox + run * BOX * 64, &maps.kvr, kRank, row, x.bar(kKFull + s));
+        __syncwarp();
+        ++c;
+        idle = false;
       }
-      __syncwarp();
-      const int box = lane / kSub, run = lane % kSub;
-      const int row = w.row(c, x.rank * kSub + run);
-      const uint32_t to = base + kOffK + s * kKSlot;
-      if (box < 4) tma_load_2d(to + box * kBox + run * BOX * 128, &maps.kv, 128 * box, row, x.bar(kKFull + s));
-      if (box == 4)
-        tma_load_2d(to + 4 * kBox + run * BOX * 64, &maps.kvr, kRank, row, x.bar(kKFull + s));
-      __syncwarp();
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {  // values: column boxes rank and 2 + rank
-      const int g = 2 * c + h, s = g % kVRing;
-      ok = g < kVRing || warp_wait<true>(x, x.bar(kVEmpty + s), (g / kVRing - 1) & 1, 12);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(x.bar(kVFull + s), kVSlot);
-        issued[1] = g;
+    {
+      const int s = g % kVRing;
+      if (g < kVRing || __all_sync(0xffffffffu, mbar_test_wait(x.bar(kVEmpty + s), (g / kVRing - 1) & 1))) {
+        if ((g & 1) == 0) vw.at(x, p, bt_row, g >> 1);
+        if (x.lane == 0) {
+          mbar_arrive_expect_tx(x.bar(kVFull + s), kVSlot);
+          issued[1] = g;
+        }
+        __syncwarp();
+        const int row = vw.row(g >> 1, (g & 1) * kSub + run);
+        if (box < 2)
+          tma_load_2d(base + kOffV + s * kVSlot + box * kBox + run * BOX * 128, &maps.kv, 128 * (2 * box + x.rank), row,
+                      x.bar(kVFull + s));
+        __syncwarp();
+        ++g;
+        idle = false;
       }
-      __syncwarp();
-      const int j = lane / kSub, run = lane % kSub;
-      const int row = w.row(c, h * kSub + run);
-      if (j < 2)
-        tma_load_2d(base + kOffV + s * kVSlot + j * kBox + run * BOX * 128, &maps.kv, 128 * (2 * j + x.rank), row,
-                    x.bar(kVFull + s));
-      __syncwarp();
+    }
+    if (!idle) {
+      t0 = 0;
+      polls = 0;
+      continue;
+    }
+    __nanosleep(40);
+    if ((++polls & 63) != 0) continue;  // (reading the global timer takes longer than most waits)
+    const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+    if (t0 == 0) t0 = now;
+    if (__shfl_sync(0xffffffffu, *x.abort, 0)) break;
+    if (now - t0 > x.limit_ns) {
+      if (x.lane == 0) {
+        report(x.status, 11);
+        *x.abort = 1;
+      }
+      break;
     }
   }
   __syncwarp();
@@ -368,7 +408,7 @@ __device__ void prepare_keys(const Ctx& x, const DecodeParams& p) {
   if (x.n_chunks > 0) read(0);
   for (int c = 0; c < x.n_chunks; ++c) {
     const int b = c & 1;
-    if (c >= 2 && !warp_wait<false>(x, x.bar(kScFree + b), ((c >> 1) - 1) & 1, 27)) break;
+    if (c >= 2 && !warp_wait(x, x.bar(kScFree + b), ((c >> 1) - 1) & 1, 27)) break;
     float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + b * 3 * kKeys;
     if (lane < 4)
       reinterpret_cast<uint32_t*>(x.smem + kOffMask)[b * 4 + lane] =
@@ -386,7 +426,7 @@ __device__ void prepare_keys(const Ctx& x, const DecodeParams& p) {
       }
     }
     __syncwarp();
-    if (c >= 2 && !warp_wait<true>(x, x.bar(kSFull + b), ((c >> 1) - 1) & 1, 28)) break;  // S two chunks back
+    if (c >= 2 && !warp_wait(x, x.bar(kSFull + b), ((c >> 1) - 1) & 1, 28)) break;  // S two chunks back
     if (lane == 0) mbar_arrive(x.bar(kSFull + b));
     if (c + 1 < x.n_chunks) read(c + 1);
   }
@@ -403,12 +443,12 @@ __device__ void qk_issue(const Ctx& x) {
   const uint64_t k_desc = smem_desc_sw128(base + kOffK, 16, 1024);
   const uint64_t kr_desc = smem_desc_sw64(base + kOffK + 4 * kBox, 512);
   const bool one = elect_one();
-  bool ok = warp_wait<false>(x, x.bar(kQFull), 0, 20);
+  bool ok = warp_wait(x, x.bar(kQFull), 0, 20);
   for (int c = 0; c < x.n_chunks; ++c) {
     const int b = c & 1, s = c % kKRing;
-    ok = ok && warp_wait<false>(x, x.bar(kKFull + s), (c / kKRing) & 1, 23) &&
-         warp_wait<true>(x, x.bar(kPeerK + s), (c / kKRing) & 1, 21);
-    ok = ok && (c < 2 || warp_wait<true>(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1, 22));
+    ok = ok && warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1, 23) &&
+         warp_wait(x, x.bar(kPeerK + s), (c / kKRing) & 1, 21);
+    ok = ok && (c < 2 || warp_wait(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1, 22));
     if (!ok) break;
     fence_after_sync();
     const uint64_t kd = k_desc + static_cast<uint64_t>((s * kKSlot) >> 4);
@@ -436,8 +476,8 @@ __device__ void qk_issue(const Ctx& x) {
 
 // Rank 0, warp 3.
 __device__ void pv_issue(const Ctx& x) {
-  constexpr uint32_t kIdHi = instr_desc(kRows, 256, 0, 0, false, true);
-  constexpr uint32_t kIdLo = instr_desc(kRows, 256, 1, 0, false, true);
+  constexpr uint32_t kIdHi = instr_desc(kRows, 256, 1, 0, false, true);
+  constexpr uint32_t kIdLo = instr_desc(kRows, 256, 0, 0, false, true);
   const uint32_t base = smem_u32(x.smem);
   const uint64_t v_desc = smem_desc_sw128(base + kOffV, kBox, 1024);  // MN-major
   const uint64_t p_desc = smem_desc_sw128(base + kOffP, 16, 1024);
@@ -445,12 +485,12 @@ __device__ void pv_issue(const Ctx& x) {
   bool ok = true;
   for (int c = 0; c < x.n_chunks && ok; ++c) {
     const int b = c & 1;
-    ok = warp_wait<true>(x, x.bar(kPFull + b), (c >> 1) & 1, 24);
+    ok = warp_wait(x, x.bar(kPFull + b), (c >> 1) & 1, 24);
 #pragma unroll 1
     for (int h = 0; h < 2 && ok; ++h) {
       const int g = 2 * c + h, s = g % kVRing;
-      ok = warp_wait<false>(x, x.bar(kVFull + s), (g / kVRing) & 1, 26) &&
-           warp_wait<true>(x, x.bar(kPeerV + s), (g / kVRing) & 1, 39);
+      ok = warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26) &&
+           warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1, 39);
       if (!ok) break;
       fence_after_sync();
       const uint64_t vb = v_desc + static_cast<uint64_t>((s * kVSlot) >> 4);
@@ -483,11 +523,11 @@ __device__ void pv_issue(const Ctx& x) {
 
 // Rank 1, warps 1 and 3: what has landed here, passed on to rank 0.
 __device__ void pass_keys(const Ctx& x) {
-  bool ok = warp_wait<false>(x, x.bar(kQFull), 0, 20);
+  bool ok = warp_wait(x, x.bar(kQFull), 0, 20);
   for (int c = 0; c < x.n_chunks && ok; ++c) {
     const int s = c % kKRing;
-    ok = warp_wait<false>(x, x.bar(kKFull + s), (c / kKRing) & 1, 23);
-    if (ok && x.lane == 0) mbar_arrive_cluster(x.lead(kPeerK + s));
+    ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1, 23);
+    if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerK + s));
     __syncwarp();
   }
   if (x.lane == 0) drain_wait(x, x.bar(kDrainQK), 0, 25);
@@ -497,8 +537,8 @@ __device__ void pass_values(const Ctx& x) {
   bool ok = true;
   for (int g = 0; g < 2 * x.n_chunks && ok; ++g) {
     const int s = g % kVRing;
-    ok = warp_wait<false>(x, x.bar(kVFull + s), (g / kVRing) & 1, 26);
-    if (ok && x.lane == 0) mbar_arrive_cluster(x.lead(kPeerV + s));
+    ok = warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26);
+    if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerV + s));
     __syncwarp();
   }
   if (x.lane == 0) drain_wait(x, x.bar(kDrainPV), 0, 29);
@@ -550,13 +590,13 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   // before it posts its own of c + 1, which the other waits for before it posts
   // that of c + 4: neither the barrier's phase nor the four buffers are passed over.
   auto follow_other = [&](int c) {
-    if (!warp_wait<false>(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 33)) return false;
+    if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 33)) return false;
     follow(row_max(c));
     return true;
   };
   for (int c = h; c < n && ok; c += 2) {
     const int ph = (c >> 1) & 1;
-    ok = warp_wait<true>(x, x.bar(kSFull + h), ph, 31);
+    ok = warp_wait(x, x.bar(kSFull + h), ph, 31);
     if (!ok) break;
     fence_after_sync();
     float s[kPart];
@@ -569,7 +609,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     }
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(x.lead(kSFree + h));  // Q K^T two chunks on may overwrite it
+    if (lane == 0) mbar_arrive_remote(x.lead(kSFree + h));  // Q K^T two chunks on may overwrite it
     const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + h * 3 * kKeys + kPart * part;
     const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * h + part];
     if constexpr (SCALE == Scale::kKey) {
@@ -607,7 +647,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     xmax[((c & 3) * 4 + part) * kOwnRows] = fmaxf(m[0], m[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kX + 2 * (c & 3) + rq));
-    ok = warp_wait<false>(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 32);
+    ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 32);
     if (!ok) break;
     const float alpha = follow(row_max(c));
     // p as hi + lo terms, 16 keys to a 16-byte chunk of each tile
@@ -636,7 +676,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
           ps[0] = fma2(a, make_float2(iv.x, iv.y), ps[0]);
           ps[1] = fma2(b, make_float2(iv.z, iv.w), ps[1]);
         }
-        p_terms4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
+        split4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
       }
       const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
       psum = UNI ? fmaf(sum, ks[2 * kKeys + kUni * i], psum) : psum + sum;
@@ -645,7 +685,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kScFree + h));
     // P V two chunks back has read this buffer of P
-    ok = c < 2 || warp_wait<true>(x, x.bar(kPFree + h), ph ^ 1, 37);
+    ok = c < 2 || warp_wait(x, x.bar(kPFree + h), ph ^ 1, 37);
     if (!ok) break;
     *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -656,7 +696,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       // chunk, this warp rescales its lanes' rows of half of their columns.
       // (This barrier's phase before, P V of c - 3, completed with that of c - 2, as
       // P V is issued in order: the parity cannot be taken for it.)
-      ok = warp_wait<true>(x, x.bar(kPFree + (h ^ 1)), ((c - 1) >> 1) & 1, 38);
+      ok = warp_wait(x, x.bar(kPFree + (h ^ 1)), ((c - 1) >> 1) & 1, 38);
       if (!ok) break;
       fence_after_sync();
 #pragma unroll 1
@@ -682,7 +722,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     // half of them by each of its two row halves.
     if (kmask != 0xffffffffu || all_see < c * kKeys + kPart * (part + 1)) {
       const int g = 2 * c + kq;
-      ok = warp_wait<false>(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1, 36);  // (its writes are seen here too)
+      ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1, 36);  // (its writes are seen here too)
       if (!ok) break;
       uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + ((lane >> 3) & 1) * kBox + kPart * kh * 128 + (lane & 7) * 16;
       for (int j = rq + 2 * (lane >> 4); j < kPart; j += 4) {
@@ -699,7 +739,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     fence_proxy_async_smem();
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(x.lead(kPFull + h));
+    if (lane == 0) mbar_arrive_remote(x.lead(kPFull + h));
   }
 
   // ---------------------------------------------------------------- epilogue
@@ -709,11 +749,11 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     lsum[(4 * h + part) * kOwnRows] = l;
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kXL + rq));
-    ok = warp_wait<false>(x, x.bar(kXL + rq), 0, 34);
+    ok = warp_wait(x, x.bar(kXL + rq), 0, 34);
   }
   // O is complete with the last chunk
   if (ok && n > 0) {
-    ok = warp_wait<true>(x, x.bar(kPFree + ((n - 1) & 1)), ((n - 1) >> 1) & 1, 35);
+    ok = warp_wait(x, x.bar(kPFree + ((n - 1) & 1)), ((n - 1) >> 1) & 1, 35);
     fence_after_sync();
   }
   if (!ok) return;
@@ -915,7 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     softmax_rows<SCALE>(x, maps, p);
   } else if (x.n_chunks > 0) {
     if (x.warp == 0) {
-      produce<BOX>(x, maps, p);
+      load_boxes<BOX>(x, maps, p);
     } else if (x.warp == 2) {
       prepare_keys<BOX, SCALE>(x, p);
     } else if (x.warp == 1) {

@@ -124,10 +124,33 @@ def run_case(c, **kw):
     return named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy(), (args, named)
 
 
+def weight_terms(c, lists, out, tol):
+    """What the bounds of ``S.decode`` leave out for a weight p' of which the first term
+    is e5m2 and the rest e4m3 (the row's largest at p' >= 2^4 again). The first is off by
+    2^-3 of p' at most and the rest by 2^-4 of that, as there; a rest below 2^-6 is
+    off by half of e4m3's smallest step, 2^-10, 2^-14 of the largest weight, and by no
+    more than itself, 2^-3 of the weight. (A first term below 2^-14 is off by 2^-17 at
+    most, 2^-21 of the largest.) The output's own rounding multiplies that by 1 + 2^-8."""
+    q = O.decode_e4m3fn(c["q"]) * QS
+    for t, slots in enumerate(lists):
+        slots = np.asarray(slots, np.int64)
+        slots = slots[slots >= 0]
+        if not len(slots):
+            continue
+        s, k = c["scales"][slots // c["g"]], O.decode_e4m3fn(c["codes"][slots])
+        z = SCALE * (q[t] @ (k * s[:, None]).T)
+        ws = np.exp(z - np.logaddexp.reduce(z, axis=1)[:, None]) * s
+        err = np.minimum(2.0 ** -14 * ws.max(1)[:, None], 2.0 ** -3 * ws)
+        tol[t] += err @ np.abs(k[:, :512]) * (1 + 2.0 ** -8)
+
+
 def expected(c):
     lists = S.token_slots(c["table"], c["lens"], c["bs"], c["qo"])
     if c["kind"] != "bf16":
-        return S.decode(c["q"][:len(lists)], QS, c["codes"], c["scales"], c["g"], lists, SCALE, c["sinks"], bounds=True)
+        out, lse, to, tl = S.decode(c["q"][:len(lists)], QS, c["codes"], c["scales"], c["g"], lists, SCALE, c["sinks"],
+                                    bounds=True)
+        weight_terms(c, lists, out, to)
+        return out, lse, to, tl
     T, H = len(lists), c["H"]
     out, lse = np.zeros((T, H, 512)), np.full((T, H), -np.inf)
     to, tl = np.zeros_like(out), np.zeros_like(lse)
@@ -458,8 +481,9 @@ def test_fork_then_decode_over_the_shared_pages():
         B.mla_decode_fwd_shared(plan, q, kv, kv_scales=sc, scale_group=g, block_table=sub, seq_lens=sl,
                                 prefix_lens=dev([L], np.int32), softmax_scale=SCALE, q_scale=QS, workspace=dws, out=out, lse=lse)
         torch.cuda.synchronize()
-        ro, rl, to, tl = S.decode(q.cpu().numpy(), QS, codes, scales, g, S.token_slots(table[active], lens[active], bs),
-                                  SCALE, bounds=True)
+        lists = S.token_slots(table[active], lens[active], bs)
+        ro, rl, to, tl = S.decode(q.cpu().numpy(), QS, codes, scales, g, lists, SCALE, bounds=True)
+        weight_terms(dict(q=q.cpu().numpy(), scales=scales, codes=codes, g=g), lists, ro, to)
         assert np.all(np.abs(out.double().cpu().numpy() - ro) <= to) and np.all(np.abs(lse.double().cpu().numpy() - rl) <= tl)
         # the last sample loses; the pool closes up
         B.mla_cache_free(dev(active[-1:], np.int32), T_, R_, freed=freed, num_freed=count, workspace=ws)

@@ -747,10 +747,10 @@ mla_status_t mla_decode_shared_plan(const mla_problem_t* prob, int32_t num_group
   const int64_t unit_tiles = (static_cast<int64_t>(p.max_qlen) * p.num_heads + 127) / 128;
   const int64_t prefix_tiles = (rows + 127) / 128 + num_groups;  // each group's last may be cut short
   const int64_t workers = plan->plan.num_sms / 2 > 0 ? plan->plan.num_sms / 2 : 1;
-  // every cut that the schedule makes, in prefix tiles or own ones, ends a worker's
-  // share: at most `workers` of either
-  const int64_t items = prefix_tiles + unit_tiles * p.num_reqs + 2 * workers;
-  const int64_t partial = (prefix_tiles + 2 * workers) * 128 + rows;
+  // every cut that the schedule makes ends a worker's share: at most `workers`, and as
+  // many pieces more
+  const int64_t items = prefix_tiles + unit_tiles * p.num_reqs + workers;
+  const int64_t partial = (prefix_tiles + workers) * 128 + rows;
   if (items > (1 << 22) || partial > (1 << 24)) return MLA_OK;  // (runs as mla_decode_fwd)
   plan->workers = static_cast<int32_t>(workers);
   plan->max_items = static_cast<int32_t>(items);

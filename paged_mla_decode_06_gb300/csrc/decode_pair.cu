@@ -68,9 +68,9 @@ constexpr int kHalf = 64;                 // keys of a CTA as B of Q K^T; K of a
 constexpr int kBox = kHalf * 128;         // 128-byte columns of 64 rows
 constexpr int kRBox = kHalf * 64;         // the rope columns of 64 rows
 constexpr int kKSlot = 4 * kBox + kRBox;  // a CTA's keys of a chunk
-constexpr int kVSlot = 2 * kBox;          // its value columns (j = 0, 1) of 64 keys
+constexpr int kVSlot = 2 * kBox;          // its value columns of an instruction, of all keys
 constexpr int kKRing = 2;                 // chunks
-constexpr int kVRing = 4;                 // halves of chunks
+constexpr int kVRing = 4;                 // slots: column box j of chunk c is number 2 c + j
 constexpr int kSoftWarps = 16;
 constexpr int kGroupWarps = 8;
 constexpr int kPart = 32;                 // keys of a softmax warp
@@ -88,17 +88,17 @@ constexpr float kMove = 7.75f;
 enum : int {
   kKFull = 0,                  // [kKRing] this CTA's keys of a chunk have landed
   kKEmpty = kKFull + kKRing,   // [kKRing] released by Q K^T
-  kVFull = kKEmpty + kKRing,   // [kVRing] this CTA's values of a half have landed
-  kVEmpty = kVFull + kVRing,   // [kVRing] released by P V
+  kVFull = kKEmpty + kKRing,   // [kVRing] a column box of this CTA's values has landed
+  kVEmpty = kVFull + kVRing,   // [kVRing] P V over it complete: released, O_j holds the chunk
   kPeerK = kVEmpty + kVRing,   // [kKRing] rank 0: rank 1's keys have landed
   kPeerV = kPeerK + kKRing,    // [kVRing] rank 0: rank 1's values
   kQFull = kPeerV + kVRing,    // this CTA's rows of q
   // of chunk c, at c % 2:
   kSFull,                      // [2] S written and key scales ready
   kSFree = kSFull + 2,         // [2] rank 0: S read by both CTAs
-  kPFull = kSFree + 2,         // [2] rank 0: P written by both CTAs
-  kPFree = kPFull + 2,         // [2] P V complete: P may be replaced, O holds the chunk
-  kX = kPFree + 2,             // [4][2] (at c % 4) the four warps of 32 rows have posted their maxima
+  kPFull = kSFree + 2,         // [2] rank 0: P written by both CTAs, O_0 rescaled
+  kOReady = kPFull + 2,        // [2] rank 0: O_1 rescaled
+  kX = kOReady + 2,            // [4][2] (at c % 4) the four warps of 32 rows have posted their maxima
   kScFree = kX + 8,            // [2] key scales read
   kXL = kScFree + 2,           // [2] the eight warps of 32 rows have posted their sums
   kDrainQK = kXL + 2,          // Q K^T and P V complete, in both CTAs
@@ -110,7 +110,7 @@ enum : int {
 constexpr int kOffBar = 0;
 constexpr int kOffTslot = 448;
 constexpr int kOffAbort = 452;
-constexpr int kOffIssued = 456;                  // {last chunk of keys, last half of values} issued
+constexpr int kOffIssued = 456;                  // {last chunk of keys, last box of values} issued
 constexpr int kOffMask = 480;                    // [2][4] bits of existing keys of chunk c (at c % 2)
 constexpr int kOffXMax = 512;                    // [4][4][64] maxima of chunk c (at c % 4) by key quarter
 constexpr int kOffScale = kOffXMax + 4096;       // [2][mul, add, inv][128]
@@ -296,7 +296,7 @@ struct RowWindow {
 };
 
 // Warp 0: the keys of each chunk (five column boxes of this CTA's 64 rows) and its
-// values (two column boxes of all 128 rows, half after half), each as soon as
+// values (two column boxes of all 128 rows), each as soon as
 // its slot is free; the boxes of a kind go out together, one lane each. (In
 // turn, the keys of a chunk waited behind the values of the one before, whose
 // slots P V frees late: 4600 cycles a chunk. A warp more for either would leave 80
@@ -342,9 +342,10 @@ __device__ void load_boxes(const Ctx& x, const PairMaps& maps, const DecodeParam
           issued[1] = g;
         }
         __syncwarp();
-        const int row = vw.row(g >> 1, (g & 1) * kSub + run);
-        if (box < 2)
-          tma_load_2d(base + kOffV + s * kVSlot + box * kBox + run * BOX * 128, &maps.kv, 128 * (2 * box + x.rank), row,
+        const int vrun = x.lane % (2 * kSub);  // (of 128 rows)
+        const int row = vw.row(g >> 1, vrun);
+        if (x.lane < 2 * kSub)
+          tma_load_2d(base + kOffV + s * kVSlot + vrun * BOX * 128, &maps.kv, 128 * (2 * (g & 1) + x.rank), row,
                       x.bar(kVFull + s));
         __syncwarp();
         ++g;
@@ -474,7 +475,8 @@ __device__ void qk_issue(const Ctx& x) {
   __syncwarp();
 }
 
-// Rank 0, warp 3.
+// Rank 0, warp 3: P V of a chunk by halves of the columns, so that a half of O may
+// be rescaled while the other is multiplied.
 __device__ void pv_issue(const Ctx& x) {
   constexpr uint32_t kIdHi = instr_desc(kRows, 256, 1, 0, false, true);
   constexpr uint32_t kIdLo = instr_desc(kRows, 256, 0, 0, false, true);
@@ -483,36 +485,27 @@ __device__ void pv_issue(const Ctx& x) {
   const uint64_t p_desc = smem_desc_sw128(base + kOffP, 16, 1024);
   const bool one = elect_one();
   bool ok = true;
-  for (int c = 0; c < x.n_chunks && ok; ++c) {
-    const int b = c & 1;
-    ok = warp_wait(x, x.bar(kPFull + b), (c >> 1) & 1, 24);
-#pragma unroll 1
-    for (int h = 0; h < 2 && ok; ++h) {
-      const int g = 2 * c + h, s = g % kVRing;
-      ok = warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26) &&
-           warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1, 39);
-      if (!ok) break;
-      fence_after_sync();
-      const uint64_t vb = v_desc + static_cast<uint64_t>((s * kVSlot) >> 4);
-      const uint64_t pb = p_desc + static_cast<uint64_t>((b * 2 * kPTile + h * kHalf) >> 4);
-      if (one) {
+  for (int g = 0; g < 2 * x.n_chunks && ok; ++g) {
+    const int j = g & 1, c = g >> 1, b = c & 1, s = g % kVRing;
+    ok = warp_wait(x, x.bar((j == 0 ? kPFull : kOReady) + b), (c >> 1) & 1, j == 0 ? 24 : 38) &&
+         warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26) &&
+         warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1, 39);
+    if (!ok) break;
+    fence_after_sync();
+    const uint64_t vb = v_desc + static_cast<uint64_t>((s * kVSlot) >> 4);
+    const uint64_t pb = p_desc + static_cast<uint64_t>((b * 2 * kPTile) >> 4);
+    const uint32_t d = x.tbase + kTmemO + 128u * j;
+    if (one) {
 #pragma unroll
-        for (int ks = 0; ks < kHalf / 32; ++ks) {
-          const uint64_t av = pb + static_cast<uint64_t>((ks * 32) >> 4);
-          const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint64_t bj = bv + static_cast<uint64_t>((j * kBox) >> 4);
-            const uint32_t d = x.tbase + kTmemO + 128u * j;
-            pair_mma(d, av, bj, kIdHi, (g | ks) != 0 ? 1u : 0u);
-            pair_mma(d, av + static_cast<uint64_t>(kPTile >> 4), bj, kIdLo, 1u);
-          }
-        }
-        pair_commit(x.bar(kVEmpty + s));
-        if (h == 1) pair_commit(x.bar(kPFree + b));
+      for (int ks = 0; ks < kKeys / 32; ++ks) {
+        const uint64_t av = pb + static_cast<uint64_t>((ks * 32) >> 4);
+        const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
+        pair_mma(d, av, bv, kIdHi, (c | ks) != 0 ? 1u : 0u);
+        pair_mma(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kIdLo, 1u);
       }
-      __syncwarp();
+      pair_commit(x.bar(kVEmpty + s));
     }
+    __syncwarp();
   }
   if (one) {
     pair_commit(x.bar(kDrainPV));
@@ -556,7 +549,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   const int kq = q4 >> 1;                  // its half of a chunk's keys
   const int h = sw >> 3;                   // chunks c with c % 2 == h, and buffer
   const int kh = (sw >> 2) & 1;            // its 32 keys of the half
-  const int part = 2 * kq + kh;            // key quarter
+  const int part = 2 * kq + kh;            // key quarter (and, of a rescaling, columns of O_kh)
   const int cq = sw >> 2;                  // quarter of the TMEM columns of O at the end
   const int r = rq * 32 + lane;            // row within the CTA
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
@@ -685,18 +678,46 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kScFree + h));
     // P V two chunks back has read this buffer of P
-    ok = c < 2 || warp_wait(x, x.bar(kPFree + h), ph ^ 1, 37);
+    auto pv_done = [&](int cc, int j, int code) {
+      const int g = 2 * cc + j;
+      return warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1, code);
+    };
+    ok = c < 2 || pv_done(c - 2, 1, 37);
     if (!ok) break;
     *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
     *reinterpret_cast<uint4*>(prow + kPTile + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     *reinterpret_cast<uint4*>(prow + kPTile + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-    if (__any_sync(0xffffffffu, alpha != 1.f)) {
-      // some rows moved their reference: once O is complete up to the previous
-      // chunk, this warp rescales its lanes' rows of half of their columns.
-      // (This barrier's phase before, P V of c - 3, completed with that of c - 2, as
-      // P V is issued in order: the parity cannot be taken for it.)
-      ok = warp_wait(x, x.bar(kPFree + (h ^ 1)), ((c - 1) >> 1) & 1, 38);
+    // Value rows of keys that do not exist (cache rows past the sequence) are
+    // zeroed, and of keys that some rows of the tile do not see the NaNs: neither
+    // may reach O through p = 0. Each warp sees to the 32 keys of its quarter, a
+    // half of them by each of its two row halves.
+    if (kmask != 0xffffffffu || all_see < c * kKeys + kPart * (part + 1)) {
+#pragma unroll 1
+      for (int j = 0; j < 2 && ok; ++j) {
+        const int g = 2 * c + j;
+        ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1, 36);  // (its writes are seen here too)
+        uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + kPart * part * 128 + (lane & 7) * 16;
+        for (int i = rq + 2 * (lane >> 3); ok && i < kPart; i += 8) {
+          uint4* at = reinterpret_cast<uint4*>(box + i * 128);
+          if (!((kmask >> i) & 1u)) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+          } else if (c * kKeys + kPart * part + i >= all_see) {
+            const uint4 v = *at;
+            *at = make_uint4(e4m3x4_without_nan(v.x), e4m3x4_without_nan(v.y), e4m3x4_without_nan(v.z),
+                             e4m3x4_without_nan(v.w));
+          }
+        }
+      }
+      if (!ok) break;
+    }
+    fence_proxy_async_smem();
+    const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
+    if (kh == 1 && lane == 0) mbar_arrive_remote(x.lead(kPFull + h));  // (P alone)
+    if (moved) {
+      // some rows moved their reference: once P V of the previous chunk into O_kh
+      // is complete, this warp rescales its lanes' rows there
+      ok = pv_done(c - 1, kh, 40);
       if (!ok) break;
       fence_after_sync();
 #pragma unroll 1
@@ -716,30 +737,9 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       }
       tmem_st_wait();
     }
-    // Value rows of keys that do not exist (cache rows past the sequence) are
-    // zeroed, and of keys that some rows of the tile do not see the NaNs: neither
-    // may reach O through p = 0. Each warp sees to the 32 keys of its quarter, a
-    // half of them by each of its two row halves.
-    if (kmask != 0xffffffffu || all_see < c * kKeys + kPart * (part + 1)) {
-      const int g = 2 * c + kq;
-      ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1, 36);  // (its writes are seen here too)
-      if (!ok) break;
-      uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + ((lane >> 3) & 1) * kBox + kPart * kh * 128 + (lane & 7) * 16;
-      for (int j = rq + 2 * (lane >> 4); j < kPart; j += 4) {
-        uint4* at = reinterpret_cast<uint4*>(box + j * 128);
-        if (!((kmask >> j) & 1u)) {
-          *at = make_uint4(0u, 0u, 0u, 0u);
-        } else if (c * kKeys + kPart * part + j >= all_see) {
-          const uint4 v = *at;
-          *at = make_uint4(e4m3x4_without_nan(v.x), e4m3x4_without_nan(v.y), e4m3x4_without_nan(v.z),
-                           e4m3x4_without_nan(v.w));
-        }
-      }
-    }
-    fence_proxy_async_smem();
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(x.lead(kPFull + h));
+    if (lane == 0) mbar_arrive_remote(x.lead((kh == 0 ? kPFull : kOReady) + h));
   }
 
   // ---------------------------------------------------------------- epilogue
@@ -753,7 +753,8 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   }
   // O is complete with the last chunk
   if (ok && n > 0) {
-    ok = warp_wait(x, x.bar(kPFree + ((n - 1) & 1)), ((n - 1) >> 1) & 1, 35);
+    const int g = 2 * n - 1;
+    ok = warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1, 35);
     fence_after_sync();
   }
   if (!ok) return;
@@ -864,7 +865,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       store(o, col0 + 32 * c, c);
     }
   }
-  if (lane == 0) bulk_wait_all();  // tiles read and written before the CTA exits
+  if (lane == 0) bulk_wait_read<0>();  // the tiles are read before the CTA exits
   __syncwarp();
 }
 
@@ -924,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(x.bar(kSFull + i), 2);  // Q K^T and the key scales
       mbar_init(x.bar(kSFree + i), 2 * kGroupWarps);
       mbar_init(x.bar(kPFull + i), 2 * kGroupWarps);
-      mbar_init(x.bar(kPFree + i), 1);
+      mbar_init(x.bar(kOReady + i), kGroupWarps);
       mbar_init(x.bar(kScFree + i), kGroupWarps);
       mbar_init(x.bar(kXL + i), 8);
     }

@@ -3,20 +3,26 @@
 // The keys of a request are those of its group's prefix (whole blocks, the same in
 // all its requests' tables) and its own behind them. The rows of all tokens of a
 // group make the tiles of its prefix, the rows of a request those of its own
-// keys; an item is a tile of 128 rows and a range of 128-key groups. With W =
-// cdiv(all tiles' groups, workers), the prefix tiles are laid end to end and
-// their sequence is cut at every multiple of W (a cut within W / 8 of a tile's
-// ends is dropped), and an own tile of more than W groups is cut into equal
-// pieces; items are handed out longest first, so that the own keys, short as a
-// rule, fill what the prefix pieces leave. A row's pieces, of either kind, write base-2
-// partials; rows of one piece in all write their output.
+// keys; an item is a tile of 128 rows and a range of 128-key groups. The tiles
+// are laid end to end, those of the prefixes first, and the sequence of their
+// groups is cut at every multiple of W = cdiv(all groups, workers); a cut within
+// W / 8 of a tile's ends is dropped, and tiles of at most W / 2 groups are not
+// cut: items are handed out longest first, and the short ones fill what the
+// others leave. A row's pieces, of either kind, write base-2 partials; rows of
+// one piece in all write their output.
 //
 // A request takes part in its group's prefix when all its tokens see all of it
-// (seq_len - qlen >= prefix); the others, and the only participant of a
-// group, take all their keys as their own. So a call gives what mla_decode_fwd
-// gives for any lengths, and only the tables are trusted to share their blocks.
+// (seq_len - qlen >= prefix); the others take all their keys as their own. So a call
+// gives what mla_decode_fwd gives for any lengths, and only the tables are trusted to
+// share their blocks. A prefix is shared where that saves more than it costs: the
+// tiles that its participants would have of their own against those of the group's
+// tokens, times its key groups; the cost is a partial more for each own tile,
+// which takes about as long as kPieceCost key groups (its store 4 us of an SM
+// pair, its part in the merge). With 128 heads a request fills its tiles
+// alone, and the common keys come from L2 as they are.
 //
-// One CTA; what it spends is a few dependent passes over the lengths.
+// One CTA. Lengths and group records are kept in shared memory (of the first 1024
+// requests and 256 groups): re-read from L2 by each pass they took 9 us.
 #include "common.cuh"
 #include "internal.h"
 
@@ -27,7 +33,9 @@ constexpr int kThreads = 512;
 constexpr int kGroupKeys = 128;
 constexpr int kTileRows = 128;
 constexpr int kBins = 512;
-constexpr int kCache = 256;   // groups whose records are kept in shared memory
+constexpr int kCache = 256;      // groups and
+constexpr int kCacheReqs = 1024; // requests that are kept in shared memory
+constexpr int kPieceCost = 6;
 
 struct Shared {
   long long red[kThreads / 32];
@@ -35,7 +43,8 @@ struct Shared {
   int start[kBins];
   int4 groups[kCache];
   long long pos[kCache];
-  int count[kCache];
+  int edge[kCache + 1];
+  int4 reqs[kCacheReqs];
 };
 
 template <typename T>
@@ -78,44 +87,19 @@ __device__ __forceinline__ int group_edge(const PrefixParams& p, int g) {  // fi
 __device__ __forceinline__ int token_edge(const PrefixParams& p, int r) {  // first token of request r
   return p.qo_indptr == nullptr ? min(r, p.num_tokens) : min(max(p.qo_indptr[r], 0), p.num_tokens);
 }
-__device__ __forceinline__ int group_of_req(const PrefixParams& p, int r) {
-  if (p.group_indptr == nullptr) return 0;
-  const int g = last_at(p.num_groups, r, [&](int i) { return p.group_indptr[i]; });
-  return r >= p.group_indptr[g] && r < p.group_indptr[g + 1] ? g : -1;
-}
+__device__ __forceinline__ int groups_of(int keys) { return keys > 0 ? keys / kGroupKeys + (keys % kGroupKeys != 0) : 0; }
 
-struct Own {
-  int tok0, qlen, len, first, groups, tiles;
-};
-__device__ __forceinline__ Own own_keys(const PrefixParams& p, int r, int shared) {
-  Own o;
-  o.tok0 = token_edge(p, r);
-  o.qlen = max(token_edge(p, r + 1) - o.tok0, 0);
-  o.len = p.seq_lens[r];
-  o.first = shared;
-  const int n = o.len - shared;
-  o.groups = n > 0 ? n / kGroupKeys + (n % kGroupKeys != 0) : 0;
-  o.tiles = static_cast<int>(min((static_cast<int64_t>(o.qlen) * p.num_heads + kTileRows - 1) / kTileRows,
-                                 static_cast<int64_t>(p.tiles_max)));
-  return o;
-}
-__device__ __forceinline__ int group_tokens(const PrefixParams& p, int g) {
-  return max(token_edge(p, group_edge(p, g + 1)) - token_edge(p, group_edge(p, g)), 0);
-}
-__device__ __forceinline__ int tiles_of(int64_t rows) { return static_cast<int>((rows + kTileRows - 1) / kTileRows); }
-
-// f(b) for each cut of the tile at [a, a + g) of the sequence, as group offsets.
+// f(b) for each cut of the tile at [a, a + g) of the sequence, as group offsets;
+// returns their number.
 template <typename F>
 __device__ __forceinline__ int tile_cuts(long long a, int g, int W, F f) {
+  if (2 * g <= W) return 0;
   const int d = W / 8;
   const long long lo = a + d + 1, hi = a + g - d - 1;
   if (hi < lo) return 0;
   int n = 0;
   for (long long c = (lo + W - 1) / W * W; c <= hi; c += W, ++n) f(static_cast<int>(c - a));
   return n;
-}
-__device__ __forceinline__ int own_pieces(int groups, int W) {
-  return groups > W + W / 8 ? (groups + W - 1) / W : 1;
 }
 __device__ __forceinline__ int bin_of(int size) { return min(size, kBins - 1); }
 
@@ -124,28 +108,47 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x;
   const int G = p.num_groups, R = p.num_reqs, H = p.num_heads;
+  const bool few = G <= kCache;
   int4* const out_groups = reinterpret_cast<int4*>(p.groups);
-  int4* const gr = G <= kCache ? s.groups : out_groups;  // {first request, keys, participants, -}, then as in PrefixParams
-  long long* const gp = G <= kCache ? s.pos : reinterpret_cast<long long*>(p.group_pos);
+  // {first request, shared keys, tiles of the participants, requests that take part}, then as in PrefixParams
+  int4* const gr = few ? s.groups : out_groups;
+  long long* const gp = few ? s.pos : reinterpret_cast<long long*>(p.group_pos);
+  auto edge = [&](int g) { return few ? s.edge[g] : group_edge(p, g); };
+  auto tiles_of = [&](int64_t tokens) { return static_cast<int>((tokens * H + kTileRows - 1) / kTileRows); };
+  // {first token, tokens, length, group of the prefix that the request takes part in or -1}
+  auto request = [&](int r) {
+    if (r < kCacheReqs) return s.reqs[r];
+    const int t0 = token_edge(p, r);
+    return make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], p.req_group[r]);
+  };
+  auto set_group = [&](int r, int g) {
+    p.req_group[r] = g;
+    if (r < kCacheReqs) s.reqs[r].w = g;
+  };
+  for (int r = tid; r < min(R, kCacheReqs); r += kThreads) {
+    const int t0 = token_edge(p, r);
+    s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
+  }
   for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;
   for (int g = tid; g < G; g += kThreads) {
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
     gr[g] = make_int4(INT32_MAX, whole * p.block_size, 0, 0);
   }
+  if (few)
+    for (int g = tid; g <= G; g += kThreads) s.edge[g] = group_edge(p, g);
   __syncthreads();
   for (int r = tid; r < R; r += kThreads) {
-    const int g = group_of_req(p, r);
-    bool part = false;
-    if (g >= 0) {
-      const int shared = gr[g].y;
-      const int qlen = token_edge(p, r + 1) - token_edge(p, r);
-      part = shared > 0 && qlen > 0 && p.seq_lens[r] - qlen >= shared;
-      if (part) {
-        atomicMin(&gr[g].x, r);
-        atomicAdd(&gr[g].z, 1);
-      }
+    const int4 q = request(r);
+    int g = last_at(G, r, edge);
+    const bool in = r >= edge(g) && r < edge(g + 1);
+    const int keys = gr[g].y;
+    if (in && keys > 0 && q.y > 0 && q.z - q.y >= keys) {
+      atomicMin(&gr[g].x, r);
+      atomicAdd(&gr[g].z, min(tiles_of(q.y), p.tiles_max));
+    } else {
+      g = -1;
     }
-    p.req_group[r] = part ? g : -1;
+    set_group(r, g);
   }
   __syncthreads();
   // prefix tiles and their places in the sequence
@@ -153,19 +156,23 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   long long pos_carry = 0;
   for (int g0 = 0; g0 < G; g0 += kThreads) {
     const int g = g0 + tid;
-    int tiles = 0, keys = 0;
-    if (g < G && gr[g].z >= 2) {
-      keys = gr[g].y;
-      tiles = tiles_of(static_cast<int64_t>(group_tokens(p, g)) * H);
+    int tiles = 0, keys = 0, tok0 = 0;
+    if (g < G) {
+      tok0 = token_edge(p, edge(g));
+      tiles = tiles_of(max(token_edge(p, edge(g + 1)) - tok0, 0));
+      const int4 v = gr[g];
+      const bool share = static_cast<long long>(v.z - tiles) * groups_of(v.y) >= static_cast<long long>(kPieceCost) * v.z;
+      if (share && v.z > 0) keys = v.y;
+      else tiles = 0;
     }
     int tsum;
     long long psum;
     const int t = tile_carry + block_scan<int>(tiles, s.red, &tsum);
-    const long long a = pos_carry + block_scan<long long>(static_cast<long long>(tiles) * cdiv(keys, kGroupKeys), s.red, &psum);
+    const long long a = pos_carry + block_scan<long long>(static_cast<long long>(tiles) * groups_of(keys), s.red, &psum);
     tile_carry += tsum;
     pos_carry += psum;
     if (g < G) {
-      const int4 v = make_int4(gr[g].x, keys, token_edge(p, group_edge(p, g)), t);
+      const int4 v = make_int4(gr[g].x, keys, tok0, t);
       gr[g] = v;
       out_groups[g] = v;
       gp[g] = a;
@@ -173,11 +180,24 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   }
   const int ptiles = min(tile_carry, p.ptiles_max);
   __syncthreads();
+  // own keys of request r
+  struct Own {
+    int4 q;
+    int first, groups, tiles;
+  };
+  auto own_keys = [&](int r) {
+    Own o;
+    o.q = request(r);
+    o.first = o.q.w >= 0 ? gr[o.q.w].y : 0;
+    o.groups = groups_of(o.q.z - o.first);
+    o.tiles = min(tiles_of(o.q.y), p.tiles_max);
+    return o;
+  };
   long long mine = 0;
   for (int r = tid; r < R; r += kThreads) {
-    int g = p.req_group[r];
-    if (g >= 0 && gr[g].y == 0) p.req_group[r] = g = -1;
-    const Own o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
+    const int g = request(r).w;
+    if (g >= 0 && gr[g].y == 0) set_group(r, -1);
+    const Own o = own_keys(r);
     mine += static_cast<long long>(o.tiles) * o.groups;
   }
   long long total;
@@ -186,49 +206,64 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   const int W = static_cast<int>(max((total + p.workers - 1) / p.workers, 1ll));
   // sizes
   auto tile_group = [&](int t) { return last_at(G, t, [&](int i) { return gr[i].w; }); };
-  for (int t = tid; t < ptiles; t += kThreads) {
-    const int g = tile_group(t), n = cdiv(gr[g].y, kGroupKeys);
+  auto count = [&](long long a, int n) {
     int prev = 0;
-    tile_cuts(gp[g] + static_cast<long long>(t - gr[g].w) * n, n, W, [&](int b) {
+    tile_cuts(a, n, W, [&](int b) {
       atomicAdd(&s.hist[bin_of(b - prev)], 1);
       prev = b;
     });
     atomicAdd(&s.hist[bin_of(n - prev)], 1);
+  };
+  for (int t = tid; t < ptiles; t += kThreads) {
+    const int g = tile_group(t), n = groups_of(gr[g].y);
+    count(gp[g] + static_cast<long long>(t - gr[g].w) * n, n);
   }
-  for (int r = tid; r < R; r += kThreads) {
-    const int g = p.req_group[r];
-    const Own o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
-    if (o.tiles == 0) continue;
-    const int k = own_pieces(o.groups, W), size = cdiv(o.groups, k);
-    for (int j = 0; j < k; ++j)
-      atomicAdd(&s.hist[bin_of(max(min(size, o.groups - j * size), 0))], o.tiles);
+  long long carry = pos_carry;
+  for (int r0 = 0; r0 < R; r0 += kThreads) {
+    Own o{};
+    if (r0 + tid < R) o = own_keys(r0 + tid);
+    long long sum;
+    const long long a = carry + block_scan<long long>(static_cast<long long>(o.tiles) * o.groups, s.red, &sum);
+    carry += sum;
+    for (int t = 0; t < o.tiles; ++t) count(a + static_cast<long long>(t) * o.groups, o.groups);
   }
   __syncthreads();
   {  // start[b] = items of the bins above b
+    static_assert(kBins == kThreads, "a bin a thread");
     const int b = kBins - 1 - tid;
     int all;
-    const int v = s.hist[b];
-    s.start[b] = block_scan<int>(v, s.red, &all);
+    s.start[b] = block_scan<int>(s.hist[b], s.red, &all);
     if (tid == 0) *p.n_items = min(all, p.max_items);
-    static_assert(kBins == kThreads, "a bin a thread");
   }
   __syncthreads();
-  auto emit = [&](int size, int unit, int tile, int kb, int ke, int4 second) {
-    const int at = atomicAdd(&s.start[bin_of(size)], 1);
-    if (at >= p.max_items) return;
-    int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
-    it[0] = make_int4(unit, tile, kb, ke);
-    it[1] = second;
+  // A tile's items: f(j) = first row of the partial of its piece j (-1: its output).
+  auto emit = [&](long long a, int n, int unit, int tile, int first, int end, int4 second, auto f) {
+    int prev = 0, j = 0;
+    auto piece = [&](int b) {
+      const int at = atomicAdd(&s.start[bin_of(b - prev)], 1);
+      if (at < p.max_items) {
+        int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
+        it[0] = make_int4(unit, tile, first + prev * kGroupKeys, b == n ? end : first + b * kGroupKeys);
+        second.x = f(j);
+        it[1] = second;
+      }
+      prev = b;
+      ++j;
+    };
+    tile_cuts(a, n, W, piece);
+    piece(n);
   };
   int row_carry = 0;  // rows of the partials
   for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
     const int t = t0 + tid;
-    int g = 0, n = 0, k = 0;
+    int4 v{};
+    int n = 0, k = 0, g = 0;
     long long a = 0;
     if (t < ptiles) {
       g = tile_group(t);
-      n = cdiv(gr[g].y, kGroupKeys);
-      a = gp[g] + static_cast<long long>(t - gr[g].w) * n;
+      v = gr[g];
+      n = groups_of(v.y);
+      a = gp[g] + static_cast<long long>(t - v.w) * n;
       k = 1 + tile_cuts(a, n, W, [](int) {});
     }
     int rows;
@@ -236,43 +271,37 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     row_carry += rows;
     if (t < ptiles) {
       reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, k);
-      const int tokens = group_tokens(p, g) | kItemPrefix;
-      int prev = 0, j = 0;
-      auto piece = [&](int b) {
-        emit(b - prev, gr[g].x, t - gr[g].w, prev * kGroupKeys, min(b * kGroupKeys, gr[g].y),
-             make_int4(base + j * kTileRows, gr[g].z, tokens, 0));
-        prev = b;
-        ++j;
-      };
-      tile_cuts(a, n, W, piece);
-      piece(n);
+      const int tokens = max(token_edge(p, edge(g + 1)) - v.z, 0);
+      emit(a, n, v.x, t - v.w, 0, v.y, make_int4(0, v.z, tokens | kItemPrefix, 0),
+           [&](int j) { return base + j * kTileRows; });
     }
   }
+  carry = pos_carry;
   for (int r0 = 0; r0 < R; r0 += kThreads) {
     const int r = r0 + tid;
     Own o{};
-    int k = 0, g = -1, rows = 0;
-    if (r < R) {
-      g = p.req_group[r];
-      o = own_keys(p, r, g >= 0 ? gr[g].y : 0);
-      if (o.tiles > 0) {
-        k = own_pieces(o.groups, W);
-        if (g >= 0 || k > 1) rows = k * o.qlen * H;
-      }
-    }
-    int sum;
-    int base = row_carry + block_scan<int>(rows, s.red, &sum);
-    row_carry += sum;
-    const int size = k > 0 ? cdiv(o.groups, k) : 0;
+    if (r < R) o = own_keys(r);
+    long long sum;
+    const long long a = carry + block_scan<long long>(static_cast<long long>(o.tiles) * o.groups, s.red, &sum);
+    carry += sum;
+    const bool part = r < R && o.q.w >= 0;
+    int rows = 0;
     for (int t = 0; t < o.tiles; ++t) {
-      const int tr = min(kTileRows, o.qlen * H - t * kTileRows);
-      reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(rows > 0 ? base : -1, k);
-      for (int j = 0; j < k; ++j) {
-        const int b0 = min(j * size, o.groups), b1 = min(b0 + size, o.groups);
-        emit(b1 - b0, r, t, o.first + b0 * kGroupKeys, j + 1 == k ? max(o.len, o.first) : o.first + b1 * kGroupKeys,
-             make_int4(rows > 0 ? base + j * tr : -1, o.tok0, o.qlen, o.len - o.qlen + 1));
-      }
-      base += rows > 0 ? k * tr : 0;
+      const int k = 1 + tile_cuts(a + static_cast<long long>(t) * o.groups, o.groups, W, [](int) {});
+      if (part || k > 1) rows += k * min(kTileRows, o.q.y * H - t * kTileRows);
+    }
+    int rsum;
+    int base = row_carry + block_scan<int>(rows, s.red, &rsum);
+    row_carry += rsum;
+    for (int t = 0; t < o.tiles; ++t) {
+      const long long at = a + static_cast<long long>(t) * o.groups;
+      const int k = 1 + tile_cuts(at, o.groups, W, [](int) {});
+      const int tr = min(kTileRows, o.q.y * H - t * kTileRows);
+      const bool split = part || k > 1;
+      reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(split ? base : -1, k);
+      emit(at, o.groups, r, t, o.first, max(o.q.z, o.first), make_int4(0, o.q.x, o.q.y, o.q.z - o.q.y + 1),
+           [&](int j) { return split ? base + j * tr : -1; });
+      if (split) base += k * tr;
     }
   }
 }
@@ -287,7 +316,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
   const int H = p.num_heads;
   const int t = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(t) * H);
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  // (the tables come from the schedule, which completed before the decode began: they
+  // are read while the decode may still run)
   int r = t, tok0 = t;
   if (p.qo_indptr != nullptr) {
     if (t < p.qo_indptr[0] || t >= p.qo_indptr[p.num_reqs]) return;  // padding of the batch
@@ -314,6 +344,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
                      : static_cast<int64_t>(own.x) + static_cast<int64_t>(s - pre.y) * own_stride + own_row % kTileRows;
   };
   const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   float M = sink2;
   float m0 = -INFINITY, l0 = 0.f;  // of piece `lane`
   for (int s = lane; s < live; s += 32) {

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI declared in include/mla_decode.h: host-side argument
 // checks, the planner, and the launches of the decode, merge and index
 // kernels. Nothing here allocates device memory or synchronises a stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -22,6 +23,7 @@ constexpr int64_t kRowsNMax = 128;  // query rows per request the rows-as-N kern
 constexpr int32_t kMaxWorkers = 1024;  // workers of the contiguous schedule
 static_assert(sizeof(mla_problem_t) == 68 && sizeof(mla_plan_t) == 168 && sizeof(mla_shared_plan_t) == 200,
               "the plan layouts the bindings mirror");
+constexpr int32_t kMaxPairs = 256;  // workers of a list of shared prefixes
 constexpr size_t kWsAlign = 256;
 
 thread_local const char* g_last_cuda_error = "";
@@ -496,7 +498,7 @@ bool shares_prefixes(const mla_problem_t& p) {
 
 // Workspace pieces of a shared call, after the status block.
 struct SharedLayout {
-  size_t n_items, items, unit_tab, req_group, groups, group_pos, prefix_tab, segm_out, segm_max, segm_expsum, end;
+  size_t n_items, worker_first, items, unit_tab, req_group, groups, group_pos, prefix_tab, segm_out, segm_max, segm_expsum, end;
 };
 SharedLayout shared_layout(const mla_shared_plan_t* sp) {
   const mla_problem_t& p = sp->plan.prob;
@@ -509,11 +511,12 @@ SharedLayout shared_layout(const mla_shared_plan_t* sp) {
     return a;
   };
   l.n_items = take(4);
+  l.worker_first = take((static_cast<size_t>(sp->workers) + 1) * 4);
   l.items = take(static_cast<size_t>(sp->max_items) * 32);
   l.unit_tab = take(R * sp->unit_tiles * 8);
   l.req_group = take(R * 4);
   l.groups = take(G * 16);
-  l.group_pos = take(G * 8);
+  l.group_pos = take(G * 4);
   l.prefix_tab = take(static_cast<size_t>(sp->prefix_tiles) * 8);
   l.segm_out = take(static_cast<size_t>(sp->partial_rows) * kRank * 4);
   l.segm_max = take(static_cast<size_t>(sp->partial_rows) * 4);
@@ -526,7 +529,7 @@ mla_status_t check_shared(const mla_shared_plan_t* sp) {
   if (sp == nullptr) return MLA_ERR_INVALID_ARG;
   const mla_status_t s = check_problem(sp->plan.prob);
   if (s != MLA_OK) return s;
-  if (sp->num_groups < 1 || sp->workers < 0 || sp->max_items < 0 || sp->unit_tiles < 0 || sp->prefix_tiles < 0 ||
+  if (sp->num_groups < 1 || sp->workers < (sp->max_items > 0 ? 1 : 0) || sp->workers > kMaxPairs || sp->max_items < 0 || sp->unit_tiles < 0 || sp->prefix_tiles < 0 ||
       sp->partial_rows < 0)
     return MLA_ERR_INVALID_ARG;
   return MLA_OK;
@@ -746,12 +749,14 @@ mla_status_t mla_decode_shared_plan(const mla_problem_t* prob, int32_t num_group
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   const int64_t unit_tiles = (static_cast<int64_t>(p.max_qlen) * p.num_heads + 127) / 128;
   const int64_t prefix_tiles = (rows + 127) / 128 + num_groups;  // each group's last may be cut short
-  const int64_t workers = plan->plan.num_sms / 2 > 0 ? plan->plan.num_sms / 2 : 1;
+  const int64_t workers = std::min<int64_t>(std::max(plan->plan.num_sms / 2, 1), kMaxPairs);
   // every cut that the schedule makes ends a worker's share: at most `workers`, and as
   // many pieces more
   const int64_t items = prefix_tiles + unit_tiles * p.num_reqs + workers;
   const int64_t partial = (prefix_tiles + workers) * 128 + rows;
-  if (items > (1 << 22) || partial > (1 << 24)) return MLA_OK;  // (runs as mla_decode_fwd)
+  // (beyond these the list's 32-bit places do not reach: the calls run as mla_decode_fwd)
+  const int64_t length = (prefix_tiles + unit_tiles * p.num_reqs) * (p.max_seq_len / 128 + 8);
+  if (items > (1 << 22) || partial > (1 << 24) || length > (1 << 30)) return MLA_OK;
   plan->workers = static_cast<int32_t>(workers);
   plan->max_items = static_cast<int32_t>(items);
   plan->unit_tiles = static_cast<int32_t>(unit_tiles);
@@ -805,16 +810,18 @@ mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q,
   x.num_heads = p.num_heads;
   x.block_size = p.block_size;
   x.cols = p.max_blocks_per_req;
-  x.workers = plan->workers > 0 ? plan->workers : 1;
+  x.workers = plan->workers;
   x.tiles_max = plan->unit_tiles;
   x.ptiles_max = plan->prefix_tiles;
   x.max_items = plan->max_items;
   x.items = reinterpret_cast<int32_t*>(ws + l.items);
   x.n_items = reinterpret_cast<int32_t*>(ws + l.n_items);
+  const bool pairs = p.kv_dtype == MLA_DTYPE_FP8_E4M3;
+  x.worker_first = pairs ? reinterpret_cast<int32_t*>(ws + l.worker_first) : nullptr;
   x.unit_tab = reinterpret_cast<int32_t*>(ws + l.unit_tab);
   x.req_group = reinterpret_cast<int32_t*>(ws + l.req_group);
   x.groups = reinterpret_cast<int32_t*>(ws + l.groups);
-  x.group_pos = reinterpret_cast<int64_t*>(ws + l.group_pos);
+  x.group_pos = reinterpret_cast<int32_t*>(ws + l.group_pos);
   x.prefix_tab = reinterpret_cast<int32_t*>(ws + l.prefix_tab);
   x.segm_out = reinterpret_cast<float*>(ws + l.segm_out);
   x.segm_max = reinterpret_cast<float*>(ws + l.segm_max);
@@ -827,6 +834,7 @@ mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q,
   mla::DecodeParams d = make_params(&plan->plan, in);
   d.items = x.items;
   d.n_items = x.n_items;
+  d.worker_first = x.worker_first;
   d.shared = 1;
   d.slot_rows = 1;  // the items name rows
   d.sinks = sinks;
@@ -840,8 +848,7 @@ mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q,
   const int64_t kv_rows = static_cast<int64_t>(p.num_blocks) * p.block_size;
   const unsigned items = static_cast<unsigned>(plan->max_items);
   int* status = reinterpret_cast<int*>(ws);
-  s = cuda_status(p.kv_dtype == MLA_DTYPE_FP8_E4M3
-                      ? mla::launch_decode_pair(d, q_rows, kv_rows, items, status, stream)
+  s = cuda_status(pairs ? mla::launch_decode_pair(d, q_rows, kv_rows, static_cast<unsigned>(plan->workers), status, stream)
                       : mla::launch_decode_tc(d, false, q_rows, kv_rows, dim3(2u * items), status, stream));
   if (s != MLA_OK) return s;
   return cuda_status(mla::launch_prefix_merge(x, stream));

@@ -44,9 +44,9 @@
 // loaded without the other). Softmax warps arrive on rank 0's barriers, from
 // either CTA.
 //
-// Warps: 0 loads, 1 issues Q K^T (rank 1: passes keys on), 2 prepares the keys'
-// scales, 3 issues P V (passes values on), 4-19 softmax and epilogue. Every wait
-// is bounded: a timeout records a code in the status word, stops the CTA's
+// Warps: 0 loads keys, 1 issues Q K^T (rank 1: passes keys on), 2 prepares the keys'
+// scales, 3 issues P V (passes values on), 4 and 5 load values, 6 watches the time, 8-23 softmax and
+// epilogue. Every wait is bounded: a timeout records a code in the status word, stops the CTA's
 // work, drains what was issued and exits.
 #include <atomic>
 #include <climits>
@@ -75,7 +75,14 @@ constexpr int kSoftWarps = 16;
 constexpr int kGroupWarps = 8;
 constexpr int kPart = 32;                 // keys of a softmax warp
 constexpr int kUni = 16;                  // keys that share their scale where the groups are multiples of it
-constexpr int kThreads = 32 * (4 + kSoftWarps);
+constexpr int kRoleWarps = 8;             // warps 0-7, then the softmax's
+constexpr int kThreads = 32 * (kRoleWarps + kSoftWarps);
+// Registers a thread: the launch's (of 65536, a warp's in steps of 8 a thread), and after the roles
+// have given some of theirs up for the softmax; the sum stays within the launch's.
+constexpr int kLaunchRegs = 80, kRoleRegs = 40, kSoftRegs = 96;
+static_assert(kThreads * kLaunchRegs <= 65536 &&
+                  32 * (kRoleWarps * kRoleRegs + kSoftWarps * kSoftRegs) <= kThreads * kLaunchRegs,
+              "registers of the launch");
 constexpr int kPTile = kOwnRows * kKeys;  // one term of P of a chunk
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;            // 256 columns: 128 for each j
@@ -100,29 +107,31 @@ enum : int {
   kOReady = kPFull + 2,        // [2] rank 0: O_1 rescaled
   kX = kOReady + 2,            // [4][2] (at c % 4) the four warps of 32 rows have posted their maxima
   kScFree = kX + 8,            // [2] key scales read
-  kXL = kScFree + 2,           // [2] the eight warps of 32 rows have posted their sums
-  kDrainQK = kXL + 2,          // Q K^T and P V complete, in both CTAs
+  kXL = kScFree + 2,           // [2] the eight warps of 32 rows have posted their sums of an item
+  kOFree = kXL + 2,            // rank 0: both CTAs have read O of an item
+  kStage,                      // an item's output has left the value ring
+  kDrainQK,                    // Q K^T and P V complete, in both CTAs
   kDrainPV,
   kNumBars
 };
 
 // Shared memory.
 constexpr int kOffBar = 0;
+constexpr int kOffWatch = 400;                  // Watch
 constexpr int kOffTslot = 448;
-constexpr int kOffAbort = 452;
-constexpr int kOffIssued = 456;                  // {last chunk of keys, last box of values} issued
+constexpr int kOffIssued = 464;                  // {last chunk of keys, of values j = 0, 1, last q} issued
 constexpr int kOffMask = 480;                    // [2][4] bits of existing keys of chunk c (at c % 2)
 constexpr int kOffXMax = 512;                    // [4][4][64] maxima of chunk c (at c % 4) by key quarter
 constexpr int kOffScale = kOffXMax + 4096;       // [2][mul, add, inv][128]
-constexpr int kOffLsum = kOffScale + 3 * 1024;   // [2][4][64] row sums by group and key quarter
-constexpr int kOffQ = 10240;                     // 4 boxes of 64 rows, 128-byte swizzle; rope box, 64-byte swizzle
+constexpr int kOffLsum = kOffScale + 3 * 1024;   // [2][2][4][64] row sums (of item i at i % 2) by group and key quarter
+constexpr int kOffQ = 12288;                     // 4 boxes of 64 rows, 128-byte swizzle; rope box, 64-byte swizzle
 constexpr int kOffP = kOffQ + kKSlot;            // [c % 2][hi, lo] 64 rows x 128 keys, 128-byte swizzle
 constexpr int kOffK = kOffP + 4 * kPTile;
 constexpr int kOffV = kOffK + kKRing * kKSlot;
 constexpr int kSmem = kOffV + kVRing * kVSlot + 1024;  // + alignment slack
-static_assert(kNumBars * 8 <= kOffTslot && kOffLsum + 2048 <= kOffQ, "header space");
+static_assert(kNumBars * 8 <= kOffWatch && kOffLsum + 4096 <= kOffQ, "header space");
 static_assert(kSmem <= 232448, "shared memory budget");
-static_assert(kKRing * kKSlot + kVRing * kVSlot >= kSoftWarps * 8192, "the epilogue stages in the rings");
+static_assert(kVRing * kVSlot >= kSoftWarps * 4096, "the epilogue stages in the value ring");
 
 struct PairMaps {
   CUtensorMap q;     // q as [T*H rows, 576], box 128 bytes x 64 rows
@@ -140,18 +149,32 @@ enum class Scale { kNone, kSixteen, kKey };
 struct Ctx {
   uint8_t* smem;
   uint32_t bar0, lead0;  // barriers of this CTA and of rank 0 (cluster addresses)
-  volatile int* abort;
-  int* status;
-  uint64_t limit_ns;
   uint32_t tbase;
   int tid, warp, lane, rank;
-  int H, unit, tok0, row0, rows_total;
-  int see0;              // keys that the first token of the unit sees; INT_MAX: all rows see all keys
-  int seg_start, seg_end, n_chunks;
-  int pslot;             // first row of the partial's slot, -1: write out/lse
+  int first, last;       // the pair's items
   __device__ uint32_t bar(int i) const { return bar0 + 8u * i; }
   __device__ uint32_t lead(int i) const { return lead0 + 8u * i; }
 };
+
+// An item of the list.
+struct Item {
+  int unit, row0, seg_start, seg_end, n;  // n: chunks
+  int pslot;             // first row of the partial's slot, -1: write out/lse
+  int tok0, tokens;
+  int see0;              // keys that the first token of the unit sees; INT_MAX: all rows see all keys
+};
+// The same for the whole warp, and for the compiler: loops that it takes for
+// divergent keep the matrix instructions' descriptors in vector registers (250
+// cycles an instruction).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ Item item_at(const DecodeParams& p, int i) {
+  int4 a = reinterpret_cast<const int4*>(p.items)[2 * i];
+  int4 b = reinterpret_cast<const int4*>(p.items)[2 * i + 1];
+  a = make_int4(uniform(a.x), uniform(a.y), uniform(a.z), uniform(a.w));
+  b = make_int4(uniform(b.x), uniform(b.y), uniform(b.z), uniform(b.w));
+  return Item{a.x, a.y * kRows, a.z, a.w, a.w > a.z ? cdiv(a.w - a.z, kKeys) : 0, b.x, b.y, b.z & kItemTokens,
+              (b.z & kItemPrefix) != 0 ? INT_MAX : b.w};
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -200,12 +223,48 @@ __device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
+// The matrix instructions of a step, with descriptors formed by additions to
+// their lower words from a base in between: what changes from one instruction to
+// the next is two words. (64-bit descriptors computed outside took the issuing
+// warp 100 to 125 cycles an instruction, more than its 64 tensor cycles.)
+//
+// Four steps of 32 columns of a 128-byte column box: D (+)= A B.
+__device__ __forceinline__ void mma_box(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b32 l, t;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n"
+      " add.u32 t, %1, 2;\n add.u32 l, %3, 2;\n mov.b64 a, {t, %2};\n mov.b64 b, {l, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n"
+      " add.u32 t, %1, 4;\n add.u32 l, %3, 4;\n mov.b64 a, {t, %2};\n mov.b64 b, {l, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n"
+      " add.u32 t, %1, 6;\n add.u32 l, %3, 6;\n mov.b64 a, {t, %2};\n mov.b64 b, {l, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two steps of the 64-byte rope box: D += A B.
+__device__ __forceinline__ void mma_rope(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .b32 l, t;\n .reg .b64 a, b;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n"
+      " add.u32 t, %1, 2;\n add.u32 l, %3, 2;\n mov.b64 a, {t, %2};\n mov.b64 b, {l, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc)
+      : "memory");
+}
+// A step of 32 keys of P V, both terms of P (kPTile bytes apart): D (+)= A B, D += A' B.
+__device__ __forceinline__ void mma_terms(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t id_hi, uint32_t id_lo, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b32 t;\n .reg .b64 a, b;\n setp.ne.b32 p, %7, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n"
+      " add.u32 t, %1, %8;\n mov.b64 a, {t, %2};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %6, 1;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(id_hi), "r"(id_lo), "r"(accumulate), "n"(kPTile >> 4)
       : "memory");
 }
 // Arrive once on the barrier at this offset in both CTAs when every MMA this
@@ -224,40 +283,63 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ------------------------------------------------------------------ waits
-__device__ __forceinline__ void report(int* status, int code) {
-  if (status != nullptr) atomicCAS(status, 0, code);
+// A wait ends when its phase completes or when the CTA gives up, which one warp
+// decides for all (watch): a clock, a limit and a report at each of some thirty waits
+// made the kernel's code a third larger, and the warps waited for instructions a
+// fifth of their time.
+struct Watch {
+  int* status;
+  uint64_t ns;            // limit
+  volatile int abort;
+  volatile int progress;  // changes with every chunk of the softmax
+  int finished;           // softmax warps that have ended
+};
+__device__ __forceinline__ Watch* watch_of(const uint8_t* smem) {
+  return reinterpret_cast<Watch*>(const_cast<uint8_t*>(smem) + kOffWatch);
 }
 
-// Bounded wait on a barrier phase, sleeping; false on timeout (recorded) or
-// abort. Barriers that the other CTA arrives on are waited for as the CTA's own:
-// no thread reads what one of the other CTA wrote through the generic proxy (P,
-// S and O are read by the tensor core of the SM that holds them, after proxy and
-// tcgen05 fences), and acquire and release at cluster scope took 1000 to 2000 cycles
-// each (168 us against 192 for 64 requests over 8192 common keys, 128 heads).
-__device__ bool wait_phase(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  const bool brief = x.limit_ns < kSleepNs;  // (a sleep may last longer than the limit: poll)
-  if (mbar_test_wait(bar, parity)) return true;
-  if (!brief && mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!(brief ? mbar_test_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepNs))) {
-    if (*x.abort) return false;
-    if (global_timer_ns() - t0 > x.limit_ns) {
-      report(x.status, code);
-      *x.abort = 1;
-      return false;
-    }
+// Wait on a barrier phase, sleeping; false when the CTA gives up. Barriers that the
+// other CTA arrives on are waited for as the CTA's own: no thread reads what one of
+// the other CTA wrote through the generic proxy (P, S and O are read by the tensor
+// core of the SM that holds them, after proxy and tcgen05 fences), and acquire and
+// release at cluster scope took 1000 to 2000 cycles each (168 us against 133 for 64
+// requests over 8192 common keys, 128 heads).
+__device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t parity) {
+  bool ok = mbar_test_wait(bar, parity);
+  while (!__all_sync(0xffffffffu, ok)) {
+    ok = mbar_try_wait_sleep(bar, parity, kSleepNs);
+    if (__any_sync(0xffffffffu, !ok && watch_of(x.smem)->abort != 0)) return false;
   }
   return true;
 }
-__device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
-  return __all_sync(0xffffffffu, wait_phase(x, bar, parity, code)) != 0;
+// Warp 6: gives up, with a code in the status word, when the softmax has made no
+// progress for the limit. All other waits come to an end with the softmax's, or
+// are bounded by themselves (drain_wait).
+__device__ void watch(const Ctx& x) {
+  Watch* w = watch_of(x.smem);
+  int seen = -1;
+  uint64_t t0 = 0;
+  if (x.lane == 0) {
+    while (*static_cast<volatile int*>(&w->finished) < kSoftWarps && !w->abort) {
+      const uint64_t now = global_timer_ns();
+      if (w->progress != seen) {
+        seen = w->progress;
+        t0 = now;
+      } else if (now - t0 > w->ns) {
+        if (w->status != nullptr) atomicCAS(w->status, 0, 11);
+        w->abort = 1;
+      }
+      __nanosleep(1000);
+    }
+  }
+  __syncwarp();
 }
-// Wait that ignores the abort flag (teardown), still bounded.
-__device__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
+// Wait that ignores the abort flag (teardown), bounded by itself.
+__device__ __forceinline__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait_sleep(bar, parity, kSleepNs)) {
     if (global_timer_ns() - t0 > kDefaultWaitNs) {
-      report(x.status, code);
+      if (watch_of(x.smem)->status != nullptr) atomicCAS(watch_of(x.smem)->status, 0, code);
       return;
     }
   }
@@ -272,22 +354,22 @@ struct RowWindow {
   static constexpr int kPer = kKeys / BOX;   // runs of a chunk
   static constexpr int kSpan = 32 / kPer;    // chunks of a window
   int cur, nxt;
-  __device__ __forceinline__ int look(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int w0) const {
-    const int pos = x.seg_start + w0 * kKeys + x.lane * BOX;
-    if (pos >= x.seg_end) return -BOX;
+  __device__ __forceinline__ int look(const Ctx& x, const DecodeParams& p, const Item& it, int w0) const {
+    const int pos = it.seg_start + w0 * kKeys + x.lane * BOX;
+    if (pos >= it.seg_end) return -BOX;
     const int blk = pos / p.block_size;
-    const int b = bt_row[blk];
+    const int b = p.block_table[static_cast<int64_t>(it.unit) * p.bt_stride + blk];
     return b < 0 ? -BOX : b * p.block_size + (pos - blk * p.block_size);
   }
-  __device__ __forceinline__ void start(const Ctx& x, const DecodeParams& p, const int32_t* bt_row) {
-    cur = look(x, p, bt_row, 0);
-    nxt = look(x, p, bt_row, kSpan);
+  __device__ __forceinline__ void start(const Ctx& x, const DecodeParams& p, const Item& it) {
+    cur = look(x, p, it, 0);
+    nxt = look(x, p, it, kSpan);
   }
   // moves on to the window of chunk c (called for every chunk in turn)
-  __device__ __forceinline__ void at(const Ctx& x, const DecodeParams& p, const int32_t* bt_row, int c) {
+  __device__ __forceinline__ void at(const Ctx& x, const DecodeParams& p, const Item& it, int c) {
     if (c > 0 && c % kSpan == 0) {
       cur = nxt;
-      nxt = look(x, p, bt_row, c + kSpan);
+      nxt = look(x, p, it, c + kSpan);
     }
   }
   __device__ __forceinline__ int row(int c, int run) const {
@@ -295,82 +377,83 @@ struct RowWindow {
   }
 };
 
-// Warp 0: the keys of each chunk (five column boxes of this CTA's 64 rows) and its
-// values (two column boxes of all 128 rows), each as soon as
-// its slot is free; the boxes of a kind go out together, one lane each. (In
-// turn, the keys of a chunk waited behind the values of the one before, whose
-// slots P V frees late: 4600 cycles a chunk. A warp more for either would leave 80
-// registers a thread.)
+// Warp 0: q of each item (its 64 rows), and the keys of each chunk (five column
+// boxes of this CTA's 64 rows), a box by each of as many lanes. Warps 4 and 5: one
+// column box of values of each chunk (all 128 rows). Copies of one warp move about 27
+// bytes a clock, of the 36 that a chunk needs in 1860 cycles, and a warp of its
+// own runs some hundred instructions in that time: with keys and values in one
+// warp a chunk took 2300 to 3500 cycles, with values and scales in one 4700. The
+// rings run on across items: q and the first keys of the next one load while this
+// one's last chunks and its output are under way; its values wait for the output, which
+// is staged in their ring.
 template <int BOX>
-__device__ void load_boxes(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
+__device__ void load_keys(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
   constexpr int kSub = kHalf / BOX;  // boxes high of 64 rows
   const int box = x.lane / kSub, run = x.lane % kSub;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   volatile int* issued = reinterpret_cast<volatile int*>(x.smem + kOffIssued);
   const uint32_t base = smem_u32(x.smem);
-  RowWindow<BOX> kw, vw;
-  kw.start(x, p, bt_row);
-  vw = kw;
-  uint64_t t0 = 0;
-  int polls = 0;
-  for (int c = 0, g = 0; g < 2 * x.n_chunks;) {
-    bool idle = true;
-    if (c < x.n_chunks) {
+  RowWindow<BOX> w;
+  int c = 0, q = 0;  // chunks and q's so far
+  for (int i = x.first; i < x.last; ++i) {
+    const Item it = item_at(p, i);
+    if (it.n == 0) continue;
+    w.start(x, p, it);
+    for (int k = 0; k < it.n; ++k, ++c) {
       const int s = c % kKRing;
-      if (c < kKRing || __all_sync(0xffffffffu, mbar_test_wait(x.bar(kKEmpty + s), (c / kKRing - 1) & 1))) {
-        kw.at(x, p, bt_row, c);
-        if (x.lane == 0) {
-          mbar_arrive_expect_tx(x.bar(kKFull + s), kKSlot);
-          issued[0] = c;
-        }
-        __syncwarp();
-        const int row = kw.row(c, x.rank * kSub + run);
-        const uint32_t to = base + kOffK + s * kKSlot;
-        if (box < 4) tma_load_2d(to + box * kBox + run * BOX * 128, &maps.kv, 128 * box, row, x.bar(kKFull + s));
-        if (box == 4) tma_load_2d(to + 4 * kBox + run * BOX * 64, &maps.kvr, kRank, row, x.bar(kKFull + s));
-        __syncwarp();
-        ++c;
-        idle = false;
-      }
-    }
-    {
-      const int s = g % kVRing;
-      if (g < kVRing || __all_sync(0xffffffffu, mbar_test_wait(x.bar(kVEmpty + s), (g / kVRing - 1) & 1))) {
-        if ((g & 1) == 0) vw.at(x, p, bt_row, g >> 1);
-        if (x.lane == 0) {
-          mbar_arrive_expect_tx(x.bar(kVFull + s), kVSlot);
-          issued[1] = g;
-        }
-        __syncwarp();
-        const int vrun = x.lane % (2 * kSub);  // (of 128 rows)
-        const int row = vw.row(g >> 1, vrun);
-        if (x.lane < 2 * kSub)
-          tma_load_2d(base + kOffV + s * kVSlot + vrun * BOX * 128, &maps.kv, 128 * (2 * (g & 1) + x.rank), row,
-                      x.bar(kVFull + s));
-        __syncwarp();
-        ++g;
-        idle = false;
-      }
-    }
-    if (!idle) {
-      t0 = 0;
-      polls = 0;
-      continue;
-    }
-    __nanosleep(40);
-    if ((++polls & 63) != 0) continue;  // (reading the global timer takes longer than most waits)
-    const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
-    if (t0 == 0) t0 = now;
-    if (__shfl_sync(0xffffffffu, *x.abort, 0)) break;
-    if (now - t0 > x.limit_ns) {
+      if (c >= kKRing && !warp_wait(x, x.bar(kKEmpty + s), (c / kKRing - 1) & 1)) return;
+      // (q, once Q K^T of the item before is complete)
+      if (k == 0 && c > 0 && !warp_wait(x, x.bar(kKEmpty + (c - 1) % kKRing), ((c - 1) / kKRing) & 1)) return;
+      w.at(x, p, it, k);
+      const uint32_t full = x.bar(kKFull + s), to = base + kOffK + s * kKSlot;
       if (x.lane == 0) {
-        report(x.status, 11);
-        *x.abort = 1;
+        mbar_arrive_expect_tx(full, kKSlot);
+        issued[0] = c;
+        if (k == 0) {
+          mbar_arrive_expect_tx(x.bar(kQFull), kKSlot);
+          issued[3] = q;
+        }
       }
-      break;
+      __syncwarp();
+      if (k == 0 && x.lane < 5) {  // (rows past the last are zeros)
+        const int qrow = it.tok0 * p.num_heads + it.row0 + kOwnRows * x.rank;
+        tma_load_2d(base + kOffQ + x.lane * kBox, x.lane < 4 ? &maps.q : &maps.qr, 128 * x.lane, qrow, x.bar(kQFull));
+      }
+      const int row = w.row(k, x.rank * kSub + run);
+      if (box < 5)
+        tma_load_2d(to + box * kBox + run * BOX * (box < 4 ? 128 : 64), box < 4 ? &maps.kv : &maps.kvr, 128 * box, row, full);
+      __syncwarp();
+    }
+    ++q;
+  }
+}
+
+template <int BOX>
+__device__ void load_values(const Ctx& x, const PairMaps& maps, const DecodeParams& p, int j) {
+  constexpr int kRuns = kKeys / BOX;  // boxes high of 128 rows
+  volatile int* issued = reinterpret_cast<volatile int*>(x.smem + kOffIssued);
+  const int run = x.lane % kRuns;
+  const uint32_t to0 = smem_u32(x.smem) + kOffV + run * BOX * 128;
+  RowWindow<BOX> w;
+  int c = 0;  // chunks so far
+  for (int i = x.first; i < x.last; ++i) {
+    const Item it = item_at(p, i);
+    if (it.n > 0) w.start(x, p, it);
+    // (the outputs in turn, those of empty items too: no phase is passed over)
+    if (i > x.first && !warp_wait(x, x.bar(kStage), (i - 1 - x.first) & 1)) return;
+    for (int k = 0; k < it.n; ++k, ++c) {
+      const int v = 2 * c + j, s = v % kVRing;
+      w.at(x, p, it, k);
+      const int row = w.row(k, run);
+      if (v >= kVRing && !warp_wait(x, x.bar(kVEmpty + s), (v / kVRing - 1) & 1)) return;
+      if (x.lane == 0) {
+        mbar_arrive_expect_tx(x.bar(kVFull + s), kVSlot);
+        issued[1 + j] = c;
+      }
+      __syncwarp();
+      if (x.lane < kRuns) tma_load_2d(to0 + s * kVSlot, &maps.kv, 128 * (2 * j + x.rank), row, x.bar(kVFull + s));
+      __syncwarp();
     }
   }
-  __syncwarp();
 }
 
 __device__ __forceinline__ float scale_of_slot(const DecodeParams& p, int s) {
@@ -383,60 +466,73 @@ __device__ __forceinline__ float scale_of_slot(const DecodeParams& p, int s) {
 // chunk ahead of the one posted, each once the softmax has read those two chunks back.
 template <int BOX, Scale SCALE>
 __device__ void prepare_keys(const Ctx& x, const DecodeParams& p) {
+  constexpr int kParts = SCALE == Scale::kKey ? 4 : 1;
   const int lane = x.lane;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(x.unit) * p.bt_stride;
   RowWindow<BOX> w;
-  w.start(x, p, bt_row);
-  float sc[4];
-  uint32_t bits[4];
-  auto read = [&](int c) {
-    w.at(x, p, bt_row, c);
-    const int n = x.seg_end - (x.seg_start + c * kKeys);
+  float sc[kParts];
+  uint32_t bits = 0u;  // lane k < 4: existing keys of part k
+  int g = 0;           // chunks so far
+  for (int i = x.first; i < x.last; ++i) {
+    const Item it = item_at(p, i);
+    if (it.n == 0) continue;
+    w.start(x, p, it);
+    auto read = [&](int c) {
+      w.at(x, p, it, c);
+      const int n = it.seg_end - (it.seg_start + c * kKeys);
+      // whether a run of this chunk has no block
+      const uint32_t gone = __ballot_sync(0xffffffffu, w.cur < 0) >> (RowWindow<BOX>::kPer * (c % RowWindow<BOX>::kSpan));
+      const bool whole = n >= kKeys && (gone & ((1u << RowWindow<BOX>::kPer) - 1u)) == 0u;
+      bits = 0xffffffffu;
+      if (!whole) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = 32 * i + lane;
-      const int row = w.row(c, j / BOX);
-      const bool there = j < n && row >= 0;
-      bits[i] = __ballot_sync(0xffffffffu, there);
-      if constexpr (SCALE == Scale::kKey) sc[i] = there ? scale_of_slot(p, row + j % BOX) : 1.f;
-    }
-    if constexpr (SCALE == Scale::kSixteen) {
-      const int j = kUni * (lane & 7);
-      const int row = w.row(c, j / BOX);
-      sc[0] = j < n && row >= 0 ? scale_of_slot(p, row + j % BOX) : 1.f;
-    }
-  };
-  if (x.n_chunks > 0) read(0);
-  for (int c = 0; c < x.n_chunks; ++c) {
-    const int b = c & 1;
-    if (c >= 2 && !warp_wait(x, x.bar(kScFree + b), ((c >> 1) - 1) & 1, 27)) break;
-    float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + b * 3 * kKeys;
-    if (lane < 4)
-      reinterpret_cast<uint32_t*>(x.smem + kOffMask)[b * 4 + lane] =
-          lane == 0 ? bits[0] : lane == 1 ? bits[1] : lane == 2 ? bits[2] : bits[3];
-    if constexpr (SCALE != Scale::kNone) {
-#pragma unroll
-      for (int i = 0; i < (SCALE == Scale::kKey ? 4 : 1); ++i) {
-        const KeyScale k = key_scale(sc[i], p.score_scale_log2);
-        const int at = SCALE == Scale::kKey ? 32 * i + lane : kUni * lane;
-        if (SCALE == Scale::kKey || lane < kKeys / kUni) {
-          ks[at] = k.mul;
-          ks[kKeys + at] = k.add;
-          ks[2 * kKeys + at] = k.inv;
+        for (int k = 0; k < 4; ++k) {
+          const int j = 32 * k + lane;
+          const int row = w.row(c, j / BOX);  // (all lanes: a shuffle)
+          const uint32_t there = __ballot_sync(0xffffffffu, j < n && row >= 0);
+          if (lane == k) bits = there;
         }
       }
+      if constexpr (SCALE != Scale::kNone) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const int j = SCALE == Scale::kKey ? 32 * k + lane : kUni * (lane & 7);
+          const int row = w.row(c, j / BOX);
+          sc[k] = j < n && row >= 0 ? scale_of_slot(p, row + j % BOX) : 1.f;
+        }
+      }
+    };
+    read(0);
+    for (int c = 0; c < it.n; ++c, ++g) {
+      const int b = g & 1;
+      if (g >= 2 && !warp_wait(x, x.bar(kScFree + b), ((g >> 1) - 1) & 1)) return;
+      float* ks = reinterpret_cast<float*>(x.smem + kOffScale) + b * 3 * kKeys;
+      if (lane < 4) reinterpret_cast<uint32_t*>(x.smem + kOffMask)[b * 4 + lane] = bits;
+      if constexpr (SCALE != Scale::kNone) {
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const KeyScale ks1 = key_scale(sc[k], p.score_scale_log2);
+          const int at = SCALE == Scale::kKey ? 32 * k + lane : kUni * lane;
+          if (SCALE == Scale::kKey || lane < kKeys / kUni) {
+            ks[at] = ks1.mul;
+            ks[kKeys + at] = ks1.add;
+            ks[2 * kKeys + at] = ks1.inv;
+          }
+        }
+      }
+      __syncwarp();
+      if (g >= 2 && !warp_wait(x, x.bar(kSFull + b), ((g >> 1) - 1) & 1)) return;  // S two chunks back
+      if (lane == 0) mbar_arrive(x.bar(kSFull + b));
+      if (c + 1 < it.n) read(c + 1);
     }
-    __syncwarp();
-    if (c >= 2 && !warp_wait(x, x.bar(kSFull + b), ((c >> 1) - 1) & 1, 28)) break;  // S two chunks back
-    if (lane == 0) mbar_arrive(x.bar(kSFull + b));
-    if (c + 1 < x.n_chunks) read(c + 1);
   }
-  __syncwarp();
 }
 
 // ------------------------------------------------------------------ MMA issue
+__device__ __forceinline__ uint32_t lo(uint64_t v) { return static_cast<uint32_t>(v); }
+__device__ __forceinline__ uint32_t hi(uint64_t v) { return static_cast<uint32_t>(v >> 32); }
+
 // Rank 0, warp 1.
-__device__ void qk_issue(const Ctx& x) {
+__device__ void qk_issue(const Ctx& x, const DecodeParams& p) {
   constexpr uint32_t kId = instr_desc(kRows, kKeys, 0, 0, false, false);
   const uint32_t base = smem_u32(x.smem);
   const uint64_t q_desc = smem_desc_sw128(base + kOffQ, 16, 1024);
@@ -444,29 +540,31 @@ __device__ void qk_issue(const Ctx& x) {
   const uint64_t k_desc = smem_desc_sw128(base + kOffK, 16, 1024);
   const uint64_t kr_desc = smem_desc_sw64(base + kOffK + 4 * kBox, 512);
   const bool one = elect_one();
-  bool ok = warp_wait(x, x.bar(kQFull), 0, 20);
-  for (int c = 0; c < x.n_chunks; ++c) {
+  bool ok = true;
+  int c = 0, q = 0;  // chunks, q's so far
+  for (int i = x.first; i < x.last && ok; ++i) {
+   const int n = item_at(p, i).n;
+   if (n > 0) ok = warp_wait(x, x.bar(kQFull), q++ & 1);
+   for (const int end = c + n; c < end && ok; ++c) {
     const int b = c & 1, s = c % kKRing;
-    ok = ok && warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1, 23) &&
-         warp_wait(x, x.bar(kPeerK + s), (c / kKRing) & 1, 21);
-    ok = ok && (c < 2 || warp_wait(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1, 22));
+    ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1) &&
+         warp_wait(x, x.bar(kPeerK + s), (c / kKRing) & 1) &&
+         (c < 2 || warp_wait(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1));
     if (!ok) break;
     fence_after_sync();
-    const uint64_t kd = k_desc + static_cast<uint64_t>((s * kKSlot) >> 4);
-    const uint64_t krd = kr_desc + static_cast<uint64_t>((s * kKSlot) >> 4);
+    const uint32_t at = (s * kKSlot) >> 4;
     const uint32_t d = x.tbase + kTmemS + 64u * b;
     if (one) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint64_t off = static_cast<uint64_t>(((i >> 2) * kBox + (i & 3) * 32) >> 4);
-        pair_mma(d, q_desc + off, kd + off, kId, i != 0 ? 1u : 0u);
-      }
-      pair_mma(d, qr_desc, krd, kId, 1u);
-      pair_mma(d, qr_desc + 2, krd + 2, kId, 1u);
+      for (int i = 0; i < 4; ++i)
+        mma_box(d, lo(q_desc) + (i * kBox >> 4), hi(q_desc), lo(k_desc) + at + (i * kBox >> 4), hi(k_desc), kId,
+                i != 0 ? 1u : 0u);
+      mma_rope(d, lo(qr_desc), hi(qr_desc), lo(kr_desc) + at, hi(kr_desc), kId);
       pair_commit(x.bar(kSFull + b));
       pair_commit(x.bar(kKEmpty + s));
     }
     __syncwarp();
+   }
   }
   if (one) {
     pair_commit(x.bar(kDrainQK));
@@ -477,7 +575,7 @@ __device__ void qk_issue(const Ctx& x) {
 
 // Rank 0, warp 3: P V of a chunk by halves of the columns, so that a half of O may
 // be rescaled while the other is multiplied.
-__device__ void pv_issue(const Ctx& x) {
+__device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
   constexpr uint32_t kIdHi = instr_desc(kRows, 256, 1, 0, false, true);
   constexpr uint32_t kIdLo = instr_desc(kRows, 256, 0, 0, false, true);
   const uint32_t base = smem_u32(x.smem);
@@ -485,27 +583,31 @@ __device__ void pv_issue(const Ctx& x) {
   const uint64_t p_desc = smem_desc_sw128(base + kOffP, 16, 1024);
   const bool one = elect_one();
   bool ok = true;
-  for (int g = 0; g < 2 * x.n_chunks && ok; ++g) {
+  int g = 0, outs = 0;  // boxes, outputs with keys so far
+  for (int i = x.first; i < x.last && ok; ++i) {
+   const int n = item_at(p, i).n;
+   // O of the item before has been read
+   if (n > 0 && outs++ > 0) ok = warp_wait(x, x.bar(kOFree), outs & 1);
+   const int begin = g;
+   for (const int end = g + 2 * n; g < end && ok; ++g) {
     const int j = g & 1, c = g >> 1, b = c & 1, s = g % kVRing;
-    ok = warp_wait(x, x.bar((j == 0 ? kPFull : kOReady) + b), (c >> 1) & 1, j == 0 ? 24 : 38) &&
-         warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26) &&
-         warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1, 39);
+    ok = warp_wait(x, x.bar((j == 0 ? kPFull : kOReady) + b), (c >> 1) & 1) &&
+         warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1) &&
+         warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1);
     if (!ok) break;
     fence_after_sync();
-    const uint64_t vb = v_desc + static_cast<uint64_t>((s * kVSlot) >> 4);
-    const uint64_t pb = p_desc + static_cast<uint64_t>((b * 2 * kPTile) >> 4);
+    const uint32_t vb = lo(v_desc) + ((s * kVSlot) >> 4), pb = lo(p_desc) + ((b * 2 * kPTile) >> 4);
     const uint32_t d = x.tbase + kTmemO + 128u * j;
+    const uint32_t more = g - begin > 1 ? 1u : 0u;
     if (one) {
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 32; ++ks) {
-        const uint64_t av = pb + static_cast<uint64_t>((ks * 32) >> 4);
-        const uint64_t bv = vb + static_cast<uint64_t>((ks * 32 * 128) >> 4);
-        pair_mma(d, av, bv, kIdHi, (c | ks) != 0 ? 1u : 0u);
-        pair_mma(d, av + static_cast<uint64_t>(kPTile >> 4), bv, kIdLo, 1u);
-      }
+      for (int ks = 0; ks < kKeys / 32; ++ks)
+        mma_terms(d, pb + (ks * 32 >> 4), hi(p_desc), vb + (ks * 32 * 128 >> 4), hi(v_desc), kIdHi, kIdLo,
+                  ks != 0 ? 1u : more);
       pair_commit(x.bar(kVEmpty + s));
     }
     __syncwarp();
+   }
   }
   if (one) {
     pair_commit(x.bar(kDrainPV));
@@ -515,24 +617,32 @@ __device__ void pv_issue(const Ctx& x) {
 }
 
 // Rank 1, warps 1 and 3: what has landed here, passed on to rank 0.
-__device__ void pass_keys(const Ctx& x) {
-  bool ok = warp_wait(x, x.bar(kQFull), 0, 20);
-  for (int c = 0; c < x.n_chunks && ok; ++c) {
-    const int s = c % kKRing;
-    ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1, 23);
-    if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerK + s));
-    __syncwarp();
+__device__ void pass_keys(const Ctx& x, const DecodeParams& p) {
+  bool ok = true;
+  int c = 0, q = 0;
+  for (int i = x.first; i < x.last && ok; ++i) {
+    const int n = item_at(p, i).n;
+    if (n > 0) ok = warp_wait(x, x.bar(kQFull), q++ & 1);  // (before the item's first keys)
+    for (const int end = c + n; c < end && ok; ++c) {
+      const int s = c % kKRing;
+      ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1);
+      if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerK + s));
+      __syncwarp();
+    }
   }
   if (x.lane == 0) drain_wait(x, x.bar(kDrainQK), 0, 25);
   __syncwarp();
 }
-__device__ void pass_values(const Ctx& x) {
+__device__ void pass_values(const Ctx& x, const DecodeParams& p) {
   bool ok = true;
-  for (int g = 0; g < 2 * x.n_chunks && ok; ++g) {
-    const int s = g % kVRing;
-    ok = warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1, 26);
-    if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerV + s));
-    __syncwarp();
+  int g = 0;
+  for (int i = x.first; i < x.last && ok; ++i) {
+    for (const int end = g + 2 * item_at(p, i).n; g < end && ok; ++g) {
+      const int s = g % kVRing;
+      ok = warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1);
+      if (ok && x.lane == 0) mbar_arrive_remote(x.lead(kPeerV + s));
+      __syncwarp();
+    }
   }
   if (x.lane == 0) drain_wait(x, x.bar(kDrainPV), 0, 29);
   __syncwarp();
@@ -543,7 +653,7 @@ template <Scale SCALE>
 __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
   constexpr bool UNI = SCALE == Scale::kSixteen, ONE = SCALE == Scale::kNone;
   const int lane = x.lane;
-  const int sw = x.warp - 4;
+  const int sw = x.warp - kRoleWarps;
   const int q4 = x.warp & 3;               // TMEM lane quarter of this warp
   const int rq = q4 & 1;                   // its 32 of the CTA's 64 rows
   const int kq = q4 >> 1;                  // its half of a chunk's keys
@@ -553,13 +663,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   const int cq = sw >> 2;                  // quarter of the TMEM columns of O at the end
   const int r = rq * 32 + lane;            // row within the CTA
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-  const int H = x.H;
-  const int rho = x.row0 + kOwnRows * x.rank + r;  // row within the unit
-  const bool row_ok = rho < x.rows_total;
-  const int vis = !row_ok ? 0 : (x.see0 == INT_MAX ? INT_MAX : x.see0 + rho / H);
-  // keys from here on (of the segment) are not seen by all rows
-  const int all_see = x.see0 == INT_MAX ? INT_MAX : x.see0 + x.row0 / H - x.seg_start;
-  const int n = x.n_chunks;
+  const int H = p.num_heads;
   bool ok = true;
 
   float* xmax = reinterpret_cast<float*>(x.smem + kOffXMax) + r;
@@ -567,6 +671,21 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   const int c0 = ((2 * part) ^ (r & 7)) << 4, c1 = ((2 * part + 1) ^ (r & 7)) << 4;
   const uint32_t ts = x.tbase + lane_off + kTmemS + 64u * h + kPart * kh;
 
+  auto pv_done = [&](int c, int j) {
+    const int g = 2 * c + j;
+    return warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1);
+  };
+  int first = 0;  // chunks (of all items) before this item's: buffers and phases run on
+  for (int i = x.first; i < x.last; ++i) {
+  const Item it = item_at(p, i);
+  const int n = it.n, end = first + n;
+  const int rows_total = it.tokens * H;
+  const int rho = it.row0 + kOwnRows * x.rank + r;  // row within the unit
+  const bool row_ok = rho < rows_total;
+  const int vis = !row_ok ? 0 : (it.see0 == INT_MAX ? INT_MAX : it.see0 + rho / H);
+  // keys from here on (of chunk 0 of all items' chunks) are not seen by all rows
+  const int start = it.seg_start - first * kKeys;
+  const int all_see = it.see0 == INT_MAX ? INT_MAX : it.see0 + it.row0 / H - start;
   float ref = -INFINITY, l = 0.f;
   auto follow = [&](float mx) {
     if (!(mx > ref + kMove)) return 1.f;  // (moves also when a row's first visible key arrives)
@@ -583,14 +702,15 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   // before it posts its own of c + 1, which the other waits for before it posts
   // that of c + 4: neither the barrier's phase nor the four buffers are passed over.
   auto follow_other = [&](int c) {
-    if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 33)) return false;
+    if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1)) return false;
     follow(row_max(c));
     return true;
   };
-  for (int c = h; c < n && ok; c += 2) {
+  for (int c = first + ((first & 1) ^ h); c < end; c += 2) {
     const int ph = (c >> 1) & 1;
-    ok = warp_wait(x, x.bar(kSFull + h), ph, 31);
+    ok = warp_wait(x, x.bar(kSFull + h), ph);
     if (!ok) break;
+    if (sw == 0 || sw == 8) watch_of(x.smem)->progress = c;
     fence_after_sync();
     float s[kPart];
     {
@@ -619,7 +739,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       }
     }
     // keys that exist and that the row may see
-    const int lim = min(vis, x.seg_end) - (x.seg_start + c * kKeys + kPart * part);
+    const int lim = min(vis, it.seg_end) - (start + c * kKeys + kPart * part);
     if (lim < kPart || kmask != 0xffffffffu) {
 #pragma unroll
       for (int j = 0; j < kPart; ++j)
@@ -635,12 +755,12 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       if constexpr (ONE) m[i] *= p.score_scale_log2;
     }
     // the row's maximum over all key quarters; the previous chunk's before it
-    ok = c == 0 || follow_other(c - 1);
+    ok = c == first || follow_other(c - 1);
     if (!ok) break;
     xmax[((c & 3) * 4 + part) * kOwnRows] = fmaxf(m[0], m[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kX + 2 * (c & 3) + rq));
-    ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1, 32);
+    ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1);
     if (!ok) break;
     const float alpha = follow(row_max(c));
     // p as hi + lo terms, 16 keys to a 16-byte chunk of each tile
@@ -678,11 +798,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kScFree + h));
     // P V two chunks back has read this buffer of P
-    auto pv_done = [&](int cc, int j, int code) {
-      const int g = 2 * cc + j;
-      return warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1, code);
-    };
-    ok = c < 2 || pv_done(c - 2, 1, 37);
+    ok = c < 2 || pv_done(c - 2, 1);
     if (!ok) break;
     *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -696,7 +812,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
 #pragma unroll 1
       for (int j = 0; j < 2 && ok; ++j) {
         const int g = 2 * c + j;
-        ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1, 36);  // (its writes are seen here too)
+        ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1);  // (its writes are seen here too)
         uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + kPart * part * 128 + (lane & 7) * 16;
         for (int i = rq + 2 * (lane >> 3); ok && i < kPart; i += 8) {
           uint4* at = reinterpret_cast<uint4*>(box + i * 128);
@@ -717,7 +833,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     if (moved) {
       // some rows moved their reference: once P V of the previous chunk into O_kh
       // is complete, this warp rescales its lanes' rows there
-      ok = pv_done(c - 1, kh, 40);
+      ok = pv_done(c - 1, kh);
       if (!ok) break;
       fence_after_sync();
 #pragma unroll 1
@@ -742,23 +858,20 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     if (lane == 0) mbar_arrive_remote(x.lead((kh == 0 ? kPFull : kOReady) + h));
   }
 
+  if (!ok) break;
   // ---------------------------------------------------------------- epilogue
-  if (ok && n > 0 && ((n - 1) & 1) != h) ok = follow_other(n - 1);  // the last one was the other group's
-  float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum) + r;
-  if (ok) {
-    lsum[(4 * h + part) * kOwnRows] = l;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kXL + rq));
-    ok = warp_wait(x, x.bar(kXL + rq), 0, 34);
-  }
+  if (n > 0 && ((end - 1) & 1) != h) ok = follow_other(end - 1);  // the last one was the other group's
+  if (!ok) break;
+  float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum) + ((i - x.first) & 1) * 8 * kOwnRows + r;
+  lsum[(4 * h + part) * kOwnRows] = l;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(x.bar(kXL + rq));
+  ok = warp_wait(x, x.bar(kXL + rq), (i - x.first) & 1);
   // O is complete with the last chunk
-  if (ok && n > 0) {
-    const int g = 2 * n - 1;
-    ok = warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1, 35);
-    fence_after_sync();
-  }
-  if (!ok) return;
-  const bool fin = x.pslot < 0;
+  if (ok && n > 0) ok = pv_done(end - 1, 1);
+  if (!ok) break;
+  fence_after_sync();
+  const bool fin = it.pslot < 0;
   float mult = 0.f;
   if (row_ok) {
     float L = 0.f;
@@ -766,7 +879,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     for (int k = 0; k < 8; ++k) L += lsum[k * kOwnRows];
     const float base = ref == -INFINITY ? 0.f : ref - kPBias;  // the reference of O and the sum
     const int head = rho % H;
-    const int64_t th = static_cast<int64_t>(x.tok0 + rho / H) * H + head;
+    const int64_t th = static_cast<int64_t>(it.tok0 + rho / H) * H + head;
     const bool writes = kq == 0 && cq == 0;
     if (fin) {
       float lse = -INFINITY;
@@ -787,7 +900,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     } else {
       mult = L != 0.f ? 1.f / L : 0.f;
       if (writes) {
-        const int64_t at = static_cast<int64_t>(x.pslot) + kOwnRows * x.rank + r;
+        const int64_t at = static_cast<int64_t>(it.pslot) + kOwnRows * x.rank + r;
         const float2 ms = partial_sums(L > 0.f ? base : -INFINITY, L);
         p.segm_max[at] = ms.x;
         p.segm_expsum[at] = ms.y;
@@ -796,77 +909,91 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     mult *= p.kv_scale;
   }
   // Each warp scales its 32 rows x 64 columns and stages them, 128 bytes of
-  // each row at a time, in the 128-byte swizzle, in the rings (which hold no
-  // more boxes in use). When all 32 rows are valid one TMA tensor store writes
-  // each staged tile; otherwise every store instruction covers four 128-byte row
-  // pieces. (TMEM loads are warp-collective.)
+  // each row at a time, in the 128-byte swizzle, in its 4 KB of the value ring
+  // (whose boxes P V has read, and whose next ones wait for kStage). When all 32
+  // rows are valid one TMA tensor store writes each staged tile; otherwise every
+  // store instruction covers four 128-byte row pieces. (TMEM loads are
+  // warp-collective.)
   const int col0 = 256 * (cq >> 1) + 128 * kq + 64 * (cq & 1);
-  const int wr = x.row0 + kOwnRows * x.rank + 32 * rq;  // the warp's first row within the unit
-  if (wr >= x.rows_total) return;
-  const bool whole = wr + 32 <= x.rows_total;
-  const int z0 = fin ? x.tok0 * H + wr : x.pslot + (wr - x.row0);
-  const CUtensorMap* map = fin ? &maps.out : &maps.part;
-  const int qc = lane & 7;                  // 16-byte piece of a 128-byte row piece
-  auto store = [&](const uint32_t (&w)[32], int col, int tile) {
-    uint8_t* buf = x.smem + kOffK + sw * 8192 + tile * 4096;
+  const int wr = it.row0 + kOwnRows * x.rank + 32 * rq;  // the warp's first row within the unit
+  if (wr < rows_total) {
+    const bool whole = wr + 32 <= rows_total;
+    const int z0 = fin ? it.tok0 * H + wr : it.pslot + (wr - it.row0);
+    const CUtensorMap* map = fin ? &maps.out : &maps.part;
+    const int qc = lane & 7;                // 16-byte piece of a 128-byte row piece
+    uint8_t* buf = x.smem + kOffV + sw * 4096;
+    auto store = [&](const uint32_t (&w)[32], int col) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    if (whole) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(map, smem_u32(buf), col, 0, z0);
-        bulk_commit_group();
-      }
-    } else {
-      __syncwarp();
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(map, smem_u32(buf), col, 0, z0);
+          bulk_commit_group();
+          bulk_wait_read<0>();
+        }
+      } else {
+        __syncwarp();
 #pragma unroll 1
-      for (int it = 0; it < 8; ++it) {
-        const int row = 4 * it + (lane >> 3);
-        if (wr + row >= x.rows_total) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 128 + ((qc ^ (row & 7)) << 4));
-        const int64_t at = static_cast<int64_t>(z0 + row) * kRank + col;
-        uint8_t* dst = fin ? static_cast<uint8_t*>(p.out) + at * 2 : reinterpret_cast<uint8_t*>(p.segm_out + at);
-        *reinterpret_cast<uint4*>(dst + qc * 16) = v;
+        for (int k = 0; k < 8; ++k) {
+          const int row = 4 * k + (lane >> 3);
+          if (wr + row >= rows_total) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 128 + ((qc ^ (row & 7)) << 4));
+          const int64_t at = static_cast<int64_t>(z0 + row) * kRank + col;
+          uint8_t* dst = fin ? static_cast<uint8_t*>(p.out) + at * 2 : reinterpret_cast<uint8_t*>(p.segm_out + at);
+          *reinterpret_cast<uint4*>(dst + qc * 16) = v;
+        }
       }
-    }
-  };
-  auto load = [&](int c, uint32_t (&o)[32]) {
-    if (n > 0) {
-      tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * cq + 32 * c, o);
-      tmem_ld_wait();
+      __syncwarp();
+    };
+    auto load = [&](int c, uint32_t (&o)[32]) {
+      if (n > 0) {
+        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * cq + 32 * c, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+      }
+    };
+    if (fin) {
+      uint32_t w[32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[32];
+        load(c, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * mult, __uint_as_float(o[2 * j + 1]) * mult);
+          w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      store(w, col0);
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = 0u;
-    }
-  };
-  if (fin) {
-    uint32_t w[32];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t o[32];
-      load(c, o);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * mult, __uint_as_float(o[2 * j + 1]) * mult);
-        w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    }
-    store(w, col0, 0);
-  } else {
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      uint32_t o[32];
-      load(c, o);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[32];
+        load(c, o);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mult);
-      store(o, col0 + 32 * c, c);
+        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mult);
+        store(o, col0 + 32 * c);
+      }
     }
   }
-  if (lane == 0) bulk_wait_read<0>();  // the tiles are read before the CTA exits
+  // O has been read (of items with keys, whose next one replaces it), and the
+  // staged tiles too
+  fence_before_sync();
   __syncwarp();
+  if (lane == 0) {
+    if (n > 0) mbar_arrive_remote(x.lead(kOFree));
+    mbar_arrive(x.bar(kStage));
+  }
+  first = end;
+  }
+  __syncwarp();
+  if (lane == 0) atomicAdd(&watch_of(x.smem)->finished, 1);
 }
 
 template <int BOX, Scale SCALE>
@@ -879,37 +1006,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // once every CTA has started
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const int item = blockIdx.x >> 1;
-  if (item >= *p.n_items) return;
-  const int4 a = reinterpret_cast<const int4*>(p.items)[2 * item];
-  const int4 b = reinterpret_cast<const int4*>(p.items)[2 * item + 1];
+  const int worker = blockIdx.x >> 1;
   Ctx x;
+  x.first = uniform(p.worker_first[worker]);
+  x.last = uniform(p.worker_first[worker + 1]);
+  if (x.first >= x.last) return;  // both CTAs of the pair
   x.smem = smem;
-  x.status = status;
-  x.limit_ns = p.wait_ns != 0 ? p.wait_ns : kDefaultWaitNs;
   x.tid = threadIdx.x;
-  x.warp = __shfl_sync(0xffffffffu, x.tid >> 5, 0);  // uniform, for the compiler too
+  x.warp = uniform(x.tid >> 5);
   x.lane = x.tid & 31;
-  x.rank = static_cast<int>(cluster_ctarank());
-  x.H = p.num_heads;
-  x.unit = a.x;
-  x.row0 = a.y * kRows;
-  x.seg_start = a.z;
-  x.seg_end = a.w;
-  x.pslot = b.x;
-  x.tok0 = b.y;
-  x.rows_total = (b.z & kItemTokens) * x.H;
-  x.see0 = (b.z & kItemPrefix) != 0 ? INT_MAX : b.w;
-  x.n_chunks = x.seg_end > x.seg_start ? cdiv(x.seg_end - x.seg_start, kKeys) : 0;
+  x.rank = uniform(static_cast<int>(cluster_ctarank()));
 
   x.bar0 = smem_u32(smem + kOffBar);
   x.lead0 = map_to_rank(x.bar0, 0);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + kOffTslot);
-  x.abort = reinterpret_cast<volatile int*>(smem + kOffAbort);
   if (x.tid == 0) {
-    *x.abort = 0;
+    Watch* w = watch_of(smem);
+    w->status = status;
+    w->ns = p.wait_ns != 0 ? p.wait_ns : kDefaultWaitNs;
+    w->abort = 0;
+    w->progress = 0;
+    w->finished = 0;
     reinterpret_cast<int*>(smem + kOffIssued)[0] = -1;
     reinterpret_cast<int*>(smem + kOffIssued)[1] = -1;
+    reinterpret_cast<int*>(smem + kOffIssued)[2] = -1;
+    reinterpret_cast<int*>(smem + kOffIssued)[3] = -1;
     for (int i = 0; i < kKRing; ++i) {
       mbar_init(x.bar(kKFull + i), 1);
       mbar_init(x.bar(kKEmpty + i), 1);
@@ -930,6 +1051,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(x.bar(kXL + i), 8);
     }
     for (int i = 0; i < 8; ++i) mbar_init(x.bar(kX + i), 4);
+    mbar_init(x.bar(kOFree), 2 * kSoftWarps);
+    mbar_init(x.bar(kStage), kSoftWarps);
     mbar_init(x.bar(kDrainQK), 1);
     mbar_init(x.bar(kDrainPV), 1);
     fence_barrier_init();
@@ -941,55 +1064,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   fence_after_sync();
   x.tbase = *tslot;
 
-  if (x.n_chunks > 0) {
-    if (x.tid == 0) {  // this CTA's rows of q (rows past the last are zeros)
-      tma_prefetch_desc(&maps.q);
-      mbar_arrive_expect_tx(x.bar(kQFull), kKSlot);
-      const int qrow = x.tok0 * x.H + x.row0 + kOwnRows * x.rank;
-      for (int j = 0; j < 4; ++j)
-        tma_load_2d(smem_u32(smem + kOffQ + j * kBox), &maps.q, 128 * j, qrow, x.bar(kQFull));
-      tma_load_2d(smem_u32(smem + kOffQ + 4 * kBox), &maps.qr, kRank, qrow, x.bar(kQFull));
-    }
-    __syncwarp();
-  }
-  if (x.warp >= 4) {
+  if (x.warp >= kRoleWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     softmax_rows<SCALE>(x, maps, p);
-  } else if (x.n_chunks > 0) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRoleRegs));
     if (x.warp == 0) {
-      load_boxes<BOX>(x, maps, p);
+      load_keys<BOX>(x, maps, p);
     } else if (x.warp == 2) {
       prepare_keys<BOX, SCALE>(x, p);
+    } else if (x.warp == 4 || x.warp == 5) {
+      load_values<BOX>(x, maps, p, x.warp - 4);
     } else if (x.warp == 1) {
-      if (x.rank == 0) qk_issue(x);
-      else pass_keys(x);
-    } else {
-      if (x.rank == 0) pv_issue(x);
-      else pass_values(x);
+      if (x.rank == 0) qk_issue(x, p);
+      else pass_keys(x, p);
+    } else if (x.warp == 3) {
+      if (x.rank == 0) pv_issue(x, p);
+      else pass_values(x, p);
+    } else if (x.warp == 6) {
+      watch(x);
     }
   }
 
   // ------------------------------------------------------------ teardown
   __syncwarp();
+  __syncthreads();
   // every load must have landed before the CTA exits (all were consumed unless a
-  // wait gave up): the last one issued to each slot
-  if (x.tid == 0 && x.n_chunks > 0) {
+  // wait gave up): the last one issued to each slot (known once all warps are
+  // here: a phase that another follows cannot be waited for by its parity)
+  if (x.tid == 0) {
     const volatile int* issued = reinterpret_cast<const volatile int*>(smem + kOffIssued);
     for (int i = 0; i < kKRing && issued[0] - i >= 0; ++i)
       drain_wait(x, x.bar(kKFull + (issued[0] - i) % kKRing), ((issued[0] - i) / kKRing) & 1, 13);
-    for (int i = 0; i < kVRing && issued[1] - i >= 0; ++i)
-      drain_wait(x, x.bar(kVFull + (issued[1] - i) % kVRing), ((issued[1] - i) / kVRing) & 1, 14);
-    drain_wait(x, x.bar(kQFull), 0, 15);
+    for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < kVRing / 2 && issued[1 + j] - i >= 0; ++i) {
+        const int v = 2 * (issued[1 + j] - i) + j;
+        drain_wait(x, x.bar(kVFull + v % kVRing), (v / kVRing) & 1, 14);
+      }
+    if (issued[3] >= 0) drain_wait(x, x.bar(kQFull), issued[3] & 1, 15);
   }
   __syncwarp();
   fence_before_sync();
-  __syncthreads();
   cluster_sync();  // the pair's instructions and arrivals are done in both CTAs
   fence_after_sync();
   if (x.warp == 1) pair_dealloc(x.tbase, kTmemCols);
 }
 
 template <int BOX, Scale SCALE>
-cudaError_t launch_variant(const PairMaps& maps, const DecodeParams& p, unsigned items, int* status,
+cudaError_t launch_variant(const PairMaps& maps, const DecodeParams& p, unsigned pairs, int* status,
                            cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -1002,7 +1124,7 @@ cudaError_t launch_variant(const PairMaps& maps, const DecodeParams& p, unsigned
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2u * items);
+  cfg.gridDim = dim3(2u * pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -1015,17 +1137,17 @@ cudaError_t launch_variant(const PairMaps& maps, const DecodeParams& p, unsigned
 }
 
 template <int BOX>
-cudaError_t launch_box(const PairMaps& maps, const DecodeParams& p, unsigned items, int* status, cudaStream_t stream) {
-  if (p.kv_scales == nullptr) return launch_variant<BOX, Scale::kNone>(maps, p, items, status, stream);
-  if (p.scale_group % kUni == 0) return launch_variant<BOX, Scale::kSixteen>(maps, p, items, status, stream);
-  return launch_variant<BOX, Scale::kKey>(maps, p, items, status, stream);
+cudaError_t launch_box(const PairMaps& maps, const DecodeParams& p, unsigned pairs, int* status, cudaStream_t stream) {
+  if (p.kv_scales == nullptr) return launch_variant<BOX, Scale::kNone>(maps, p, pairs, status, stream);
+  if (p.scale_group % kUni == 0) return launch_variant<BOX, Scale::kSixteen>(maps, p, pairs, status, stream);
+  return launch_variant<BOX, Scale::kKey>(maps, p, pairs, status, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, unsigned items, int* status,
+cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, unsigned pairs, int* status,
                                cudaStream_t stream) {
-  if (p.block_size % 16 != 0 || p.items == nullptr) return cudaErrorInvalidValue;
+  if (p.block_size % 16 != 0 || p.items == nullptr || p.worker_first == nullptr) return cudaErrorInvalidValue;
   // the highest box that never crosses a block's end
   const int box = p.block_size % 64 == 0 ? 64 : p.block_size % 32 == 0 ? 32 : 16;
   PairMaps maps{};
@@ -1037,9 +1159,9 @@ cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv
   if (e == cudaSuccess)
     e = make_out_map(&maps.part, p.segm_out, static_cast<uint64_t>(p.segm_rows), 1, false, 32, 32, true);
   if (e != cudaSuccess) return e;
-  return box == 64 ? launch_box<64>(maps, p, items, status, stream)
-         : box == 32 ? launch_box<32>(maps, p, items, status, stream)
-                     : launch_box<16>(maps, p, items, status, stream);
+  return box == 64 ? launch_box<64>(maps, p, pairs, status, stream)
+         : box == 32 ? launch_box<32>(maps, p, pairs, status, stream)
+                     : launch_box<16>(maps, p, pairs, status, stream);
 }
 
 }  // namespace mla

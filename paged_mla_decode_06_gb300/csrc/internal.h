@@ -291,9 +291,9 @@ cudaError_t launch_decode_vs(const DecodeParams& p, int64_t q_rows, int64_t kv_r
                              cudaStream_t stream);
 
 // tcgen05 kernel of a batch that shares prefixes (e4m3): tiles of 128 query rows on
-// two CTAs that share each instruction; block size a multiple of 16. `items`: item
-// slots of the list.
-cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, unsigned items, int* status,
+// two CTAs that share each instruction, and run the items of a worker (pair) of the
+// list; block size a multiple of 16.
+cudaError_t launch_decode_pair(const DecodeParams& p, int64_t q_rows, int64_t kv_rows, unsigned pairs, int* status,
                                cudaStream_t stream);
 
 // Work list and merge of a batch that shares prefixes (prefix_sched.cu).
@@ -306,10 +306,11 @@ struct PrefixParams {
   int32_t workers, tiles_max, ptiles_max, max_items;
   int32_t* items;                // [max_items, 8]
   int32_t* n_items;
+  int32_t* worker_first;         // [workers + 1]: first item of each worker (at most 511 of them); null: longest first
   int32_t* unit_tab;             // [R * tiles_max, 2]: first partial row (-1), pieces
   int32_t* req_group;            // [R]: group whose prefix the request takes part in, or -1
   int32_t* groups;               // [G, 4]: first request, shared keys, first token, first prefix tile
-  int64_t* group_pos;            // [G]
+  int32_t* group_pos;            // [G]: its tiles' place in the sequence
   int32_t* prefix_tab;           // [ptiles_max, 2]: first partial row, pieces
   const float* segm_out;         // [rows, 512]
   const float* segm_max;

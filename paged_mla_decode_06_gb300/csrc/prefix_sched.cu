@@ -4,12 +4,14 @@
 // all its requests' tables) and its own behind them. The rows of all tokens of a
 // group make the tiles of its prefix, the rows of a request those of its own
 // keys; an item is a tile of 128 rows and a range of 128-key groups. The tiles
-// are laid end to end, those of the prefixes first, and the sequence of their
-// groups is cut at every multiple of W = cdiv(all groups, workers); a cut within
-// W / 8 of a tile's ends is dropped, and tiles of at most W / 2 groups are not
-// cut: items are handed out longest first, and the short ones fill what the
-// others leave. A row's pieces, of either kind, write base-2 partials; rows of
-// one piece in all write their output.
+// are laid end to end, those of the prefixes first, each as long as its groups
+// and, where workers run items one after another, kItemCost more for what an item
+// costs besides; the sequence is cut at every multiple of W = cdiv(its length,
+// workers), at least kMinShare. A cut within W / 8 of a tile's ends is dropped, and so are
+// cuts of tiles that are short against W. A worker's items are those with their middle
+// in its share. (Kernels of one item a pair get the longest first instead, and
+// the short ones fill what the others leave.) A row's pieces, of either kind, write
+// base-2 partials; rows of one piece in all write their output.
 //
 // A request takes part in its group's prefix when all its tokens see all of it
 // (seq_len - qlen >= prefix); the others take all their keys as their own. So a call
@@ -36,38 +38,42 @@ constexpr int kBins = 512;
 constexpr int kCache = 256;      // groups and
 constexpr int kCacheReqs = 1024; // requests that are kept in shared memory
 constexpr int kPieceCost = 6;
+constexpr int kItemCost = 2;      // of a worker's item: its start and its output, in groups
+constexpr int kMinShare = 4;     // groups: pieces of less cost more than they save
 
 struct Shared {
-  long long red[kThreads / 32];
-  int hist[kBins];
+  int red[kThreads / 32];
+  int hist[kBins];   // items by size, or by worker
   int start[kBins];
   int4 groups[kCache];
-  long long pos[kCache];
+  int pos[kCache];
   int edge[kCache + 1];
   int4 reqs[kCacheReqs];
 };
 
-template <typename T>
-__device__ T block_scan(T v, long long* red, T* total) {  // exclusive
+// Exclusive prefix of v over the block. (Out of line, as the loops are not unrolled: the
+// kernel runs once a call, and mostly waits for its own code.)
+__device__ __noinline__ int block_scan(int v, int* red, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T inc = v;
+  int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T n = __shfl_up_sync(0xffffffffu, inc, o);
+    const int n = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += n;
   }
   __syncthreads();
   if (lane == 31) red[warp] = inc;
   __syncthreads();
-  T before = 0, all = 0;
+  // (every warp scans the warps' sums)
+  const int mine = lane < kThreads / 32 ? red[lane] : 0;
+  int all = mine;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const T s = static_cast<T>(red[w]);
-    if (w < warp) before += s;
-    all += s;
+  for (int o = 1; o < kThreads / 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += n;
   }
-  *total = all;
-  return before + inc - v;
+  *total = __shfl_sync(0xffffffffu, all, kThreads / 32 - 1);
+  return __shfl_sync(0xffffffffu, all - mine, warp) + inc - v;
 }
 
 // Last i in [0, n) with at(i) <= v (at does not decrease; 0 if none).
@@ -89,30 +95,31 @@ __device__ __forceinline__ int token_edge(const PrefixParams& p, int r) {  // fi
 }
 __device__ __forceinline__ int groups_of(int keys) { return keys > 0 ? keys / kGroupKeys + (keys % kGroupKeys != 0) : 0; }
 
-// f(b) for each cut of the tile at [a, a + g) of the sequence, as group offsets;
-// returns their number.
-template <typename F>
-__device__ __forceinline__ int tile_cuts(long long a, int g, int W, F f) {
-  if (2 * g <= W) return 0;
-  const int d = W / 8;
-  const long long lo = a + d + 1, hi = a + g - d - 1;
-  if (hi < lo) return 0;
-  int n = 0;
-  for (long long c = (lo + W - 1) / W * W; c <= hi; c += W, ++n) f(static_cast<int>(c - a));
-  return n;
-}
-__device__ __forceinline__ int bin_of(int size) { return min(size, kBins - 1); }
-
+// Where a tile may be cut.
+struct Cutter {
+  int W, cost, least, d;  // shares; length of an item besides its groups; groups of a tile that may be cut; of its ends that may not
+  // f(b) for each cut of the tile of g groups at place a, as group offsets; returns their number
+  template <typename F>
+  __device__ __forceinline__ int cuts(int a, int g, F f) const {
+    if (g < least) return 0;
+    const int z = a + cost, hi = g - d;
+    int n = 0;
+    for (int b = (z + d + W - 1) / W * W - z; b <= hi; b += W, ++n) f(b);
+    return n;
+  }
+};
 __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixParams p) {
   __shared__ Shared s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x;
   const int G = p.num_groups, R = p.num_reqs, H = p.num_heads;
   const bool few = G <= kCache;
+  const bool sorted = p.worker_first == nullptr;
+  const int cost = sorted ? 0 : kItemCost;
   int4* const out_groups = reinterpret_cast<int4*>(p.groups);
   // {first request, shared keys, tiles of the participants, requests that take part}, then as in PrefixParams
   int4* const gr = few ? s.groups : out_groups;
-  long long* const gp = few ? s.pos : reinterpret_cast<long long*>(p.group_pos);
+  int* const gp = few ? s.pos : p.group_pos;
   auto edge = [&](int g) { return few ? s.edge[g] : group_edge(p, g); };
   auto tiles_of = [&](int64_t tokens) { return static_cast<int>((tokens * H + kTileRows - 1) / kTileRows); };
   // {first token, tokens, length, group of the prefix that the request takes part in or -1}
@@ -125,18 +132,23 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     p.req_group[r] = g;
     if (r < kCacheReqs) s.reqs[r].w = g;
   };
+#pragma unroll 1
   for (int r = tid; r < min(R, kCacheReqs); r += kThreads) {
     const int t0 = token_edge(p, r);
     s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
   }
+#pragma unroll 1
   for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;
+#pragma unroll 1
   for (int g = tid; g < G; g += kThreads) {
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
     gr[g] = make_int4(INT32_MAX, whole * p.block_size, 0, 0);
   }
   if (few)
+#pragma unroll 1
     for (int g = tid; g <= G; g += kThreads) s.edge[g] = group_edge(p, g);
   __syncthreads();
+#pragma unroll 1
   for (int r = tid; r < R; r += kThreads) {
     const int4 q = request(r);
     int g = last_at(G, r, edge);
@@ -153,7 +165,8 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   __syncthreads();
   // prefix tiles and their places in the sequence
   int tile_carry = 0;
-  long long pos_carry = 0;
+  int pos_carry = 0;
+#pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += kThreads) {
     const int g = g0 + tid;
     int tiles = 0, keys = 0, tok0 = 0;
@@ -161,14 +174,14 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       tok0 = token_edge(p, edge(g));
       tiles = tiles_of(max(token_edge(p, edge(g + 1)) - tok0, 0));
       const int4 v = gr[g];
-      const bool share = static_cast<long long>(v.z - tiles) * groups_of(v.y) >= static_cast<long long>(kPieceCost) * v.z;
+      const bool share = static_cast<int64_t>(v.z - tiles) * groups_of(v.y) >= static_cast<int64_t>(kPieceCost) * v.z;
       if (share && v.z > 0) keys = v.y;
       else tiles = 0;
     }
     int tsum;
-    long long psum;
-    const int t = tile_carry + block_scan<int>(tiles, s.red, &tsum);
-    const long long a = pos_carry + block_scan<long long>(static_cast<long long>(tiles) * groups_of(keys), s.red, &psum);
+    int psum;
+    const int t = tile_carry + block_scan(tiles, s.red, &tsum);
+    const int a = pos_carry + block_scan(tiles * (groups_of(keys) + cost), s.red, &psum);
     tile_carry += tsum;
     pos_carry += psum;
     if (g < G) {
@@ -193,54 +206,70 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     o.tiles = min(tiles_of(o.q.y), p.tiles_max);
     return o;
   };
-  long long mine = 0;
+  int mine = 0;
+#pragma unroll 1
   for (int r = tid; r < R; r += kThreads) {
     const int g = request(r).w;
     if (g >= 0 && gr[g].y == 0) set_group(r, -1);
     const Own o = own_keys(r);
-    mine += static_cast<long long>(o.tiles) * o.groups;
+    mine += o.tiles * (o.groups + cost);
   }
-  long long total;
-  block_scan<long long>(mine, s.red, &total);
+  int total;
+  block_scan(mine, s.red, &total);
   total += pos_carry;
-  const int W = static_cast<int>(max((total + p.workers - 1) / p.workers, 1ll));
-  // sizes
+  Cutter cut;
+  cut.W = max((total + p.workers - 1) / p.workers, kMinShare);
+  cut.cost = cost;
+  cut.least = sorted ? cut.W / 2 + 1 : 3 * kItemCost;
+  cut.d = sorted ? max(cut.W / 8, 1) : kItemCost;
   auto tile_group = [&](int t) { return last_at(G, t, [&](int i) { return gr[i].w; }); };
-  auto count = [&](long long a, int n) {
+  // the place in the list that items are counted by: their size, or the worker whose
+  // share their middle falls in
+  auto bin = [&](int a, int from, int to) {
+    if (sorted) return kBins - 1 - min(to - from, kBins - 1);
+    const int begin = a + (from > 0 ? cost + from : 0);
+    return min((begin + (a + cost + to - begin) / 2) / cut.W, p.workers - 1);
+  };
+  auto count = [&](int a, int n) {
     int prev = 0;
-    tile_cuts(a, n, W, [&](int b) {
-      atomicAdd(&s.hist[bin_of(b - prev)], 1);
+    cut.cuts(a, n, [&](int b) {
+      atomicAdd(&s.hist[bin(a, prev, b)], 1);
       prev = b;
     });
-    atomicAdd(&s.hist[bin_of(n - prev)], 1);
+    atomicAdd(&s.hist[bin(a, prev, n)], 1);
   };
+#pragma unroll 1
   for (int t = tid; t < ptiles; t += kThreads) {
     const int g = tile_group(t), n = groups_of(gr[g].y);
-    count(gp[g] + static_cast<long long>(t - gr[g].w) * n, n);
+    count(gp[g] + (t - gr[g].w) * (n + cost), n);
   }
-  long long carry = pos_carry;
+  int carry = pos_carry;
+#pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += kThreads) {
     Own o{};
     if (r0 + tid < R) o = own_keys(r0 + tid);
-    long long sum;
-    const long long a = carry + block_scan<long long>(static_cast<long long>(o.tiles) * o.groups, s.red, &sum);
+    int sum;
+    const int a = carry + block_scan(o.tiles * (o.groups + cost), s.red, &sum);
     carry += sum;
-    for (int t = 0; t < o.tiles; ++t) count(a + static_cast<long long>(t) * o.groups, o.groups);
+#pragma unroll 1
+    for (int t = 0; t < o.tiles; ++t) count(a + t * (o.groups + cost), o.groups);
   }
   __syncthreads();
-  {  // start[b] = items of the bins above b
+  {  // start[b] = items of the bins before b
     static_assert(kBins == kThreads, "a bin a thread");
-    const int b = kBins - 1 - tid;
     int all;
-    s.start[b] = block_scan<int>(s.hist[b], s.red, &all);
+    const int at = block_scan(s.hist[tid], s.red, &all);
+    s.start[tid] = at;
     if (tid == 0) *p.n_items = min(all, p.max_items);
+    if (!sorted && tid <= p.workers) p.worker_first[tid] = min(at, p.max_items);
   }
   __syncthreads();
   // A tile's items: f(j) = first row of the partial of its piece j (-1: its output).
-  auto emit = [&](long long a, int n, int unit, int tile, int first, int end, int4 second, auto f) {
+  // (Items of a bin are in any order: no result depends on it.)
+  auto emit = [&](int a, int n, int unit, int tile, int first, int end, int4 second, auto f) {
     int prev = 0, j = 0;
     auto piece = [&](int b) {
-      const int at = atomicAdd(&s.start[bin_of(b - prev)], 1);
+      const int at = atomicAdd(&s.start[bin(a, prev, b)], 1);
       if (at < p.max_items) {
         int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
         it[0] = make_int4(unit, tile, first + prev * kGroupKeys, b == n ? end : first + b * kGroupKeys);
@@ -250,24 +279,25 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       prev = b;
       ++j;
     };
-    tile_cuts(a, n, W, piece);
+    cut.cuts(a, n, piece);
     piece(n);
   };
   int row_carry = 0;  // rows of the partials
+#pragma unroll 1
   for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
     const int t = t0 + tid;
     int4 v{};
     int n = 0, k = 0, g = 0;
-    long long a = 0;
+    int a = 0;
     if (t < ptiles) {
       g = tile_group(t);
       v = gr[g];
       n = groups_of(v.y);
-      a = gp[g] + static_cast<long long>(t - v.w) * n;
-      k = 1 + tile_cuts(a, n, W, [](int) {});
+      a = gp[g] + (t - v.w) * (n + cost);
+      k = 1 + cut.cuts(a, n, [](int) {});
     }
     int rows;
-    const int base = row_carry + block_scan<int>(k * kTileRows, s.red, &rows);
+    const int base = row_carry + block_scan(k * kTileRows, s.red, &rows);
     row_carry += rows;
     if (t < ptiles) {
       reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, k);
@@ -277,25 +307,28 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     }
   }
   carry = pos_carry;
+#pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += kThreads) {
     const int r = r0 + tid;
     Own o{};
     if (r < R) o = own_keys(r);
-    long long sum;
-    const long long a = carry + block_scan<long long>(static_cast<long long>(o.tiles) * o.groups, s.red, &sum);
+    int sum;
+    const int a = carry + block_scan(o.tiles * (o.groups + cost), s.red, &sum);
     carry += sum;
     const bool part = r < R && o.q.w >= 0;
     int rows = 0;
+#pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
-      const int k = 1 + tile_cuts(a + static_cast<long long>(t) * o.groups, o.groups, W, [](int) {});
+      const int k = 1 + cut.cuts(a + t * (o.groups + cost), o.groups, [](int) {});
       if (part || k > 1) rows += k * min(kTileRows, o.q.y * H - t * kTileRows);
     }
     int rsum;
-    int base = row_carry + block_scan<int>(rows, s.red, &rsum);
+    int base = row_carry + block_scan(rows, s.red, &rsum);
     row_carry += rsum;
+#pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
-      const long long at = a + static_cast<long long>(t) * o.groups;
-      const int k = 1 + tile_cuts(at, o.groups, W, [](int) {});
+      const int at = a + t * (o.groups + cost);
+      const int k = 1 + cut.cuts(at, o.groups, [](int) {});
       const int tr = min(kTileRows, o.q.y * H - t * kTileRows);
       const bool split = part || k > 1;
       reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(split ? base : -1, k);
@@ -307,17 +340,19 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
 }
 
 // One warp a row: its pieces over the prefix, then those over its own keys, in
-// their order, weighted as mla_merge_segments does.
+// their order, weighted as mla_merge_segments does. The tables are read while the
+// decode may still run; the first two pieces' outputs are loaded with their weights, not
+// after them, and two at a time, so that 32 warps fit an SM (four at a time, behind the
+// weights: 14 us against XX for 8192 rows of two pieces).
 constexpr int kMergeWarps = 4;
 
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const PrefixParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
   const int H = p.num_heads;
   const int t = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(t) * H);
-  // (the tables come from the schedule, which completed before the decode began: they
-  // are read while the decode may still run)
+  // (the tables come from the schedule, which completed before the decode began)
   int r = t, tok0 = t;
   if (p.qo_indptr != nullptr) {
     if (t < p.qo_indptr[0] || t >= p.qo_indptr[p.num_reqs]) return;  // padding of the batch
@@ -345,16 +380,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   };
   const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  float4 x[2][4];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (s0 + u >= live) continue;
+      const float4* src = reinterpret_cast<const float4*>(p.segm_out + at(s0 + u) * kRank);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) x[u][v] = __ldcg(src + v * 32 + lane);
+    }
+  };
   float M = sink2;
   float m0 = -INFINITY, l0 = 0.f;  // of piece `lane`
-  for (int s = lane; s < live; s += 32) {
-    const int64_t i = at(s);
-    const float l = p.segm_expsum[i], m = p.segm_max[i];
-    if (s == lane) {
-      l0 = l;
-      m0 = m;
-    }
-    if (l > 0.f) M = fmaxf(M, m);
+  if (lane < live) {
+    l0 = __ldcg(p.segm_expsum + at(lane));
+    m0 = __ldcg(p.segm_max + at(lane));
+  }
+  load(0);
+  if (l0 > 0.f) M = fmaxf(M, m0);
+  for (int s = lane + 32; s < live; s += 32) {
+    const float m = __ldcg(p.segm_max + at(s));
+    if (__ldcg(p.segm_expsum + at(s)) > 0.f) M = fmaxf(M, m);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -371,32 +417,24 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   for (int s0 = 0; s0 < live; s0 += 32) {
     if (s0 > 0) {
       const int s = s0 + lane;
-      l0 = s < live ? p.segm_expsum[at(s)] : 0.f;
-      m0 = s < live ? p.segm_max[at(s)] : -INFINITY;
+      l0 = s < live ? __ldcg(p.segm_expsum + at(s)) : 0.f;
+      m0 = s < live ? __ldcg(p.segm_max + at(s)) : -INFINITY;
     }
     const float mine = l0 > 0.f ? l0 * exp2f(m0 - M) : 0.f;
-    for (int k = 0; k < 32 && s0 + k < live; k += 4) {
-      float4 x[4][4];
-      float w[4];
+#pragma unroll 1
+    for (int k = 0; k < 32 && s0 + k < live; k += 2) {
+      if (s0 + k > 0) load(s0 + k);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        w[u] = __shfl_sync(0xffffffffu, mine, (k + u) & 31);
-        if (s0 + k + u >= live) w[u] = 0.f;
-        // (a piece without mass may hold anything)
-        const float4* src = reinterpret_cast<const float4*>(p.segm_out + at(min(s0 + k + u, live - 1)) * kRank);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[u][v] = w[u] != 0.f ? __ldcg(src + v * 32 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        sum += w[u];
+      for (int u = 0; u < 2; ++u) {
+        const float w = __shfl_sync(0xffffffffu, mine, k + u);
+        if (s0 + k + u >= live || w == 0.f) continue;  // (a piece without mass may hold anything)
+        sum += w;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          if (w[u] == 0.f) continue;
-          acc[v][0] += w[u] * x[u][v].x;
-          acc[v][1] += w[u] * x[u][v].y;
-          acc[v][2] += w[u] * x[u][v].z;
-          acc[v][3] += w[u] * x[u][v].w;
+          acc[v][0] += w * x[u][v].x;
+          acc[v][1] += w * x[u][v].y;
+          acc[v][2] += w * x[u][v].z;
+          acc[v][3] += w * x[u][v].w;
         }
       }
     }

@@ -682,7 +682,8 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   const int rows_total = it.tokens * H;
   const int rho = it.row0 + kOwnRows * x.rank + r;  // row within the unit
   const bool row_ok = rho < rows_total;
-  const int vis = !row_ok ? 0 : (it.see0 == INT_MAX ? INT_MAX : it.see0 + rho / H);
+  const int token = rho / H;
+  const int vis = !row_ok ? 0 : (it.see0 == INT_MAX ? INT_MAX : it.see0 + token);
   // keys from here on (of chunk 0 of all items' chunks) are not seen by all rows
   const int start = it.seg_start - first * kKeys;
   const int all_see = it.see0 == INT_MAX ? INT_MAX : it.see0 + it.row0 / H - start;
@@ -878,8 +879,8 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
 #pragma unroll
     for (int k = 0; k < 8; ++k) L += lsum[k * kOwnRows];
     const float base = ref == -INFINITY ? 0.f : ref - kPBias;  // the reference of O and the sum
-    const int head = rho % H;
-    const int64_t th = static_cast<int64_t>(it.tok0 + rho / H) * H + head;
+    const int head = rho - token * H;
+    const int64_t th = static_cast<int64_t>(it.tok0) * H + rho;
     const bool writes = kq == 0 && cq == 0;
     if (fin) {
       float lse = -INFINITY;
@@ -910,24 +911,23 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   }
   // Each warp scales its 32 rows x 64 columns and stages them, 128 bytes of
   // each row at a time, in the 128-byte swizzle, in its 4 KB of the value ring
-  // (whose boxes P V has read, and whose next ones wait for kStage). When all 32
-  // rows are valid one TMA tensor store writes each staged tile; otherwise every
-  // store instruction covers four 128-byte row pieces. (TMEM loads are
-  // warp-collective.)
+  // (whose boxes P V has read, and whose next ones wait for kStage), and one TMA
+  // tensor store writes each staged tile; where some of the 32 rows do not exist
+  // each lane stores its row (of 16 rows, staged, 1700 cycles a tile). (TMEM loads
+  // are warp-collective.)
   const int col0 = 256 * (cq >> 1) + 128 * kq + 64 * (cq & 1);
   const int wr = it.row0 + kOwnRows * x.rank + 32 * rq;  // the warp's first row within the unit
   if (wr < rows_total) {
     const bool whole = wr + 32 <= rows_total;
     const int z0 = fin ? it.tok0 * H + wr : it.pslot + (wr - it.row0);
     const CUtensorMap* map = fin ? &maps.out : &maps.part;
-    const int qc = lane & 7;                // 16-byte piece of a 128-byte row piece
     uint8_t* buf = x.smem + kOffV + sw * 4096;
     auto store = [&](const uint32_t (&w)[32], int col) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
       if (whole) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -935,19 +935,14 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
           bulk_commit_group();
           bulk_wait_read<0>();
         }
-      } else {
         __syncwarp();
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          const int row = 4 * k + (lane >> 3);
-          if (wr + row >= rows_total) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(buf + row * 128 + ((qc ^ (row & 7)) << 4));
-          const int64_t at = static_cast<int64_t>(z0 + row) * kRank + col;
-          uint8_t* dst = fin ? static_cast<uint8_t*>(p.out) + at * 2 : reinterpret_cast<uint8_t*>(p.segm_out + at);
-          *reinterpret_cast<uint4*>(dst + qc * 16) = v;
-        }
+      } else if (row_ok) {
+        const int64_t at = static_cast<int64_t>(z0 + lane) * kRank + col;
+        uint4* dst = reinterpret_cast<uint4*>(fin ? static_cast<uint8_t*>(p.out) + at * 2
+                                                  : reinterpret_cast<uint8_t*>(p.segm_out + at));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
       }
-      __syncwarp();
     };
     auto load = [&](int c, uint32_t (&o)[32]) {
       if (n > 0) {
@@ -1002,15 +997,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  // the list, once the grid that wrote it has completed; the merge may launch
-  // once every CTA has started
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const int worker = blockIdx.x >> 1;
   Ctx x;
-  x.first = uniform(p.worker_first[worker]);
-  x.last = uniform(p.worker_first[worker + 1]);
-  if (x.first >= x.last) return;  // both CTAs of the pair
   x.smem = smem;
   x.tid = threadIdx.x;
   x.warp = uniform(x.tid >> 5);
@@ -1058,11 +1045,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (x.warp == 1) pair_alloc(smem_u32(tslot), kTmemCols);
+  if (x.tid == 32 * kRoleWarps) {
+    tma_prefetch_desc(&maps.kv);
+    tma_prefetch_desc(&maps.kvr);
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.qr);
+  }
   fence_before_sync();
   __syncthreads();
   cluster_sync();  // the barriers of both CTAs are there
   fence_after_sync();
   x.tbase = *tslot;
+  // the list, once the grid that wrote it has completed (what is above this runs
+  // beside it); the merge may launch once every CTA is here
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // (a pair without items runs through, so that all its waits and commits have their match)
+  x.first = uniform(p.worker_first[blockIdx.x >> 1]);
+  x.last = uniform(p.worker_first[(blockIdx.x >> 1) + 1]);
 
   if (x.warp >= kRoleWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));

@@ -38,7 +38,7 @@ constexpr int kBins = 512;
 constexpr int kCache = 256;      // groups and
 constexpr int kCacheReqs = 1024; // requests that are kept in shared memory
 constexpr int kPieceCost = 6;
-constexpr int kItemCost = 2;      // of a worker's item: its start and its output, in groups
+constexpr int kItemCost = 4;      // of a worker's item: its start and its output, in groups
 constexpr int kMinShare = 4;     // groups: pieces of less cost more than they save
 
 struct Shared {
@@ -339,16 +339,21 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   }
 }
 
-// One warp a row: its pieces over the prefix, then those over its own keys, in
-// their order, weighted as mla_merge_segments does. The tables are read while the
-// decode may still run; the first two pieces' outputs are loaded with their weights, not
-// after them, and two at a time, so that 32 warps fit an SM (four at a time, behind the
-// weights: 14 us against XX for 8192 rows of two pieces).
+// One warp a row, or (SLICED, few rows) four, each of 128 of its columns: the
+// row's pieces over the prefix, then those over its own keys, in their order,
+// weighted as mla_merge_segments does. The tables are read while the decode may still
+// run; the first pieces' outputs are loaded with their weights, not after them, and two
+// at a time (eight of a slice), so that 32 warps fit an SM (four at a time and behind the
+// weights: 14 us against 8 for 8192 rows of two pieces).
 constexpr int kMergeWarps = 4;
 
+template <bool SLICED>
 __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const PrefixParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  constexpr int kVec = SLICED ? 1 : 4;    // float4 of a lane
+  constexpr int kBatch = SLICED ? 8 : 2;  // pieces loaded at once
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = SLICED ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
+  const int first = SLICED ? 32 * warp + lane : lane;  // float4 of the row
   if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
   const int H = p.num_heads;
   const int t = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(t) * H);
@@ -380,14 +385,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
   };
   const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  float4 x[2][4];
+  float4 x[kBatch][kVec];
   auto load = [&](int s0) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       if (s0 + u >= live) continue;
       const float4* src = reinterpret_cast<const float4*>(p.segm_out + at(s0 + u) * kRank);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) x[u][v] = __ldcg(src + v * 32 + lane);
+      for (int v = 0; v < kVec; ++v) x[u][v] = __ldcg(src + v * 32 + first);
     }
   };
   float M = sink2;
@@ -408,11 +413,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
   // (a sink that is NaN leaves M to the others and makes the sum NaN)
   if (M == -INFINITY && !(sink2 != sink2)) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) out[v * 32 + lane] = make_uint2(0u, 0u);
-    if (lane == 0) p.lse[row] = -INFINITY;
+    for (int v = 0; v < kVec; ++v) out[v * 32 + first] = make_uint2(0u, 0u);
+    if (first == 0) p.lse[row] = -INFINITY;
     return;
   }
-  float acc[4][4] = {};
+  float acc[kVec][4] = {};
   float sum = sink2 == -INFINITY ? 0.f : exp2f(sink2 - M);
   for (int s0 = 0; s0 < live; s0 += 32) {
     if (s0 > 0) {
@@ -422,15 +427,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
     }
     const float mine = l0 > 0.f ? l0 * exp2f(m0 - M) : 0.f;
 #pragma unroll 1
-    for (int k = 0; k < 32 && s0 + k < live; k += 2) {
+    for (int k = 0; k < 32 && s0 + k < live; k += kBatch) {
       if (s0 + k > 0) load(s0 + k);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
         const float w = __shfl_sync(0xffffffffu, mine, k + u);
         if (s0 + k + u >= live || w == 0.f) continue;  // (a piece without mass may hold anything)
         sum += w;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
+        for (int v = 0; v < kVec; ++v) {
           acc[v][0] += w * x[u][v].x;
           acc[v][1] += w * x[u][v].y;
           acc[v][2] += w * x[u][v].z;
@@ -441,12 +446,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
   }
   const float inv = 1.f / sum;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
+  for (int v = 0; v < kVec; ++v) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc[v][0] * inv, acc[v][1] * inv);
     const __nv_bfloat162 b = __floats2bfloat162_rn(acc[v][2] * inv, acc[v][3] * inv);
-    out[v * 32 + lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    out[v * 32 + first] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
-  if (lane == 0) p.lse[row] = kLn2 * (M + log2f(sum));
+  if (first == 0) p.lse[row] = kLn2 * (M + log2f(sum));
 }
 
 }  // namespace
@@ -460,7 +465,8 @@ cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   if (rows == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  const bool sliced = rows <= 2048;
+  cfg.gridDim = dim3(static_cast<unsigned>(sliced ? rows : (rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -468,7 +474,8 @@ cudaError_t launch_prefix_merge(const PrefixParams& p, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, p);
+  return sliced ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<true>, p)
+                : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<false>, p);
 }
 
 }  // namespace mla

@@ -498,7 +498,7 @@ bool shares_prefixes(const mla_problem_t& p) {
 
 // Workspace pieces of a shared call, after the status block.
 struct SharedLayout {
-  size_t n_items, worker_first, items, unit_tab, req_group, groups, group_pos, prefix_tab, segm_out, segm_max, segm_expsum, end;
+  size_t n_items, worker_first, items, unit_tab, req_group, groups, group_pos, req_pos, prefix_tab, segm_out, segm_max, segm_expsum, end;
 };
 SharedLayout shared_layout(const mla_shared_plan_t* sp) {
   const mla_problem_t& p = sp->plan.prob;
@@ -517,6 +517,7 @@ SharedLayout shared_layout(const mla_shared_plan_t* sp) {
   l.req_group = take(R * 4);
   l.groups = take(G * 16);
   l.group_pos = take(G * 4);
+  l.req_pos = take(R * 4);
   l.prefix_tab = take(static_cast<size_t>(sp->prefix_tiles) * 8);
   l.segm_out = take(static_cast<size_t>(sp->partial_rows) * kRank * 4);
   l.segm_max = take(static_cast<size_t>(sp->partial_rows) * 4);
@@ -745,7 +746,8 @@ mla_status_t mla_decode_shared_plan(const mla_problem_t* prob, int32_t num_group
   if (num_groups > 65535) return MLA_ERR_UNSUPPORTED;
   plan->num_groups = num_groups;
   plan->workspace_bytes = plan->plan.workspace_bytes;
-  if (!shares_prefixes(p)) return MLA_OK;
+  // (prefixes of fewer key groups than a piece costs are never shared: prefix_sched.cu)
+  if (!shares_prefixes(p) || p.max_seq_len < 128 * mla::kPieceCost) return MLA_OK;
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_heads;
   const int64_t unit_tiles = (static_cast<int64_t>(p.max_qlen) * p.num_heads + 127) / 128;
   const int64_t prefix_tiles = (rows + 127) / 128 + num_groups;  // each group's last may be cut short
@@ -822,6 +824,7 @@ mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q,
   x.req_group = reinterpret_cast<int32_t*>(ws + l.req_group);
   x.groups = reinterpret_cast<int32_t*>(ws + l.groups);
   x.group_pos = reinterpret_cast<int32_t*>(ws + l.group_pos);
+  x.req_pos = reinterpret_cast<int32_t*>(ws + l.req_pos);
   x.prefix_tab = reinterpret_cast<int32_t*>(ws + l.prefix_tab);
   x.segm_out = reinterpret_cast<float*>(ws + l.segm_out);
   x.segm_max = reinterpret_cast<float*>(ws + l.segm_max);

@@ -23,8 +23,9 @@
 // pair, its part in the merge). With 128 heads a request fills its tiles
 // alone, and the common keys come from L2 as they are.
 //
-// One CTA. Lengths and group records are kept in shared memory (of the first 1024
-// requests and 256 groups): re-read from L2 by each pass they took 9 us.
+// One CTA, a thread to a tile's first piece and one to the piece behind each cut.
+// Lengths and group records are kept in shared memory (of the first 1024 requests and
+// 256 groups): it runs beside the decode's start, and before all of its work.
 #include "common.cuh"
 #include "internal.h"
 
@@ -37,9 +38,9 @@ constexpr int kTileRows = 128;
 constexpr int kBins = 512;
 constexpr int kCache = 256;      // groups and
 constexpr int kCacheReqs = 1024; // requests that are kept in shared memory
-constexpr int kPieceCost = 6;
 constexpr int kItemCost = 4;      // of a worker's item: its start and its output, in groups
 constexpr int kMinShare = 4;     // groups: pieces of less cost more than they save
+constexpr int kLeastCut = 6, kLeastEnd = 2;  // of a worker's tile: groups to be cut at all, and on either side of a cut
 
 struct Shared {
   int red[kThreads / 32];
@@ -47,6 +48,7 @@ struct Shared {
   int start[kBins];
   int4 groups[kCache];
   int pos[kCache];
+  int req_pos[kCacheReqs];
   int edge[kCache + 1];
   int4 reqs[kCacheReqs];
 };
@@ -95,32 +97,39 @@ __device__ __forceinline__ int token_edge(const PrefixParams& p, int r) {  // fi
 }
 __device__ __forceinline__ int groups_of(int keys) { return keys > 0 ? keys / kGroupKeys + (keys % kGroupKeys != 0) : 0; }
 
-// Where a tile may be cut.
+// Where a tile may be cut: at the multiples of W in its part of the sequence.
 struct Cutter {
   int W, cost, least, d;  // shares; length of an item besides its groups; groups of a tile that may be cut; of its ends that may not
-  // f(b) for each cut of the tile of g groups at place a, as group offsets; returns their number
-  template <typename F>
-  __device__ __forceinline__ int cuts(int a, int g, F f) const {
-    if (g < least) return 0;
-    const int z = a + cost, hi = g - d;
-    int n = 0;
-    for (int b = (z + d + W - 1) / W * W - z; b <= hi; b += W, ++n) f(b);
-    return n;
+  // the first cut, as a multiple of W, of the tile of g groups at place a; and their number
+  __device__ __forceinline__ int first(int a) const { return (a + cost + d + W - 1) / W; }
+  __device__ __forceinline__ int count(int a, int g) const {
+    return g < least ? 0 : max((a + cost + g - d) / W - first(a) + 1, 0);
   }
 };
+// Piece j of a tile with `cuts` cuts: groups [from, to).
+struct Piece {
+  int from, to;
+};
+__device__ __forceinline__ Piece piece_of(const Cutter& c, int a, int g, int cuts, int j) {
+  const int z = c.first(a) * c.W - a - c.cost;
+  return Piece{j == 0 ? 0 : z + (j - 1) * c.W, j == cuts ? g : z + j * c.W};
+}
+
 __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixParams p) {
   __shared__ Shared s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x;
   const int G = p.num_groups, R = p.num_reqs, H = p.num_heads;
-  const bool few = G <= kCache;
   const bool sorted = p.worker_first == nullptr;
-  const int cost = sorted ? 0 : kItemCost;
+  Cutter cut;
+  cut.cost = sorted ? 0 : kItemCost;
+  const int cost = cut.cost;
   int4* const out_groups = reinterpret_cast<int4*>(p.groups);
-  // {first request, shared keys, tiles of the participants, requests that take part}, then as in PrefixParams
-  int4* const gr = few ? s.groups : out_groups;
-  int* const gp = few ? s.pos : p.group_pos;
-  auto edge = [&](int g) { return few ? s.edge[g] : group_edge(p, g); };
+  // {first request, shared keys, tiles of the participants, -}, then as in PrefixParams
+  int4* const gr = G <= kCache ? s.groups : out_groups;
+  int* const gp = G <= kCache ? s.pos : p.group_pos;  // places of the groups' first tiles
+  int* const rp = R <= kCacheReqs ? s.req_pos : p.req_pos;  // and of the requests'
+  auto edge = [&](int g) { return G <= kCache ? s.edge[g] : group_edge(p, g); };
   auto tiles_of = [&](int64_t tokens) { return static_cast<int>((tokens * H + kTileRows - 1) / kTileRows); };
   // {first token, tokens, length, group of the prefix that the request takes part in or -1}
   auto request = [&](int r) {
@@ -137,14 +146,13 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     const int t0 = token_edge(p, r);
     s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
   }
-#pragma unroll 1
-  for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;
+  s.hist[tid] = 0;
 #pragma unroll 1
   for (int g = tid; g < G; g += kThreads) {
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
     gr[g] = make_int4(INT32_MAX, whole * p.block_size, 0, 0);
   }
-  if (few)
+  if (G <= kCache)
 #pragma unroll 1
     for (int g = tid; g <= G; g += kThreads) s.edge[g] = group_edge(p, g);
   __syncthreads();
@@ -164,34 +172,33 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   }
   __syncthreads();
   // prefix tiles and their places in the sequence
-  int tile_carry = 0;
-  int pos_carry = 0;
+  int ptiles = 0, prefix_end = 0;
 #pragma unroll 1
   for (int g0 = 0; g0 < G; g0 += kThreads) {
     const int g = g0 + tid;
-    int tiles = 0, keys = 0, tok0 = 0;
+    int tiles = 0, keys = 0, tok0 = 0, first = 0;
     if (g < G) {
       tok0 = token_edge(p, edge(g));
       tiles = tiles_of(max(token_edge(p, edge(g + 1)) - tok0, 0));
       const int4 v = gr[g];
+      first = v.x;
       const bool share = static_cast<int64_t>(v.z - tiles) * groups_of(v.y) >= static_cast<int64_t>(kPieceCost) * v.z;
       if (share && v.z > 0) keys = v.y;
       else tiles = 0;
     }
-    int tsum;
-    int psum;
-    const int t = tile_carry + block_scan(tiles, s.red, &tsum);
-    const int a = pos_carry + block_scan(tiles * (groups_of(keys) + cost), s.red, &psum);
-    tile_carry += tsum;
-    pos_carry += psum;
+    int tsum, psum;
+    const int length = tiles * (groups_of(keys) + cost);
+    const int t = ptiles + block_scan(tiles, s.red, &tsum);
+    const int a = prefix_end + block_scan(length, s.red, &psum);
+    ptiles += tsum;
+    prefix_end += psum;
     if (g < G) {
-      const int4 v = make_int4(gr[g].x, keys, tok0, t);
+      const int4 v = make_int4(first, keys, tok0, t);
       gr[g] = v;
       out_groups[g] = v;
       gp[g] = a;
     }
   }
-  const int ptiles = min(tile_carry, p.ptiles_max);
   __syncthreads();
   // own keys of request r
   struct Own {
@@ -206,54 +213,102 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     o.tiles = min(tiles_of(o.q.y), p.tiles_max);
     return o;
   };
-  int mine = 0;
+  int total = prefix_end;
 #pragma unroll 1
-  for (int r = tid; r < R; r += kThreads) {
-    const int g = request(r).w;
-    if (g >= 0 && gr[g].y == 0) set_group(r, -1);
-    const Own o = own_keys(r);
-    mine += o.tiles * (o.groups + cost);
+  for (int r0 = 0; r0 < R; r0 += kThreads) {
+    const int r = r0 + tid;
+    int length = 0;
+    if (r < R) {
+      const int g = request(r).w;
+      if (g >= 0 && gr[g].y == 0) set_group(r, -1);
+      const Own o = own_keys(r);
+      length = o.tiles * (o.groups + cost);
+    }
+    int sum;
+    const int a = total + block_scan(length, s.red, &sum);
+    total += sum;
+    if (r < R) rp[r] = a;
   }
-  int total;
-  block_scan(mine, s.red, &total);
-  total += pos_carry;
-  Cutter cut;
   cut.W = max((total + p.workers - 1) / p.workers, kMinShare);
-  cut.cost = cost;
-  cut.least = sorted ? cut.W / 2 + 1 : 3 * kItemCost;
-  cut.d = sorted ? max(cut.W / 8, 1) : kItemCost;
-  auto tile_group = [&](int t) { return last_at(G, t, [&](int i) { return gr[i].w; }); };
-  // the place in the list that items are counted by: their size, or the worker whose
-  // share their middle falls in
-  auto bin = [&](int a, int from, int to) {
-    if (sorted) return kBins - 1 - min(to - from, kBins - 1);
-    const int begin = a + (from > 0 ? cost + from : 0);
-    return min((begin + (a + cost + to - begin) / 2) / cut.W, p.workers - 1);
+  cut.least = sorted ? cut.W / 2 + 1 : kLeastCut;
+  cut.d = sorted ? max(cut.W / 8, 1) : kLeastEnd;
+  __syncthreads();
+  const int W = cut.W;
+  // A tile: its place, its groups, what its items say.
+  struct Tile {
+    int a, n, unit, tile, first, end;
+    int4 second;
+    int stride;  // rows of a piece's partial
   };
-  auto count = [&](int a, int n) {
-    int prev = 0;
-    cut.cuts(a, n, [&](int b) {
-      atomicAdd(&s.hist[bin(a, prev, b)], 1);
-      prev = b;
-    });
-    atomicAdd(&s.hist[bin(a, prev, n)], 1);
+  auto prefix_tile = [&](int t) {
+    const int g = last_at(G, t, [&](int i) { return gr[i].w; });
+    const int4 v = gr[g];
+    const int n = groups_of(v.y);
+    const int tokens = max(token_edge(p, edge(g + 1)) - v.z, 0);
+    return Tile{gp[g] + (t - v.w) * (n + cost), n, v.x, t - v.w, 0, v.y, make_int4(-1, v.z, tokens | kItemPrefix, 0), kTileRows};
+  };
+  auto own_tile = [&](const Own& o, int r, int t) {
+    return Tile{rp[r] + t * (o.groups + cost), o.groups, r, t, o.first, max(o.q.z, o.first),
+                make_int4(-1, o.q.x, o.q.y, o.q.z - o.q.y + 1), min(kTileRows, o.q.y * H - t * kTileRows)};
+  };
+  // The bin that an item is counted by, its place in the list: its size (the largest
+  // first), or the worker whose share its middle falls in.
+  auto bin = [&](const Tile& t, const Piece& q) {
+    if (sorted) return kBins - 1 - min(q.to - q.from, kBins - 1);
+    const int begin = t.a + (q.from > 0 ? cost + q.from : 0);
+    return min((begin + (t.a + cost + q.to - begin) / 2) / W, p.workers - 1);
+  };
+  // Cut w of the sequence (w W): f(tile, its number of cuts, the piece behind this one,
+  // the tile's entry in the tables), if a tile is cut there.
+  const int all_cuts = (total - 1) / W;
+  auto at_cut = [&](int w, auto f) {
+    const int at = w * W;
+    Tile t;
+    const int2* tab;
+    if (at < prefix_end) {
+      const int g = last_at(G, at, [&](int i) { return gp[i]; });
+      const int i = min(gr[g].w + (at - gp[g]) / (groups_of(gr[g].y) + cost), ptiles - 1);
+      t = prefix_tile(i);
+      tab = reinterpret_cast<const int2*>(p.prefix_tab) + i;
+    } else {
+      const int r = last_at(R, at, [&](int i) { return rp[i]; });
+      const Own o = own_keys(r);
+      if (o.tiles == 0) return;
+      const int i = min((at - rp[r]) / (o.groups + cost), o.tiles - 1);
+      t = own_tile(o, r, i);
+      tab = reinterpret_cast<const int2*>(p.unit_tab) + static_cast<int64_t>(r) * p.tiles_max + i;
+    }
+    const int cuts = cut.count(t.a, t.n), j = w - cut.first(t.a) + 1;
+    if (j >= 1 && j <= cuts) f(t, cuts, j, tab);
+  };
+  auto emit = [&](Tile t, int cuts, int j, int base) {
+    const Piece q = piece_of(cut, t.a, t.n, cuts, j);
+    const int at = atomicAdd(&s.start[bin(t, q)], 1);
+    if (at >= p.max_items) return;
+    int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
+    it[0] = make_int4(t.unit, t.tile, t.first + q.from * kGroupKeys, j == cuts ? t.end : t.first + q.to * kGroupKeys);
+    t.second.x = base < 0 ? -1 : base + j * t.stride;
+    it[1] = t.second;
   };
 #pragma unroll 1
   for (int t = tid; t < ptiles; t += kThreads) {
-    const int g = tile_group(t), n = groups_of(gr[g].y);
-    count(gp[g] + (t - gr[g].w) * (n + cost), n);
+    const Tile v = prefix_tile(t);
+    atomicAdd(&s.hist[bin(v, piece_of(cut, v.a, v.n, cut.count(v.a, v.n), 0))], 1);
   }
-  int carry = pos_carry;
 #pragma unroll 1
-  for (int r0 = 0; r0 < R; r0 += kThreads) {
-    Own o{};
-    if (r0 + tid < R) o = own_keys(r0 + tid);
-    int sum;
-    const int a = carry + block_scan(o.tiles * (o.groups + cost), s.red, &sum);
-    carry += sum;
+  for (int r = tid; r < R; r += kThreads) {
+    const Own o = own_keys(r);
 #pragma unroll 1
-    for (int t = 0; t < o.tiles; ++t) count(a + t * (o.groups + cost), o.groups);
+    for (int t = 0; t < o.tiles; ++t) {
+      const Tile v = own_tile(o, r, t);
+      atomicAdd(&s.hist[bin(v, piece_of(cut, v.a, v.n, cut.count(v.a, v.n), 0))], 1);
+    }
   }
+#pragma unroll 1
+  for (int w = tid + 1; w <= all_cuts; w += kThreads)
+    at_cut(w, [&](const Tile& t, int cuts, int j, const int2*) {
+      atomicAdd(&s.hist[bin(t, piece_of(cut, t.a, t.n, cuts, j))], 1);
+    });
   __syncthreads();
   {  // start[b] = items of the bins before b
     static_assert(kBins == kThreads, "a bin a thread");
@@ -264,79 +319,56 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     if (!sorted && tid <= p.workers) p.worker_first[tid] = min(at, p.max_items);
   }
   __syncthreads();
-  // A tile's items: f(j) = first row of the partial of its piece j (-1: its output).
-  // (Items of a bin are in any order: no result depends on it.)
-  auto emit = [&](int a, int n, int unit, int tile, int first, int end, int4 second, auto f) {
-    int prev = 0, j = 0;
-    auto piece = [&](int b) {
-      const int at = atomicAdd(&s.start[bin(a, prev, b)], 1);
-      if (at < p.max_items) {
-        int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
-        it[0] = make_int4(unit, tile, first + prev * kGroupKeys, b == n ? end : first + b * kGroupKeys);
-        second.x = f(j);
-        it[1] = second;
-      }
-      prev = b;
-      ++j;
-    };
-    cut.cuts(a, n, piece);
-    piece(n);
-  };
-  int row_carry = 0;  // rows of the partials
+  // the tables, and each tile's first item
+  int rows = 0;  // of the partials
 #pragma unroll 1
   for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
     const int t = t0 + tid;
-    int4 v{};
-    int n = 0, k = 0, g = 0;
-    int a = 0;
+    Tile v{};
+    int cuts = -1;
     if (t < ptiles) {
-      g = tile_group(t);
-      v = gr[g];
-      n = groups_of(v.y);
-      a = gp[g] + (t - v.w) * (n + cost);
-      k = 1 + cut.cuts(a, n, [](int) {});
+      v = prefix_tile(t);
+      cuts = cut.count(v.a, v.n);
     }
-    int rows;
-    const int base = row_carry + block_scan(k * kTileRows, s.red, &rows);
-    row_carry += rows;
+    int sum;
+    const int base = rows + block_scan((cuts + 1) * kTileRows, s.red, &sum);
+    rows += sum;
     if (t < ptiles) {
-      reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, k);
-      const int tokens = max(token_edge(p, edge(g + 1)) - v.z, 0);
-      emit(a, n, v.x, t - v.w, 0, v.y, make_int4(0, v.z, tokens | kItemPrefix, 0),
-           [&](int j) { return base + j * kTileRows; });
+      reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, cuts + 1);
+      emit(v, cuts, 0, base);
     }
   }
-  carry = pos_carry;
 #pragma unroll 1
   for (int r0 = 0; r0 < R; r0 += kThreads) {
     const int r = r0 + tid;
     Own o{};
     if (r < R) o = own_keys(r);
-    int sum;
-    const int a = carry + block_scan(o.tiles * (o.groups + cost), s.red, &sum);
-    carry += sum;
     const bool part = r < R && o.q.w >= 0;
-    int rows = 0;
+    int mine = 0;
 #pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
-      const int k = 1 + cut.cuts(a + t * (o.groups + cost), o.groups, [](int) {});
-      if (part || k > 1) rows += k * min(kTileRows, o.q.y * H - t * kTileRows);
+      const Tile v = own_tile(o, r, t);
+      const int cuts = cut.count(v.a, v.n);
+      if (part || cuts > 0) mine += (cuts + 1) * v.stride;
     }
-    int rsum;
-    int base = row_carry + block_scan(rows, s.red, &rsum);
-    row_carry += rsum;
+    int sum;
+    int base = rows + block_scan(mine, s.red, &sum);
+    rows += sum;
 #pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
-      const int at = a + t * (o.groups + cost);
-      const int k = 1 + cut.cuts(at, o.groups, [](int) {});
-      const int tr = min(kTileRows, o.q.y * H - t * kTileRows);
-      const bool split = part || k > 1;
-      reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(split ? base : -1, k);
-      emit(at, o.groups, r, t, o.first, max(o.q.z, o.first), make_int4(0, o.q.x, o.q.y, o.q.z - o.q.y + 1),
-           [&](int j) { return split ? base + j * tr : -1; });
-      if (split) base += k * tr;
+      const Tile v = own_tile(o, r, t);
+      const int cuts = cut.count(v.a, v.n);
+      const bool split = part || cuts > 0;
+      reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(split ? base : -1, cuts + 1);
+      emit(v, cuts, 0, split ? base : -1);
+      if (split) base += (cuts + 1) * v.stride;
     }
   }
+  __syncthreads();
+  // the items behind the cuts
+#pragma unroll 1
+  for (int w = tid + 1; w <= all_cuts; w += kThreads)
+    at_cut(w, [&](const Tile& t, int cuts, int j, const int2* tab) { emit(t, cuts, j, tab->x); });
 }
 
 // One warp a row, or (SLICED, few rows) four, each of 128 of its columns: the

@@ -517,7 +517,7 @@ SharedLayout shared_layout(const mla_shared_plan_t* sp) {
   l.req_group = take(R * 4);
   l.groups = take(G * 16);
   l.group_pos = take(G * 4);
-  l.req_pos = take(R * 4);
+  l.req_pos = take(R * 8);
   l.prefix_tab = take(static_cast<size_t>(sp->prefix_tiles) * 8);
   l.segm_out = take(static_cast<size_t>(sp->partial_rows) * kRank * 4);
   l.segm_max = take(static_cast<size_t>(sp->partial_rows) * 4);

@@ -336,6 +336,7 @@ __device__ void watch(const Ctx& x) {
 }
 // Wait that ignores the abort flag (teardown), bounded by itself.
 __device__ __forceinline__ void drain_wait(const Ctx& x, uint32_t bar, uint32_t parity, int code) {
+  if (mbar_test_wait(bar, parity)) return;  // (nearly always; reading the timer takes longer)
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait_sleep(bar, parity, kSleepNs)) {
     if (global_timer_ns() - t0 > kDefaultWaitNs) {

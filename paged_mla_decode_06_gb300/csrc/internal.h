@@ -311,7 +311,7 @@ struct PrefixParams {
   int32_t* req_group;            // [R]: group whose prefix the request takes part in, or -1
   int32_t* groups;               // [G, 4]: first request, shared keys, first token, first prefix tile
   int32_t* group_pos;            // [G]: its tiles' place in the sequence
-  int32_t* req_pos;              // [R]: the same of each request's own tiles
+  int32_t* req_pos;              // [2 R]: the same of each request's own tiles, and their first items
   int32_t* prefix_tab;           // [ptiles_max, 2]: first partial row, pieces
   const float* segm_out;         // [rows, 512]
   const float* segm_max;

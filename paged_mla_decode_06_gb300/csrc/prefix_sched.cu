@@ -44,11 +44,12 @@ constexpr int kLeastCut = 6, kLeastEnd = 2;  // of a worker's tile: groups to be
 
 struct Shared {
   int red[kThreads / 32];
-  int hist[kBins];   // items by size, or by worker
+  int hist[kBins];   // items by size
   int start[kBins];
   int4 groups[kCache];
   int pos[kCache];
   int req_pos[kCacheReqs];
+  int req_item[kCacheReqs];
   int edge[kCache + 1];
   int4 reqs[kCacheReqs];
 };
@@ -76,6 +77,15 @@ __device__ __noinline__ int block_scan(int v, int* red, int* total) {
   }
   *total = __shfl_sync(0xffffffffu, all, kThreads / 32 - 1);
   return __shfl_sync(0xffffffffu, all - mine, warp) + inc - v;
+}
+
+__device__ __forceinline__ int2 block_scan2(int2 v, int* red, int2* total) {
+  int2 r;
+  int2 all;
+  r.x = block_scan(v.x, red, &all.x);
+  r.y = block_scan(v.y, red, &all.y);
+  *total = all;
+  return r;
 }
 
 // Last i in [0, n) with at(i) <= v (at does not decrease; 0 if none).
@@ -115,20 +125,21 @@ __device__ __forceinline__ Piece piece_of(const Cutter& c, int a, int g, int cut
   return Piece{j == 0 ? 0 : z + (j - 1) * c.W, j == cuts ? g : z + j * c.W};
 }
 
+template <bool SORTED>
 __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixParams p) {
   __shared__ Shared s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x;
   const int G = p.num_groups, R = p.num_reqs, H = p.num_heads;
-  const bool sorted = p.worker_first == nullptr;
+  constexpr int cost = SORTED ? 0 : kItemCost;
   Cutter cut;
-  cut.cost = sorted ? 0 : kItemCost;
-  const int cost = cut.cost;
+  cut.cost = cost;
   int4* const out_groups = reinterpret_cast<int4*>(p.groups);
   // {first request, shared keys, tiles of the participants, -}, then as in PrefixParams
   int4* const gr = G <= kCache ? s.groups : out_groups;
   int* const gp = G <= kCache ? s.pos : p.group_pos;  // places of the groups' first tiles
-  int* const rp = R <= kCacheReqs ? s.req_pos : p.req_pos;  // and of the requests'
+  int* const rp = R <= kCacheReqs ? s.req_pos : p.req_pos;  // and of the requests',
+  int* const ri = R <= kCacheReqs ? s.req_item : p.req_pos + R;  // and the requests' first items
   auto edge = [&](int g) { return G <= kCache ? s.edge[g] : group_edge(p, g); };
   auto tiles_of = [&](int64_t tokens) { return static_cast<int>((tokens * H + kTileRows - 1) / kTileRows); };
   // {first token, tokens, length, group of the prefix that the request takes part in or -1}
@@ -136,6 +147,11 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     if (r < kCacheReqs) return s.reqs[r];
     const int t0 = token_edge(p, r);
     return make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], p.req_group[r]);
+  };
+  auto first_token = [&](int r) { return r < min(R, kCacheReqs) ? s.reqs[r].x : token_edge(p, r); };
+  auto group_tokens = [&](int g) {  // {first, number}
+    const int t0 = first_token(edge(g));
+    return make_int2(t0, max(first_token(edge(g + 1)) - t0, 0));
   };
   auto set_group = [&](int r, int g) {
     p.req_group[r] = g;
@@ -146,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     const int t0 = token_edge(p, r);
     s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
   }
-  s.hist[tid] = 0;
+  if (SORTED) s.hist[tid] = 0;
 #pragma unroll 1
   for (int g = tid; g < G; g += kThreads) {
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
@@ -178,28 +194,36 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     const int g = g0 + tid;
     int tiles = 0, keys = 0, tok0 = 0, first = 0;
     if (g < G) {
-      tok0 = token_edge(p, edge(g));
-      tiles = tiles_of(max(token_edge(p, edge(g + 1)) - tok0, 0));
+      const int2 tokens = group_tokens(g);
+      tok0 = tokens.x;
+      tiles = tiles_of(tokens.y);
       const int4 v = gr[g];
       first = v.x;
       const bool share = static_cast<int64_t>(v.z - tiles) * groups_of(v.y) >= static_cast<int64_t>(kPieceCost) * v.z;
       if (share && v.z > 0) keys = v.y;
       else tiles = 0;
     }
-    int tsum, psum;
     const int length = tiles * (groups_of(keys) + cost);
-    const int t = ptiles + block_scan(tiles, s.red, &tsum);
-    const int a = prefix_end + block_scan(length, s.red, &psum);
-    ptiles += tsum;
-    prefix_end += psum;
+    int2 sum = make_int2(tiles, length), at = make_int2(0, 0);
+    if (G > 1) at = block_scan2(sum, s.red, &sum);
+    const int t = ptiles + at.x, a = prefix_end + at.y;
+    if (G > 1) {
+      ptiles += sum.x;
+      prefix_end += sum.y;
+    }
     if (g < G) {
       const int4 v = make_int4(first, keys, tok0, t);
       gr[g] = v;
       out_groups[g] = v;
       gp[g] = a;
+      if (G == 1) s.start[0] = tiles;
     }
   }
   __syncthreads();
+  if (G == 1) {
+    ptiles = s.start[0];
+    prefix_end = ptiles * (groups_of(gr[0].y) + cost);
+  }
   // own keys of request r
   struct Own {
     int4 q;
@@ -230,8 +254,8 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     if (r < R) rp[r] = a;
   }
   cut.W = max((total + p.workers - 1) / p.workers, kMinShare);
-  cut.least = sorted ? cut.W / 2 + 1 : kLeastCut;
-  cut.d = sorted ? max(cut.W / 8, 1) : kLeastEnd;
+  cut.least = SORTED ? cut.W / 2 + 1 : kLeastCut;
+  cut.d = SORTED ? max(cut.W / 8, 1) : kLeastEnd;
   __syncthreads();
   const int W = cut.W;
   // A tile: its place, its groups, what its items say.
@@ -244,83 +268,88 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     const int g = last_at(G, t, [&](int i) { return gr[i].w; });
     const int4 v = gr[g];
     const int n = groups_of(v.y);
-    const int tokens = max(token_edge(p, edge(g + 1)) - v.z, 0);
+    const int tokens = group_tokens(g).y;
     return Tile{gp[g] + (t - v.w) * (n + cost), n, v.x, t - v.w, 0, v.y, make_int4(-1, v.z, tokens | kItemPrefix, 0), kTileRows};
   };
   auto own_tile = [&](const Own& o, int r, int t) {
     return Tile{rp[r] + t * (o.groups + cost), o.groups, r, t, o.first, max(o.q.z, o.first),
                 make_int4(-1, o.q.x, o.q.y, o.q.z - o.q.y + 1), min(kTileRows, o.q.y * H - t * kTileRows)};
   };
-  // The bin that an item is counted by, its place in the list: its size (the largest
-  // first), or the worker whose share its middle falls in.
-  auto bin = [&](const Tile& t, const Piece& q) {
-    if (sorted) return kBins - 1 - min(q.to - q.from, kBins - 1);
-    const int begin = t.a + (q.from > 0 ? cost + q.from : 0);
-    return min((begin + (t.a + cost + q.to - begin) / 2) / W, p.workers - 1);
-  };
-  // Cut w of the sequence (w W): f(tile, its number of cuts, the piece behind this one,
-  // the tile's entry in the tables), if a tile is cut there.
-  const int all_cuts = (total - 1) / W;
-  auto at_cut = [&](int w, auto f) {
-    const int at = w * W;
+  // Cut w of the sequence: the tile that place w W lies in, its entry in the tables and,
+  // of an own tile, its first item; false where it is no tile's.
+  struct At {
     Tile t;
     const int2* tab;
+    int item;
+  };
+  auto at_cut = [&](int w, At& c) {
+    const int at = w * W;
     if (at < prefix_end) {
       const int g = last_at(G, at, [&](int i) { return gp[i]; });
       const int i = min(gr[g].w + (at - gp[g]) / (groups_of(gr[g].y) + cost), ptiles - 1);
-      t = prefix_tile(i);
-      tab = reinterpret_cast<const int2*>(p.prefix_tab) + i;
-    } else {
-      const int r = last_at(R, at, [&](int i) { return rp[i]; });
-      const Own o = own_keys(r);
-      if (o.tiles == 0) return;
-      const int i = min((at - rp[r]) / (o.groups + cost), o.tiles - 1);
-      t = own_tile(o, r, i);
-      tab = reinterpret_cast<const int2*>(p.unit_tab) + static_cast<int64_t>(r) * p.tiles_max + i;
+      c.t = prefix_tile(i);
+      c.tab = reinterpret_cast<const int2*>(p.prefix_tab) + i;
+      c.item = c.tab->x / kTileRows;
+      return true;
     }
-    const int cuts = cut.count(t.a, t.n), j = w - cut.first(t.a) + 1;
-    if (j >= 1 && j <= cuts) f(t, cuts, j, tab);
+    const int r = last_at(R, at, [&](int i) { return rp[i]; });
+    const Own o = own_keys(r);
+    if (o.tiles == 0) return false;
+    const int i = min((at - rp[r]) / (o.groups + cost), o.tiles - 1);
+    c.t = own_tile(o, r, i);
+    c.tab = reinterpret_cast<const int2*>(p.unit_tab) + static_cast<int64_t>(r) * p.tiles_max + i;
+    if (!SORTED) {
+      c.item = ri[r];
+#pragma unroll 1
+      for (int t = 0; t < i; ++t) {
+        const Tile v = own_tile(o, r, t);
+        c.item += cut.count(v.a, v.n) + 1;
+      }
+    }
+    return true;
   };
-  auto emit = [&](Tile t, int cuts, int j, int base) {
+  auto emit = [&](Tile t, int cuts, int j, int base, int at) {
     const Piece q = piece_of(cut, t.a, t.n, cuts, j);
-    const int at = atomicAdd(&s.start[bin(t, q)], 1);
+    if (SORTED) at = atomicAdd(&s.start[kBins - 1 - min(q.to - q.from, kBins - 1)], 1);
     if (at >= p.max_items) return;
     int4* it = reinterpret_cast<int4*>(p.items) + 2 * static_cast<int64_t>(at);
     it[0] = make_int4(t.unit, t.tile, t.first + q.from * kGroupKeys, j == cuts ? t.end : t.first + q.to * kGroupKeys);
     t.second.x = base < 0 ? -1 : base + j * t.stride;
     it[1] = t.second;
   };
+  const int all_cuts = (total - 1) / W;
+  if constexpr (SORTED) {
+    // the places of the items by their size: how many are larger
+    auto count = [&](const Tile& t, int j) {
+      const int cuts = cut.count(t.a, t.n);
+      const Piece q = piece_of(cut, t.a, t.n, cuts, j);
+      atomicAdd(&s.hist[kBins - 1 - min(q.to - q.from, kBins - 1)], 1);
+    };
 #pragma unroll 1
-  for (int t = tid; t < ptiles; t += kThreads) {
-    const Tile v = prefix_tile(t);
-    atomicAdd(&s.hist[bin(v, piece_of(cut, v.a, v.n, cut.count(v.a, v.n), 0))], 1);
-  }
+    for (int t = tid; t < ptiles; t += kThreads) count(prefix_tile(t), 0);
 #pragma unroll 1
-  for (int r = tid; r < R; r += kThreads) {
-    const Own o = own_keys(r);
+    for (int r = tid; r < R; r += kThreads) {
+      const Own o = own_keys(r);
 #pragma unroll 1
-    for (int t = 0; t < o.tiles; ++t) {
-      const Tile v = own_tile(o, r, t);
-      atomicAdd(&s.hist[bin(v, piece_of(cut, v.a, v.n, cut.count(v.a, v.n), 0))], 1);
+      for (int t = 0; t < o.tiles; ++t) count(own_tile(o, r, t), 0);
     }
-  }
 #pragma unroll 1
-  for (int w = tid + 1; w <= all_cuts; w += kThreads)
-    at_cut(w, [&](const Tile& t, int cuts, int j, const int2*) {
-      atomicAdd(&s.hist[bin(t, piece_of(cut, t.a, t.n, cuts, j))], 1);
-    });
-  __syncthreads();
-  {  // start[b] = items of the bins before b
+    for (int w = tid + 1; w <= all_cuts; w += kThreads) {
+      At c;
+      if (!at_cut(w, c)) continue;
+      const int j = w - cut.first(c.t.a) + 1;
+      if (j >= 1 && j <= cut.count(c.t.a, c.t.n)) count(c.t, j);
+    }
+    __syncthreads();
     static_assert(kBins == kThreads, "a bin a thread");
     int all;
     const int at = block_scan(s.hist[tid], s.red, &all);
     s.start[tid] = at;
     if (tid == 0) *p.n_items = min(all, p.max_items);
-    if (!sorted && tid <= p.workers) p.worker_first[tid] = min(at, p.max_items);
+    __syncthreads();
   }
-  __syncthreads();
   // the tables, and each tile's first item
-  int rows = 0;  // of the partials
+  int rows = 0, items = 0;  // of the partials, of the list
 #pragma unroll 1
   for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
     const int t = t0 + tid;
@@ -331,11 +360,12 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       cuts = cut.count(v.a, v.n);
     }
     int sum;
-    const int base = rows + block_scan((cuts + 1) * kTileRows, s.red, &sum);
-    rows += sum;
+    const int at = items + block_scan(cuts + 1, s.red, &sum);
+    items += sum;
+    rows += sum * kTileRows;
     if (t < ptiles) {
-      reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(base, cuts + 1);
-      emit(v, cuts, 0, base);
+      reinterpret_cast<int2*>(p.prefix_tab)[t] = make_int2(at * kTileRows, cuts + 1);
+      emit(v, cuts, 0, at * kTileRows, at);
     }
   }
 #pragma unroll 1
@@ -344,31 +374,59 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     Own o{};
     if (r < R) o = own_keys(r);
     const bool part = r < R && o.q.w >= 0;
-    int mine = 0;
+    int2 mine = make_int2(0, 0);
 #pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
       const Tile v = own_tile(o, r, t);
-      const int cuts = cut.count(v.a, v.n);
-      if (part || cuts > 0) mine += (cuts + 1) * v.stride;
+      const int k = cut.count(v.a, v.n) + 1;
+      mine.x += k;
+      if (part || k > 1) mine.y += k * v.stride;
     }
-    int sum;
-    int base = rows + block_scan(mine, s.red, &sum);
-    rows += sum;
+    int2 sum;
+    const int2 before = block_scan2(mine, s.red, &sum);
+    int at = items + before.x, base = rows + before.y;
+    items += sum.x;
+    rows += sum.y;
+    if (r < R) ri[r] = at;
 #pragma unroll 1
     for (int t = 0; t < o.tiles; ++t) {
       const Tile v = own_tile(o, r, t);
       const int cuts = cut.count(v.a, v.n);
       const bool split = part || cuts > 0;
       reinterpret_cast<int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + t] = make_int2(split ? base : -1, cuts + 1);
-      emit(v, cuts, 0, split ? base : -1);
+      emit(v, cuts, 0, split ? base : -1, at);
+      at += cuts + 1;
       if (split) base += (cuts + 1) * v.stride;
     }
   }
   __syncthreads();
-  // the items behind the cuts
+  // the items behind the cuts; and each worker's first item: of the piece that the start
+  // of its share lies in, or the next where that one's middle is before it
+  items = min(items, p.max_items);
 #pragma unroll 1
-  for (int w = tid + 1; w <= all_cuts; w += kThreads)
-    at_cut(w, [&](const Tile& t, int cuts, int j, const int2* tab) { emit(t, cuts, j, tab->x); });
+  for (int w = tid + 1; w <= (SORTED ? all_cuts : max(all_cuts, p.workers)); w += kThreads) {
+    At c;
+    if (w > all_cuts || !at_cut(w, c)) {
+      if (!SORTED && w <= p.workers) p.worker_first[w] = items;
+      continue;
+    }
+    const int cuts = cut.count(c.t.a, c.t.n), j = w - cut.first(c.t.a) + 1;
+    const bool here = j >= 1 && j <= cuts;
+    if (here) emit(c.t, cuts, j, c.tab->x, c.item + j);
+    if (!SORTED && w <= p.workers) {
+      int at = c.item + (here ? j : j < 1 ? 0 : cuts);
+      if (!here) {
+        const Piece q = piece_of(cut, c.t.a, c.t.n, cuts, j < 1 ? 0 : cuts);
+        const int begin = c.t.a + (q.from > 0 ? cost + q.from : 0);
+        at += (begin + c.t.a + cost + q.to) / 2 < w * W ? 1 : 0;
+      }
+      p.worker_first[w] = min(at, items);
+    }
+  }
+  if (!SORTED && tid == 0) {
+    p.worker_first[0] = 0;
+    *p.n_items = items;
+  }
 }
 
 // One warp a row, or (SLICED, few rows) four, each of 128 of its columns: the
@@ -489,7 +547,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
 }  // namespace
 
 cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t stream) {
-  prefix_schedule_kernel<<<1, kThreads, 0, stream>>>(p);
+  if (p.worker_first == nullptr)
+    prefix_schedule_kernel<true><<<1, kThreads, 0, stream>>>(p);
+  else
+    prefix_schedule_kernel<false><<<1, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

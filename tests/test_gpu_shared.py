@@ -265,6 +265,25 @@ def test_more_groups_than_the_schedule_caches():
     check(shared_case(15, "scaled", 4, 64, 64, groups))
 
 
+@pytest.mark.parametrize("kind,bs", [("scaled", 16), ("bf16", 64)])
+def test_more_requests_than_the_schedule_caches(kind, bs):
+    groups = [(3 * bs + 200, [1 + (i * j) % 60 for i in range(370)]) for j in (3, 5, 7)]
+    check(shared_case(27, kind, 2, bs, bs, groups, alone=[5, 300]))
+
+
+def test_repeated_calls_leave_no_status():
+    """Waits that are passed over, or that take another phase for theirs, show in some
+    call of many."""
+    c = shared_case(28, "scaled", 32, 64, 1, [(1500 + 700 * i, [3 + 97 * j % 700 for j in range(8)]) for i in range(6)],
+                    qlens=[1 + i % 3 for i in range(48)])
+    args, named = args_of(c, plan_of(c))
+    for _ in range(1500):
+        B.mla_decode_fwd_shared(*args, **named)
+    torch.cuda.synchronize()
+    assert B.mla_workspace_status(args[0].plan, named["workspace"]) == 0
+    compare(c, named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy())
+
+
 def test_uneven_scales_and_a_key_that_outweighs_the_rest():
     c = shared_case(16, "scaled", 20, 64, 1, [(1500, [3, 400, 64])])
     rng = np.random.default_rng(0)

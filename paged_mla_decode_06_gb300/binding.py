@@ -736,28 +736,32 @@ def mla_rope_qk(rope: Rope, positions, *, ql_nope=None, q_pe=None, q_out=None, q
     torch = _torch or _load_torch()
     i32, b16 = torch.int32, torch.bfloat16
     codes = (b16,) if q_scale is None else (torch.float8_e4m3fn, torch.uint8)
-    rope_cols = HEAD_DIM - KV_LORA_RANK
     dev, T, H = positions.get_device(), positions.numel(), 0
     ok = (dev >= 0 and dev == torch._C._cuda_getDevice() and positions.dtype is i32 and positions.is_contiguous()
-          and (ql_nope is None) == (q_pe is None) == (q_out is None) and (k_pe is None) == (k_out is None)
           and (ql_nope is not None or k_pe is not None))
     nope = pe = out = keys = kout = None
     n_st = p_st = (0, 0, 0)
-    k_st = ko_st = rope_cols
-    if ok and ql_nope is not None:
-        H = ql_nope.shape[1] if ql_nope.dim() == 3 else 0
-        ok = (H > 0 and ql_nope.shape == (T, H, KV_LORA_RANK) and ql_nope.dtype is b16 and ql_nope.get_device() == dev
-              and _last_dense(ql_nope) and q_pe.shape == (T, H, rope_cols) and q_pe.dtype is b16
-              and q_pe.get_device() == dev and _last_dense(q_pe) and q_out.shape == (T, H, HEAD_DIM)
-              and q_out.dtype in codes and q_out.get_device() == dev and q_out.is_contiguous())
-        nope, pe, out, n_st, p_st = ql_nope.data_ptr(), q_pe.data_ptr(), q_out.data_ptr(), ql_nope.stride(), q_pe.stride()
-    if ok and k_pe is not None:
-        ok = (k_pe.shape == (T, rope_cols) and k_pe.dtype is b16 and k_pe.get_device() == dev and _last_dense(k_pe)
-              and k_out.shape == (T, rope_cols) and k_out.dtype is b16 and k_out.get_device() == dev
-              and _dense_rows(k_out.shape, k_out.stride(), 1))
-        keys, kout = k_pe.data_ptr(), k_out.data_ptr()
-        if T > 1:
-            k_st, ko_st = k_pe.stride(0), k_out.stride(0)
+    k_st = ko_st = (64, 1)
+    if ql_nope is None:
+        ok = ok and q_pe is None and q_out is None
+    elif ok:
+        ok = False
+        if q_pe is not None and q_out is not None and ql_nope.dim() == 3:
+            n_st, p_st, H = ql_nope.stride(), q_pe.stride(), ql_nope.size(1)
+            ok = (H > 0 and ql_nope.shape == (T, H, 512) and ql_nope.dtype is b16 and ql_nope.get_device() == dev
+                  and n_st[2] == 1 and q_pe.shape == (T, H, 64) and q_pe.dtype is b16 and q_pe.get_device() == dev
+                  and p_st[2] == 1 and q_out.shape == (T, H, 576) and q_out.dtype in codes
+                  and q_out.get_device() == dev and q_out.is_contiguous())
+            nope, pe, out = ql_nope.data_ptr(), q_pe.data_ptr(), q_out.data_ptr()
+    if k_pe is None:
+        ok = ok and k_out is None
+    elif ok:
+        ok = False
+        if k_out is not None and k_pe.shape == (T, 64) and k_out.shape == (T, 64):
+            k_st, ko_st = k_pe.stride(), k_out.stride()
+            ok = (k_pe.dtype is b16 and k_pe.get_device() == dev and k_st[1] == 1 and k_out.dtype is b16
+                  and k_out.get_device() == dev and ko_st[1] == 1 and (T < 2 or ko_st[0] >= 64))
+            keys, kout = k_pe.data_ptr(), k_out.data_ptr()
     fn = "mla_rope_qk"
     if not ok:
         named = [("ql_nope", ql_nope, (b16,)), ("q_pe", q_pe, (b16,)), ("q_out", q_out, codes), ("k_pe", k_pe, (b16,)),
@@ -771,10 +775,14 @@ def mla_rope_qk(rope: Rope, positions, *, ql_nope=None, q_pe=None, q_out=None, q
                 [(t is None or _last_dense(t), f"the last dimension of {n} must be contiguous") for n, t, _ in named] +
                 [(False, f"the shapes must be [{T}, H, 512], [{T}, H, 64] and contiguous [{T}, H, 576]; [{T}, 64] with "
                          "rows of k_out that do not overlap")])
+    if T < 2 or H < 2:  # (strides of dimensions of one element say nothing)
+        n_st, p_st = ((st[0] if T > 1 else 0, st[1] if H > 1 else 0) for st in (n_st, p_st))
+        if T < 2:
+            k_st = ko_st = (64, 1)
     status = lib.mla_rope_qk(
         ctypes.byref(rope), positions.data_ptr(), T, H, nope, n_st[0], n_st[1], pe, p_st[0], p_st[1],
-        MLA_DTYPE_BF16 if q_scale is None else MLA_DTYPE_FP8_E4M3, 1.0 if q_scale is None else q_scale, out, keys, k_st,
-        kout, ko_st, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        MLA_DTYPE_BF16 if q_scale is None else MLA_DTYPE_FP8_E4M3, 1.0 if q_scale is None else q_scale, out, keys,
+        k_st[0], kout, max(ko_st[0], 64), torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status:
         _check(fn, status)
 
@@ -809,14 +817,19 @@ def _int_lists(fn: str, dev: int, tables, lists):
     tensor or None, size or None)] on device ``dev``."""
     i32 = _torch.int32
     for name, t, n in lists:
-        if t is not None and not (t.dtype is i32 and t.get_device() == dev and t.is_contiguous()
-                                  and (n is None or t.numel() == n)):
-            _refuse(fn, dev, [(name, t, (i32,))], [(t.is_contiguous(), f"{name} must be contiguous"),
-                                                   (False, f"{name} must hold {n} numbers")])
+        if t is None or (t.dtype is i32 and t.get_device() == dev and t.is_contiguous()
+                         and (n is None or t.numel() == n)):
+            continue
+        _refuse(fn, dev, [(name, t, (i32,))], [(t.is_contiguous(), f"{name} must be contiguous"),
+                                               (False, f"{name} must hold {n} numbers")])
     for name, t in tables:
-        if not (t.dtype is i32 and t.get_device() == dev and t.dim() == 2 and _dense_rows(t.shape, t.stride(), 1)):
-            _refuse(fn, dev, [(name, t, (i32,))],
-                    [(False, f"{name} must be [rows, columns] with dense rows that do not overlap")])
+        if t.dtype is i32 and t.get_device() == dev and t.dim() == 2:
+            rows, cols = t.shape
+            st = t.stride()
+            if cols > 0 and (rows == 0 or ((st[1] == 1 or cols == 1) and (rows == 1 or st[0] >= cols))):
+                continue
+        _refuse(fn, dev, [(name, t, (i32,))],
+                [(False, f"{name} must be [rows, columns] with dense rows that do not overlap")])
 
 
 def _table_stride(t) -> int:

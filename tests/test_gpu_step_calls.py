@@ -116,6 +116,19 @@ def test_rope_in_place_keys_and_each_alone():
     B.mla_rope_qk(rope, i32([]), k_pe=k[:0], k_out=ko[:0])
 
 
+def test_rope_strides_of_single_elements_say_nothing():
+    rope = B.mla_rope_plan()
+    pos, nope, pe, k = rope_case(6, 3, 1)
+    q, ko = torch.zeros((3, 1, 576), dtype=torch.bfloat16, device="cuda"), torch.zeros_like(k)
+    B.mla_rope_qk(rope, i32(pos), ql_nope=nope, q_pe=pe, q_out=q, k_pe=k, k_out=ko)
+    odd = lambda x, st: torch.as_strided(x.contiguous(), x.shape, st)
+    for i in range(3):
+        q1, k1 = torch.zeros_like(q[:1]), torch.zeros_like(ko[:1])
+        B.mla_rope_qk(rope, i32(pos[i:i + 1]), ql_nope=odd(nope[i:i + 1], (3, 5, 1)), q_pe=odd(pe[i:i + 1], (3, 5, 1)),
+                      q_out=q1, k_pe=odd(k[i:i + 1], (3, 1)), k_out=k1)
+        assert torch.equal(q1, q[i:i + 1]) and torch.equal(k1, ko[i:i + 1])
+
+
 def test_rope_position_zero_is_the_concatenation_and_non_finite_values_stay_in_their_pair():
     rope = B.mla_rope_plan(dim=32)
     _, nope, pe, _ = rope_case(8, 4, 16)

@@ -179,6 +179,78 @@ def test_page_workspaces_and_sizes(lib):
     assert lib.mla_cache_free is not None
 
 
+# ---------------------------------------------------------------- the decode over shared prefixes
+
+def _problem(dtype="fp8", block=64, **kw):
+    base = dict(num_tokens=6, num_reqs=6, num_heads=16, block_size=block, num_blocks=100, max_blocks_per_req=40,
+                max_seq_len=40 * block, num_sms=152, dtype=dtype)
+    base.update(kw)
+    return B.make_problem(**base)
+
+
+def test_shared_plan():
+    p = B.mla_decode_shared_plan(_problem(), num_groups=2)
+    assert p.num_groups == 2 and p.workers == 76 and p.unit_tiles == 1 and p.prefix_tiles == 1 + 2
+    assert p.max_items == 3 + 6 + 76 and p.partial_rows == (3 + 76) * 128 + 96
+    assert p.workspace_bytes >= p.partial_rows * 2056 and p.workspace_bytes >= p.plan.workspace_bytes
+    p = B.mla_decode_shared_plan(_problem(num_heads=128, max_qlen=3, num_tokens=18))
+    assert p.unit_tiles == 3 and p.prefix_tiles == 18 + 1
+
+
+@pytest.mark.parametrize("kw", [dict(block=8), dict(block=24), dict(dtype="bf16", block=32), dict(num_segments=2),
+                                dict(kernel=B.MLA_KERNEL_TCGEN05), dict(max_seq_len=500)])
+def test_shared_plans_that_run_as_the_plain_decode(kw):
+    p = B.mla_decode_shared_plan(_problem(**kw))
+    assert p.max_items == 0 and p.workspace_bytes == p.plan.workspace_bytes
+
+
+def test_shared_plan_refusals(lib):
+    out = B.SharedPlan()
+    pr = _problem()
+    assert lib.mla_decode_shared_plan(None, 1, ctypes.byref(out)) == B.MLA_ERR_INVALID_ARG
+    assert lib.mla_decode_shared_plan(ctypes.byref(pr), 1, None) == B.MLA_ERR_INVALID_ARG
+    for g, want in ((0, B.MLA_ERR_INVALID_ARG), (-1, B.MLA_ERR_INVALID_ARG), (65536, B.MLA_ERR_UNSUPPORTED)):
+        assert lib.mla_decode_shared_plan(ctypes.byref(pr), g, ctypes.byref(out)) == want
+    pr = _problem(num_reqs=0, topk=128, max_blocks_per_req=0, max_seq_len=0)
+    assert lib.mla_decode_shared_plan(ctypes.byref(pr), 1, ctypes.byref(out)) == B.MLA_ERR_UNSUPPORTED
+    pr = _problem(num_heads=0)
+    assert lib.mla_decode_shared_plan(ctypes.byref(pr), 1, ctypes.byref(out)) == B.MLA_ERR_INVALID_ARG
+
+
+def _shared(lib, plan, q=P, kv=P, sc=P, g=64, bt=P, stride=40, sl=P, qo=None, pre=P, gi=P, scale=1.0, qs=1.0, ks=1.0,
+            sinks=None, ws=P, nbytes=1 << 40, out=P, lse=P):
+    f = ctypes.c_float
+    return lib.mla_decode_fwd_shared(None if plan is None else ctypes.byref(plan), q, kv, sc, g, bt, stride, sl, qo, pre, gi,
+                                     f(scale), f(qs), f(ks), sinks, ws, nbytes, out, lse, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(plan=None), 1), (dict(q=None), 1), (dict(q=P + 8), 1), (dict(kv=None), 1), (dict(kv=P + 8), 1),
+    (dict(sc=None), 1), (dict(g=0), 1), (dict(g=48), 1), (dict(g=-64), 1), (dict(sc=P + 2), 1), (dict(bt=None), 1),
+    (dict(bt=P + 2), 1), (dict(stride=39), 1), (dict(sl=None), 1), (dict(sl=P + 1), 1), (dict(pre=None), 1),
+    (dict(pre=P + 2), 1), (dict(gi=P + 2), 1), (dict(gi=None), 1), (dict(scale=0.0), 1), (dict(scale=math.nan), 1),
+    (dict(qs=-1.0), 1), (dict(ks=2.0), 1), (dict(ks=math.inf), 1), (dict(sinks=P), 1), (dict(out=None), 1),
+    (dict(out=P + 8), 1), (dict(lse=None), 1), (dict(lse=P + 2), 1), (dict(ws=None), 3), (dict(nbytes=1000), 3),
+    (dict(ws=P + 128), 1)])
+def test_shared_refusals(lib, kw, status):
+    plan = B.mla_decode_shared_plan(_problem(), num_groups=2)
+    assert _shared(lib, **dict(dict(plan=plan), **kw)) == status
+
+
+def test_shared_refusals_of_other_plans(lib):
+    plan = B.mla_decode_shared_plan(_problem(dtype="bf16"), num_groups=2)
+    assert _shared(lib, plan) == B.MLA_ERR_UNSUPPORTED                      # group scales of a bf16 cache
+    plan = B.mla_decode_shared_plan(_problem(has_sinks=True), num_groups=2)
+    assert _shared(lib, plan) == B.MLA_ERR_INVALID_ARG                      # no sinks
+    plan = B.mla_decode_shared_plan(_problem(max_qlen=2), num_groups=2)
+    assert _shared(lib, plan) == B.MLA_ERR_INVALID_ARG                      # no token offsets
+    plan = B.mla_decode_shared_plan(_problem(), num_groups=2)
+    plan.workers = 0
+    assert _shared(lib, plan) == B.MLA_ERR_INVALID_ARG
+    plan = B.mla_decode_shared_plan(_problem(num_tokens=0, num_reqs=0), num_groups=2)
+    assert _shared(lib, plan, q=None, kv=None) == B.MLA_OK                  # nothing to do
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     i = torch.zeros(2, dtype=torch.int32)

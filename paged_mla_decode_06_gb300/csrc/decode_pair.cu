@@ -701,7 +701,7 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     return fmaxf(fmaxf(xm[0], xm[kOwnRows]), fmaxf(xm[2 * kOwnRows], xm[3 * kOwnRows]));
   };
   // the maximum of chunk c, which the other group posted. A group looks at it
-  // before it posts its own of c + 1, which the other waits for before it posts
+  // before it posts its own of c + 3, which the other waits for before it posts
   // that of c + 4: neither the barrier's phase nor the four buffers are passed over.
   auto follow_other = [&](int c) {
     if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1)) return false;
@@ -757,11 +757,11 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
       if constexpr (ONE) m[i] *= p.score_scale_log2;
     }
     // the row's maximum over all key quarters; the previous chunk's before it
-    ok = c == first || follow_other(c - 1);
-    if (!ok) break;
     xmax[((c & 3) * 4 + part) * kOwnRows] = fmaxf(m[0], m[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(x.bar(kX + 2 * (c & 3) + rq));
+    ok = c == first || follow_other(c - 1);
+    if (!ok) break;
     ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1);
     if (!ok) break;
     const float alpha = follow(row_max(c));

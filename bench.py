@@ -128,8 +128,8 @@ def _flops(w):
 PROFILED_TRAFFIC = {
     (4, "dsv3", None): {  # decode_tc.cu, DeepSeek-V3-shaped batch (profiles/decode_tc_dsv3.md)
         "source": "decode_tc.cu",
-        "code_sha256": "8627e3e3dff2a7f099e4577878849af60304b92bd461a6cd133bfca0f5975a21",
-        "dram_per_alg_byte": (139.609088 + 3.360256) / 138.103440,
+        "code_sha256": "da13d048665d44c7ddcc538794e7f607b56fd22feefee2e364670f59ea46aa8b",
+        "dram_per_alg_byte": (139.570176 + 3.544576) / 138.103440,
     },
     (5, "fp8", 16): {  # decode_hn.cu, e4m3 batch at 16 heads (profiles/decode_hn_fp8.md)
         "source": "decode_hn.cu",

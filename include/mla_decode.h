@@ -717,7 +717,8 @@ MLA_API mla_status_t mla_rope_plan(const mla_rope_problem_t* prob, mla_rope_t* r
  *           projection's rows; num_heads 0: no queries
  *   q_out   [T, H, 576] contiguous, in out_dtype, not overlapping the inputs
  *   k_pe    [T, 64] bf16, row stride k_pe_stride, or NULL: no keys; k_out [T, 64]
- *           bf16, row stride k_out_stride: k_pe itself, or not overlapping it
+ *           bf16, row stride k_out_stride: k_pe itself with its stride, or not
+ *           overlapping it
  * The last dims are contiguous; ql_nope and q_out 16-byte aligned, the strides of
  * ql_nope multiples of 8; q_pe, k_pe and k_out 4-byte aligned, their strides
  * even. One launch on `stream`. Errors: MLA_ERR_INVALID_ARG (also where neither
@@ -776,8 +777,9 @@ MLA_API mla_status_t mla_cache_copy_blocks(const int32_t* src, const int32_t* ds
                                            cudaStream_t stream);
 
 /* Workspace bytes of mla_cache_free and mla_cache_compact for a pool of num_blocks;
- * 0 for num_blocks <= 0. Zero it once after allocating. One call at a time may use
- * a workspace; calls on one stream follow one another. */
+ * 0 for num_blocks <= 0. Zero it once after allocating, and again before calls with
+ * another num_blocks (the lists of one size lie where another keeps its zeros). One
+ * call at a time may use a workspace; calls on one stream follow one another. */
 MLA_API size_t mla_cache_workspace(int32_t num_blocks);
 
 /*

@@ -154,6 +154,7 @@ mla_status_t mla_rope_qk(const mla_rope_t* rope, const int32_t* positions, int32
     if (k_out == nullptr || !aligned(k_pe, 4) || !aligned(k_out, 4) || k_pe_stride % 2 || k_out_stride % 2)
       return MLA_ERR_INVALID_ARG;
     if (num_tokens > 1 && (k_pe_stride < 0 || k_out_stride < kRopeCols)) return MLA_ERR_INVALID_ARG;
+    if (num_tokens > 1 && k_pe == k_out && k_pe_stride != k_out_stride) return MLA_ERR_INVALID_ARG;
     p.k_pe = k_pe;
     p.k_st = k_pe_stride;
     p.k_out = k_out;

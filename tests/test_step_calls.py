@@ -84,7 +84,7 @@ def _rope(lib, rope="default", pos=P, T=4, H=2, nope=P, nt=1024, nh=512, pe=P, p
     dict(rope=None), dict(T=-1), dict(H=-1), dict(pos=None), dict(pos=P + 2), dict(nope=None), dict(pe=None),
     dict(out=None), dict(nope=P + 8), dict(out=P + 8), dict(pe=P + 2), dict(nt=1028), dict(nh=516), dict(pt=129),
     dict(ph=65), dict(nt=-8), dict(dt=2), dict(qs=0.0), dict(qs=math.nan), dict(qs=math.inf), dict(qs=1e-45),
-    dict(k=P + 2), dict(ko=None), dict(ko=P + 2), dict(ks=65), dict(kos=62), dict(kos=65), dict(H=0, k=None)])
+    dict(k=P + 2), dict(ko=None), dict(ko=P + 2), dict(ks=65), dict(kos=62), dict(kos=65), dict(ks=128), dict(H=0, k=None)])
 def test_rope_refusals(lib, kw):
     assert _rope(lib, **kw) == B.MLA_ERR_INVALID_ARG
 

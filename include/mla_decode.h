@@ -500,20 +500,29 @@ MLA_API mla_status_t mla_decode_fwd_scaled(const mla_plan_t* plan, const void* q
  *   prefix_lens  [num_groups] int32: tokens that all requests of a group have in common
  *                from position 0 on; whole blocks of them, prefix_lens[g] / block_size,
  *                are shared: the first cells of the table rows of the group's requests
- *                (those that take part) must be equal there, or hold equal blocks
+ *                (those that take part) must be equal there, or hold equal blocks.
+ *                (With kv_scales, keys of a negative cell are skipped, as there;
+ *                without, the cells of visible keys must name blocks.)
  *   group_indptr [num_groups + 1] int32, nondecreasing: group g has requests
  *                [group_indptr[g], group_indptr[g + 1]); NULL with one group: all
- *                requests. Requests of no group share nothing.
+ *                requests. Requests of no group share nothing, and where an entry is
+ *                below the one before it no request does.
  * A request takes part in its group's prefix when every one of its tokens sees all of it:
  * seq_lens[r] - qlen_r >= the shared keys. Others (padding with shorter
  * lengths among them) and the only participant of a group are decoded on their own, right
  * for any lengths. The rows of every token in a group are computed over its
  * prefix, so that padding is better kept behind the last group.
  * Prefixes are shared for e4m3 with a block size that is a multiple of 16, and bf16 with
- * a multiple of 64; other plans, and plans that ask for a kernel or a number of
- * segments, run as mla_decode_fwd(_scaled). Sparse lists have no prefix.
- * Groups whose prefixes are shorter than a few hundred keys gain little: 4 requests
- * of 16 heads over 200 common keys take as long either way.
+ * a multiple of 64; other plans, plans that ask for a kernel or a number of segments, and
+ * plans with max_seq_len < 768 run as mla_decode_fwd(_scaled), prefix_lens and group_indptr
+ * unread. Sparse lists have no prefix. A prefix is shared where that saves work: the
+ * 128-row tiles that its participants have fewer in common, times the prefix's 128-key
+ * groups, have to be at least 6 times the tiles that they have on their own (each of which
+ * is merged with a partial more). So requests that fill their tiles alone (128 heads, or 16
+ * heads of 8 tokens) share nothing: their common keys come from L2.
+ * e4m3: a weight (times its key's scale) enters the product rounded to 7 bits or more down to 2^-7
+ * of the row's largest, to 3 or more down to 2^-18, and is off by 2^-21 of the largest at
+ * most where it is smaller still.
  * Three launches on `stream` (list, decode, merge).
  *
  * mla_decode_shared_plan -- the plan of such calls for up to num_groups groups; host only,

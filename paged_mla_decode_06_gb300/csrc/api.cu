@@ -814,7 +814,6 @@ mla_status_t mla_decode_fwd_shared(const mla_shared_plan_t* plan, const void* q,
   x.cols = p.max_blocks_per_req;
   x.workers = plan->workers;
   x.tiles_max = plan->unit_tiles;
-  x.ptiles_max = plan->prefix_tiles;
   x.max_items = plan->max_items;
   x.items = reinterpret_cast<int32_t*>(ws + l.items);
   x.n_items = reinterpret_cast<int32_t*>(ws + l.n_items);

@@ -303,7 +303,7 @@ struct PrefixParams {
   const int32_t* prefix_lens;    // [G]
   const int32_t* group_indptr;   // [G+1] requests, or null (one group of all)
   int32_t num_reqs, num_groups, num_tokens, num_heads, block_size, cols;
-  int32_t workers, tiles_max, ptiles_max, max_items;
+  int32_t workers, tiles_max, max_items;
   int32_t* items;                // [max_items, 8]
   int32_t* n_items;
   int32_t* worker_first;         // [workers + 1]: first item of each worker (at most 511 of them); null: longest first
@@ -312,7 +312,7 @@ struct PrefixParams {
   int32_t* groups;               // [G, 4]: first request, shared keys, first token, first prefix tile
   int32_t* group_pos;            // [G]: its tiles' place in the sequence
   int32_t* req_pos;              // [2 R]: the same of each request's own tiles, and their first items
-  int32_t* prefix_tab;           // [ptiles_max, 2]: first partial row, pieces
+  int32_t* prefix_tab;           // [prefix tiles, 2]: first partial row, pieces
   const float* segm_out;         // [rows, 512]
   const float* segm_max;
   const float* segm_expsum;

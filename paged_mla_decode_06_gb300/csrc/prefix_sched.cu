@@ -36,9 +36,9 @@ constexpr int kThreads = 512;
 constexpr int kGroupKeys = 128;
 constexpr int kTileRows = 128;
 constexpr int kBins = 512;
-constexpr int kCache = 256;      // groups and
-constexpr int kCacheReqs = 1024; // requests that are kept in shared memory
-constexpr int kItemCost = 4;      // of a worker's item: its start and its output, in groups
+constexpr int kCache = 256;       // groups and
+constexpr int kCacheReqs = 1024;  // requests that are kept in shared memory
+constexpr int kItemCost = 4;     // of a worker's item: its start and its output, in groups
 constexpr int kMinShare = 4;     // groups: pieces of less cost more than they save
 constexpr int kLeastCut = 6, kLeastEnd = 2;  // of a worker's tile: groups to be cut at all, and on either side of a cut
 
@@ -109,7 +109,8 @@ __device__ __forceinline__ int groups_of(int keys) { return keys > 0 ? keys / kG
 
 // Where a tile may be cut: at the multiples of W in its part of the sequence.
 struct Cutter {
-  int W, cost, least, d;  // shares; length of an item besides its groups; groups of a tile that may be cut; of its ends that may not
+  int W, cost;   // shares; length of an item besides its groups
+  int least, d;  // groups of a tile that may be cut; of its ends that may not
   // the first cut, as a multiple of W, of the tile of g groups at place a; and their number
   __device__ __forceinline__ int first(int a) const { return (a + cost + d + W - 1) / W; }
   __device__ __forceinline__ int count(int a, int g) const {
@@ -163,20 +164,25 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
   }
   if (SORTED) s.hist[tid] = 0;
+  bool falls = false;
 #pragma unroll 1
   for (int g = tid; g < G; g += kThreads) {
+    const int first = group_edge(p, g), end = group_edge(p, g + 1);
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
+    falls |= first > end;
+    if (G <= kCache) {
+      s.edge[g] = first;
+      s.edge[g + 1] = end;  // (the next thread's first)
+    }
     gr[g] = make_int4(INT32_MAX, whole * p.block_size, 0, 0);
   }
-  if (G <= kCache)
-#pragma unroll 1
-    for (int g = tid; g <= G; g += kThreads) s.edge[g] = group_edge(p, g);
-  __syncthreads();
+  // (groups that overlap would have more tiles than the workspace has room for)
+  const bool apart = __syncthreads_or(falls) == 0;
 #pragma unroll 1
   for (int r = tid; r < R; r += kThreads) {
     const int4 q = request(r);
     int g = last_at(G, r, edge);
-    const bool in = r >= edge(g) && r < edge(g + 1);
+    const bool in = apart && r >= edge(g) && r < edge(g + 1);
     const int keys = gr[g].y;
     if (in && keys > 0 && q.y > 0 && q.z - q.y >= keys) {
       atomicMin(&gr[g].x, r);

@@ -19,12 +19,19 @@
 //                            rows of P as two terms (hi e5m2, lo e4m3), and value
 //                            columns 256 j + 128 r .. + 127 of all 128 keys, read MN-major: 16
 //                            instructions of 64.3 cycles.
-// That is 1860 tensor cycles a chunk and pair. (The value-split kernel takes 2180,
-// having both SMs compute all scores, and 3100 to 3400 in all, bound by its
-// softmax of all 128 rows in either SM.) An instruction reads the same
+// That is 1860 tensor cycles a chunk and pair. An instruction reads the same
 // shared-memory offsets in both CTAs, so a CTA's own keys as B of Q K^T and its
 // columns as B of P V cannot share a copy: K and V have rings of their own, and
-// a chunk brings 52 KB of keys and values, 16 KB of them twice, into each SM.
+// a chunk brings 68 KB into each SM, 36 of keys and 32 of values.
+//
+// Measured: 2190 cycles a chunk where tiles follow one another: 68 of the 88 us that
+// the kernel takes for 64 requests over 8192 common keys at 128 heads (165 GFLOP, 62 chunks a
+// pair; 0.99 of the measured bf16 rate, half of the e4m3 one). What bounds it there is the
+// tensor pipe, 85 % busy, and a softmax of about 4400 cycles a chunk for each of its
+// two groups, which leaves no slack. The rest of the time is the start (6 us to the
+// first P V) and the items' ends (5 us each: the last P V, the output, the first scores of
+// the next). The value-split kernel, which computes all scores in both SMs and the
+// softmax of all 128 rows too, takes 3100 to 3400 cycles a chunk.
 //
 // The softmax works on chunks: one group of eight warps takes the even ones,
 // another the odd ones. TMEM lanes 0..63 hold the rows' scores of keys 0..63,
@@ -44,10 +51,11 @@
 // loaded without the other). Softmax warps arrive on rank 0's barriers, from
 // either CTA.
 //
-// Warps: 0 loads keys, 1 issues Q K^T (rank 1: passes keys on), 2 prepares the keys'
-// scales, 3 issues P V (passes values on), 4 and 5 load values, 6 watches the time, 8-23 softmax and
-// epilogue. Every wait is bounded: a timeout records a code in the status word, stops the CTA's
-// work, drains what was issued and exits.
+// Warps: 0 loads q and keys, 1 issues Q K^T (rank 1: passes keys on), 2 prepares the
+// keys' scales, 3 issues P V (passes values on), 4 and 5 load values, 6 watches the
+// time, 8-23 softmax and epilogue (7 has no work: registers move by four warps).
+// Every wait is bounded: a timeout records a code in the status word, stops
+// the CTA's work, drains what was issued and exits.
 #include <atomic>
 #include <climits>
 
@@ -89,6 +97,8 @@ constexpr uint32_t kTmemO = 0;            // 256 columns: 128 for each j
 constexpr uint32_t kTmemS = 256;          // [2] 64: S of chunk c at c % 2
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr uint32_t kSleepNs = 20000;
+// 2^kPBias is the weight of the reference, 2^(kPBias + kMove) the largest. (Of 0 to 4, which
+// move 11.75 to 7.75: 2 to 4 % of the time; 4 keeps 7 bits of a weight furthest down.)
 constexpr float kPBias = 4.f;
 constexpr float kMove = 7.75f;
 
@@ -100,8 +110,7 @@ enum : int {
   kPeerK = kVEmpty + kVRing,   // [kKRing] rank 0: rank 1's keys have landed
   kPeerV = kPeerK + kKRing,    // [kVRing] rank 0: rank 1's values
   kQFull = kPeerV + kVRing,    // this CTA's rows of q
-  // of chunk c, at c % 2:
-  kSFull,                      // [2] S written and key scales ready
+  kSFull,                      // [2] (of chunk c at c % 2, as the next four) S written and key scales ready
   kSFree = kSFull + 2,         // [2] rank 0: S read by both CTAs
   kPFull = kSFree + 2,         // [2] rank 0: P written by both CTAs, O_0 rescaled
   kOReady = kPFull + 2,        // [2] rank 0: O_1 rescaled
@@ -109,9 +118,10 @@ enum : int {
   kScFree = kX + 8,            // [2] key scales read
   kXL = kScFree + 2,           // [2] the eight warps of 32 rows have posted their sums of an item
   kOFree = kXL + 2,            // rank 0: both CTAs have read O of an item
-  kStage,                      // an item's output has left the value ring
-  kDrainQK,                    // Q K^T and P V complete, in both CTAs
+  kStage,                      // [2] the output of an item with keys, number m at m % 2, has left the value ring
+  kDrainQK = kStage + 2,       // Q K^T and P V complete, in both CTAs
   kDrainPV,
+  kDone,                       // all softmax warps have ended
   kNumBars
 };
 
@@ -131,7 +141,7 @@ constexpr int kOffV = kOffK + kKRing * kKSlot;
 constexpr int kSmem = kOffV + kVRing * kVSlot + 1024;  // + alignment slack
 static_assert(kNumBars * 8 <= kOffWatch && kOffLsum + 4096 <= kOffQ, "header space");
 static_assert(kSmem <= 232448, "shared memory budget");
-static_assert(kVRing * kVSlot >= kSoftWarps * 4096, "the epilogue stages in the value ring");
+static_assert(kVRing * kVSlot == kSoftWarps * 4096, "a group stages its output in the slots of its chunks");
 
 struct PairMaps {
   CUtensorMap q;     // q as [T*H rows, 576], box 128 bytes x 64 rows
@@ -163,6 +173,13 @@ struct Item {
   int tok0, tokens;
   int see0;              // keys that the first token of the unit sees; INT_MAX: all rows see all keys
 };
+// Whether one of the softmax's groups writes the output of an item that others follow, while
+// the other goes on: of many rows, whose stores take their time however many warps
+// make them (64 requests over 8192 common keys, 128 heads: 102.4 -> 99.7 us). Few rows are
+// done sooner by both (16 heads over 16384 common keys: 52.9 -> 51.1).
+__device__ __forceinline__ bool one_writes(const Item& it, int num_heads) {
+  return it.tokens * num_heads - it.row0 > kOwnRows;
+}
 // The same for the whole warp, and for the compiler: loops that it takes for
 // divergent keep the matrix instructions' descriptors in vector registers (250
 // cycles an instruction).
@@ -292,7 +309,6 @@ struct Watch {
   uint64_t ns;            // limit
   volatile int abort;
   volatile int progress;  // changes with every chunk of the softmax
-  int finished;           // softmax warps that have ended
 };
 __device__ __forceinline__ Watch* watch_of(const uint8_t* smem) {
   return reinterpret_cast<Watch*>(const_cast<uint8_t*>(smem) + kOffWatch);
@@ -314,13 +330,14 @@ __device__ __forceinline__ bool warp_wait(const Ctx& x, uint32_t bar, uint32_t p
 }
 // Warp 6: gives up, with a code in the status word, when the softmax has made no
 // progress for the limit. All other waits come to an end with the softmax's, or
-// are bounded by themselves (drain_wait).
+// are bounded by themselves (drain_wait). (It sleeps on the barrier that ends its
+// work: asleep on a timer it kept the CTA for 1 to 2 us more.)
 __device__ void watch(const Ctx& x) {
   Watch* w = watch_of(x.smem);
   int seen = -1;
   uint64_t t0 = 0;
   if (x.lane == 0) {
-    while (*static_cast<volatile int*>(&w->finished) < kSoftWarps && !w->abort) {
+    while (!mbar_try_wait_sleep(x.bar(kDone), 0, kSleepNs) && !w->abort) {
       const uint64_t now = global_timer_ns();
       if (w->progress != seen) {
         seen = w->progress;
@@ -329,7 +346,6 @@ __device__ void watch(const Ctx& x) {
         if (w->status != nullptr) atomicCAS(w->status, 0, 11);
         w->abort = 1;
       }
-      __nanosleep(1000);
     }
   }
   __syncwarp();
@@ -385,8 +401,9 @@ struct RowWindow {
 // own runs some hundred instructions in that time: with keys and values in one
 // warp a chunk took 2300 to 3500 cycles, with values and scales in one 4700. The
 // rings run on across items: q and the first keys of the next one load while this
-// one's last chunks and its output are under way; its values wait for the output, which
-// is staged in their ring.
+// one's last chunks and its output are under way, and so do the values of its first
+// chunk; those of the second wait for the output, which is staged in the slots of this one's
+// last chunk.
 template <int BOX>
 __device__ void load_keys(const Ctx& x, const PairMaps& maps, const DecodeParams& p) {
   constexpr int kSub = kHalf / BOX;  // boxes high of 64 rows
@@ -435,14 +452,19 @@ __device__ void load_values(const Ctx& x, const PairMaps& maps, const DecodePara
   const int run = x.lane % kRuns;
   const uint32_t to0 = smem_u32(x.smem) + kOffV + run * BOX * 128;
   RowWindow<BOX> w;
-  int c = 0;  // chunks so far
+  int c = 0, m = 0;   // chunks, items with keys so far
+  bool half = false;  // the last one's output takes half of the ring
   for (int i = x.first; i < x.last; ++i) {
     const Item it = item_at(p, i);
-    if (it.n > 0) w.start(x, p, it);
-    // (the outputs in turn, those of empty items too: no phase is passed over)
-    if (i > x.first && !warp_wait(x, x.bar(kStage), (i - 1 - x.first) & 1)) return;
+    if (it.n == 0) continue;
+    w.start(x, p, it);
     for (int k = 0; k < it.n; ++k, ++c) {
       const int v = 2 * c + j, s = v % kVRing;
+      // The output one item back is staged in all slots or in those of its last chunk, which
+      // are the second one's here; the one before may have been in the first one's. (The
+      // barriers' next phases wait for this item's values: none is passed over.)
+      const int out = k == 0 && half ? m - 2 : m - 1;
+      if (k < 2 && out >= 0 && !warp_wait(x, x.bar(kStage + (out & 1)), (out >> 1) & 1)) return;
       w.at(x, p, it, k);
       const int row = w.row(k, run);
       if (v >= kVRing && !warp_wait(x, x.bar(kVEmpty + s), (v / kVRing - 1) & 1)) return;
@@ -454,6 +476,8 @@ __device__ void load_values(const Ctx& x, const PairMaps& maps, const DecodePara
       if (x.lane < kRuns) tma_load_2d(to0 + s * kVSlot, &maps.kv, 128 * (2 * j + x.rank), row, x.bar(kVFull + s));
       __syncwarp();
     }
+    ++m;
+    half = one_writes(it, p.num_heads);
   }
 }
 
@@ -544,28 +568,28 @@ __device__ void qk_issue(const Ctx& x, const DecodeParams& p) {
   bool ok = true;
   int c = 0, q = 0;  // chunks, q's so far
   for (int i = x.first; i < x.last && ok; ++i) {
-   const int n = item_at(p, i).n;
-   if (n > 0) ok = warp_wait(x, x.bar(kQFull), q++ & 1);
-   for (const int end = c + n; c < end && ok; ++c) {
-    const int b = c & 1, s = c % kKRing;
-    ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1) &&
-         warp_wait(x, x.bar(kPeerK + s), (c / kKRing) & 1) &&
-         (c < 2 || warp_wait(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1));
-    if (!ok) break;
-    fence_after_sync();
-    const uint32_t at = (s * kKSlot) >> 4;
-    const uint32_t d = x.tbase + kTmemS + 64u * b;
-    if (one) {
+    const int n = item_at(p, i).n;
+    if (n > 0) ok = warp_wait(x, x.bar(kQFull), q++ & 1);
+    for (const int end = c + n; c < end && ok; ++c) {
+      const int b = c & 1, s = c % kKRing;
+      ok = warp_wait(x, x.bar(kKFull + s), (c / kKRing) & 1) &&
+           warp_wait(x, x.bar(kPeerK + s), (c / kKRing) & 1) &&
+           (c < 2 || warp_wait(x, x.bar(kSFree + b), ((c >> 1) - 1) & 1));
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t at = (s * kKSlot) >> 4;
+      const uint32_t d = x.tbase + kTmemS + 64u * b;
+      if (one) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_box(d, lo(q_desc) + (i * kBox >> 4), hi(q_desc), lo(k_desc) + at + (i * kBox >> 4), hi(k_desc), kId,
-                i != 0 ? 1u : 0u);
-      mma_rope(d, lo(qr_desc), hi(qr_desc), lo(kr_desc) + at, hi(kr_desc), kId);
-      pair_commit(x.bar(kSFull + b));
-      pair_commit(x.bar(kKEmpty + s));
+        for (int i = 0; i < 4; ++i)
+          mma_box(d, lo(q_desc) + (i * kBox >> 4), hi(q_desc), lo(k_desc) + at + (i * kBox >> 4), hi(k_desc), kId,
+                  i != 0 ? 1u : 0u);
+        mma_rope(d, lo(qr_desc), hi(qr_desc), lo(kr_desc) + at, hi(kr_desc), kId);
+        pair_commit(x.bar(kSFull + b));
+        pair_commit(x.bar(kKEmpty + s));
+      }
+      __syncwarp();
     }
-    __syncwarp();
-   }
   }
   if (one) {
     pair_commit(x.bar(kDrainQK));
@@ -586,29 +610,29 @@ __device__ void pv_issue(const Ctx& x, const DecodeParams& p) {
   bool ok = true;
   int g = 0, outs = 0;  // boxes, outputs with keys so far
   for (int i = x.first; i < x.last && ok; ++i) {
-   const int n = item_at(p, i).n;
-   // O of the item before has been read
-   if (n > 0 && outs++ > 0) ok = warp_wait(x, x.bar(kOFree), outs & 1);
-   const int begin = g;
-   for (const int end = g + 2 * n; g < end && ok; ++g) {
-    const int j = g & 1, c = g >> 1, b = c & 1, s = g % kVRing;
-    ok = warp_wait(x, x.bar((j == 0 ? kPFull : kOReady) + b), (c >> 1) & 1) &&
-         warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1) &&
-         warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1);
-    if (!ok) break;
-    fence_after_sync();
-    const uint32_t vb = lo(v_desc) + ((s * kVSlot) >> 4), pb = lo(p_desc) + ((b * 2 * kPTile) >> 4);
-    const uint32_t d = x.tbase + kTmemO + 128u * j;
-    const uint32_t more = g - begin > 1 ? 1u : 0u;
-    if (one) {
+    const int n = item_at(p, i).n;
+    // O of the item before has been read
+    if (n > 0 && outs++ > 0) ok = warp_wait(x, x.bar(kOFree), outs & 1);
+    const int begin = g;
+    for (const int end = g + 2 * n; g < end && ok; ++g) {
+      const int j = g & 1, c = g >> 1, b = c & 1, s = g % kVRing;
+      ok = warp_wait(x, x.bar((j == 0 ? kPFull : kOReady) + b), (c >> 1) & 1) &&
+           warp_wait(x, x.bar(kVFull + s), (g / kVRing) & 1) &&
+           warp_wait(x, x.bar(kPeerV + s), (g / kVRing) & 1);
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t vb = lo(v_desc) + ((s * kVSlot) >> 4), pb = lo(p_desc) + ((b * 2 * kPTile) >> 4);
+      const uint32_t d = x.tbase + kTmemO + 128u * j;
+      const uint32_t more = g - begin > 1 ? 1u : 0u;
+      if (one) {
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 32; ++ks)
-        mma_terms(d, pb + (ks * 32 >> 4), hi(p_desc), vb + (ks * 32 * 128 >> 4), hi(v_desc), kIdHi, kIdLo,
-                  ks != 0 ? 1u : more);
-      pair_commit(x.bar(kVEmpty + s));
+        for (int ks = 0; ks < kKeys / 32; ++ks)
+          mma_terms(d, pb + (ks * 32 >> 4), hi(p_desc), vb + (ks * 32 * 128 >> 4), hi(v_desc), kIdHi, kIdLo,
+                    ks != 0 ? 1u : more);
+        pair_commit(x.bar(kVEmpty + s));
+      }
+      __syncwarp();
     }
-    __syncwarp();
-   }
   }
   if (one) {
     pair_commit(x.bar(kDrainPV));
@@ -661,7 +685,6 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
   const int h = sw >> 3;                   // chunks c with c % 2 == h, and buffer
   const int kh = (sw >> 2) & 1;            // its 32 keys of the half
   const int part = 2 * kq + kh;            // key quarter (and, of a rescaling, columns of O_kh)
-  const int cq = sw >> 2;                  // quarter of the TMEM columns of O at the end
   const int r = rq * 32 + lane;            // row within the CTA
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const int H = p.num_heads;
@@ -677,319 +700,340 @@ __device__ void softmax_rows(const Ctx& x, const PairMaps& maps, const DecodePar
     return warp_wait(x, x.bar(kVEmpty + g % kVRing), (g / kVRing) & 1);
   };
   int first = 0;  // chunks (of all items) before this item's: buffers and phases run on
+  int m = 0;      // items with keys so far
   for (int i = x.first; i < x.last; ++i) {
-  const Item it = item_at(p, i);
-  const int n = it.n, end = first + n;
-  const int rows_total = it.tokens * H;
-  const int rho = it.row0 + kOwnRows * x.rank + r;  // row within the unit
-  const bool row_ok = rho < rows_total;
-  const int token = rho / H;
-  const int vis = !row_ok ? 0 : (it.see0 == INT_MAX ? INT_MAX : it.see0 + token);
-  // keys from here on (of chunk 0 of all items' chunks) are not seen by all rows
-  const int start = it.seg_start - first * kKeys;
-  const int all_see = it.see0 == INT_MAX ? INT_MAX : it.see0 + it.row0 / H - start;
-  float ref = -INFINITY, l = 0.f;
-  auto follow = [&](float mx) {
-    if (!(mx > ref + kMove)) return 1.f;  // (moves also when a row's first visible key arrives)
-    const float a = ref == -INFINITY ? 1.f : fast_exp2(ref - mx);
-    ref = mx;
-    l *= a;
-    return a;
-  };
-  auto row_max = [&](int c) {
-    const float* xm = xmax + (c & 3) * 4 * kOwnRows;
-    return fmaxf(fmaxf(xm[0], xm[kOwnRows]), fmaxf(xm[2 * kOwnRows], xm[3 * kOwnRows]));
-  };
-  // the maximum of chunk c, which the other group posted. A group looks at it
-  // before it posts its own of c + 3, which the other waits for before it posts
-  // that of c + 4: neither the barrier's phase nor the four buffers are passed over.
-  auto follow_other = [&](int c) {
-    if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1)) return false;
-    follow(row_max(c));
-    return true;
-  };
-  for (int c = first + ((first & 1) ^ h); c < end; c += 2) {
-    const int ph = (c >> 1) & 1;
-    ok = warp_wait(x, x.bar(kSFull + h), ph);
-    if (!ok) break;
-    if (sw == 0 || sw == 8) watch_of(x.smem)->progress = c;
-    fence_after_sync();
-    float s[kPart];
-    {
-      uint32_t sr[kPart];
-      tmem_ld_32x32b_x32(ts, sr);
-      tmem_ld_wait();
+    const Item it = item_at(p, i);
+    const int n = it.n, end = first + n;
+    const int rows_total = it.tokens * H;
+    const int rho = it.row0 + kOwnRows * x.rank + r;  // row within the unit
+    const bool row_ok = rho < rows_total;
+    const int token = rho / H;
+    const int vis = !row_ok ? 0 : (it.see0 == INT_MAX ? INT_MAX : it.see0 + token);
+    // keys from here on (of chunk 0 of all items' chunks) are not seen by all rows
+    const int start = it.seg_start - first * kKeys;
+    const int all_see = it.see0 == INT_MAX ? INT_MAX : it.see0 + it.row0 / H - start;
+    float ref = -INFINITY, l = 0.f;
+    auto follow = [&](float mx) {
+      if (!(mx > ref + kMove)) return 1.f;  // (moves also when a row's first visible key arrives)
+      const float a = ref == -INFINITY ? 1.f : fast_exp2(ref - mx);
+      ref = mx;
+      l *= a;
+      return a;
+    };
+    auto row_max = [&](int c) {
+      const float* xm = xmax + (c & 3) * 4 * kOwnRows;
+      return fmaxf(fmaxf(xm[0], xm[kOwnRows]), fmaxf(xm[2 * kOwnRows], xm[3 * kOwnRows]));
+    };
+    // the maximum of chunk c, which the other group posted. A group looks at it
+    // before it posts its own of c + 3, which the other waits for before it posts
+    // that of c + 4: neither the barrier's phase nor the four buffers are passed over.
+    auto follow_other = [&](int c) {
+      if (!warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1)) return false;
+      follow(row_max(c));
+      return true;
+    };
+    for (int c = first + ((first & 1) ^ h); c < end; c += 2) {
+      const int ph = (c >> 1) & 1;
+      ok = warp_wait(x, x.bar(kSFull + h), ph);
+      if (!ok) break;
+      if (sw == 0 || sw == 8) watch_of(x.smem)->progress = c;
+      fence_after_sync();
+      float s[kPart];
+      {
+        uint32_t sr[kPart];
+        tmem_ld_32x32b_x32(ts, sr);
+        tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < kPart; ++j) s[j] = __uint_as_float(sr[j]);
-    }
-    fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_remote(x.lead(kSFree + h));  // Q K^T two chunks on may overwrite it
-    const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + h * 3 * kKeys + kPart * part;
-    const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * h + part];
-    if constexpr (SCALE == Scale::kKey) {
-#pragma unroll
-      for (int j = 0; j < kPart; j += 4) {
-        const float4 mu = *reinterpret_cast<const float4*>(ks + j);
-        const float4 ad = *reinterpret_cast<const float4*>(ks + kKeys + j);
-        const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(mu.x, mu.y), make_float2(ad.x, ad.y));
-        const float2 b = fma2(make_float2(s[j + 2], s[j + 3]), make_float2(mu.z, mu.w), make_float2(ad.z, ad.w));
-        s[j] = a.x;
-        s[j + 1] = a.y;
-        s[j + 2] = b.x;
-        s[j + 3] = b.y;
+        for (int j = 0; j < kPart; ++j) s[j] = __uint_as_float(sr[j]);
       }
-    }
-    // keys that exist and that the row may see
-    const int lim = min(vis, it.seg_end) - (start + c * kKeys + kPart * part);
-    if (lim < kPart || kmask != 0xffffffffu) {
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(x.lead(kSFree + h));  // Q K^T two chunks on may overwrite it
+      const float* ks = reinterpret_cast<const float*>(x.smem + kOffScale) + h * 3 * kKeys + kPart * part;
+      const uint32_t kmask = reinterpret_cast<const uint32_t*>(x.smem + kOffMask)[4 * h + part];
+      if constexpr (SCALE == Scale::kKey) {
 #pragma unroll
-      for (int j = 0; j < kPart; ++j)
-        if (!(j < lim && ((kmask >> j) & 1u))) s[j] = -INFINITY;
-    }
-    float m[2];  // of either half of the keys
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* e = s + kUni * i;
-      m[i] = fmaxf(max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), max3(e[6], e[7], e[8])),
-                   max3(max3(e[9], e[10], e[11]), max3(e[12], e[13], e[14]), e[15]));
-      if constexpr (UNI) m[i] = fmaf(m[i], ks[kUni * i], ks[kKeys + kUni * i]);  // (mul > 0; -inf stays)
-      if constexpr (ONE) m[i] *= p.score_scale_log2;
-    }
-    // the row's maximum over all key quarters; the previous chunk's before it
-    xmax[((c & 3) * 4 + part) * kOwnRows] = fmaxf(m[0], m[1]);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kX + 2 * (c & 3) + rq));
-    ok = c == first || follow_other(c - 1);
-    if (!ok) break;
-    ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1);
-    if (!ok) break;
-    const float alpha = follow(row_max(c));
-    // p as hi + lo terms, 16 keys to a 16-byte chunk of each tile
-    const float base = ref == -INFINITY ? 0.f : ref - kPBias;
-    float psum = 0.f;
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float mu = UNI ? ks[kUni * i] : ONE ? p.score_scale_log2 : 1.f;
-      const float sh = UNI ? ks[kKeys + kUni * i] - base : -base;
-      const float2 mul2 = make_float2(mu, mu), shift2 = make_float2(sh, sh);
-      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int j = 4 * i; j < 4 * i + 4; ++j) {
-        const int e = 4 * j;
-        float2 a = make_float2(s[e], s[e + 1]), b = make_float2(s[e + 2], s[e + 3]);
-        a = UNI || ONE ? fma2(a, mul2, shift2) : add2(a, shift2);
-        b = UNI || ONE ? fma2(b, mul2, shift2) : add2(b, shift2);
-        a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-        b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
-        if constexpr (UNI || ONE) {
-          ps[0] = add2(ps[0], a);
-          ps[1] = add2(ps[1], b);
-        } else {
-          const float4 iv = *reinterpret_cast<const float4*>(ks + 2 * kKeys + e);
-          ps[0] = fma2(a, make_float2(iv.x, iv.y), ps[0]);
-          ps[1] = fma2(b, make_float2(iv.z, iv.w), ps[1]);
+        for (int j = 0; j < kPart; j += 4) {
+          const float4 mu = *reinterpret_cast<const float4*>(ks + j);
+          const float4 ad = *reinterpret_cast<const float4*>(ks + kKeys + j);
+          const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(mu.x, mu.y), make_float2(ad.x, ad.y));
+          const float2 b = fma2(make_float2(s[j + 2], s[j + 3]), make_float2(mu.z, mu.w), make_float2(ad.z, ad.w));
+          s[j] = a.x;
+          s[j + 1] = a.y;
+          s[j + 2] = b.x;
+          s[j + 3] = b.y;
         }
-        split4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
       }
-      const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-      psum = UNI ? fmaf(sum, ks[2 * kKeys + kUni * i], psum) : psum + sum;
-    }
-    l += psum;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(x.bar(kScFree + h));
-    // P V two chunks back has read this buffer of P
-    ok = c < 2 || pv_done(c - 2, 1);
-    if (!ok) break;
-    *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-    *reinterpret_cast<uint4*>(prow + kPTile + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(prow + kPTile + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-    // Value rows of keys that do not exist (cache rows past the sequence) are
-    // zeroed, and of keys that some rows of the tile do not see the NaNs: neither
-    // may reach O through p = 0. Each warp sees to the 32 keys of its quarter, a
-    // half of them by each of its two row halves.
-    if (kmask != 0xffffffffu || all_see < c * kKeys + kPart * (part + 1)) {
+      // keys that exist and that the row may see
+      const int lim = min(vis, it.seg_end) - (start + c * kKeys + kPart * part);
+      if (lim < kPart || kmask != 0xffffffffu) {
+#pragma unroll
+        for (int j = 0; j < kPart; ++j)
+          if (!(j < lim && ((kmask >> j) & 1u))) s[j] = -INFINITY;
+      }
+      float m[2];  // of either half of the keys
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* e = s + kUni * i;
+        m[i] = fmaxf(max3(max3(e[0], e[1], e[2]), max3(e[3], e[4], e[5]), max3(e[6], e[7], e[8])),
+                     max3(max3(e[9], e[10], e[11]), max3(e[12], e[13], e[14]), e[15]));
+        if constexpr (UNI) m[i] = fmaf(m[i], ks[kUni * i], ks[kKeys + kUni * i]);  // (mul > 0; -inf stays)
+        if constexpr (ONE) m[i] *= p.score_scale_log2;
+      }
+      // the row's maximum over all key quarters; the previous chunk's before it
+      xmax[((c & 3) * 4 + part) * kOwnRows] = fmaxf(m[0], m[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.bar(kX + 2 * (c & 3) + rq));
+      ok = c == first || follow_other(c - 1);
+      if (!ok) break;
+      ok = warp_wait(x, x.bar(kX + 2 * (c & 3) + rq), (c >> 2) & 1);
+      if (!ok) break;
+      const float alpha = follow(row_max(c));
+      // p as hi + lo terms, 16 keys to a 16-byte chunk of each tile
+      const float base = ref == -INFINITY ? 0.f : ref - kPBias;
+      float psum = 0.f;
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mu = UNI ? ks[kUni * i] : ONE ? p.score_scale_log2 : 1.f;
+        const float sh = UNI ? ks[kKeys + kUni * i] - base : -base;
+        const float2 mul2 = make_float2(mu, mu), shift2 = make_float2(sh, sh);
+        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int j = 4 * i; j < 4 * i + 4; ++j) {
+          const int e = 4 * j;
+          float2 a = make_float2(s[e], s[e + 1]), b = make_float2(s[e + 2], s[e + 3]);
+          a = UNI || ONE ? fma2(a, mul2, shift2) : add2(a, shift2);
+          b = UNI || ONE ? fma2(b, mul2, shift2) : add2(b, shift2);
+          a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+          b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
+          if constexpr (UNI || ONE) {
+            ps[0] = add2(ps[0], a);
+            ps[1] = add2(ps[1], b);
+          } else {
+            const float4 iv = *reinterpret_cast<const float4*>(ks + 2 * kKeys + e);
+            ps[0] = fma2(a, make_float2(iv.x, iv.y), ps[0]);
+            ps[1] = fma2(b, make_float2(iv.z, iv.w), ps[1]);
+          }
+          split4(a.x, a.y, b.x, b.y, hi[j], lo[j]);
+        }
+        const float sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+        psum = UNI ? fmaf(sum, ks[2 * kKeys + kUni * i], psum) : psum + sum;
+      }
+      l += psum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x.bar(kScFree + h));
+      // P V two chunks back has read this buffer of P
+      ok = c < 2 || pv_done(c - 2, 1);
+      if (!ok) break;
+      *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(prow + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      *reinterpret_cast<uint4*>(prow + kPTile + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(prow + kPTile + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      // Value rows of keys that do not exist (cache rows past the sequence) are
+      // zeroed, and of keys that some rows of the tile do not see the NaNs: neither
+      // may reach O through p = 0. Each warp sees to the 32 keys of its quarter, a
+      // half of them by each of its two row halves.
+      if (kmask != 0xffffffffu || all_see < c * kKeys + kPart * (part + 1)) {
 #pragma unroll 1
-      for (int j = 0; j < 2 && ok; ++j) {
-        const int g = 2 * c + j;
-        ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1);  // (its writes are seen here too)
-        uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + kPart * part * 128 + (lane & 7) * 16;
-        for (int i = rq + 2 * (lane >> 3); ok && i < kPart; i += 8) {
-          uint4* at = reinterpret_cast<uint4*>(box + i * 128);
-          if (!((kmask >> i) & 1u)) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-          } else if (c * kKeys + kPart * part + i >= all_see) {
-            const uint4 v = *at;
-            *at = make_uint4(e4m3x4_without_nan(v.x), e4m3x4_without_nan(v.y), e4m3x4_without_nan(v.z),
-                             e4m3x4_without_nan(v.w));
+        for (int j = 0; j < 2 && ok; ++j) {
+          const int g = 2 * c + j;
+          ok = warp_wait(x, x.bar(kVFull + g % kVRing), (g / kVRing) & 1);  // (its writes are seen here too)
+          uint8_t* box = x.smem + kOffV + g % kVRing * kVSlot + kPart * part * 128 + (lane & 7) * 16;
+          for (int i = rq + 2 * (lane >> 3); ok && i < kPart; i += 8) {
+            uint4* at = reinterpret_cast<uint4*>(box + i * 128);
+            if (!((kmask >> i) & 1u)) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else if (c * kKeys + kPart * part + i >= all_see) {
+              const uint4 v = *at;
+              *at = make_uint4(e4m3x4_without_nan(v.x), e4m3x4_without_nan(v.y), e4m3x4_without_nan(v.z),
+                               e4m3x4_without_nan(v.w));
+            }
+          }
+        }
+        if (!ok) break;
+      }
+      fence_proxy_async_smem();
+      const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
+      if (kh == 1 && lane == 0) mbar_arrive_remote(x.lead(kPFull + h));  // (P alone)
+      if (moved) {
+        // some rows moved their reference: once P V of the previous chunk into O_kh
+        // is complete, this warp rescales its lanes' rows there
+        ok = pv_done(c - 1, kh);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * kh + 64 * k;
+          uint32_t o[32], o2[32];
+          tmem_ld_32x32b_x32(ta, o);
+          tmem_ld_32x32b_x32(ta + 32, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            o2[i] = __float_as_uint(__uint_as_float(o2[i]) * alpha);
+          }
+          tmem_st_32x32b_x32(ta, o);
+          tmem_st_32x32b_x32(ta + 32, o2);
+        }
+        tmem_st_wait();
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(x.lead((kh == 0 ? kPFull : kOReady) + h));
+    }
+
+    if (!ok) break;
+    // ---------------------------------------------------------------- epilogue
+    // The group of the last chunk writes the output, while the other goes on to
+    // the next item's first chunk, which is its own: P V over that waits for O alone.
+    // After the last item, and of few rows, both write.
+    const bool mine = h == ((end - 1) & 1), both = i + 1 == x.last || !one_writes(it, H);
+    if (n > 0 && !mine) ok = follow_other(end - 1);
+    // (all sums of the item before are there: no arrival counts for another's phase)
+    if (ok && i > x.first) ok = warp_wait(x, x.bar(kXL + rq), (i - 1 - x.first) & 1);
+    if (!ok) break;
+    float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum) + ((i - x.first) & 1) * 8 * kOwnRows + r;
+    lsum[(4 * h + part) * kOwnRows] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(x.bar(kXL + rq));
+    first = end;
+    m += n > 0 ? 1 : 0;
+    if (!mine && !both) continue;
+    ok = warp_wait(x, x.bar(kXL + rq), (i - x.first) & 1);
+    // O is complete with the last chunk
+    if (ok && n > 0) ok = pv_done(end - 1, 1);
+    if (!ok) break;
+    fence_after_sync();
+    const bool fin = it.pslot < 0;
+    float mult = 0.f;
+    if (row_ok) {
+      float L = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) L += lsum[k * kOwnRows];
+      const float base = ref == -INFINITY ? 0.f : ref - kPBias;  // the reference of O and the sum
+      const int head = rho - token * H;
+      const int64_t th = static_cast<int64_t>(it.tok0) * H + rho;
+      const bool writes = mine && kq == 0 && kh == 0;
+      if (fin) {
+        float lse = -INFINITY;
+        if (p.sinks != nullptr) {
+          const float s2 = p.sinks[head] * kLog2e;
+          const float M = fmaxf(L > 0.f ? base : -INFINITY, s2);
+          const float e = L > 0.f ? exp2f(base - M) : 0.f;
+          const float W = L * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));  // (-inf: no sink; NaN stays)
+          if (W != 0.f) {
+            mult = e / W;
+            lse = kLn2 * (M + log2f(W));
+          }
+        } else if (L != 0.f) {
+          mult = 1.f / L;
+          lse = kLn2 * (base + log2f(L));
+        }
+        if (writes) p.lse[th] = lse;
+      } else {
+        mult = L != 0.f ? 1.f / L : 0.f;
+        if (writes) {
+          const int64_t at = static_cast<int64_t>(it.pslot) + kOwnRows * x.rank + r;
+          const float2 ms = partial_sums(L > 0.f ? base : -INFINITY, L);
+          p.segm_max[at] = ms.x;
+          p.segm_expsum[at] = ms.y;
+        }
+      }
+      mult *= p.kv_scale;
+    }
+    // Each warp scales its 32 rows of 64 columns (of 128, where one group writes) and
+    // stages them, 128 bytes of each row at a time, in the 128-byte swizzle, in its
+    // 4 KB of the value ring (its group's half, the slots of the last chunk, which P V has
+    // read and whose next values wait for kStage), and one TMA tensor store writes each
+    // staged tile. Where some of the 32 rows do not exist the warp stores the others, four at
+    // a time (a row by each lane: 1400 cycles a tile of 16), and the zeros of an
+    // item without keys, which has no slots. (TMEM loads are warp-collective.)
+    const int wr = it.row0 + kOwnRows * x.rank + 32 * rq;  // the warp's first row within the unit
+    if (wr < rows_total) {
+      const bool whole = n > 0 && wr + 32 <= rows_total;
+      const int z0 = fin ? it.tok0 * H + wr : it.pslot + (wr - it.row0);
+      const CUtensorMap* map = fin ? &maps.out : &maps.part;
+      uint8_t* buf = x.smem + kOffV + sw * 4096;
+      auto store = [&](const uint32_t (&w)[32], int col) {
+        if (n > 0) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          fence_proxy_async_smem();  // (for the store, and for the loads that come here next)
+        }
+        if (whole) {
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(map, smem_u32(buf), col, 0, z0);
+            bulk_commit_group();
+            bulk_wait_read<0>();
+          }
+        } else {
+          __syncwarp();
+          uint8_t* dst = (fin ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.segm_out)) +
+                         (static_cast<int64_t>(z0) * kRank + col) * (fin ? 2 : 4) + 16 * (lane & 7);
+          for (int i = lane >> 3; wr + i < min(rows_total, wr + 32); i += 4) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (n > 0) v = *reinterpret_cast<const uint4*>(buf + i * 128 + (((lane ^ i) & 7) << 4));
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i) * kRank * (fin ? 2 : 4)) = v;
+          }
+        }
+        __syncwarp();
+      };
+      auto load = [&](int at, uint32_t (&o)[32]) {
+        if (n > 0) {
+          tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + at, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+      };
+      // quarters of the TMEM columns of O
+      const int cq0 = both ? 2 * h + kh : 2 * kh, cq1 = cq0 + (both ? 1 : 2);
+#pragma unroll 1
+      for (int cq = cq0; cq < cq1; ++cq) {
+        const int col0 = 256 * (cq >> 1) + 128 * kq + 64 * (cq & 1);
+        if (fin) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            load(64 * cq + 32 * c, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * mult, __uint_as_float(o[2 * j + 1]) * mult);
+              w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          store(w, col0);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            load(64 * cq + 32 * c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mult);
+            store(o, col0 + 32 * c);
           }
         }
       }
-      if (!ok) break;
     }
-    fence_proxy_async_smem();
-    const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
-    if (kh == 1 && lane == 0) mbar_arrive_remote(x.lead(kPFull + h));  // (P alone)
-    if (moved) {
-      // some rows moved their reference: once P V of the previous chunk into O_kh
-      // is complete, this warp rescales its lanes' rows there
-      ok = pv_done(c - 1, kh);
-      if (!ok) break;
-      fence_after_sync();
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t ta = x.tbase + lane_off + kTmemO + 128 * kh + 64 * k;
-        uint32_t o[32], o2[32];
-        tmem_ld_32x32b_x32(ta, o);
-        tmem_ld_32x32b_x32(ta + 32, o2);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          o2[i] = __float_as_uint(__uint_as_float(o2[i]) * alpha);
-        }
-        tmem_st_32x32b_x32(ta, o);
-        tmem_st_32x32b_x32(ta + 32, o2);
-      }
-      tmem_st_wait();
-    }
+    // O has been read (of items with keys, whose next one replaces it), and the
+    // staged tiles too
     fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(x.lead((kh == 0 ? kPFull : kOReady) + h));
-  }
-
-  if (!ok) break;
-  // ---------------------------------------------------------------- epilogue
-  if (n > 0 && ((end - 1) & 1) != h) ok = follow_other(end - 1);  // the last one was the other group's
-  if (!ok) break;
-  float* lsum = reinterpret_cast<float*>(x.smem + kOffLsum) + ((i - x.first) & 1) * 8 * kOwnRows + r;
-  lsum[(4 * h + part) * kOwnRows] = l;
-  __syncwarp();
-  if (lane == 0) mbar_arrive(x.bar(kXL + rq));
-  ok = warp_wait(x, x.bar(kXL + rq), (i - x.first) & 1);
-  // O is complete with the last chunk
-  if (ok && n > 0) ok = pv_done(end - 1, 1);
-  if (!ok) break;
-  fence_after_sync();
-  const bool fin = it.pslot < 0;
-  float mult = 0.f;
-  if (row_ok) {
-    float L = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) L += lsum[k * kOwnRows];
-    const float base = ref == -INFINITY ? 0.f : ref - kPBias;  // the reference of O and the sum
-    const int head = rho - token * H;
-    const int64_t th = static_cast<int64_t>(it.tok0) * H + rho;
-    const bool writes = kq == 0 && cq == 0;
-    if (fin) {
-      float lse = -INFINITY;
-      if (p.sinks != nullptr) {
-        const float s2 = p.sinks[head] * kLog2e;
-        const float M = fmaxf(L > 0.f ? base : -INFINITY, s2);
-        const float e = L > 0.f ? exp2f(base - M) : 0.f;
-        const float W = L * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));  // (-inf: no sink; NaN stays)
-        if (W != 0.f) {
-          mult = e / W;
-          lse = kLn2 * (M + log2f(W));
-        }
-      } else if (L != 0.f) {
-        mult = 1.f / L;
-        lse = kLn2 * (base + log2f(L));
-      }
-      if (writes) p.lse[th] = lse;
-    } else {
-      mult = L != 0.f ? 1.f / L : 0.f;
-      if (writes) {
-        const int64_t at = static_cast<int64_t>(it.pslot) + kOwnRows * x.rank + r;
-        const float2 ms = partial_sums(L > 0.f ? base : -INFINITY, L);
-        p.segm_max[at] = ms.x;
-        p.segm_expsum[at] = ms.y;
-      }
-    }
-    mult *= p.kv_scale;
-  }
-  // Each warp scales its 32 rows x 64 columns and stages them, 128 bytes of
-  // each row at a time, in the 128-byte swizzle, in its 4 KB of the value ring
-  // (whose boxes P V has read, and whose next ones wait for kStage), and one TMA
-  // tensor store writes each staged tile; where some of the 32 rows do not exist
-  // each lane stores its row (of 16 rows, staged, 1700 cycles a tile). (TMEM loads
-  // are warp-collective.)
-  const int col0 = 256 * (cq >> 1) + 128 * kq + 64 * (cq & 1);
-  const int wr = it.row0 + kOwnRows * x.rank + 32 * rq;  // the warp's first row within the unit
-  if (wr < rows_total) {
-    const bool whole = wr + 32 <= rows_total;
-    const int z0 = fin ? it.tok0 * H + wr : it.pslot + (wr - it.row0);
-    const CUtensorMap* map = fin ? &maps.out : &maps.part;
-    uint8_t* buf = x.smem + kOffV + sw * 4096;
-    auto store = [&](const uint32_t (&w)[32], int col) {
-      if (whole) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(map, smem_u32(buf), col, 0, z0);
-          bulk_commit_group();
-          bulk_wait_read<0>();
-        }
-        __syncwarp();
-      } else if (row_ok) {
-        const int64_t at = static_cast<int64_t>(z0 + lane) * kRank + col;
-        uint4* dst = reinterpret_cast<uint4*>(fin ? static_cast<uint8_t*>(p.out) + at * 2
-                                                  : reinterpret_cast<uint8_t*>(p.segm_out + at));
-#pragma unroll
-        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-      }
-    };
-    auto load = [&](int c, uint32_t (&o)[32]) {
-      if (n > 0) {
-        tmem_ld_32x32b_x32(x.tbase + lane_off + kTmemO + 64 * cq + 32 * c, o);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0u;
-      }
-    };
-    if (fin) {
-      uint32_t w[32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        load(c, o);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * mult, __uint_as_float(o[2 * j + 1]) * mult);
-          w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-      }
-      store(w, col0);
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        load(c, o);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * mult);
-        store(o, col0 + 32 * c);
-      }
+    if (lane == 0 && n > 0) {
+      const int count = both ? 1 : 2;
+      mbar_arrive_remote(x.lead(kOFree), count);
+      mbar_arrive(x.bar(kStage + ((m - 1) & 1)), count);
     }
   }
-  // O has been read (of items with keys, whose next one replaces it), and the
-  // staged tiles too
-  fence_before_sync();
   __syncwarp();
-  if (lane == 0) {
-    if (n > 0) mbar_arrive_remote(x.lead(kOFree));
-    mbar_arrive(x.bar(kStage));
-  }
-  first = end;
-  }
-  __syncwarp();
-  if (lane == 0) atomicAdd(&watch_of(x.smem)->finished, 1);
+  if (lane == 0) mbar_arrive(x.bar(kDone));
 }
 
 template <int BOX, Scale SCALE>
@@ -1014,7 +1058,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     w->ns = p.wait_ns != 0 ? p.wait_ns : kDefaultWaitNs;
     w->abort = 0;
     w->progress = 0;
-    w->finished = 0;
     reinterpret_cast<int*>(smem + kOffIssued)[0] = -1;
     reinterpret_cast<int*>(smem + kOffIssued)[1] = -1;
     reinterpret_cast<int*>(smem + kOffIssued)[2] = -1;
@@ -1037,12 +1080,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(x.bar(kOReady + i), kGroupWarps);
       mbar_init(x.bar(kScFree + i), kGroupWarps);
       mbar_init(x.bar(kXL + i), 8);
+      mbar_init(x.bar(kStage + i), kSoftWarps);
     }
     for (int i = 0; i < 8; ++i) mbar_init(x.bar(kX + i), 4);
-    mbar_init(x.bar(kOFree), 2 * kSoftWarps);
-    mbar_init(x.bar(kStage), kSoftWarps);
+    mbar_init(x.bar(kOFree), 2 * kSoftWarps);  // (one group's warps count twice)
     mbar_init(x.bar(kDrainQK), 1);
     mbar_init(x.bar(kDrainPV), 1);
+    mbar_init(x.bar(kDone), kSoftWarps);
     fence_barrier_init();
   }
   if (x.warp == 1) pair_alloc(smem_u32(tslot), kTmemCols);

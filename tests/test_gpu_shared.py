@@ -155,6 +155,8 @@ def expected(c):
     out, lse = np.zeros((T, H, 512)), np.full((T, H), -np.inf)
     to, tl = np.zeros_like(out), np.zeros_like(lse)
     for t, slots in enumerate(lists):
+        slots = np.asarray(slots, np.int64)
+        slots = slots[slots >= 0]
         kv = c["values"][slots]
         out[t], lse[t] = S.attend(c["q64"][t], kv, SCALE, c["sinks"])
         if not len(slots):
@@ -430,13 +432,166 @@ def test_bounded_wait_runs_out_and_is_reported(kind, heads):
     compare(c, named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy())
 
 
-def test_fork_then_decode_over_the_shared_pages():
+# ---- prefixes long enough, and read by enough requests, to be shared
+def shared_groups(c):
+    """Of each group, whether its prefix is computed once: the tiles that its participants
+    have fewer in common, times the prefix's groups of 128 keys, are at least 6 times theirs."""
+    qlens, found = np.diff(c["qo"]), []
+    tiles = lambda tokens: -(-int(tokens) * c["H"] // 128)
+    for p, a, b in zip(c["prefix"], c["edges"], c["edges"][1:]):
+        keys = int(p) // c["bs"] * c["bs"]
+        own = sum(tiles(qlens[r]) for r in range(a, b) if qlens[r] > 0 and c["lens"][r] - qlens[r] >= keys)
+        found.append(keys > 0 and own > 0 and (own - tiles(qlens[a:b].sum())) * -(-keys // 128) >= 6 * own)
+    return found
+
+
+@pytest.mark.parametrize("kind,bs,g,heads", [(*k, h) for k in KINDS for h in (7, 64)]
+                         + [(*k, h) for k in (KINDS[0], KINDS[1], KINDS[-2]) for h in (1, 16, 33)])
+def test_shared_tiles_of_many_requests(kind, bs, g, heads):
+    """Two groups, one to four tokens a request, lone requests and padding behind them."""
+    several = heads <= 16
+    c = shared_case(heads, kind, heads, bs, g, [(1999, [1 + 53 * i % 400 + 3 for i in range(12)]), (2560, [4, 700] * 5)],
+                    alone=[0, 1, 260], qlens=[1 + i % 4 if several else 1 for i in range(22)] + [1, 1, 2], sinks=heads in (7, 33),
+                    pad=2)
+    assert shared_groups(c) == [True, True]
+    check(c)
+
+
+@pytest.mark.parametrize("kind", ["scaled", "fp8", "bf16"])
+@pytest.mark.parametrize("prefix", [832, 850, 896, 1023, 1024, 16384])
+def test_shared_prefixes_of_any_length(kind, prefix):
+    c = shared_case(prefix, kind, 8, 64, 64, [(prefix, [1, 64, 65, 127, 128, 129, 300, 2, 3, 4, 5, 6, 7, 1, 1, 900])])
+    assert shared_groups(c) == [True]
+    check(c)
+
+
+@pytest.mark.parametrize("bs,g", [(64, 16), (16, 1), (48, 48)])
+def test_nan_keys_of_a_shared_prefix_and_behind_it(bs, g):
+    c = shared_case(40, "scaled", 24, bs, g, [(1536, [6, 5, 9, 70, 3, 140, 8, 8]), (2048, [70, 4, 4, 6, 9, 30, 7, 5])],
+                    qlens=[4, 1, 3, 2, 1, 1, 1, 1] + [1, 2, 3, 1, 1, 4, 1, 1])
+    assert shared_groups(c) == [True, True]
+    ro, rl, to, tl = expected(c)
+    for r, at in ((0, 1541), (3, 1604), (9, 7), (0, 1000), (13, 2060)):
+        slot = S.row_slots(c["table"][r], bs, at + 1)[at]
+        codes = c["codes"].copy()
+        codes[slot, 11] = 0x7F                            # a value column
+        out, lse, _ = run_case(dict(c, codes=codes))
+        seen = [slot in np.asarray(s) for s in S.token_slots(c["table"], c["lens"], bs, c["qo"])]
+        assert any(seen) and not all(seen)
+        for t, s in enumerate(seen):
+            assert np.isnan(lse[t]).all() == s and np.isnan(lse[t]).any() == s, (r, at, t)
+            assert np.isnan(out[t]).any() == s
+            if not s:
+                assert np.all(np.abs(out[t] - ro[t]) <= to[t]) and np.all(np.abs(lse[t] - rl[t]) <= tl[t])
+
+
+def test_odd_queries_and_sinks_over_a_shared_prefix():
+    c = shared_case(41, "scaled", 24, 64, 64, [(1600, [6, 5, 9, 1, 2, 3, 80, 4])], sinks=True)
+    assert shared_groups(c) == [True]
+    ro, rl, to, tl = expected(c)
+    odd = np.zeros(rl.shape, bool)
+    q, sinks = c["q"].copy(), c["sinks"].copy()
+    q[1, 3, 500], sinks[4] = 0x7F, np.nan
+    odd[1, 3] = odd[:, 4] = True
+    out, lse, _ = run_case(dict(c, q=q, sinks=sinks))
+    assert np.array_equal(np.isnan(lse), odd) and np.isnan(out[odd]).all()
+    assert np.all((np.abs(out - ro) <= to)[~odd]) and np.all((np.abs(lse - rl) <= tl)[~odd])
+    sinks[:] = -np.inf
+    a, al, _ = run_case(dict(c, sinks=sinks))
+    b, bl, _ = run_case(dict(c, sinks=None))
+    assert np.array_equal(a, b) and np.array_equal(al, bl)
+
+
+@pytest.mark.parametrize("bs,g", [(64, 8), (16, 16), (32, 1)])
+def test_missing_blocks_of_a_shared_prefix(bs, g):
+    c = shared_case(42, "scaled", 20, bs, g, [(1664, [300, 70, 9, 33, 64, 1, 2, 3])])
+    assert shared_groups(c) == [True]
+    c["table"][:, 128 // bs] = -1
+    c["table"][:, 1024 // bs:1152 // bs] = -1             # a whole chunk of keys
+    c["table"][0, 1750 // bs] = -1
+    check(c)
+    c["table"][:, :1664 // bs] = -1                       # the whole prefix
+    check(c)
+
+
+@pytest.mark.parametrize("kind", ["scaled", "fp8", "bf16"])
+def test_members_that_take_no_part_in_a_shared_prefix(kind):
+    """Requests too short for their group's prefix are decoded on their own, the first of
+    them too, whose table row is then not the prefix's."""
+    c = shared_case(43, kind, 12, 64, 64, [(1280, [5 + 7 * i for i in range(14)]), (1408, [4] * 12)],
+                    qlens=[1 + i % 3 for i in range(26)])
+    full = c["lens"].copy()
+    for cut in ({0: 0}, {0: 1, 5: 1280, 6: 0, 25: 1000}, {r: 1281 for r in range(0, 14, 3)}, {r: r for r in range(3, 26)}):
+        c["lens"] = full.copy()
+        for r, n in cut.items():
+            c["lens"][r] = n
+        out, lse, _ = run_case(c)
+        compare(c, out, lse)
+    c["lens"] = full.copy()
+    c["lens"][0] = 0
+    c["table"][0, :] = c["table"][0, -1]
+    assert all(shared_groups(c))
+    check(c)
+
+
+@pytest.mark.parametrize("kind", ["scaled", "bf16"])
+def test_shared_prefixes_captured_and_replayed_with_other_groups(kind):
+    c = shared_case(44, kind, 16, 64, 64, [(1600, [300, 200, 100, 5, 6, 7, 8, 9]), (2000, [64, 65] * 4)], pad=2)
+    plan = plan_of(c)
+    args, named = args_of(c, plan)
+    call = lambda: B.mla_decode_fwd_shared(*args, **named)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    full, found = c["lens"].copy(), set()
+    for lens, prefix, edges in ((full, [1600, 2000], [0, 8, 16]), (full - 4, [1600, 2000], [0, 8, 16]),
+                                (full, [64, 1999], [0, 8, 16]), (full, [1600, 0], [0, 3, 16]), (full, [1000, 1300], [1, 8, 12]), (full, [0, 0], [0, 8, 16]),
+                                (full, [1600, 1216], [0, 8, 16]), (full * 0, [1600, 2000], [0, 8, 16]),
+                                (full, [1600, 2000], [8, 0, 16]), (full, [1600, 1600], [0, 16, 8]),
+                                (full, [1600, 2000], [-5, 8, 99]), (full, [10 ** 9, -7], [0, 8, 16])):
+        c.update(lens=np.array(lens), prefix=np.array(prefix), edges=np.array(edges))
+        found.add(tuple(shared_groups(c)) if edges == sorted(edges) and 0 <= edges[0] and edges[-1] <= 16 else None)
+        named["seq_lens"].copy_(dev(lens, np.int32))
+        named["prefix_lens"].copy_(dev(prefix, np.int32))
+        named["group_indptr"].copy_(dev(edges, np.int32))
+        named["out"].fill_(3.0), named["lse"].fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert B.mla_workspace_status(plan.plan, named["workspace"]) == 0
+        compare(c, named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy())
+    assert {(True, True), (False, False)} <= found
+
+
+def test_empty_requests_in_a_row():
+    """Requests without keys, many of them one after another among long ones: their rows
+    are written, and no wait of the loads takes one's output for another's."""
+    for seed, kind in ((46, "scaled"), (47, "fp8"), (48, "bf16")):
+        c = shared_case(seed, kind, 16, 64, 64, [(1600, [5 + 40 * i for i in range(10)])],
+                        alone=[0] * 90 + [700, 0, 0, 0, 300, 0, 5] + [0] * 60, sinks=seed == 46)
+        check(c)
+        c = shared_case(seed, kind, 128, 64, 64, [(1600, [5, 700])], alone=[0] * 40 + [900] + [0] * 41)
+        check(c)
+
+
+@pytest.mark.parametrize("groups", [2, 300])
+def test_groups_that_overlap_share_nothing(groups):
+    """An entry of group_indptr below the one before it: every request on its own."""
+    c = shared_case(45, "scaled", 8, 64, 64, [(1280, [5 + 7 * i for i in range(12)])])
+    c["prefix"] = np.full(groups, 1280)
+    c["edges"] = np.array(([0, 12] * groups)[:groups + 1])
+    check(c)
+
+
+@pytest.mark.parametrize("L", [333, 1400])
+def test_fork_then_decode_over_the_shared_pages(L):
     """Samples of a prompt as a server makes them: fork, block tables, rotary
     positions, append, the shared decode; then losers freed and the pool compacted, and
     another step."""
     rng = np.random.default_rng(30)
-    bs, g, H, L, n = 64, 16, 16, 333, 5
-    nb, cols, rows_n = 60, 12, n + 1
+    bs, g, H, n = 64, 16, 16, 5
+    nb, cols, rows_n = 60, L // 64 + 7, n + 1
     codes, scales = np.zeros((nb * bs, 576), np.uint8), np.full(nb * bs // g, np.nan)
     prompt = bf16(rng.standard_normal((L, 576)))[0]
     ids = rng.permutation(nb)

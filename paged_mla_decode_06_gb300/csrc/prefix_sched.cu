@@ -111,10 +111,17 @@ __device__ __forceinline__ int groups_of(int keys) { return keys > 0 ? keys / kG
 struct Cutter {
   int W, cost;   // shares; length of an item besides its groups
   int least, d;  // groups of a tile that may be cut; of its ends that may not
+  unsigned inv;  // (2^32 - 1) / W
+  // v / W for 0 <= v < 2^31: the product is at most one too small. (A division is some
+  // thirty instructions in a row, and code that the kernel runs once.)
+  __device__ __forceinline__ int over(int v) const {
+    const int q = static_cast<int>(__umulhi(static_cast<unsigned>(v), inv));
+    return q + (v - q * W >= W ? 1 : 0);
+  }
   // the first cut, as a multiple of W, of the tile of g groups at place a; and their number
-  __device__ __forceinline__ int first(int a) const { return (a + cost + d + W - 1) / W; }
+  __device__ __forceinline__ int first(int a) const { return over(a + cost + d + W - 1); }
   __device__ __forceinline__ int count(int a, int g) const {
-    return g < least ? 0 : max((a + cost + g - d) / W - first(a) + 1, 0);
+    return g < least ? 0 : max(over(a + cost + g - d) - first(a) + 1, 0);
   }
 };
 // Piece j of a tile with `cuts` cuts: groups [from, to).
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     if (r < R) rp[r] = a;
   }
   cut.W = max((total + p.workers - 1) / p.workers, kMinShare);
+  cut.inv = 0xffffffffu / static_cast<unsigned>(cut.W);
   cut.least = SORTED ? cut.W / 2 + 1 : kLeastCut;
   cut.d = SORTED ? max(cut.W / 8, 1) : kLeastEnd;
   __syncthreads();

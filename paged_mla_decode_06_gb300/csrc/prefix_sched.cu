@@ -23,7 +23,10 @@
 // pair, its part in the merge). With 128 heads a request fills its tiles
 // alone, and the common keys come from L2 as they are.
 //
-// One CTA, a thread to a tile's first piece and one to the piece behind each cut.
+// Bound by latency: 6 to 7 us a launch (57 to 66 requests), 12000 cycles of which with 512
+// threads were 1700 of reading the lengths, 900 and 900 of participants and groups, 1900 of own
+// keys, 2400 and 2600 of the tables, 1600 of the cuts; much of it waiting for code that
+// runs once. One CTA, a thread to a tile's first piece and one to the piece behind each cut.
 // Lengths and group records are kept in shared memory (of the first 1024 requests and
 // 256 groups): it runs beside the decode's start, and before all of its work.
 #include "common.cuh"
@@ -32,7 +35,10 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 512;
+// Threads: few wait for one another sooner, many take more requests at once (57 requests of 3
+// tokens: 64.8 us with 128, 65.9 with 512; 128 requests in 16 groups: 45.0 and 44.1).
+constexpr int kMaxThreads = 512, kFewThreads = 128;
+constexpr int kFewReqs = 96;
 constexpr int kGroupKeys = 128;
 constexpr int kTileRows = 128;
 constexpr int kBins = 512;
@@ -43,7 +49,7 @@ constexpr int kMinShare = 4;     // groups: pieces of less cost more than they s
 constexpr int kLeastCut = 6, kLeastEnd = 2;  // of a worker's tile: groups to be cut at all, and on either side of a cut
 
 struct Shared {
-  int red[kThreads / 32];
+  int red[kMaxThreads / 32];
   int hist[kBins];   // items by size
   int start[kBins];
   int4 groups[kCache];
@@ -56,6 +62,7 @@ struct Shared {
 
 // Exclusive prefix of v over the block. (Out of line, as the loops are not unrolled: the
 // kernel runs once a call, and mostly waits for its own code.)
+template <int THREADS>
 __device__ __noinline__ int block_scan(int v, int* red, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = v;
@@ -68,22 +75,23 @@ __device__ __noinline__ int block_scan(int v, int* red, int* total) {
   if (lane == 31) red[warp] = inc;
   __syncthreads();
   // (every warp scans the warps' sums)
-  const int mine = lane < kThreads / 32 ? red[lane] : 0;
+  const int mine = lane < THREADS / 32 ? red[lane] : 0;
   int all = mine;
 #pragma unroll
-  for (int o = 1; o < kThreads / 32; o <<= 1) {
+  for (int o = 1; o < THREADS / 32; o <<= 1) {
     const int n = __shfl_up_sync(0xffffffffu, all, o);
     if (lane >= o) all += n;
   }
-  *total = __shfl_sync(0xffffffffu, all, kThreads / 32 - 1);
+  *total = __shfl_sync(0xffffffffu, all, THREADS / 32 - 1);
   return __shfl_sync(0xffffffffu, all - mine, warp) + inc - v;
 }
 
+template <int THREADS>
 __device__ __forceinline__ int2 block_scan2(int2 v, int* red, int2* total) {
   int2 r;
   int2 all;
-  r.x = block_scan(v.x, red, &all.x);
-  r.y = block_scan(v.y, red, &all.y);
+  r.x = block_scan<THREADS>(v.x, red, &all.x);
+  r.y = block_scan<THREADS>(v.y, red, &all.y);
   *total = all;
   return r;
 }
@@ -133,8 +141,8 @@ __device__ __forceinline__ Piece piece_of(const Cutter& c, int a, int g, int cut
   return Piece{j == 0 ? 0 : z + (j - 1) * c.W, j == cuts ? g : z + j * c.W};
 }
 
-template <bool SORTED>
-__global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixParams p) {
+template <bool SORTED, int THREADS>
+__global__ void __launch_bounds__(THREADS) prefix_schedule_kernel(const PrefixParams p) {
   __shared__ Shared s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x;
@@ -166,14 +174,15 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     if (r < kCacheReqs) s.reqs[r].w = g;
   };
 #pragma unroll 1
-  for (int r = tid; r < min(R, kCacheReqs); r += kThreads) {
+  for (int r = tid; r < min(R, kCacheReqs); r += THREADS) {
     const int t0 = token_edge(p, r);
     s.reqs[r] = make_int4(t0, max(token_edge(p, r + 1) - t0, 0), p.seq_lens[r], -1);
   }
-  if (SORTED) s.hist[tid] = 0;
+  if (SORTED)
+    for (int b = tid; b < kBins; b += THREADS) s.hist[b] = 0;
   bool falls = false;
 #pragma unroll 1
-  for (int g = tid; g < G; g += kThreads) {
+  for (int g = tid; g < G; g += THREADS) {
     const int first = group_edge(p, g), end = group_edge(p, g + 1);
     const int whole = min(max(p.prefix_lens[g], 0) / p.block_size, p.cols);
     falls |= first > end;
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   // (groups that overlap would have more tiles than the workspace has room for)
   const bool apart = __syncthreads_or(falls) == 0;
 #pragma unroll 1
-  for (int r = tid; r < R; r += kThreads) {
+  for (int r = tid; r < R; r += THREADS) {
     const int4 q = request(r);
     int g = last_at(G, r, edge);
     const bool in = apart && r >= edge(g) && r < edge(g + 1);
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   // prefix tiles and their places in the sequence
   int ptiles = 0, prefix_end = 0;
 #pragma unroll 1
-  for (int g0 = 0; g0 < G; g0 += kThreads) {
+  for (int g0 = 0; g0 < G; g0 += THREADS) {
     const int g = g0 + tid;
     int tiles = 0, keys = 0, tok0 = 0, first = 0;
     if (g < G) {
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     }
     const int length = tiles * (groups_of(keys) + cost);
     int2 sum = make_int2(tiles, length), at = make_int2(0, 0);
-    if (G > 1) at = block_scan2(sum, s.red, &sum);
+    if (G > 1) at = block_scan2<THREADS>(sum, s.red, &sum);
     const int t = ptiles + at.x, a = prefix_end + at.y;
     if (G > 1) {
       ptiles += sum.x;
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   };
   int total = prefix_end;
 #pragma unroll 1
-  for (int r0 = 0; r0 < R; r0 += kThreads) {
+  for (int r0 = 0; r0 < R; r0 += THREADS) {
     const int r = r0 + tid;
     int length = 0;
     if (r < R) {
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       length = o.tiles * (o.groups + cost);
     }
     int sum;
-    const int a = total + block_scan(length, s.red, &sum);
+    const int a = total + block_scan<THREADS>(length, s.red, &sum);
     total += sum;
     if (r < R) rp[r] = a;
   }
@@ -340,32 +349,39 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       atomicAdd(&s.hist[kBins - 1 - min(q.to - q.from, kBins - 1)], 1);
     };
 #pragma unroll 1
-    for (int t = tid; t < ptiles; t += kThreads) count(prefix_tile(t), 0);
+    for (int t = tid; t < ptiles; t += THREADS) count(prefix_tile(t), 0);
 #pragma unroll 1
-    for (int r = tid; r < R; r += kThreads) {
+    for (int r = tid; r < R; r += THREADS) {
       const Own o = own_keys(r);
 #pragma unroll 1
       for (int t = 0; t < o.tiles; ++t) count(own_tile(o, r, t), 0);
     }
 #pragma unroll 1
-    for (int w = tid + 1; w <= all_cuts; w += kThreads) {
+    for (int w = tid + 1; w <= all_cuts; w += THREADS) {
       At c;
       if (!at_cut(w, c)) continue;
       const int j = w - cut.first(c.t.a) + 1;
       if (j >= 1 && j <= cut.count(c.t.a, c.t.n)) count(c.t, j);
     }
     __syncthreads();
-    static_assert(kBins == kThreads, "a bin a thread");
+    constexpr int kPer = kBins / THREADS;  // bins of a thread
+    int mine = 0;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) mine += s.hist[kPer * tid + b];
     int all;
-    const int at = block_scan(s.hist[tid], s.red, &all);
-    s.start[tid] = at;
+    int at = block_scan<THREADS>(mine, s.red, &all);
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      s.start[kPer * tid + b] = at;
+      at += s.hist[kPer * tid + b];
+    }
     if (tid == 0) *p.n_items = min(all, p.max_items);
     __syncthreads();
   }
   // the tables, and each tile's first item
   int rows = 0, items = 0;  // of the partials, of the list
 #pragma unroll 1
-  for (int t0 = 0; t0 < ptiles; t0 += kThreads) {
+  for (int t0 = 0; t0 < ptiles; t0 += THREADS) {
     const int t = t0 + tid;
     Tile v{};
     int cuts = -1;
@@ -374,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       cuts = cut.count(v.a, v.n);
     }
     int sum;
-    const int at = items + block_scan(cuts + 1, s.red, &sum);
+    const int at = items + block_scan<THREADS>(cuts + 1, s.red, &sum);
     items += sum;
     rows += sum * kTileRows;
     if (t < ptiles) {
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
     }
   }
 #pragma unroll 1
-  for (int r0 = 0; r0 < R; r0 += kThreads) {
+  for (int r0 = 0; r0 < R; r0 += THREADS) {
     const int r = r0 + tid;
     Own o{};
     if (r < R) o = own_keys(r);
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
       if (part || k > 1) mine.y += k * v.stride;
     }
     int2 sum;
-    const int2 before = block_scan2(mine, s.red, &sum);
+    const int2 before = block_scan2<THREADS>(mine, s.red, &sum);
     int at = items + before.x, base = rows + before.y;
     items += sum.x;
     rows += sum.y;
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) prefix_schedule_kernel(const PrefixP
   // of its share lies in, or the next where that one's middle is before it
   items = min(items, p.max_items);
 #pragma unroll 1
-  for (int w = tid + 1; w <= (SORTED ? all_cuts : max(all_cuts, p.workers)); w += kThreads) {
+  for (int w = tid + 1; w <= (SORTED ? all_cuts : max(all_cuts, p.workers)); w += THREADS) {
     At c;
     if (w > all_cuts || !at_cut(w, c)) {
       if (!SORTED && w <= p.workers) p.worker_first[w] = items;
@@ -561,10 +577,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
 }  // namespace
 
 cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t stream) {
-  if (p.worker_first == nullptr)
-    prefix_schedule_kernel<true><<<1, kThreads, 0, stream>>>(p);
-  else
-    prefix_schedule_kernel<false><<<1, kThreads, 0, stream>>>(p);
+  const bool few = p.num_reqs <= kFewReqs;
+  if (p.worker_first == nullptr) {
+    if (few) prefix_schedule_kernel<true, kFewThreads><<<1, kFewThreads, 0, stream>>>(p);
+    else prefix_schedule_kernel<true, kMaxThreads><<<1, kMaxThreads, 0, stream>>>(p);
+  } else {
+    if (few) prefix_schedule_kernel<false, kFewThreads><<<1, kFewThreads, 0, stream>>>(p);
+    else prefix_schedule_kernel<false, kMaxThreads><<<1, kMaxThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

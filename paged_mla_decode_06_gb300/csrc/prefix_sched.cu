@@ -7,11 +7,12 @@
 // are laid end to end, those of the prefixes first, each as long as its groups
 // and, where workers run items one after another, kItemCost more for what an item
 // costs besides; the sequence is cut at every multiple of W = cdiv(its length,
-// workers), at least kMinShare. A cut within W / 8 of a tile's ends is dropped, and so are
-// cuts of tiles that are short against W. A worker's items are those with their middle
-// in its share. (Kernels of one item a pair get the longest first instead, and
-// the short ones fill what the others leave.) A row's pieces, of either kind, write
-// base-2 partials; rows of one piece in all write their output.
+// workers), at least kMinShare. Cuts within kLeastEnd groups of a tile's ends are
+// dropped, and those of tiles of less than kLeastCut. A worker's items are those with
+// their middle in its share. (Kernels of one item a pair get the longest first instead, cut
+// no nearer than W / 8 to an end and not in tiles of half a share, and the short ones
+// fill what the others leave.) A row's pieces, of either kind, write base-2
+// partials; rows of one piece in all write their output.
 //
 // A request takes part in its group's prefix when all its tokens see all of it
 // (seq_len - qlen >= prefix); the others take all their keys as their own. So a call

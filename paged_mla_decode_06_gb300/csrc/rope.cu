@@ -14,6 +14,10 @@
 // once, in registers, and the loads of kBatch heads are in flight together while
 // they are. (Angles of both of a lane's columns are made even where they are one pair's:
 // the two do not show beside the loads.)
+//
+// Measured: 8191 tokens of 16 heads to bf16 47.7 us, 6.4 TB/s (0.94 of the copy rate); 64 of
+// 128 heads to e4m3 4.8 us in a captured graph, of which 2.0 are its 13.5 MB and the rest
+// the chain of position, angle, rows.
 #include "common.cuh"
 #include "internal.h"
 

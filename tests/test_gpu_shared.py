@@ -575,6 +575,43 @@ def test_empty_requests_in_a_row():
         check(c)
 
 
+@pytest.mark.parametrize("kind", ["scaled", "bf16"])
+@pytest.mark.parametrize("kw", [dict(num_sms=1), dict(num_sms=7), dict(num_sms=600), dict(max_qlen=9),
+                                dict(max_seq_len=2048)])
+def test_plans_for_other_bounds(kind, kw):
+    """Fewer and more workers than the GPU has, looser bounds than the call's."""
+    c = shared_case(49, kind, 16, 64, 64, [(1600, [5 + 40 * i for i in range(10)])], alone=[0, 700],
+                    qlens=[1, 2, 3] * 4)
+    assert shared_groups(c) == [True]
+    p = B.make_problem(**dict(dict(
+        num_tokens=c["T"], num_heads=16, block_size=64, num_blocks=c["nb"], num_reqs=len(c["lens"]),
+        max_blocks_per_req=c["table"].shape[1], max_seq_len=int(c["lens"].max()), max_qlen=3,
+        dtype="bf16" if kind == "bf16" else "fp8"), **kw))
+    plan = B.mla_decode_shared_plan(p, num_groups=1)
+    args, named = args_of(c, plan)
+    B.mla_decode_fwd_shared(*args, **named)
+    torch.cuda.synchronize()
+    assert B.mla_workspace_status(plan.plan, named["workspace"]) == 0
+    compare(c, named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy())
+
+
+@pytest.mark.parametrize("kind", ["scaled", "bf16"])
+def test_tokens_before_the_first_request_are_left(kind):
+    c = shared_case(50, kind, 16, 64, 64, [(1600, [5 + 40 * i for i in range(10)])], qlens=[1, 2] * 5, pad=2)
+    d = dict(c, qo=c["qo"] + 2, q=(torch.roll if kind == "bf16" else np.roll)(c["q"], 2, 0))
+    out, lse, _ = run_case(d)
+    assert (out[:2] == 3.0).all() and (lse[:2] == 3.0).all()
+    n = len(out) - 2
+    c["T"], c["pad"] = n, 0
+    compare(c, out[2:], lse[2:])
+
+
+@pytest.mark.parametrize("kind", ["scaled", "fp8", "bf16"])
+def test_requests_of_several_tiles(kind):
+    c = shared_case(51, kind, 128, 64, 64, [(1300, [4, 90, 300])], alone=[2, 500], qlens=[4, 1, 3, 2, 4], sinks=True)
+    check(c)
+
+
 @pytest.mark.parametrize("groups", [2, 300])
 def test_groups_that_overlap_share_nothing(groups):
     """An entry of group_indptr below the one before it: every request on its own."""

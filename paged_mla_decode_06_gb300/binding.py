@@ -875,13 +875,17 @@ def mla_cache_copy_blocks(src, dst, kv_cache, kv_scales=None, *, scale_group: in
         _check(fn, status)
 
 
-def mla_cache_free(rows, block_table, ref_counts, *, lens=None, block_size: int = 1, freed, num_freed, workspace,
-                   stream=None) -> None:
+def mla_cache_free(rows, block_table, ref_counts, *, lens=None, block_size: int | None = None, freed, num_freed,
+                   workspace, stream=None) -> None:
     """Gives up the table rows ``rows``, all their columns or those of ``lens`` tokens
     in blocks of ``block_size``; the blocks that no row holds any more go to
     ``freed``, in ascending order, their number to ``num_freed``."""
     lib, fn = _lib or load_library(), "mla_cache_free"
     torch = _torch or _load_torch()
+    if block_size is None:
+        if lens is not None:
+            raise MLAError(fn, MLA_ERR_INVALID_ARG, "lens are in tokens: they need a block_size")
+        block_size = 1
     dev, n = block_table.get_device(), rows.numel()
     if not (dev >= 0 and dev == torch._C._cuda_getDevice() and workspace.get_device() == dev
             and workspace.is_contiguous()):

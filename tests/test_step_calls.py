@@ -268,3 +268,10 @@ def test_binding_refuses_host_tensors():
         B.mla_cache_free(i, t, i, freed=i, num_freed=i[:1], workspace=kv)
     with pytest.raises(B.MLAError, match="CUDA"):
         B.mla_cache_compact(i, t, kv, sc, scale_group=64, num_live=i[:1], workspace=kv)
+
+
+def test_binding_refuses_lengths_without_a_block_size():
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(B.MLAError, match="block_size"):
+        B.mla_cache_free(i, torch.zeros(2, 2, dtype=torch.int32), i, lens=i, freed=i, num_freed=i[:1],
+                         workspace=torch.zeros(256, dtype=torch.uint8))

@@ -271,6 +271,7 @@ def test_binding_refuses_host_tensors():
 
 
 def test_binding_refuses_lengths_without_a_block_size():
+    torch = pytest.importorskip("torch")
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(B.MLAError, match="block_size"):
         B.mla_cache_free(i, torch.zeros(2, 2, dtype=torch.int32), i, lens=i, freed=i, num_freed=i[:1],

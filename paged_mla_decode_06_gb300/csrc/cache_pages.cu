@@ -8,7 +8,7 @@
 // around it is done by the same launches.
 //
 // Measured: 4000 bf16 blocks of 64 copied in 95.5 us, 6.2 TB/s (0.91 of the copy rate);
-// 16384 e4m3 blocks, 60 % in use, compacted in 59.6 (scan 9, then the moves at 0.92 of the
+// 16384 e4m3 blocks, 60 % in use, compacted in 57.5 (scan 7, then the moves at 0.92 of the
 // rate); 64 prompts forked into 8 samples each in 6.2 us and 4 forks of one in 3.4 in a
 // captured graph, latency: earlier forks counted, table cells, rows.
 #include "common.cuh"

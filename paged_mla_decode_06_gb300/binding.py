@@ -832,6 +832,18 @@ def _int_lists(fn: str, dev: int, tables, lists):
                 [(False, f"{name} must be [rows, columns] with dense rows that do not overlap")])
 
 
+def _table(t, i32, dev: int):
+    """(rows, columns, row stride) of a 2-D int32 tensor with dense rows that do not
+    overlap, on device ``dev``; no columns of another one."""
+    shape = t.shape
+    if t.dtype is not i32 or t.get_device() != dev or len(shape) != 2:
+        return 0, 0, 0
+    (rows, cols), (across, along) = shape, t.stride()
+    if rows > 0 and not ((along == 1 or cols == 1) and (rows == 1 or across >= cols)):
+        return 0, 0, 0
+    return rows, cols, across if rows > 1 else cols
+
+
 def _table_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
@@ -848,15 +860,25 @@ def mla_cache_fork(parent, child, lens, free_blocks, block_table, ref_counts, kv
     ``free_blocks`` (None: no free block)."""
     lib, fn = _lib or load_library(), "mla_cache_fork"
     dev, nb, bs, code = _pages_args(fn, kv_cache, kv_scales, scale_group)
-    n = parent.numel()
-    _int_lists(fn, dev, [("block_table", block_table)],
-               [("parent", parent, n), ("child", child, n), ("lens", lens, n), ("free_blocks", free_blocks, None),
-                ("ref_counts", ref_counts, nb), ("taken", taken, 1)])
-    rows, cols = block_table.shape
+    n, i32, free, num_free = parent.numel(), _torch.int32, None, 0
+    rows, cols, stride = _table(block_table, i32, dev)
+    ok = (cols > 0 and parent.dtype is i32 and parent.get_device() == dev and parent.is_contiguous()
+          and child.dtype is i32 and child.get_device() == dev and child.is_contiguous() and child.numel() == n
+          and lens.dtype is i32 and lens.get_device() == dev and lens.is_contiguous() and lens.numel() == n
+          and ref_counts.dtype is i32 and ref_counts.get_device() == dev and ref_counts.is_contiguous()
+          and ref_counts.numel() == nb
+          and taken.dtype is i32 and taken.get_device() == dev and taken.numel() == 1)
+    if free_blocks is not None:
+        ok = ok and free_blocks.dtype is i32 and free_blocks.get_device() == dev and free_blocks.is_contiguous()
+        free, num_free = free_blocks.data_ptr(), free_blocks.numel()
+    if not ok:
+        _int_lists(fn, dev, [("block_table", block_table)],
+                   [("parent", parent, n), ("child", child, n), ("lens", lens, n), ("free_blocks", free_blocks, None),
+                    ("ref_counts", ref_counts, nb), ("taken", taken, 1)])
     status = lib.mla_cache_fork(
-        parent.data_ptr(), child.data_ptr(), lens.data_ptr(), n, _ptr(free_blocks),
-        0 if free_blocks is None else free_blocks.numel(), block_table.data_ptr(), _table_stride(block_table), rows, cols,
-        ref_counts.data_ptr(), nb, bs, code, scale_group, kv_cache.data_ptr(), _ptr(kv_scales), taken.data_ptr(),
+        parent.data_ptr(), child.data_ptr(), lens.data_ptr(), n, free, num_free, block_table.data_ptr(), stride, rows, cols,
+        ref_counts.data_ptr(), nb, bs, code, scale_group, kv_cache.data_ptr(),
+        None if kv_scales is None else kv_scales.data_ptr(), taken.data_ptr(),
         _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status:
         _check(fn, status)
@@ -890,12 +912,19 @@ def mla_cache_free(rows, block_table, ref_counts, *, lens=None, block_size: int 
     if not (dev >= 0 and dev == torch._C._cuda_getDevice() and workspace.get_device() == dev
             and workspace.is_contiguous()):
         _refuse(fn, dev, [("workspace", workspace, (workspace.dtype,))], [(False, "workspace must be contiguous")])
-    _int_lists(fn, dev, [("block_table", block_table)],
-               [("rows", rows, n), ("lens", lens, n), ("ref_counts", ref_counts, None), ("freed", freed, None),
-                ("num_freed", num_freed, 1)])
-    num_rows, cols = block_table.shape
+    i32 = torch.int32
+    num_rows, cols, stride = _table(block_table, i32, dev)
+    if not (cols > 0 and rows.dtype is i32 and rows.get_device() == dev and rows.is_contiguous()
+            and (lens is None or (lens.dtype is i32 and lens.get_device() == dev and lens.is_contiguous()
+                                  and lens.numel() == n))
+            and ref_counts.dtype is i32 and ref_counts.get_device() == dev and ref_counts.is_contiguous()
+            and freed.dtype is i32 and freed.get_device() == dev and freed.is_contiguous()
+            and num_freed.dtype is i32 and num_freed.get_device() == dev and num_freed.numel() == 1):
+        _int_lists(fn, dev, [("block_table", block_table)],
+                   [("rows", rows, n), ("lens", lens, n), ("ref_counts", ref_counts, None), ("freed", freed, None),
+                    ("num_freed", num_freed, 1)])
     status = lib.mla_cache_free(
-        rows.data_ptr(), _ptr(lens), n, block_table.data_ptr(), _table_stride(block_table), num_rows, cols,
+        rows.data_ptr(), None if lens is None else lens.data_ptr(), n, block_table.data_ptr(), stride, num_rows, cols,
         ref_counts.data_ptr(), ref_counts.numel(), block_size, freed.data_ptr(), freed.numel(), num_freed.data_ptr(),
         workspace.data_ptr(), _ws_bytes(workspace),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))

@@ -51,10 +51,10 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
   const int64_t gw = SLICED ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + warp;
   const int slice = SLICED ? warp : 0;
   const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_heads;
-  if (gw >= total) return;
+  if (gw >= total) return leave_merge();
   const int t = static_cast<int>(gw / p.num_heads);
   const int h = static_cast<int>(gw % p.num_heads);
-  if (p.part.qo_indptr != nullptr && (t < p.part.qo_indptr[0] || t >= p.part.qo_indptr[p.part.num_reqs])) return;
+  if (p.part.qo_indptr != nullptr && (t < p.part.qo_indptr[0] || t >= p.part.qo_indptr[p.part.num_reqs])) return leave_merge();
   const float sink2 = p.sinks != nullptr ? p.sinks[h] * kLog2e : -INFINITY;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + gw * p.rank;
   if (p.unit_tab != nullptr) {
@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
     // written by the decode kernel itself. The unit table comes from the
     // schedule kernel, which completed before the decode began, so it is
     // read while the decode (this grid's programmatic primary) may still
-    // run, and a row that was not split leaves at once; only the partials
-    // wait for the decode to complete.
+    // run, and a row that was not split leaves at once (but in the first
+    // block: leave_merge); only the partials wait for the decode to complete.
     int u = t, tok0 = t;
     if (!p.sparse && p.part.qo_indptr != nullptr) {
       u = request_of(p.part, t);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(const MergeP
     int2 e = make_int2(-1, 0);
     if (r / tr < p.tiles_max)
       e = reinterpret_cast<const int2*>(p.unit_tab)[static_cast<int64_t>(u) * p.tiles_max + r / tr];
-    if (e.y <= 1) return;
+    if (e.y <= 1) return leave_merge();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     merge_row<VPL, WIDTH, true>(p.segm_out, p.segm_max, p.segm_expsum, static_cast<int64_t>(e.x) * tr + r % tr,
                          tr, e.y, sink2, out, p.lse + gw, lane, slice);

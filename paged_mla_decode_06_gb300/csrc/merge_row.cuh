@@ -18,6 +18,16 @@
 
 namespace mla {
 
+// The end of a row that the merge has nothing to do for. The decode lets its merge
+// launch early, and what follows the merge on the stream, or in a captured graph,
+// waits for the merge alone: a grid that ended without waiting for the decode would
+// let it run while the decode still writes. So the first block, whose first warp
+// always has a row, waits before it leaves. (The others need not: rows that leave
+// make room for those that wait.)
+__device__ __forceinline__ void leave_merge() {
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
 template <bool Coherent>
 __device__ __forceinline__ float4 merge_load(const float4* p) {
   if constexpr (Coherent) return __ldcg(p);

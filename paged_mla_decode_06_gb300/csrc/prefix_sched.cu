@@ -32,6 +32,7 @@
 // 256 groups): it runs beside the decode's start, and before all of its work.
 #include "common.cuh"
 #include "internal.h"
+#include "merge_row.cuh"
 
 namespace mla {
 namespace {
@@ -465,7 +466,8 @@ __global__ void __launch_bounds__(THREADS) prefix_schedule_kernel(const PrefixPa
 // weighted as mla_merge_segments does. The tables are read while the decode may still
 // run; the first pieces' outputs are loaded with their weights, not after them, and two
 // at a time (eight of a slice), so that 32 warps fit an SM (four at a time and behind the
-// weights: 14 us against 8 for 8192 rows of two pieces).
+// weights: 14 us against 8 for 8192 rows of two pieces). Rows without pieces leave at
+// once, but in the first block, by leave_merge.
 constexpr int kMergeWarps = 4;
 
 template <bool SLICED>
@@ -475,21 +477,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 8) prefix_merge_kernel(const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = SLICED ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
   const int first = SLICED ? 32 * warp + lane : lane;  // float4 of the row
-  if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return;
+  if (row >= static_cast<int64_t>(p.num_tokens) * p.num_heads) return leave_merge();
   const int H = p.num_heads;
   const int t = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<int64_t>(t) * H);
   // (the tables come from the schedule, which completed before the decode began)
   int r = t, tok0 = t;
   if (p.qo_indptr != nullptr) {
-    if (t < p.qo_indptr[0] || t >= p.qo_indptr[p.num_reqs]) return;  // padding of the batch
+    if (t < p.qo_indptr[0] || t >= p.qo_indptr[p.num_reqs]) return leave_merge();  // padding of the batch
     r = last_at(p.num_reqs, t, [&](int i) { return p.qo_indptr[i]; });
     tok0 = p.qo_indptr[r];
   }
   const int own_row = (t - tok0) * H + h;
-  if (own_row / kTileRows >= p.tiles_max) return;
+  if (own_row / kTileRows >= p.tiles_max) return leave_merge();
   const int g = p.req_group[r];
   const int2 own = reinterpret_cast<const int2*>(p.unit_tab)[static_cast<int64_t>(r) * p.tiles_max + own_row / kTileRows];
-  if (own.x < 0) return;  // one piece in all: written by the decode
+  if (own.x < 0) return leave_merge();  // one piece in all: written by the decode
   const int end = token_edge(p, r + 1);
   const int own_stride = min(kTileRows, (end - tok0) * H - own_row / kTileRows * kTileRows);
   int2 pre = make_int2(0, 0);

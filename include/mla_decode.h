@@ -230,7 +230,9 @@ MLA_API mla_status_t mla_decode_plan(const mla_problem_t* prob, mla_plan_t* plan
  *                initialisation.
  *   out          [T, H, 512] bf16; lse [T, H] fp32 natural log. Every element
  *                of a request's rows is written; a row with no visible key
- *                gets out = 0 and lse = -inf (or its sink). Tokens before
+ *                gets out = 0 and lse = -inf (or its sink); one that sees a key
+ *                with a NaN, or whose query has one, gets NaN in both, whether
+ *                it is split or not. Tokens before
  *                qo_indptr[0] or at or past qo_indptr[R] (the padding of a
  *                captured batch) are left as they were.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_WORKSPACE, MLA_ERR_CUDA.

@@ -792,7 +792,7 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
                 f = e / W;
                 lse = kLn2 * (M + log2f(W));
               }
-            } else if (GS ? L != 0.f : L > 0.f) {  // (GS: NaN stays)
+            } else if (L != 0.f) {  // (NaN stays)
               f = 1.f / L;
               lse = kLn2 * (base + log2f(L));
             }
@@ -801,16 +801,10 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
             const int64_t ts = it.pslot >= 0 ? static_cast<int64_t>(it.pslot) * (CL * NR) + x.rank * NR + t8
                                              : th * p.num_segments + it.seg;
             const float mt = mtrue[lb + t8];
-            if constexpr (GS) {
-              const float2 part = partial_sums(L > 0.f ? mt : -INFINITY, L > 0.f ? L * exp2f(base - mt) : L);
-              p.segm_max[ts] = part.x;
-              p.segm_expsum[ts] = part.y;
-              f = L != 0.f ? 1.f / L : 0.f;
-            } else {
-              p.segm_max[ts] = L > 0.f ? mt : -INFINITY;
-              p.segm_expsum[ts] = L > 0.f ? L * exp2f(base - mt) : 0.f;
-              f = L > 0.f ? 1.f / L : 0.f;
-            }
+            const float2 part = partial_sums(L > 0.f ? mt : -INFINITY, L > 0.f ? L * exp2f(base - mt) : L);
+            p.segm_max[ts] = part.x;
+            p.segm_expsum[ts] = part.y;
+            f = L != 0.f ? 1.f / L : 0.f;
           }
         }
         mult[t8] = f * p.kv_scale;

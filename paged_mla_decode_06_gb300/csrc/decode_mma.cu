@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
         mult = 0.f;
         lse = -INFINITY;
       }
-      if (GS && L != L) mult = lse = L;
+      if (L != L) mult = lse = L;
       mult *= p.kv_scale;
       __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(p.out) + th * kRank + cs * C::kVW + 2 * (lane & 3);
 #pragma unroll
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       }
       if (cs == 0 && (lane & 3) == 0) p.lse[th] = lse;
     } else {
-      const float mult = L > 0.f || (GS && L != L) ? p.kv_scale / L : 0.f;
+      const float mult = L != 0.f ? p.kv_scale / L : 0.f;
       const int64_t ts = th * p.num_segments + seg;
       float* dst = p.segm_out + ts * kRank + cs * C::kVW + 2 * (lane & 3);
 #pragma unroll
@@ -470,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
         *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * i] * mult, o[n][2 * i + 1] * mult);
       }
       if (cs == 0 && (lane & 3) == 0) {
-        float2 part = make_float2(L > 0.f ? m : -INFINITY, L);
-        if constexpr (GS) part = partial_sums(part.x, part.y);
+        const float2 part = partial_sums(L > 0.f ? m : -INFINITY, L);
         p.segm_max[ts] = part.x;
         p.segm_expsum[ts] = part.y;
       }

@@ -607,14 +607,14 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
         const float W = l * e + exp2f(s2 - M);
         mult = e / W;
         lse = kLn2 * (M + log2f(W));
-      } else if (l > 0.f) {
+      } else if (l != 0.f) {  // (a NaN stays)
         mult = 1.f / l;
         lse = kLn2 * (m_ref + log2f(l));
       } else {
         mult = 0.f;
       }
     } else {
-      mult = l > 0.f ? 1.f / l : 0.f;
+      mult = l != 0.f ? 1.f / l : 0.f;
     }
     if (row_ok) {
       if (x.fin) {
@@ -622,8 +622,9 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
       } else {
         const int64_t ts = x.pslot >= 0 ? static_cast<int64_t>(x.pslot) * p.slot_rows + r
                                         : th * p.num_segments + x.seg;
-        p.segm_max[ts] = l > 0.f ? m_true : -INFINITY;
-        p.segm_expsum[ts] = l > 0.f ? l * exp2f(m_ref - m_true) : 0.f;
+        const float2 part = partial_sums(l > 0.f ? m_true : -INFINITY, l > 0.f ? l * exp2f(m_ref - m_true) : l);
+        p.segm_max[ts] = part.x;
+        p.segm_expsum[ts] = part.y;
       }
     }
     st_cluster_f32(x.peer + kOffMult + 4 * r, mult * p.kv_scale);

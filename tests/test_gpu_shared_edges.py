@@ -1,12 +1,13 @@
 """The decode of a batch that shares prefixes, and the decodes beside it, at their edges:
-calls without a split row in captured graphs."""
+calls without a split row in captured graphs, rows and keys that are no numbers."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import scaled_oracle as S
 from paged_mla_decode_06_gb300 import binding as B
 from paged_mla_decode_06_gb300 import build as BUILD
-from tests.test_gpu_shared import KVS, QS, SCALE, args_of, dev, shared_case
+from tests.test_gpu_shared import args_of, dev, expected, shared_case, shared_groups
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,76 @@ def replayed_like_eager(call, plan, decode_plan, named, c, parts, lengths):
         wrong += (got_lse.view(torch.int32) != want[i % 2][1].view(torch.int32)).sum()
     assert wrong.item() == 0
     assert B.mla_workspace_status(decode_plan, named["workspace"]) == 0
+
+
+# ---- rows and keys that are no numbers
+
+def poisoned(c, keys=(), queries=(), value=float("nan")):
+    """``keys``: (slot, column), ``queries``: (token, head, column) that hold ``value``
+    (e4m3: NaN)."""
+    if c["kind"] == "bf16":
+        d = dict(c, kv=c["kv"].clone(), q=c["q"].clone())
+        for slot, col in keys:
+            d["kv"][slot, col] = value
+        for t, h, col in queries:
+            d["q"][t, h, col] = value
+        return d
+    d = dict(c, codes=c["codes"].copy(), q=c["q"].copy())
+    for slot, col in keys:
+        d["codes"][slot, col] = 0x7F
+    for t, h, col in queries:
+        d["q"][t, h, col] = 0xFF
+    return d
+
+
+def ran(c, plan):
+    args, named = args_of(c, plan)
+    B.mla_decode_fwd_shared(*args, **named)
+    torch.cuda.synchronize()
+    assert B.mla_workspace_status(plan.plan, named["workspace"]) == 0
+    return named["out"].double().cpu().numpy(), named["lse"].double().cpu().numpy()
+
+
+def right_but(c, odd, out, lse):
+    """Every row outside ``odd`` [T, H] within its bounds, no number in it NaN."""
+    ro, rl, to, tl = expected(c)
+    n = len(ro)
+    assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
+    out, lse = out[:n], lse[:n]
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(lse)[~odd], empty[~odd])
+    assert np.all((np.abs(out - ro) <= to)[~odd])
+    assert np.all((np.abs(np.where(empty, 0, lse) - np.where(empty, 0, rl)) <= tl)[~odd & ~empty])
+
+
+# (kind, block size, group, heads, keys of the prefix, what the plan asks for): shared
+# prefixes, and the plain decode of plans that cannot share on each of its kernels, whole and
+# in pieces
+ROUTES = [("bf16", 64, 64, 24, 1536, {}), ("fp8", 64, 64, 24, 1536, {}), ("scaled", 64, 16, 24, 1536, {}),
+          ("bf16", 64, 64, 128, 300, {}), ("bf16", 64, 64, 24, 1536, dict(num_segments=3)), ("bf16", 16, 16, 16, 300, {}),
+          ("bf16", 16, 16, 33, 1536, dict(num_segments=3)), ("fp8", 64, 64, 16, 300, {}),
+          ("fp8", 64, 64, 128, 1536, dict(num_segments=3)), ("fp8", 8, 8, 16, 300, {}),
+          ("fp8", 8, 8, 33, 1536, dict(num_segments=3)),
+          ("fp8", 64, 64, 24, 1536, dict(num_segments=2, kernel=B.MLA_KERNEL_TCGEN05))]
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("kind,bs,g,heads,prefix,kw", ROUTES)
+def test_rows_that_see_a_nan_are_nan_on_every_route(kind, bs, g, heads, prefix, kw, sinks):
+    """A NaN key of the prefix, of one request's own keys, of one head's query: the rows
+    that see it are NaN in output and LSE, the others right."""
+    c = shared_case(62, kind, heads, bs, g, [(prefix, [6, 5, 9, 70, 3, 140, 8, 8])], alone=[260, 0], sinks=sinks)
+    plan = B.mla_decode_shared_plan(problem_of(c, **kw), num_groups=1)
+    assert (plan.max_items > 0) == (prefix > 768 and not kw)
+    assert plan.max_items == 0 or shared_groups(c) == [True]
+    for keys, queries in (([(c["table"][0, 200 // bs] * bs + 200 % bs, 11)], []),
+                          ([(c["table"][3, (prefix + 60) // bs] * bs + (prefix + 60) % bs, 575)], [(1, 3, 500), (8, 2, 7)])):
+        odd = np.zeros((c["T"], heads), bool)
+        for slot, _ in keys:
+            odd[[slot in np.asarray(s) for s in S.token_slots(c["table"], c["lens"], bs, c["qo"])]] = True
+        for t, h, _ in queries:
+            odd[t, h] = True
+        assert odd.any() and not odd.all()
+        out, lse = ran(poisoned(c, keys, queries), plan)
+        assert np.isnan(out[odd]).all() and np.isnan(lse[odd]).all()
+        right_but(c, odd, out, lse)

@@ -232,7 +232,8 @@ MLA_API mla_status_t mla_decode_plan(const mla_problem_t* prob, mla_plan_t* plan
  *                of a request's rows is written; a row with no visible key
  *                gets out = 0 and lse = -inf (or its sink); one that sees a key
  *                with a NaN, or whose query has one, gets NaN in both, whether
- *                it is split or not. Tokens before
+ *                it is split or not; what is not finite in keys that only later
+ *                tokens of the request see does not reach it. Tokens before
  *                qo_indptr[0] or at or past qo_indptr[R] (the padding of a
  *                captured batch) are left as they were.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_WORKSPACE, MLA_ERR_CUDA.

@@ -139,15 +139,18 @@ __device__ __forceinline__ void p_terms4(float p0, float p1, float p2, float p3,
       : "f"(p0), "f"(p1), "f"(p2), "f"(p3));
 }
 
-// Values with their NaNs as zeros: four e4m3 codes, or two f16 values of codes
-// (infinities do not occur). For the values of keys that some rows of a tile do
-// not see: 0 times a NaN would reach those rows; a row that sees such a key is
-// NaN by its score.
+// Values with what is not finite as zeros: four e4m3 codes, or two f16 values of
+// codes (NaNs alone: infinities do not occur), or two bf16 values. For the values of
+// keys that some rows of a tile do not see: 0 times a NaN or an infinity would reach
+// those rows; a row that sees a NaN is NaN by its score.
 __device__ __forceinline__ uint32_t e4m3x4_without_nan(uint32_t w) {
   return w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
 __device__ __forceinline__ uint32_t f16x2_without_nan(uint32_t w) {
   return w & ~__vcmpeq2(w & 0x7C007C00u, 0x7C007C00u);
+}
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {
+  return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
 }
 
 // A key of a cache with group scales, as the softmax takes it. With s the

@@ -723,28 +723,26 @@ __device__ void softmax_rows(const Ctx& x, const HnMaps& maps, const DecodeParam
           for (int q = 0; q < 8; ++q) row[q] = z;
         }
       }
-      if constexpr (GS) {
-        if (causal) {
-          // nor may a NaN of a key that only the later tokens see (the boxes
-          // have landed, this shows their writes)
+      if (causal) {
+        // nor may a NaN of a key that only the later tokens see (the boxes
+        // have landed, this shows their writes)
 #pragma unroll
-          for (int mm = 0; mm < 2; ++mm) {
-            const int i = g * (kBoxes - 1) + 2 * (sw >> 2) + mm, slot = i % C::kSlots;
-            ok = ok && warp_wait(x, x.bar(kFull + slot), (i / C::kSlots) & 1, 39);
-            if (!ok || !key_ok || pos < vis_min) continue;
-            uint4* row = reinterpret_cast<uint4*>(x.smem + C::kOffRing + slot * kSlot + k * 128);
+        for (int mm = 0; mm < 2; ++mm) {
+          const int i = g * (kBoxes - 1) + 2 * (sw >> 2) + mm, slot = i % C::kSlots;
+          ok = ok && warp_wait(x, x.bar(kFull + slot), (i / C::kSlots) & 1, 39);
+          if (!ok || !key_ok || pos < vis_min) continue;
+          uint4* row = reinterpret_cast<uint4*>(x.smem + C::kOffRing + slot * kSlot + k * 128);
 #pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-              uint4 v = row[q];
-              v.x = e4m3x4_without_nan(v.x);
-              v.y = e4m3x4_without_nan(v.y);
-              v.z = e4m3x4_without_nan(v.z);
-              v.w = e4m3x4_without_nan(v.w);
-              row[q] = v;
-            }
+          for (int q = 0; q < 8; ++q) {
+            uint4 v = row[q];
+            v.x = e4m3x4_without_nan(v.x);
+            v.y = e4m3x4_without_nan(v.y);
+            v.z = e4m3x4_without_nan(v.z);
+            v.w = e4m3x4_without_nan(v.w);
+            row[q] = v;
           }
-          if (!ok) break;
         }
+        if (!ok) break;
       }
       fence_proxy_async_smem();
       fence_before_sync();

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
     }
     int64_t ahead = -1;  // of the chunk that the next iteration copies
     if (tid < C::kKC) ahead = find_slot(c + C::kStages, tid);
-    const uint8_t* kvs;
+    uint8_t* kvs;
     if constexpr (FP8) {
       const uint8_t* raw = smem + C::kOffStage + stage * C::kStageBytes;
       uint8_t* comp = smem + C::kOffCompute;
@@ -376,15 +376,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       o[n][2] *= alpha[1];
       o[n][3] *= alpha[1];
     }
-    if constexpr (GS) {
-      // values of keys that only the later tokens of the tile see (S is complete)
-      const int lo = part_len - qlen + row0 / H + 1 - c0;
-      if (qlen > 1 && lo < C::kKC) {
-        for (int i = max(lo, 0) * 64 + tid; i < C::kKC * 64; i += kThreads) {
-          uint4* v = reinterpret_cast<uint4*>(smem + C::kOffCompute + i / 64 * (kQStride * 2) + i % 64 * 16);
-          const uint4 w = *v;
-          *v = make_uint4(f16x2_without_nan(w.x), f16x2_without_nan(w.y), f16x2_without_nan(w.z), f16x2_without_nan(w.w));
-        }
+    // values of keys that only the later tokens of the tile see (S is complete)
+    const int lo = part_len - qlen + row0 / H + 1 - c0;
+    if (qlen > 1 && lo < C::kKC) {
+      auto finite = [](uint32_t w) { return FP8 ? f16x2_without_nan(w) : bf16x2_finite(w); };
+      for (int i = max(lo, 0) * 64 + tid; i < C::kKC * 64; i += kThreads) {
+        uint4* v = reinterpret_cast<uint4*>(kvs + i / 64 * (kQStride * 2) + i % 64 * 16);
+        const uint4 w = *v;
+        *v = make_uint4(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
       }
     }
     if (tid < C::kKC) key_slot[(c + C::kStages) % C::kSlotStages * C::kKC + tid] = ahead;

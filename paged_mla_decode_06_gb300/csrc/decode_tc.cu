@@ -140,6 +140,8 @@ struct Ctx {
   int seg, seg_start, seg_end, n_chunks, unit;
   int pslot;  // balanced schedule: partial slot of this piece, -1 = write out/lse
   bool fin;   // write the output (else base-2 partials)
+  // the first key that some row of the tile does not see: its first row sees least
+  __device__ int hidden_from() const { return part_len - qlen + row0 / H + 1; }
   __device__ uint32_t bar(int i) const { return bar0 + 8u * i; }
   __device__ uint32_t peer_bar(int i) const { return peer + kOffBar + 8u * i; }
 };
@@ -728,9 +730,12 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
     if constexpr (!FP8 && !SPARSE) {
       // The segment's last chunk may end inside the page: zero the value
       // rows past the segment so that whatever the cache holds there cannot
-      // reach O through P = 0.
-      const int nvalid = min(kKeys, x.seg_end - (x.seg_start + c * kKeys));
-      if (nvalid < kKeys) {
+      // reach O through P = 0; nor may what is not finite in the values of keys
+      // that only later tokens see.
+      const int c0 = x.seg_start + c * kKeys;
+      const int nvalid = min(kKeys, x.seg_end - c0);
+      const int from = max(0, min(nvalid, x.hidden_from() - c0));
+      if (from < kKeys) {
         const int st = c % C::kStagesV;
         ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kVFull + st), (c / C::kStagesV) & 1, false, 53));
         if (!ok) break;
@@ -738,9 +743,14 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
         for (int i = x.tid - 64; i < C::kBoxesV * kKeys * 8; i += 128) {
           const int box = i >> 9;
           const int row = (i >> 3) & 63;
-          if (row >= nvalid)
-            *reinterpret_cast<uint4*>(vst + box * kBox + row * 128 + (i & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+          if (row < from) continue;
+          uint4* at = reinterpret_cast<uint4*>(vst + box * kBox + row * 128 + (i & 7) * 16);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row < nvalid) {
+            v = *at;
+            v = make_uint4(bf16x2_finite(v.x), bf16x2_finite(v.y), bf16x2_finite(v.z), bf16x2_finite(v.w));
+          }
+          *at = v;
         }
         fence_proxy_async_smem();
       }
@@ -887,7 +897,8 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
 
 // ------------------------------------------------------------------ value CTA: e4m3 widening
 // 128 threads widen the chunk's 512 e4m3 value columns (4 boxes) to f16 (8
-// boxes, exact) in buffer c & 1, zeroing rows past the segment.
+// boxes, exact) in buffer c & 1, zeroing rows past the segment, and NaNs of
+// keys that only later tokens see.
 template <bool SPARSE>
 __device__ void widen_values(const Ctx& x) {
   using C = Cfg<true, SPARSE>;
@@ -902,7 +913,9 @@ __device__ void widen_values(const Ctx& x) {
       ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kPvDone + slot), ((c - 2) >> 1) & 1, false, 62));
       if (!ok) break;
     }
-    const int nvalid = min(kKeys, x.seg_end - (x.seg_start + c * kKeys));
+    const int c0 = x.seg_start + c * kKeys;
+    const int nvalid = min(kKeys, x.seg_end - c0);
+    const int hidden = x.hidden_from() - c0;
     const uint8_t* src = x.smem + C::kOffV + st * C::kBoxesV * kBox;
     uint8_t* dst = x.smem + C::kOffV16 + slot * 8 * kBox;
     for (int i = ct; i < C::kBoxesV * kKeys * 8; i += 128) {
@@ -919,6 +932,10 @@ __device__ void widen_values(const Ctx& x) {
       for (int e2 = 0; e2 < 4; ++e2) {
         hh[2 * e2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[e2] & 0xFFFF));
         hh[2 * e2 + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[e2] >> 16));
+      }
+      if (row >= hidden) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hh[e] = f16x2_without_nan(hh[e]);
       }
       const int lc = (k & 3) * 2;
       uint8_t* drow = dst + (box * 2 + (k >> 2)) * kBox + row * 128;

@@ -169,3 +169,25 @@ def test_rows_that_see_a_nan_are_nan_on_every_route(kind, bs, g, heads, prefix, 
         out, lse = ran(poisoned(c, keys, queries), plan)
         assert np.isnan(out[odd]).all() and np.isnan(lse[odd]).all()
         right_but(c, odd, out, lse)
+
+
+@pytest.mark.parametrize("kind,bs,g,heads,prefix,kw", ROUTES)
+def test_keys_that_later_tokens_see_do_not_reach_the_earlier_ones(kind, bs, g, heads, prefix, kw):
+    """The last keys of requests of several tokens, NaN or infinite in their value columns:
+    the tokens before them, in whose softmax they are masked, keep their results."""
+    c = shared_case(63, kind, heads, bs, g, [(prefix, [6, 5, 9, 70, 3, 140, 8, 8])], alone=[260, 0],
+                    qlens=[4, 1, 3, 2, 1, 1, 1, 1, 2, 1])
+    plan = B.mla_decode_shared_plan(problem_of(c, **kw), num_groups=1)
+    assert (plan.max_items > 0) == (prefix > 768 and not kw)
+    assert plan.max_items == 0 or shared_groups(c) == [True]
+    slots = [S.row_slots(c["table"][r], bs, int(c["lens"][r]))[at] for r, at in ((0, -1), (0, -2), (2, -1), (3, -1), (8, -1))]
+    keys = [(s, col) for s in slots for col in (0, 11, 300, 511)]
+    seen = [any(s in np.asarray(t) for s in slots) for t in S.token_slots(c["table"], c["lens"], bs, c["qo"])]
+    odd = np.zeros((c["T"], heads), bool)
+    odd[seen] = True
+    assert [int(s) for s in seen] == [0, 0, 1, 1, 0, 0, 0, 1, 0, 1, 0, 0, 0, 0, 0, 1, 0]
+    for value in (float("nan"), float("inf"), float("-inf")) if kind == "bf16" else (float("nan"),):
+        out, lse = ran(poisoned(c, keys, value=value), plan)
+        right_but(c, odd, out, lse)
+        if value != value:
+            assert np.isnan(out[odd]).all() and np.isnan(lse[odd]).all()

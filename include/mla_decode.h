@@ -219,7 +219,8 @@ MLA_API mla_status_t mla_decode_plan(const mla_problem_t* prob, mla_plan_t* plan
  *                q/kv scales of bf16).
  *   sinks        [H] fp32 natural-log sink logits or NULL ([sparse]
  *                _forward_mla): a sink adds e^sink to the softmax denominator
- *                and nothing to the output.
+ *                and nothing to the output; one of -inf counts as none, one
+ *                that is NaN makes its head's rows NaN.
  *   workspace    plan->workspace_bytes of device memory, 256-byte aligned.
  *                Its first int32 is a device status word that must be zero
  *                before the first call (zero it once after allocating): the

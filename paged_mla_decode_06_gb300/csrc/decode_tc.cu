@@ -606,9 +606,9 @@ __device__ void score_softmax(const Ctx& x, const DecodeParams& p) {
         const float s2 = p.sinks[head] * kLog2e;
         const float M = fmaxf(m_ref, s2);
         const float e = l > 0.f ? exp2f(m_ref - M) : 0.f;
-        const float W = l * e + exp2f(s2 - M);
-        mult = e / W;
-        lse = kLn2 * (M + log2f(W));
+        const float W = l * e + (s2 == -INFINITY ? 0.f : exp2f(s2 - M));  // (-inf: no sink; NaN stays)
+        mult = W != 0.f ? e / W : 0.f;
+        if (W != 0.f) lse = kLn2 * (M + log2f(W));
       } else if (l != 0.f) {  // (a NaN stays)
         mult = 1.f / l;
         lse = kLn2 * (m_ref + log2f(l));

@@ -191,3 +191,26 @@ def test_keys_that_later_tokens_see_do_not_reach_the_earlier_ones(kind, bs, g, h
         right_but(c, odd, out, lse)
         if value != value:
             assert np.isnan(out[odd]).all() and np.isnan(lse[odd]).all()
+
+
+@pytest.mark.parametrize("kind,bs,g,heads,prefix,kw", ROUTES)
+def test_sinks_of_minus_infinity_and_nan_on_every_route(kind, bs, g, heads, prefix, kw):
+    """A sink of -inf is none, also for rows without a key; one that is NaN makes its head's
+    rows NaN."""
+    c = shared_case(64, kind, heads, bs, g, [(prefix, [6, 5, 9, 70, 3, 140, 8, 8])], alone=[260, 0, 70], sinks=True)
+    plan = B.mla_decode_shared_plan(problem_of(c, **kw), num_groups=1)
+    assert plan.max_items == 0 or shared_groups(c) == [True]
+    odd = np.zeros((c["T"], heads), bool)
+    c["sinks"][:] = -np.inf
+    c["sinks"][3] = 0.5
+    out, lse = ran(c, plan)
+    plain = dict(c, sinks=None)
+    pout, plse = ran(plain, B.mla_decode_shared_plan(problem_of(plain, **kw), num_groups=1))
+    odd[:, 3] = True
+    assert np.array_equal(out[~odd], pout[~odd]) and np.array_equal(lse[~odd], plse[~odd])
+    c["sinks"][:] = 0.5
+    c["sinks"][3] = np.nan
+    out, lse = ran(c, plan)
+    assert np.isnan(lse[:, 3]).all() and np.isnan(out[np.arange(len(out)) != 9, 3]).all()  # (without keys: unspecified)
+    c["sinks"][3] = 0.5
+    right_but(c, odd, out, lse)

@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
   float m_run[2] = {-INFINITY, -INFINITY};
   float l_run[2] = {0.f, 0.f};
   const float scale2 = p.score_scale_log2;
+  // keys before the first one that some row of the tile does not see
+  const int seen = qlen > 1 ? part_len - qlen + row0 / H + 1 : INT_MAX;
 
   const uint32_t sQ_u32 = smem_u32(sQ);
   const uint32_t sP_u32 = smem_u32(sP);
@@ -377,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(const DecodePar
       o[n][3] *= alpha[1];
     }
     // values of keys that only the later tokens of the tile see (S is complete)
-    const int lo = part_len - qlen + row0 / H + 1 - c0;
-    if (qlen > 1 && lo < C::kKC) {
+    const int lo = seen - c0;
+    if (lo < C::kKC) {
       auto finite = [](uint32_t w) { return FP8 ? f16x2_without_nan(w) : bf16x2_finite(w); };
       for (int i = max(lo, 0) * 64 + tid; i < C::kKC * 64; i += kThreads) {
         uint4* v = reinterpret_cast<uint4*>(kvs + i / 64 * (kQStride * 2) + i % 64 * 16);

@@ -140,8 +140,9 @@ struct Ctx {
   int seg, seg_start, seg_end, n_chunks, unit;
   int pslot;  // balanced schedule: partial slot of this piece, -1 = write out/lse
   bool fin;   // write the output (else base-2 partials)
-  // the first key that some row of the tile does not see: its first row sees least
-  __device__ int hidden_from() const { return part_len - qlen + row0 / H + 1; }
+  // keys of the segment before the first one that some row of the tile does not see
+  // (its first row sees least) or that does not exist
+  __device__ int seen_by_all() const { return min(seg_end, part_len - qlen + row0 / H + 1) - seg_start; }
   __device__ uint32_t bar(int i) const { return bar0 + 8u * i; }
   __device__ uint32_t peer_bar(int i) const { return peer + kOffBar + 8u * i; }
 };
@@ -695,7 +696,7 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
   const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
   const int H = x.H;
   const float* alpha_rx = reinterpret_cast<const float*>(x.smem + kOffAlpha);
-  const int n = x.n_chunks;
+  const int n = x.n_chunks, seen = x.seen_by_all();
   bool ok = true;
   for (int c = 0; c < n && ok; ++c) {
     const int slot = c & 1;
@@ -732,10 +733,9 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
       // rows past the segment so that whatever the cache holds there cannot
       // reach O through P = 0; nor may what is not finite in the values of keys
       // that only later tokens see.
-      const int c0 = x.seg_start + c * kKeys;
-      const int nvalid = min(kKeys, x.seg_end - c0);
-      const int from = max(0, min(nvalid, x.hidden_from() - c0));
+      const int from = seen - c * kKeys;
       if (from < kKeys) {
+        const int nvalid = x.seg_end - (x.seg_start + c * kKeys);
         const int st = c % C::kStagesV;
         ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kVFull + st), (c / C::kStagesV) & 1, false, 53));
         if (!ok) break;
@@ -902,7 +902,7 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
 template <bool SPARSE>
 __device__ void widen_values(const Ctx& x) {
   using C = Cfg<true, SPARSE>;
-  const int ct = x.tid - 192;
+  const int ct = x.tid - 192, seen = x.seen_by_all();
   bool ok = true;
   for (int c = 0; c < x.n_chunks && ok; ++c) {
     const int st = c % C::kStagesV;
@@ -913,9 +913,8 @@ __device__ void widen_values(const Ctx& x) {
       ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kPvDone + slot), ((c - 2) >> 1) & 1, false, 62));
       if (!ok) break;
     }
-    const int c0 = x.seg_start + c * kKeys;
-    const int nvalid = min(kKeys, x.seg_end - c0);
-    const int hidden = x.hidden_from() - c0;
+    const int nvalid = min(kKeys, x.seg_end - (x.seg_start + c * kKeys));
+    const int from = seen - c * kKeys;
     const uint8_t* src = x.smem + C::kOffV + st * C::kBoxesV * kBox;
     uint8_t* dst = x.smem + C::kOffV16 + slot * 8 * kBox;
     for (int i = ct; i < C::kBoxesV * kKeys * 8; i += 128) {
@@ -933,7 +932,7 @@ __device__ void widen_values(const Ctx& x) {
         hh[2 * e2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[e2] & 0xFFFF));
         hh[2 * e2 + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[e2] >> 16));
       }
-      if (row >= hidden) {
+      if (row >= from) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) hh[e] = f16x2_without_nan(hh[e]);
       }

@@ -254,8 +254,8 @@ struct CompactParams {
   int32_t num_rows, cols;
   int32_t* num_live;           // [1]
   int32_t* head;               // {blocks in use, moves}
-  int32_t* holes;              // [num_blocks / 2]
-  int32_t* from;               // [num_blocks / 2]
+  int32_t* holes;              // [num_blocks / 2 + 1]
+  int32_t* from;               // [num_blocks / 2 + 1]
   int32_t* back;               // [num_blocks]
   PageCopy copy;
 };
@@ -306,7 +306,7 @@ struct PrefixParams {
   int32_t workers, tiles_max, max_items;
   int32_t* items;                // [max_items, 8]
   int32_t* n_items;
-  int32_t* worker_first;         // [workers + 1]: first item of each worker (at most 511 of them); null: longest first
+  int32_t* worker_first;         // [workers + 1]: first item of each worker (at most 256 of them); null: longest first
   int32_t* unit_tab;             // [R * tiles_max, 2]: first partial row (-1), pieces
   int32_t* req_group;            // [R]: group whose prefix the request takes part in, or -1
   int32_t* groups;               // [G, 4]: first request, shared keys, first token, first prefix tile

@@ -179,6 +179,12 @@ def test_page_workspaces_and_sizes(lib):
     assert lib.mla_cache_free is not None
 
 
+def test_a_call_that_frees_no_rows_checks_its_workspace_too(lib):
+    assert _free(lib, n=0, ws=None) == B.MLA_ERR_WORKSPACE
+    assert _free(lib, n=0, nbytes=B.mla_cache_workspace(10) - 1) == B.MLA_ERR_WORKSPACE
+    assert _free(lib, n=0, ws=P + 4) == B.MLA_ERR_INVALID_ARG
+
+
 # ---------------------------------------------------------------- the decode over shared prefixes
 
 def _problem(dtype="fp8", block=64, **kw):

@@ -1,5 +1,8 @@
 """The decode of a batch that shares prefixes, and the decodes beside it, at their edges:
-calls without a split row in captured graphs, rows and keys that are no numbers."""
+calls without a split row in captured graphs, rows and keys that are no numbers, more groups
+and requests than the schedule keeps, the same bits on every run."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -214,3 +217,77 @@ def test_sinks_of_minus_infinity_and_nan_on_every_route(kind, bs, g, heads, pref
     assert np.isnan(lse[:, 3]).all() and np.isnan(out[np.arange(len(out)) != 9, 3]).all()  # (without keys: unspecified)
     c["sinks"][3] = 0.5
     right_but(c, odd, out, lse)
+
+
+# ---- batches beyond what the schedule keeps in shared memory (256 groups, 1024 requests)
+
+def repeated(c, order):
+    """Groups ``order`` of the case one after another, as many requests of each as its
+    second number: their table rows, lengths and queries again and again. Returns the new
+    case and the token of ``c`` that each of its tokens repeats."""
+    reqs, prefix, edges = [], [], [0]
+    for g, n in order:
+        a, b = c["edges"][g], c["edges"][g + 1]
+        reqs += [a + i % (b - a) for i in range(n)]
+        prefix.append(c["prefix"][g])
+        edges.append(len(reqs))
+    reqs = np.array(reqs)
+    qlens = np.diff(c["qo"])
+    tokens = np.concatenate([np.arange(c["qo"][r], c["qo"][r + 1]) for r in reqs])
+    d = dict(c, lens=c["lens"][reqs], table=c["table"][reqs], qo=np.concatenate([[0], np.cumsum(qlens[reqs])]),
+             T=len(tokens), q=c["q"][tokens], prefix=np.array(prefix), edges=np.array(edges))
+    return d, tokens
+
+
+@functools.lru_cache(maxsize=None)
+def groups_to_repeat(kind, bs, g, several):
+    c = shared_case(65, kind, 2 if several else 3, bs, g, [(1216 + 64 * i, [4 + 19 * j % 90 for j in range(9)]) for i in range(4)],
+                    qlens=[1 + i % 3 for i in range(36)] if several else None)
+    return c, expected(c)
+
+
+@pytest.mark.parametrize("kind,bs,g", [("scaled", 16, 16), ("fp8", 64, 64), ("bf16", 64, 64)])
+@pytest.mark.parametrize("groups,each", [(300, 3), (3, 400), (300, 8), (257, 4)])
+@pytest.mark.parametrize("several", [False, True])
+def test_more_groups_and_requests_than_the_schedule_keeps(kind, bs, g, groups, each, several):
+    base, (ro, rl, to, tl) = groups_to_repeat(kind, bs, g, several)
+    c, of = repeated(base, [(i % 4, each + (i % 2 if groups == 257 else 0)) for i in range(groups)])
+    plan = B.mla_decode_shared_plan(problem_of(c), num_groups=groups)
+    assert plan.max_items > 0 and all(shared_groups(c))
+    assert len(c["lens"]) > 1024 or groups > 256
+    out, lse = ran(c, plan)
+    assert np.all(np.abs(out - ro[of]) <= to[of]) and np.all(np.abs(lse - rl[of]) <= tl[of])
+
+
+@pytest.mark.parametrize("kind,bs,g", [("scaled", 64, 16), ("scaled", 64, 1), ("fp8", 64, 64), ("bf16", 64, 64)])
+def test_a_shared_prefix_gives_the_same_bits_on_every_run_and_agrees_with_the_plain_decode(kind, bs, g):
+    """Whatever the workspace held, and with the plain calls' results over the same tables
+    within the bounds of both."""
+    c = shared_case(66, kind, 16, bs, g, [(3000, [1 + 97 * i % 900 for i in range(12)])], sinks=True)
+    assert shared_groups(c) == [True]
+    plan = B.mla_decode_shared_plan(problem_of(c), num_groups=1)
+    assert plan.max_items > 0
+    args, named = args_of(c, plan)
+    first = None
+    for fill in (0, 0xFF, 0x01, 0x7F):
+        named["workspace"][256:].fill_(fill)
+        named["out"].fill_(0), named["lse"].fill_(0)
+        for _ in range(3):
+            B.mla_decode_fwd_shared(*args, **named)
+        torch.cuda.synchronize()
+        assert B.mla_workspace_status(plan.plan, named["workspace"]) == 0
+        got = named["out"].clone(), named["lse"].clone()
+        first = first or got
+        assert torch.equal(got[0].view(torch.int16), first[0].view(torch.int16)) and torch.equal(got[1], first[1])
+    ro, rl, to, tl = expected(c)
+    assert np.all(np.abs(first[0].double().cpu().numpy() - ro) <= to)
+    assert np.all(np.abs(first[1].double().cpu().numpy() - rl) <= tl)
+    plain = {k: v for k, v in named.items() if k not in ("prefix_lens", "group_indptr", "kv_scales", "scale_group")}
+    if kind == "scaled":
+        del plain["kv_scale"]
+        B.mla_decode_fwd_scaled(plan.plan, *args[1:], named["kv_scales"], scale_group=g, **plain)
+    else:
+        B.mla_decode_fwd(plan.plan, *args[1:], **plain)
+    torch.cuda.synchronize()
+    assert np.all(np.abs(named["out"].double().cpu().numpy() - first[0].double().cpu().numpy()) <= 2 * to)
+    assert np.all(np.abs(named["lse"].double().cpu().numpy() - first[1].double().cpu().numpy()) <= 2 * tl)

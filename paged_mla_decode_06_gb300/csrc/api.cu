@@ -570,9 +570,7 @@ mla_status_t mla_decode_plan(const mla_problem_t* prob, mla_plan_t* plan) {
 
   int32_t sms = p.num_sms;
   if (sms == 0) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const cudaError_t e = mla::device_sms(&sms);
     if (e != cudaSuccess) return cuda_status(e);
   }
   plan->num_sms = sms;

@@ -45,7 +45,7 @@ constexpr int kWarpGroup = 8;              // largest group a warp takes
 constexpr int kMaxWindow = 256;            // tokens of a CTA's window
 constexpr int kSlotCache = 512;            // slots a CTA keeps in shared memory
 constexpr int kMaxExp = 60;                // scales lie in [2^-60, 2^60]
-constexpr int kWindowCtas = 304;           // CTAs of a long call: two an SM, once over (twice over:
+constexpr int kWindowCtas = 2;             // CTAs an SM of a long call, once over (twice over:
                                            // 16 prompts of 2047 tokens 15.6 us against 14.5)
 
 // Row t's piece (the caller's pointer to it advances by the part's stride).
@@ -287,7 +287,10 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
   // one token a CTA while there are few, so that the tokens of a decode step
   // (a run each) spread over the SMs; more tokens are taken in windows, whose
   // CTAs mostly find one run of a prompt
-  int window = (p.num_tokens + kWindowCtas - 1) / kWindowCtas;
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  int window = (p.num_tokens - 1) / (kWindowCtas * sms) + 1;
   if (window > kMaxWindow) window = kMaxWindow;
   const unsigned ctas = static_cast<unsigned>((p.num_tokens - 1) / window + 1);
   append_cta_kernel<<<ctas, kThreads, 0, stream>>>(p, window);

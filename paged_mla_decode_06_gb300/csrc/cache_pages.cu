@@ -344,19 +344,12 @@ __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactPar
   }
 }
 
-int device_sms(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return static_cast<int>(e);
-}
-
 }  // namespace
 
 cudaError_t launch_copy_blocks(const PageCopy& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   int sms = 0;
-  const cudaError_t e = static_cast<cudaError_t>(device_sms(&sms));
+  const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   const int64_t total = static_cast<int64_t>(n) * c.block_units;
   const int64_t want = (total + kUnroll * kThreads - 1) / (kUnroll * kThreads);
@@ -367,9 +360,12 @@ cudaError_t launch_copy_blocks(const PageCopy& c, const int32_t* src, const int3
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
   if (p.num_forks == 0) return cudaMemsetAsync(p.taken, 0, sizeof(int32_t), stream);
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
   // a block's rows by one to eight CTAs: up to four an SM in all, no CTA without work
   const int upb = p.copy.block_units;
-  int parts = 608 / p.num_forks;
+  int parts = 4 * sms / p.num_forks;
   if (parts > upb / (2 * kThreads)) parts = upb / (2 * kThreads);
   if (parts > 8) parts = 8;
   if (parts < 1) parts = 1;
@@ -386,7 +382,7 @@ cudaError_t launch_free(const FreeParams& p, cudaStream_t stream) {
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   int sms = 0;
-  cudaError_t e = static_cast<cudaError_t>(device_sms(&sms));
+  cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   compact_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p);
   e = cudaGetLastError();

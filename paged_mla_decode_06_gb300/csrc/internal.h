@@ -7,6 +7,13 @@
 
 namespace mla {
 
+// SMs of the current device.
+inline cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
 // Decode kernel variants chosen by the planner.
 enum KernelId : int32_t {
   kMmaRows16 = 1,   // warp-MMA split-K kernel, 16 query rows per CTA

@@ -36,3 +36,10 @@ def test_a_dependent_grid_waits_before_it_ends():
         assert not re.search(r"\breturn\s*;", waits[name]), name
     leave = re.search(r"void leave_merge\(\) \{(.*?)\n\}", (CSRC / "merge_row.cuh").read_text(), re.S).group(1)
     assert re.search(r"if \(blockIdx\.x == 0\)\s*asm volatile\(\"griddepcontrol\.wait", leave)
+
+
+def test_no_launch_has_a_number_of_sms_written_into_it():
+    """Grids follow the device's own count (152 here, and its small multiples)."""
+    for f in sorted(CSRC.glob("*.cu")):
+        code = re.sub(r"//[^\n]*", "", f.read_text())
+        assert not re.search(r"\b(76|152|304|456|608|912|1216)\b", code), f.name

@@ -747,8 +747,11 @@ MLA_API mla_status_t mla_rope_qk(const mla_rope_t* rope, const int32_t* position
 /*
  * The pages of requests that share them. ref_counts [num_blocks] int32 holds, for
  * each physical block, the number of table cells that hold it: 0 for a free block, 1
- * for one that mla_block_tables took from the free list (the caller sets that), more
- * after forks. A block with more than one reference is only read: the
+ * for one that mla_block_tables took from the free list, more after forks. That call
+ * knows no counts: the caller sets the 1 for the first min(*taken, num_free) entries of
+ * the list it gave, on the stream behind it (an elementwise step that reads *taken on the
+ * device; nothing need come back to the host). A block whose 1 was left out counts as
+ * unused to mla_cache_compact, and is not listed by mla_cache_free. A block with more than one reference is only read: the
  * step's tokens go into a request's own last block, which forking copies. The four
  * calls take the cache as kv_cache [num_blocks, block_size, 576] in kv_dtype with
  * kv_scales [num_blocks * block_size / scale_group] fp32, or NULL and scale_group 0

@@ -392,3 +392,52 @@ def test_pages_captured_and_replayed():
         r, t, c, s, n = S.compact(r, t, c, s)
         assert live.item() == n and np.array_equal(T.cpu().numpy(), t) and np.array_equal(R.cpu().numpy(), r)
         check_cache(kv, sc, c, s)
+
+
+def test_counts_of_a_steps_blocks_are_set_on_the_device():
+    """Steps of a captured server: block tables, the counts of the blocks that they took by
+    elementwise operations that read ``taken`` on the GPU, rows given up. No block goes below
+    zero, and what is not in use is in the list."""
+    bs, R, cols, nb = 16, 6, 40, 90
+    rng = np.random.default_rng(91)
+    T_, refs = i32(np.full((R, cols), -1)), i32(np.zeros(nb))
+    lens, qsl, free = i32(np.ones(R)), i32(np.arange(R + 1)), i32(np.zeros(nb))
+    num_free = torch.zeros(1, dtype=torch.int32, device="cuda")
+    taken, count = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    slot = torch.zeros(R, dtype=torch.int32, device="cuda")
+    gone, freed = i32(np.full(2, -1)), i32(np.zeros(nb))
+    ws = torch.zeros(B.mla_cache_workspace(nb), dtype=torch.uint8, device="cuda")
+    place = torch.arange(nb, device="cuda", dtype=torch.int32)
+
+    def step():
+        B.mla_block_tables(qsl, lens, free, T_, block_size=bs, slot_mapping=slot, taken=taken)
+        refs.index_add_(0, free, (place < torch.minimum(taken, num_free)).int())
+        B.mla_cache_free(gone, T_, refs, freed=freed, num_freed=count, workspace=ws)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    T_.fill_(-1), refs.zero_()
+    table, want, ids = np.full((R, cols), -1), np.zeros(nb, np.int64), list(rng.permutation(nb))
+    n = np.zeros(R, np.int64)
+    for k in range(60):
+        n += 1
+        drop = [int(rng.integers(R))] if k % 9 == 8 else []
+        lens.copy_(i32(n))
+        # (the list has room for every entry; those behind its end name no block of their own)
+        free.copy_(i32(ids + [0] * (nb - len(ids))))
+        num_free.fill_(len(ids))
+        gone.copy_(i32(drop + [-1] * (2 - len(drop))))
+        g.replay()
+        for r in range(R):
+            if (n[r] - 1) % bs == 0:
+                table[r, (n[r] - 1) // bs] = ids[0]
+                want[ids.pop(0)] += 1
+        table, want, back = S.free(drop, None, table, want, bs)
+        ids += back
+        for r in drop:
+            n[r] = 0
+        assert np.array_equal(T_.cpu().numpy(), table) and np.array_equal(refs.cpu().numpy(), want)
+        assert freed[:count.item()].tolist() == back and want.min() >= 0
+        assert sorted(ids) == np.flatnonzero(want == 0).tolist()

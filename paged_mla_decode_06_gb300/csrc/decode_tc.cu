@@ -740,11 +740,10 @@ __device__ void value_rows(const Ctx& x, const TcMaps& maps, const DecodeParams&
         ok = __all_sync(0xffffffffu, wait_phase(x, x.bar(kVFull + st), (c / C::kStagesV) & 1, false, 53));
         if (!ok) break;
         uint8_t* vst = x.smem + C::kOffV + st * C::kBoxesV * kBox;
-        for (int i = x.tid - 64; i < C::kBoxesV * kKeys * 8; i += 128) {
-          const int box = i >> 9;
-          const int row = (i >> 3) & 63;
-          if (row < from) continue;
-          uint4* at = reinterpret_cast<uint4*>(vst + box * kBox + row * 128 + (i & 7) * 16);
+        static_assert(C::kBoxesV == 8, "64 pieces of 16 bytes a row");
+        for (int i = max(from, 0) * 64 + x.tid - 64; i < kKeys * 64; i += 128) {
+          const int row = i >> 6;
+          uint4* at = reinterpret_cast<uint4*>(vst + ((i >> 3) & 7) * kBox + row * 128 + (i & 7) * 16);
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (row < nvalid) {
             v = *at;

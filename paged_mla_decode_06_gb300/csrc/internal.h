@@ -2,16 +2,23 @@
 // layer (api.cu) and the kernels. Not part of the public interface.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime_api.h>
 
 namespace mla {
 
-// SMs of the current device.
+// SMs of the current device, asked for once a device (a query takes 0.2 us of a call's 9).
 inline cudaError_t device_sms(int* sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 // Decode kernel variants chosen by the planner.

@@ -128,18 +128,18 @@ def _flops(w):
 PROFILED_TRAFFIC = {
     (4, "dsv3", None): {  # decode_tc.cu, DeepSeek-V3-shaped batch (profiles/decode_tc_dsv3.md)
         "source": "decode_tc.cu",
-        "code_sha256": "da13d048665d44c7ddcc538794e7f607b56fd22feefee2e364670f59ea46aa8b",
-        "dram_per_alg_byte": (139.570176 + 3.544576) / 138.103440,
+        "code_sha256": "a0cbec8b5c38be322e16d0739a54475ab1a57086f8092c6491cce27d178348db",
+        "dram_per_alg_byte": (139.650048 + 3.526144) / 138.103440,
     },
     (5, "fp8", 16): {  # decode_hn.cu, e4m3 batch at 16 heads (profiles/decode_hn_fp8.md)
         "source": "decode_hn.cu",
-        "code_sha256": "83249ff255d7f132f4904c3ba508e1279cadc75e47b6643e91502954249c9e33",
-        "dram_per_alg_byte": (226.828800 + 3.382784) / 226.738272,
+        "code_sha256": "4af127cb66a02c64f05d31a78331246fcdd37bb8eb5d57f9611affbe76fe7638",
+        "dram_per_alg_byte": (226.827776 + 3.591680) / 226.738272,
     },
     (5, "fp8", 128): {  # decode_hn.cu on clusters of two CTAs, e4m3 batch at 128 heads (same file)
         "source": "decode_hn.cu",
-        "code_sha256": "83249ff255d7f132f4904c3ba508e1279cadc75e47b6643e91502954249c9e33",
-        "dram_per_alg_byte": (229.603072 + 7.410944) / 228.286560,
+        "code_sha256": "4af127cb66a02c64f05d31a78331246fcdd37bb8eb5d57f9611affbe76fe7638",
+        "dram_per_alg_byte": (229.549824 + 7.723776) / 228.286560,
     },
 }
 

@@ -53,7 +53,8 @@
 //
 // Warps: 0 loads q and keys, 1 issues Q K^T (rank 1: passes keys on), 2 prepares the
 // keys' scales, 3 issues P V (passes values on), 4 and 5 load values, 6 watches the
-// time, 8-23 softmax and epilogue (7 has no work: registers move by four warps).
+// time, 8-23 softmax and epilogue (7 has no work: registers move by four warps). 80
+// registers a thread at launch; the softmax spills 68 to 88 bytes (32 without group scales).
 // Every wait is bounded: a timeout records a code in the status word, stops
 // the CTA's work, drains what was issued and exits.
 #include <atomic>

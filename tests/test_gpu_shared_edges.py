@@ -10,6 +10,8 @@ import torch
 from oracle import scaled_oracle as S
 from paged_mla_decode_06_gb300 import binding as B
 from paged_mla_decode_06_gb300 import build as BUILD
+from paged_mla_decode_06_gb300 import inputs as I
+from tests.gpu_helpers import oracle_slots, run_gpu
 from tests.test_gpu_shared import args_of, dev, expected, shared_case, shared_groups
 
 pytestmark = pytest.mark.gpu
@@ -291,3 +293,23 @@ def test_a_shared_prefix_gives_the_same_bits_on_every_run_and_agrees_with_the_pl
     torch.cuda.synchronize()
     assert np.all(np.abs(named["out"].double().cpu().numpy() - first[0].double().cpu().numpy()) <= 2 * to)
     assert np.all(np.abs(named["lse"].double().cpu().numpy() - first[1].double().cpu().numpy()) <= 2 * tl)
+
+
+@pytest.mark.parametrize("kernel,ns", [(B.MLA_KERNEL_AUTO, None), (B.MLA_KERNEL_AUTO, 3), (B.MLA_KERNEL_WARP_MMA, None),
+                                       (B.MLA_KERNEL_WARP_MMA, 3)])
+def test_sparse_rows_that_list_a_nan_key_are_nan(kernel, ns):
+    """Keys of a slot list with a NaN, in the rope and in the value columns: the tokens that
+    list them are NaN in output and LSE, the others as without it."""
+    w = I.sparse_topk(num_reqs=2, tokens_per_req=6, num_heads=32, cache_tokens=4096, topk=1024, interspersed_rows=1, max_pad=64)
+    slots = oracle_slots(w)
+    out, lse, _ = run_gpu(w, num_segments=ns, kernel=kernel)
+    lists = [set(s[s >= 0].tolist()) for s in slots]
+    counts = np.bincount(slots[slots >= 0])
+    rare = [int(s) for s in np.flatnonzero(counts == 1)[[3, -7]]]      # of one token each
+    seen = np.array([any(s in t for s in rare) for t in lists])
+    assert 1 <= seen.sum() <= 2
+    flat = w.cache.reshape(-1, 576)
+    flat[rare[0], 570], flat[rare[1], 9] = I.BF16_NAN_BITS, I.BF16_NAN_BITS
+    bad, bad_lse, _ = run_gpu(w, num_segments=ns, kernel=kernel)
+    assert np.isnan(bad[seen]).all() and np.isnan(bad_lse[seen]).all()
+    assert np.array_equal(bad[~seen], out[~seen]) and np.array_equal(bad_lse[~seen], lse[~seen])
